@@ -307,6 +307,150 @@ kascade_status kascade_run_stack_profiled(const kascade_desc* desc, int32_t mode
                                           void* ws, size_t ws_bytes, void* stream,
                                           void* const* layer_events);
 
+/* ------------------------------------------- paged 4-bit key/value cache -- */
+/* Decode for a server's cache: sequences of different lengths, each a list of
+ * fixed-size blocks, keys and values held in 4 bits (the pages describe
+ * neither; the layers over the cache are theirs, Methodology 2-3).
+ *
+ * pages [num_blocks][Hkv][block_size/16][18 d] bytes, one such buffer per
+ * layer (kascade_qcache_bytes), 16-byte aligned. The last axis is a group of
+ * 16 tokens: 16 rows of K codes (d/2 bytes each, element 2i in the low half
+ * of byte i), 16 rows of K scales (d/16 bytes), 16 rows of V codes, 16 rows of
+ * V scales. 16 consecutive elements of a row share one scale; with
+ * x' = x / {k,v}_scale and amax the block's largest |x'|,
+ *   s    = amax/6 rounded to e4m3 (ties to even, at most 448),
+ *   code = x'/s rounded to e2m1 {0, .5, 1, 1.5, 2, 3, 4, 6} (same, at most 6),
+ * and the stored element is code * s * {k,v}_scale, exact in bf16. Blocks with
+ * amax/6 <= 2^-10 are stored as zeros, magnitudes above 2688 (infinities
+ * among them) saturate, and a block that holds a NaN reads back as NaN.
+ *
+ * block_table [B][max_blocks] int32: entry j of row b is the block that holds
+ * tokens j*block_size .. of sequence b (all layers share it). A slot is
+ * block * block_size + offset. kv_lens [B] int32: cached tokens of each
+ * sequence, 0 <= kv_lens[b] <= desc->kv_len, read on the device; a sequence
+ * of length 0 outputs zeros. What the pages hold behind a sequence's last
+ * token is never used. desc->kv_len <= max_blocks*block_size is the longest
+ * length and the row stride of scores; desc->dtype is that of q, out and of
+ * appended rows (bf16, or fp32 computed to fp32 accuracy). A length out of
+ * range, or a block id outside [0, num_blocks), sets KASCADE_ERR_BAD_INPUT on the device;
+ * those keys are not read and count as masked.
+ * Limits beyond the descriptor's: num_blocks*block_size < 2^31,
+ * B*max_blocks < 2^31 (KASCADE_ERR_UNSUPPORTED). */
+typedef struct {
+  int32_t block_size;   /* 16, 32, 64, 128 or 256 tokens */
+  int32_t num_blocks;   /* blocks of the cache */
+  int32_t max_blocks;   /* columns of a block table */
+  float k_scale;        /* powers of two in [2^-32, 2^32]; 0 selects 1 */
+  float v_scale;
+} kascade_qcache;
+
+/* Bytes of one layer's pages (0 for an invalid geometry). */
+size_t kascade_qcache_bytes(const kascade_qcache* cache, int32_t n_kv_heads, int32_t head_dim);
+
+/* Workspace of the attention calls below: topk = 0 for
+ * kascade_qcache_dense_decode, the sets' size for the others. 0 if invalid.
+ * Plan, append and read need only the workspace header, 256 bytes. */
+size_t kascade_qcache_workspace_size(const kascade_desc* desc, const kascade_qcache* cache,
+                                     int32_t topk);
+
+/* Block tables and slots of one step, on the device. Sequence b goes from
+ * L = kv_lens[b] to L' = max(0, L + new_lens[b]) tokens: it grows (new tokens
+ * to append), shrinks (tokens taken back) or, with -L or less, ends. It then
+ * holds ceil(L'/block_size) blocks: those it gives back are pushed on the
+ * stack free_blocks [num_blocks] (free_count of them valid) in (sequence,
+ * column) order, then those it takes are popped from it in that order. Writes
+ *   block_table     the entries of taken blocks (others are left as they are);
+ *   kv_lens_out [B], free_count_out [1]   (may be kv_lens and free_count);
+ *   cu_new [B+1]    running number of new tokens: sequence b's rows of this
+ *                   step are cu_new[b] .. cu_new[b+1]-1;
+ *   slot_map [max_new]   the slot of every new token, -1 behind the last.
+ * A step that cannot be served (too few free blocks, more tokens than
+ * max_blocks*block_size or than max_new, an id or a length out of range)
+ * changes no table, stack, length or count, leaves every slot -1 and cu_new
+ * 0, and sets KASCADE_ERR_BAD_INPUT on the device. n_seqs <= 16384. */
+kascade_status kascade_qcache_plan(const kascade_qcache* cache, int32_t n_seqs,
+                                   const int32_t* kv_lens, const int32_t* new_lens,
+                                   int32_t* block_table, int32_t* free_blocks,
+                                   const int32_t* free_count, int32_t* kv_lens_out,
+                                   int32_t* free_count_out, int32_t* cu_new, int32_t* slot_map,
+                                   int32_t max_new, void* ws, size_t ws_bytes, void* stream);
+
+/* Quantise rows of new keys and values into their slots. k, v: row (t, g) of
+ * head_dim contiguous elements at k + t*strides[0] + g*strides[1] and
+ * v + t*strides[2] + g*strides[3] (host array of four element strides, each a
+ * multiple of 16 bytes), so the decode layout [T,Hkv,d] and the prefill
+ * layout [Hkv,N,d] are both taken as they are. slot_map [n_tokens]: distinct
+ * slots; a negative one is padding (skipped), one beyond the cache sets
+ * KASCADE_ERR_BAD_INPUT and is skipped. */
+kascade_status kascade_qcache_append(const kascade_qcache* cache, int32_t n_kv_heads,
+                                     int32_t head_dim, int32_t dtype, const void* k,
+                                     const void* v, const int64_t* strides,
+                                     const int32_t* slot_map, int32_t n_tokens, void* pages,
+                                     void* ws, size_t ws_bytes, void* stream);
+
+/* The stored values of rows, in the same layouts (to attend over a cached
+ * prefix with the prefill calls, or to calibrate on it); zeros for a negative
+ * slot. Slots may repeat. */
+kascade_status kascade_qcache_read(const kascade_qcache* cache, int32_t n_kv_heads,
+                                   int32_t head_dim, int32_t dtype, const void* pages,
+                                   const int32_t* slot_map, int32_t n_tokens, void* k, void* v,
+                                   const int64_t* strides, void* ws, size_t ws_bytes,
+                                   void* stream);
+
+/* Exact attention of one query per sequence over its cached tokens (as
+ * kascade_dense_decode). When scores_out is not NULL the fp32 logits
+ * sigma*q.k are written there, [B,Hq,kv_len], -inf behind the last token. */
+kascade_status kascade_qcache_dense_decode(const kascade_desc* desc, const kascade_qcache* cache,
+                                           const void* q, const void* pages,
+                                           const int32_t* block_table, const int32_t* kv_lens,
+                                           void* out, float* scores_out, void* ws,
+                                           size_t ws_bytes, void* stream);
+
+/* Anchor layer (as kascade_anchor_decode, both index modes): the exact output
+ * and the exact Top-k of every row, min(topk, kv_lens[b]) ascending positions
+ * and -1 behind them; 1 <= topk <= desc->kv_len. scores_out as there, -inf
+ * behind the last token. */
+kascade_status kascade_qcache_anchor_decode(const kascade_desc* desc, const kascade_qcache* cache,
+                                            const void* q, const void* pages,
+                                            const int32_t* block_table, const int32_t* kv_lens,
+                                            int32_t topk, void* out, int32_t* idx_out,
+                                            float* scores_out, void* ws, size_t ws_bytes,
+                                            void* stream);
+
+/* Reuse layer (as kascade_reuse_decode, both index modes): idx rows hold
+ * ascending distinct positions in [0, kv_lens[b]), then -1 entries; an empty
+ * set outputs zeros. Entries that break this set KASCADE_ERR_BAD_INPUT and
+ * are not read. Per query head sets need kv_len <= 262144. */
+kascade_status kascade_qcache_reuse_decode(const kascade_desc* desc, const kascade_qcache* cache,
+                                           const void* q, const void* pages,
+                                           const int32_t* block_table, const int32_t* kv_lens,
+                                           int32_t topk, const int32_t* idx, void* out, void* ws,
+                                           size_t ws_bytes, void* stream);
+
+/* The device state one decode step works on. */
+typedef struct {
+  int32_t* block_table;       /* [B, max_blocks] */
+  int32_t* kv_lens;           /* [B]; updated by the step's plan */
+  const int32_t* new_lens;    /* [B], or NULL: no plan, kv_lens and slot_map are as given */
+  int32_t* free_blocks;       /* [num_blocks], with new_lens only, as the next two */
+  int32_t* free_count;        /* [1] */
+  int32_t* cu_new;            /* [B + 1] */
+  int32_t* slot_map;          /* [max_new] */
+  int32_t max_new;            /* rows of every k_new[l], v_new[l] */
+} kascade_qcache_step;
+
+/* One decode step over a layer stack: the plan (when step->new_lens is not
+ * NULL), then per layer l the append of k_new[l], v_new[l] [max_new,Hkv,d]
+ * (skipped when k_new and v_new are NULL) and the anchor, reuse or dense
+ * layer over pages[l], dispatched as kascade_run_stack does. q, k_new,
+ * v_new, pages, out: host arrays of device pointers. A sequence's query
+ * attends to its new tokens too. */
+kascade_status kascade_qcache_run_stack(
+    const kascade_desc* desc, const kascade_qcache* cache, const kascade_qcache_step* step,
+    int32_t n_layers, const void* const* q, const void* const* k_new, const void* const* v_new,
+    void* const* pages, int32_t topk, const int32_t* anchors, int32_t n_anchors, void* const* out,
+    int32_t* idx_buf, void* ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------------------------------------ scheduling -- */
 
 /* Cross-layer Top-k overlap for the anchor DP (Methodology 4). sets: device

@@ -448,13 +448,18 @@ __global__ void __launch_bounds__((NW + 1) * 32)
 // plan[unit][c][kPlanCap], with its length in plan_count[unit][c]. Reuse
 // CTA (c, unit) consumes exactly chunk c.
 // ------------------------------------------------------------------------
-__device__ __forceinline__ int warp_lower_bound(const int32_t* row, int n, int v) {
+// `padded`: the row may end in -1 entries, which then order behind every key.
+__device__ __forceinline__ int warp_lower_bound(const int32_t* row, int n, int v, bool padded) {
   const int lane = threadIdx.x & 31;
+  auto at_least = [&](int p) {
+    const int32_t x = __ldg(row + p);
+    return padded ? static_cast<uint32_t>(x) >= static_cast<uint32_t>(v) : x >= v;
+  };
   int lo = 0, hi = n;   // first index in [lo, hi] with row[i] >= v
   while (hi - lo > 32) {
     const int step = (hi - lo + 31) / 32;
     const int p = lo + (lane + 1) * step - 1;
-    const bool ge = p >= hi || __ldg(row + p) >= v;
+    const bool ge = p >= hi || at_least(p);
     const unsigned int bal = __ballot_sync(0xffffffffu, ge);
     if (bal == 0u) return hi;
     const int f = __ffs(bal) - 1;
@@ -463,7 +468,7 @@ __device__ __forceinline__ int warp_lower_bound(const int32_t* row, int n, int v
     lo = nlo;
   }
   const int p = lo + lane;
-  const bool ge = p < hi && __ldg(row + p) >= v;
+  const bool ge = p < hi && at_least(p);
   const unsigned int bal = __ballot_sync(0xffffffffu, ge);
   return bal ? lo + __ffs(bal) - 1 : hi;
 }
@@ -480,7 +485,11 @@ __global__ void __launch_bounds__(256) k_build_union_plan(const __grid_constant_
   const int c = blockIdx.x, unit = blockIdx.y, nch = gridDim.x;
   const int b = unit / a.Hkv, g = unit % a.Hkv;
   const int G = a.G, topk = a.topk;
-  const int n0 = c * R, n1 = min(a.N, n0 + R);
+  // ragged sequences (lens given): sets of sequence b lie in [0, lens[b]) and
+  // end in -1 entries where they are shorter than topk
+  const bool padded = a.lens != nullptr;
+  const int n = padded ? min(max(a.lens[b], 0), a.N) : a.N;
+  const int n0 = c * R, n1 = min(n, n0 + R);
   const int words = (R + 31) / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // sets of this unit: one per query head of the group, or the group's one
@@ -497,12 +506,13 @@ __global__ void __launch_bounds__(256) k_build_union_plan(const __grid_constant_
     const int slot = job < nsets ? job : job - nsets;
     const bool is_hi = job >= nsets;
     const int32_t* row = set_row(slot);
-    const int pos = warp_lower_bound(row, topk, is_hi ? n1 : n0);
+    const int pos = warp_lower_bound(row, topk, is_hi ? n1 : n0, padded);
     if (lane == 0) {
       if (is_hi) s_hi[slot] = pos;
       else s_lo[slot] = pos;
       // entries below 0 (first chunk) or at/after N (last chunk) are invalid
-      if ((!is_hi && c == 0 && pos > 0) || (is_hi && c == nch - 1 && pos < topk))
+      if ((!is_hi && c == 0 && pos > 0) ||
+          (is_hi && c == nch - 1 && pos < topk && !padded))
         report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x201);
     }
   }
@@ -520,6 +530,9 @@ __global__ void __launch_bounds__(256) k_build_union_plan(const __grid_constant_
       }
       atomicOr(&bm[slot][key >> 5], 1u << (key & 31));
     }
+    if (padded && c == nch - 1)   // nothing but padding behind a set's last key
+      for (int i = hi + threadIdx.x; i < topk; i += blockDim.x)
+        if (__ldg(row + i) != -1) report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x204);
   }
   __syncthreads();
   // contiguous word runs per thread; block scan of union counts

@@ -49,6 +49,8 @@ struct DecodeArgs {
   const uint32_t* plan;     // union plan [B*Hkv][chunks][2048]: key | mask << 24
   const int32_t* plan_count;  // [B*Hkv][chunks]
   const int32_t* idx;       // sets [B,Hq,topk], or [B,Hkv,topk] when pooled
+  const int32_t* lens;      // union plan only: [B] lengths of ragged sequences whose sets
+                            // may end in -1 entries, or null (every sequence N keys)
   int pooled;               // 1: one set per (sequence, KV head)
   int plan_stride;          // G * topk
   int topk;
@@ -128,6 +130,10 @@ struct TopkArgs {
   // Plain rows (null when unused): row r's selection as a bitmap of its n
   // positions, sel_bits + r * ceil(n / 32) (bit p % 32 of word p / 32).
   uint32_t* sel_bits;
+  // Plain rows of ragged sequences (null when unused): row r holds
+  // row_lens[r / rows_per_len] scores (at most n; the row stride stays n).
+  const int32_t* row_lens;
+  int rows_per_len;
 };
 cudaError_t launch_topk(const TopkArgs& a, cudaStream_t st);
 

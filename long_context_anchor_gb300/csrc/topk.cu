@@ -52,7 +52,7 @@ __device__ __forceinline__ RowDesc row_desc(const TopkArgs& a, int r) {
   RowDesc d;
   if (a.prefill_tiles == 0) {
     d.ptr = a.scores + static_cast<size_t>(r) * a.n;
-    d.len = a.n;
+    d.len = a.row_lens != nullptr ? min(max(a.row_lens[r / a.rows_per_len], 0), a.n) : a.n;
   } else {
     // packed rows of one (sequence, head): tile t starts at (tile/2)*t*(t+1)
     const int nT = a.prefill_tiles;

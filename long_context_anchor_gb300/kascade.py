@@ -6,6 +6,7 @@ workspace) and the current CUDA stream. Importing this module loads
 ``libkascade.so`` from this package directory and raises if it is missing;
 there is no fallback.
 """
+import contextlib
 import ctypes
 import math
 import os
@@ -36,8 +37,23 @@ class Desc(ctypes.Structure):
                 ("index_mode", ctypes.c_int32)]
 
 
+class QCache(ctypes.Structure):
+    """kascade_qcache: geometry of a paged 4-bit key/value cache."""
+    _fields_ = [("block_size", ctypes.c_int32), ("num_blocks", ctypes.c_int32),
+                ("max_blocks", ctypes.c_int32), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float)]
+
+
+class QCacheStep(ctypes.Structure):
+    """kascade_qcache_step: the device state one decode step works on."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("block_table", "kv_lens", "new_lens", "free_blocks",
+                                               "free_count", "cu_new", "slot_map")]
+    _fields_ += [("max_new", ctypes.c_int32)]
+
+
 _vp, _i32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
 _DP = ctypes.POINTER(Desc)
+_QP, _I64P = ctypes.POINTER(QCache), ctypes.POINTER(ctypes.c_int64)
 _SIGS = {
     "kascade_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "kascade_workspace_size": (_sz, [_DP, _i32, _i32]),
@@ -68,6 +84,22 @@ _SIGS = {
                                                   ctypes.POINTER(_vp), ctypes.POINTER(_vp), _i32,
                                                   ctypes.POINTER(_i32), _i32, ctypes.POINTER(_vp),
                                                   _vp, _vp, _sz, _vp, ctypes.POINTER(_vp)]),
+    "kascade_qcache_bytes": (_sz, [_QP, _i32, _i32]),
+    "kascade_qcache_workspace_size": (_sz, [_DP, _QP, _i32]),
+    "kascade_qcache_plan": (ctypes.c_int, [_QP, _i32] + [_vp] * 9 + [_i32, _vp, _sz, _vp]),
+    "kascade_qcache_append": (ctypes.c_int, [_QP, _i32, _i32, _i32, _vp, _vp, _I64P, _vp, _i32,
+                                             _vp, _vp, _sz, _vp]),
+    "kascade_qcache_read": (ctypes.c_int, [_QP, _i32, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _I64P,
+                                           _vp, _sz, _vp]),
+    "kascade_qcache_dense_decode": (ctypes.c_int, [_DP, _QP] + [_vp] * 7 + [_sz, _vp]),
+    "kascade_qcache_anchor_decode": (ctypes.c_int, [_DP, _QP] + [_vp] * 4 + [_i32] + [_vp] * 4 +
+                                     [_sz, _vp]),
+    "kascade_qcache_reuse_decode": (ctypes.c_int, [_DP, _QP] + [_vp] * 4 + [_i32] + [_vp] * 3 +
+                                    [_sz, _vp]),
+    "kascade_qcache_run_stack": (ctypes.c_int, [_DP, _QP, ctypes.POINTER(QCacheStep), _i32] +
+                                 [ctypes.POINTER(_vp)] * 4 +
+                                 [_i32, ctypes.POINTER(_i32), _i32, ctypes.POINTER(_vp), _vp, _vp,
+                                  _sz, _vp]),
     "kascade_overlap_workspace_size": (_sz, [_i32, _i32, _i32]),
     "kascade_calibrate_workspace_size": (_sz, [_DP, _i32, _i32]),
     "kascade_calibrate": (ctypes.c_int, [_DP, _i32, ctypes.POINTER(_vp), ctypes.POINTER(_vp),
@@ -158,9 +190,14 @@ class Workspace:
     def __init__(self, device=None):
         self.device = torch.device(device if device is not None else "cuda")
         self.buf: Optional[torch.Tensor] = None
+        self.captured = False     # a graph holds the buffer's address
 
     def get(self, nbytes: int, stream=None) -> torch.Tensor:
         if self.buf is None or self.buf.numel() < nbytes:
+            if self.captured:
+                raise RuntimeError("this workspace was captured into a CUDA graph, which holds its "
+                                   "address: it cannot grow to %d bytes (use another one, or size "
+                                   "it before the capture)" % nbytes)
             self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
             _check(_lib.kascade_workspace_init(_ptr(self.buf), self.buf.numel(), _stream(stream)),
                    "kascade_workspace_init")
@@ -567,6 +604,370 @@ def kascade_attention(qs, ks, vs, topk, anchors, group_map=None, scale=None, poo
     outs, _ = run_stack(mode, qs, ks, vs, topk, list(anchors), group_map=group_map, scale=scale,
                         ws=ws, stream=stream, pooled=pooled)
     return outs
+
+
+# ------------------------------------------------- paged 4-bit key/value cache --
+# The pages (one uint8 tensor per layer, qcache_alloc) hold num_blocks blocks of
+# block_size tokens, [num_blocks, Hkv, block_size/16, 18*d]; a block table
+# [B, max_blocks] lists each sequence's blocks and kv_lens [B] its cached
+# tokens. Number format, layout and error behaviour: include/kascade.h.
+
+def qcache_alloc(num_blocks, n_kv_heads, head_dim, block_size=64, device="cuda"):
+    """Zeroed pages of one layer: uint8 [num_blocks, Hkv, block_size/16, 18*d]."""
+    geo = QCache(int(block_size), int(num_blocks), 1, 0.0, 0.0)
+    n = _lib.kascade_qcache_bytes(ctypes.byref(geo), int(n_kv_heads), int(head_dim))
+    if n == 0:
+        raise KascadeError(INVALID_ARG, "kascade_qcache_bytes")
+    return torch.zeros(int(num_blocks), int(n_kv_heads), int(block_size) // 16, 18 * int(head_dim),
+                       dtype=torch.uint8, device=device)
+
+
+def _pages(pages, name="pages"):
+    """Validated (num_blocks, Hkv, block_size, d) of one layer's pages."""
+    if not isinstance(pages, torch.Tensor) or pages.dim() != 4:
+        raise ValueError("%s: expected a uint8 tensor [num_blocks, Hkv, block_size/16, 18*d]" % name)
+    nb, hkv, groups, size = pages.shape
+    if size not in (18 * 64, 18 * 128):
+        raise ValueError("%s: last axis %d, expected 18*d with d 64 or 128" % (name, size))
+    _expect(pages, name, pages.shape, torch.uint8)
+    return nb, hkv, groups * 16, size // 18
+
+
+def _on(dev, stream):
+    """The stream a call runs on (the tensors' device's current one by default),
+    and a context in which that device and stream are current, so that
+    outputs and workspaces allocated by the call belong to the stream."""
+    if dev.type != "cuda":      # only reachable with a stand-in library
+        return None, contextlib.nullcontext()
+    if stream is None and dev.index == torch.cuda.current_device():
+        return torch.cuda.current_stream(dev), contextlib.nullcontext()
+    s = stream if stream is not None else torch.cuda.current_stream(dev)
+    if s.device != dev:
+        raise ValueError("stream: on %s, expected %s" % (s.device, dev))
+    return s, torch.cuda.stream(s)
+
+
+def _qws(ws, dev, nbytes, stream):
+    """The workspace buffer of a cache call. A captured call needs a workspace
+    of its own, large enough already: a graph keeps its address, so the
+    shared default one (which grows) or one grown inside the capture would be
+    gone when the graph is replayed."""
+    if dev.type == "cuda" and torch.cuda.is_current_stream_capturing():
+        if ws is None or ws.buf is None or ws.buf.numel() < nbytes:
+            raise ValueError("a captured call needs ws=Workspace(device), sized before the capture "
+                             "(run the call once with it)")
+        ws.captured = True
+        return ws.buf
+    ws = ws if ws is not None else default_workspace(dev)
+    buf = ws.get(nbytes, stream)
+    if buf.device != dev:
+        raise ValueError("ws: on %s, expected %s" % (buf.device, dev))
+    return buf
+
+
+def qcache_workspace_size(desc, geo, topk: int) -> int:
+    n = _lib.kascade_qcache_workspace_size(ctypes.byref(desc), ctypes.byref(geo), int(topk))
+    if n == 0:
+        raise KascadeError(INVALID_ARG, "kascade_qcache_workspace_size")
+    return n
+
+
+def qcache_plan(kv_lens, new_lens, block_table, free_blocks, free_count, block_size, max_new,
+                kv_lens_out=None, free_count_out=None, ws=None, stream=None):
+    """Block tables and slots of one step, on the device: sequence b goes from
+    kv_lens[b] to max(0, kv_lens[b] + new_lens[b]) tokens, takes blocks from the
+    top of the stack free_blocks [num_blocks] (free_count [1] of them valid)
+    and gives back those it no longer needs. block_table [B, max_blocks] and
+    free_blocks are updated in place. Returns (slot_map [max_new], cu_new
+    [B+1], kv_lens_out [B], free_count_out [1]), all int32; the last two may
+    be given (kv_lens and free_count themselves included)."""
+    for name, t, nd in (("kv_lens", kv_lens, 1), ("block_table", block_table, 2),
+                        ("free_blocks", free_blocks, 1)):
+        if not isinstance(t, torch.Tensor) or t.dim() != nd:
+            raise ValueError("%s: expected an int32 tensor with %d axes" % (name, nd))
+    B, width = block_table.shape
+    for name, t, shape in (("kv_lens", kv_lens, (B,)), ("new_lens", new_lens, (B,)),
+                           ("block_table", block_table, (B, width)),
+                           ("free_blocks", free_blocks, free_blocks.shape),
+                           ("free_count", free_count, (1,))):
+        _expect(t, name, shape, torch.int32)
+    named = [("kv_lens", kv_lens), ("new_lens", new_lens), ("block_table", block_table),
+             ("free_blocks", free_blocks), ("free_count", free_count)]
+    for name, t, shape in (("kv_lens_out", kv_lens_out, (B,)),
+                           ("free_count_out", free_count_out, (1,))):
+        if t is not None:
+            _expect(t, name, shape, torch.int32)
+            named.append((name, t))
+    dev = _same_cuda_device(named)
+    geo = QCache(int(block_size), free_blocks.numel(), width, 0.0, 0.0)
+    st, ctx = _on(dev, stream)
+    with ctx:
+        new = lambda n: torch.empty(n, dtype=torch.int32, device=dev)
+        slots, cu = new(int(max_new)), new(B + 1)
+        lens = new(B) if kv_lens_out is None else kv_lens_out
+        count = new(1) if free_count_out is None else free_count_out
+        buf = _qws(ws, dev, 256, st)
+        _check(_lib.kascade_qcache_plan(ctypes.byref(geo), B, _ptr(kv_lens), _ptr(new_lens),
+                                        _ptr(block_table), _ptr(free_blocks), _ptr(free_count),
+                                        _ptr(lens), _ptr(count), _ptr(cu), _ptr(slots),
+                                        int(max_new), _ptr(buf), buf.numel(), _stream(st)),
+               "kascade_qcache_plan")
+    return slots, cu, lens, count
+
+
+def _rows(k, v, T, hkv, d):
+    """Element strides of k and v [T, Hkv, d] (last axis contiguous, rows on
+    16-byte boundaries), for the library."""
+    strides = []
+    for name, t in (("k", k), ("v", v)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s: expected a torch.Tensor" % name)
+        if tuple(t.shape) != (T, hkv, d):
+            raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), (T, hkv, d)))
+        _dtype_code(t)
+        if t.dtype != k.dtype:
+            raise TypeError("%s: dtype %s, expected %s" % (name, t.dtype, k.dtype))
+        unit = 16 // t.element_size()
+        row = [t.stride(0) if T > 1 else 0, t.stride(1) if hkv > 1 else 0]
+        if t.numel() and (t.stride(2) != 1 or any(s % unit for s in row) or t.data_ptr() % 16):
+            raise ValueError("%s: rows must be contiguous and start on 16-byte boundaries" % name)
+        strides += row
+    return (ctypes.c_int64 * 4)(*strides)
+
+
+def qcache_append(k, v, slot_map, pages, k_scale=1.0, v_scale=1.0, ws=None, stream=None):
+    """Quantise rows k, v [T, Hkv, d] (bf16 or fp32; any token and head strides,
+    so a prefill layer's k[b].transpose(0, 1) is taken as it is) into the slots
+    slot_map [T] int32 (distinct; negative: skipped) of pages, in place."""
+    nb, hkv, bs, d = _pages(pages)
+    if not isinstance(slot_map, torch.Tensor) or slot_map.dim() != 1:
+        raise ValueError("slot_map: expected an int32 tensor [T]")
+    T = slot_map.numel()
+    _expect(slot_map, "slot_map", (T,), torch.int32)
+    strides = _rows(k, v, T, hkv, d)
+    dev = _same_cuda_device([("k", k), ("v", v), ("slot_map", slot_map), ("pages", pages)])
+    geo = QCache(bs, nb, 1, float(k_scale), float(v_scale))
+    st, ctx = _on(dev, stream)
+    with ctx:
+        buf = _qws(ws, dev, 256, st)
+        _check(_lib.kascade_qcache_append(ctypes.byref(geo), hkv, d, _dtype_code(k), _ptr(k),
+                                          _ptr(v), strides, _ptr(slot_map), T, _ptr(pages),
+                                          _ptr(buf), buf.numel(), _stream(st)),
+               "kascade_qcache_append")
+    return pages
+
+
+def qcache_read(pages, slot_map, dtype=torch.bfloat16, k_scale=1.0, v_scale=1.0, k=None, v=None,
+                ws=None, stream=None):
+    """The stored values of slots slot_map [T] int32 as (k, v) [T, Hkv, d] (bf16
+    or fp32; zeros for a negative slot). k, v: outputs to fill instead, of any
+    token and head strides whose rows do not overlap."""
+    nb, hkv, bs, d = _pages(pages)
+    if not isinstance(slot_map, torch.Tensor) or slot_map.dim() != 1:
+        raise ValueError("slot_map: expected an int32 tensor [T]")
+    T = slot_map.numel()
+    _expect(slot_map, "slot_map", (T,), torch.int32)
+    if (k is None) != (v is None):
+        raise ValueError("k, v: give both outputs or neither")
+    dev = _same_cuda_device([("pages", pages), ("slot_map", slot_map)])
+    geo = QCache(bs, nb, 1, float(k_scale), float(v_scale))
+    st, ctx = _on(dev, stream)
+    with ctx:
+        if k is None:
+            k = torch.empty(T, hkv, d, dtype=dtype, device=dev)
+            v = torch.empty_like(k)
+        strides = _rows(k, v, T, hkv, d)
+        if T and any(n > 1 and s == 0 for t in (k, v) for n, s in zip(t.shape[:2], t.stride())):
+            raise ValueError("k, v: output rows must not overlap")
+        _same_cuda_device([("pages", pages), ("k", k), ("v", v)])
+        buf = _qws(ws, dev, 256, st)
+        _check(_lib.kascade_qcache_read(ctypes.byref(geo), hkv, d, _dtype_code(k), _ptr(pages),
+                                        _ptr(slot_map), T, _ptr(k), _ptr(v), strides, _ptr(buf),
+                                        buf.numel(), _stream(st)), "kascade_qcache_read")
+    return k, v
+
+
+def _qattn(q, pages, block_table, kv_lens, kv_len, group_map, scale, k_scale, v_scale, pooled,
+           extra):
+    """Validated descriptor, geometry, sizes and device of one attention call."""
+    nb, hkv, bs, d = _pages(pages)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q: expected a tensor [B,Hq,d]")
+    code = _dtype_code(q)
+    B, Hq, dq = q.shape
+    if dq != d:
+        raise ValueError("q: head_dim %d, the pages hold %d" % (dq, d))
+    _expect(q, "q", q.shape, q.dtype)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table: expected an int32 tensor [B, max_blocks]")
+    width = block_table.shape[1]
+    _expect(block_table, "block_table", (B, width), torch.int32)
+    _expect(kv_lens, "kv_lens", (B,), torch.int32)
+    dev = _same_cuda_device([("q", q), ("pages", pages), ("block_table", block_table),
+                             ("kv_lens", kv_lens)] + extra)
+    N = width * bs if kv_len is None else int(kv_len)
+    desc = make_desc(B, Hq, hkv, d, N, code, scale or 0.0, group_map, pooled)
+    return desc, QCache(bs, nb, width, float(k_scale), float(v_scale)), (B, Hq, hkv, N, d), dev
+
+
+def qcache_dense_decode(q, pages, block_table, kv_lens, kv_len=None, group_map=None, scale=None,
+                        k_scale=1.0, v_scale=1.0, return_scores=False, out=None, ws=None,
+                        stream=None):
+    """Exact decode attention q [B,Hq,d] over the cached tokens of each sequence
+    -> out [B,Hq,d], or (out, scores [B,Hq,kv_len] fp32 logits, -inf behind
+    the last token). kv_len: the longest length any kv_lens[b] may have
+    (default: what the block table can hold)."""
+    extra = []
+    if out is not None:
+        _expect(out, "out", q.shape, q.dtype)
+        extra.append(("out", out))
+    desc, geo, (B, Hq, _, N, _), dev = _qattn(q, pages, block_table, kv_lens, kv_len, group_map,
+                                              scale, k_scale, v_scale, False, extra)
+    st, ctx = _on(dev, stream)
+    with ctx:
+        out = torch.empty_like(q) if out is None else out
+        scores = (torch.empty(B, Hq, N, dtype=torch.float32, device=dev) if return_scores
+                  else None)
+        buf = _qws(ws, dev, qcache_workspace_size(desc, geo, 0), st)
+        _check(_lib.kascade_qcache_dense_decode(ctypes.byref(desc), ctypes.byref(geo), _ptr(q),
+                                                _ptr(pages), _ptr(block_table), _ptr(kv_lens),
+                                                _ptr(out), _ptr(scores), _ptr(buf), buf.numel(),
+                                                _stream(st)), "kascade_qcache_dense_decode")
+    return (out, scores) if return_scores else out
+
+
+def qcache_anchor_decode(q, pages, block_table, kv_lens, topk, kv_len=None, group_map=None,
+                         scale=None, k_scale=1.0, v_scale=1.0, return_scores=False, out=None,
+                         idx=None, ws=None, stream=None, pooled=False):
+    """Anchor layer over the cache: (out [B,Hq,d], idx [B,H,topk] int32[, scores
+    [B,H,kv_len] fp32]), as anchor_decode; rows of a sequence with fewer than
+    topk tokens end in -1 entries."""
+    extra = []
+    if out is not None:
+        _expect(out, "out", q.shape, q.dtype)
+        extra.append(("out", out))
+    if idx is not None:
+        extra.append(("idx", idx))
+    desc, geo, (B, Hq, hkv, N, _), dev = _qattn(q, pages, block_table, kv_lens, kv_len, group_map,
+                                                scale, k_scale, v_scale, pooled, extra)
+    H = hkv if pooled else Hq
+    if idx is not None:
+        _expect(idx, "idx", (B, H, int(topk)), torch.int32)
+    st, ctx = _on(dev, stream)
+    with ctx:
+        out = torch.empty_like(q) if out is None else out
+        idx = torch.empty(B, H, int(topk), dtype=torch.int32, device=dev) if idx is None else idx
+        scores = torch.empty(B, H, N, dtype=torch.float32, device=dev) if return_scores else None
+        buf = _qws(ws, dev, qcache_workspace_size(desc, geo, int(topk)), st)
+        _check(_lib.kascade_qcache_anchor_decode(ctypes.byref(desc), ctypes.byref(geo), _ptr(q),
+                                                 _ptr(pages), _ptr(block_table), _ptr(kv_lens),
+                                                 int(topk), _ptr(out), _ptr(idx), _ptr(scores),
+                                                 _ptr(buf), buf.numel(), _stream(st)),
+               "kascade_qcache_anchor_decode")
+    return (out, idx, scores) if return_scores else (out, idx)
+
+
+def qcache_reuse_decode(q, pages, block_table, kv_lens, idx, kv_len=None, group_map=None,
+                        scale=None, k_scale=1.0, v_scale=1.0, out=None, ws=None, stream=None,
+                        pooled=False):
+    """Reuse layer over the cache and saved sets idx [B,Hq,topk] (pooled:
+    [B,Hkv,topk]; int32, ascending, -1 behind the last entry)."""
+    if not isinstance(idx, torch.Tensor) or idx.dim() != 3:
+        raise ValueError("idx: expected an int32 tensor [B,H,topk]")
+    extra = [("idx", idx)]
+    if out is not None:
+        _expect(out, "out", q.shape, q.dtype)
+        extra.append(("out", out))
+    desc, geo, (B, Hq, hkv, _, _), dev = _qattn(q, pages, block_table, kv_lens, kv_len, group_map,
+                                                scale, k_scale, v_scale, pooled, extra)
+    topk = idx.shape[-1]
+    _expect(idx, "idx", (B, hkv if pooled else Hq, topk), torch.int32)
+    st, ctx = _on(dev, stream)
+    with ctx:
+        out = torch.empty_like(q) if out is None else out
+        buf = _qws(ws, dev, qcache_workspace_size(desc, geo, topk), st)
+        _check(_lib.kascade_qcache_reuse_decode(ctypes.byref(desc), ctypes.byref(geo), _ptr(q),
+                                                _ptr(pages), _ptr(block_table), _ptr(kv_lens),
+                                                topk, _ptr(idx), _ptr(out), _ptr(buf),
+                                                buf.numel(), _stream(st)),
+               "kascade_qcache_reuse_decode")
+    return out
+
+
+def qcache_run_stack(qs, pages, block_table, kv_lens, topk, anchors, new_ks=None, new_vs=None,
+                     new_lens=None, free_blocks=None, free_count=None, slot_map=None, cu_new=None,
+                     kv_len=None, group_map=None, scale=None, k_scale=1.0, v_scale=1.0, outs=None,
+                     idx_buf=None, ws=None, stream=None, pooled=False):
+    """One decode step over a layer stack on paged 4-bit caches: per-layer lists
+    qs [B,Hq,d] and pages, and optionally the step's new rows new_ks, new_vs
+    [T,Hkv,d]. With new_lens [B] (and free_blocks, free_count) the step first
+    plans its blocks and slots, updating block_table, kv_lens, free_blocks and
+    free_count in place; without, new rows go to slot_map [T] and kv_lens
+    counts them already. Then every layer appends its rows and runs as anchor,
+    reuse or (before the first anchor) dense layer. Returns (outs, idx_buf)."""
+    L = len(qs)
+    if L < 1 or len(pages) != L:
+        raise ValueError("qs, pages: one tensor per layer each (got %d, %d)" % (L, len(pages)))
+    if (new_ks is None) != (new_vs is None):
+        raise ValueError("new_ks, new_vs: give both or neither")
+    if new_ks is not None and (len(new_ks) != L or len(new_vs) != L):
+        raise ValueError("new_ks, new_vs: one tensor per layer")
+    if (new_lens is None) != (free_blocks is None) or (new_lens is None) != (free_count is None):
+        raise ValueError("new_lens, free_blocks, free_count: give all or none")
+    if new_lens is None and new_ks is not None and slot_map is None:
+        raise ValueError("new rows need new_lens (a plan) or slot_map")
+    extra = []
+    desc, geo, (B, Hq, hkv, N, d), dev = _qattn(qs[0], pages[0], block_table, kv_lens, kv_len,
+                                                group_map, scale, k_scale, v_scale, pooled, extra)
+    _all_like(qs, "qs", qs[0].shape, qs[0].dtype, dev)
+    _all_like(pages, "pages", pages[0].shape, torch.uint8, dev)
+    T = 0
+    if new_ks is not None:
+        if not isinstance(new_ks[0], torch.Tensor) or new_ks[0].dim() != 3:
+            raise ValueError("new_ks[0]: expected a tensor [T,Hkv,d]")
+        T = new_ks[0].shape[0]
+        for name, ts in (("new_ks", new_ks), ("new_vs", new_vs)):
+            _all_like(ts, name, torch.Size((T, hkv, d)), qs[0].dtype, dev)
+    elif slot_map is not None:
+        T = slot_map.numel()
+    ints = [("new_lens", new_lens, (B,)), ("slot_map", slot_map, (T,)), ("cu_new", cu_new, (B + 1,)),
+            ("free_count", free_count, (1,))]
+    if free_blocks is not None:
+        ints.append(("free_blocks", free_blocks, (pages[0].shape[0],)))
+    for name, t, shape in ints:
+        if t is not None:
+            _expect(t, name, shape, torch.int32)
+            _same_cuda_device([("qs[0]", qs[0]), (name, t)])
+    H = hkv if pooled else Hq
+    if outs is not None:
+        if len(outs) != L:
+            raise ValueError("outs: one tensor per layer (got %d for %d layers)" % (len(outs), L))
+        _all_like(outs, "outs", qs[0].shape, qs[0].dtype, dev)
+    if idx_buf is not None:
+        _expect(idx_buf, "idx_buf", (B, H, int(topk)), torch.int32)
+        _same_cuda_device([("qs[0]", qs[0]), ("idx_buf", idx_buf)])
+    st, ctx = _on(dev, stream)
+    with ctx:
+        new = lambda *n: torch.empty(*n, dtype=torch.int32, device=dev)
+        outs = [torch.empty_like(q) for q in qs] if outs is None else outs
+        idx_buf = new(B, H, max(1, int(topk))) if idx_buf is None else idx_buf
+        if new_lens is not None:
+            slot_map = new(T) if slot_map is None else slot_map
+            cu_new = new(B + 1) if cu_new is None else cu_new
+        addr = lambda t: None if t is None else t.data_ptr()
+        step = QCacheStep(addr(block_table), addr(kv_lens), addr(new_lens), addr(free_blocks),
+                          addr(free_count), addr(cu_new), addr(slot_map), T)
+        buf = _qws(ws, dev, qcache_workspace_size(desc, geo, int(topk) if len(anchors) else 0), st)
+        arr = lambda ts: (ctypes.c_void_p * L)(*[t.data_ptr() for t in ts])
+        an = (ctypes.c_int32 * max(1, len(anchors)))(*[int(a) for a in anchors])
+        _check(_lib.kascade_qcache_run_stack(ctypes.byref(desc), ctypes.byref(geo),
+                                             ctypes.byref(step), L, arr(qs),
+                                             arr(new_ks) if new_ks is not None else None,
+                                             arr(new_vs) if new_vs is not None else None,
+                                             arr(pages), int(topk), an, len(anchors), arr(outs),
+                                             _ptr(idx_buf), _ptr(buf), buf.numel(), _stream(st)),
+               "kascade_qcache_run_stack")
+    return outs, idx_buf
 
 
 # -------------------------------------------------------------- scheduling --
