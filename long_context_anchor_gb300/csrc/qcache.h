@@ -51,8 +51,11 @@ struct QDecodeArgs {
   int16_t heads[kMaxQHeads];  // heads[g*G + slot]
 };
 
-// Floats of one split partial: per query head of the group m, l and d outputs.
-constexpr size_t qpart_floats(int G, int d) { return static_cast<size_t>(G) * (d + 2); }
+// Floats of one split partial: per query head of the group m and l, then (on a
+// 16-byte boundary) d outputs each.
+constexpr int qpart_head(int G) { return (2 * G + 3) & ~3; }
+constexpr size_t qpart_floats(int G, int d) { return qpart_head(G) + static_cast<size_t>(G) * d; }
+constexpr size_t qalign16(size_t x) { return (x + 15) & ~size_t(15); }
 constexpr int kQMaxCtas = 1024;   // CTAs of one attention launch at most
 
 cudaError_t launch_qdecode_dense(const QDecodeArgs& a, int head_dim, int dtype, cudaStream_t st);

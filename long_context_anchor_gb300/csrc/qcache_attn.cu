@@ -29,7 +29,8 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kPShift = 14;          // weights are held as 2^14 p
 constexpr int kQExp = 12;            // q's largest element is scaled to [2^12, 2^13)
-constexpr int kNW = 8;               // warps per CTA
+constexpr int kNW = 8;               // warps per CTA (and at most 8 heads per KV head)
+constexpr int kDenseMaxCtas = 512;   // two per SM
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                               uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -61,21 +62,29 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+// 2^x, to 2^-22; results below 2^-126 are zero
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 __device__ __forceinline__ float f16_rounded(float x) { return __half2float(__float2half_rn(x)); }
 
 // Running state of one warp over the keys of one (sequence, KV head). Thread
 // (gid = lane/4, c4 = lane%4) owns heads 2 c4, 2 c4 + 1 and output dims
 // gid * D/8 .. + D/8 of both: o[i] = (dim 2i, head 2c4), (2i, 2c4+1),
 // (2i + 1, 2c4), (2i + 1, 2c4 + 1).
+// mu = m - 14 (what the exponents subtract), finite while m is still -inf.
 template <int D>
 struct QState {
-  float m[2], l[2];
+  float m[2], mu[2], l[2];
   float o[D / 16][4];
 };
 
 template <int D>
 __device__ __forceinline__ void qstate_init(QState<D>& st) {
   st.m[0] = st.m[1] = kNegInf;
+  st.mu[0] = st.mu[1] = -kPShift;
   st.l[0] = st.l[1] = 0.f;
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) st.o[i][0] = st.o[i][1] = st.o[i][2] = st.o[i][3] = 0.f;
@@ -143,9 +152,9 @@ __device__ void load_q(const QDecodeArgs& a, int b, int g, QFrag<D, TERMS>& qf) 
   qf.mult[1] = __shfl_sync(0xffffffffu, down, 8 * c4 + 4);
 }
 
-// One slice of 16 keys in registers: the K rows of keys gid and gid + 8 (this
-// lane's D/4 elements of each), the V rows of keys 2 c4, 2 c4 + 1, 2 c4 + 8,
-// 2 c4 + 9 (elements gid * D/8 .. of each), and their scales.
+// One slice of 16 keys in registers: the K rows of score rows gid and gid + 8
+// (this lane's D/4 elements of each), the V rows of score rows 2 c4, 2 c4 + 1,
+// 2 c4 + 8, 2 c4 + 9 (elements gid * D/8 .. of each), and their scales.
 template <int D>
 struct QSlice {
   uint32_t k[2][D / 32];
@@ -154,7 +163,7 @@ struct QSlice {
   uint32_t vs[4];
 };
 
-// raw[0] = (key gid, head 2c4), raw[1] = (gid, 2c4+1), raw[2], raw[3]: gid + 8
+// raw[0] = (score row gid, head 2c4), raw[1] = (gid, 2c4+1), raw[2], raw[3]: gid + 8
 template <int D, int TERMS>
 __device__ __forceinline__ void slice_logits(const QSlice<D>& s, const QFrag<D, TERMS>& qf,
                                              float (&raw)[4]) {
@@ -187,39 +196,48 @@ __device__ __forceinline__ void slice_logits(const QSlice<D>& s, const QFrag<D, 
   for (int i = 0; i < 4; ++i) raw[i] = acc[0][i] + acc[1][i];
 }
 
-// Online softmax on the log2-domain scores x (masked entries -inf) and
-// O^T += V^T P^T. The running maximum moves only when a score exceeds it
-// (one vote), so the common slice rescales nothing. Masked keys' V scales
-// must be zero in `s` (what lies there may be anything).
-template <int D, int TERMS>
-__device__ __forceinline__ void slice_softmax_pv(QState<D>& st, const float (&x)[4],
-                                                 const QSlice<D>& s) {
-  if (__any_sync(0xffffffffu, fmaxf(x[0], x[2]) > st.m[0] || fmaxf(x[1], x[3]) > st.m[1])) {
-    float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
+// Moves the running maxima up to those of NS slices' log2-domain scores x. The
+// maximum changes rarely (one vote finds out), so the common slice rescales
+// nothing.
+template <int D, int NS>
+__device__ __forceinline__ void raise_max(QState<D>& st, const float (&x)[NS][4]) {
+  float mx0 = fmaxf(x[0][0], x[0][2]), mx1 = fmaxf(x[0][1], x[0][3]);
 #pragma unroll
-    for (int off = 4; off < 32; off <<= 1) {
-      mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
-      mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
-    }
-    const float mn0 = fmaxf(st.m[0], mx0), mn1 = fmaxf(st.m[1], mx1);
-    const float al0 = st.m[0] == kNegInf ? 0.f : fast_exp2(st.m[0] - mn0);
-    const float al1 = st.m[1] == kNegInf ? 0.f : fast_exp2(st.m[1] - mn1);
-    st.m[0] = mn0;
-    st.m[1] = mn1;
-    st.l[0] *= al0;
-    st.l[1] *= al1;
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      st.o[i][0] *= al0;
-      st.o[i][1] *= al1;
-      st.o[i][2] *= al0;
-      st.o[i][3] *= al1;
-    }
+  for (int i = 1; i < NS; ++i) {
+    mx0 = fmax3(mx0, x[i][0], x[i][2]);
+    mx1 = fmax3(mx1, x[i][1], x[i][3]);
   }
-  const float mu0 = (st.m[0] == kNegInf ? 0.f : st.m[0]) - kPShift;
-  const float mu1 = (st.m[1] == kNegInf ? 0.f : st.m[1]) - kPShift;
-  const float p0 = fast_exp2(x[0] - mu0), p1 = fast_exp2(x[1] - mu1);
-  const float p2 = fast_exp2(x[2] - mu0), p3 = fast_exp2(x[3] - mu1);
+  if (!__any_sync(0xffffffffu, mx0 > st.m[0] || mx1 > st.m[1])) return;
+#pragma unroll
+  for (int off = 4; off < 32; off <<= 1) {
+    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
+    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
+  }
+  const float mn0 = fmaxf(st.m[0], mx0), mn1 = fmaxf(st.m[1], mx1);
+  const float al0 = st.m[0] == kNegInf ? 0.f : fast_exp2(st.m[0] - mn0);
+  const float al1 = st.m[1] == kNegInf ? 0.f : fast_exp2(st.m[1] - mn1);
+  st.m[0] = mn0;
+  st.m[1] = mn1;
+  st.mu[0] = (mn0 == kNegInf ? 0.f : mn0) - kPShift;
+  st.mu[1] = (mn1 == kNegInf ? 0.f : mn1) - kPShift;
+  st.l[0] *= al0;
+  st.l[1] *= al1;
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) {
+    st.o[i][0] *= al0;
+    st.o[i][1] *= al1;
+    st.o[i][2] *= al0;
+    st.o[i][3] *= al1;
+  }
+}
+
+// The weights of one slice's scores x (masked entries -inf) under the running
+// maxima, and O^T += V^T P^T. Masked keys' V scales must be zero in `s` (what
+// lies there may be anything).
+template <int D, int TERMS>
+__device__ __forceinline__ void slice_pv(QState<D>& st, const float (&x)[4], const QSlice<D>& s) {
+  const float p0 = ex2(x[0] - st.mu[0]), p1 = ex2(x[1] - st.mu[1]);
+  const float p2 = ex2(x[2] - st.mu[0]), p3 = ex2(x[3] - st.mu[1]);
   st.l[0] += p0 + p2;
   st.l[1] += p1 + p3;
   uint32_t b[TERMS][2];
@@ -256,7 +274,7 @@ __device__ __forceinline__ void slice_softmax_pv(QState<D>& st, const float (&x)
 
 // ------------------------------------------------------------------ joining --
 // A piece is one warp's (or CTA's) state over part of a (sequence, KV head):
-// m[G], l[G] (log2-domain maximum; sum of 2^14 p), o[G][D].
+// m[G], l[G] (log2-domain maximum; sum of 2^14 p), and at qpart_head(G) o[G][D].
 template <int D>
 __device__ __forceinline__ void piece_store(float* p, QState<D>& st, int G) {
   const int lane = threadIdx.x & 31, gid = lane >> 2, c4 = lane & 3;
@@ -273,52 +291,120 @@ __device__ __forceinline__ void piece_store(float* p, QState<D>& st, int G) {
       p[h + i] = st.m[i];
       p[G + h + i] = st.l[i];
     }
-    float* o = p + 2 * G + (h + i) * D + gid * (D / 8);
+    float* o = p + qpart_head(G) + (h + i) * D + gid * (D / 8);
 #pragma unroll
-    for (int j = 0; j < D / 16; ++j)
-      *reinterpret_cast<float2*>(o + 2 * j) = make_float2(st.o[j][i], st.o[j][2 + i]);
+    for (int j = 0; j < D / 16; j += 2)
+      *reinterpret_cast<float4*>(o + 2 * j) =
+          make_float4(st.o[j][i], st.o[j][2 + i], st.o[j + 1][i], st.o[j + 1][2 + i]);
   }
+}
+
+template <bool F32>
+__device__ __forceinline__ void out_store4(const QDecodeArgs& a, size_t at, float4 y) {
+  if (F32) {
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = y;
+  } else {
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+        make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+  }
+}
+
+__device__ __forceinline__ void write_row_stat(const QDecodeArgs& a, size_t row, float m, float l) {
+  if (a.row_stat != nullptr)   // in logit units, without the 2^14
+    a.row_stat[row] = make_float2(m * kLn2, l == 0.f ? 0.f : ldexpf(1.f / l, kPShift));
 }
 
 // Join n pieces, the i-th at piece(i), with all threads of the CTA. When `dst`
 // is null the result is the output of (b, g), else the joined piece goes to
-// dst. Pieces are added in order, so the result does not depend on timing.
-template <int D, bool F32, typename Piece>
-__device__ void join_pieces(const QDecodeArgs& a, Piece piece, int n, int b, int g, float* dst) {
-  const int G = a.G;
-  for (int e = threadIdx.x; e < G * D; e += blockDim.x) {
-    const int h = e / D, dd = e % D;
+// dst. Warp h makes head h's weights of all pieces in `scratch` (n * G floats,
+// then 4 * blockDim.x), then every thread sums four dims over an equal share of
+// the pieces with its loads in flight together, and the shares are added in
+// order: the result does not depend on timing.
+template <int D, bool F32, bool GLOBAL, typename Piece>
+__device__ void join_pieces(const QDecodeArgs& a, Piece piece, int n, int b, int g, float* dst,
+                            float* scratch) {
+  __shared__ float s_m[8], s_l[8];
+  const int G = a.G, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto ld = [](const float* p) { return GLOBAL ? __ldcg(p) : *p; };
+  float4* sums = reinterpret_cast<float4*>(scratch);                       // [blockDim.x]
+  float* wts = scratch + 4 * blockDim.x;                                   // [n][G]
+  if (warp < G) {
     float M = kNegInf;
-    for (int s = 0; s < n; ++s) M = fmaxf(M, piece(s)[h]);
-    float L = 0.f, acc = 0.f;
-    for (int s = 0; s < n; ++s) {
-      const float* p = piece(s);
-      // a piece without keys has m = -inf and l = o = 0
-      const float w = p[h] == kNegInf ? 1.f : fast_exp2(p[h] - M);
-      L = fmaf(w, p[G + h], L);
-      acc = fmaf(w, p[2 * G + e], acc);
+    for (int s = lane; s < n; s += 32) {
+      const float m = ld(piece(s) + warp);
+      wts[s * G + warp] = m;
+      M = fmaxf(M, m);
     }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float L = 0.f;
+    for (int s = lane; s < n; s += 32) {
+      const float m = wts[s * G + warp];
+      // a piece without keys has m = -inf and l = o = 0
+      const float w = m == kNegInf ? 1.f : fast_exp2(m - M);
+      wts[s * G + warp] = w;
+      L = fmaf(w, ld(piece(s) + G + warp), L);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+    if (lane == 0) {
+      s_m[warp] = M;
+      s_l[warp] = L;
+    }
+  }
+  __syncthreads();
+  const int elems = G * (D / 4);                 // float4 elements: 16 .. 256
+  const int shares = static_cast<int>(blockDim.x) / elems;
+  const int e = tid % elems, share = tid / elems, h = e / (D / 4);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (share < shares) {
+    const int per = (n + shares - 1) / shares;
+    const int s1 = min(n, (share + 1) * per);
+#pragma unroll 8
+    for (int s = share * per; s < s1; ++s) {
+      const float4* p = reinterpret_cast<const float4*>(piece(s) + qpart_head(G)) + e;
+      const float4 o = GLOBAL ? __ldcg(p) : *p;
+      const float w = wts[s * G + h];
+      acc.x = fmaf(w, o.x, acc.x);
+      acc.y = fmaf(w, o.y, acc.y);
+      acc.z = fmaf(w, o.z, acc.z);
+      acc.w = fmaf(w, o.w, acc.w);
+    }
+    if (shares > 1) sums[tid] = acc;
+  }
+  __syncthreads();
+  if (share == 0) {
+    for (int k = 1; k < shares; ++k) {
+      const float4 o = sums[k * elems + e];
+      acc.x += o.x;
+      acc.y += o.y;
+      acc.z += o.z;
+      acc.w += o.w;
+    }
+    const float M = s_m[h], L = s_l[h];
+    const bool first = (e & (D / 4 - 1)) == 0;
     if (dst != nullptr) {
-      dst[2 * G + e] = acc;
-      if (dd == 0) {
+      *reinterpret_cast<float4*>(dst + qpart_head(G) + 4 * e) = acc;
+      if (first) {
         dst[h] = M;
         dst[G + h] = L;
       }
     } else {
       const size_t row = static_cast<size_t>(b) * a.Hq + a.heads[g * G + h];
-      const float y = L == 0.f ? 0.f : acc / L * a.v_scale;   // L == 0: no key at all
-      if (F32) static_cast<float*>(a.out)[row * D + dd] = y;
-      else static_cast<__nv_bfloat16*>(a.out)[row * D + dd] = __float2bfloat16_rn(y);
-      if (dd == 0 && a.row_stat != nullptr)   // in logit units, without the 2^14
-        a.row_stat[row] = make_float2(M * kLn2, L == 0.f ? 0.f : ldexpf(1.f / L, kPShift));
+      const float inv = L == 0.f ? 0.f : a.v_scale / L;   // L == 0: no key at all
+      out_store4<F32>(a, row * D + 4 * (e & (D / 4 - 1)),
+                      make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+      if (first) write_row_stat(a, row, M, L);
     }
   }
+  __syncthreads();   // scratch is free again
 }
 
 // This CTA's piece of a unit shared by n CTAs is in its place: count it, and
 // let the last CTA to arrive join all of them into the output.
 template <int D, bool F32, typename Piece>
-__device__ void arrive_and_join(const QDecodeArgs& a, int unit, Piece piece, int n, int b, int g) {
+__device__ void arrive_and_join(const QDecodeArgs& a, int unit, Piece piece, int n, int b, int g,
+                                float* scratch) {
   __shared__ unsigned int s_last;
   __threadfence();
   __syncthreads();
@@ -327,10 +413,30 @@ __device__ void arrive_and_join(const QDecodeArgs& a, int unit, Piece piece, int
   __syncthreads();
   if (s_last != 0u) {
     __threadfence();
-    join_pieces<D, F32>(a, piece, n, b, g, nullptr);
+    join_pieces<D, F32, true>(a, piece, n, b, g, nullptr, scratch);
     if (threadIdx.x == 0) a.counters[unit] = 0u;   // ready for the next launch
   }
   __syncthreads();
+}
+
+// A whole unit held by one warp: straight from its registers to the output.
+template <int D, bool F32>
+__device__ __forceinline__ void warp_output(const QDecodeArgs& a, QState<D>& st, int b, int g) {
+  const int lane = threadIdx.x & 31, gid = lane >> 2, c4 = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) st.l[i] += __shfl_xor_sync(0xffffffffu, st.l[i], off);
+    if (2 * c4 + i >= a.G) continue;
+    const size_t row = static_cast<size_t>(b) * a.Hq + a.heads[g * a.G + 2 * c4 + i];
+    const float inv = st.l[i] == 0.f ? 0.f : a.v_scale / st.l[i];
+#pragma unroll
+    for (int j = 0; j < D / 16; j += 2)
+      out_store4<F32>(a, row * D + gid * (D / 8) + 2 * j,
+                      make_float4(st.o[j][i] * inv, st.o[j][2 + i] * inv, st.o[j + 1][i] * inv,
+                                  st.o[j + 1][2 + i] * inv));
+    if (gid == 0) write_row_stat(a, row, st.m[i], st.l[i]);
+  }
 }
 
 // ------------------------------------------------------------------- slices --
@@ -360,42 +466,54 @@ __device__ __forceinline__ const uint8_t* group_at(const QDecodeArgs& a, const i
                        qgroup_bytes(D);
 }
 
-template <int N>
+// Row r of a slice's score tile is its key row_key(r): within each four rows
+// the second pair is swapped, so that the four V rows that lanes c4 = 0 .. 3
+// load together (rows 2 c4 of the tile) alternate between even and odd keys.
+// In shared memory at d = 128 (64-byte rows) that halves their bank conflicts.
+__device__ __forceinline__ int row_key(int r) { return r ^ ((r >> 1) & 1); }
+// key of a slice that V register i of this lane belongs to
+__device__ __forceinline__ int v_key(int i) {
+  return row_key(2 * (threadIdx.x & 3) + (i & 1)) + 8 * (i >> 1);
+}
+
+// Loads from global memory (through the read-only path) or from shared memory.
+template <bool SHARED, typename T>
+__device__ __forceinline__ T load_as(const uint8_t* p) {
+  const T* q = reinterpret_cast<const T*>(p);
+  return SHARED ? *q : __ldg(q);
+}
+template <bool SHARED, int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
   static_assert(N == 1 || N == 2 || N == 4, "one vector load");
   if (N == 4) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 v = load_as<SHARED, uint4>(p);
     w[0] = v.x;
     w[N / 4] = v.y;
     w[N / 2] = v.z;
     w[N - 1] = v.w;
   } else if (N == 2) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+    const uint2 v = load_as<SHARED, uint2>(p);
     w[0] = v.x;
     w[N - 1] = v.y;
   } else {
-    w[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+    w[0] = load_as<SHARED, uint32_t>(p);
   }
 }
 
 // This lane's part of the K row (grp, r) and of the V row (grp, r).
-template <int D>
+template <int D, bool SHARED>
 __device__ __forceinline__ void load_k_row(QSlice<D>& s, int i, const uint8_t* grp, int r) {
   const int c4 = threadIdx.x & 3;
-  load_words(grp + r * (D / 2) + c4 * (D / 8), s.k[i]);
-  const uint8_t* sc = grp + 8 * D + r * (D / 16);
-  s.ks[i] = D == 128 ? __ldg(reinterpret_cast<const uint16_t*>(sc) + c4)
-                     : static_cast<uint32_t>(__ldg(sc + c4));
+  load_words<SHARED>(grp + r * (D / 2) + c4 * (D / 8), s.k[i]);
+  const uint8_t* sc = grp + 8 * D + r * (D / 16) + c4 * (D / 64);
+  s.ks[i] = D == 128 ? static_cast<uint32_t>(load_as<SHARED, uint16_t>(sc))
+                     : static_cast<uint32_t>(load_as<SHARED, uint8_t>(sc));
 }
-template <int D>
+template <int D, bool SHARED>
 __device__ __forceinline__ void load_v_row(QSlice<D>& s, int i, const uint8_t* grp, int r) {
   const int gid = (threadIdx.x & 31) >> 2;
-  load_words(grp + 9 * D + r * (D / 2) + gid * (D / 16), s.v[i]);
-  s.vs[i] = __ldg(grp + 17 * D + r * (D / 16) + gid * D / 128);
-}
-// key of a slice that V register i of this lane belongs to
-__device__ __forceinline__ int v_key(int i) {
-  return 2 * (threadIdx.x & 3) + (i & 1) + 8 * (i >> 1);
+  load_words<SHARED>(grp + 9 * D + r * (D / 2) + gid * (D / 16), s.v[i]);
+  s.vs[i] = load_as<SHARED, uint8_t>(grp + 17 * D + r * (D / 16) + gid * D / 128);
 }
 
 // -------------------------------------------------------------------- dense --
@@ -405,7 +523,38 @@ __device__ __forceinline__ int v_key(int i) {
 // units: the warp's pieces of units it does not hold alone go to shared
 // memory, the CTA joins those of its warps after one barrier, and a unit that
 // several CTAs share is joined by the last of them to arrive.
-constexpr int kMinRun = 4;   // slices per warp at least
+//
+// Every warp feeds itself: a ring of kDenseStages stages of two slices, each
+// filled by bulk copies (a group of the cache is one contiguous piece, so a
+// slice is one copy) that lane 0 issues as soon as the warp has left the
+// stage; no warp waits for another one before the end.
+constexpr int kMinRun = 4;        // slices per warp at least
+constexpr int kStep = 2;          // slices per stage
+constexpr int kDenseStages = 2;
+
+// Where a warp is in the line of slices.
+struct Cursor {
+  int f;        // first slice of the line not covered by earlier units of this run
+  int b, g;     // unit
+  int nb;       // its slices
+  int s0, s, s1;   // this run's part of them: [s0, s1), next one s
+};
+__device__ __forceinline__ void cursor_enter(Cursor& c, const int* pref, int B, int Hkv, int f,
+                                             int end) {
+  int lo = 0, hi = B;   // the sequence: pref[lo] * Hkv <= f < pref[lo + 1] * Hkv
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (pref[mid] * Hkv <= f) lo = mid;
+    else hi = mid;
+  }
+  c.f = f;
+  c.b = lo;
+  c.nb = pref[lo + 1] - pref[lo];
+  const int in = f - pref[lo] * Hkv;
+  c.g = in / c.nb;
+  c.s0 = c.s = in - c.g * c.nb;
+  c.s1 = min(c.nb, c.s0 + end - f);
+}
 
 template <int D, int TERMS>
 __global__ void __launch_bounds__(kNW * 32, 2)
@@ -413,15 +562,27 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   pdl_wait();
   pdl_trigger();
   constexpr bool F32 = TERMS == 2;
+  constexpr int kGroupBytes = qgroup_bytes(D), kStageBytes = kStep * kGroupBytes;
   extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ __align__(8) uint64_t s_full[kNW][kDenseStages];
+  __shared__ unsigned char s_have[kNW][kDenseStages];   // bit i: slice i of the stage was copied
   __shared__ int s_tot[kNW];
   __shared__ int s_unit[2 * kNW], s_list[2 * kNW], s_nlist;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, c4 = lane & 3;
   const int pf = static_cast<int>(qpart_floats(a.G, D));
-  float* slots = reinterpret_cast<float*>(smem);                 // [2 kNW][pf]
-  int* pref = reinterpret_cast<int*>(slots + 2 * kNW * pf);      // [B + 1] slices before b, per head
+  // a ring per warp, which at the end holds the warp's last piece; a place for
+  // its first piece; slices before every sequence, per head
+  uint8_t* ring = smem + warp * kDenseStages * kStageBytes;
+  float* firsts = reinterpret_cast<float*>(smem + kNW * kDenseStages * kStageBytes);   // [kNW][pf]
+  int* pref = reinterpret_cast<int*>(firsts + kNW * pf);                               // [B + 1]
+  auto slot_at = [&](int i) -> float* {   // slot 2w: warp w's first piece, 2w + 1: its last
+    return (i & 1) ? reinterpret_cast<float*>(smem + (i >> 1) * kDenseStages * kStageBytes)
+                   : firsts + (i >> 1) * pf;
+  };
 
-  // slices before every sequence
+  if (lane == 0)
+    for (int i = 0; i < kDenseStages; ++i) mbar_init(&s_full[warp][i], 1);
+  if (tid == 0) fence_barrier_init();
   int carry = 0;
   for (int b0 = 0; b0 < a.B; b0 += kNW * 32) {
     const int b = b0 + tid;
@@ -444,6 +605,7 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   }
   if (tid == 0) pref[a.B] = carry;
   if (tid < 2 * kNW) s_unit[tid] = -1;
+  fence_barrier_init();
   __syncthreads();
   const int total = carry * a.Hkv;
   const int nwarps = static_cast<int>(gridDim.x) * kNW;
@@ -451,22 +613,65 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   const int w0 = min(total, (static_cast<int>(blockIdx.x) * kNW + warp) * per);
   const int w1 = min(total, w0 + per);
 
-  QState<D> st;
-  for (int f = w0; f < w1;) {
-    int lo = 0, hi = a.B;   // the sequence: pref[lo] * Hkv <= f < pref[lo + 1] * Hkv
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (pref[mid] * a.Hkv <= f) lo = mid;
-      else hi = mid;
+  // ---- copies: `in` runs ahead of the arithmetic by up to kDenseStages steps
+  Cursor in = {}, at;
+  int ids = 0, ids_base = 0, ids_key = -1;   // lane i: block of slice ids_base + i of sequence ids_key
+  int issued = 0, taken = 0;
+  bool alive = true;
+  auto issue = [&]() {   // all lanes
+    if (in.s == in.s1) {
+      if (in.f + in.s1 - in.s0 >= w1) return;
+      cursor_enter(in, pref, a.B, a.Hkv, in.f + in.s1 - in.s0, w1);
     }
-    const int b = lo, nb = pref[b + 1] - pref[b];
-    const int g = (f - pref[b] * a.Hkv) / nb;
-    const int s0 = f - pref[b] * a.Hkv - g * nb;
-    const int s1 = min(nb, s0 + w1 - f);
-    const int n = len_of(a, b, false);
-    const int32_t* trow = a.table + static_cast<size_t>(b) * a.max_blocks;
+    const int sh = a.bs_shift - 4;
+    if (ids_key != in.b || in.s < ids_base || in.s + kStep > ids_base + 32) {
+      ids_key = in.b;
+      ids_base = in.s;
+      const int s = in.s + lane;
+      ids = s < in.nb ? __ldg(a.table + static_cast<size_t>(in.b) * a.max_blocks + (s >> sh)) : -1;
+    }
+    const int stage = issued % kDenseStages;
+    uint8_t* dst = ring + stage * kStageBytes;
+    int block[kStep];
+    unsigned int have = 0u;
+#pragma unroll
+    for (int i = 0; i < kStep; ++i) {
+      block[i] = __shfl_sync(0xffffffffu, ids, (in.s + i - ids_base) & 31);
+      if (in.s + i < in.s1) {
+        if (block[i] >= 0 && block[i] < a.num_blocks) have |= 1u << i;
+        else report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x522);
+      }
+    }
+    if (lane == 0) {
+      s_have[warp][stage] = static_cast<unsigned char>(have);
+      mbar_arrive_expect_tx(&s_full[warp][stage], __popc(have) * kGroupBytes);
+#pragma unroll
+      for (int i = 0; i < kStep; ++i)
+        if ((have >> i) & 1u) {
+          const int s = in.s + i;
+          const size_t grp = ((static_cast<size_t>(block[i]) * a.Hkv + in.g) << sh) +
+                             (s & ((1 << sh) - 1));
+          bulk_load(dst + i * kGroupBytes, a.cache + grp * kGroupBytes, kGroupBytes,
+                    &s_full[warp][stage]);
+        }
+    }
+    in.s = min(in.s1, in.s + kStep);
+    ++issued;
+  };
+  if (w0 < w1) {
+    cursor_enter(in, pref, a.B, a.Hkv, w0, w1);
+#pragma unroll
+    for (int i = 0; i < kDenseStages; ++i) issue();
+  }
+
+  // ---- arithmetic
+  const int row0 = row_key(gid);   // keys row0 and row0 + 8 of a slice
+  for (int f = w0; f < w1;) {
+    cursor_enter(at, pref, a.B, a.Hkv, f, w1);
+    const int b = at.b, g = at.g, n = len_of(a, b, false);
     QFrag<D, TERMS> qf;
     load_q(a, b, g, qf);
+    QState<D> st;
     qstate_init(st);
     float* sp[2] = {nullptr, nullptr};
     if (a.scores != nullptr)
@@ -474,57 +679,80 @@ __global__ void __launch_bounds__(kNW * 32, 2)
       for (int i = 0; i < 2; ++i)
         if (2 * c4 + i < a.G)
           sp[i] = a.scores + (static_cast<size_t>(b) * a.Hq + a.heads[g * a.G + 2 * c4 + i]) * a.N;
-    for (int s = s0; s < s1; ++s) {
-      const uint8_t* grp = group_at<D>(a, trow, g, s);
-      const int key0 = 16 * s + gid;
-      float lg[4] = {kNegInf, kNegInf, kNegInf, kNegInf};
-      QSlice<D> sl;
-      if (grp != nullptr) {
-        load_k_row(sl, 0, grp, gid);
-        load_k_row(sl, 1, grp, gid + 8);
+    const float ml[2] = {qf.mult[0] * kLog2e, qf.mult[1] * kLog2e};
+    while (at.s < at.s1 && alive) {
+      const int stage = taken % kDenseStages;
+      if (!mbar_wait_warp(&s_full[warp][stage], (taken / kDenseStages) & 1, a.err, 0x531)) {
+        // a wait that gave up (reported): leave no copy in flight, and pass over
+        // the rest of the run so that every unit still gets its arrivals
+        for (; taken < issued; ++taken)
+          mbar_wait_warp(&s_full[warp][taken % kDenseStages], (taken / kDenseStages) & 1, a.err,
+                         0x532);
+        alive = false;
+        break;
+      }
+      ++taken;
+      const uint8_t* buf = ring + stage * kStageBytes;
+      const unsigned int have = s_have[warp][stage];
+      float x[kStep][4];
+      QSlice<D> sl[kStep];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) load_v_row(sl, i, grp, v_key(i));
-        slice_logits(sl, qf, lg);
+      for (int i = 0; i < kStep; ++i) {
+        load_k_row<D, true>(sl[i], 0, buf + i * kGroupBytes, row0);
+        load_k_row<D, true>(sl[i], 1, buf + i * kGroupBytes, row0 + 8);
+        slice_logits(sl[i], qf, x[i]);
+      }
+      // keys that do not count: behind the sequence's end, in a stage half that
+      // belongs to no slice of this run, in a block the table does not name
+      const bool full = have == (1u << kStep) - 1u && 16 * (at.s + kStep) <= n;
+      if (!full) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) lg[i] *= qf.mult[i & 1];
-        if (16 * s + 16 > n) {   // the sequence ends inside this slice
+        for (int i = 0; i < kStep; ++i)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            if (key0 + 8 * (i >> 1) >= n) lg[i] = kNegInf;
-            if (16 * s + v_key(i) >= n) sl.vs[i] = 0u;
+          for (int j = 0; j < 4; ++j)
+            if (!((have >> i) & 1u) || 16 * (at.s + i) + row0 + 8 * (j >> 1) >= n) x[i][j] = kNegInf;
+      }
+      if (a.scores != nullptr) {
+#pragma unroll
+        for (int i = 0; i < kStep; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int key = 16 * (at.s + i) + row0 + 8 * (j >> 1);
+            if (sp[j & 1] != nullptr && (full || (at.s + i < at.s1 && key < n)))
+              sp[j & 1][key] = x[i][j] * qf.mult[j & 1];
           }
+      }
+#pragma unroll
+      for (int i = 0; i < kStep; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[i][j] *= ml[j & 1];
+      raise_max<D, kStep>(st, x);
+#pragma unroll
+      for (int i = 0; i < kStep; ++i) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) load_v_row<D, true>(sl[i], j, buf + i * kGroupBytes, v_key(j));
+        if (!full) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (!((have >> i) & 1u) || 16 * (at.s + i) + v_key(j) >= n) sl[i].vs[j] = 0u;
         }
+        slice_pv<D, TERMS>(st, x[i], sl[i]);
       }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (sp[i & 1] != nullptr && key0 + 8 * (i >> 1) < n) sp[i & 1][key0 + 8 * (i >> 1)] = lg[i];
-      if (grp == nullptr) continue;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) lg[i] *= kLog2e;
-      slice_softmax_pv<D, TERMS>(st, lg, sl);
-    }
-    // a warp's run holds at most its first and its last unit in part
-    const int slot = 2 * warp + (f == w0 ? 0 : 1);
-    const bool whole = s0 == 0 && s1 == nb;
-    piece_store<D>(slots + slot * pf, st, a.G);
-    if (!whole) {
-      if (lane == 0) s_unit[slot] = b * a.Hkv + g;
-    } else {
+      at.s = min(at.s1, at.s + kStep);
+      // the stage is refilled through the async proxy: this warp's reads first
+      fence_proxy_async_smem();
       __syncwarp();
-      const float* p = slots + slot * pf;
-      for (int e = lane; e < a.G * D; e += 32) {
-        const int h = e / D;
-        const size_t row = static_cast<size_t>(b) * a.Hq + a.heads[g * a.G + h];
-        const float L = p[a.G + h];
-        const float y = L == 0.f ? 0.f : p[2 * a.G + e] / L * a.v_scale;
-        if (F32) static_cast<float*>(a.out)[row * D + e % D] = y;
-        else static_cast<__nv_bfloat16*>(a.out)[row * D + e % D] = __float2bfloat16_rn(y);
-        if (e % D == 0 && a.row_stat != nullptr)
-          a.row_stat[row] = make_float2(p[h] * kLn2, L == 0.f ? 0.f : ldexpf(1.f / L, kPShift));
-      }
-      __syncwarp();   // the slot is used again
+      issue();
     }
-    f += s1 - s0;
+    f += at.s1 - at.s0;
+    if (at.s0 == 0 && at.s1 == at.nb) {
+      warp_output<D, F32>(a, st, b, g);
+    } else {
+      // in part: a run's first unit or its last (whose ring is free by then)
+      const int slot = 2 * warp + (at.f == w0 ? 0 : 1);
+      piece_store<D>(slot_at(slot), st, a.G);
+      if (lane == 0) s_unit[slot] = b * a.Hkv + g;
+    }
   }
   __syncthreads();
   if (tid == 0) {
@@ -536,44 +764,49 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   __syncthreads();
   const int nlist = s_nlist;
   const int per_cta = per * kNW, c0 = static_cast<int>(blockIdx.x) * per_cta;
+  float* scratch = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(pref) +
+                                            qalign16((static_cast<size_t>(a.B) + 1) * sizeof(int)));
+  // this CTA's units: joined here if it holds all of one, else its piece goes
+  // to CTA c's place 2c + 1 (a unit that starts inside c's run) or 2c (one
+  // that started before it, or with it)
+  const size_t stride = qpart_floats(a.G, D);
+  int shared_unit[2], shared = 0;
   for (int i = 0; i < nlist;) {
     const int unit = s_unit[s_list[i]];
     int j = i;
     while (j < nlist && s_unit[s_list[j]] == unit) ++j;
     const int b = unit / a.Hkv, g = unit % a.Hkv, nb = pref[b + 1] - pref[b];
     const int u0 = pref[b] * a.Hkv + g * nb, u1 = u0 + nb;   // the unit's slices
-    auto mine = [&](int s) -> const float* { return slots + s_list[i + s] * pf; };
-    const int first = u0 / per_cta, ncta = (u1 - 1) / per_cta - first + 1;
-    if (ncta == 1) {
-      join_pieces<D, F32>(a, mine, j - i, b, g, nullptr);
-    } else {
-      // CTA c keeps the piece of a unit that starts inside its run at 2c + 1,
-      // of one that started before it (or with it) at 2c
-      float* part = a.part;
-      const size_t stride = qpart_floats(a.G, D);
-      join_pieces<D, F32>(a, mine, j - i, b, g,
-                          part + (2 * static_cast<size_t>(blockIdx.x) + (u0 > c0 ? 1 : 0)) * stride);
-      const int odd = u0 > first * per_cta ? 1 : 0;
-      auto all = [=](int s) -> const float* {
-        return part + (2 * static_cast<size_t>(first + s) + (s == 0 ? odd : 0)) * stride;
-      };
-      arrive_and_join<D, F32>(a, unit, all, ncta, b, g);
+    auto mine = [&](int s) -> const float* { return slot_at(s_list[i + s]); };
+    float* dst = nullptr;
+    if (u0 < c0 || u1 > c0 + per_cta) {
+      dst = a.part + (2 * static_cast<size_t>(blockIdx.x) + (u0 > c0 ? 1 : 0)) * stride;
+      shared_unit[shared++ & 1] = unit;
     }
+    join_pieces<D, F32, false>(a, mine, j - i, b, g, dst, scratch);
     i = j;
+  }
+  // units shared with other CTAs (at most the first and the last); the rings are free
+  for (int k = 0; k < shared; ++k) {
+    const int unit = shared_unit[k & 1];
+    const int b = unit / a.Hkv, g = unit % a.Hkv, nb = pref[b + 1] - pref[b];
+    const int u0 = pref[b] * a.Hkv + g * nb;
+    const int first = u0 / per_cta, ncta = (u0 + nb - 1) / per_cta - first + 1;
+    const float* part = a.part;
+    const int odd = u0 > first * per_cta ? 1 : 0;
+    auto all = [=](int s) -> const float* {
+      return part + (2 * static_cast<size_t>(first + s) + (s == 0 ? odd : 0)) * stride;
+    };
+    arrive_and_join<D, F32>(a, unit, all, ncta, b, g, reinterpret_cast<float*>(smem));
   }
   // sequences without keys: zeros; scores behind the last key
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-    const int n = len_of(a, b, false);
-    if (n == 0) {
-      const size_t base = static_cast<size_t>(b) * a.Hq * D;
-      for (int e = tid; e < a.Hq * D; e += blockDim.x) {
-        if (F32) static_cast<float*>(a.out)[base + e] = 0.f;
-        else static_cast<__nv_bfloat16*>(a.out)[base + e] = __float2bfloat16_rn(0.f);
-      }
-      if (a.row_stat != nullptr)
-        for (int h = tid; h < a.Hq; h += blockDim.x)
-          a.row_stat[static_cast<size_t>(b) * a.Hq + h] = make_float2(kNegInf, 0.f);
-    }
+    if (pref[b + 1] != pref[b]) continue;
+    const size_t base = static_cast<size_t>(b) * a.Hq * D;
+    for (int e = 4 * tid; e < a.Hq * D; e += 4 * kNW * 32)
+      out_store4<F32>(a, base + e, make_float4(0.f, 0.f, 0.f, 0.f));
+    for (int h = tid; h < a.Hq; h += kNW * 32)
+      write_row_stat(a, static_cast<size_t>(b) * a.Hq + h, kNegInf, 0.f);
   }
   if (a.scores != nullptr && a.fill_tail)
     for (int r = blockIdx.x; r < a.B * a.Hq; r += gridDim.x)
@@ -678,17 +911,17 @@ __global__ void __launch_bounds__(kNW * 32, 2)
     if (grp == nullptr) mask = 0u;
     const unsigned long long base = reinterpret_cast<unsigned long long>(grp);
     QSlice<D> s;
-    float lg[4];
+    float x[1][4];
     uint32_t mk[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int src = gid + 8 * i;
+      const int src = row_key(gid) + 8 * i;
       const uint8_t* p =
           reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, base, src));
       const int r = __shfl_sync(0xffffffffu, key, src) & 15;
       mk[i] = __shfl_sync(0xffffffffu, mask, src);
       if (mk[i] != 0u) {
-        load_k_row(s, i, p, r);
+        load_k_row<D, false>(s, i, p, r);
       } else {
 #pragma unroll
         for (int w = 0; w < D / 32; ++w) s.k[i][w] = 0u;
@@ -702,18 +935,18 @@ __global__ void __launch_bounds__(kNW * 32, 2)
           reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, base, src));
       const int r = __shfl_sync(0xffffffffu, key, src) & 15;
       if (p != nullptr) {
-        load_v_row(s, i, p, r);
+        load_v_row<D, false>(s, i, p, r);
       } else {
 #pragma unroll
         for (int w = 0; w < D / 64; ++w) s.v[i][w] = 0u;
         s.vs[i] = 0u;
       }
     }
-    slice_logits(s, qf, lg);
+    slice_logits(s, qf, x[0]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const bool in = (mk[i >> 1] >> (2 * c4 + (i & 1))) & 1u;
-      lg[i] = in ? lg[i] * qf.mult[i & 1] * kLog2e : kNegInf;
+      x[0][i] = in ? x[0][i] * (qf.mult[i & 1] * kLog2e) : kNegInf;
     }
     // A V block that holds a NaN (scale 0x7f or 0xff) would reach every head of
     // the group through 0 * NaN in the product: it is taken out of the slice,
@@ -737,7 +970,8 @@ __global__ void __launch_bounds__(kNW * 32, 2)
         nan_heads >>= 2 * c4;
       }
     }
-    slice_softmax_pv<D, TERMS>(st, lg, s);
+    raise_max<D, 1>(st, x);
+    slice_pv<D, TERMS>(st, x[0], s);
     if (!POOLED && (nan_heads & 3u) != 0u) {
 #pragma unroll
       for (int j = 0; j < D / 16; ++j)
@@ -748,15 +982,17 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   }
   piece_store<D>(slots + warp * pf, st, a.G);
   __syncthreads();
+  float* scratch = slots + kNW * pf;
   auto mine = [&](int w) -> const float* { return slots + w * pf; };
   if (a.S == 1) {
-    join_pieces<D, F32>(a, mine, kNW, b, g, nullptr);
+    join_pieces<D, F32, false>(a, mine, kNW, b, g, nullptr, scratch);
     return;
   }
   float* part = a.part + static_cast<size_t>(unit) * a.S * pf;
-  join_pieces<D, F32>(a, mine, kNW, b, g, part + static_cast<size_t>(blockIdx.x) * pf);
+  join_pieces<D, F32, false>(a, mine, kNW, b, g, part + static_cast<size_t>(blockIdx.x) * pf,
+                      scratch);
   auto all = [=](int w) -> const float* { return part + static_cast<size_t>(w) * pf; };
-  arrive_and_join<D, F32>(a, unit, all, a.S, b, g);
+  arrive_and_join<D, F32>(a, unit, all, a.S, b, g, scratch);
 }
 
 // CTAs of a kernel that the current device holds at once (asked once per host
@@ -789,18 +1025,27 @@ cudaError_t resident_ctas(K kern, size_t smem, int& ctas) {
 
 template <int D, int TERMS>
 cudaError_t launch_dense_t(const QDecodeArgs& a, cudaStream_t st) {
-  const size_t smem = 2 * kNW * qpart_floats(a.G, D) * sizeof(float) +
-                      (static_cast<size_t>(a.B) + 1) * sizeof(int);
+  // rings (at the end the scratch of joins between CTAs), first pieces, prefix,
+  // the scratch of joins between the CTA's warps
+  constexpr size_t kRings = kNW * kDenseStages * kStep * qgroup_bytes(D);
+  static_assert(kRings >= (4 * kNW * 32 + static_cast<size_t>(kDenseMaxCtas) * 8) * sizeof(float),
+                "weights of one piece per CTA");
+  static_assert(kDenseStages * kStep * qgroup_bytes(D) >= qpart_floats(8, D) * sizeof(float),
+                "a warp's last piece in its ring");
+  const size_t smem = kRings + kNW * qpart_floats(a.G, D) * sizeof(float) +
+                      qalign16((static_cast<size_t>(a.B) + 1) * sizeof(int)) +
+                      (4 * kNW * 32 + 2 * kNW * static_cast<size_t>(a.G)) * sizeof(float);
   auto kern = k_qdecode_dense<D, TERMS>;
   int ctas = 0;
   const cudaError_t e = resident_ctas(kern, smem, ctas);
   if (e != cudaSuccess) return e;
+  if (ctas > kDenseMaxCtas) ctas = kDenseMaxCtas;
   return launch_pdl(kern, dim3(ctas), dim3(kNW * 32), smem, st, a);
 }
 
 template <int D, int TERMS, bool POOLED>
 cudaError_t launch_reuse_t(const QDecodeArgs& a, cudaStream_t st) {
-  const size_t smem = kNW * qpart_floats(a.G, D) * sizeof(float);
+  const size_t smem = (kNW * qpart_floats(a.G, D) + 4 * kNW * 32 + kMaxSplits * a.G) * sizeof(float);
   auto kern = k_qdecode_reuse<D, TERMS, POOLED>;
   int ctas = 0;
   const cudaError_t e = resident_ctas(kern, smem, ctas);
@@ -812,6 +1057,7 @@ cudaError_t launch_reuse_t(const QDecodeArgs& a, cudaStream_t st) {
                           : (a.G * a.topk + 16 * kNW - 1) / (16 * kNW);
   int s = ctas / units;
   if (s > most) s = most;
+  if (s > kMaxSplits) s = kMaxSplits;   // the last CTA joins that many pieces
   u.S = s < 1 ? 1 : s;
   return launch_pdl(kern, dim3(u.S, units), dim3(kNW * 32), smem, st, u);
 }
