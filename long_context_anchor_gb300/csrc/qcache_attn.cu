@@ -147,7 +147,8 @@ __device__ void load_q(const QDecodeArgs& a, int b, int g, QFrag<D, TERMS>& qf) 
       if (TERMS == 2) qf.f[TERMS - 1][i][j] = pack_f16(lo - f16_rounded(lo), hi - f16_rounded(hi));
     }
   }
-  const float down = a.scale * ldexpf(1.f, e - kQExp);
+  // positive even where it underflows: masked scores are -inf times it
+  const float down = fmaxf(a.scale * ldexpf(1.f, e - kQExp), 1e-37f);
   qf.mult[0] = __shfl_sync(0xffffffffu, down, 8 * c4);
   qf.mult[1] = __shfl_sync(0xffffffffu, down, 8 * c4 + 4);
 }
@@ -167,7 +168,7 @@ struct QSlice {
 template <int D, int TERMS>
 __device__ __forceinline__ void slice_logits(const QSlice<D>& s, const QFrag<D, TERMS>& qf,
                                              float (&raw)[4]) {
-  float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+  raw[0] = raw[1] = raw[2] = raw[3] = 0.f;
   uint32_t sc[2][D / 64];
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
@@ -188,12 +189,10 @@ __device__ __forceinline__ void slice_logits(const QSlice<D>& s, const QFrag<D, 
     }
 #pragma unroll
     for (int t = 0; t < TERMS; ++t) {
-      mma_f16_16816(acc[0], x[0], y[0], x[1], y[1], qf.f[t][2 * w][0], qf.f[t][2 * w][1]);
-      mma_f16_16816(acc[1], x[2], y[2], x[3], y[3], qf.f[t][2 * w + 1][0], qf.f[t][2 * w + 1][1]);
+      mma_f16_16816(raw, x[0], y[0], x[1], y[1], qf.f[t][2 * w][0], qf.f[t][2 * w][1]);
+      mma_f16_16816(raw, x[2], y[2], x[3], y[3], qf.f[t][2 * w + 1][0], qf.f[t][2 * w + 1][1]);
     }
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) raw[i] = acc[0][i] + acc[1][i];
 }
 
 // Moves the running maxima up to those of NS slices' log2-domain scores x. The
@@ -231,24 +230,20 @@ __device__ __forceinline__ void raise_max(QState<D>& st, const float (&x)[NS][4]
   }
 }
 
-// The weights of one slice's scores x (masked entries -inf) under the running
-// maxima, and O^T += V^T P^T. Masked keys' V scales must be zero in `s` (what
-// lies there may be anything).
+// O^T += V^T P^T with one slice's weights p. Masked keys' V scales must be zero
+// in `s` (what lies there may be anything).
 template <int D, int TERMS>
-__device__ __forceinline__ void slice_pv(QState<D>& st, const float (&x)[4], const QSlice<D>& s) {
-  const float p0 = ex2(x[0] - st.mu[0]), p1 = ex2(x[1] - st.mu[1]);
-  const float p2 = ex2(x[2] - st.mu[0]), p3 = ex2(x[3] - st.mu[1]);
-  st.l[0] += p0 + p2;
-  st.l[1] += p1 + p3;
+__device__ __forceinline__ void slice_pv(float (&o)[D / 16][4], const float (&p)[4],
+                                         const QSlice<D>& s) {
   uint32_t b[TERMS][2];
-  b[0][0] = movmatrix_t(pack_f16(p0, p1));
-  b[0][1] = movmatrix_t(pack_f16(p2, p3));
+  b[0][0] = movmatrix_t(pack_f16(p[0], p[1]));
+  b[0][1] = movmatrix_t(pack_f16(p[2], p[3]));
   if (TERMS == 2) {
-    b[TERMS - 1][0] = movmatrix_t(pack_f16(p0 - f16_rounded(p0), p1 - f16_rounded(p1)));
-    b[TERMS - 1][1] = movmatrix_t(pack_f16(p2 - f16_rounded(p2), p3 - f16_rounded(p3)));
+    b[TERMS - 1][0] = movmatrix_t(pack_f16(p[0] - f16_rounded(p[0]), p[1] - f16_rounded(p[1])));
+    b[TERMS - 1][1] = movmatrix_t(pack_f16(p[2] - f16_rounded(p[2]), p[3] - f16_rounded(p[3])));
   }
-  const uint32_t s01 = cvt_e4m3x2(s.vs[0] | (s.vs[1] << 8));
-  const uint32_t s23 = cvt_e4m3x2(s.vs[2] | (s.vs[3] << 8));
+  const uint32_t s01 = cvt_e4m3x2(__byte_perm(s.vs[0], s.vs[1], 0x0040));
+  const uint32_t s23 = cvt_e4m3x2(__byte_perm(s.vs[2], s.vs[3], 0x0040));
 #pragma unroll
   for (int w = 0; w < D / 64; ++w) {
     // codes of one element of two keys side by side: even elements, odd ones
@@ -267,7 +262,7 @@ __device__ __forceinline__ void slice_pv(QState<D>& st, const float (&x)[4], con
       const uint32_t a2 = hmul2(eb[i], s23), a3 = hmul2(db[i], s23);
 #pragma unroll
       for (int t = 0; t < TERMS; ++t)
-        mma_f16_16816(st.o[4 * w + i], a0, a1, a2, a3, b[t][0], b[t][1]);
+        mma_f16_16816(o[4 * w + i], a0, a1, a2, a3, b[t][0], b[t][1]);
     }
   }
 }
@@ -517,61 +512,64 @@ __device__ __forceinline__ void load_v_row(QSlice<D>& s, int i, const uint8_t* g
 }
 
 // -------------------------------------------------------------------- dense --
-// The slices of all units (unit = sequence * Hkv + KV head; a sequence of n
-// keys has ceil(n / 16) per head) form one line, and every warp of the grid
-// takes an equal run of it, so that ragged batches balance. A run may span
-// units: the warp's pieces of units it does not hold alone go to shared
-// memory, the CTA joins those of its warps after one barrier, and a unit that
-// several CTAs share is joined by the last of them to arrive.
+// The steps of all units (unit = sequence * Hkv + KV head; a step is 16 *
+// kStep keys, and a sequence of n keys has ceil(n / (16 kStep)) per head) form one
+// line, and every warp of the grid takes an equal run of it, so that ragged
+// batches balance. A run may span units: the warp's pieces of units it does
+// not hold alone go to shared memory, the CTA joins those of its warps after
+// one barrier, and a unit that several CTAs share is joined by the last of
+// them to arrive.
 //
-// Every warp feeds itself: a ring of kDenseStages stages of two slices, each
-// filled by bulk copies (a group of the cache is one contiguous piece, so a
-// slice is one copy) that lane 0 issues as soon as the warp has left the
-// stage; no warp waits for another one before the end.
-constexpr int kMinRun = 4;        // slices per warp at least
-constexpr int kStep = 2;          // slices per stage
+// Every warp feeds itself: a ring of kDenseStages stages of one step, each
+// filled by one bulk copy per block that the step touches (groups of a block
+// are contiguous), which the first lanes issue as soon as the warp has left
+// the stage; no warp waits for another one before the end.
+constexpr int kMinRun = 2;        // steps per warp at least
 constexpr int kDenseStages = 2;
+template <int D>
+constexpr int kStepOf = 256 / D;  // slices per step: 4608 bytes either way
 
-// Where a warp is in the line of slices.
+// Where a warp is in the line of steps.
 struct Cursor {
-  int f;        // first slice of the line not covered by earlier units of this run
-  int b, g;     // unit
-  int nb;       // its slices
+  int f;           // its run's first step of this unit
+  int b, g, n;     // unit, cached tokens
+  int ns;          // steps of the unit
   int s0, s, s1;   // this run's part of them: [s0, s1), next one s
 };
-__device__ __forceinline__ void cursor_enter(Cursor& c, const int* pref, int B, int Hkv, int f,
-                                             int end) {
-  int lo = 0, hi = B;   // the sequence: pref[lo] * Hkv <= f < pref[lo + 1] * Hkv
+__device__ __forceinline__ void cursor_enter(Cursor& c, const QDecodeArgs& a, const int* pref,
+                                             int f, int end) {
+  int lo = 0, hi = a.B;   // the sequence: pref[lo] * Hkv <= f < pref[lo + 1] * Hkv
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (pref[mid] * Hkv <= f) lo = mid;
+    if (pref[mid] * a.Hkv <= f) lo = mid;
     else hi = mid;
   }
   c.f = f;
   c.b = lo;
-  c.nb = pref[lo + 1] - pref[lo];
-  const int in = f - pref[lo] * Hkv;
-  c.g = in / c.nb;
-  c.s0 = c.s = in - c.g * c.nb;
-  c.s1 = min(c.nb, c.s0 + end - f);
+  c.n = len_of(a, lo, false);
+  c.ns = pref[lo + 1] - pref[lo];
+  const int in = f - pref[lo] * a.Hkv;
+  c.g = in / c.ns;
+  c.s0 = c.s = in - c.g * c.ns;
+  c.s1 = min(c.ns, c.s0 + end - f);
 }
 
-template <int D, int TERMS>
+template <int D, int TERMS, bool SCORES>
 __global__ void __launch_bounds__(kNW * 32, 2)
     k_qdecode_dense(const __grid_constant__ QDecodeArgs a) {
   pdl_wait();
   pdl_trigger();
   constexpr bool F32 = TERMS == 2;
+  constexpr int kStep = kStepOf<D>, kKeys = 16 * kStep;
   constexpr int kGroupBytes = qgroup_bytes(D), kStageBytes = kStep * kGroupBytes;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ __align__(8) uint64_t s_full[kNW][kDenseStages];
-  __shared__ unsigned char s_have[kNW][kDenseStages];   // bit i: slice i of the stage was copied
   __shared__ int s_tot[kNW];
   __shared__ int s_unit[2 * kNW], s_list[2 * kNW], s_nlist;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, c4 = lane & 3;
   const int pf = static_cast<int>(qpart_floats(a.G, D));
   // a ring per warp, which at the end holds the warp's last piece; a place for
-  // its first piece; slices before every sequence, per head
+  // its first piece; steps before every sequence, per head
   uint8_t* ring = smem + warp * kDenseStages * kStageBytes;
   float* firsts = reinterpret_cast<float*>(smem + kNW * kDenseStages * kStageBytes);   // [kNW][pf]
   int* pref = reinterpret_cast<int*>(firsts + kNW * pf);                               // [B + 1]
@@ -582,11 +580,10 @@ __global__ void __launch_bounds__(kNW * 32, 2)
 
   if (lane == 0)
     for (int i = 0; i < kDenseStages; ++i) mbar_init(&s_full[warp][i], 1);
-  if (tid == 0) fence_barrier_init();
   int carry = 0;
   for (int b0 = 0; b0 < a.B; b0 += kNW * 32) {
     const int b = b0 + tid;
-    const int n = b < a.B ? (len_of(a, b, blockIdx.x == 0) + 15) >> 4 : 0;
+    const int n = b < a.B ? (len_of(a, b, blockIdx.x == 0) + kKeys - 1) / kKeys : 0;
     int incl = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -613,145 +610,234 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   const int w0 = min(total, (static_cast<int>(blockIdx.x) * kNW + warp) * per);
   const int w1 = min(total, w0 + per);
 
-  // ---- copies: `in` runs ahead of the arithmetic by up to kDenseStages steps
+  // ---- copies: `in` runs ahead of the arithmetic by kDenseStages steps. Lane i
+  // < ncopy issues the step's i-th copy of copy_slices slices; its block id is
+  // loaded when `in` gets to the step, one step before it is used.
+  const int copy_sh = min(a.bs_shift, D == 128 ? 5 : 6);   // log2 of a copy's keys
+  const int ncopy = kKeys >> copy_sh;
+  const uint32_t copy_bytes = static_cast<uint32_t>(kGroupBytes) << (copy_sh - 4);
+  const int gmask = (1 << (a.bs_shift - 4)) - 1;
   Cursor in = {}, at;
-  int ids = 0, ids_base = 0, ids_key = -1;   // lane i: block of slice ids_base + i of sequence ids_key
-  int issued = 0, taken = 0;
+  int id = -1;
+  bool more = w0 < w1;            // `in` stands at a step of this run
+  int in_stage = 0;
+  unsigned int have = 0u;         // byte i: the copies that stage i got
+  int pending = 0;                // steps issued and not taken
   bool alive = true;
-  auto issue = [&]() {   // all lanes
-    if (in.s == in.s1) {
-      if (in.f + in.s1 - in.s0 >= w1) return;
-      cursor_enter(in, pref, a.B, a.Hkv, in.f + in.s1 - in.s0, w1);
-    }
-    const int sh = a.bs_shift - 4;
-    if (ids_key != in.b || in.s < ids_base || in.s + kStep > ids_base + 32) {
-      ids_key = in.b;
-      ids_base = in.s;
-      const int s = in.s + lane;
-      ids = s < in.nb ? __ldg(a.table + static_cast<size_t>(in.b) * a.max_blocks + (s >> sh)) : -1;
-    }
-    const int stage = issued % kDenseStages;
-    uint8_t* dst = ring + stage * kStageBytes;
-    int block[kStep];
-    unsigned int have = 0u;
-#pragma unroll
-    for (int i = 0; i < kStep; ++i) {
-      block[i] = __shfl_sync(0xffffffffu, ids, (in.s + i - ids_base) & 31);
-      if (in.s + i < in.s1) {
-        if (block[i] >= 0 && block[i] < a.num_blocks) have |= 1u << i;
-        else report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x522);
-      }
-    }
-    if (lane == 0) {
-      s_have[warp][stage] = static_cast<unsigned char>(have);
-      mbar_arrive_expect_tx(&s_full[warp][stage], __popc(have) * kGroupBytes);
-#pragma unroll
-      for (int i = 0; i < kStep; ++i)
-        if ((have >> i) & 1u) {
-          const int s = in.s + i;
-          const size_t grp = ((static_cast<size_t>(block[i]) * a.Hkv + in.g) << sh) +
-                             (s & ((1 << sh) - 1));
-          bulk_load(dst + i * kGroupBytes, a.cache + grp * kGroupBytes, kGroupBytes,
-                    &s_full[warp][stage]);
-        }
-    }
-    in.s = min(in.s1, in.s + kStep);
-    ++issued;
+  auto fetch_id = [&]() {
+    const int key = in.s * kKeys + (lane << copy_sh);
+    id = 0;                       // nothing to copy: neither read nor reported
+    if (lane < ncopy && key < in.n)
+      id = __ldg(a.table + static_cast<size_t>(in.b) * a.max_blocks + (key >> a.bs_shift));
   };
-  if (w0 < w1) {
-    cursor_enter(in, pref, a.B, a.Hkv, w0, w1);
-#pragma unroll
-    for (int i = 0; i < kDenseStages; ++i) issue();
+  auto issue = [&]() {            // all lanes, `more` holds
+    const int key = in.s * kKeys + (lane << copy_sh);
+    const bool want = lane < ncopy && key < in.n;
+    const bool ok = want && static_cast<unsigned int>(id) < static_cast<unsigned int>(a.num_blocks);
+    if (want && !ok) report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x522);
+    const unsigned int got = __ballot_sync(0xffffffffu, ok);
+    uint64_t* bar = &s_full[warp][in_stage];
+    if (lane == 0) mbar_arrive_expect_tx(bar, __popc(got) * copy_bytes);
+    __syncwarp();
+    if (ok) {
+      const size_t grp = ((static_cast<size_t>(id) * a.Hkv + in.g) << (a.bs_shift - 4)) +
+                         ((key >> 4) & gmask);
+      bulk_load(ring + in_stage * kStageBytes + lane * copy_bytes, a.cache + grp * kGroupBytes,
+                copy_bytes, bar);
+    }
+    have = (have & ~(0xffu << (8 * in_stage))) | (got << (8 * in_stage));
+    in_stage ^= 1;
+    ++pending;
+    if (++in.s == in.s1) {
+      const int next = in.f + in.s1 - in.s0;
+      more = next < w1;
+      if (more) cursor_enter(in, a, pref, next, w1);
+    }
+    if (more) fetch_id();
+  };
+  static_assert(kDenseStages == 2, "stages alternate");
+  if (more) {
+    cursor_enter(in, a, pref, w0, w1);
+    fetch_id();
+    issue();
+    if (more) issue();
   }
 
   // ---- arithmetic
   const int row0 = row_key(gid);   // keys row0 and row0 + 8 of a slice
+  int stage = 0;
+  uint32_t phase = 0;
   for (int f = w0; f < w1;) {
-    cursor_enter(at, pref, a.B, a.Hkv, f, w1);
-    const int b = at.b, g = at.g, n = len_of(a, b, false);
+    cursor_enter(at, a, pref, f, w1);
+    const int n = at.n;
     QFrag<D, TERMS> qf;
-    load_q(a, b, g, qf);
-    QState<D> st;
-    qstate_init(st);
+    load_q(a, at.b, at.g, qf);
     float* sp[2] = {nullptr, nullptr};
-    if (a.scores != nullptr)
+    if (SCORES)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
         if (2 * c4 + i < a.G)
-          sp[i] = a.scores + (static_cast<size_t>(b) * a.Hq + a.heads[g * a.G + 2 * c4 + i]) * a.N;
-    const float ml[2] = {qf.mult[0] * kLog2e, qf.mult[1] * kLog2e};
-    while (at.s < at.s1 && alive) {
-      const int stage = taken % kDenseStages;
-      if (!mbar_wait_warp(&s_full[warp][stage], (taken / kDenseStages) & 1, a.err, 0x531)) {
+          sp[i] = a.scores +
+                  (static_cast<size_t>(at.b) * a.Hq + a.heads[at.g * a.G + 2 * c4 + i]) * a.N;
+    const uint64_t ml = f2_pack(qf.mult[0] * kLog2e, qf.mult[1] * kLog2e);
+    // m: running maxima (log2 units); nmu = 14 - m, +inf before the first key
+    float m0 = kNegInf, m1 = kNegInf;
+    uint64_t nmu = f2_pack(-kNegInf, -kNegInf), l = f2_pack(0.f, 0.f);
+    float o[D / 16][4];
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    for (; at.s < at.s1 && alive; ++at.s) {
+      if (!mbar_wait_warp(&s_full[warp][stage], phase, a.err, 0x531)) {
         // a wait that gave up (reported): leave no copy in flight, and pass over
         // the rest of the run so that every unit still gets its arrivals
-        for (; taken < issued; ++taken)
-          mbar_wait_warp(&s_full[warp][taken % kDenseStages], (taken / kDenseStages) & 1, a.err,
-                         0x532);
+        for (; pending > 0; --pending) {
+          mbar_wait_warp(&s_full[warp][stage], phase, a.err, 0x532);
+          stage ^= 1;
+          phase ^= stage == 0 ? 1u : 0u;
+        }
         alive = false;
         break;
       }
-      ++taken;
       const uint8_t* buf = ring + stage * kStageBytes;
-      const unsigned int have = s_have[warp][stage];
-      float x[kStep][4];
-      QSlice<D> sl[kStep];
+      const unsigned int got = (have >> (8 * stage)) & 0xffu;
+      if (got != 0u || SCORES) {
+        uint64_t t[kStep][2];   // scores of (row0; row0 + 8) for both heads: raw, then exponents
 #pragma unroll
-      for (int i = 0; i < kStep; ++i) {
-        load_k_row<D, true>(sl[i], 0, buf + i * kGroupBytes, row0);
-        load_k_row<D, true>(sl[i], 1, buf + i * kGroupBytes, row0 + 8);
-        slice_logits(sl[i], qf, x[i]);
-      }
-      // keys that do not count: behind the sequence's end, in a stage half that
-      // belongs to no slice of this run, in a block the table does not name
-      const bool full = have == (1u << kStep) - 1u && 16 * (at.s + kStep) <= n;
-      if (!full) {
-#pragma unroll
-        for (int i = 0; i < kStep; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (!((have >> i) & 1u) || 16 * (at.s + i) + row0 + 8 * (j >> 1) >= n) x[i][j] = kNegInf;
-      }
-      if (a.scores != nullptr) {
-#pragma unroll
-        for (int i = 0; i < kStep; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int key = 16 * (at.s + i) + row0 + 8 * (j >> 1);
-            if (sp[j & 1] != nullptr && (full || (at.s + i < at.s1 && key < n)))
-              sp[j & 1][key] = x[i][j] * qf.mult[j & 1];
-          }
-      }
-#pragma unroll
-      for (int i = 0; i < kStep; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[i][j] *= ml[j & 1];
-      raise_max<D, kStep>(st, x);
-#pragma unroll
-      for (int i = 0; i < kStep; ++i) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) load_v_row<D, true>(sl[i], j, buf + i * kGroupBytes, v_key(j));
+        for (int i = 0; i < kStep; ++i) {
+          QSlice<D> sl;
+          load_k_row<D, true>(sl, 0, buf + i * kGroupBytes, row0);
+          load_k_row<D, true>(sl, 1, buf + i * kGroupBytes, row0 + 8);
+          float raw[4];
+          slice_logits(sl, qf, raw);
+          t[i][0] = f2_pack(raw[0], raw[1]);
+          t[i][1] = f2_pack(raw[2], raw[3]);
+        }
+        // keys that do not count: behind the sequence's end, or in a block the
+        // table does not name
+        const int key0 = at.s * kKeys + row0;
+        const bool full = got == (1u << ncopy) - 1u && (at.s + 1) * kKeys <= n;
+        auto counts = [&](int i, int key) {
+          return ((got >> ((16 * i) >> copy_sh)) & 1u) != 0u && key < n;
+        };
         if (!full) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (!((have >> i) & 1u) || 16 * (at.s + i) + v_key(j) >= n) sl[i].vs[j] = 0u;
+          for (int i = 0; i < kStep; ++i)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              // -inf through any multiplier's sign: the multiplier is positive
+              if (!counts(i, key0 + 16 * i + 8 * r)) t[i][r] = f2_pack(kNegInf, kNegInf);
         }
-        slice_pv<D, TERMS>(st, x[i], sl[i]);
+        if (SCORES) {
+#pragma unroll
+          for (int i = 0; i < kStep; ++i)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const int key = key0 + 16 * i + 8 * r;
+              float v0, v1;
+              f2_unpack(t[i][r], v0, v1);
+              if (full || key < n) {
+                if (sp[0] != nullptr) sp[0][key] = v0 * qf.mult[0];
+                if (sp[1] != nullptr) sp[1][key] = v1 * qf.mult[1];
+              }
+            }
+        }
+        if (got != 0u) {
+          auto exponents = [&](float& top0, float& top1, uint64_t (&y)[kStep][2]) {
+            top0 = top1 = kNegInf;
+#pragma unroll
+            for (int i = 0; i < kStep; ++i) {
+              float a0, a1, b0, b1;
+              // product and sum rounded apart, as the maximum was: a fused one
+              // would leave the product's rounding, large for a huge score
+              y[i][0] = f2_add(f2_mul(t[i][0], ml), nmu);
+              y[i][1] = f2_add(f2_mul(t[i][1], ml), nmu);
+              f2_unpack(y[i][0], a0, a1);
+              f2_unpack(y[i][1], b0, b1);
+              top0 = fmax3(top0, a0, b0);
+              top1 = fmax3(top1, a1, b1);
+            }
+          };
+          uint64_t y[kStep][2];
+          float top0, top1;
+          exponents(top0, top1, y);
+          if (__any_sync(0xffffffffu, fmaxf(top0, top1) > static_cast<float>(kPShift))) {
+            // a score above the running maximum: raise it and rescale
+            float x0 = kNegInf, x1 = kNegInf, ml0, ml1;
+            f2_unpack(ml, ml0, ml1);
+#pragma unroll
+            for (int i = 0; i < kStep; ++i) {
+              float a0, a1, b0, b1;
+              f2_unpack(t[i][0], a0, a1);
+              f2_unpack(t[i][1], b0, b1);
+              x0 = fmax3(x0, a0 * ml0, b0 * ml0);
+              x1 = fmax3(x1, a1 * ml1, b1 * ml1);
+            }
+#pragma unroll
+            for (int off = 4; off < 32; off <<= 1) {
+              x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
+              x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
+            }
+            x0 = fmaxf(x0, m0);
+            x1 = fmaxf(x1, m1);
+            const float al0 = m0 == kNegInf ? 0.f : fast_exp2(m0 - x0);
+            const float al1 = m1 == kNegInf ? 0.f : fast_exp2(m1 - x1);
+            m0 = x0;
+            m1 = x1;
+            nmu = f2_pack(kPShift - m0, kPShift - m1);
+            l = f2_mul(l, f2_pack(al0, al1));
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              o[i][0] *= al0;
+              o[i][1] *= al1;
+              o[i][2] *= al0;
+              o[i][3] *= al1;
+            }
+            exponents(top0, top1, y);
+          }
+#pragma unroll
+          for (int i = 0; i < kStep; ++i) {
+            QSlice<D> sl;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) load_v_row<D, true>(sl, j, buf + i * kGroupBytes, v_key(j));
+            if (!full) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (!counts(i, at.s * kKeys + 16 * i + v_key(j))) sl.vs[j] = 0u;
+            }
+            float p[4];
+            f2_unpack(y[i][0], p[0], p[1]);
+            f2_unpack(y[i][1], p[2], p[3]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) p[j] = ex2(p[j]);
+            l = f2_add(l, f2_add(f2_pack(p[0], p[1]), f2_pack(p[2], p[3])));
+            slice_pv<D, TERMS>(o, p, sl);
+          }
+        }
       }
-      at.s = min(at.s1, at.s + kStep);
+      stage ^= 1;
+      phase ^= stage == 0 ? 1u : 0u;
+      --pending;
       // the stage is refilled through the async proxy: this warp's reads first
       fence_proxy_async_smem();
       __syncwarp();
-      issue();
+      if (more) issue();
     }
     f += at.s1 - at.s0;
-    if (at.s0 == 0 && at.s1 == at.nb) {
-      warp_output<D, F32>(a, st, b, g);
+    QState<D> st;
+    st.m[0] = m0;
+    st.m[1] = m1;
+    f2_unpack(l, st.l[0], st.l[1]);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) st.o[i][j] = o[i][j];
+    if (at.s0 == 0 && at.s1 == at.ns) {
+      warp_output<D, F32>(a, st, at.b, at.g);
     } else {
       // in part: a run's first unit or its last (whose ring is free by then)
       const int slot = 2 * warp + (at.f == w0 ? 0 : 1);
       piece_store<D>(slot_at(slot), st, a.G);
-      if (lane == 0) s_unit[slot] = b * a.Hkv + g;
+      if (lane == 0) s_unit[slot] = at.b * a.Hkv + at.g;
     }
   }
   __syncthreads();
@@ -776,7 +862,7 @@ __global__ void __launch_bounds__(kNW * 32, 2)
     int j = i;
     while (j < nlist && s_unit[s_list[j]] == unit) ++j;
     const int b = unit / a.Hkv, g = unit % a.Hkv, nb = pref[b + 1] - pref[b];
-    const int u0 = pref[b] * a.Hkv + g * nb, u1 = u0 + nb;   // the unit's slices
+    const int u0 = pref[b] * a.Hkv + g * nb, u1 = u0 + nb;   // the unit's steps
     auto mine = [&](int s) -> const float* { return slot_at(s_list[i + s]); };
     float* dst = nullptr;
     if (u0 < c0 || u1 > c0 + per_cta) {
@@ -808,7 +894,7 @@ __global__ void __launch_bounds__(kNW * 32, 2)
     for (int h = tid; h < a.Hq; h += kNW * 32)
       write_row_stat(a, static_cast<size_t>(b) * a.Hq + h, kNegInf, 0.f);
   }
-  if (a.scores != nullptr && a.fill_tail)
+  if (SCORES && a.fill_tail)
     for (int r = blockIdx.x; r < a.B * a.Hq; r += gridDim.x)
       for (int j = len_of(a, r / a.Hq, false) + tid; j < a.N; j += blockDim.x)
         a.scores[static_cast<size_t>(r) * a.N + j] = kNegInf;
@@ -971,7 +1057,13 @@ __global__ void __launch_bounds__(kNW * 32, 2)
       }
     }
     raise_max<D, 1>(st, x);
-    slice_pv<D, TERMS>(st, x[0], s);
+    float p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p[i] = ex2(x[0][i] - st.mu[i & 1]);
+      st.l[i & 1] += p[i];
+    }
+    slice_pv<D, TERMS>(st.o, p, s);
     if (!POOLED && (nan_heads & 3u) != 0u) {
 #pragma unroll
       for (int j = 0; j < D / 16; ++j)
@@ -1023,24 +1115,29 @@ cudaError_t resident_ctas(K kern, size_t smem, int& ctas) {
   return cudaSuccess;
 }
 
-template <int D, int TERMS>
+template <int D, int TERMS, bool SCORES>
 cudaError_t launch_dense_t(const QDecodeArgs& a, cudaStream_t st) {
   // rings (at the end the scratch of joins between CTAs), first pieces, prefix,
   // the scratch of joins between the CTA's warps
-  constexpr size_t kRings = kNW * kDenseStages * kStep * qgroup_bytes(D);
+  constexpr size_t kRing = kDenseStages * kStepOf<D> * qgroup_bytes(D), kRings = kNW * kRing;
   static_assert(kRings >= (4 * kNW * 32 + static_cast<size_t>(kDenseMaxCtas) * 8) * sizeof(float),
                 "weights of one piece per CTA");
-  static_assert(kDenseStages * kStep * qgroup_bytes(D) >= qpart_floats(8, D) * sizeof(float),
-                "a warp's last piece in its ring");
+  static_assert(kRing >= qpart_floats(8, D) * sizeof(float), "a warp's last piece in its ring");
   const size_t smem = kRings + kNW * qpart_floats(a.G, D) * sizeof(float) +
                       qalign16((static_cast<size_t>(a.B) + 1) * sizeof(int)) +
                       (4 * kNW * 32 + 2 * kNW * static_cast<size_t>(a.G)) * sizeof(float);
-  auto kern = k_qdecode_dense<D, TERMS>;
+  auto kern = k_qdecode_dense<D, TERMS, SCORES>;
   int ctas = 0;
   const cudaError_t e = resident_ctas(kern, smem, ctas);
   if (e != cudaSuccess) return e;
   if (ctas > kDenseMaxCtas) ctas = kDenseMaxCtas;
   return launch_pdl(kern, dim3(ctas), dim3(kNW * 32), smem, st, a);
+}
+
+template <int D, int TERMS>
+cudaError_t launch_dense_s(const QDecodeArgs& a, cudaStream_t st) {
+  return a.scores != nullptr ? launch_dense_t<D, TERMS, true>(a, st)
+                             : launch_dense_t<D, TERMS, false>(a, st);
 }
 
 template <int D, int TERMS, bool POOLED>
@@ -1066,8 +1163,8 @@ cudaError_t launch_reuse_t(const QDecodeArgs& a, cudaStream_t st) {
 
 cudaError_t launch_qdecode_dense(const QDecodeArgs& a, int d, int dtype, cudaStream_t st) {
   if (dtype == KASCADE_F32)
-    return d == 128 ? launch_dense_t<128, 2>(a, st) : launch_dense_t<64, 2>(a, st);
-  return d == 128 ? launch_dense_t<128, 1>(a, st) : launch_dense_t<64, 1>(a, st);
+    return d == 128 ? launch_dense_s<128, 2>(a, st) : launch_dense_s<64, 2>(a, st);
+  return d == 128 ? launch_dense_s<128, 1>(a, st) : launch_dense_s<64, 1>(a, st);
 }
 
 cudaError_t launch_qdecode_reuse(const QDecodeArgs& a, int d, int dtype, cudaStream_t st) {
