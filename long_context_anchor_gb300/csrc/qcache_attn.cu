@@ -30,7 +30,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kPShift = 14;          // weights are held as 2^14 p
 constexpr int kQExp = 12;            // q's largest element is scaled to [2^12, 2^13)
 constexpr int kNW = 8;               // warps per CTA (and at most 8 heads per KV head)
-constexpr int kDenseMaxCtas = 512;   // two per SM
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                               uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -100,10 +99,10 @@ struct QFrag {
   float mult[2];
 };
 
+// Head gid's dims c4 * D/4 .. + D/4 as they are in memory (zeros for no head).
 template <int D, int TERMS>
-__device__ void load_q(const QDecodeArgs& a, int b, int g, QFrag<D, TERMS>& qf) {
+__device__ __forceinline__ void load_q(const QDecodeArgs& a, int b, int g, float (&x)[D / 4]) {
   const int lane = threadIdx.x & 31, gid = lane >> 2, c4 = lane & 3;
-  float x[D / 4];
   const bool ok = gid < a.G;
   const size_t row = ok ? static_cast<size_t>(b) * a.Hq + a.heads[g * a.G + gid] : 0;
   if (TERMS == 2) {
@@ -129,6 +128,12 @@ __device__ void load_q(const QDecodeArgs& a, int b, int g, QFrag<D, TERMS>& qf) 
       x[4 * i + 3] = __uint_as_float(v.y & 0xffff0000u);
     }
   }
+}
+
+template <int D, int TERMS>
+__device__ __forceinline__ void make_q(const QDecodeArgs& a, const float (&x)[D / 4],
+                                       QFrag<D, TERMS>& qf) {
+  const int c4 = threadIdx.x & 3;
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < D / 4; ++i) amax = fmaxf(amax, fabsf(x[i]));
@@ -309,109 +314,128 @@ __device__ __forceinline__ void write_row_stat(const QDecodeArgs& a, size_t row,
     a.row_stat[row] = make_float2(m * kLn2, l == 0.f ? 0.f : ldexpf(1.f / l, kPShift));
 }
 
-// Join n pieces, the i-th at piece(i), with all threads of the CTA. When `dst`
-// is null the result is the output of (b, g), else the joined piece goes to
-// dst. Warp h makes head h's weights of all pieces in `scratch` (n * G floats,
-// then 4 * blockDim.x), then every thread sums four dims over an equal share of
-// the pieces with its loads in flight together, and the shares are added in
-// order: the result does not depend on timing.
-template <int D, bool F32, bool GLOBAL, typename Piece>
-__device__ void join_pieces(const QDecodeArgs& a, Piece piece, int n, int b, int g, float* dst,
-                            float* scratch) {
-  __shared__ float s_m[8], s_l[8];
-  const int G = a.G, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  auto ld = [](const float* p) { return GLOBAL ? __ldcg(p) : *p; };
-  float4* sums = reinterpret_cast<float4*>(scratch);                       // [blockDim.x]
-  float* wts = scratch + 4 * blockDim.x;                                   // [n][G]
-  if (warp < G) {
-    float M = kNegInf;
-    for (int s = lane; s < n; s += 32) {
-      const float m = ld(piece(s) + warp);
-      wts[s * G + warp] = m;
-      M = fmaxf(M, m);
-    }
+// Four dims e (float4 index within [G][D / 4]) of head h over pieces s0 .. s1-1,
+// the i-th at piece(i): running maximum, sum and output, with the loads of
+// several pieces in flight together.
+struct Joined {
+  float m, l;
+  float4 o;
+};
+// x += the N parts y (their weights do not wait for one another)
+template <int N>
+__device__ __forceinline__ void join_into(Joined& x, const Joined (&y)[N]) {
+  float M = x.m;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    float L = 0.f;
-    for (int s = lane; s < n; s += 32) {
-      const float m = wts[s * G + warp];
-      // a piece without keys has m = -inf and l = o = 0
-      const float w = m == kNegInf ? 1.f : fast_exp2(m - M);
-      wts[s * G + warp] = w;
-      L = fmaf(w, ld(piece(s) + G + warp), L);
-    }
+  for (int k = 0; k < N; ++k) M = fmaxf(M, y[k].m);
+  // a part without keys has m = -inf and l = o = 0 (or l NaN, which stays)
+  const float wx = x.m == kNegInf ? 1.f : ex2(x.m - M);
+  x.m = M;
+  x.l *= wx;
+  x.o.x *= wx;
+  x.o.y *= wx;
+  x.o.z *= wx;
+  x.o.w *= wx;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-    if (lane == 0) {
-      s_m[warp] = M;
-      s_l[warp] = L;
-    }
+  for (int k = 0; k < N; ++k) {
+    const float w = y[k].m == kNegInf ? 1.f : ex2(y[k].m - M);
+    x.l = fmaf(w, y[k].l, x.l);
+    x.o.x = fmaf(w, y[k].o.x, x.o.x);
+    x.o.y = fmaf(w, y[k].o.y, x.o.y);
+    x.o.z = fmaf(w, y[k].o.z, x.o.z);
+    x.o.w = fmaf(w, y[k].o.w, x.o.w);
   }
-  __syncthreads();
-  const int elems = G * (D / 4);                 // float4 elements: 16 .. 256
-  const int shares = static_cast<int>(blockDim.x) / elems;
-  const int e = tid % elems, share = tid / elems, h = e / (D / 4);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (share < shares) {
-    const int per = (n + shares - 1) / shares;
-    const int s1 = min(n, (share + 1) * per);
-#pragma unroll 8
-    for (int s = share * per; s < s1; ++s) {
-      const float4* p = reinterpret_cast<const float4*>(piece(s) + qpart_head(G)) + e;
-      const float4 o = GLOBAL ? __ldcg(p) : *p;
-      const float w = wts[s * G + h];
-      acc.x = fmaf(w, o.x, acc.x);
-      acc.y = fmaf(w, o.y, acc.y);
-      acc.z = fmaf(w, o.z, acc.z);
-      acc.w = fmaf(w, o.w, acc.w);
-    }
-    if (shares > 1) sums[tid] = acc;
-  }
-  __syncthreads();
-  if (share == 0) {
-    for (int k = 1; k < shares; ++k) {
-      const float4 o = sums[k * elems + e];
-      acc.x += o.x;
-      acc.y += o.y;
-      acc.z += o.z;
-      acc.w += o.w;
-    }
-    const float M = s_m[h], L = s_l[h];
-    const bool first = (e & (D / 4 - 1)) == 0;
-    if (dst != nullptr) {
-      *reinterpret_cast<float4*>(dst + qpart_head(G) + 4 * e) = acc;
-      if (first) {
-        dst[h] = M;
-        dst[G + h] = L;
+}
+template <bool GLOBAL, typename Piece>
+__device__ __forceinline__ Joined join_some(Piece piece, int s0, int s1, int G, int h, int e) {
+  constexpr int kBatch = GLOBAL ? 8 : 4;   // loads of L2 lines take longer
+  Joined x = {kNegInf, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int s = s0; s < s1; s += kBatch) {
+    Joined y[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      y[k] = {kNegInf, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      if (s + k < s1) {
+        const float* p = piece(s + k);
+        const float4* o = reinterpret_cast<const float4*>(p + qpart_head(G)) + e;
+        y[k].m = GLOBAL ? __ldcg(p + h) : p[h];
+        y[k].l = GLOBAL ? __ldcg(p + G + h) : p[G + h];
+        y[k].o = GLOBAL ? __ldcg(o) : *o;
       }
-    } else {
-      const size_t row = static_cast<size_t>(b) * a.Hq + a.heads[g * G + h];
-      const float inv = L == 0.f ? 0.f : a.v_scale / L;   // L == 0: no key at all
-      out_store4<F32>(a, row * D + 4 * (e & (D / 4 - 1)),
-                      make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-      if (first) write_row_stat(a, row, M, L);
     }
+    join_into(x, y);
   }
-  __syncthreads();   // scratch is free again
+  return x;
 }
 
-// This CTA's piece of a unit shared by n CTAs is in its place: count it, and
-// let the last CTA to arrive join all of them into the output.
-template <int D, bool F32, typename Piece>
-__device__ void arrive_and_join(const QDecodeArgs& a, int unit, Piece piece, int n, int b, int g,
-                                float* scratch) {
+// The output (b, g, head slot h, dims 4 e4 ..) of a joined whole.
+template <int D, bool F32>
+__device__ __forceinline__ void joined_output(const QDecodeArgs& a, const Joined& x, int b, int g,
+                                              int h, int e4) {
+  const size_t row = static_cast<size_t>(b) * a.Hq + a.heads[g * a.G + h];
+  const float inv = x.l == 0.f ? 0.f : a.v_scale / x.l;   // 0: no key at all
+  out_store4<F32>(a, row * D + 4 * e4,
+                  make_float4(x.o.x * inv, x.o.y * inv, x.o.z * inv, x.o.w * inv));
+  if (e4 == 0) write_row_stat(a, row, x.m, x.l);
+}
+
+// A unit shared by n CTAs: its first CTA's piece, and the others' from `rest` on.
+struct SharedUnit {
+  int unit, b, g, n;
+  const float* first;
+  const float* rest;
+  size_t step;
+};
+
+// This CTA's pieces of up to two such units are in their places. Count them,
+// and where this CTA is the last to arrive join all of the unit's pieces into
+// the output: equal shares of the pieces per group of threads, added in order,
+// so the result does not depend on timing. `scratch`: blockDim.x Joined.
+template <int D, bool F32>
+__device__ void arrive_and_join(const QDecodeArgs& a, int n_units, const SharedUnit (&units)[2],
+                                Joined* scratch) {
   __shared__ unsigned int s_last;
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0)
-    s_last = atomicAdd(&a.counters[unit], 1u) == static_cast<unsigned int>(n - 1) ? 1u : 0u;
-  __syncthreads();
-  if (s_last != 0u) {
+  const int tid = threadIdx.x, G = a.G;
+  __syncthreads();   // every piece of this CTA is written
+  if (tid == 0) {
     __threadfence();
-    join_pieces<D, F32, true>(a, piece, n, b, g, nullptr, scratch);
-    if (threadIdx.x == 0) a.counters[unit] = 0u;   // ready for the next launch
+    unsigned int last = 0u;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (k < n_units && atomicAdd(&a.counters[units[k].unit], 1u) ==
+                             static_cast<unsigned int>(units[k].n - 1)) {
+        a.counters[units[k].unit] = 0u;   // ready for the next launch
+        last |= 1u << k;
+      }
+    __threadfence();
+    s_last = last;
   }
   __syncthreads();
+  const unsigned int last = s_last;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    if (!((last >> k) & 1u)) continue;
+    const SharedUnit& u = units[k];
+    const int n = u.n;
+    const int elems = G * (D / 4);                 // 16 .. 256
+    int shares = static_cast<int>(blockDim.x) / elems;
+    if (shares > (n + 3) / 4) shares = (n + 3) / 4;
+    const int e = tid % elems, share = tid / elems, h = e / (D / 4), e4 = e & (D / 4 - 1);
+    const int per = (n + shares - 1) / shares;
+    auto mine = [&](int i) -> const float* { return i == 0 ? u.first : u.rest + (i - 1) * u.step; };
+    Joined x = {kNegInf, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    if (share < shares) x = join_some<true>(mine, share * per, min(n, (share + 1) * per), G, h, e);
+    if (shares > 1) {
+      if (share > 0 && share < shares) scratch[tid] = x;
+      __syncthreads();
+      if (share == 0)
+        for (int i = 1; i < shares; ++i) {
+          const Joined y[1] = {scratch[i * elems + e]};
+          join_into(x, y);
+        }
+      __syncthreads();
+    }
+    if (share == 0) joined_output<D, F32>(a, x, u.b, u.g, h, e4);
+  }
 }
 
 // A whole unit held by one warp: straight from its registers to the output.
@@ -617,7 +641,7 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   const int ncopy = kKeys >> copy_sh;
   const uint32_t copy_bytes = static_cast<uint32_t>(kGroupBytes) << (copy_sh - 4);
   const int gmask = (1 << (a.bs_shift - 4)) - 1;
-  Cursor in = {}, at;
+  Cursor in = {}, at = {};
   int id = -1;
   bool more = w0 < w1;            // `in` stands at a step of this run
   int in_stage = 0;
@@ -656,9 +680,12 @@ __global__ void __launch_bounds__(kNW * 32, 2)
     if (more) fetch_id();
   };
   static_assert(kDenseStages == 2, "stages alternate");
+  float qx[D / 4];   // the query of the unit that comes next
   if (more) {
     cursor_enter(in, a, pref, w0, w1);
     fetch_id();
+    at = in;
+    load_q<D, TERMS>(a, at.b, at.g, qx);
     issue();
     if (more) issue();
   }
@@ -668,10 +695,13 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   int stage = 0;
   uint32_t phase = 0;
   for (int f = w0; f < w1;) {
-    cursor_enter(at, a, pref, f, w1);
+    if (f != w0) {
+      cursor_enter(at, a, pref, f, w1);
+      load_q<D, TERMS>(a, at.b, at.g, qx);
+    }
     const int n = at.n;
     QFrag<D, TERMS> qf;
-    load_q(a, at.b, at.g, qf);
+    make_q(a, qx, qf);
     float* sp[2] = {nullptr, nullptr};
     if (SCORES)
 #pragma unroll
@@ -850,41 +880,52 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   __syncthreads();
   const int nlist = s_nlist;
   const int per_cta = per * kNW, c0 = static_cast<int>(blockIdx.x) * per_cta;
-  float* scratch = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(pref) +
-                                            qalign16((static_cast<size_t>(a.B) + 1) * sizeof(int)));
-  // this CTA's units: joined here if it holds all of one, else its piece goes
-  // to CTA c's place 2c + 1 (a unit that starts inside c's run) or 2c (one
-  // that started before it, or with it)
+  // This CTA's pieces, in order of their units: a unit is joined here if the
+  // CTA holds all of it, else its piece goes to CTA c's place 2c + 1 (a unit
+  // that starts inside c's run) or 2c (one that started before it, or with it).
   const size_t stride = qpart_floats(a.G, D);
-  int shared_unit[2], shared = 0;
-  for (int i = 0; i < nlist;) {
+  SharedUnit shared[2] = {};   // at most the first and the last unit of the run
+  int n_shared = 0;
+  const int elems = a.G * (D / 4);
+  for (int i = 0, first_elem = 0; i < nlist;) {
     const int unit = s_unit[s_list[i]];
     int j = i;
     while (j < nlist && s_unit[s_list[j]] == unit) ++j;
     const int b = unit / a.Hkv, g = unit % a.Hkv, nb = pref[b + 1] - pref[b];
     const int u0 = pref[b] * a.Hkv + g * nb, u1 = u0 + nb;   // the unit's steps
-    auto mine = [&](int s) -> const float* { return slot_at(s_list[i + s]); };
     float* dst = nullptr;
     if (u0 < c0 || u1 > c0 + per_cta) {
       dst = a.part + (2 * static_cast<size_t>(blockIdx.x) + (u0 > c0 ? 1 : 0)) * stride;
-      shared_unit[shared++ & 1] = unit;
+      const int first = u0 / per_cta;
+      const SharedUnit u = {unit, b, g, (u1 - 1) / per_cta - first + 1,
+                            a.part + (2 * static_cast<size_t>(first) +
+                                      (u0 > first * per_cta ? 1 : 0)) * stride,
+                            a.part + 2 * (static_cast<size_t>(first) + 1) * stride, 2 * stride};
+      if (n_shared == 0) shared[0] = u;
+      else shared[1] = u;
+      ++n_shared;
     }
-    join_pieces<D, F32, false>(a, mine, j - i, b, g, dst, scratch);
+    // the next unit's elements go to the threads that this one leaves free
+    const int e = (tid - first_elem) & (kNW * 32 - 1);
+    if (e < elems) {
+      const int h = e / (D / 4), e4 = e & (D / 4 - 1);
+      const Joined x = join_some<false>(
+          [&](int s) -> const float* { return slot_at(s_list[i + s]); }, 0, j - i, a.G, h, e);
+      if (dst != nullptr) {
+        reinterpret_cast<float4*>(dst + qpart_head(a.G))[e] = x.o;
+        if (e4 == 0) {
+          dst[h] = x.m;
+          dst[a.G + h] = x.l;
+        }
+      } else {
+        joined_output<D, F32>(a, x, b, g, h, e4);
+      }
+    }
+    first_elem += elems;
     i = j;
   }
-  // units shared with other CTAs (at most the first and the last); the rings are free
-  for (int k = 0; k < shared; ++k) {
-    const int unit = shared_unit[k & 1];
-    const int b = unit / a.Hkv, g = unit % a.Hkv, nb = pref[b + 1] - pref[b];
-    const int u0 = pref[b] * a.Hkv + g * nb;
-    const int first = u0 / per_cta, ncta = (u0 + nb - 1) / per_cta - first + 1;
-    const float* part = a.part;
-    const int odd = u0 > first * per_cta ? 1 : 0;
-    auto all = [=](int s) -> const float* {
-      return part + (2 * static_cast<size_t>(first + s) + (s == 0 ? odd : 0)) * stride;
-    };
-    arrive_and_join<D, F32>(a, unit, all, ncta, b, g, reinterpret_cast<float*>(smem));
-  }
+  if (n_shared > 0)
+    arrive_and_join<D, F32>(a, n_shared, shared, reinterpret_cast<Joined*>(smem));
   // sequences without keys: zeros; scores behind the last key
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     if (pref[b + 1] != pref[b]) continue;
@@ -962,7 +1003,11 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   QState<D> st;
   qstate_init(st);
   QFrag<D, TERMS> qf;
-  load_q(a, b, g, qf);
+  {
+    float x[D / 4];
+    load_q<D, TERMS>(a, b, g, x);
+    make_q(a, x, qf);
+  }
   int fc = 0;
   for (int sl = g0 + warp; sl < g1; sl += kNW) {
     // entry i of the slice in lanes i and i + 16: its key's group and row, and
@@ -1074,17 +1119,26 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   }
   piece_store<D>(slots + warp * pf, st, a.G);
   __syncthreads();
-  float* scratch = slots + kNW * pf;
-  auto mine = [&](int w) -> const float* { return slots + w * pf; };
-  if (a.S == 1) {
-    join_pieces<D, F32, false>(a, mine, kNW, b, g, nullptr, scratch);
-    return;
-  }
   float* part = a.part + static_cast<size_t>(unit) * a.S * pf;
-  join_pieces<D, F32, false>(a, mine, kNW, b, g, part + static_cast<size_t>(blockIdx.x) * pf,
-                      scratch);
-  auto all = [=](int w) -> const float* { return part + static_cast<size_t>(w) * pf; };
-  arrive_and_join<D, F32>(a, unit, all, a.S, b, g, scratch);
+  float* dst = part + static_cast<size_t>(blockIdx.x) * pf;
+  const int elems = a.G * (D / 4);
+  for (int e = tid; e < elems; e += kNW * 32) {
+    const int h = e / (D / 4), e4 = e & (D / 4 - 1);
+    const Joined x = join_some<false>([&](int w) -> const float* { return slots + w * pf; }, 0,
+                                      kNW, a.G, h, e);
+    if (a.S == 1) {
+      joined_output<D, F32>(a, x, b, g, h, e4);
+    } else {
+      reinterpret_cast<float4*>(dst + qpart_head(a.G))[e] = x.o;
+      if (e4 == 0) {
+        dst[h] = x.m;
+        dst[a.G + h] = x.l;
+      }
+    }
+  }
+  if (a.S == 1) return;
+  const SharedUnit units[2] = {{unit, b, g, a.S, part, part + pf, static_cast<size_t>(pf)}, {}};
+  arrive_and_join<D, F32>(a, 1, units, reinterpret_cast<Joined*>(slots));
 }
 
 // CTAs of a kernel that the current device holds at once (asked once per host
@@ -1117,20 +1171,16 @@ cudaError_t resident_ctas(K kern, size_t smem, int& ctas) {
 
 template <int D, int TERMS, bool SCORES>
 cudaError_t launch_dense_t(const QDecodeArgs& a, cudaStream_t st) {
-  // rings (at the end the scratch of joins between CTAs), first pieces, prefix,
-  // the scratch of joins between the CTA's warps
+  // rings (at the end the scratch of the join between CTAs), first pieces, prefix
   constexpr size_t kRing = kDenseStages * kStepOf<D> * qgroup_bytes(D), kRings = kNW * kRing;
-  static_assert(kRings >= (4 * kNW * 32 + static_cast<size_t>(kDenseMaxCtas) * 8) * sizeof(float),
-                "weights of one piece per CTA");
+  static_assert(kRings >= kNW * 32 * sizeof(Joined), "scratch of the join between CTAs");
   static_assert(kRing >= qpart_floats(8, D) * sizeof(float), "a warp's last piece in its ring");
   const size_t smem = kRings + kNW * qpart_floats(a.G, D) * sizeof(float) +
-                      qalign16((static_cast<size_t>(a.B) + 1) * sizeof(int)) +
-                      (4 * kNW * 32 + 2 * kNW * static_cast<size_t>(a.G)) * sizeof(float);
+                      qalign16((static_cast<size_t>(a.B) + 1) * sizeof(int));
   auto kern = k_qdecode_dense<D, TERMS, SCORES>;
   int ctas = 0;
   const cudaError_t e = resident_ctas(kern, smem, ctas);
   if (e != cudaSuccess) return e;
-  if (ctas > kDenseMaxCtas) ctas = kDenseMaxCtas;
   return launch_pdl(kern, dim3(ctas), dim3(kNW * 32), smem, st, a);
 }
 
@@ -1142,7 +1192,8 @@ cudaError_t launch_dense_s(const QDecodeArgs& a, cudaStream_t st) {
 
 template <int D, int TERMS, bool POOLED>
 cudaError_t launch_reuse_t(const QDecodeArgs& a, cudaStream_t st) {
-  const size_t smem = (kNW * qpart_floats(a.G, D) + 4 * kNW * 32 + kMaxSplits * a.G) * sizeof(float);
+  size_t smem = kNW * qpart_floats(a.G, D) * sizeof(float);
+  if (smem < kNW * 32 * sizeof(Joined)) smem = kNW * 32 * sizeof(Joined);
   auto kern = k_qdecode_reuse<D, TERMS, POOLED>;
   int ctas = 0;
   const cudaError_t e = resident_ctas(kern, smem, ctas);
