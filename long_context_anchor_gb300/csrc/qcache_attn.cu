@@ -1142,19 +1142,28 @@ __global__ void __launch_bounds__(kNW * 32, 2)
 }
 
 // CTAs of a kernel that the current device holds at once (asked once per host
-// thread, device and shared memory size).
-template <typename K>
-cudaError_t resident_ctas(K kern, size_t smem, int& ctas) {
+// thread, device and shared memory size). The kernel may use all the shared
+// memory there is: the same value whatever the call, so that threads calling
+// with different sizes do not undo one another's setting.
+template <void (*kern)(const QDecodeArgs)>   // by value: each kernel has its own record
+cudaError_t resident_ctas(size_t smem, int& ctas) {
   thread_local int dev_of = -1, slots = 0;
   thread_local size_t smem_of = 0;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
   if (dev != dev_of || smem != smem_of) {
-    int sms = 0, per_sm = 0;
+    int sms = 0, per_sm = 0, most = 0;
+    cudaFuncAttributes fa;
+    if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
+    if ((e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) !=
+        cudaSuccess)
+      return e;
+    most -= static_cast<int>(fa.sharedSizeBytes);
+    if (smem > static_cast<size_t>(most)) return cudaErrorNotSupported;
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) !=
+        cudaSuccess)
+      return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
       return e;
     if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kNW * 32, smem)) !=
@@ -1177,9 +1186,9 @@ cudaError_t launch_dense_t(const QDecodeArgs& a, cudaStream_t st) {
   static_assert(kRing >= qpart_floats(8, D) * sizeof(float), "a warp's last piece in its ring");
   const size_t smem = kRings + kNW * qpart_floats(a.G, D) * sizeof(float) +
                       qalign16((static_cast<size_t>(a.B) + 1) * sizeof(int));
-  auto kern = k_qdecode_dense<D, TERMS, SCORES>;
+  constexpr auto kern = k_qdecode_dense<D, TERMS, SCORES>;
   int ctas = 0;
-  const cudaError_t e = resident_ctas(kern, smem, ctas);
+  const cudaError_t e = resident_ctas<kern>(smem, ctas);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(ctas), dim3(kNW * 32), smem, st, a);
 }
@@ -1194,9 +1203,9 @@ template <int D, int TERMS, bool POOLED>
 cudaError_t launch_reuse_t(const QDecodeArgs& a, cudaStream_t st) {
   size_t smem = kNW * qpart_floats(a.G, D) * sizeof(float);
   if (smem < kNW * 32 * sizeof(Joined)) smem = kNW * 32 * sizeof(Joined);
-  auto kern = k_qdecode_reuse<D, TERMS, POOLED>;
+  constexpr auto kern = k_qdecode_reuse<D, TERMS, POOLED>;
   int ctas = 0;
-  const cudaError_t e = resident_ctas(kern, smem, ctas);
+  const cudaError_t e = resident_ctas<kern>(smem, ctas);
   if (e != cudaSuccess) return e;
   QDecodeArgs u = a;
   const int units = a.B * a.Hkv;

@@ -6,8 +6,8 @@ workspace) and the current CUDA stream. Importing this module loads
 ``libkascade.so`` from this package directory and raises if it is missing;
 there is no fallback.
 """
-import contextlib
 import ctypes
+import functools
 import math
 import os
 from typing import List, Optional, Sequence
@@ -622,47 +622,93 @@ def qcache_alloc(num_blocks, n_kv_heads, head_dim, block_size=64, device="cuda")
                        dtype=torch.uint8, device=device)
 
 
+# A decode step's calls take a few microseconds on the GPU, so the host side is
+# kept short: each tensor passes one combined test and gets the detailed one
+# only when that fails, and the structures that depend on sizes alone are built
+# once per geometry.
+
+def _fits(t, name, shape, dtype, dev):
+    """One tensor's type, shape, dtype, device and contiguity."""
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype
+            and t.device == dev and t.is_contiguous()):
+        _expect(t, name, shape, dtype)
+        raise ValueError("%s: on %s, expected %s" % (name, t.device, dev))
+
+
+def _cuda(t, name):
+    """The CUDA device of a call's first tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s: expected a torch.Tensor" % name)
+    dev = t.device
+    if dev.type != _DEVICE_TYPE:
+        raise ValueError("%s: on %s; the library takes CUDA device tensors" % (name, dev))
+    return dev
+
+
+def _on(dev, stream):
+    """Context in which the tensors' device and the call's stream are current,
+    so that what the call allocates belongs to that stream; None if they are
+    (the default: that device's current stream)."""
+    if dev.type != "cuda":      # only reachable with a stand-in library
+        return None
+    if stream is None:
+        if dev.index == torch._C._cuda_getDevice():
+            return None
+        return torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError("stream: on %s, expected %s" % (stream.device, dev))
+    return torch.cuda.stream(stream)
+
+
+def _raw_stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev.index) if dev.type == "cuda" else None
+
+
+def _qws(ws, dev, nbytes):
+    """The workspace buffer of a cache call. A captured call needs a workspace
+    of its own, large enough already: a graph keeps its address, so the
+    shared default one (which grows) or one grown inside the capture would be
+    gone when the graph is replayed."""
+    if dev.type == "cuda" and torch._C._cuda_isCurrentStreamCapturing():
+        if ws is None or ws.buf is None or ws.buf.numel() < nbytes:
+            raise ValueError("a captured call needs ws=Workspace(device), sized before the capture "
+                             "(run the call once with it)")
+        ws.captured = True
+    if ws is None:
+        ws = default_workspace(dev)
+    buf = ws.buf
+    if buf is None or buf.numel() < nbytes:
+        buf = ws.get(nbytes)
+    if buf.device != dev:
+        raise ValueError("ws: on %s, expected %s" % (buf.device, dev))
+    return buf
+
+
 def _pages(pages, name="pages"):
     """Validated (num_blocks, Hkv, block_size, d) of one layer's pages."""
     if not isinstance(pages, torch.Tensor) or pages.dim() != 4:
         raise ValueError("%s: expected a uint8 tensor [num_blocks, Hkv, block_size/16, 18*d]" % name)
     nb, hkv, groups, size = pages.shape
-    if size not in (18 * 64, 18 * 128):
+    if size != 2304 and size != 1152:
         raise ValueError("%s: last axis %d, expected 18*d with d 64 or 128" % (name, size))
-    _expect(pages, name, pages.shape, torch.uint8)
+    if pages.dtype is not torch.uint8 or not pages.is_contiguous():
+        _expect(pages, name, pages.shape, torch.uint8)
     return nb, hkv, groups * 16, size // 18
 
 
-def _on(dev, stream):
-    """The stream a call runs on (the tensors' device's current one by default),
-    and a context in which that device and stream are current, so that
-    outputs and workspaces allocated by the call belong to the stream."""
-    if dev.type != "cuda":      # only reachable with a stand-in library
-        return None, contextlib.nullcontext()
-    if stream is None and dev.index == torch.cuda.current_device():
-        return torch.cuda.current_stream(dev), contextlib.nullcontext()
-    s = stream if stream is not None else torch.cuda.current_stream(dev)
-    if s.device != dev:
-        raise ValueError("stream: on %s, expected %s" % (s.device, dev))
-    return s, torch.cuda.stream(s)
+@functools.lru_cache(maxsize=256)
+def _qgeo(block_size, num_blocks, max_blocks, k_scale, v_scale):
+    """A kascade_qcache structure by value (read only), as a ctypes reference."""
+    return ctypes.byref(QCache(block_size, num_blocks, max_blocks, k_scale, v_scale))
 
 
-def _qws(ws, dev, nbytes, stream):
-    """The workspace buffer of a cache call. A captured call needs a workspace
-    of its own, large enough already: a graph keeps its address, so the
-    shared default one (which grows) or one grown inside the capture would be
-    gone when the graph is replayed."""
-    if dev.type == "cuda" and torch.cuda.is_current_stream_capturing():
-        if ws is None or ws.buf is None or ws.buf.numel() < nbytes:
-            raise ValueError("a captured call needs ws=Workspace(device), sized before the capture "
-                             "(run the call once with it)")
-        ws.captured = True
-        return ws.buf
-    ws = ws if ws is not None else default_workspace(dev)
-    buf = ws.get(nbytes, stream)
-    if buf.device != dev:
-        raise ValueError("ws: on %s, expected %s" % (buf.device, dev))
-    return buf
+@functools.lru_cache(maxsize=256)
+def _qdesc(B, Hq, Hkv, d, N, code, scale, group_map, pooled, bs, nb, width, k_scale, v_scale, topk):
+    """Descriptor, geometry (ctypes references, read only) and workspace bytes of
+    an attention call of these sizes."""
+    desc = make_desc(B, Hq, Hkv, d, N, code, scale, group_map, pooled)
+    geo = QCache(bs, nb, width, k_scale, v_scale)
+    return ctypes.byref(desc), ctypes.byref(geo), qcache_workspace_size(desc, geo, topk)
 
 
 def qcache_workspace_size(desc, geo, topk: int) -> int:
@@ -681,58 +727,74 @@ def qcache_plan(kv_lens, new_lens, block_table, free_blocks, free_count, block_s
     free_blocks are updated in place. Returns (slot_map [max_new], cu_new
     [B+1], kv_lens_out [B], free_count_out [1]), all int32; the last two may
     be given (kv_lens and free_count themselves included)."""
-    for name, t, nd in (("kv_lens", kv_lens, 1), ("block_table", block_table, 2),
-                        ("free_blocks", free_blocks, 1)):
-        if not isinstance(t, torch.Tensor) or t.dim() != nd:
-            raise ValueError("%s: expected an int32 tensor with %d axes" % (name, nd))
+    dev = _cuda(block_table, "block_table")
+    if block_table.dim() != 2:
+        raise ValueError("block_table: expected an int32 tensor [B, max_blocks]")
+    if not isinstance(free_blocks, torch.Tensor) or free_blocks.dim() != 1:
+        raise ValueError("free_blocks: expected an int32 tensor [num_blocks]")
     B, width = block_table.shape
-    for name, t, shape in (("kv_lens", kv_lens, (B,)), ("new_lens", new_lens, (B,)),
-                           ("block_table", block_table, (B, width)),
-                           ("free_blocks", free_blocks, free_blocks.shape),
-                           ("free_count", free_count, (1,))):
-        _expect(t, name, shape, torch.int32)
-    named = [("kv_lens", kv_lens), ("new_lens", new_lens), ("block_table", block_table),
-             ("free_blocks", free_blocks), ("free_count", free_count)]
-    for name, t, shape in (("kv_lens_out", kv_lens_out, (B,)),
-                           ("free_count_out", free_count_out, (1,))):
-        if t is not None:
-            _expect(t, name, shape, torch.int32)
-            named.append((name, t))
-    dev = _same_cuda_device(named)
-    geo = QCache(int(block_size), free_blocks.numel(), width, 0.0, 0.0)
-    st, ctx = _on(dev, stream)
+    i32 = torch.int32
+    _fits(block_table, "block_table", (B, width), i32, dev)
+    _fits(kv_lens, "kv_lens", (B,), i32, dev)
+    _fits(new_lens, "new_lens", (B,), i32, dev)
+    _fits(free_blocks, "free_blocks", free_blocks.shape, i32, dev)
+    _fits(free_count, "free_count", (1,), i32, dev)
+    if kv_lens_out is not None:
+        _fits(kv_lens_out, "kv_lens_out", (B,), i32, dev)
+    if free_count_out is not None:
+        _fits(free_count_out, "free_count_out", (1,), i32, dev)
+    max_new = int(max_new)
+    geo = _qgeo(int(block_size), free_blocks.shape[0], width, 0.0, 0.0)
+
+    def run():
+        slots, cu, lens, count = torch.empty(max_new + 2 * B + 2, dtype=i32, device=dev).split(
+            (max_new, B + 1, B, 1))
+        lens = lens if kv_lens_out is None else kv_lens_out
+        count = count if free_count_out is None else free_count_out
+        buf = _qws(ws, dev, 256)
+        _check(_lib.kascade_qcache_plan(geo, B, kv_lens.data_ptr(), new_lens.data_ptr(),
+                                        block_table.data_ptr(), free_blocks.data_ptr(),
+                                        free_count.data_ptr(), lens.data_ptr(), count.data_ptr(),
+                                        cu.data_ptr(), slots.data_ptr(), max_new, buf.data_ptr(),
+                                        buf.numel(), _raw_stream(dev)), "kascade_qcache_plan")
+        return slots, cu, lens, count
+
+    ctx = _on(dev, stream)
+    if ctx is None:
+        return run()
     with ctx:
-        new = lambda n: torch.empty(n, dtype=torch.int32, device=dev)
-        slots, cu = new(int(max_new)), new(B + 1)
-        lens = new(B) if kv_lens_out is None else kv_lens_out
-        count = new(1) if free_count_out is None else free_count_out
-        buf = _qws(ws, dev, 256, st)
-        _check(_lib.kascade_qcache_plan(ctypes.byref(geo), B, _ptr(kv_lens), _ptr(new_lens),
-                                        _ptr(block_table), _ptr(free_blocks), _ptr(free_count),
-                                        _ptr(lens), _ptr(count), _ptr(cu), _ptr(slots),
-                                        int(max_new), _ptr(buf), buf.numel(), _stream(st)),
-               "kascade_qcache_plan")
-    return slots, cu, lens, count
+        return run()
 
 
-def _rows(k, v, T, hkv, d):
-    """Element strides of k and v [T, Hkv, d] (last axis contiguous, rows on
-    16-byte boundaries), for the library."""
-    strides = []
-    for name, t in (("k", k), ("v", v)):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError("%s: expected a torch.Tensor" % name)
-        if tuple(t.shape) != (T, hkv, d):
-            raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), (T, hkv, d)))
-        _dtype_code(t)
-        if t.dtype != k.dtype:
-            raise TypeError("%s: dtype %s, expected %s" % (name, t.dtype, k.dtype))
-        unit = 16 // t.element_size()
-        row = [t.stride(0) if T > 1 else 0, t.stride(1) if hkv > 1 else 0]
-        if t.numel() and (t.stride(2) != 1 or any(s % unit for s in row) or t.data_ptr() % 16):
-            raise ValueError("%s: rows must be contiguous and start on 16-byte boundaries" % name)
-        strides += row
-    return (ctypes.c_int64 * 4)(*strides)
+_ROW_CODES = {torch.bfloat16: (BF16, 8), torch.float32: (F32, 4)}   # code, elements per 16 bytes
+
+
+def _row_strides(t, name, shape, dtype, dev, unit):
+    """Token and head strides of rows t [T, Hkv, d], which must be contiguous and
+    start on 16-byte boundaries (strides of axes of length 1 do not matter)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s: expected a torch.Tensor" % name)
+    if t.shape != shape:
+        raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+    if t.dtype is not dtype:
+        raise TypeError("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
+    if t.device != dev:
+        raise ValueError("%s: on %s, expected %s" % (name, t.device, dev))
+    tok, head, one = t.stride()
+    if shape[0] <= 1:
+        tok = 0
+    if shape[1] <= 1:
+        head = 0
+    if shape[0] and (one != 1 or tok % unit or head % unit or t.data_ptr() % 16):
+        raise ValueError("%s: rows must be contiguous and start on 16-byte boundaries" % name)
+    return tok, head
+
+
+def _slots(slot_map, dev):
+    if not isinstance(slot_map, torch.Tensor) or slot_map.dim() != 1:
+        raise ValueError("slot_map: expected an int32 tensor [T]")
+    _fits(slot_map, "slot_map", slot_map.shape, torch.int32, dev)
+    return slot_map.shape[0]
 
 
 def qcache_append(k, v, slot_map, pages, k_scale=1.0, v_scale=1.0, ws=None, stream=None):
@@ -740,21 +802,29 @@ def qcache_append(k, v, slot_map, pages, k_scale=1.0, v_scale=1.0, ws=None, stre
     so a prefill layer's k[b].transpose(0, 1) is taken as it is) into the slots
     slot_map [T] int32 (distinct; negative: skipped) of pages, in place."""
     nb, hkv, bs, d = _pages(pages)
-    if not isinstance(slot_map, torch.Tensor) or slot_map.dim() != 1:
-        raise ValueError("slot_map: expected an int32 tensor [T]")
-    T = slot_map.numel()
-    _expect(slot_map, "slot_map", (T,), torch.int32)
-    strides = _rows(k, v, T, hkv, d)
-    dev = _same_cuda_device([("k", k), ("v", v), ("slot_map", slot_map), ("pages", pages)])
-    geo = QCache(bs, nb, 1, float(k_scale), float(v_scale))
-    st, ctx = _on(dev, stream)
-    with ctx:
-        buf = _qws(ws, dev, 256, st)
-        _check(_lib.kascade_qcache_append(ctypes.byref(geo), hkv, d, _dtype_code(k), _ptr(k),
-                                          _ptr(v), strides, _ptr(slot_map), T, _ptr(pages),
-                                          _ptr(buf), buf.numel(), _stream(st)),
+    dev = _cuda(pages, "pages")
+    T = _slots(slot_map, dev)
+    if not isinstance(k, torch.Tensor) or k.dtype not in _ROW_CODES:
+        raise TypeError("k: expected a bfloat16 or float32 tensor")
+    code, unit = _ROW_CODES[k.dtype]
+    kt, kh = _row_strides(k, "k", (T, hkv, d), k.dtype, dev, unit)
+    vt, vh = _row_strides(v, "v", (T, hkv, d), k.dtype, dev, unit)
+    geo = _qgeo(bs, nb, 1, float(k_scale), float(v_scale))
+
+    def run():
+        buf = _qws(ws, dev, 256)
+        _check(_lib.kascade_qcache_append(geo, hkv, d, code, k.data_ptr(), v.data_ptr(),
+                                          (ctypes.c_int64 * 4)(kt, kh, vt, vh),
+                                          slot_map.data_ptr(), T, pages.data_ptr(),
+                                          buf.data_ptr(), buf.numel(), _raw_stream(dev)),
                "kascade_qcache_append")
-    return pages
+        return pages
+
+    ctx = _on(dev, stream)
+    if ctx is None:
+        return run()
+    with ctx:
+        return run()
 
 
 def qcache_read(pages, slot_map, dtype=torch.bfloat16, k_scale=1.0, v_scale=1.0, k=None, v=None,
@@ -763,51 +833,69 @@ def qcache_read(pages, slot_map, dtype=torch.bfloat16, k_scale=1.0, v_scale=1.0,
     or fp32; zeros for a negative slot). k, v: outputs to fill instead, of any
     token and head strides whose rows do not overlap."""
     nb, hkv, bs, d = _pages(pages)
-    if not isinstance(slot_map, torch.Tensor) or slot_map.dim() != 1:
-        raise ValueError("slot_map: expected an int32 tensor [T]")
-    T = slot_map.numel()
-    _expect(slot_map, "slot_map", (T,), torch.int32)
+    dev = _cuda(pages, "pages")
+    T = _slots(slot_map, dev)
     if (k is None) != (v is None):
         raise ValueError("k, v: give both outputs or neither")
-    dev = _same_cuda_device([("pages", pages), ("slot_map", slot_map)])
-    geo = QCache(bs, nb, 1, float(k_scale), float(v_scale))
-    st, ctx = _on(dev, stream)
-    with ctx:
-        if k is None:
-            k = torch.empty(T, hkv, d, dtype=dtype, device=dev)
-            v = torch.empty_like(k)
-        strides = _rows(k, v, T, hkv, d)
-        if T and any(n > 1 and s == 0 for t in (k, v) for n, s in zip(t.shape[:2], t.stride())):
+    if k is not None:
+        if not isinstance(k, torch.Tensor):
+            raise TypeError("k: expected a torch.Tensor")
+        dtype = k.dtype
+    if dtype not in _ROW_CODES:
+        raise TypeError("rows are read as bfloat16 or float32")
+    code, unit = _ROW_CODES[dtype]
+    shape = (T, hkv, d)
+    if k is None:
+        strides = (hkv * d, d, hkv * d, d)
+    else:
+        strides = (_row_strides(k, "k", shape, dtype, dev, unit) +
+                   _row_strides(v, "v", shape, dtype, dev, unit))
+        if T and any(n > 1 and st == 0 for st, n in zip(strides, (T, hkv, T, hkv))):
             raise ValueError("k, v: output rows must not overlap")
-        _same_cuda_device([("pages", pages), ("k", k), ("v", v)])
-        buf = _qws(ws, dev, 256, st)
-        _check(_lib.kascade_qcache_read(ctypes.byref(geo), hkv, d, _dtype_code(k), _ptr(pages),
-                                        _ptr(slot_map), T, _ptr(k), _ptr(v), strides, _ptr(buf),
-                                        buf.numel(), _stream(st)), "kascade_qcache_read")
-    return k, v
+    geo = _qgeo(bs, nb, 1, float(k_scale), float(v_scale))
+
+    def run():
+        ok = torch.empty(shape, dtype=dtype, device=dev) if k is None else k
+        ov = torch.empty(shape, dtype=dtype, device=dev) if v is None else v
+        buf = _qws(ws, dev, 256)
+        _check(_lib.kascade_qcache_read(geo, hkv, d, code, pages.data_ptr(), slot_map.data_ptr(),
+                                        T, ok.data_ptr(), ov.data_ptr(),
+                                        (ctypes.c_int64 * 4)(*strides), buf.data_ptr(),
+                                        buf.numel(), _raw_stream(dev)), "kascade_qcache_read")
+        return ok, ov
+
+    ctx = _on(dev, stream)
+    if ctx is None:
+        return run()
+    with ctx:
+        return run()
 
 
-def _qattn(q, pages, block_table, kv_lens, kv_len, group_map, scale, k_scale, v_scale, pooled,
-           extra):
-    """Validated descriptor, geometry, sizes and device of one attention call."""
+def _qattn(q, pages, block_table, kv_lens, kv_len, group_map, scale, k_scale, v_scale, pooled, topk,
+           out):
+    """Checks one attention call's common tensors; returns (descriptor and
+    geometry references, workspace bytes, (B, Hq, Hkv, N), device)."""
     nb, hkv, bs, d = _pages(pages)
+    dev = _cuda(pages, "pages")
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q: expected a tensor [B,Hq,d]")
     code = _dtype_code(q)
     B, Hq, dq = q.shape
     if dq != d:
         raise ValueError("q: head_dim %d, the pages hold %d" % (dq, d))
-    _expect(q, "q", q.shape, q.dtype)
+    _fits(q, "q", q.shape, q.dtype, dev)
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table: expected an int32 tensor [B, max_blocks]")
     width = block_table.shape[1]
-    _expect(block_table, "block_table", (B, width), torch.int32)
-    _expect(kv_lens, "kv_lens", (B,), torch.int32)
-    dev = _same_cuda_device([("q", q), ("pages", pages), ("block_table", block_table),
-                             ("kv_lens", kv_lens)] + extra)
+    _fits(block_table, "block_table", (B, width), torch.int32, dev)
+    _fits(kv_lens, "kv_lens", (B,), torch.int32, dev)
+    if out is not None:
+        _fits(out, "out", q.shape, q.dtype, dev)
     N = width * bs if kv_len is None else int(kv_len)
-    desc = make_desc(B, Hq, hkv, d, N, code, scale or 0.0, group_map, pooled)
-    return desc, QCache(bs, nb, width, float(k_scale), float(v_scale)), (B, Hq, hkv, N, d), dev
+    desc, geo, nbytes = _qdesc(B, Hq, hkv, d, N, code, float(scale or 0.0),
+                               None if group_map is None else tuple(int(x) for x in group_map),
+                               bool(pooled), bs, nb, width, float(k_scale), float(v_scale), topk)
+    return desc, geo, nbytes, (B, Hq, hkv, N), dev
 
 
 def qcache_dense_decode(q, pages, block_table, kv_lens, kv_len=None, group_map=None, scale=None,
@@ -817,23 +905,28 @@ def qcache_dense_decode(q, pages, block_table, kv_lens, kv_len=None, group_map=N
     -> out [B,Hq,d], or (out, scores [B,Hq,kv_len] fp32 logits, -inf behind
     the last token). kv_len: the longest length any kv_lens[b] may have
     (default: what the block table can hold)."""
-    extra = []
-    if out is not None:
-        _expect(out, "out", q.shape, q.dtype)
-        extra.append(("out", out))
-    desc, geo, (B, Hq, _, N, _), dev = _qattn(q, pages, block_table, kv_lens, kv_len, group_map,
-                                              scale, k_scale, v_scale, False, extra)
-    st, ctx = _on(dev, stream)
-    with ctx:
-        out = torch.empty_like(q) if out is None else out
+    desc, geo, nbytes, (B, Hq, _, N), dev = _qattn(q, pages, block_table, kv_lens, kv_len,
+                                                   group_map, scale, k_scale, v_scale, False, 0,
+                                                   out)
+
+    def run():
+        o = torch.empty_like(q) if out is None else out
         scores = (torch.empty(B, Hq, N, dtype=torch.float32, device=dev) if return_scores
                   else None)
-        buf = _qws(ws, dev, qcache_workspace_size(desc, geo, 0), st)
-        _check(_lib.kascade_qcache_dense_decode(ctypes.byref(desc), ctypes.byref(geo), _ptr(q),
-                                                _ptr(pages), _ptr(block_table), _ptr(kv_lens),
-                                                _ptr(out), _ptr(scores), _ptr(buf), buf.numel(),
-                                                _stream(st)), "kascade_qcache_dense_decode")
-    return (out, scores) if return_scores else out
+        buf = _qws(ws, dev, nbytes)
+        _check(_lib.kascade_qcache_dense_decode(desc, geo, q.data_ptr(), pages.data_ptr(),
+                                                block_table.data_ptr(), kv_lens.data_ptr(),
+                                                o.data_ptr(),
+                                                scores.data_ptr() if return_scores else None,
+                                                buf.data_ptr(), buf.numel(), _raw_stream(dev)),
+               "kascade_qcache_dense_decode")
+        return (o, scores) if return_scores else o
+
+    ctx = _on(dev, stream)
+    if ctx is None:
+        return run()
+    with ctx:
+        return run()
 
 
 def qcache_anchor_decode(q, pages, block_table, kv_lens, topk, kv_len=None, group_map=None,
@@ -842,29 +935,32 @@ def qcache_anchor_decode(q, pages, block_table, kv_lens, topk, kv_len=None, grou
     """Anchor layer over the cache: (out [B,Hq,d], idx [B,H,topk] int32[, scores
     [B,H,kv_len] fp32]), as anchor_decode; rows of a sequence with fewer than
     topk tokens end in -1 entries."""
-    extra = []
-    if out is not None:
-        _expect(out, "out", q.shape, q.dtype)
-        extra.append(("out", out))
-    if idx is not None:
-        extra.append(("idx", idx))
-    desc, geo, (B, Hq, hkv, N, _), dev = _qattn(q, pages, block_table, kv_lens, kv_len, group_map,
-                                                scale, k_scale, v_scale, pooled, extra)
+    topk = int(topk)
+    desc, geo, nbytes, (B, Hq, hkv, N), dev = _qattn(q, pages, block_table, kv_lens, kv_len,
+                                                     group_map, scale, k_scale, v_scale, pooled,
+                                                     max(topk, 1), out)
     H = hkv if pooled else Hq
     if idx is not None:
-        _expect(idx, "idx", (B, H, int(topk)), torch.int32)
-    st, ctx = _on(dev, stream)
-    with ctx:
-        out = torch.empty_like(q) if out is None else out
-        idx = torch.empty(B, H, int(topk), dtype=torch.int32, device=dev) if idx is None else idx
+        _fits(idx, "idx", (B, H, topk), torch.int32, dev)
+
+    def run():
+        o = torch.empty_like(q) if out is None else out
+        ix = torch.empty(B, H, topk, dtype=torch.int32, device=dev) if idx is None else idx
         scores = torch.empty(B, H, N, dtype=torch.float32, device=dev) if return_scores else None
-        buf = _qws(ws, dev, qcache_workspace_size(desc, geo, int(topk)), st)
-        _check(_lib.kascade_qcache_anchor_decode(ctypes.byref(desc), ctypes.byref(geo), _ptr(q),
-                                                 _ptr(pages), _ptr(block_table), _ptr(kv_lens),
-                                                 int(topk), _ptr(out), _ptr(idx), _ptr(scores),
-                                                 _ptr(buf), buf.numel(), _stream(st)),
+        buf = _qws(ws, dev, nbytes)
+        _check(_lib.kascade_qcache_anchor_decode(desc, geo, q.data_ptr(), pages.data_ptr(),
+                                                 block_table.data_ptr(), kv_lens.data_ptr(), topk,
+                                                 o.data_ptr(), ix.data_ptr(),
+                                                 scores.data_ptr() if return_scores else None,
+                                                 buf.data_ptr(), buf.numel(), _raw_stream(dev)),
                "kascade_qcache_anchor_decode")
-    return (out, idx, scores) if return_scores else (out, idx)
+        return (o, ix, scores) if return_scores else (o, ix)
+
+    ctx = _on(dev, stream)
+    if ctx is None:
+        return run()
+    with ctx:
+        return run()
 
 
 def qcache_reuse_decode(q, pages, block_table, kv_lens, idx, kv_len=None, group_map=None,
@@ -874,24 +970,27 @@ def qcache_reuse_decode(q, pages, block_table, kv_lens, idx, kv_len=None, group_
     [B,Hkv,topk]; int32, ascending, -1 behind the last entry)."""
     if not isinstance(idx, torch.Tensor) or idx.dim() != 3:
         raise ValueError("idx: expected an int32 tensor [B,H,topk]")
-    extra = [("idx", idx)]
-    if out is not None:
-        _expect(out, "out", q.shape, q.dtype)
-        extra.append(("out", out))
-    desc, geo, (B, Hq, hkv, _, _), dev = _qattn(q, pages, block_table, kv_lens, kv_len, group_map,
-                                                scale, k_scale, v_scale, pooled, extra)
-    topk = idx.shape[-1]
-    _expect(idx, "idx", (B, hkv if pooled else Hq, topk), torch.int32)
-    st, ctx = _on(dev, stream)
-    with ctx:
-        out = torch.empty_like(q) if out is None else out
-        buf = _qws(ws, dev, qcache_workspace_size(desc, geo, topk), st)
-        _check(_lib.kascade_qcache_reuse_decode(ctypes.byref(desc), ctypes.byref(geo), _ptr(q),
-                                                _ptr(pages), _ptr(block_table), _ptr(kv_lens),
-                                                topk, _ptr(idx), _ptr(out), _ptr(buf),
-                                                buf.numel(), _stream(st)),
+    topk = idx.shape[2]
+    desc, geo, nbytes, (B, Hq, hkv, _), dev = _qattn(q, pages, block_table, kv_lens, kv_len,
+                                                     group_map, scale, k_scale, v_scale, pooled,
+                                                     max(topk, 1), out)
+    _fits(idx, "idx", (B, hkv if pooled else Hq, topk), torch.int32, dev)
+
+    def run():
+        o = torch.empty_like(q) if out is None else out
+        buf = _qws(ws, dev, nbytes)
+        _check(_lib.kascade_qcache_reuse_decode(desc, geo, q.data_ptr(), pages.data_ptr(),
+                                                block_table.data_ptr(), kv_lens.data_ptr(), topk,
+                                                idx.data_ptr(), o.data_ptr(), buf.data_ptr(),
+                                                buf.numel(), _raw_stream(dev)),
                "kascade_qcache_reuse_decode")
-    return out
+        return o
+
+    ctx = _on(dev, stream)
+    if ctx is None:
+        return run()
+    with ctx:
+        return run()
 
 
 def qcache_run_stack(qs, pages, block_table, kv_lens, topk, anchors, new_ks=None, new_vs=None,
@@ -916,9 +1015,10 @@ def qcache_run_stack(qs, pages, block_table, kv_lens, topk, anchors, new_ks=None
         raise ValueError("new_lens, free_blocks, free_count: give all or none")
     if new_lens is None and new_ks is not None and slot_map is None:
         raise ValueError("new rows need new_lens (a plan) or slot_map")
-    extra = []
-    desc, geo, (B, Hq, hkv, N, d), dev = _qattn(qs[0], pages[0], block_table, kv_lens, kv_len,
-                                                group_map, scale, k_scale, v_scale, pooled, extra)
+    topk = int(topk)
+    desc, geo, nbytes, (B, Hq, hkv, N), dev = _qattn(
+        qs[0], pages[0], block_table, kv_lens, kv_len, group_map, scale, k_scale, v_scale, pooled,
+        max(topk, 1) if len(anchors) else 0, None)
     _all_like(qs, "qs", qs[0].shape, qs[0].dtype, dev)
     _all_like(pages, "pages", pages[0].shape, torch.uint8, dev)
     T = 0
@@ -927,47 +1027,49 @@ def qcache_run_stack(qs, pages, block_table, kv_lens, topk, anchors, new_ks=None
             raise ValueError("new_ks[0]: expected a tensor [T,Hkv,d]")
         T = new_ks[0].shape[0]
         for name, ts in (("new_ks", new_ks), ("new_vs", new_vs)):
-            _all_like(ts, name, torch.Size((T, hkv, d)), qs[0].dtype, dev)
+            _all_like(ts, name, torch.Size((T, hkv, qs[0].shape[2])), qs[0].dtype, dev)
     elif slot_map is not None:
         T = slot_map.numel()
     ints = [("new_lens", new_lens, (B,)), ("slot_map", slot_map, (T,)), ("cu_new", cu_new, (B + 1,)),
-            ("free_count", free_count, (1,))]
-    if free_blocks is not None:
-        ints.append(("free_blocks", free_blocks, (pages[0].shape[0],)))
+            ("free_count", free_count, (1,)), ("free_blocks", free_blocks, (pages[0].shape[0],))]
     for name, t, shape in ints:
         if t is not None:
-            _expect(t, name, shape, torch.int32)
-            _same_cuda_device([("qs[0]", qs[0]), (name, t)])
+            _fits(t, name, shape, torch.int32, dev)
     H = hkv if pooled else Hq
     if outs is not None:
         if len(outs) != L:
             raise ValueError("outs: one tensor per layer (got %d for %d layers)" % (len(outs), L))
         _all_like(outs, "outs", qs[0].shape, qs[0].dtype, dev)
     if idx_buf is not None:
-        _expect(idx_buf, "idx_buf", (B, H, int(topk)), torch.int32)
-        _same_cuda_device([("qs[0]", qs[0]), ("idx_buf", idx_buf)])
-    st, ctx = _on(dev, stream)
-    with ctx:
+        _fits(idx_buf, "idx_buf", (B, H, max(topk, 1)), torch.int32, dev)
+
+    def run():
         new = lambda *n: torch.empty(*n, dtype=torch.int32, device=dev)
-        outs = [torch.empty_like(q) for q in qs] if outs is None else outs
-        idx_buf = new(B, H, max(1, int(topk))) if idx_buf is None else idx_buf
+        os_ = [torch.empty_like(q) for q in qs] if outs is None else outs
+        ib = new(B, H, max(1, topk)) if idx_buf is None else idx_buf
+        sm, cu = slot_map, cu_new
         if new_lens is not None:
-            slot_map = new(T) if slot_map is None else slot_map
-            cu_new = new(B + 1) if cu_new is None else cu_new
+            sm = new(T) if sm is None else sm
+            cu = new(B + 1) if cu is None else cu
         addr = lambda t: None if t is None else t.data_ptr()
         step = QCacheStep(addr(block_table), addr(kv_lens), addr(new_lens), addr(free_blocks),
-                          addr(free_count), addr(cu_new), addr(slot_map), T)
-        buf = _qws(ws, dev, qcache_workspace_size(desc, geo, int(topk) if len(anchors) else 0), st)
+                          addr(free_count), addr(cu), addr(sm), T)
+        buf = _qws(ws, dev, nbytes)
         arr = lambda ts: (ctypes.c_void_p * L)(*[t.data_ptr() for t in ts])
         an = (ctypes.c_int32 * max(1, len(anchors)))(*[int(a) for a in anchors])
-        _check(_lib.kascade_qcache_run_stack(ctypes.byref(desc), ctypes.byref(geo),
-                                             ctypes.byref(step), L, arr(qs),
+        _check(_lib.kascade_qcache_run_stack(desc, geo, ctypes.byref(step), L, arr(qs),
                                              arr(new_ks) if new_ks is not None else None,
                                              arr(new_vs) if new_vs is not None else None,
-                                             arr(pages), int(topk), an, len(anchors), arr(outs),
-                                             _ptr(idx_buf), _ptr(buf), buf.numel(), _stream(st)),
-               "kascade_qcache_run_stack")
-    return outs, idx_buf
+                                             arr(pages), topk, an, len(anchors), arr(os_),
+                                             ib.data_ptr(), buf.data_ptr(), buf.numel(),
+                                             _raw_stream(dev)), "kascade_qcache_run_stack")
+        return os_, ib
+
+    ctx = _on(dev, stream)
+    if ctx is None:
+        return run()
+    with ctx:
+        return run()
 
 
 # -------------------------------------------------------------- scheduling --

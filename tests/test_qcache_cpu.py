@@ -193,7 +193,9 @@ def fake(K, monkeypatch):
     monkeypatch.setattr(K, "_lib", rec)
     monkeypatch.setattr(K, "_stream", lambda stream=None: None)
     monkeypatch.setattr(K, "_DEVICE_TYPE", "cpu")
-    return rec
+    K._qdesc.cache_clear()
+    yield rec
+    K._qdesc.cache_clear()      # its sizes came from the stand-in
 
 
 def _state(B=3, Hq=8, Hkv=2, d=128, bs=32, nb=20, width=5, dtype=BF):
