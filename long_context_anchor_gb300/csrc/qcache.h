@@ -75,6 +75,7 @@ struct QPlanArgs {
   int32_t* cu_new;            // [B + 1]
   int32_t* slot_map;          // [max_new]
   unsigned int* err;
+  unsigned int* flag;         // two words of the workspace header, zero between calls
   int B, bs_shift, num_blocks, max_blocks, max_new;
 };
 cudaError_t launch_qplan(const QPlanArgs& a, cudaStream_t st);

@@ -285,6 +285,7 @@ kascade_status run_qplan(const QCacheShape& c, int n_seqs, const int32_t* kv_len
   a.cu_new = cu_new;
   a.slot_map = slot_map;
   a.err = static_cast<unsigned int*>(ws);
+  a.flag = static_cast<WsHeader*>(ws)->pad;
   a.B = n_seqs;
   a.bs_shift = c.bs_shift;
   a.num_blocks = c.num_blocks;

@@ -1,7 +1,7 @@
 // qcache_store.cu — the paged 4-bit key/value cache's bookkeeping and rows:
 //
-//   k_qplan    block tables and the stack of free blocks from request lengths
-//   k_qslots   the slot of every new token
+//   k_qplan    block tables, the stack of free blocks and the slots of new
+//              tokens from request lengths
 //   k_qappend  rows quantised into their slots
 //   k_qread    rows read back from their slots
 //
@@ -22,40 +22,65 @@ namespace kascade {
 namespace {
 
 // ---------------------------------------------------------------- planner --
+// A sequence of L tokens that changes by n tokens ends with L' = max(0, L + n)
+// of them and holds ceil(L' / block_size) blocks. Blocks given back are pushed
+// on the stack in (sequence, column) order, then blocks taken are popped in
+// the same order, so the outcome does not depend on timing: with c blocks on
+// the stack and G given back, the j-th block taken is the one at c + G - 1 - j,
+// which is the (G - 1 - j)-th given back or an old entry of the stack. No
+// entry that is read is written in the same step, so after the checks every
+// move and every slot is made on its own.
+//
+// Everything is checked before anything is written: a step that cannot be
+// served changes nothing, leaves every slot -1 and records bad input. Small
+// steps run in one CTA and one launch; larger ones in two launches of many
+// CTAs, checks first, each CTA scanning the lengths for itself.
 constexpr int kPlanThreads = 1024;
+// One launch up to this many blocks and new tokens (one round of the CTA's
+// threads or two): 1.1 us of 8 requests' step are saved by the second launch
+// not made, while 32768 moved blocks take one CTA 150 us and two launches of
+// 152 CTAs 14 us.
+constexpr int kPlanOneCta = 2048;
 
-// Inclusive scan over the block, two values at once.
-__device__ __forceinline__ void block_scan2(int& x, int& y, int2* warp_tot) {
+struct PlanScan {
+  int gives, takes;      // blocks given back and taken by all sequences
+  int c;                 // valid entries of the stack
+  bool bad;              // the same in every thread
+};
+
+// Inclusive scan over the block, three values at once; totals in tot.
+__device__ __forceinline__ void block_scan3(int (&v)[3], int3* warp_tot, int (&tot)[3]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int ox = __shfl_up_sync(0xffffffffu, x, off);
-    const int oy = __shfl_up_sync(0xffffffffu, y, off);
-    if (lane >= off) {
-      x += ox;
-      y += oy;
-    }
-  }
-  if (lane == 31) warp_tot[warp] = make_int2(x, y);
-  __syncthreads();
-  if (warp == 0) {
-    int2 t = warp_tot[lane];
+  auto scan = [&](int (&x)[3]) {
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int ox = __shfl_up_sync(0xffffffffu, t.x, off);
-      const int oy = __shfl_up_sync(0xffffffffu, t.y, off);
-      if (lane >= off) {
-        t.x += ox;
-        t.y += oy;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const unsigned int o = __shfl_up_sync(0xffffffffu, x[i], off);
+        if (lane >= off) x[i] = static_cast<int>(x[i] + o);
       }
     }
-    warp_tot[lane] = t;
+  };
+  scan(v);
+  if (lane == 31) warp_tot[warp] = make_int3(v[0], v[1], v[2]);
+  __syncthreads();
+  if (warp == 0) {
+    const int3 t = warp_tot[lane];
+    int w[3] = {t.x, t.y, t.z};
+    scan(w);
+    warp_tot[lane] = make_int3(w[0], w[1], w[2]);
   }
   __syncthreads();
   if (warp > 0) {
-    x += warp_tot[warp - 1].x;
-    y += warp_tot[warp - 1].y;
+    const int3 t = warp_tot[warp - 1];
+    v[0] += t.x;
+    v[1] += t.y;
+    v[2] += t.z;
   }
+  const int3 t = warp_tot[31];
+  tot[0] = t.x;
+  tot[1] = t.y;
+  tot[2] = t.z;
   __syncthreads();
 }
 
@@ -70,161 +95,178 @@ __device__ __forceinline__ int owner_of(const int* pre, int B, int i) {
   return lo;
 }
 
-// One CTA. A sequence of L tokens that changes by n tokens ends with
-// L' = max(0, L + n) of them and holds ceil(L' / block_size) blocks. Blocks
-// given back are pushed on the stack in (sequence, column) order, then blocks
-// taken are popped in the same order, so the outcome does not depend on
-// timing. Everything is checked before anything is written: a step that
-// cannot be served (not enough free blocks, a table row too short, more new
-// tokens than slots, an id or a length out of range) changes nothing, leaves
-// every slot -1 and records bad input. Bound by latency: a few dependent
-// rounds of loads and block scans.
+// A sequence's tokens before and after; false (both 0) if out of range.
+__device__ __forceinline__ bool plan_len(const QPlanArgs& a, int b, int& L, int& to) {
+  const long long cap = static_cast<long long>(a.max_blocks) << a.bs_shift;
+  L = a.kv_lens[b];
+  const long long t = static_cast<long long>(L) + a.new_lens[b];
+  const bool ok = L >= 0 && L <= cap && t <= cap;
+  to = t < 0 ? 0 : static_cast<int>(t);
+  if (!ok) L = to = 0;
+  return ok;
+}
+__device__ __forceinline__ int plan_blocks(const QPlanArgs& a, int tokens) {
+  return (tokens + (1 << a.bs_shift) - 1) >> a.bs_shift;
+}
+
+// pre[0..2]: what sequences before b give back, take and add, [B + 1] each.
+__device__ PlanScan plan_scan(const QPlanArgs& a, int* const (&pre)[3]) {
+  __shared__ int3 warp_tot[32];
+  const int tid = threadIdx.x;
+  PlanScan r;
+  r.c = *a.free_count;
+  __shared__ long long s_tokens[32];
+  int carry[3] = {0, 0, 0};
+  long long tokens = 0;
+  bool bad = false;
+  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int v[3] = {0, 0, 0}, own[3], tot[3];
+    if (b < a.B) {
+      int L, to;
+      bad |= !plan_len(a, b, L, to);
+      const int have = plan_blocks(a, L), need = plan_blocks(a, to);
+      v[0] = max(0, have - need);
+      v[1] = max(0, need - have);
+      v[2] = max(0, to - L);   // may add up to more than 32 bits: refused below
+      tokens += v[2];
+    }
+#pragma unroll
+    for (int i = 0; i < 3; ++i) own[i] = v[i];
+    block_scan3(v, warp_tot, tot);
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      if (b < a.B) pre[i][b] = carry[i] + v[i] - own[i];
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+      carry[i] = static_cast<int>(static_cast<unsigned int>(carry[i]) + tot[i]);
+  }
+  auto warp_sum = [](long long x) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x;
+  };
+  tokens = warp_sum(tokens);
+  if ((tid & 31) == 0) s_tokens[tid >> 5] = tokens;
+  r.gives = carry[0];
+  r.takes = carry[1];
+  if (tid == 0) {
+    pre[0][a.B] = r.gives;
+    pre[1][a.B] = r.takes;
+    pre[2][a.B] = carry[2];
+  }
+  const long long top = static_cast<long long>(r.c) + r.gives;
+  bad |= r.c < 0 || r.c > a.num_blocks || top > a.num_blocks || r.takes > top;
+  __syncthreads();
+  if (tid < 32) bad |= warp_sum(s_tokens[tid]) > a.max_new;
+  r.bad = __syncthreads_or(bad) != 0;
+  return r;
+}
+
+// The i-th block given back.
+__device__ __forceinline__ int plan_given(const QPlanArgs& a, const int* give, int i) {
+  const int b = owner_of(give, a.B, i);
+  int L, to;
+  plan_len(a, b, L, to);
+  return a.table[static_cast<size_t>(b) * a.max_blocks + plan_blocks(a, to) + i - give[b]];
+}
+// The j-th block taken.
+__device__ __forceinline__ int plan_taken(const QPlanArgs& a, const PlanScan& r, const int* give,
+                                          int j) {
+  return j < r.gives ? plan_given(a, give, r.gives - 1 - j) : a.free_blocks[r.c + r.gives - 1 - j];
+}
+
+// Ids that move: those given back, and the old part of the stack that is taken.
+__device__ bool plan_bad_ids(const QPlanArgs& a, const PlanScan& r, const int* give, int t0,
+                             int step) {
+  bool bad = false;
+  auto check = [&](int id) { bad |= id < 0 || id >= a.num_blocks; };
+  for (int i = t0; i < r.gives; i += step) check(plan_given(a, give, i));
+  for (int j = r.gives + t0; j < r.takes; j += step) check(plan_taken(a, r, give, j));
+  return bad;
+}
+
+// Thread t0 of `step`: its share of the moves and of the slots.
+__device__ void plan_apply(const QPlanArgs& a, const PlanScan& r, int* const (&pre)[3], bool bad,
+                           int t0, int step) {
+  const int sh = a.bs_shift;
+  if (!bad) {
+    for (int i = t0; i < r.gives; i += step) a.free_blocks[r.c + i] = plan_given(a, pre[0], i);
+    for (int j = t0; j < r.takes; j += step) {
+      const int b = owner_of(pre[1], a.B, j);
+      int L, to;
+      plan_len(a, b, L, to);
+      a.table[static_cast<size_t>(b) * a.max_blocks + plan_blocks(a, L) + j - pre[1][b]] =
+          plan_taken(a, r, pre[0], j);
+    }
+  }
+  const int total = bad ? 0 : pre[2][a.B];
+  for (int i = t0; i < a.max_new; i += step) {
+    int slot = -1;
+    if (i < total) {
+      const int b = owner_of(pre[2], a.B, i);
+      int L, to;
+      plan_len(a, b, L, to);
+      const int p = L + i - pre[2][b], col = p >> sh, have = plan_blocks(a, L);
+      // the block that the sequence's last token is in, or one taken now
+      const int id = col < have ? a.table[static_cast<size_t>(b) * a.max_blocks + col]
+                                : plan_taken(a, r, pre[0], pre[1][b] + col - have);
+      if (id >= 0 && id < a.num_blocks) slot = (id << sh) | (p & ((1 << sh) - 1));
+      else report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x502);
+    }
+    a.slot_map[i] = slot;
+  }
+}
+
+// Lengths, running numbers of new tokens and the stack's count, by one CTA
+// once nothing reads the old ones (they may be the same arrays).
+__device__ void plan_finish(const QPlanArgs& a, const PlanScan& r, const int* add, bool bad) {
+  for (int b = threadIdx.x; b < a.B; b += kPlanThreads) {
+    int L, to;
+    const int keep = a.kv_lens[b];
+    plan_len(a, b, L, to);
+    a.kv_lens_out[b] = bad ? keep : to;
+    a.cu_new[b + 1] = bad ? 0 : add[b + 1];
+  }
+  if (threadIdx.x == 0) {
+    a.cu_new[0] = 0;
+    *a.free_count_out = bad ? r.c : r.c + r.gives - r.takes;
+    if (bad) report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x501);
+  }
+}
+
+// CHECK: bad ids are noted in the workspace header's word `flag`. APPLY: the
+// step itself; the last CTA to finish writes the lengths and clears the
+// header's words again. Both: the whole step in one CTA. Bound by latency: a
+// few dependent rounds of loads and block scans.
+template <bool CHECK, bool APPLY>
 __global__ void __launch_bounds__(kPlanThreads) k_qplan(const __grid_constant__ QPlanArgs a) {
   pdl_wait();
   pdl_trigger();
   extern __shared__ int sm[];
-  int* pre_give = sm;                 // [B + 1] blocks given back before sequence b
-  int* pre_take = sm + a.B + 1;       // [B + 1] blocks taken before sequence b
-  __shared__ int2 warp_tot[32];
-  __shared__ int s_bad;
-  const int tid = threadIdx.x, B = a.B, sh = a.bs_shift;
-  const int bs = 1 << sh;
-  const long long cap = static_cast<long long>(a.max_blocks) << sh;
-  if (tid == 0) s_bad = 0;
+  int* const pre[3] = {sm, sm + a.B + 1, sm + 2 * (a.B + 1)};
+  const PlanScan r = plan_scan(a, pre);
+  const int t0 = blockIdx.x * kPlanThreads + threadIdx.x, step = gridDim.x * kPlanThreads;
+  bool bad = r.bad;
+  if (CHECK && !bad) {
+    bad = plan_bad_ids(a, r, pre[0], t0, step);
+    if (APPLY) bad = __syncthreads_or(bad) != 0;
+    else if (bad) atomicOr(a.flag, 1u);
+  }
+  if (!APPLY) return;
+  if (!CHECK) bad |= *a.flag != 0u;
+  plan_apply(a, r, pre, bad, t0, step);
   __syncthreads();
-  auto read_len = [&](int b, int& L, int& to) -> bool {
-    L = a.kv_lens[b];
-    const long long t = static_cast<long long>(L) + a.new_lens[b];
-    const bool ok = L >= 0 && L <= cap && t <= cap;
-    to = t < 0 ? 0 : static_cast<int>(t);
-    if (!ok) L = to = 0;
-    return ok;
-  };
-  int carry_g = 0, carry_t = 0;
-  long long tokens = 0;
-  bool bad = false;
-  for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
-    const int b = b0 + tid;
-    int give = 0, take = 0;
-    if (b < B) {
-      int L, to;
-      bad |= !read_len(b, L, to);
-      const int have = (L + bs - 1) >> sh, need = (to + bs - 1) >> sh;
-      give = max(0, have - need);
-      take = max(0, need - have);
-      tokens += max(0, to - L);
-    }
-    int ig = give, it = take;
-    block_scan2(ig, it, warp_tot);
-    if (b < B) {
-      pre_give[b] = carry_g + ig - give;
-      pre_take[b] = carry_t + it - take;
-    }
-    carry_g += warp_tot[31].x;   // totals of this round (the scan ends with a barrier)
-    carry_t += warp_tot[31].y;
-    __syncthreads();
+  if (CHECK) {
+    plan_finish(a, r, pre[2], bad);
+    return;
   }
-  const int gives = carry_g, takes = carry_t;
-  if (tid == 0) {
-    pre_give[B] = gives;
-    pre_take[B] = takes;
-  }
-  const int c = *a.free_count;
-  const long long top = static_cast<long long>(c) + gives;
-  bad |= c < 0 || c > a.num_blocks || top > a.num_blocks || takes > top;
-  // new tokens of all sequences
-  __shared__ unsigned long long s_tokens;
-  if (tid == 0) s_tokens = 0;
+  __shared__ bool s_last;
+  if (threadIdx.x == 0) s_last = atomicAdd(a.flag + 1, 1u) == gridDim.x - 1;
   __syncthreads();
-  if (tokens) atomicAdd(&s_tokens, static_cast<unsigned long long>(tokens));
-  if (bad) s_bad = 1;
-  __syncthreads();
-  if (static_cast<long long>(s_tokens) > a.max_new && tid == 0) s_bad = 1;
-  __syncthreads();
-  // ids that move: those given back, and the old part of the stack that is taken
-  if (!s_bad) {
-    for (int i = tid; i < gives; i += kPlanThreads) {
-      const int b = owner_of(pre_give, B, i);
-      int L, to;
-      read_len(b, L, to);
-      const int id = a.table[static_cast<size_t>(b) * a.max_blocks + ((to + bs - 1) >> sh) + i -
-                             pre_give[b]];
-      if (id < 0 || id >= a.num_blocks) s_bad = 1;
-    }
-    for (int i = max(0, takes - gives) - 1 - tid; i >= 0; i -= kPlanThreads) {
-      const int id = a.free_blocks[c - 1 - i];
-      if (id < 0 || id >= a.num_blocks) s_bad = 1;
-    }
-  }
-  __syncthreads();
-  bad = s_bad != 0;
-  if (bad && tid == 0) report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x501);
-  if (!bad) {
-    for (int i = tid; i < gives; i += kPlanThreads) {
-      const int b = owner_of(pre_give, B, i);
-      int L, to;
-      read_len(b, L, to);
-      a.free_blocks[c + i] = a.table[static_cast<size_t>(b) * a.max_blocks +
-                                     ((to + bs - 1) >> sh) + i - pre_give[b]];
-    }
-    __syncthreads();   // the blocks given back are on the stack before any is taken
-    for (int i = tid; i < takes; i += kPlanThreads) {
-      const int b = owner_of(pre_take, B, i);
-      int L, to;
-      read_len(b, L, to);
-      a.table[static_cast<size_t>(b) * a.max_blocks + ((L + bs - 1) >> sh) + i - pre_take[b]] =
-          a.free_blocks[static_cast<int>(top) - 1 - i];
-    }
-  }
-  __syncthreads();
-  // lengths (kv_lens_out may be kv_lens: each is read and written by one thread) and
-  // the running number of new tokens
-  int carry = 0;
-  for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
-    const int b = b0 + tid;
-    int add = 0, zero = 0;
-    if (b < B) {
-      int L, to;
-      const bool ok = read_len(b, L, to);
-      const int keep = a.kv_lens[b];
-      add = bad ? 0 : max(0, to - L);
-      a.kv_lens_out[b] = bad || !ok ? keep : to;
-    }
-    int incl = add;
-    block_scan2(incl, zero, warp_tot);
-    if (b < B) a.cu_new[b + 1] = carry + incl;
-    carry += warp_tot[31].x;
-    __syncthreads();
-  }
-  if (tid == 0) {
-    a.cu_new[0] = 0;
-    *a.free_count_out = bad ? c : static_cast<int>(top) - takes;
-  }
-}
-
-// Slots of the new tokens, in sequence order; -1 behind the last one. The
-// position follows from the new length, so kv_lens_out may be kv_lens.
-__global__ void __launch_bounds__(256) k_qslots(const __grid_constant__ QPlanArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  const int sh = a.bs_shift, mask = (1 << sh) - 1;
-  const int total = a.cu_new[a.B];
-  for (int i = blockIdx.x * 256 + threadIdx.x; i < a.max_new; i += gridDim.x * 256) {
-    int slot = -1;
-    if (i < total) {
-      int lo = 0, hi = a.B;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (a.cu_new[mid] <= i) lo = mid;
-        else hi = mid;
-      }
-      const int p = a.kv_lens_out[lo] - a.cu_new[lo + 1] + i;
-      const int id = a.table[static_cast<size_t>(lo) * a.max_blocks + (p >> sh)];
-      if (id >= 0 && id < a.num_blocks) slot = (id << sh) | (p & mask);
-      else report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x502);   // the old last block's id
-    }
-    a.slot_map[i] = slot;
-  }
+  if (!s_last) return;
+  plan_finish(a, r, pre[2], bad);
+  if (threadIdx.x == 0) a.flag[0] = a.flag[1] = 0u;
 }
 
 // -------------------------------------------------------------------- rows --
@@ -423,15 +465,28 @@ cudaError_t launch_rows(K kern, const QRowArgs& a, cudaStream_t st) {
 
 }  // namespace
 
+namespace {
+template <bool CHECK, bool APPLY>
+cudaError_t launch_plan(const QPlanArgs& a, int ctas, cudaStream_t st) {
+  const size_t smem = 3 * (static_cast<size_t>(a.B) + 1) * sizeof(int);
+  auto kern = k_qplan<CHECK, APPLY>;
+  if (smem > 48 * 1024) {   // up to 192 KB, the same setting whatever the call
+    const cudaError_t e =
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             3 * (kMaxCounterUnits + 1) * static_cast<int>(sizeof(int)));
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(kern, dim3(ctas), dim3(kPlanThreads), smem, st, a);
+}
+}  // namespace
+
 cudaError_t launch_qplan(const QPlanArgs& a, cudaStream_t st) {
-  const size_t smem = 2 * (static_cast<size_t>(a.B) + 1) * sizeof(int);
-  cudaError_t e = cudaFuncSetAttribute(k_qplan, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  if ((e = launch_pdl(k_qplan, dim3(1), dim3(kPlanThreads), smem, st, a)) != cudaSuccess) return e;
-  if (a.max_new == 0) return cudaSuccess;
-  const int blocks = (a.max_new + 255) / 256;
-  return launch_pdl(k_qslots, dim3(blocks < 608 ? blocks : 608), dim3(256), 0, st, a);
+  const int most = a.num_blocks > a.max_new ? a.num_blocks : a.max_new;   // ids or slots to write
+  if (a.B <= kPlanThreads && most <= kPlanOneCta) return launch_plan<true, true>(a, 1, st);
+  int ctas = (most + kPlanThreads - 1) / kPlanThreads;
+  if (ctas > 152) ctas = 152;
+  const cudaError_t e = launch_plan<true, false>(a, ctas, st);
+  return e != cudaSuccess ? e : launch_plan<false, true>(a, ctas, st);
 }
 
 cudaError_t launch_qappend(const QRowArgs& a, int dtype, cudaStream_t st) {

@@ -265,11 +265,12 @@ def test_plan_against_oracle(K, B, bs, width):
 
 @pytest.mark.parametrize("what", ["blocks", "slots", "width", "length", "given", "free", "count",
                                   "big", "full"])
-def test_plan_refusals_change_nothing(K, what):
+@pytest.mark.parametrize("nb", [12, 3012])      # one launch, two launches
+def test_plan_refusals_change_nothing(K, what, nb):
     bs, width = 16, 4
     lens, new = [20, 33, 64], [5, 30, -40]
     table = np.array([[0, 1, -1, -1], [2, 3, 4, -1], [5, 6, 7, 8]])
-    free = np.array([9, 10, 11] + [-1] * 9)
+    free = np.array([9, 10, 11] + [-1] * (nb - 3))
     count, max_new = 3, 99
     assert Q.plan(lens, new, table, free, count, bs, max_new) is not None
     if what == "blocks":
@@ -279,16 +280,16 @@ def test_plan_refusals_change_nothing(K, what):
     if what == "length":
         lens = [-1, 33, 64]
     if what == "given":
-        table[2, 3] = 12
+        table[2, 3] = nb
     if what == "free":
-        free[1] = 99
+        free[1] = nb + 87
         new = [40, 1, 0]
     if what == "count":
-        count = 13
+        count = nb + 1
     if what == "big":
         new = [2 ** 31 - 1, 0, 0]
     if what == "full":
-        count = 11                       # 11 free and 2 given back: more than the cache has
+        count = nb - 1                   # with the 2 given back: more than the cache has
     if what == "width":
         new = [50, 1, 0]
     assert Q.plan(lens, new, table, free, count, bs, max_new) is None
@@ -299,6 +300,14 @@ def test_plan_refusals_change_nothing(K, what):
     assert (slots == -1).all() and not cu.any()
     assert torch.equal(l2, ints(lens)) and int(c2) == count
     assert torch.equal(d[2], ints(table)) and torch.equal(d[3], ints(free))
+    # and the next step is served
+    good = Q.plan([20, 33, 64], [5, 30, -40], np.array([[0, 1, -1, -1], [2, 3, 4, -1], [5, 6, 7, 8]]),
+                  np.array([9, 10, 11] + [-1] * (nb - 3)), 3, bs, 99)
+    got = K.qcache_plan(ints([20, 33, 64]), ints([5, 30, -40]),
+                        ints([[0, 1, -1, -1], [2, 3, 4, -1], [5, 6, 7, 8]]),
+                        ints([9, 10, 11] + [-1] * (nb - 3)), ints([3]), bs, 99, ws=ws)
+    assert np.array_equal(got[0].cpu().numpy(), good[0]) and int(got[3]) == good[3]
+    assert ws.device_error() == K.OK
 
 
 # ------------------------------------------------------------------ dense --
