@@ -6,6 +6,7 @@ workspace) and the current CUDA stream. Importing this module loads
 ``libkascade.so`` from this package directory and raises if it is missing;
 there is no fallback.
 """
+import contextlib
 import ctypes
 import functools
 import math
@@ -645,15 +646,18 @@ def _cuda(t, name):
     return dev
 
 
+def _elsewhere(dev, stream):
+    """Whether a call has to switch to another device or stream first (_on)."""
+    return stream is not None or (dev.type == "cuda" and dev.index != torch._C._cuda_getDevice())
+
+
 def _on(dev, stream):
     """Context in which the tensors' device and the call's stream are current,
-    so that what the call allocates belongs to that stream; None if they are
-    (the default: that device's current stream)."""
+    so that what the call allocates belongs to that stream; inside it the call
+    is made again without a stream."""
     if dev.type != "cuda":      # only reachable with a stand-in library
-        return None
+        return contextlib.nullcontext()
     if stream is None:
-        if dev.index == torch._C._cuda_getDevice():
-            return None
         return torch.cuda.device(dev)
     if stream.device != dev:
         raise ValueError("stream: on %s, expected %s" % (stream.device, dev))
@@ -675,7 +679,7 @@ def _qws(ws, dev, nbytes):
                              "(run the call once with it)")
         ws.captured = True
     if ws is None:
-        ws = default_workspace(dev)
+        ws = _default_ws.get(dev.index) or default_workspace(dev)
     buf = ws.buf
     if buf is None or buf.numel() < nbytes:
         buf = ws.get(nbytes)
@@ -745,25 +749,21 @@ def qcache_plan(kv_lens, new_lens, block_table, free_blocks, free_count, block_s
         _fits(free_count_out, "free_count_out", (1,), i32, dev)
     max_new = int(max_new)
     geo = _qgeo(int(block_size), free_blocks.shape[0], width, 0.0, 0.0)
-
-    def run():
-        slots, cu, lens, count = torch.empty(max_new + 2 * B + 2, dtype=i32, device=dev).split(
-            (max_new, B + 1, B, 1))
-        lens = lens if kv_lens_out is None else kv_lens_out
-        count = count if free_count_out is None else free_count_out
-        buf = _qws(ws, dev, 256)
-        _check(_lib.kascade_qcache_plan(geo, B, kv_lens.data_ptr(), new_lens.data_ptr(),
-                                        block_table.data_ptr(), free_blocks.data_ptr(),
-                                        free_count.data_ptr(), lens.data_ptr(), count.data_ptr(),
-                                        cu.data_ptr(), slots.data_ptr(), max_new, buf.data_ptr(),
-                                        buf.numel(), _raw_stream(dev)), "kascade_qcache_plan")
-        return slots, cu, lens, count
-
-    ctx = _on(dev, stream)
-    if ctx is None:
-        return run()
-    with ctx:
-        return run()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return qcache_plan(kv_lens, new_lens, block_table, free_blocks, free_count, block_size,
+                               max_new, kv_lens_out, free_count_out, ws)
+    slots, cu, lens, count = torch.split_with_sizes(
+        torch.empty(max_new + 2 * B + 2, dtype=i32, device=dev), (max_new, B + 1, B, 1))
+    lens = lens if kv_lens_out is None else kv_lens_out
+    count = count if free_count_out is None else free_count_out
+    buf = _qws(ws, dev, 256)
+    _check(_lib.kascade_qcache_plan(geo, B, kv_lens.data_ptr(), new_lens.data_ptr(),
+                                    block_table.data_ptr(), free_blocks.data_ptr(),
+                                    free_count.data_ptr(), lens.data_ptr(), count.data_ptr(),
+                                    cu.data_ptr(), slots.data_ptr(), max_new, buf.data_ptr(),
+                                    buf.numel(), _raw_stream(dev)), "kascade_qcache_plan")
+    return slots, cu, lens, count
 
 
 _ROW_CODES = {torch.bfloat16: (BF16, 8), torch.float32: (F32, 4)}   # code, elements per 16 bytes
@@ -810,21 +810,16 @@ def qcache_append(k, v, slot_map, pages, k_scale=1.0, v_scale=1.0, ws=None, stre
     kt, kh = _row_strides(k, "k", (T, hkv, d), k.dtype, dev, unit)
     vt, vh = _row_strides(v, "v", (T, hkv, d), k.dtype, dev, unit)
     geo = _qgeo(bs, nb, 1, float(k_scale), float(v_scale))
-
-    def run():
-        buf = _qws(ws, dev, 256)
-        _check(_lib.kascade_qcache_append(geo, hkv, d, code, k.data_ptr(), v.data_ptr(),
-                                          (ctypes.c_int64 * 4)(kt, kh, vt, vh),
-                                          slot_map.data_ptr(), T, pages.data_ptr(),
-                                          buf.data_ptr(), buf.numel(), _raw_stream(dev)),
-               "kascade_qcache_append")
-        return pages
-
-    ctx = _on(dev, stream)
-    if ctx is None:
-        return run()
-    with ctx:
-        return run()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return qcache_append(k, v, slot_map, pages, k_scale, v_scale, ws)
+    buf = _qws(ws, dev, 256)
+    _check(_lib.kascade_qcache_append(geo, hkv, d, code, k.data_ptr(), v.data_ptr(),
+                                      (ctypes.c_int64 * 4)(kt, kh, vt, vh),
+                                      slot_map.data_ptr(), T, pages.data_ptr(),
+                                      buf.data_ptr(), buf.numel(), _raw_stream(dev)),
+           "kascade_qcache_append")
+    return pages
 
 
 def qcache_read(pages, slot_map, dtype=torch.bfloat16, k_scale=1.0, v_scale=1.0, k=None, v=None,
@@ -853,22 +848,17 @@ def qcache_read(pages, slot_map, dtype=torch.bfloat16, k_scale=1.0, v_scale=1.0,
         if T and any(n > 1 and st == 0 for st, n in zip(strides, (T, hkv, T, hkv))):
             raise ValueError("k, v: output rows must not overlap")
     geo = _qgeo(bs, nb, 1, float(k_scale), float(v_scale))
-
-    def run():
-        ok = torch.empty(shape, dtype=dtype, device=dev) if k is None else k
-        ov = torch.empty(shape, dtype=dtype, device=dev) if v is None else v
-        buf = _qws(ws, dev, 256)
-        _check(_lib.kascade_qcache_read(geo, hkv, d, code, pages.data_ptr(), slot_map.data_ptr(),
-                                        T, ok.data_ptr(), ov.data_ptr(),
-                                        (ctypes.c_int64 * 4)(*strides), buf.data_ptr(),
-                                        buf.numel(), _raw_stream(dev)), "kascade_qcache_read")
-        return ok, ov
-
-    ctx = _on(dev, stream)
-    if ctx is None:
-        return run()
-    with ctx:
-        return run()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return qcache_read(pages, slot_map, dtype, k_scale, v_scale, k, v, ws)
+    ok = torch.empty(shape, dtype=dtype, device=dev) if k is None else k
+    ov = torch.empty(shape, dtype=dtype, device=dev) if v is None else v
+    buf = _qws(ws, dev, 256)
+    _check(_lib.kascade_qcache_read(geo, hkv, d, code, pages.data_ptr(), slot_map.data_ptr(),
+                                    T, ok.data_ptr(), ov.data_ptr(),
+                                    (ctypes.c_int64 * 4)(*strides), buf.data_ptr(),
+                                    buf.numel(), _raw_stream(dev)), "kascade_qcache_read")
+    return ok, ov
 
 
 def _qattn(q, pages, block_table, kv_lens, kv_len, group_map, scale, k_scale, v_scale, pooled, topk,
@@ -876,23 +866,33 @@ def _qattn(q, pages, block_table, kv_lens, kv_len, group_map, scale, k_scale, v_
     """Checks one attention call's common tensors; returns (descriptor and
     geometry references, workspace bytes, (B, Hq, Hkv, N), device)."""
     nb, hkv, bs, d = _pages(pages)
-    dev = _cuda(pages, "pages")
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q: expected a tensor [B,Hq,d]")
-    code = _dtype_code(q)
-    B, Hq, dq = q.shape
-    if dq != d:
-        raise ValueError("q: head_dim %d, the pages hold %d" % (dq, d))
-    _fits(q, "q", q.shape, q.dtype, dev)
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
-        raise ValueError("block_table: expected an int32 tensor [B, max_blocks]")
+    dev = pages.device
+    if not (dev.type == _DEVICE_TYPE and isinstance(q, torch.Tensor)
+            and isinstance(block_table, torch.Tensor) and isinstance(kv_lens, torch.Tensor)
+            and q.dim() == 3 and block_table.dim() == 2 and q.dtype in _ROW_CODES
+            and q.shape[2] == d and q.device == dev and q.is_contiguous()
+            and block_table.shape[0] == q.shape[0] and block_table.dtype is torch.int32
+            and block_table.device == dev and block_table.is_contiguous()
+            and kv_lens.shape == q.shape[:1] and kv_lens.dtype is torch.int32
+            and kv_lens.device == dev and kv_lens.is_contiguous()):
+        _cuda(pages, "pages")        # what is wrong, in words
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q: expected a tensor [B,Hq,d]")
+        _dtype_code(q)
+        if q.shape[2] != d:
+            raise ValueError("q: head_dim %d, the pages hold %d" % (q.shape[2], d))
+        _fits(q, "q", q.shape, q.dtype, dev)
+        if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+            raise ValueError("block_table: expected an int32 tensor [B, max_blocks]")
+        _fits(block_table, "block_table", (q.shape[0], block_table.shape[1]), torch.int32, dev)
+        _fits(kv_lens, "kv_lens", (q.shape[0],), torch.int32, dev)
+    B, Hq, _ = q.shape
     width = block_table.shape[1]
-    _fits(block_table, "block_table", (B, width), torch.int32, dev)
-    _fits(kv_lens, "kv_lens", (B,), torch.int32, dev)
     if out is not None:
         _fits(out, "out", q.shape, q.dtype, dev)
     N = width * bs if kv_len is None else int(kv_len)
-    desc, geo, nbytes = _qdesc(B, Hq, hkv, d, N, code, float(scale or 0.0),
+    desc, geo, nbytes = _qdesc(B, Hq, hkv, d, N, _ROW_CODES[q.dtype][0],
+                               0.0 if scale is None else float(scale),
                                None if group_map is None else tuple(int(x) for x in group_map),
                                bool(pooled), bs, nb, width, float(k_scale), float(v_scale), topk)
     return desc, geo, nbytes, (B, Hq, hkv, N), dev
@@ -908,25 +908,21 @@ def qcache_dense_decode(q, pages, block_table, kv_lens, kv_len=None, group_map=N
     desc, geo, nbytes, (B, Hq, _, N), dev = _qattn(q, pages, block_table, kv_lens, kv_len,
                                                    group_map, scale, k_scale, v_scale, False, 0,
                                                    out)
-
-    def run():
-        o = torch.empty_like(q) if out is None else out
-        scores = (torch.empty(B, Hq, N, dtype=torch.float32, device=dev) if return_scores
-                  else None)
-        buf = _qws(ws, dev, nbytes)
-        _check(_lib.kascade_qcache_dense_decode(desc, geo, q.data_ptr(), pages.data_ptr(),
-                                                block_table.data_ptr(), kv_lens.data_ptr(),
-                                                o.data_ptr(),
-                                                scores.data_ptr() if return_scores else None,
-                                                buf.data_ptr(), buf.numel(), _raw_stream(dev)),
-               "kascade_qcache_dense_decode")
-        return (o, scores) if return_scores else o
-
-    ctx = _on(dev, stream)
-    if ctx is None:
-        return run()
-    with ctx:
-        return run()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return qcache_dense_decode(q, pages, block_table, kv_lens, kv_len, group_map, scale,
+                                       k_scale, v_scale, return_scores, out, ws)
+    o = torch.empty_like(q) if out is None else out
+    scores = (torch.empty(B, Hq, N, dtype=torch.float32, device=dev) if return_scores
+              else None)
+    buf = _qws(ws, dev, nbytes)
+    _check(_lib.kascade_qcache_dense_decode(desc, geo, q.data_ptr(), pages.data_ptr(),
+                                            block_table.data_ptr(), kv_lens.data_ptr(),
+                                            o.data_ptr(),
+                                            scores.data_ptr() if return_scores else None,
+                                            buf.data_ptr(), buf.numel(), _raw_stream(dev)),
+           "kascade_qcache_dense_decode")
+    return (o, scores) if return_scores else o
 
 
 def qcache_anchor_decode(q, pages, block_table, kv_lens, topk, kv_len=None, group_map=None,
@@ -942,25 +938,22 @@ def qcache_anchor_decode(q, pages, block_table, kv_lens, topk, kv_len=None, grou
     H = hkv if pooled else Hq
     if idx is not None:
         _fits(idx, "idx", (B, H, topk), torch.int32, dev)
-
-    def run():
-        o = torch.empty_like(q) if out is None else out
-        ix = torch.empty(B, H, topk, dtype=torch.int32, device=dev) if idx is None else idx
-        scores = torch.empty(B, H, N, dtype=torch.float32, device=dev) if return_scores else None
-        buf = _qws(ws, dev, nbytes)
-        _check(_lib.kascade_qcache_anchor_decode(desc, geo, q.data_ptr(), pages.data_ptr(),
-                                                 block_table.data_ptr(), kv_lens.data_ptr(), topk,
-                                                 o.data_ptr(), ix.data_ptr(),
-                                                 scores.data_ptr() if return_scores else None,
-                                                 buf.data_ptr(), buf.numel(), _raw_stream(dev)),
-               "kascade_qcache_anchor_decode")
-        return (o, ix, scores) if return_scores else (o, ix)
-
-    ctx = _on(dev, stream)
-    if ctx is None:
-        return run()
-    with ctx:
-        return run()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return qcache_anchor_decode(q, pages, block_table, kv_lens, topk, kv_len, group_map, scale,
+                                        k_scale, v_scale, return_scores, out, idx, ws,
+                                        pooled=pooled)
+    o = torch.empty_like(q) if out is None else out
+    ix = torch.empty(B, H, topk, dtype=torch.int32, device=dev) if idx is None else idx
+    scores = torch.empty(B, H, N, dtype=torch.float32, device=dev) if return_scores else None
+    buf = _qws(ws, dev, nbytes)
+    _check(_lib.kascade_qcache_anchor_decode(desc, geo, q.data_ptr(), pages.data_ptr(),
+                                             block_table.data_ptr(), kv_lens.data_ptr(), topk,
+                                             o.data_ptr(), ix.data_ptr(),
+                                             scores.data_ptr() if return_scores else None,
+                                             buf.data_ptr(), buf.numel(), _raw_stream(dev)),
+           "kascade_qcache_anchor_decode")
+    return (o, ix, scores) if return_scores else (o, ix)
 
 
 def qcache_reuse_decode(q, pages, block_table, kv_lens, idx, kv_len=None, group_map=None,
@@ -975,22 +968,18 @@ def qcache_reuse_decode(q, pages, block_table, kv_lens, idx, kv_len=None, group_
                                                      group_map, scale, k_scale, v_scale, pooled,
                                                      max(topk, 1), out)
     _fits(idx, "idx", (B, hkv if pooled else Hq, topk), torch.int32, dev)
-
-    def run():
-        o = torch.empty_like(q) if out is None else out
-        buf = _qws(ws, dev, nbytes)
-        _check(_lib.kascade_qcache_reuse_decode(desc, geo, q.data_ptr(), pages.data_ptr(),
-                                                block_table.data_ptr(), kv_lens.data_ptr(), topk,
-                                                idx.data_ptr(), o.data_ptr(), buf.data_ptr(),
-                                                buf.numel(), _raw_stream(dev)),
-               "kascade_qcache_reuse_decode")
-        return o
-
-    ctx = _on(dev, stream)
-    if ctx is None:
-        return run()
-    with ctx:
-        return run()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return qcache_reuse_decode(q, pages, block_table, kv_lens, idx, kv_len, group_map, scale,
+                                       k_scale, v_scale, out, ws, pooled=pooled)
+    o = torch.empty_like(q) if out is None else out
+    buf = _qws(ws, dev, nbytes)
+    _check(_lib.kascade_qcache_reuse_decode(desc, geo, q.data_ptr(), pages.data_ptr(),
+                                            block_table.data_ptr(), kv_lens.data_ptr(), topk,
+                                            idx.data_ptr(), o.data_ptr(), buf.data_ptr(),
+                                            buf.numel(), _raw_stream(dev)),
+           "kascade_qcache_reuse_decode")
+    return o
 
 
 def qcache_run_stack(qs, pages, block_table, kv_lens, topk, anchors, new_ks=None, new_vs=None,
@@ -1042,34 +1031,32 @@ def qcache_run_stack(qs, pages, block_table, kv_lens, topk, anchors, new_ks=None
         _all_like(outs, "outs", qs[0].shape, qs[0].dtype, dev)
     if idx_buf is not None:
         _fits(idx_buf, "idx_buf", (B, H, max(topk, 1)), torch.int32, dev)
-
-    def run():
-        new = lambda *n: torch.empty(*n, dtype=torch.int32, device=dev)
-        os_ = [torch.empty_like(q) for q in qs] if outs is None else outs
-        ib = new(B, H, max(1, topk)) if idx_buf is None else idx_buf
-        sm, cu = slot_map, cu_new
-        if new_lens is not None:
-            sm = new(T) if sm is None else sm
-            cu = new(B + 1) if cu is None else cu
-        addr = lambda t: None if t is None else t.data_ptr()
-        step = QCacheStep(addr(block_table), addr(kv_lens), addr(new_lens), addr(free_blocks),
-                          addr(free_count), addr(cu), addr(sm), T)
-        buf = _qws(ws, dev, nbytes)
-        arr = lambda ts: (ctypes.c_void_p * L)(*[t.data_ptr() for t in ts])
-        an = (ctypes.c_int32 * max(1, len(anchors)))(*[int(a) for a in anchors])
-        _check(_lib.kascade_qcache_run_stack(desc, geo, ctypes.byref(step), L, arr(qs),
-                                             arr(new_ks) if new_ks is not None else None,
-                                             arr(new_vs) if new_vs is not None else None,
-                                             arr(pages), topk, an, len(anchors), arr(os_),
-                                             ib.data_ptr(), buf.data_ptr(), buf.numel(),
-                                             _raw_stream(dev)), "kascade_qcache_run_stack")
-        return os_, ib
-
-    ctx = _on(dev, stream)
-    if ctx is None:
-        return run()
-    with ctx:
-        return run()
+    if _elsewhere(dev, stream):
+        with _on(dev, stream):
+            return qcache_run_stack(qs, pages, block_table, kv_lens, topk, anchors, new_ks, new_vs,
+                                    new_lens, free_blocks, free_count, slot_map, cu_new, kv_len,
+                                    group_map, scale, k_scale, v_scale, outs, idx_buf, ws,
+                                    pooled=pooled)
+    new = lambda *n: torch.empty(*n, dtype=torch.int32, device=dev)
+    os_ = [torch.empty_like(q) for q in qs] if outs is None else outs
+    ib = new(B, H, max(1, topk)) if idx_buf is None else idx_buf
+    sm, cu = slot_map, cu_new
+    if new_lens is not None:
+        sm = new(T) if sm is None else sm
+        cu = new(B + 1) if cu is None else cu
+    addr = lambda t: None if t is None else t.data_ptr()
+    step = QCacheStep(addr(block_table), addr(kv_lens), addr(new_lens), addr(free_blocks),
+                      addr(free_count), addr(cu), addr(sm), T)
+    buf = _qws(ws, dev, nbytes)
+    arr = lambda ts: (ctypes.c_void_p * L)(*[t.data_ptr() for t in ts])
+    an = (ctypes.c_int32 * max(1, len(anchors)))(*[int(a) for a in anchors])
+    _check(_lib.kascade_qcache_run_stack(desc, geo, ctypes.byref(step), L, arr(qs),
+                                         arr(new_ks) if new_ks is not None else None,
+                                         arr(new_vs) if new_vs is not None else None,
+                                         arr(pages), topk, an, len(anchors), arr(os_),
+                                         ib.data_ptr(), buf.data_ptr(), buf.numel(),
+                                         _raw_stream(dev)), "kascade_qcache_run_stack")
+    return os_, ib
 
 
 # -------------------------------------------------------------- scheduling --
