@@ -183,6 +183,14 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src, uint32_t 
 __device__ __forceinline__ void cp_async16_s(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// 4- or 8-byte global -> shared copy; !ok zero-fills without reading.
+template <int BYTES>
+__device__ __forceinline__ void cp_async_small(void* dst, const void* src, bool ok) {
+  static_assert(BYTES == 4 || BYTES == 8, "sizes without the L1 bypass");
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src),
+               "n"(BYTES), "r"(ok ? BYTES : 0)
+               : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }

@@ -100,6 +100,10 @@ kascade_status check_call(const kascade_desc* desc, const kascade_qcache* cache,
   if (static_cast<long long>(k.c.max_blocks) * k.c.block_size < k.s.N)
     return KASCADE_ERR_INVALID_ARG;
   if (static_cast<long long>(k.s.B) * k.c.max_blocks >= (1ll << 31)) return KASCADE_ERR_UNSUPPORTED;
+  // a group's number fits 28 bits (2^28 groups are more than any GPU's memory)
+  if (static_cast<long long>(k.c.num_blocks) * k.s.Hkv * (k.c.block_size / kQGroup) >=
+      (1ll << 28) - 1)
+    return KASCADE_ERR_UNSUPPORTED;
   return KASCADE_OK;
 }
 

@@ -10,9 +10,10 @@
 // code * scale with 2 + 4 significant bits, at most 2688 and a multiple of
 // 2^-10, so it is exact in fp16. q is scaled by a power of two per head so that
 // its largest element lies in [2^12, 2^13): a bf16 q is then exact in fp16
-// down to 2^-26 of that element, an fp32 q is the sum of two fp16 terms (22 bits). The softmax weights
-// are kept as 2^14 p, so that a weight down to 2^-38 of the row's largest one
-// still counts; for fp32 outputs they too are a sum of two fp16 terms.
+// down to 2^-26 of that element, an fp32 q is the sum of two fp16 terms (22
+// bits). The softmax weights are kept as 2^14 p, so that a weight down to 2^-38
+// of the row's largest one still counts; for fp32 outputs they too are a sum of
+// two fp16 terms.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -25,11 +26,16 @@ namespace kascade {
 namespace {
 
 #define kNegInf (-CUDART_INF_F)
+// Running maximum before the first key: below every score, and finite, so
+// that neither exponents nor joins need a case for it.
+constexpr float kNoKey = -3.0e38f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kPShift = 14;          // weights are held as 2^14 p
 constexpr int kQExp = 12;            // q's largest element is scaled to [2^12, 2^13)
-constexpr int kNW = 8;               // warps per CTA (and at most 8 heads per KV head)
+// Slices of 16 keys per step: a step is 4608 bytes at either head size.
+template <int D>
+constexpr int kStepOf = 256 / D;
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                               uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -38,6 +44,16 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
       "{%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// the same with a zero addend
+__device__ __forceinline__ void mma_f16_16816_first(float (&d)[4], uint32_t a0, uint32_t a1,
+                                                    uint32_t a2, uint32_t a3, uint32_t b0,
+                                                    uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
 // the four bytes of w, each two e2m1 codes, as pairs of fp16 (low half first)
 __device__ __forceinline__ void cvt_e2m1x8(uint32_t w, uint32_t (&h)[4]) {
@@ -57,6 +73,12 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
+// low nibbles of a, high nibbles of b
+__device__ __forceinline__ uint32_t nibbles(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xCA;" : "=r"(d) : "r"(0x0f0f0f0fu), "r"(a), "r"(b));
+  return d;
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&v);
@@ -69,26 +91,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ float f16_rounded(float x) { return __half2float(__float2half_rn(x)); }
 
-// Running state of one warp over the keys of one (sequence, KV head). Thread
-// (gid = lane/4, c4 = lane%4) owns heads 2 c4, 2 c4 + 1 and output dims
-// gid * D/8 .. + D/8 of both: o[i] = (dim 2i, head 2c4), (2i, 2c4+1),
-// (2i + 1, 2c4), (2i + 1, 2c4 + 1).
-// mu = m - 14 (what the exponents subtract), finite while m is still -inf.
-template <int D>
-struct QState {
-  float m[2], mu[2], l[2];
-  float o[D / 16][4];
-};
-
-template <int D>
-__device__ __forceinline__ void qstate_init(QState<D>& st) {
-  st.m[0] = st.m[1] = kNegInf;
-  st.mu[0] = st.mu[1] = -kPShift;
-  st.l[0] = st.l[1] = 0.f;
-#pragma unroll
-  for (int i = 0; i < D / 16; ++i) st.o[i][0] = st.o[i][1] = st.o[i][2] = st.o[i][3] = 0.f;
-}
-
+// -------------------------------------------------------------------- query --
 // The query fragments (B operand) of head gid of the group: lane c4 holds dims
 // c4 * D/4 .. + D/4, four of them per MMA, so that a key row's codes are the A
 // operand in stored order. mult[i]: what turns the raw product of head
@@ -117,15 +120,17 @@ __device__ __forceinline__ void load_q(const QDecodeArgs& a, int b, int g, float
       x[4 * i + 3] = v.w;
     }
   } else {
-    const uint2* p = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.q) +
+    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
                                                     row * D + c4 * (D / 4));
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      const uint2 v = ok ? __ldg(p + i) : make_uint2(0u, 0u);
-      x[4 * i] = __uint_as_float(v.x << 16);
-      x[4 * i + 1] = __uint_as_float(v.x & 0xffff0000u);
-      x[4 * i + 2] = __uint_as_float(v.y << 16);
-      x[4 * i + 3] = __uint_as_float(v.y & 0xffff0000u);
+    for (int i = 0; i < D / 32; ++i) {
+      const uint4 v = ok ? __ldg(p + i) : make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+        x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+      }
     }
   }
 }
@@ -158,34 +163,74 @@ __device__ __forceinline__ void make_q(const QDecodeArgs& a, const float (&x)[D 
   qf.mult[1] = __shfl_sync(0xffffffffu, down, 8 * c4 + 4);
 }
 
-// One slice of 16 keys in registers: the K rows of score rows gid and gid + 8
-// (this lane's D/4 elements of each), the V rows of score rows 2 c4, 2 c4 + 1,
-// 2 c4 + 8, 2 c4 + 9 (elements gid * D/8 .. of each), and their scales.
+// --------------------------------------------------------------------- step --
+// A step's kStepOf<D> slices lie in shared memory, each laid out as a group of
+// the cache. Row r of a slice's score tile is its key row_key(r): within each
+// four rows the second pair is swapped, so that the four V rows that lanes c4
+// = 0 .. 3 load together (rows 2 c4 of the tile) alternate between even and odd
+// keys, which halves their bank conflicts at d = 128 (64-byte rows).
+__device__ __forceinline__ int row_key(int r) { return r ^ ((r >> 1) & 1); }
+// key of a slice that V row i (0 .. 3) of this lane belongs to
+__device__ __forceinline__ int v_key(int i) {
+  return row_key(2 * (threadIdx.x & 3) + (i & 1)) + 8 * (i >> 1);
+}
+
+template <int N>
+__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  static_assert(N == 1 || N == 2 || N == 4, "one vector load");
+  if (N == 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(p);
+    w[0] = v.x;
+    w[N / 4] = v.y;
+    w[N / 2] = v.z;
+    w[N - 1] = v.w;
+  } else if (N == 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(p);
+    w[0] = v.x;
+    w[N - 1] = v.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(p);
+  }
+}
+
+// This lane's places in a group: its D/4 elements of the K row of score row
+// gid (score row gid + 8 lies 8 rows on), its elements gid * D/8 .. of the V
+// rows of score rows 2 c4 and 2 c4 + 1 (and 8 rows on), and their scales.
 template <int D>
-struct QSlice {
-  uint32_t k[2][D / 32];
-  uint32_t ks[2];        // e4m3 bytes: two at d = 128, one at d = 64
-  uint32_t v[4][D / 64];
-  uint32_t vs[4];
+struct LanePlaces {
+  int k, ks, v[2], vs[2];
+  __device__ __forceinline__ LanePlaces() {
+    const int lane = threadIdx.x & 31, gid = lane >> 2, c4 = lane & 3;
+    k = row_key(gid) * (D / 2) + c4 * (D / 8);
+    ks = 8 * D + row_key(gid) * (D / 16) + c4 * (D / 64);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v[i] = 9 * D + v_key(i) * (D / 2) + gid * (D / 16);
+      vs[i] = 17 * D + v_key(i) * (D / 16) + gid * D / 128;
+    }
+  }
 };
 
-// raw[0] = (score row gid, head 2c4), raw[1] = (gid, 2c4+1), raw[2], raw[3]: gid + 8
+// Raw products of one slice: raw[0] = (score row gid, head 2 c4), raw[1] =
+// (gid, 2 c4 + 1), raw[2], raw[3]: score row gid + 8.
 template <int D, int TERMS>
-__device__ __forceinline__ void slice_logits(const QSlice<D>& s, const QFrag<D, TERMS>& qf,
-                                             float (&raw)[4]) {
-  raw[0] = raw[1] = raw[2] = raw[3] = 0.f;
-  uint32_t sc[2][D / 64];
+__device__ __forceinline__ void slice_products(const uint8_t* grp, const LanePlaces<D>& at,
+                                               const QFrag<D, TERMS>& qf, float (&raw)[4]) {
+  uint32_t k[2][D / 32], sc[2][D / 64];
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
-    const uint32_t h = cvt_e4m3x2(s.ks[r]);
+    load_words(grp + at.k + 8 * r * (D / 2), k[r]);
+    const uint8_t* p = grp + at.ks + 8 * r * (D / 16);
+    const uint32_t h = cvt_e4m3x2(D == 128 ? static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p))
+                                           : static_cast<uint32_t>(*p));
     sc[r][0] = __byte_perm(h, h, 0x1010);
     if (D == 128) sc[r][D / 64 - 1] = __byte_perm(h, h, 0x3232);
   }
 #pragma unroll
   for (int w = 0; w < D / 32; ++w) {   // 8 elements of each row: two MMAs
     uint32_t x[4], y[4];
-    cvt_e2m1x8(s.k[0][w], x);
-    cvt_e2m1x8(s.k[1][w], y);
+    cvt_e2m1x8(k[0][w], x);
+    cvt_e2m1x8(k[1][w], y);
     const int blk = D == 128 ? w / 2 : 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -194,52 +239,42 @@ __device__ __forceinline__ void slice_logits(const QSlice<D>& s, const QFrag<D, 
     }
 #pragma unroll
     for (int t = 0; t < TERMS; ++t) {
-      mma_f16_16816(raw, x[0], y[0], x[1], y[1], qf.f[t][2 * w][0], qf.f[t][2 * w][1]);
+      if (w == 0 && t == 0)
+        mma_f16_16816_first(raw, x[0], y[0], x[1], y[1], qf.f[t][2 * w][0], qf.f[t][2 * w][1]);
+      else
+        mma_f16_16816(raw, x[0], y[0], x[1], y[1], qf.f[t][2 * w][0], qf.f[t][2 * w][1]);
       mma_f16_16816(raw, x[2], y[2], x[3], y[3], qf.f[t][2 * w + 1][0], qf.f[t][2 * w + 1][1]);
     }
   }
 }
 
-// Moves the running maxima up to those of NS slices' log2-domain scores x. The
-// maximum changes rarely (one vote finds out), so the common slice rescales
-// nothing.
-template <int D, int NS>
-__device__ __forceinline__ void raise_max(QState<D>& st, const float (&x)[NS][4]) {
-  float mx0 = fmaxf(x[0][0], x[0][2]), mx1 = fmaxf(x[0][1], x[0][3]);
+// Running state of one warp over keys of one (sequence, KV head). Thread
+// (gid = lane/4, c4 = lane%4) owns heads 2 c4, 2 c4 + 1 and output dims
+// gid * D/8 .. + D/8 of both: o[i] = (dim 2i, head 2c4), (2i, 2c4+1),
+// (2i + 1, 2c4), (2i + 1, 2c4 + 1). m: running maxima (log2 units); nmu = 14 - m;
+// l: this lane's sums of 2^14 p. nmu and l hold both heads, packed.
+template <int D>
+struct QState {
+  float m[2];
+  uint64_t nmu, l;
+  float o[D / 16][4];
+  __device__ __forceinline__ void clear() {
+    m[0] = m[1] = kNoKey;
+    nmu = f2_pack(kPShift - kNoKey, kPShift - kNoKey);
+    l = f2_pack(0.f, 0.f);
 #pragma unroll
-  for (int i = 1; i < NS; ++i) {
-    mx0 = fmax3(mx0, x[i][0], x[i][2]);
-    mx1 = fmax3(mx1, x[i][1], x[i][3]);
+    for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
   }
-  if (!__any_sync(0xffffffffu, mx0 > st.m[0] || mx1 > st.m[1])) return;
-#pragma unroll
-  for (int off = 4; off < 32; off <<= 1) {
-    mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
-    mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
-  }
-  const float mn0 = fmaxf(st.m[0], mx0), mn1 = fmaxf(st.m[1], mx1);
-  const float al0 = st.m[0] == kNegInf ? 0.f : fast_exp2(st.m[0] - mn0);
-  const float al1 = st.m[1] == kNegInf ? 0.f : fast_exp2(st.m[1] - mn1);
-  st.m[0] = mn0;
-  st.m[1] = mn1;
-  st.mu[0] = (mn0 == kNegInf ? 0.f : mn0) - kPShift;
-  st.mu[1] = (mn1 == kNegInf ? 0.f : mn1) - kPShift;
-  st.l[0] *= al0;
-  st.l[1] *= al1;
-#pragma unroll
-  for (int i = 0; i < D / 16; ++i) {
-    st.o[i][0] *= al0;
-    st.o[i][1] *= al1;
-    st.o[i][2] *= al0;
-    st.o[i][3] *= al1;
-  }
-}
+};
 
-// O^T += V^T P^T with one slice's weights p. Masked keys' V scales must be zero
-// in `s` (what lies there may be anything).
+// O^T += V^T P^T of one slice with weights p and scales vs of this lane's V rows.
 template <int D, int TERMS>
-__device__ __forceinline__ void slice_pv(float (&o)[D / 16][4], const float (&p)[4],
-                                         const QSlice<D>& s) {
+__device__ __forceinline__ void slice_values(float (&o)[D / 16][4], const float (&p)[4],
+                                             const uint8_t* grp, const LanePlaces<D>& at,
+                                             const uint32_t (&vs)[4]) {
+  uint32_t v[4][D / 64];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) load_words(grp + at.v[i & 1] + (i >> 1) * 8 * (D / 2), v[i]);
   uint32_t b[TERMS][2];
   b[0][0] = movmatrix_t(pack_f16(p[0], p[1]));
   b[0][1] = movmatrix_t(pack_f16(p[2], p[3]));
@@ -247,20 +282,16 @@ __device__ __forceinline__ void slice_pv(float (&o)[D / 16][4], const float (&p)
     b[TERMS - 1][0] = movmatrix_t(pack_f16(p[0] - f16_rounded(p[0]), p[1] - f16_rounded(p[1])));
     b[TERMS - 1][1] = movmatrix_t(pack_f16(p[2] - f16_rounded(p[2]), p[3] - f16_rounded(p[3])));
   }
-  const uint32_t s01 = cvt_e4m3x2(__byte_perm(s.vs[0], s.vs[1], 0x0040));
-  const uint32_t s23 = cvt_e4m3x2(__byte_perm(s.vs[2], s.vs[3], 0x0040));
+  const uint32_t s01 = cvt_e4m3x2(__byte_perm(vs[0], vs[1], 0x0040));
+  const uint32_t s23 = cvt_e4m3x2(__byte_perm(vs[2], vs[3], 0x0040));
 #pragma unroll
   for (int w = 0; w < D / 64; ++w) {
     // codes of one element of two keys side by side: even elements, odd ones
-    const uint32_t e01 = (s.v[0][w] & 0x0f0f0f0fu) | ((s.v[1][w] << 4) & 0xf0f0f0f0u);
-    const uint32_t d01 = ((s.v[0][w] >> 4) & 0x0f0f0f0fu) | (s.v[1][w] & 0xf0f0f0f0u);
-    const uint32_t e23 = (s.v[2][w] & 0x0f0f0f0fu) | ((s.v[3][w] << 4) & 0xf0f0f0f0u);
-    const uint32_t d23 = ((s.v[2][w] >> 4) & 0x0f0f0f0fu) | (s.v[3][w] & 0xf0f0f0f0u);
     uint32_t ea[4], da[4], eb[4], db[4];
-    cvt_e2m1x8(e01, ea);
-    cvt_e2m1x8(d01, da);
-    cvt_e2m1x8(e23, eb);
-    cvt_e2m1x8(d23, db);
+    cvt_e2m1x8(nibbles(v[0][w], v[1][w] << 4), ea);
+    cvt_e2m1x8(nibbles(v[0][w] >> 4, v[1][w]), da);
+    cvt_e2m1x8(nibbles(v[2][w], v[3][w] << 4), eb);
+    cvt_e2m1x8(nibbles(v[2][w] >> 4, v[3][w]), db);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t a0 = hmul2(ea[i], s01), a1 = hmul2(da[i], s01);
@@ -272,26 +303,115 @@ __device__ __forceinline__ void slice_pv(float (&o)[D / 16][4], const float (&p)
   }
 }
 
+// One step: t[i][r] holds the raw products of slice i, score row gid + 8 r, for
+// both heads (masked: -inf), ml the heads' factors to log2 units. The running
+// maximum moves only when a score exceeds it (one vote), so the common step
+// rescales nothing. fix(i, vs) may change the V scales of slice i (a masked
+// key's must become 0: what lies there may be anything) and returns the heads
+// of this lane (bits 0, 1) whose outputs become NaN.
+template <int D, int TERMS, typename Fix>
+__device__ __forceinline__ void attend(QState<D>& st, const uint64_t (&t)[kStepOf<D>][2],
+                                       uint64_t ml, const uint8_t* buf, const LanePlaces<D>& at,
+                                       Fix fix) {
+  constexpr int kStep = kStepOf<D>;
+  uint64_t y[kStep][2];
+  auto exponents = [&]() {   // 14 + score - maximum; their largest over both heads
+    float top = kNegInf;
+#pragma unroll
+    for (int i = 0; i < kStep; ++i)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        // product and sum rounded apart, as the maximum was: a fused one would
+        // leave the product's rounding, large for a huge score
+        y[i][r] = f2_add(f2_mul(t[i][r], ml), st.nmu);
+        float y0, y1;
+        f2_unpack(y[i][r], y0, y1);
+        top = fmax3(top, y0, y1);
+      }
+    return top;
+  };
+  if (__any_sync(0xffffffffu, exponents() > static_cast<float>(kPShift))) {
+    float x0 = kNoKey, x1 = kNoKey;
+#pragma unroll
+    for (int i = 0; i < kStep; ++i) {
+      float a0, a1, b0, b1;
+      f2_unpack(f2_mul(t[i][0], ml), a0, a1);
+      f2_unpack(f2_mul(t[i][1], ml), b0, b1);
+      x0 = fmax3(x0, a0, b0);
+      x1 = fmax3(x1, a1, b1);
+    }
+#pragma unroll
+    for (int off = 4; off < 32; off <<= 1) {
+      x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
+      x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
+    }
+    x0 = fmaxf(x0, st.m[0]);
+    x1 = fmaxf(x1, st.m[1]);
+    const float al0 = ex2(st.m[0] - x0), al1 = ex2(st.m[1] - x1);
+    st.m[0] = x0;
+    st.m[1] = x1;
+    st.nmu = f2_pack(kPShift - x0, kPShift - x1);
+    st.l = f2_mul(st.l, f2_pack(al0, al1));
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      st.o[i][0] *= al0;
+      st.o[i][1] *= al1;
+      st.o[i][2] *= al0;
+      st.o[i][3] *= al1;
+    }
+    exponents();
+  }
+#pragma unroll
+  for (int i = 0; i < kStep; ++i) {
+    const uint8_t* grp = buf + i * qgroup_bytes(D);
+    uint32_t vs[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) vs[j] = grp[at.vs[j & 1] + (j >> 1) * 8 * (D / 16)];
+    const uint32_t nan_heads = fix(i, vs);
+    float p[4];
+    f2_unpack(y[i][0], p[0], p[1]);
+    f2_unpack(y[i][1], p[2], p[3]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) p[j] = ex2(p[j]);
+    st.l = f2_add(st.l, f2_add(f2_pack(p[0], p[1]), f2_pack(p[2], p[3])));
+    slice_values<D, TERMS>(st.o, p, grp, at, vs);
+    if ((nan_heads & 3u) != 0u) {
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if ((nan_heads >> (e & 1)) & 1u) st.o[j][e] = CUDART_NAN_F;
+    }
+  }
+}
+
 // ------------------------------------------------------------------ joining --
 // A piece is one warp's (or CTA's) state over part of a (sequence, KV head):
 // m[G], l[G] (log2-domain maximum; sum of 2^14 p), and at qpart_head(G) o[G][D].
 template <int D>
-__device__ __forceinline__ void piece_store(float* p, QState<D>& st, int G) {
-  const int lane = threadIdx.x & 31, gid = lane >> 2, c4 = lane & 3;
+__device__ __forceinline__ void lane_sums(const QState<D>& st, float (&l)[2]) {
+  f2_unpack(st.l, l[0], l[1]);
 #pragma unroll
   for (int off = 4; off < 32; off <<= 1) {
-    st.l[0] += __shfl_xor_sync(0xffffffffu, st.l[0], off);
-    st.l[1] += __shfl_xor_sync(0xffffffffu, st.l[1], off);
+    l[0] += __shfl_xor_sync(0xffffffffu, l[0], off);
+    l[1] += __shfl_xor_sync(0xffffffffu, l[1], off);
   }
-  const int h = 2 * c4;
+}
+
+template <int D>
+__device__ __forceinline__ void piece_store(float* p, const QState<D>& st, int G) {
+  const int lane = threadIdx.x & 31, gid = lane >> 2, c4 = lane & 3;
+  float l[2];
+  lane_sums(st, l);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    if (h + i >= G) continue;
+    const int h = 2 * c4 + i;
+    if (h >= G) continue;
     if (gid == 0) {
-      p[h + i] = st.m[i];
-      p[G + h + i] = st.l[i];
+      p[h] = st.m[i];
+      p[G + h] = l[i];
     }
-    float* o = p + qpart_head(G) + (h + i) * D + gid * (D / 8);
+    float* o = p + qpart_head(G) + h * D + gid * (D / 8);
 #pragma unroll
     for (int j = 0; j < D / 16; j += 2)
       *reinterpret_cast<float4*>(o + 2 * j) =
@@ -327,8 +447,8 @@ __device__ __forceinline__ void join_into(Joined& x, const Joined (&y)[N]) {
   float M = x.m;
 #pragma unroll
   for (int k = 0; k < N; ++k) M = fmaxf(M, y[k].m);
-  // a part without keys has m = -inf and l = o = 0 (or l NaN, which stays)
-  const float wx = x.m == kNegInf ? 1.f : ex2(x.m - M);
+  // a part without keys has m = kNoKey and l = o = 0 (or l NaN, which stays)
+  const float wx = ex2(x.m - M);
   x.m = M;
   x.l *= wx;
   x.o.x *= wx;
@@ -337,7 +457,7 @@ __device__ __forceinline__ void join_into(Joined& x, const Joined (&y)[N]) {
   x.o.w *= wx;
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    const float w = y[k].m == kNegInf ? 1.f : ex2(y[k].m - M);
+    const float w = ex2(y[k].m - M);
     x.l = fmaf(w, y[k].l, x.l);
     x.o.x = fmaf(w, y[k].o.x, x.o.x);
     x.o.y = fmaf(w, y[k].o.y, x.o.y);
@@ -348,12 +468,12 @@ __device__ __forceinline__ void join_into(Joined& x, const Joined (&y)[N]) {
 template <bool GLOBAL, typename Piece>
 __device__ __forceinline__ Joined join_some(Piece piece, int s0, int s1, int G, int h, int e) {
   constexpr int kBatch = GLOBAL ? 8 : 4;   // loads of L2 lines take longer
-  Joined x = {kNegInf, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  Joined x = {kNoKey, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
   for (int s = s0; s < s1; s += kBatch) {
     Joined y[kBatch];
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      y[k] = {kNegInf, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      y[k] = {kNoKey, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
       if (s + k < s1) {
         const float* p = piece(s + k);
         const float4* o = reinterpret_cast<const float4*>(p + qpart_head(G)) + e;
@@ -416,49 +536,56 @@ __device__ void arrive_and_join(const QDecodeArgs& a, int n_units, const SharedU
     if (!((last >> k) & 1u)) continue;
     const SharedUnit& u = units[k];
     const int n = u.n;
-    const int elems = G * (D / 4);                 // 16 .. 256
-    int shares = static_cast<int>(blockDim.x) / elems;
+    auto mine = [&](int i) -> const float* { return i == 0 ? u.first : u.rest + (i - 1) * u.step; };
+    const int elems = G * (D / 4), threads = static_cast<int>(blockDim.x);   // 16 .. 256
+    int shares = threads / elems;
     if (shares > (n + 3) / 4) shares = (n + 3) / 4;
+    if (shares <= 1) {
+      for (int e = tid; e < elems; e += threads) {
+        const int h = e / (D / 4);
+        joined_output<D, F32>(a, join_some<true>(mine, 0, n, G, h, e), u.b, u.g, h,
+                              e & (D / 4 - 1));
+      }
+      continue;
+    }
     const int e = tid % elems, share = tid / elems, h = e / (D / 4), e4 = e & (D / 4 - 1);
     const int per = (n + shares - 1) / shares;
-    auto mine = [&](int i) -> const float* { return i == 0 ? u.first : u.rest + (i - 1) * u.step; };
-    Joined x = {kNegInf, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    Joined x = {kNoKey, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
     if (share < shares) x = join_some<true>(mine, share * per, min(n, (share + 1) * per), G, h, e);
-    if (shares > 1) {
-      if (share > 0 && share < shares) scratch[tid] = x;
-      __syncthreads();
-      if (share == 0)
-        for (int i = 1; i < shares; ++i) {
-          const Joined y[1] = {scratch[i * elems + e]};
-          join_into(x, y);
-        }
-      __syncthreads();
+    if (share > 0 && share < shares) scratch[tid] = x;
+    __syncthreads();
+    if (share == 0) {
+      for (int i = 1; i < shares; ++i) {
+        const Joined y[1] = {scratch[i * elems + e]};
+        join_into(x, y);
+      }
+      joined_output<D, F32>(a, x, u.b, u.g, h, e4);
     }
-    if (share == 0) joined_output<D, F32>(a, x, u.b, u.g, h, e4);
+    __syncthreads();
   }
 }
 
 // A whole unit held by one warp: straight from its registers to the output.
 template <int D, bool F32>
-__device__ __forceinline__ void warp_output(const QDecodeArgs& a, QState<D>& st, int b, int g) {
+__device__ __forceinline__ void warp_output(const QDecodeArgs& a, const QState<D>& st, int b,
+                                            int g) {
   const int lane = threadIdx.x & 31, gid = lane >> 2, c4 = lane & 3;
+  float l[2];
+  lane_sums(st, l);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-#pragma unroll
-    for (int off = 4; off < 32; off <<= 1) st.l[i] += __shfl_xor_sync(0xffffffffu, st.l[i], off);
     if (2 * c4 + i >= a.G) continue;
     const size_t row = static_cast<size_t>(b) * a.Hq + a.heads[g * a.G + 2 * c4 + i];
-    const float inv = st.l[i] == 0.f ? 0.f : a.v_scale / st.l[i];
+    const float inv = l[i] == 0.f ? 0.f : a.v_scale / l[i];
 #pragma unroll
     for (int j = 0; j < D / 16; j += 2)
       out_store4<F32>(a, row * D + gid * (D / 8) + 2 * j,
                       make_float4(st.o[j][i] * inv, st.o[j][2 + i] * inv, st.o[j + 1][i] * inv,
                                   st.o[j + 1][2 + i] * inv));
-    if (gid == 0) write_row_stat(a, row, st.m[i], st.l[i]);
+    if (gid == 0) write_row_stat(a, row, st.m[i], l[i]);
   }
 }
 
-// ------------------------------------------------------------------- slices --
 // A sequence's cached tokens; one outside what the call and its block table
 // hold is reported and cut to it.
 __device__ __forceinline__ int len_of(const QDecodeArgs& a, int b, bool report) {
@@ -468,71 +595,6 @@ __device__ __forceinline__ int len_of(const QDecodeArgs& a, int b, bool report) 
   if (n >= 0 && n <= cap) return n;
   if (report) report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x521);
   return n < 0 ? 0 : cap;
-}
-
-// The group that holds keys 16 s .. 16 s + 15 of a sequence, for KV head g;
-// null (and reported) if the table's entry is no block of the cache.
-template <int D>
-__device__ __forceinline__ const uint8_t* group_at(const QDecodeArgs& a, const int32_t* table_row,
-                                                   int g, int s) {
-  const int sh = a.bs_shift - 4;
-  const int block = __ldg(table_row + (s >> sh));
-  if (block < 0 || block >= a.num_blocks) {
-    report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x522);
-    return nullptr;
-  }
-  return a.cache + (((static_cast<size_t>(block) * a.Hkv + g) << sh) + (s & ((1 << sh) - 1))) *
-                       qgroup_bytes(D);
-}
-
-// Row r of a slice's score tile is its key row_key(r): within each four rows
-// the second pair is swapped, so that the four V rows that lanes c4 = 0 .. 3
-// load together (rows 2 c4 of the tile) alternate between even and odd keys.
-// In shared memory at d = 128 (64-byte rows) that halves their bank conflicts.
-__device__ __forceinline__ int row_key(int r) { return r ^ ((r >> 1) & 1); }
-// key of a slice that V register i of this lane belongs to
-__device__ __forceinline__ int v_key(int i) {
-  return row_key(2 * (threadIdx.x & 3) + (i & 1)) + 8 * (i >> 1);
-}
-
-// Loads from global memory (through the read-only path) or from shared memory.
-template <bool SHARED, typename T>
-__device__ __forceinline__ T load_as(const uint8_t* p) {
-  const T* q = reinterpret_cast<const T*>(p);
-  return SHARED ? *q : __ldg(q);
-}
-template <bool SHARED, int N>
-__device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
-  static_assert(N == 1 || N == 2 || N == 4, "one vector load");
-  if (N == 4) {
-    const uint4 v = load_as<SHARED, uint4>(p);
-    w[0] = v.x;
-    w[N / 4] = v.y;
-    w[N / 2] = v.z;
-    w[N - 1] = v.w;
-  } else if (N == 2) {
-    const uint2 v = load_as<SHARED, uint2>(p);
-    w[0] = v.x;
-    w[N - 1] = v.y;
-  } else {
-    w[0] = load_as<SHARED, uint32_t>(p);
-  }
-}
-
-// This lane's part of the K row (grp, r) and of the V row (grp, r).
-template <int D, bool SHARED>
-__device__ __forceinline__ void load_k_row(QSlice<D>& s, int i, const uint8_t* grp, int r) {
-  const int c4 = threadIdx.x & 3;
-  load_words<SHARED>(grp + r * (D / 2) + c4 * (D / 8), s.k[i]);
-  const uint8_t* sc = grp + 8 * D + r * (D / 16) + c4 * (D / 64);
-  s.ks[i] = D == 128 ? static_cast<uint32_t>(load_as<SHARED, uint16_t>(sc))
-                     : static_cast<uint32_t>(load_as<SHARED, uint8_t>(sc));
-}
-template <int D, bool SHARED>
-__device__ __forceinline__ void load_v_row(QSlice<D>& s, int i, const uint8_t* grp, int r) {
-  const int gid = (threadIdx.x & 31) >> 2;
-  load_words<SHARED>(grp + 9 * D + r * (D / 2) + gid * (D / 16), s.v[i]);
-  s.vs[i] = load_as<SHARED, uint8_t>(grp + 17 * D + r * (D / 16) + gid * D / 128);
 }
 
 // -------------------------------------------------------------------- dense --
@@ -548,10 +610,9 @@ __device__ __forceinline__ void load_v_row(QSlice<D>& s, int i, const uint8_t* g
 // filled by one bulk copy per block that the step touches (groups of a block
 // are contiguous), which the first lanes issue as soon as the warp has left
 // the stage; no warp waits for another one before the end.
+constexpr int kNW = 8;            // warps per CTA (and at most 8 heads per KV head)
 constexpr int kMinRun = 2;        // steps per warp at least
 constexpr int kDenseStages = 2;
-template <int D>
-constexpr int kStepOf = 256 / D;  // slices per step: 4608 bytes either way
 
 // Where a warp is in the line of steps.
 struct Cursor {
@@ -691,6 +752,7 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   }
 
   // ---- arithmetic
+  const LanePlaces<D> places;
   const int row0 = row_key(gid);   // keys row0 and row0 + 8 of a slice
   int stage = 0;
   uint32_t phase = 0;
@@ -710,12 +772,8 @@ __global__ void __launch_bounds__(kNW * 32, 2)
           sp[i] = a.scores +
                   (static_cast<size_t>(at.b) * a.Hq + a.heads[at.g * a.G + 2 * c4 + i]) * a.N;
     const uint64_t ml = f2_pack(qf.mult[0] * kLog2e, qf.mult[1] * kLog2e);
-    // m: running maxima (log2 units); nmu = 14 - m, +inf before the first key
-    float m0 = kNegInf, m1 = kNegInf;
-    uint64_t nmu = f2_pack(-kNegInf, -kNegInf), l = f2_pack(0.f, 0.f);
-    float o[D / 16][4];
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    QState<D> st;
+    st.clear();
     for (; at.s < at.s1 && alive; ++at.s) {
       if (!mbar_wait_warp(&s_full[warp][stage], phase, a.err, 0x531)) {
         // a wait that gave up (reported): leave no copy in flight, and pass over
@@ -731,38 +789,34 @@ __global__ void __launch_bounds__(kNW * 32, 2)
       const uint8_t* buf = ring + stage * kStageBytes;
       const unsigned int got = (have >> (8 * stage)) & 0xffu;
       if (got != 0u || SCORES) {
-        uint64_t t[kStep][2];   // scores of (row0; row0 + 8) for both heads: raw, then exponents
+        uint64_t t[kStep][2];
 #pragma unroll
         for (int i = 0; i < kStep; ++i) {
-          QSlice<D> sl;
-          load_k_row<D, true>(sl, 0, buf + i * kGroupBytes, row0);
-          load_k_row<D, true>(sl, 1, buf + i * kGroupBytes, row0 + 8);
           float raw[4];
-          slice_logits(sl, qf, raw);
+          slice_products(buf + i * kGroupBytes, places, qf, raw);
           t[i][0] = f2_pack(raw[0], raw[1]);
           t[i][1] = f2_pack(raw[2], raw[3]);
         }
         // keys that do not count: behind the sequence's end, or in a block the
         // table does not name
-        const int key0 = at.s * kKeys + row0;
-        const bool full = got == (1u << ncopy) - 1u && (at.s + 1) * kKeys <= n;
+        const int first = at.s * kKeys;
+        const bool full = got == (1u << ncopy) - 1u && first + kKeys <= n;
         auto counts = [&](int i, int key) {
-          return ((got >> ((16 * i) >> copy_sh)) & 1u) != 0u && key < n;
+          return ((got >> ((16 * i) >> copy_sh)) & 1u) != 0u && first + 16 * i + key < n;
         };
         if (!full) {
 #pragma unroll
           for (int i = 0; i < kStep; ++i)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-              // -inf through any multiplier's sign: the multiplier is positive
-              if (!counts(i, key0 + 16 * i + 8 * r)) t[i][r] = f2_pack(kNegInf, kNegInf);
+              if (!counts(i, row0 + 8 * r)) t[i][r] = f2_pack(kNegInf, kNegInf);
         }
         if (SCORES) {
 #pragma unroll
           for (int i = 0; i < kStep; ++i)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const int key = key0 + 16 * i + 8 * r;
+              const int key = first + row0 + 16 * i + 8 * r;
               float v0, v1;
               f2_unpack(t[i][r], v0, v1);
               if (full || key < n) {
@@ -771,78 +825,15 @@ __global__ void __launch_bounds__(kNW * 32, 2)
               }
             }
         }
-        if (got != 0u) {
-          auto exponents = [&](float& top0, float& top1, uint64_t (&y)[kStep][2]) {
-            top0 = top1 = kNegInf;
-#pragma unroll
-            for (int i = 0; i < kStep; ++i) {
-              float a0, a1, b0, b1;
-              // product and sum rounded apart, as the maximum was: a fused one
-              // would leave the product's rounding, large for a huge score
-              y[i][0] = f2_add(f2_mul(t[i][0], ml), nmu);
-              y[i][1] = f2_add(f2_mul(t[i][1], ml), nmu);
-              f2_unpack(y[i][0], a0, a1);
-              f2_unpack(y[i][1], b0, b1);
-              top0 = fmax3(top0, a0, b0);
-              top1 = fmax3(top1, a1, b1);
-            }
-          };
-          uint64_t y[kStep][2];
-          float top0, top1;
-          exponents(top0, top1, y);
-          if (__any_sync(0xffffffffu, fmaxf(top0, top1) > static_cast<float>(kPShift))) {
-            // a score above the running maximum: raise it and rescale
-            float x0 = kNegInf, x1 = kNegInf, ml0, ml1;
-            f2_unpack(ml, ml0, ml1);
-#pragma unroll
-            for (int i = 0; i < kStep; ++i) {
-              float a0, a1, b0, b1;
-              f2_unpack(t[i][0], a0, a1);
-              f2_unpack(t[i][1], b0, b1);
-              x0 = fmax3(x0, a0 * ml0, b0 * ml0);
-              x1 = fmax3(x1, a1 * ml1, b1 * ml1);
-            }
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) {
-              x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, off));
-              x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, off));
-            }
-            x0 = fmaxf(x0, m0);
-            x1 = fmaxf(x1, m1);
-            const float al0 = m0 == kNegInf ? 0.f : fast_exp2(m0 - x0);
-            const float al1 = m1 == kNegInf ? 0.f : fast_exp2(m1 - x1);
-            m0 = x0;
-            m1 = x1;
-            nmu = f2_pack(kPShift - m0, kPShift - m1);
-            l = f2_mul(l, f2_pack(al0, al1));
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-              o[i][0] *= al0;
-              o[i][1] *= al1;
-              o[i][2] *= al0;
-              o[i][3] *= al1;
-            }
-            exponents(top0, top1, y);
-          }
-#pragma unroll
-          for (int i = 0; i < kStep; ++i) {
-            QSlice<D> sl;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) load_v_row<D, true>(sl, j, buf + i * kGroupBytes, v_key(j));
+        if (got != 0u)
+          attend<D, TERMS>(st, t, ml, buf, places, [&](int i, uint32_t (&vs)[4]) {
             if (!full) {
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                if (!counts(i, at.s * kKeys + 16 * i + v_key(j))) sl.vs[j] = 0u;
+                if (!counts(i, v_key(j))) vs[j] = 0u;
             }
-            float p[4];
-            f2_unpack(y[i][0], p[0], p[1]);
-            f2_unpack(y[i][1], p[2], p[3]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) p[j] = ex2(p[j]);
-            l = f2_add(l, f2_add(f2_pack(p[0], p[1]), f2_pack(p[2], p[3])));
-            slice_pv<D, TERMS>(o, p, sl);
-          }
-        }
+            return 0u;
+          });
       }
       stage ^= 1;
       phase ^= stage == 0 ? 1u : 0u;
@@ -853,14 +844,6 @@ __global__ void __launch_bounds__(kNW * 32, 2)
       if (more) issue();
     }
     f += at.s1 - at.s0;
-    QState<D> st;
-    st.m[0] = m0;
-    st.m[1] = m1;
-    f2_unpack(l, st.l[0], st.l[1]);
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) st.o[i][j] = o[i][j];
     if (at.s0 == 0 && at.s1 == at.ns) {
       warp_output<D, F32>(a, st, at.b, at.g);
     } else {
@@ -933,7 +916,7 @@ __global__ void __launch_bounds__(kNW * 32, 2)
     for (int e = 4 * tid; e < a.Hq * D; e += 4 * kNW * 32)
       out_store4<F32>(a, base + e, make_float4(0.f, 0.f, 0.f, 0.f));
     for (int h = tid; h < a.Hq; h += kNW * 32)
-      write_row_stat(a, static_cast<size_t>(b) * a.Hq + h, kNegInf, 0.f);
+      write_row_stat(a, static_cast<size_t>(b) * a.Hq + h, kNoKey, 0.f);
   }
   if (SCORES && a.fill_tail)
     for (int r = blockIdx.x; r < a.B * a.Hq; r += gridDim.x)
@@ -952,24 +935,37 @@ __global__ void __launch_bounds__(256) k_qfill_tail(float* __restrict__ rows,
 }
 
 // -------------------------------------------------------------------- reuse --
-// One (sequence, KV head) per blockIdx.y; its 16-entry slices, numbered across
-// the chunks of its union plan (per query head sets: key | head mask << 24,
-// ascending) or across its set (pooled), are split into S equal runs, one per
-// CTA, and a run's slices go to the CTA's warps in turn. Rows are gathered
-// through the block table straight into the MMA fragments: a K row is read by
-// four lanes, a V row by eight, whole 32-byte sectors either way.
+// One (sequence, KV head) per blockIdx.y. Its gather list (per query head sets:
+// the union plan's entries key | head mask << 24, in 16-entry slices per plan
+// chunk; pooled: the set itself) is numbered in steps of kStepOf<D> slices, and
+// the steps are split into S equal runs, one per CTA, whose steps go to the
+// CTA's warps in turn. A warp gathers each step's rows through the block table
+// into the group layout of one of its two stages (16-byte cp.async for codes,
+// one 8- or 4-byte one per row for scales; rows of no use are zero-filled, not
+// read), so that the arithmetic is the dense kernel's. Entries are loaded two
+// steps before their copies and block ids one step before, so that no copy
+// waits for either.
+constexpr int kReuseNW = 4, kReuseStages = 2, kReuseCtasPerSm = 4;
+// A row in one word: the group's number in the cache and the row in it.
+constexpr uint32_t kNoRow = 0xffffffffu;
+
 template <int D, int TERMS, bool POOLED>
-__global__ void __launch_bounds__(kNW * 32, 2)
+__global__ void __launch_bounds__(kReuseNW * 32, kReuseCtasPerSm)
     k_qdecode_reuse(const __grid_constant__ QDecodeArgs a) {
   pdl_wait();
   pdl_trigger();
   constexpr bool F32 = TERMS == 2;
+  constexpr int kStep = kStepOf<D>, kRows = 16 * kStep, kPer = kRows / 32;   // rows per lane
+  constexpr int kGroupBytes = qgroup_bytes(D), kStageBytes = kStep * kGroupBytes;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int s_pref[kMaxSplits + 1], s_cnt[kMaxSplits];
+  __shared__ unsigned char s_mask[kReuseNW][kReuseStages][kRows];   // heads per gathered row
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, c4 = lane & 3;
   const int pf = static_cast<int>(qpart_floats(a.G, D));
-  float* slots = reinterpret_cast<float*>(smem);   // [kNW][pf]
+  uint8_t* ring = smem + warp * kReuseStages * kStageBytes;   // at the end: the warp's piece
   const int unit = blockIdx.y, b = unit / a.Hkv, g = unit % a.Hkv;
+  float qx[D / 4];
+  load_q<D, TERMS>(a, b, g, qx);
   const int n = len_of(a, b, blockIdx.x == 0 && g == 0);
   const int nch = POOLED ? 0 : a.plan_chunks;
   if (!POOLED && warp == 0) {
@@ -992,140 +988,185 @@ __global__ void __launch_bounds__(kNW * 32, 2)
     }
     if (lane == 0) s_pref[nch] = carry;
   }
-  __syncthreads();
-  const int total = POOLED ? (a.topk + 15) / 16 : s_pref[nch];
+  if (!POOLED) __syncthreads();
+  const int slices = POOLED ? (a.topk + 15) / 16 : s_pref[nch];
+  const int total = (slices + kStep - 1) / kStep;
   const int per = (total + a.S - 1) / a.S;
   const int g0 = min(total, static_cast<int>(blockIdx.x) * per), g1 = min(total, g0 + per);
   const int32_t* set = POOLED ? a.idx + static_cast<size_t>(unit) * a.topk : nullptr;
   const int32_t* trow = a.table + static_cast<size_t>(b) * a.max_blocks;
-  const uint32_t every = (1u << a.G) - 1u;
+  const int sh = a.bs_shift - 4, gmask = (1 << sh) - 1;
 
-  QState<D> st;
-  qstate_init(st);
-  QFrag<D, TERMS> qf;
-  {
-    float x[D / 4];
-    load_q<D, TERMS>(a, b, g, x);
-    make_q(a, x, qf);
-  }
-  int fc = 0;
-  for (int sl = g0 + warp; sl < g1; sl += kNW) {
-    // entry i of the slice in lanes i and i + 16: its key's group and row, and
-    // the heads that attend to it (none: padding, not read)
-    uint32_t mask = 0u;
-    int key = 0;
-    if (POOLED) {
-      const int e = sl * 16 + (lane & 15);
-      if (e < a.topk) {
-        key = __ldg(set + e);
-        const int before = e > 0 ? __ldg(set + e - 1) : -1;
-        if (key >= n || (key >= 0 && (key <= before || (before < 0 && e > 0)))) {
+  // ---- gather: row j of lane l is row l + 32 j of a step
+  int fc[kPer] = {};        // plan chunk cursors: rows only move forward
+  int2 raw[kPer];           // entries of the step after the next to be copied (pooled: and
+                            // the entry before each)
+  int key[kPer], blk[kPer]; // rows of the next step to be copied
+  uint32_t mask[kPer];
+  auto fetch = [&](int step) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      raw[j] = POOLED ? make_int2(-1, -1) : make_int2(0, 0);
+      if (step >= g1) continue;
+      const int row = lane + 32 * j;
+      if (POOLED) {
+        const int e = step * kRows + row;
+        if (e < a.topk) raw[j] = make_int2(__ldg(set + e), e > 0 ? __ldg(set + e - 1) : -2);
+      } else {
+        const int sl = step * kStep + (row >> 4);
+        if (sl >= slices) continue;
+        while (fc[j] + 1 < nch && s_pref[fc[j] + 1] <= sl) ++fc[j];
+        const int e = (sl - s_pref[fc[j]]) * 16 + (row & 15);
+        if (e < s_cnt[fc[j]])
+          raw[j].x = static_cast<int>(
+              __ldg(a.plan + (static_cast<size_t>(unit) * nch + fc[j]) * kPlanCapEntries + e));
+      }
+    }
+  };
+  auto resolve = [&]() {    // the fetched entries become rows; their block ids are requested
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      mask[j] = 0u;
+      key[j] = blk[j] = 0;
+      if (POOLED) {
+        const int k = raw[j].x, before = raw[j].y;   // -2 before the first entry
+        const bool ok = k >= 0 && k < n && k > before && before != -1;
+        if (ok) {
+          key[j] = k;
+          mask[j] = (1u << a.G) - 1u;
+        } else if (k != -1) {
           report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x523);
-        } else if (key >= 0) {
-          mask = every;
-        } else if (key != -1) {
-          report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x524);
+        }
+      } else {
+        const int k = raw[j].x & 0xffffff;
+        if (k < n) {
+          key[j] = k;
+          mask[j] = static_cast<uint32_t>(raw[j].x) >> 24;
         }
       }
-    } else {
-      while (fc + 1 < nch && s_pref[fc + 1] <= sl) ++fc;
-      const int e = (sl - s_pref[fc]) * 16 + (lane & 15);
-      if (e < s_cnt[fc]) {
-        const uint32_t ent =
-            __ldg(a.plan + (static_cast<size_t>(unit) * nch + fc) * kPlanCapEntries + e);
-        key = static_cast<int>(ent & 0xffffffu);
-        mask = key < n ? ent >> 24 : 0u;
-      }
+      if (mask[j] != 0u) blk[j] = __ldg(trow + (key[j] >> a.bs_shift));
     }
-    const uint8_t* grp = nullptr;
-    if (mask != 0u) grp = group_at<D>(a, trow, g, key >> 4);
-    if (grp == nullptr) mask = 0u;
-    const unsigned long long base = reinterpret_cast<unsigned long long>(grp);
-    QSlice<D> s;
-    float x[1][4];
-    uint32_t mk[2];
+  };
+  auto copy = [&](int stage) {
+    uint8_t* dst = ring + stage * kStageBytes;
+    uint32_t place[kPer];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int src = row_key(gid) + 8 * i;
-      const uint8_t* p =
-          reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, base, src));
-      const int r = __shfl_sync(0xffffffffu, key, src) & 15;
-      mk[i] = __shfl_sync(0xffffffffu, mask, src);
-      if (mk[i] != 0u) {
-        load_k_row<D, false>(s, i, p, r);
-      } else {
-#pragma unroll
-        for (int w = 0; w < D / 32; ++w) s.k[i][w] = 0u;
-        s.ks[i] = 0u;
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int src = v_key(i);
-      const uint8_t* p =
-          reinterpret_cast<const uint8_t*>(__shfl_sync(0xffffffffu, base, src));
-      const int r = __shfl_sync(0xffffffffu, key, src) & 15;
-      if (p != nullptr) {
-        load_v_row<D, false>(s, i, p, r);
-      } else {
-#pragma unroll
-        for (int w = 0; w < D / 64; ++w) s.v[i][w] = 0u;
-        s.vs[i] = 0u;
-      }
-    }
-    slice_logits(s, qf, x[0]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const bool in = (mk[i >> 1] >> (2 * c4 + (i & 1))) & 1u;
-      x[0][i] = in ? x[0][i] * (qf.mult[i & 1] * kLog2e) : kNegInf;
-    }
-    // A V block that holds a NaN (scale 0x7f or 0xff) would reach every head of
-    // the group through 0 * NaN in the product: it is taken out of the slice,
-    // and only the heads whose set holds the key get the NaN.
-    uint32_t nan_heads = 0u;
-    if (!POOLED) {
-      const uint32_t vs4 = s.vs[0] | (s.vs[1] << 8) | (s.vs[2] << 16) | (s.vs[3] << 24);
-      const uint32_t bad = __vcmpeq4(vs4 & 0x7f7f7f7fu, 0x7f7f7f7fu);
-      if (__any_sync(0xffffffffu, bad != 0u)) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t km = __shfl_sync(0xffffffffu, mask, v_key(i));
-          if ((bad >> (8 * i)) & 1u) {
-            s.vs[i] = 0u;
-            nan_heads |= km;
-          }
+    for (int j = 0; j < kPer; ++j) {
+      place[j] = kNoRow;
+      if (mask[j] != 0u) {
+        if (static_cast<unsigned int>(blk[j]) < static_cast<unsigned int>(a.num_blocks)) {
+          const uint32_t grp = ((static_cast<uint32_t>(blk[j]) * a.Hkv + g) << sh) |
+                               ((key[j] >> 4) & gmask);
+          place[j] = (grp << 4) | (key[j] & 15);
+        } else {
+          report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x522);
         }
-        // the four lanes that share these dims hold other keys and other heads
-        nan_heads |= __shfl_xor_sync(0xffffffffu, nan_heads, 1);
-        nan_heads |= __shfl_xor_sync(0xffffffffu, nan_heads, 2);
-        nan_heads >>= 2 * c4;
       }
+      const bool ok = place[j] != kNoRow;
+      const int row = lane + 32 * j;
+      s_mask[warp][stage][row] = static_cast<unsigned char>(ok ? mask[j] : 0u);
+      // this lane's own rows' scales
+      const uint8_t* src = a.cache + static_cast<size_t>(ok ? place[j] >> 4 : 0u) * kGroupBytes +
+                           8 * D + (ok ? place[j] & 15u : 0u) * (D / 16);
+      uint8_t* to = dst + (row >> 4) * kGroupBytes + 8 * D + (row & 15) * (D / 16);
+      cp_async_small<D / 16>(to, src, ok);
+      cp_async_small<D / 16>(to + 9 * D, src + 9 * D, ok);
     }
-    raise_max<D, 1>(st, x);
-    float p[4];
+    constexpr int kChunks = D / 32;               // 16-byte pieces of a row's codes
+    constexpr int kTurns = kRows * kChunks / 32;
+    const int ch = lane % kChunks;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      p[i] = ex2(x[0][i] - st.mu[i & 1]);
-      st.l[i & 1] += p[i];
+    for (int i = 0; i < kTurns; ++i) {
+      const int row = lane / kChunks + i * (32 / kChunks);
+      const uint32_t pl = __shfl_sync(0xffffffffu, place[(i * (32 / kChunks)) / 32], row & 31);
+      const bool ok = pl != kNoRow;
+      const uint8_t* src = a.cache + static_cast<size_t>(ok ? pl >> 4 : 0u) * kGroupBytes +
+                           (ok ? pl & 15u : 0u) * (D / 2) + ch * 16;
+      uint8_t* to = dst + (row >> 4) * kGroupBytes + (row & 15) * (D / 2) + ch * 16;
+      cp_async16(to, src, ok ? 16u : 0u);
+      cp_async16(to + 9 * D, src + 9 * D, ok ? 16u : 0u);
     }
-    slice_pv<D, TERMS>(st.o, p, s);
-    if (!POOLED && (nan_heads & 3u) != 0u) {
+  };
+  int next = g0 + warp;           // step that is copied next
+  fetch(next);
+  resolve();
+  fetch(next + kReuseNW);
 #pragma unroll
-      for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if ((nan_heads >> (i & 1)) & 1u) st.o[j][i] = CUDART_NAN_F;
-    }
+  for (int i = 0; i < kReuseStages; ++i) {
+    if (next < g1) copy(i);
+    cp_async_commit();
+    next += kReuseNW;
+    resolve();
+    fetch(next + kReuseNW);
   }
-  piece_store<D>(slots + warp * pf, st, a.G);
+
+  // ---- arithmetic
+  QFrag<D, TERMS> qf;
+  make_q(a, qx, qf);
+  const uint64_t ml = f2_pack(qf.mult[0] * kLog2e, qf.mult[1] * kLog2e);
+  const LanePlaces<D> places;
+  const int row0 = row_key(gid);
+  QState<D> st;
+  st.clear();
+  int stage = 0;
+  for (int s = g0 + warp; s < g1; s += kReuseNW) {
+    cp_async_wait<kReuseStages - 1>();
+    __syncwarp();
+    const uint8_t* buf = ring + stage * kStageBytes;
+    const unsigned char* masks = s_mask[warp][stage];
+    uint64_t t[kStep][2];
+#pragma unroll
+    for (int i = 0; i < kStep; ++i) {
+      float r[4];
+      slice_products(buf + i * kGroupBytes, places, qf, r);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t m = masks[16 * i + row0 + 8 * e] >> (2 * c4);
+        t[i][e] = f2_pack((m & 1u) ? r[2 * e] : kNegInf, (m & 2u) ? r[2 * e + 1] : kNegInf);
+      }
+    }
+    attend<D, TERMS>(st, t, ml, buf, places, [&](int i, uint32_t (&vs)[4]) -> uint32_t {
+      if (POOLED) return 0u;
+      // A V block that holds a NaN (scale 0x7f or 0xff) would reach every head of
+      // the group through 0 * NaN in the product: it is taken out of the
+      // slice, and only the heads whose set holds the key get the NaN.
+      const uint32_t vs4 = __byte_perm(__byte_perm(vs[0], vs[1], 0x0040),
+                                       __byte_perm(vs[2], vs[3], 0x0040), 0x5410);
+      const uint32_t bad = __vcmpeq4(vs4 & 0x7f7f7f7fu, 0x7f7f7f7fu);
+      if (!__any_sync(0xffffffffu, bad != 0u)) return 0u;
+      uint32_t heads = 0u;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if ((bad >> (8 * j)) & 1u) {
+          vs[j] = 0u;
+          heads |= masks[16 * i + v_key(j)];
+        }
+      // the four lanes that share these dims hold other keys and other heads
+      heads |= __shfl_xor_sync(0xffffffffu, heads, 1);
+      heads |= __shfl_xor_sync(0xffffffffu, heads, 2);
+      return heads >> (2 * c4);
+    });
+    __syncwarp();   // the stage is free
+    if (next < g1) copy(stage);
+    cp_async_commit();
+    next += kReuseNW;
+    resolve();
+    fetch(next + kReuseNW);
+    stage ^= 1;
+  }
+  static_assert(kReuseStages == 2, "stages alternate");
+  cp_async_wait<0>();
+  __syncwarp();
+  auto slot = [&](int w) { return reinterpret_cast<float*>(smem + w * kReuseStages * kStageBytes); };
+  piece_store<D>(slot(warp), st, a.G);
   __syncthreads();
   float* part = a.part + static_cast<size_t>(unit) * a.S * pf;
   float* dst = part + static_cast<size_t>(blockIdx.x) * pf;
   const int elems = a.G * (D / 4);
-  for (int e = tid; e < elems; e += kNW * 32) {
+  for (int e = tid; e < elems; e += kReuseNW * 32) {
     const int h = e / (D / 4), e4 = e & (D / 4 - 1);
-    const Joined x = join_some<false>([&](int w) -> const float* { return slots + w * pf; }, 0,
-                                      kNW, a.G, h, e);
+    const Joined x = join_some<false>([&](int w) -> const float* { return slot(w); }, 0, kReuseNW,
+                                      a.G, h, e);
     if (a.S == 1) {
       joined_output<D, F32>(a, x, b, g, h, e4);
     } else {
@@ -1138,7 +1179,7 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   }
   if (a.S == 1) return;
   const SharedUnit units[2] = {{unit, b, g, a.S, part, part + pf, static_cast<size_t>(pf)}, {}};
-  arrive_and_join<D, F32>(a, 1, units, reinterpret_cast<Joined*>(slots));
+  arrive_and_join<D, F32>(a, 1, units, reinterpret_cast<Joined*>(smem));
 }
 
 // CTAs of a kernel that the current device holds at once (asked once per host
@@ -1146,7 +1187,7 @@ __global__ void __launch_bounds__(kNW * 32, 2)
 // memory there is: the same value whatever the call, so that threads calling
 // with different sizes do not undo one another's setting.
 template <void (*kern)(const QDecodeArgs)>   // by value: each kernel has its own record
-cudaError_t resident_ctas(size_t smem, int& ctas) {
+cudaError_t resident_ctas(size_t smem, int threads, int& ctas) {
   thread_local int dev_of = -1, slots = 0;
   thread_local size_t smem_of = 0;
   int dev = 0;
@@ -1166,7 +1207,7 @@ cudaError_t resident_ctas(size_t smem, int& ctas) {
       return e;
     if ((e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess)
       return e;
-    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kNW * 32, smem)) !=
+    if ((e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem)) !=
         cudaSuccess)
       return e;
     slots = sms * per_sm;
@@ -1188,7 +1229,7 @@ cudaError_t launch_dense_t(const QDecodeArgs& a, cudaStream_t st) {
                       qalign16((static_cast<size_t>(a.B) + 1) * sizeof(int));
   constexpr auto kern = k_qdecode_dense<D, TERMS, SCORES>;
   int ctas = 0;
-  const cudaError_t e = resident_ctas<kern>(smem, ctas);
+  const cudaError_t e = resident_ctas<kern>(smem, kNW * 32, ctas);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(ctas), dim3(kNW * 32), smem, st, a);
 }
@@ -1201,22 +1242,24 @@ cudaError_t launch_dense_s(const QDecodeArgs& a, cudaStream_t st) {
 
 template <int D, int TERMS, bool POOLED>
 cudaError_t launch_reuse_t(const QDecodeArgs& a, cudaStream_t st) {
-  size_t smem = kNW * qpart_floats(a.G, D) * sizeof(float);
-  if (smem < kNW * 32 * sizeof(Joined)) smem = kNW * 32 * sizeof(Joined);
+  constexpr size_t kRing = kReuseStages * kStepOf<D> * qgroup_bytes(D), smem = kReuseNW * kRing;
+  static_assert(smem >= kReuseNW * 32 * sizeof(Joined), "scratch of the join between CTAs");
+  static_assert(kRing >= qpart_floats(8, D) * sizeof(float), "a warp's piece in its ring");
   constexpr auto kern = k_qdecode_reuse<D, TERMS, POOLED>;
   int ctas = 0;
-  const cudaError_t e = resident_ctas<kern>(smem, ctas);
+  const cudaError_t e = resident_ctas<kern>(smem, kReuseNW * 32, ctas);
   if (e != cudaSuccess) return e;
   QDecodeArgs u = a;
   const int units = a.B * a.Hkv;
-  // at least one slice per warp where the sets are long enough
-  const int most = POOLED ? (a.topk + 16 * kNW - 1) / (16 * kNW)
-                          : (a.G * a.topk + 16 * kNW - 1) / (16 * kNW);
+  // as many CTAs per unit as fill one wave, and at least one step per warp
+  // where the sets are long enough
+  const int rows = (POOLED ? 1 : a.G) * a.topk, cta_rows = 16 * kStepOf<D> * kReuseNW;
+  const int most = (rows + cta_rows - 1) / cta_rows;
   int s = ctas / units;
   if (s > most) s = most;
   if (s > kMaxSplits) s = kMaxSplits;   // the last CTA joins that many pieces
   u.S = s < 1 ? 1 : s;
-  return launch_pdl(kern, dim3(u.S, units), dim3(kNW * 32), smem, st, u);
+  return launch_pdl(kern, dim3(u.S, units), dim3(kReuseNW * 32), smem, st, u);
 }
 
 }  // namespace
