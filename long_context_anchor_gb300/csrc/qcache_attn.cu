@@ -104,41 +104,37 @@ struct QFrag {
 
 // Head gid's dims c4 * D/4 .. + D/4 as they are in memory (zeros for no head).
 template <int D, int TERMS>
-__device__ __forceinline__ void load_q(const QDecodeArgs& a, int b, int g, float (&x)[D / 4]) {
+struct QRaw {
+  uint4 v[TERMS * D / 32];
+};
+template <int D, int TERMS>
+__device__ __forceinline__ void load_q(const QDecodeArgs& a, int b, int g, QRaw<D, TERMS>& x) {
   const int lane = threadIdx.x & 31, gid = lane >> 2, c4 = lane & 3;
   const bool ok = gid < a.G;
   const size_t row = ok ? static_cast<size_t>(b) * a.Hq + a.heads[g * a.G + gid] : 0;
-  if (TERMS == 2) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + row * D +
-                                                      c4 * (D / 4));
+  const uint4* p = static_cast<const uint4*>(a.q) + (row * D + c4 * (D / 4)) * TERMS / 8;
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      const float4 v = ok ? __ldg(p + i) : make_float4(0.f, 0.f, 0.f, 0.f);
-      x[4 * i] = v.x;
-      x[4 * i + 1] = v.y;
-      x[4 * i + 2] = v.z;
-      x[4 * i + 3] = v.w;
-    }
-  } else {
-    const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                    row * D + c4 * (D / 4));
+  for (int i = 0; i < TERMS * D / 32; ++i) x.v[i] = ok ? __ldg(p + i) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+template <int D, int TERMS>
+__device__ __forceinline__ void make_q(const QDecodeArgs& a, const QRaw<D, TERMS>& raw,
+                                       QFrag<D, TERMS>& qf) {
+  const int c4 = threadIdx.x & 3;
+  float x[D / 4];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      const uint4 v = ok ? __ldg(p + i) : make_uint4(0u, 0u, 0u, 0u);
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  for (int i = 0; i < TERMS * D / 32; ++i) {
+    const uint32_t w[4] = {raw.v[i].x, raw.v[i].y, raw.v[i].z, raw.v[i].w};
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 4; ++j) {
+      if (TERMS == 2) {
+        x[4 * i + j] = __uint_as_float(w[j]);
+      } else {   // two bf16
         x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
         x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
       }
     }
   }
-}
-
-template <int D, int TERMS>
-__device__ __forceinline__ void make_q(const QDecodeArgs& a, const float (&x)[D / 4],
-                                       QFrag<D, TERMS>& qf) {
-  const int c4 = threadIdx.x & 3;
   float amax = 0.f;
 #pragma unroll
   for (int i = 0; i < D / 4; ++i) amax = fmaxf(amax, fabsf(x[i]));
@@ -614,29 +610,26 @@ constexpr int kNW = 8;            // warps per CTA (and at most 8 heads per KV h
 constexpr int kMinRun = 2;        // steps per warp at least
 constexpr int kDenseStages = 2;
 
-// Where a warp is in the line of steps.
-struct Cursor {
-  int f;           // its run's first step of this unit
-  int b, g, n;     // unit, cached tokens
-  int ns;          // steps of the unit
-  int s0, s, s1;   // this run's part of them: [s0, s1), next one s
+// The unit that holds step f of the line.
+struct Place {
+  int b, g, n;     // sequence, KV head, cached tokens
+  int ns, s;       // the unit's steps, and f's number among them
 };
-__device__ __forceinline__ void cursor_enter(Cursor& c, const QDecodeArgs& a, const int* pref,
-                                             int f, int end) {
+__device__ __forceinline__ Place place_of(const QDecodeArgs& a, const int* pref, int f) {
   int lo = 0, hi = a.B;   // the sequence: pref[lo] * Hkv <= f < pref[lo + 1] * Hkv
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (pref[mid] * a.Hkv <= f) lo = mid;
     else hi = mid;
   }
-  c.f = f;
-  c.b = lo;
-  c.n = len_of(a, lo, false);
-  c.ns = pref[lo + 1] - pref[lo];
+  Place p;
+  p.b = lo;
+  p.n = len_of(a, lo, false);
+  p.ns = pref[lo + 1] - pref[lo];
   const int in = f - pref[lo] * a.Hkv;
-  c.g = in / c.ns;
-  c.s0 = c.s = in - c.g * c.ns;
-  c.s1 = min(c.ns, c.s0 + end - f);
+  p.g = in / p.ns;
+  p.s = in - p.g * p.ns;
+  return p;
 }
 
 template <int D, int TERMS, bool SCORES>
@@ -695,60 +688,69 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   const int w0 = min(total, (static_cast<int>(blockIdx.x) * kNW + warp) * per);
   const int w1 = min(total, w0 + per);
 
-  // ---- copies: `in` runs ahead of the arithmetic by kDenseStages steps. Lane i
-  // < ncopy issues the step's i-th copy of copy_slices slices; its block id is
-  // loaded when `in` gets to the step, one step before it is used.
+  // ---- copies, kDenseStages steps ahead of the arithmetic. Lane i < ncopy
+  // issues the step's i-th copy; its block id is loaded when the step before
+  // is issued.
   const int copy_sh = min(a.bs_shift, D == 128 ? 5 : 6);   // log2 of a copy's keys
   const int ncopy = kKeys >> copy_sh;
   const uint32_t copy_bytes = static_cast<uint32_t>(kGroupBytes) << (copy_sh - 4);
-  const int gmask = (1 << (a.bs_shift - 4)) - 1;
-  Cursor in = {}, at = {};
-  int id = -1;
-  bool more = w0 < w1;            // `in` stands at a step of this run
+  const uint32_t gmask = (1u << (a.bs_shift - 4)) - 1u;
+  const uint32_t head_bytes = static_cast<uint32_t>(kGroupBytes) << (a.bs_shift - 4);
+  const uint32_t block_bytes = head_bytes * static_cast<uint32_t>(a.Hkv);
+  int in_f = w0;                  // line step that is issued next
+  int in_left = 0;                // steps of the run in its unit from there on
+  int in_key = 0, in_n = 0;       // this lane's copy: first key, tokens of the sequence
+  const int32_t* in_row = a.table;     // the sequence's row of the block table
+  const uint8_t* in_base = a.cache;    // the KV head's place in block 0
+  int id = 0;                     // this lane's block
   int in_stage = 0;
   unsigned int have = 0u;         // byte i: the copies that stage i got
   int pending = 0;                // steps issued and not taken
   bool alive = true;
-  auto fetch_id = [&]() {
-    const int key = in.s * kKeys + (lane << copy_sh);
-    id = 0;                       // nothing to copy: neither read nor reported
-    if (lane < ncopy && key < in.n)
-      id = __ldg(a.table + static_cast<size_t>(in.b) * a.max_blocks + (key >> a.bs_shift));
+  auto enter = [&](const Place& p) {
+    in_left = min(p.ns - p.s, w1 - in_f);
+    in_key = lane < ncopy ? p.s * kKeys + (lane << copy_sh) : p.n;   // other lanes copy nothing
+    in_n = p.n;
+    in_row = a.table + static_cast<size_t>(p.b) * a.max_blocks;
+    in_base = a.cache + static_cast<size_t>(p.g) * head_bytes;
   };
-  auto issue = [&]() {            // all lanes, `more` holds
-    const int key = in.s * kKeys + (lane << copy_sh);
-    const bool want = lane < ncopy && key < in.n;
-    const bool ok = want && static_cast<unsigned int>(id) < static_cast<unsigned int>(a.num_blocks);
-    if (want && !ok) report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x522);
+  auto fetch_id = [&]() {
+    id = 0;
+    if (in_key < in_n) id = __ldg(in_row + (in_key >> a.bs_shift));
+  };
+  auto issue = [&]() {            // all lanes; in_f < w1 holds
+    const bool want = in_key < in_n;
+    const bool ok = want && static_cast<uint32_t>(id) < static_cast<uint32_t>(a.num_blocks);
     const unsigned int got = __ballot_sync(0xffffffffu, ok);
     uint64_t* bar = &s_full[warp][in_stage];
     if (lane == 0) mbar_arrive_expect_tx(bar, __popc(got) * copy_bytes);
     __syncwarp();
-    if (ok) {
-      const size_t grp = ((static_cast<size_t>(id) * a.Hkv + in.g) << (a.bs_shift - 4)) +
-                         ((key >> 4) & gmask);
-      bulk_load(ring + in_stage * kStageBytes + lane * copy_bytes, a.cache + grp * kGroupBytes,
+    if (ok)
+      bulk_load(ring + in_stage * kStageBytes + lane * copy_bytes,
+                in_base + static_cast<uint64_t>(static_cast<uint32_t>(id)) * block_bytes +
+                    ((static_cast<uint32_t>(in_key) >> 4) & gmask) * kGroupBytes,
                 copy_bytes, bar);
-    }
-    have = (have & ~(0xffu << (8 * in_stage))) | (got << (8 * in_stage));
+    else if (want)
+      report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x522);
+    have = __byte_perm(have, got, in_stage == 0 ? 0x3214 : 0x3240);
     in_stage ^= 1;
     ++pending;
-    if (++in.s == in.s1) {
-      const int next = in.f + in.s1 - in.s0;
-      more = next < w1;
-      if (more) cursor_enter(in, a, pref, next, w1);
-    }
-    if (more) fetch_id();
+    ++in_f;
+    in_key += kKeys;
+    if (lane >= ncopy) in_key = in_n;
+    if (--in_left == 0 && in_f < w1) enter(place_of(a, pref, in_f));
+    if (in_f < w1) fetch_id();
   };
   static_assert(kDenseStages == 2, "stages alternate");
-  float qx[D / 4];   // the query of the unit that comes next
-  if (more) {
-    cursor_enter(in, a, pref, w0, w1);
+  Place at = {};
+  QRaw<D, TERMS> qx;   // the query of the unit that comes next
+  if (w0 < w1) {
+    at = place_of(a, pref, w0);
+    enter(at);
     fetch_id();
-    at = in;
     load_q<D, TERMS>(a, at.b, at.g, qx);
     issue();
-    if (more) issue();
+    if (in_f < w1) issue();
   }
 
   // ---- arithmetic
@@ -758,10 +760,11 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   uint32_t phase = 0;
   for (int f = w0; f < w1;) {
     if (f != w0) {
-      cursor_enter(at, a, pref, f, w1);
+      at = place_of(a, pref, f);
       load_q<D, TERMS>(a, at.b, at.g, qx);
     }
-    const int n = at.n;
+    const int n = at.n, steps = min(at.ns - at.s, w1 - f);
+    int first = at.s * kKeys;   // first key of the step
     QFrag<D, TERMS> qf;
     make_q(a, qx, qf);
     float* sp[2] = {nullptr, nullptr};
@@ -774,8 +777,9 @@ __global__ void __launch_bounds__(kNW * 32, 2)
     const uint64_t ml = f2_pack(qf.mult[0] * kLog2e, qf.mult[1] * kLog2e);
     QState<D> st;
     st.clear();
-    for (; at.s < at.s1 && alive; ++at.s) {
-      if (!mbar_wait_warp(&s_full[warp][stage], phase, a.err, 0x531)) {
+    for (int left = steps; left > 0 && alive; --left, first += kKeys) {
+      if (!__all_sync(0xffffffffu, mbar_try_wait(&s_full[warp][stage], phase)) &&
+          !mbar_wait_warp(&s_full[warp][stage], phase, a.err, 0x531)) {
         // a wait that gave up (reported): leave no copy in flight, and pass over
         // the rest of the run so that every unit still gets its arrivals
         for (; pending > 0; --pending) {
@@ -799,7 +803,6 @@ __global__ void __launch_bounds__(kNW * 32, 2)
         }
         // keys that do not count: behind the sequence's end, or in a block the
         // table does not name
-        const int first = at.s * kKeys;
         const bool full = got == (1u << ncopy) - 1u && first + kKeys <= n;
         auto counts = [&](int i, int key) {
           return ((got >> ((16 * i) >> copy_sh)) & 1u) != 0u && first + 16 * i + key < n;
@@ -841,17 +844,17 @@ __global__ void __launch_bounds__(kNW * 32, 2)
       // the stage is refilled through the async proxy: this warp's reads first
       fence_proxy_async_smem();
       __syncwarp();
-      if (more) issue();
+      if (in_f < w1) issue();
     }
-    f += at.s1 - at.s0;
-    if (at.s0 == 0 && at.s1 == at.ns) {
+    if (at.s == 0 && steps == at.ns) {
       warp_output<D, F32>(a, st, at.b, at.g);
     } else {
       // in part: a run's first unit or its last (whose ring is free by then)
-      const int slot = 2 * warp + (at.f == w0 ? 0 : 1);
+      const int slot = 2 * warp + (f == w0 ? 0 : 1);
       piece_store<D>(slot_at(slot), st, a.G);
       if (lane == 0) s_unit[slot] = at.b * a.Hkv + at.g;
     }
+    f += steps;
   }
   __syncthreads();
   if (tid == 0) {
@@ -964,7 +967,7 @@ __global__ void __launch_bounds__(kReuseNW * 32, kReuseCtasPerSm)
   const int pf = static_cast<int>(qpart_floats(a.G, D));
   uint8_t* ring = smem + warp * kReuseStages * kStageBytes;   // at the end: the warp's piece
   const int unit = blockIdx.y, b = unit / a.Hkv, g = unit % a.Hkv;
-  float qx[D / 4];
+  QRaw<D, TERMS> qx;
   load_q<D, TERMS>(a, b, g, qx);
   const int n = len_of(a, b, blockIdx.x == 0 && g == 0);
   const int nch = POOLED ? 0 : a.plan_chunks;
