@@ -183,13 +183,20 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src, uint32_t 
 __device__ __forceinline__ void cp_async16_s(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-// 4- or 8-byte global -> shared copy; !ok zero-fills without reading.
+// 4-, 8- or 16-byte global -> shared copy of scattered pieces; !ok zero-fills
+// without reading. L2 fetches the 64 bytes around a piece: without the
+// qualifier it fetched 126 of each 128-byte line (random 32-byte reads).
 template <int BYTES>
-__device__ __forceinline__ void cp_async_small(void* dst, const void* src, bool ok) {
-  static_assert(BYTES == 4 || BYTES == 8, "sizes without the L1 bypass");
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)), "l"(src),
-               "n"(BYTES), "r"(ok ? BYTES : 0)
-               : "memory");
+__device__ __forceinline__ void cp_async_scattered(void* dst, const void* src, bool ok) {
+  static_assert(BYTES == 4 || BYTES == 8 || BYTES == 16, "cp.async sizes");
+  if (BYTES == 16)
+    asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)),
+                 "l"(src), "r"(ok ? 16 : 0)
+                 : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global.L2::64B [%0], [%1], %2, %3;" ::"r"(smem_u32(dst)),
+                 "l"(src), "n"(BYTES), "r"(ok ? BYTES : 0)
+                 : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");

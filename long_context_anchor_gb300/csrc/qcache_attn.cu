@@ -1072,8 +1072,8 @@ __global__ void __launch_bounds__(kReuseNW * 32, kReuseCtasPerSm)
       const uint8_t* src = a.cache + static_cast<size_t>(ok ? place[j] >> 4 : 0u) * kGroupBytes +
                            8 * D + (ok ? place[j] & 15u : 0u) * (D / 16);
       uint8_t* to = dst + (row >> 4) * kGroupBytes + 8 * D + (row & 15) * (D / 16);
-      cp_async_small<D / 16>(to, src, ok);
-      cp_async_small<D / 16>(to + 9 * D, src + 9 * D, ok);
+      cp_async_scattered<D / 16>(to, src, ok);
+      cp_async_scattered<D / 16>(to + 9 * D, src + 9 * D, ok);
     }
     constexpr int kChunks = D / 32;               // 16-byte pieces of a row's codes
     constexpr int kTurns = kRows * kChunks / 32;
@@ -1086,8 +1086,8 @@ __global__ void __launch_bounds__(kReuseNW * 32, kReuseCtasPerSm)
       const uint8_t* src = a.cache + static_cast<size_t>(ok ? pl >> 4 : 0u) * kGroupBytes +
                            (ok ? pl & 15u : 0u) * (D / 2) + ch * 16;
       uint8_t* to = dst + (row >> 4) * kGroupBytes + (row & 15) * (D / 2) + ch * 16;
-      cp_async16(to, src, ok ? 16u : 0u);
-      cp_async16(to + 9 * D, src + 9 * D, ok ? 16u : 0u);
+      cp_async_scattered<16>(to, src, ok);
+      cp_async_scattered<16>(to + 9 * D, src + 9 * D, ok);
     }
   };
   int next = g0 + warp;           // step that is copied next
