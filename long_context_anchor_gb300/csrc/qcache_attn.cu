@@ -597,7 +597,10 @@ __device__ __forceinline__ int len_of(const QDecodeArgs& a, int b, bool report) 
 // The steps of all units (unit = sequence * Hkv + KV head; a step is 16 *
 // kStep keys, and a sequence of n keys has ceil(n / (16 kStep)) per head) form one
 // line, and every warp of the grid takes an equal run of it, so that ragged
-// batches balance. A run may span units: the warp's pieces of units it does
+// batches balance. A unit starts with kUnitCost places without a step: what
+// its query, its first loads and its output cost a warp, so that runs of many
+// short units do not come last (48 sequences of 0 to 16001 keys: 84 us
+// without, 75 us with). A run may span units: the warp's pieces of units it does
 // not hold alone go to shared memory, the CTA joins those of its warps after
 // one barrier, and a unit that several CTAs share is joined by the last of
 // them to arrive.
@@ -606,34 +609,46 @@ __device__ __forceinline__ int len_of(const QDecodeArgs& a, int b, bool report) 
 // filled by one bulk copy per block that the step touches (groups of a block
 // are contiguous), which the first lanes issue as soon as the warp has left
 // the stage; no warp waits for another one before the end.
-constexpr int kNW = 8;            // warps per CTA (and at most 8 heads per KV head)
+// One CTA of 16 warps per SM: on a GB300 the 8B shape takes 65.5 us so, 67.3 as
+// two CTAs of 8 and 69.2 as four of 4 (the joins get longer); five of 4, with
+// 102 registers per thread, 95.
+constexpr int kNW = 16, kDenseCtasPerSm = 1;
 constexpr int kMinRun = 2;        // steps per warp at least
 constexpr int kDenseStages = 2;
 
-// The unit that holds step f of the line.
-struct Place {
+constexpr int kUnitCost = 1;
+
+// The part of a run that lies in the unit at place f of the line: steps [s0, s1)
+// of its ns (none, if the run has only the unit's first place), and the place
+// behind it.
+struct Part {
   int b, g, n;     // sequence, KV head, cached tokens
-  int ns, s;       // the unit's steps, and f's number among them
+  int ns, s0, s1;
+  int next;
 };
-__device__ __forceinline__ Place place_of(const QDecodeArgs& a, const int* pref, int f) {
+__device__ __forceinline__ Part part_at(const QDecodeArgs& a, const int* pref, int f, int end) {
   int lo = 0, hi = a.B;   // the sequence: pref[lo] * Hkv <= f < pref[lo + 1] * Hkv
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (pref[mid] * a.Hkv <= f) lo = mid;
     else hi = mid;
   }
-  Place p;
+  Part p;
   p.b = lo;
   p.n = len_of(a, lo, false);
-  p.ns = pref[lo + 1] - pref[lo];
+  const int places = pref[lo + 1] - pref[lo];
   const int in = f - pref[lo] * a.Hkv;
-  p.g = in / p.ns;
-  p.s = in - p.g * p.ns;
+  p.g = in / places;
+  const int at = in - p.g * places;
+  p.ns = places - kUnitCost;
+  p.next = min(end, f + places - at);
+  p.s0 = max(0, at - kUnitCost);
+  p.s1 = max(0, at - kUnitCost + p.next - f);
   return p;
 }
 
 template <int D, int TERMS, bool SCORES>
-__global__ void __launch_bounds__(kNW * 32, 2)
+__global__ void __launch_bounds__(kNW * 32, kDenseCtasPerSm)
     k_qdecode_dense(const __grid_constant__ QDecodeArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -661,7 +676,8 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   int carry = 0;
   for (int b0 = 0; b0 < a.B; b0 += kNW * 32) {
     const int b = b0 + tid;
-    const int n = b < a.B ? (len_of(a, b, blockIdx.x == 0) + kKeys - 1) / kKeys : 0;
+    int n = b < a.B ? (len_of(a, b, blockIdx.x == 0) + kKeys - 1) / kKeys : 0;
+    if (n > 0) n += kUnitCost;
     int incl = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -697,8 +713,8 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   const uint32_t gmask = (1u << (a.bs_shift - 4)) - 1u;
   const uint32_t head_bytes = static_cast<uint32_t>(kGroupBytes) << (a.bs_shift - 4);
   const uint32_t block_bytes = head_bytes * static_cast<uint32_t>(a.Hkv);
-  int in_f = w0;                  // line step that is issued next
-  int in_left = 0;                // steps of the run in its unit from there on
+  int in_next = w0;               // place of the unit after the one being issued
+  int in_left = 0;                // steps of the run left to issue in this unit
   int in_key = 0, in_n = 0;       // this lane's copy: first key, tokens of the sequence
   const int32_t* in_row = a.table;     // the sequence's row of the block table
   const uint8_t* in_base = a.cache;    // the KV head's place in block 0
@@ -707,9 +723,10 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   unsigned int have = 0u;         // byte i: the copies that stage i got
   int pending = 0;                // steps issued and not taken
   bool alive = true;
-  auto enter = [&](const Place& p) {
-    in_left = min(p.ns - p.s, w1 - in_f);
-    in_key = lane < ncopy ? p.s * kKeys + (lane << copy_sh) : p.n;   // other lanes copy nothing
+  auto enter = [&](const Part& p) {
+    in_next = p.next;
+    in_left = p.s1 - p.s0;
+    in_key = lane < ncopy ? p.s0 * kKeys + (lane << copy_sh) : p.n;   // other lanes copy nothing
     in_n = p.n;
     in_row = a.table + static_cast<size_t>(p.b) * a.max_blocks;
     in_base = a.cache + static_cast<size_t>(p.g) * head_bytes;
@@ -718,7 +735,7 @@ __global__ void __launch_bounds__(kNW * 32, 2)
     id = 0;
     if (in_key < in_n) id = __ldg(in_row + (in_key >> a.bs_shift));
   };
-  auto issue = [&]() {            // all lanes; in_f < w1 holds
+  auto issue = [&]() {            // all lanes; in_left > 0 holds
     const bool want = in_key < in_n;
     const bool ok = want && static_cast<uint32_t>(id) < static_cast<uint32_t>(a.num_blocks);
     const unsigned int got = __ballot_sync(0xffffffffu, ok);
@@ -735,22 +752,24 @@ __global__ void __launch_bounds__(kNW * 32, 2)
     have = __byte_perm(have, got, in_stage == 0 ? 0x3214 : 0x3240);
     in_stage ^= 1;
     ++pending;
-    ++in_f;
     in_key += kKeys;
     if (lane >= ncopy) in_key = in_n;
-    if (--in_left == 0 && in_f < w1) enter(place_of(a, pref, in_f));
-    if (in_f < w1) fetch_id();
+    if (--in_left == 0) {
+      while (in_left == 0 && in_next < w1) enter(part_at(a, pref, in_next, w1));
+    }
+    if (in_left > 0) fetch_id();
   };
   static_assert(kDenseStages == 2, "stages alternate");
-  Place at = {};
+  Part at = {};
   QRaw<D, TERMS> qx;   // the query of the unit that comes next
-  if (w0 < w1) {
-    at = place_of(a, pref, w0);
+  at.next = w0;
+  while (at.s0 == at.s1 && at.next < w1) at = part_at(a, pref, at.next, w1);
+  if (at.s0 < at.s1) {
     enter(at);
     fetch_id();
     load_q<D, TERMS>(a, at.b, at.g, qx);
     issue();
-    if (in_f < w1) issue();
+    if (in_left > 0) issue();
   }
 
   // ---- arithmetic
@@ -758,13 +777,9 @@ __global__ void __launch_bounds__(kNW * 32, 2)
   const int row0 = row_key(gid);   // keys row0 and row0 + 8 of a slice
   int stage = 0;
   uint32_t phase = 0;
-  for (int f = w0; f < w1;) {
-    if (f != w0) {
-      at = place_of(a, pref, f);
-      load_q<D, TERMS>(a, at.b, at.g, qx);
-    }
-    const int n = at.n, steps = min(at.ns - at.s, w1 - f);
-    int first = at.s * kKeys;   // first key of the step
+  for (bool first_unit = true; at.s0 < at.s1; first_unit = false) {
+    const int n = at.n, steps = at.s1 - at.s0;
+    int first = at.s0 * kKeys;   // first key of the step
     QFrag<D, TERMS> qf;
     make_q(a, qx, qf);
     float* sp[2] = {nullptr, nullptr};
@@ -844,17 +859,24 @@ __global__ void __launch_bounds__(kNW * 32, 2)
       // the stage is refilled through the async proxy: this warp's reads first
       fence_proxy_async_smem();
       __syncwarp();
-      if (in_f < w1) issue();
+      if (in_left > 0) issue();
     }
-    if (at.s == 0 && steps == at.ns) {
+    if (steps == at.ns) {
       warp_output<D, F32>(a, st, at.b, at.g);
     } else {
       // in part: a run's first unit or its last (whose ring is free by then)
-      const int slot = 2 * warp + (f == w0 ? 0 : 1);
+      const int slot = 2 * warp + (first_unit ? 0 : 1);
       piece_store<D>(slot_at(slot), st, a.G);
       if (lane == 0) s_unit[slot] = at.b * a.Hkv + at.g;
     }
-    f += steps;
+    // the run's next unit
+    int next = at.next;
+    at.s0 = at.s1 = 0;
+    while (at.s0 == at.s1 && next < w1) {
+      at = part_at(a, pref, next, w1);
+      next = at.next;
+    }
+    if (at.s0 < at.s1) load_q<D, TERMS>(a, at.b, at.g, qx);
   }
   __syncthreads();
   if (tid == 0) {
@@ -878,7 +900,7 @@ __global__ void __launch_bounds__(kNW * 32, 2)
     int j = i;
     while (j < nlist && s_unit[s_list[j]] == unit) ++j;
     const int b = unit / a.Hkv, g = unit % a.Hkv, nb = pref[b + 1] - pref[b];
-    const int u0 = pref[b] * a.Hkv + g * nb, u1 = u0 + nb;   // the unit's steps
+    const int u1 = pref[b] * a.Hkv + (g + 1) * nb, u0 = u1 - nb + kUnitCost;   // its steps' places
     float* dst = nullptr;
     if (u0 < c0 || u1 > c0 + per_cta) {
       dst = a.part + (2 * static_cast<size_t>(blockIdx.x) + (u0 > c0 ? 1 : 0)) * stride;
@@ -892,8 +914,7 @@ __global__ void __launch_bounds__(kNW * 32, 2)
       ++n_shared;
     }
     // the next unit's elements go to the threads that this one leaves free
-    const int e = (tid - first_elem) & (kNW * 32 - 1);
-    if (e < elems) {
+    for (int e = (tid - first_elem) & (kNW * 32 - 1); e < elems; e += kNW * 32) {
       const int h = e / (D / 4), e4 = e & (D / 4 - 1);
       const Joined x = join_some<false>(
           [&](int s) -> const float* { return slot_at(s_list[i + s]); }, 0, j - i, a.G, h, e);
