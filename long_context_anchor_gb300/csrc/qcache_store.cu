@@ -10,7 +10,7 @@
 //   s    = amax / 6 rounded to e4m3 (nearest, ties to even, at most 448)
 //   code = x' / s rounded to e2m1 {0, .5, 1, 1.5, 2, 3, 4, 6} (same, at most 6)
 // and the stored element is code * s * {k,v}_scale. Both quotients are
-// rounded once, from their exact value: see round_quotient.
+// rounded as their exact values would be: see round_quotient.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -270,24 +270,12 @@ __global__ void __launch_bounds__(kPlanThreads) k_qplan(const __grid_constant__ 
 }
 
 // -------------------------------------------------------------------- rows --
+// One thread per 16 elements: thread i of (head, K or V) takes block i % (d / 16)
+// of token i / (d / 16), so that a warp writes neighbouring rows of one group
+// of the cache. Every element is read once and its 4.5 bits written once (or
+// the other way): bound by DRAM. 16384 tokens x 8 heads x 128 (105 MB either
+// way): 20 us to write, 19.5 us to read.
 constexpr int kRowThreads = 256;
-
-// x / s rounded so that the rounding to a few bits that follows is the
-// rounding of the exact quotient: q is x / s to the last bit (one Newton
-// correction of x * (1/s)), and where the division leaves a remainder q is
-// moved one last place towards it, so that a q that sits on a tie only by
-// its own rounding falls on the right side. Rounding q to 2 to 4 bits cannot
-// be changed by that step otherwise.
-__device__ __forceinline__ float round_quotient(float x, float s, float inv) {
-  float q = x * inv;
-  q = fmaf(fmaf(-q, s, x), inv, q);
-  const float r = fmaf(-q, s, x);
-  if (r != 0.f && q != 0.f) {
-    const int step = ((r > 0.f) == (q > 0.f)) ? 1 : -1;
-    q = __int_as_float(__float_as_int(q) + step);
-  }
-  return q;
-}
 
 __device__ __forceinline__ uint32_t e4m3_of(float x) {
   uint16_t r;
@@ -301,41 +289,86 @@ __device__ __forceinline__ float e4m3_value(uint32_t b) {
   asm("{.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;}" : "=f"(f) : "r"(h));
   return f;
 }
-// two e2m1 codes, `lo` in the low half of the byte
-__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {
+// eight e2m1 codes, the first in the lowest four bits
+__device__ __forceinline__ uint32_t e2m1x8(const float (&x)[8]) {
   uint32_t r;
-  asm("{.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n\tcvt.u32.u8 %0, b;}"
+  asm("{.reg .b8 b0, b1, b2, b3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+      "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+      "mov.b32 %0, {b0, b1, b2, b3};}"
       : "=r"(r)
-      : "f"(hi), "f"(lo));
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
   return r;
 }
 
-template <typename T>
-__device__ __forceinline__ void load16(const T* p, float (&x)[16]);
-template <>
-__device__ __forceinline__ void load16<float>(const float* p, float (&x)[16]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float4 f = __ldg(reinterpret_cast<const float4*>(p) + i);
-    x[4 * i] = f.x;
-    x[4 * i + 1] = f.y;
-    x[4 * i + 2] = f.z;
-    x[4 * i + 3] = f.w;
-  }
-}
-template <>
-__device__ __forceinline__ void load16<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[16]) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(p) + i);
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-      x[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+// x / s such that rounding it to the 1 to 4 bits of e2m1 or e4m3 is rounding
+// the exact quotient. One Newton correction of x * (1/s) makes q the quotient
+// to its last bit, and exact where the quotient has few bits, as every tie
+// has. A bf16 x (8 bits) over an s of at most 4 bits is otherwise at least 2^-13
+// away from a tie, so that is all it needs (EXACT false). The quotient of an
+// fp32 x may round onto a tie: where the division leaves a remainder, q moves
+// one last place towards it.
+template <bool EXACT>
+__device__ __forceinline__ float round_quotient(float x, float s, float inv) {
+  float q = x * inv;
+  q = fmaf(fmaf(-q, s, x), inv, q);
+  if (EXACT) {
+    const float r = fmaf(-q, s, x);
+    if (r != 0.f && q != 0.f) {
+      const int step = ((r > 0.f) == (q > 0.f)) ? 1 : -1;
+      q = __int_as_float(__float_as_int(q) + step);
     }
   }
+  return q;
 }
+
+// 16 elements as stored: raw words, the largest magnitude (NaN if there is one).
+template <typename T>
+struct Row16;
+template <>
+struct Row16<float> {
+  float x[16];
+  __device__ __forceinline__ void load(const void* p) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float4 f = __ldg(static_cast<const float4*>(p) + i);
+      x[4 * i] = f.x;
+      x[4 * i + 1] = f.y;
+      x[4 * i + 2] = f.z;
+      x[4 * i + 3] = f.w;
+    }
+  }
+  __device__ __forceinline__ float amax() const {
+    uint32_t m = 0u;   // magnitudes order as their bits do, NaNs above infinity
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+    return __uint_as_float(m);
+  }
+  __device__ __forceinline__ float get(int i) const { return x[i]; }
+};
+template <>
+struct Row16<__nv_bfloat16> {
+  uint32_t w[8];
+  __device__ __forceinline__ void load(const void* p) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint4 u = __ldg(static_cast<const uint4*>(p) + i);
+      w[4 * i] = u.x;
+      w[4 * i + 1] = u.y;
+      w[4 * i + 2] = u.z;
+      w[4 * i + 3] = u.w;
+    }
+  }
+  __device__ __forceinline__ float amax() const {
+    uint32_t m = w[0] & 0x7fff7fffu;   // two magnitudes side by side
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+    return __uint_as_float(max(m << 16, m & 0xffff0000u));
+  }
+  __device__ __forceinline__ float get(int i) const {
+    return __uint_as_float((i & 1) ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+  }
+};
 __device__ __forceinline__ void store16(float* p, const float (&x)[16]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -350,89 +383,89 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, const float (&x)[16]) 
                    pack_bf16(x[8 * i + 4], x[8 * i + 5]), pack_bf16(x[8 * i + 6], x[8 * i + 7]));
 }
 
-// Byte address of (slot, head)'s row of codes of K (which = 0) or V (1), and
-// of its scales.
-struct RowAddr {
+// What one thread works on, and where its codes and scale are.
+struct RowPlace {
+  int tok, head, which, blk;
+  int slot;                 // negative: padding
   uint8_t* codes;
-  uint8_t* scales;
+  uint8_t* scale;
 };
-__device__ __forceinline__ RowAddr row_addr(const QRowArgs& a, int which, int slot, int head) {
-  const int sh = a.bs_shift, gpb = 1 << (sh - 4);
-  const size_t block = static_cast<size_t>(slot >> sh);
-  const int in = slot & ((1 << sh) - 1);
-  uint8_t* grp = a.cache + ((block * a.Hkv + head) * gpb + (in >> 4)) * (18 * a.d) +
-                 which * (9 * a.d);
-  const int r = in & 15;
-  return {grp + r * (a.d / 2), grp + 8 * a.d + r * (a.d / 16)};
+template <int D>
+__device__ __forceinline__ bool row_place(const QRowArgs& a, RowPlace& p) {
+  constexpr int kBlocks = D / 16;
+  const int i = blockIdx.x * kRowThreads + threadIdx.x;
+  p.head = blockIdx.y;
+  p.which = blockIdx.z;
+  p.tok = i / kBlocks;
+  p.blk = i % kBlocks;
+  if (p.tok >= a.T) return false;
+  p.slot = a.slot_map[p.tok];
+  if (p.slot < 0) return true;
+  const int sh = a.bs_shift;
+  if ((p.slot >> sh) >= a.num_blocks) {
+    report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x511);
+    p.slot = -1;
+    return true;
+  }
+  const size_t grp = ((static_cast<size_t>(p.slot >> sh) * a.Hkv + p.head) << (sh - 4)) +
+                     ((p.slot & ((1 << sh) - 1)) >> 4);
+  uint8_t* at = a.cache + grp * (18 * D) + p.which * (9 * D);
+  const int r = p.slot & 15;
+  p.codes = at + r * (D / 2) + p.blk * 8;
+  p.scale = at + 8 * D + r * (D / 16) + p.blk;
+  return true;
 }
 
-// One thread per 16 elements; consecutive threads take a row's blocks, then
-// the next token of the same head, so that a warp writes neighbouring rows of
-// one group. Bound by DRAM: each element is read once and its 4.5 bits are
-// written once.
-template <typename T>
+template <typename T, int D>
 __global__ void __launch_bounds__(kRowThreads) k_qappend(const __grid_constant__ QRowArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int per_row = a.d / 16, which = blockIdx.y;
-  const long long n = static_cast<long long>(a.T) * a.Hkv * per_row;
-  const long long i = static_cast<long long>(blockIdx.x) * kRowThreads + threadIdx.x;
-  if (i >= n) return;
-  const int blk = static_cast<int>(i % per_row);
-  const long long row = i / per_row;
-  const int tok = static_cast<int>(row % a.T), head = static_cast<int>(row / a.T);
-  const int slot = a.slot_map[tok];
-  if (slot < 0) return;   // padding
-  if (slot >= (a.num_blocks << a.bs_shift)) {
-    report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x511);
-    return;
-  }
-  float x[16];
-  load16(static_cast<const T*>(a.src[which]) + tok * a.tok_stride[which] +
-             head * a.head_stride[which] + blk * 16, x);
-  float amax = 0.f;
-  bool nan = false;
-#pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    x[e] *= a.scale[which];
-    nan |= x[e] != x[e];
-    // what saturates does so here already, infinities among it
-    x[e] = fminf(fmaxf(x[e], -2688.f), 2688.f);
-    amax = fmaxf(amax, fabsf(x[e]));
-  }
-  const uint32_t sb = nan ? 0x7fu : e4m3_of(round_quotient(amax, 6.f, 1.f / 6.f));
-  const float s = e4m3_value(sb);
+  constexpr bool kExact = sizeof(T) == 4;
+  RowPlace p;
+  if (!row_place<D>(a, p) || p.slot < 0) return;
+  Row16<T> x;
+  x.load(static_cast<const T*>(a.src[p.which]) + p.tok * a.tok_stride[p.which] +
+         p.head * a.head_stride[p.which] + p.blk * 16);
+  // the cache's own scale is a power of two: it goes into the block's scale
+  const float unit = a.scale[p.which];
+  float amax = x.amax();
+  const bool nan = amax != amax;
+  amax = fminf(amax * unit, 2688.f);   // what is above saturates, infinities among it
+  const uint32_t sb = nan ? 0x7fu : e4m3_of(round_quotient<kExact>(amax, 6.f, 1.f / 6.f));
   uint32_t w[2] = {0u, 0u};
-  if (s > 0.f) {   // a block of zeros, or one that rounds to them, has scale 0 (and NaN none)
-    const float inv = 1.f / s;
+  if ((sb & 0x7fu) != 0u && !nan) {   // scale 0: the block's elements all round to 0
+    const float s = e4m3_value(sb) / unit, inv = 1.f / s;
+    auto codes = [&](auto element) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      w[e >> 2] |= e2m1_pair(round_quotient(x[2 * e], s, inv), round_quotient(x[2 * e + 1], s, inv))
-                   << (8 * (e & 3));
+      for (int h = 0; h < 2; ++h) {
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = round_quotient<kExact>(element(8 * h + e), s, inv);
+        w[h] = e2m1x8(y);
+      }
+    };
+    if (amax < 2688.f) {
+      codes([&](int i) { return x.get(i); });
+    } else {   // an infinity's quotient is NaN: what passes 6 s is cut first
+      const float most = 8.f * s;
+      codes([&](int i) { return fminf(fmaxf(x.get(i), -most), most); });
+    }
   }
-  const RowAddr ra = row_addr(a, which, slot, head);
-  reinterpret_cast<uint2*>(ra.codes)[blk] = make_uint2(w[0], w[1]);
-  ra.scales[blk] = static_cast<uint8_t>(sb);
+  *reinterpret_cast<uint2*>(p.codes) = make_uint2(w[0], w[1]);
+  *p.scale = static_cast<uint8_t>(sb);
 }
 
-// The same threads, the other way; a padding slot's row is zero.
-template <typename T>
+// The other way; a padding slot's row is zero.
+template <typename T, int D>
 __global__ void __launch_bounds__(kRowThreads) k_qread(const __grid_constant__ QRowArgs a) {
   pdl_wait();
   pdl_trigger();
-  const int per_row = a.d / 16, which = blockIdx.y;
-  const long long n = static_cast<long long>(a.T) * a.Hkv * per_row;
-  const long long i = static_cast<long long>(blockIdx.x) * kRowThreads + threadIdx.x;
-  if (i >= n) return;
-  const int blk = static_cast<int>(i % per_row);
-  const long long row = i / per_row;
-  const int tok = static_cast<int>(row % a.T), head = static_cast<int>(row / a.T);
-  const int slot = a.slot_map[tok];
+  RowPlace p;
+  if (!row_place<D>(a, p)) return;
   float x[16];
-  if (slot >= 0 && slot < (a.num_blocks << a.bs_shift)) {
-    const RowAddr ra = row_addr(a, which, slot, head);
-    const uint2 c = *(reinterpret_cast<const uint2*>(ra.codes) + blk);
-    const float s = e4m3_value(ra.scales[blk]) * a.scale[which];
+  if (p.slot >= 0) {
+    const uint2 c = *reinterpret_cast<const uint2*>(p.codes);
+    const float s = e4m3_value(*p.scale) * a.scale[p.which];
     const uint32_t w[2] = {c.x, c.y};
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -446,21 +479,19 @@ __global__ void __launch_bounds__(kRowThreads) k_qread(const __grid_constant__ Q
       x[2 * e + 1] = hi * s;
     }
   } else {
-    if (slot >= 0) report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x512);
 #pragma unroll
     for (int e = 0; e < 16; ++e) x[e] = 0.f;
   }
-  store16(static_cast<T*>(a.dst[which]) + tok * a.tok_stride[which] +
-              head * a.head_stride[which] + blk * 16, x);
+  store16(static_cast<T*>(a.dst[p.which]) + p.tok * a.tok_stride[p.which] +
+              p.head * a.head_stride[p.which] + p.blk * 16, x);
 }
 
 template <typename K>
 cudaError_t launch_rows(K kern, const QRowArgs& a, cudaStream_t st) {
-  const long long n = static_cast<long long>(a.T) * a.Hkv * (a.d / 16);
-  if (n == 0) return cudaSuccess;
-  const long long blocks = (n + kRowThreads - 1) / kRowThreads;
-  if (blocks > 0x7fffffffll) return cudaErrorNotSupported;
-  return launch_pdl(kern, dim3(static_cast<unsigned int>(blocks), 2), dim3(kRowThreads), 0, st, a);
+  if (a.T == 0) return cudaSuccess;
+  const int per_cta = kRowThreads / (a.d / 16);   // tokens
+  return launch_pdl(kern, dim3((a.T + per_cta - 1) / per_cta, a.Hkv, 2), dim3(kRowThreads), 0, st,
+                    a);
 }
 
 }  // namespace
@@ -490,13 +521,19 @@ cudaError_t launch_qplan(const QPlanArgs& a, cudaStream_t st) {
 }
 
 cudaError_t launch_qappend(const QRowArgs& a, int dtype, cudaStream_t st) {
-  return dtype == KASCADE_F32 ? launch_rows(k_qappend<float>, a, st)
-                              : launch_rows(k_qappend<__nv_bfloat16>, a, st);
+  if (dtype == KASCADE_F32)
+    return a.d == 128 ? launch_rows(k_qappend<float, 128>, a, st)
+                      : launch_rows(k_qappend<float, 64>, a, st);
+  return a.d == 128 ? launch_rows(k_qappend<__nv_bfloat16, 128>, a, st)
+                    : launch_rows(k_qappend<__nv_bfloat16, 64>, a, st);
 }
 
 cudaError_t launch_qread(const QRowArgs& a, int dtype, cudaStream_t st) {
-  return dtype == KASCADE_F32 ? launch_rows(k_qread<float>, a, st)
-                              : launch_rows(k_qread<__nv_bfloat16>, a, st);
+  if (dtype == KASCADE_F32)
+    return a.d == 128 ? launch_rows(k_qread<float, 128>, a, st)
+                      : launch_rows(k_qread<float, 64>, a, st);
+  return a.d == 128 ? launch_rows(k_qread<__nv_bfloat16, 128>, a, st)
+                    : launch_rows(k_qread<__nv_bfloat16, 64>, a, st);
 }
 
 }  // namespace kascade

@@ -766,25 +766,25 @@ def qcache_plan(kv_lens, new_lens, block_table, free_blocks, free_count, block_s
     return slots, cu, lens, count
 
 
+_I64x4 = ctypes.c_int64 * 4
 _ROW_CODES = {torch.bfloat16: (BF16, 8), torch.float32: (F32, 4)}   # code, elements per 16 bytes
 
 
 def _row_strides(t, name, shape, dtype, dev, unit):
     """Token and head strides of rows t [T, Hkv, d], which must be contiguous and
     start on 16-byte boundaries (strides of axes of length 1 do not matter)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s: expected a torch.Tensor" % name)
-    if t.shape != shape:
-        raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
-    if t.dtype is not dtype:
-        raise TypeError("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
-    if t.device != dev:
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype
+            and t.device == dev):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s: expected a torch.Tensor" % name)
+        if t.shape != shape:
+            raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+        if t.dtype is not dtype:
+            raise TypeError("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
         raise ValueError("%s: on %s, expected %s" % (name, t.device, dev))
     tok, head, one = t.stride()
-    if shape[0] <= 1:
-        tok = 0
-    if shape[1] <= 1:
-        head = 0
+    if shape[0] <= 1 or shape[1] <= 1:
+        tok, head = tok if shape[0] > 1 else 0, head if shape[1] > 1 else 0
     if shape[0] and (one != 1 or tok % unit or head % unit or t.data_ptr() % 16):
         raise ValueError("%s: rows must be contiguous and start on 16-byte boundaries" % name)
     return tok, head
@@ -815,7 +815,7 @@ def qcache_append(k, v, slot_map, pages, k_scale=1.0, v_scale=1.0, ws=None, stre
             return qcache_append(k, v, slot_map, pages, k_scale, v_scale, ws)
     buf = _qws(ws, dev, 256)
     _check(_lib.kascade_qcache_append(geo, hkv, d, code, k.data_ptr(), v.data_ptr(),
-                                      (ctypes.c_int64 * 4)(kt, kh, vt, vh),
+                                      _I64x4(kt, kh, vt, vh),
                                       slot_map.data_ptr(), T, pages.data_ptr(),
                                       buf.data_ptr(), buf.numel(), _raw_stream(dev)),
            "kascade_qcache_append")
@@ -856,7 +856,7 @@ def qcache_read(pages, slot_map, dtype=torch.bfloat16, k_scale=1.0, v_scale=1.0,
     buf = _qws(ws, dev, 256)
     _check(_lib.kascade_qcache_read(geo, hkv, d, code, pages.data_ptr(), slot_map.data_ptr(),
                                     T, ok.data_ptr(), ov.data_ptr(),
-                                    (ctypes.c_int64 * 4)(*strides), buf.data_ptr(),
+                                    _I64x4(*strides), buf.data_ptr(),
                                     buf.numel(), _raw_stream(dev)), "kascade_qcache_read")
     return ok, ov
 
