@@ -32,6 +32,9 @@ constexpr float kNoKey = -3.0e38f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kPShift = 14;          // weights are held as 2^14 p
+// The running maximum is a reference, not the maximum itself: it is raised once
+// a score passes it by more than this (weights then reach 2^15.75, within fp16).
+constexpr float kSlack = 1.75f;
 constexpr int kQExp = 12;            // q's largest element is scaled to [2^12, 2^13)
 // Slices of 16 keys per step: a step is 4608 bytes at either head size.
 template <int D>
@@ -247,7 +250,8 @@ __device__ __forceinline__ void slice_products(const uint8_t* grp, const LanePla
 // Running state of one warp over keys of one (sequence, KV head). Thread
 // (gid = lane/4, c4 = lane%4) owns heads 2 c4, 2 c4 + 1 and output dims
 // gid * D/8 .. + D/8 of both: o[i] = (dim 2i, head 2c4), (2i, 2c4+1),
-// (2i + 1, 2c4), (2i + 1, 2c4 + 1). m: running maxima (log2 units); nmu = 14 - m;
+// (2i + 1, 2c4), (2i + 1, 2c4 + 1). m: running maxima (log2 units, within kSlack);
+// nmu = 14 - m;
 // l: this lane's sums of 2^14 p. nmu and l hold both heads, packed.
 template <int D>
 struct QState {
@@ -301,8 +305,8 @@ __device__ __forceinline__ void slice_values(float (&o)[D / 16][4], const float 
 
 // One step: t[i][r] holds the raw products of slice i, score row gid + 8 r, for
 // both heads (masked: -inf), ml the heads' factors to log2 units. The running
-// maximum moves only when a score exceeds it (one vote), so the common step
-// rescales nothing. fix(i, vs) may change the V scales of slice i (a masked
+// maximum moves only when a score passes it by kSlack (one vote), so the common
+// step rescales nothing. fix(i, vs) may change the V scales of slice i (a masked
 // key's must become 0: what lies there may be anything) and returns the heads
 // of this lane (bits 0, 1) whose outputs become NaN.
 template <int D, int TERMS, typename Fix>
@@ -326,7 +330,7 @@ __device__ __forceinline__ void attend(QState<D>& st, const uint64_t (&t)[kStepO
       }
     return top;
   };
-  if (__any_sync(0xffffffffu, exponents() > static_cast<float>(kPShift))) {
+  if (__any_sync(0xffffffffu, exponents() > kPShift + kSlack)) {
     float x0 = kNoKey, x1 = kNoKey;
 #pragma unroll
     for (int i = 0; i < kStep; ++i) {
@@ -819,15 +823,26 @@ __global__ void __launch_bounds__(kNW * 32, kDenseCtasPerSm)
         // keys that do not count: behind the sequence's end, or in a block the
         // table does not name
         const bool full = got == (1u << ncopy) - 1u && first + kKeys <= n;
-        auto counts = [&](int i, int key) {
-          return ((got >> ((16 * i) >> copy_sh)) & 1u) != 0u && first + 16 * i + key < n;
-        };
         if (!full) {
+          // rare, and kept apart by its loop: as selects in every step it cost
+          // 30 instructions a slice. What lies in these keys' V rows may be
+          // anything: their scales become 0 in the stage.
+          auto counts = [&](int key) {
+            return ((got >> (key >> copy_sh)) & 1u) != 0u && first + key < n;
+          };
+          for (int r = lane; r < kKeys; r += 32)
+            if (!counts(r)) {
+              uint8_t* sc = ring + stage * kStageBytes + (r >> 4) * kGroupBytes + 17 * D +
+                            (r & 15) * (D / 16);
+#pragma unroll
+              for (int i = 0; i < D / 64; ++i) reinterpret_cast<uint32_t*>(sc)[i] = 0u;
+            }
+          __syncwarp();
 #pragma unroll
           for (int i = 0; i < kStep; ++i)
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-              if (!counts(i, row0 + 8 * r)) t[i][r] = f2_pack(kNegInf, kNegInf);
+              if (!counts(16 * i + row0 + 8 * r)) t[i][r] = f2_pack(kNegInf, kNegInf);
         }
         if (SCORES) {
 #pragma unroll
@@ -844,14 +859,7 @@ __global__ void __launch_bounds__(kNW * 32, kDenseCtasPerSm)
             }
         }
         if (got != 0u)
-          attend<D, TERMS>(st, t, ml, buf, places, [&](int i, uint32_t (&vs)[4]) {
-            if (!full) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (!counts(i, v_key(j))) vs[j] = 0u;
-            }
-            return 0u;
-          });
+          attend<D, TERMS>(st, t, ml, buf, places, [](int, uint32_t (&)[4]) { return 0u; });
       }
       stage ^= 1;
       phase ^= stage == 0 ? 1u : 0u;
