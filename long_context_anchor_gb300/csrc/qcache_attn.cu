@@ -516,18 +516,18 @@ __device__ void arrive_and_join(const QDecodeArgs& a, int n_units, const SharedU
   __shared__ unsigned int s_last;
   const int tid = threadIdx.x, G = a.G;
   __syncthreads();   // every piece of this CTA is written
-  if (tid == 0) {
-    __threadfence();
-    unsigned int last = 0u;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (k < n_units && atomicAdd(&a.counters[units[k].unit], 1u) ==
-                             static_cast<unsigned int>(units[k].n - 1)) {
-        a.counters[units[k].unit] = 0u;   // ready for the next launch
-        last |= 1u << k;
-      }
-    __threadfence();
-    s_last = last;
+  if (tid < 32) {    // a lane per unit
+    bool mine = false;
+    if (tid < n_units) {
+      const int unit = tid == 0 ? units[0].unit : units[1].unit;
+      const int n = tid == 0 ? units[0].n : units[1].n;
+      __threadfence();
+      mine = atomicAdd(&a.counters[unit], 1u) == static_cast<unsigned int>(n - 1);
+      if (mine) a.counters[unit] = 0u;   // ready for the next launch
+      __threadfence();
+    }
+    const unsigned int last = __ballot_sync(0xffffffffu, mine);
+    if (tid == 0) s_last = last;
   }
   __syncthreads();
   const unsigned int last = s_last;
@@ -887,11 +887,12 @@ __global__ void __launch_bounds__(kNW * 32, kDenseCtasPerSm)
     if (at.s0 < at.s1) load_q<D, TERMS>(a, at.b, at.g, qx);
   }
   __syncthreads();
-  if (tid == 0) {
-    int m = 0;
-    for (int i = 0; i < 2 * kNW; ++i)
-      if (s_unit[i] >= 0) s_list[m++] = i;
-    s_nlist = m;
+  static_assert(2 * kNW <= 32, "a lane per slot");
+  if (warp == 0) {   // the slots in use, in order
+    const bool used = lane < 2 * kNW && s_unit[lane] >= 0;
+    const unsigned int m = __ballot_sync(0xffffffffu, used);
+    if (used) s_list[__popc(m & ((1u << lane) - 1u))] = lane;
+    if (lane == 0) s_nlist = __popc(m);
   }
   __syncthreads();
   const int nlist = s_nlist;
