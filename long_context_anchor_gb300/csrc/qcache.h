@@ -37,6 +37,7 @@ struct QDecodeArgs {
   float* part;                // split partials
   unsigned int* counters;     // [B*Hkv] split arrival counters (self-resetting)
   unsigned int* err;
+  int firsts_global;          // dense: where a warp's first piece waits (see there)
   int fill_tail;              // scores behind a sequence's last key become -inf
   int B, Hq, Hkv, G, N;
   int bs_shift, num_blocks, max_blocks;
@@ -56,7 +57,10 @@ struct QDecodeArgs {
 constexpr int qpart_head(int G) { return (2 * G + 3) & ~3; }
 constexpr size_t qpart_floats(int G, int d) { return qpart_head(G) + static_cast<size_t>(G) * d; }
 constexpr size_t qalign16(size_t x) { return (x + 15) & ~size_t(15); }
-constexpr int kQMaxCtas = 1024;   // CTAs of one attention launch at most
+constexpr int kQMaxCtas = 256;   // CTAs of one dense launch at most (one per SM)
+// Pieces that QDecodeArgs::part holds: two per dense CTA and one per warp of it,
+// or one per reuse CTA.
+constexpr int kQPieces = kQMaxCtas * (2 + 16);
 
 cudaError_t launch_qdecode_dense(const QDecodeArgs& a, int head_dim, int dtype, cudaStream_t st);
 cudaError_t launch_qdecode_reuse(const QDecodeArgs& a, int head_dim, int dtype, cudaStream_t st);

@@ -65,7 +65,7 @@ QLayout qlayout(const Shape& s, int topk) {
   L.counters = sizeof(WsHeader);
   size_t off = kWsStateBytes;
   L.part = off;
-  off = align256(off + 2 * static_cast<size_t>(kQMaxCtas) * qpart_floats(s.G, s.d) * 4);
+  off = align256(off + static_cast<size_t>(kQPieces) * qpart_floats(s.G, s.d) * 4);
   if (topk >= 1) {
     L.spill = off;
     off = align256(off + static_cast<size_t>(s.B) * s.Hq * s.N * 4);

@@ -665,14 +665,18 @@ __global__ void __launch_bounds__(kNW * 32, kDenseCtasPerSm)
   __shared__ int s_unit[2 * kNW], s_list[2 * kNW], s_nlist;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, c4 = lane & 3;
   const int pf = static_cast<int>(qpart_floats(a.G, D));
-  // a ring per warp, which at the end holds the warp's last piece; a place for
-  // its first piece; steps before every sequence, per head
+  // a ring per warp, which at the end holds the warp's last piece; places before
+  // every sequence in the line, per head; room for the warps' first pieces (in
+  // global memory, behind the CTAs' pieces, where a batch's places take it)
   uint8_t* ring = smem + warp * kDenseStages * kStageBytes;
-  float* firsts = reinterpret_cast<float*>(smem + kNW * kDenseStages * kStageBytes);   // [kNW][pf]
-  int* pref = reinterpret_cast<int*>(firsts + kNW * pf);                               // [B + 1]
+  int* pref = reinterpret_cast<int*>(smem + kNW * kDenseStages * kStageBytes);   // [B + 1]
+  float* firsts = a.firsts_global
+                      ? a.part + (2 * static_cast<size_t>(gridDim.x) + blockIdx.x * kNW) * pf
+                      : reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(pref) +
+                                                 qalign16((static_cast<size_t>(a.B) + 1) * 4));
   auto slot_at = [&](int i) -> float* {   // slot 2w: warp w's first piece, 2w + 1: its last
     return (i & 1) ? reinterpret_cast<float*>(smem + (i >> 1) * kDenseStages * kStageBytes)
-                   : firsts + (i >> 1) * pf;
+                   : firsts + static_cast<size_t>(i >> 1) * pf;
   };
 
   if (lane == 0)
@@ -887,7 +891,7 @@ __global__ void __launch_bounds__(kNW * 32, kDenseCtasPerSm)
     if (at.s0 < at.s1) load_q<D, TERMS>(a, at.b, at.g, qx);
   }
   __syncthreads();
-  static_assert(2 * kNW <= 32, "a lane per slot");
+  static_assert(2 * kNW <= 32 && kNW + 2 <= kQPieces / kQMaxCtas, "a lane per slot, pieces per CTA");
   if (warp == 0) {   // the slots in use, in order
     const bool used = lane < 2 * kNW && s_unit[lane] >= 0;
     const unsigned int m = __ballot_sync(0xffffffffu, used);
@@ -1248,23 +1252,29 @@ cudaError_t resident_ctas(size_t smem, int threads, int& ctas) {
     smem_of = smem;
   }
   if (slots < 1) return cudaErrorNotSupported;
-  ctas = slots < kQMaxCtas ? slots : kQMaxCtas;
+  ctas = slots;
   return cudaSuccess;
 }
 
 template <int D, int TERMS, bool SCORES>
 cudaError_t launch_dense_t(const QDecodeArgs& a, cudaStream_t st) {
-  // rings (at the end the scratch of the join between CTAs), first pieces, prefix
+  // rings (at the end the scratch of the join between CTAs), places, first
+  // pieces; the latter only up to what fits beside them at every batch size
+  // (16384 sequences: 64 KB of places)
   constexpr size_t kRing = kDenseStages * kStepOf<D> * qgroup_bytes(D), kRings = kNW * kRing;
   static_assert(kRings >= kNW * 32 * sizeof(Joined), "scratch of the join between CTAs");
   static_assert(kRing >= qpart_floats(8, D) * sizeof(float), "a warp's last piece in its ring");
-  const size_t smem = kRings + kNW * qpart_floats(a.G, D) * sizeof(float) +
-                      qalign16((static_cast<size_t>(a.B) + 1) * sizeof(int));
+  size_t smem = kRings + qalign16((static_cast<size_t>(a.B) + 1) * sizeof(int));
+  const size_t firsts = kNW * qpart_floats(a.G, D) * sizeof(float);
+  QDecodeArgs u = a;
+  u.firsts_global = smem + firsts > 224 * 1024 ? 1 : 0;
+  if (!u.firsts_global) smem += firsts;
   constexpr auto kern = k_qdecode_dense<D, TERMS, SCORES>;
   int ctas = 0;
   const cudaError_t e = resident_ctas<kern>(smem, kNW * 32, ctas);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(ctas), dim3(kNW * 32), smem, st, a);
+  if (ctas > kQMaxCtas) ctas = kQMaxCtas;
+  return launch_pdl(kern, dim3(ctas), dim3(kNW * 32), smem, st, u);
 }
 
 template <int D, int TERMS>
@@ -1291,6 +1301,7 @@ cudaError_t launch_reuse_t(const QDecodeArgs& a, cudaStream_t st) {
   int s = ctas / units;
   if (s > most) s = most;
   if (s > kMaxSplits) s = kMaxSplits;   // the last CTA joins that many pieces
+  if (s * units > kQPieces) s = 1;      // one piece needs no room
   u.S = s < 1 ? 1 : s;
   return launch_pdl(kern, dim3(u.S, units), dim3(kReuseNW * 32), smem, st, u);
 }

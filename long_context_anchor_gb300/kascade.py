@@ -221,11 +221,20 @@ class Workspace:
 _default_ws = {}
 
 
-def default_workspace(device) -> Workspace:
+def default_workspace(device, stream=None) -> Workspace:
+    """The workspace of calls that name none: one per device, and one more per
+    stream other than the device's default one for the cache calls (qcache_*),
+    so that those on two streams do not share one. stream: torch.cuda.Stream."""
     dev = torch.device(device)
-    key = dev.index if dev.index is not None else torch.cuda.current_device()
+    index = dev.index if dev.index is not None else torch.cuda.current_device()
+    raw = 0 if stream is None else stream.cuda_stream
+    return _workspace_of(index, raw)
+
+
+def _workspace_of(index, raw):
+    key = (index, raw) if raw else index
     if key not in _default_ws:
-        _default_ws[key] = Workspace(torch.device("cuda", key))
+        _default_ws[key] = Workspace(torch.device("cuda", index))
     return _default_ws[key]
 
 
@@ -646,9 +655,17 @@ def _cuda(t, name):
     return dev
 
 
-def _elsewhere(dev, stream):
-    """Whether a call has to switch to another device or stream first (_on)."""
-    return stream is not None or (dev.type == "cuda" and dev.index != torch._C._cuda_getDevice())
+# torch.cuda.current_device, current_stream and is_current_stream_capturing
+# without their wrapper objects (each costs a microsecond or two)
+_current_device = torch._C._cuda_getDevice
+_current_raw_stream = torch._C._cuda_getCurrentRawStream
+_capturing = torch._C._cuda_isCurrentStreamCapturing
+
+
+def _elsewhere(index, stream):
+    """Whether a call whose tensors are on CUDA device `index` (-1: not on one)
+    has to switch to another device or stream first (_on)."""
+    return stream is not None or (index >= 0 and index != _current_device())
 
 
 def _on(dev, stream):
@@ -664,26 +681,28 @@ def _on(dev, stream):
     return torch.cuda.stream(stream)
 
 
-def _raw_stream(dev):
-    return torch._C._cuda_getCurrentRawStream(dev.index) if dev.type == "cuda" else None
+def _raw_stream(index):
+    return _current_raw_stream(index) if index >= 0 else None
 
 
-def _qws(ws, dev, nbytes):
-    """The workspace buffer of a cache call. A captured call needs a workspace
+def _qws(ws, dev, index, nbytes):
+    """The workspace buffer of a cache call (by default the current stream's
+    own, default_workspace). A captured call needs a workspace
     of its own, large enough already: a graph keeps its address, so the
     shared default one (which grows) or one grown inside the capture would be
     gone when the graph is replayed."""
-    if dev.type == "cuda" and torch._C._cuda_isCurrentStreamCapturing():
+    if index >= 0 and _capturing():
         if ws is None or ws.buf is None or ws.buf.numel() < nbytes:
             raise ValueError("a captured call needs ws=Workspace(device), sized before the capture "
                              "(run the call once with it)")
         ws.captured = True
     if ws is None:
-        ws = _default_ws.get(dev.index) or default_workspace(dev)
+        raw = _current_raw_stream(index)
+        ws = _default_ws.get((index, raw) if raw else index) or _workspace_of(index, raw)
     buf = ws.buf
     if buf is None or buf.numel() < nbytes:
         buf = ws.get(nbytes)
-    if buf.device != dev:
+    if buf.get_device() != index:
         raise ValueError("ws: on %s, expected %s" % (buf.device, dev))
     return buf
 
@@ -749,7 +768,8 @@ def qcache_plan(kv_lens, new_lens, block_table, free_blocks, free_count, block_s
         _fits(free_count_out, "free_count_out", (1,), i32, dev)
     max_new = int(max_new)
     geo = _qgeo(int(block_size), free_blocks.shape[0], width, 0.0, 0.0)
-    if _elsewhere(dev, stream):
+    index = block_table.get_device()
+    if _elsewhere(index, stream):
         with _on(dev, stream):
             return qcache_plan(kv_lens, new_lens, block_table, free_blocks, free_count, block_size,
                                max_new, kv_lens_out, free_count_out, ws)
@@ -757,12 +777,12 @@ def qcache_plan(kv_lens, new_lens, block_table, free_blocks, free_count, block_s
         torch.empty(max_new + 2 * B + 2, dtype=i32, device=dev), (max_new, B + 1, B, 1))
     lens = lens if kv_lens_out is None else kv_lens_out
     count = count if free_count_out is None else free_count_out
-    buf = _qws(ws, dev, 256)
+    buf = _qws(ws, dev, index, 256)
     _check(_lib.kascade_qcache_plan(geo, B, kv_lens.data_ptr(), new_lens.data_ptr(),
                                     block_table.data_ptr(), free_blocks.data_ptr(),
                                     free_count.data_ptr(), lens.data_ptr(), count.data_ptr(),
                                     cu.data_ptr(), slots.data_ptr(), max_new, buf.data_ptr(),
-                                    buf.numel(), _raw_stream(dev)), "kascade_qcache_plan")
+                                    buf.numel(), _raw_stream(index)), "kascade_qcache_plan")
     return slots, cu, lens, count
 
 
@@ -810,14 +830,15 @@ def qcache_append(k, v, slot_map, pages, k_scale=1.0, v_scale=1.0, ws=None, stre
     kt, kh = _row_strides(k, "k", (T, hkv, d), k.dtype, dev, unit)
     vt, vh = _row_strides(v, "v", (T, hkv, d), k.dtype, dev, unit)
     geo = _qgeo(bs, nb, 1, float(k_scale), float(v_scale))
-    if _elsewhere(dev, stream):
+    index = pages.get_device()
+    if _elsewhere(index, stream):
         with _on(dev, stream):
             return qcache_append(k, v, slot_map, pages, k_scale, v_scale, ws)
-    buf = _qws(ws, dev, 256)
+    buf = _qws(ws, dev, index, 256)
     _check(_lib.kascade_qcache_append(geo, hkv, d, code, k.data_ptr(), v.data_ptr(),
                                       _I64x4(kt, kh, vt, vh),
                                       slot_map.data_ptr(), T, pages.data_ptr(),
-                                      buf.data_ptr(), buf.numel(), _raw_stream(dev)),
+                                      buf.data_ptr(), buf.numel(), _raw_stream(index)),
            "kascade_qcache_append")
     return pages
 
@@ -848,16 +869,17 @@ def qcache_read(pages, slot_map, dtype=torch.bfloat16, k_scale=1.0, v_scale=1.0,
         if T and any(n > 1 and st == 0 for st, n in zip(strides, (T, hkv, T, hkv))):
             raise ValueError("k, v: output rows must not overlap")
     geo = _qgeo(bs, nb, 1, float(k_scale), float(v_scale))
-    if _elsewhere(dev, stream):
+    index = pages.get_device()
+    if _elsewhere(index, stream):
         with _on(dev, stream):
             return qcache_read(pages, slot_map, dtype, k_scale, v_scale, k, v, ws)
     ok = torch.empty(shape, dtype=dtype, device=dev) if k is None else k
     ov = torch.empty(shape, dtype=dtype, device=dev) if v is None else v
-    buf = _qws(ws, dev, 256)
+    buf = _qws(ws, dev, index, 256)
     _check(_lib.kascade_qcache_read(geo, hkv, d, code, pages.data_ptr(), slot_map.data_ptr(),
                                     T, ok.data_ptr(), ov.data_ptr(),
                                     _I64x4(*strides), buf.data_ptr(),
-                                    buf.numel(), _raw_stream(dev)), "kascade_qcache_read")
+                                    buf.numel(), _raw_stream(index)), "kascade_qcache_read")
     return ok, ov
 
 
@@ -908,19 +930,20 @@ def qcache_dense_decode(q, pages, block_table, kv_lens, kv_len=None, group_map=N
     desc, geo, nbytes, (B, Hq, _, N), dev = _qattn(q, pages, block_table, kv_lens, kv_len,
                                                    group_map, scale, k_scale, v_scale, False, 0,
                                                    out)
-    if _elsewhere(dev, stream):
+    index = pages.get_device()
+    if _elsewhere(index, stream):
         with _on(dev, stream):
             return qcache_dense_decode(q, pages, block_table, kv_lens, kv_len, group_map, scale,
                                        k_scale, v_scale, return_scores, out, ws)
     o = torch.empty_like(q) if out is None else out
     scores = (torch.empty(B, Hq, N, dtype=torch.float32, device=dev) if return_scores
               else None)
-    buf = _qws(ws, dev, nbytes)
+    buf = _qws(ws, dev, index, nbytes)
     _check(_lib.kascade_qcache_dense_decode(desc, geo, q.data_ptr(), pages.data_ptr(),
                                             block_table.data_ptr(), kv_lens.data_ptr(),
                                             o.data_ptr(),
                                             scores.data_ptr() if return_scores else None,
-                                            buf.data_ptr(), buf.numel(), _raw_stream(dev)),
+                                            buf.data_ptr(), buf.numel(), _raw_stream(index)),
            "kascade_qcache_dense_decode")
     return (o, scores) if return_scores else o
 
@@ -938,7 +961,8 @@ def qcache_anchor_decode(q, pages, block_table, kv_lens, topk, kv_len=None, grou
     H = hkv if pooled else Hq
     if idx is not None:
         _fits(idx, "idx", (B, H, topk), torch.int32, dev)
-    if _elsewhere(dev, stream):
+    index = pages.get_device()
+    if _elsewhere(index, stream):
         with _on(dev, stream):
             return qcache_anchor_decode(q, pages, block_table, kv_lens, topk, kv_len, group_map, scale,
                                         k_scale, v_scale, return_scores, out, idx, ws,
@@ -946,12 +970,12 @@ def qcache_anchor_decode(q, pages, block_table, kv_lens, topk, kv_len=None, grou
     o = torch.empty_like(q) if out is None else out
     ix = torch.empty(B, H, topk, dtype=torch.int32, device=dev) if idx is None else idx
     scores = torch.empty(B, H, N, dtype=torch.float32, device=dev) if return_scores else None
-    buf = _qws(ws, dev, nbytes)
+    buf = _qws(ws, dev, index, nbytes)
     _check(_lib.kascade_qcache_anchor_decode(desc, geo, q.data_ptr(), pages.data_ptr(),
                                              block_table.data_ptr(), kv_lens.data_ptr(), topk,
                                              o.data_ptr(), ix.data_ptr(),
                                              scores.data_ptr() if return_scores else None,
-                                             buf.data_ptr(), buf.numel(), _raw_stream(dev)),
+                                             buf.data_ptr(), buf.numel(), _raw_stream(index)),
            "kascade_qcache_anchor_decode")
     return (o, ix, scores) if return_scores else (o, ix)
 
@@ -968,16 +992,17 @@ def qcache_reuse_decode(q, pages, block_table, kv_lens, idx, kv_len=None, group_
                                                      group_map, scale, k_scale, v_scale, pooled,
                                                      max(topk, 1), out)
     _fits(idx, "idx", (B, hkv if pooled else Hq, topk), torch.int32, dev)
-    if _elsewhere(dev, stream):
+    index = pages.get_device()
+    if _elsewhere(index, stream):
         with _on(dev, stream):
             return qcache_reuse_decode(q, pages, block_table, kv_lens, idx, kv_len, group_map, scale,
                                        k_scale, v_scale, out, ws, pooled=pooled)
     o = torch.empty_like(q) if out is None else out
-    buf = _qws(ws, dev, nbytes)
+    buf = _qws(ws, dev, index, nbytes)
     _check(_lib.kascade_qcache_reuse_decode(desc, geo, q.data_ptr(), pages.data_ptr(),
                                             block_table.data_ptr(), kv_lens.data_ptr(), topk,
                                             idx.data_ptr(), o.data_ptr(), buf.data_ptr(),
-                                            buf.numel(), _raw_stream(dev)),
+                                            buf.numel(), _raw_stream(index)),
            "kascade_qcache_reuse_decode")
     return o
 
@@ -1031,7 +1056,8 @@ def qcache_run_stack(qs, pages, block_table, kv_lens, topk, anchors, new_ks=None
         _all_like(outs, "outs", qs[0].shape, qs[0].dtype, dev)
     if idx_buf is not None:
         _fits(idx_buf, "idx_buf", (B, H, max(topk, 1)), torch.int32, dev)
-    if _elsewhere(dev, stream):
+    index = qs[0].get_device()
+    if _elsewhere(index, stream):
         with _on(dev, stream):
             return qcache_run_stack(qs, pages, block_table, kv_lens, topk, anchors, new_ks, new_vs,
                                     new_lens, free_blocks, free_count, slot_map, cu_new, kv_len,
@@ -1047,7 +1073,7 @@ def qcache_run_stack(qs, pages, block_table, kv_lens, topk, anchors, new_ks=None
     addr = lambda t: None if t is None else t.data_ptr()
     step = QCacheStep(addr(block_table), addr(kv_lens), addr(new_lens), addr(free_blocks),
                       addr(free_count), addr(cu), addr(sm), T)
-    buf = _qws(ws, dev, nbytes)
+    buf = _qws(ws, dev, index, nbytes)
     arr = lambda ts: (ctypes.c_void_p * L)(*[t.data_ptr() for t in ts])
     an = (ctypes.c_int32 * max(1, len(anchors)))(*[int(a) for a in anchors])
     _check(_lib.kascade_qcache_run_stack(desc, geo, ctypes.byref(step), L, arr(qs),
@@ -1055,7 +1081,7 @@ def qcache_run_stack(qs, pages, block_table, kv_lens, topk, anchors, new_ks=None
                                          arr(new_vs) if new_vs is not None else None,
                                          arr(pages), topk, an, len(anchors), arr(os_),
                                          ib.data_ptr(), buf.data_ptr(), buf.numel(),
-                                         _raw_stream(dev)), "kascade_qcache_run_stack")
+                                         _raw_stream(index)), "kascade_qcache_run_stack")
     return os_, ib
 
 

@@ -733,6 +733,91 @@ def test_other_streams(K):
     assert all(torch.equal(x, want) for x in got)
 
 
+def test_streams_do_not_share_the_default_workspace(K):
+    rng = np.random.default_rng(25)
+    lens, d, bs = [6000, 100], 64, 32
+    pages, table = filled(K, rng, lens, 2, d, bs)
+    T, dl = ints(table), ints(lens)
+    qs = [torch.randn(2, 8, d, device="cuda").to(BF) for _ in range(3)]
+    want = [K.qcache_dense_decode(q, pages, T, dl) for q in qs]
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = [(i, K.qcache_dense_decode(qs[i], pages, T, dl, stream=streams[i]))
+           for _ in range(10) for i in range(3)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want[i]) for i, x in got)
+    bufs = {K.default_workspace("cuda", s).buf.data_ptr() for s in streams + [None]}
+    assert len(bufs) == 4
+    assert K.default_workspace("cuda", streams[0]).device_error(streams[0]) == K.OK
+
+
+@pytest.mark.parametrize("d,Hq", [(128, 8), (64, 2)])
+def test_largest_batch(K, d, Hq):
+    """16384 sequences, most of a few tokens, one long: the line's places fill
+    the shared memory beside the rings."""
+    B, bs = 16384, 16
+    rng = np.random.default_rng(d)
+    lens = rng.integers(0, 4, B)
+    lens[rng.choice(B, 40, replace=False)] = rng.integers(0, 300, 40)
+    lens[77] = 5000
+    pages, table = filled(K, rng, lens.tolist(), 1, d, bs)
+    q = torch.from_numpy(rng.standard_normal((B, Hq, d))).to(BF).cuda()
+    out = K.qcache_dense_decode(q, pages, ints(table), ints(lens), kv_len=5000)
+    assert not out[torch.from_numpy(lens == 0).cuda()].any()
+    pick = np.concatenate([np.nonzero(lens > 3)[0], rng.choice(B, 200, replace=False)])
+    check_attention(q[pick], out[pick], pages, table[pick], lens[pick].tolist(), 1, d, [0] * Hq,
+                    max_units=400)
+
+
+def test_captured_steps_of_the_stack(K):
+    """A step with its plan captured once: every replay takes the state the one
+    before left, as eager steps on a copy do."""
+    rng = np.random.default_rng(31)
+    B, Hq, Hkv, d, bs, width, nb, L, k = 4, 8, 2, 128, 16, 8, 36, 3, 12
+    pages = [K.qcache_alloc(nb, Hkv, d, bs) for _ in range(L)]
+    state = dict(block_table=torch.full((B, width), -1, dtype=I32, device="cuda"),
+                 kv_lens=torch.zeros(B, dtype=I32, device="cuda"),
+                 free_blocks=ints(rng.permutation(nb)), free_count=ints([nb]))
+    copy = {n: t.clone() for n, t in state.items()}
+    pages2 = [p.clone() for p in pages]
+    new = ints([1] * B)
+    qs = [torch.randn(B, Hq, d, device="cuda").to(BF) for _ in range(L)]
+    nk = [torch.randn(B, Hkv, d, device="cuda").to(BF) for _ in range(L)]
+    nv = [torch.randn(B, Hkv, d, device="cuda").to(BF) for _ in range(L)]
+    outs, idx = [torch.empty_like(q) for q in qs], torch.empty(B, Hq, k, dtype=I32, device="cuda")
+    slots, cu = torch.empty(B, dtype=I32, device="cuda"), torch.empty(B + 1, dtype=I32, device="cuda")
+    ws, eager = K.Workspace(), K.Workspace()
+
+    def step(st, pg, w, **kw):
+        return K.qcache_run_stack(qs, pg, st["block_table"], st["kv_lens"], k, [1], new_ks=nk,
+                                  new_vs=nv, new_lens=new, free_blocks=st["free_blocks"],
+                                  free_count=st["free_count"], ws=w, **kw)
+
+    step({n: t.clone() for n, t in state.items()}, [p.clone() for p in pages], ws)   # sizes ws
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(state, pages, ws, outs=outs, idx_buf=idx, slot_map=slots, cu_new=cu)
+    grow = [[1, 1, 1, 1]] * 20 + [[40, 0, 1, 3], [-9, 1, -99, 1], [1, 1, 1, 0]]
+    for n in grow:
+        new.copy_(ints(n))
+        for t in qs + nk + nv:
+            t.copy_(torch.randn_like(t.float()).to(BF))
+        if sum(max(0, x) for x in n) > B:       # more rows than the step has: refused
+            before = state["kv_lens"].clone()
+            g.replay()
+            torch.cuda.synchronize()
+            assert ws.device_error() == K.BAD_INPUT and torch.equal(state["kv_lens"], before)
+            continue
+        g.replay()
+        want, wi = step(copy, pages2, eager)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(outs, want)) and torch.equal(idx, wi)
+        assert all(torch.equal(state[x], copy[x]) for x in state)
+        assert all(torch.equal(a, b) for a, b in zip(pages, pages2))
+    assert ws.device_error() == K.OK and eager.device_error() == K.OK
+
+
 def test_workspace_shared_with_other_calls(K):
     """One workspace, calls of many shapes and of the other entry points in turn."""
     rng = np.random.default_rng(16)
