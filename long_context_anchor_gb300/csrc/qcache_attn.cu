@@ -603,8 +603,8 @@ __device__ __forceinline__ int len_of(const QDecodeArgs& a, int b, bool report) 
 // line, and every warp of the grid takes an equal run of it, so that ragged
 // batches balance. A unit starts with kUnitCost places without a step: what
 // its query, its first loads and its output cost a warp, so that runs of many
-// short units do not come last (48 sequences of 0 to 16001 keys: 84 us
-// without, 75 us with). A run may span units: the warp's pieces of units it does
+// short units do not come last (48 sequences of 0 to 16001 keys: 82 us without,
+// 72 with one place, 66 with two, 67 with four). A run may span units: the warp's pieces of units it does
 // not hold alone go to shared memory, the CTA joins those of its warps after
 // one barrier, and a unit that several CTAs share is joined by the last of
 // them to arrive.
@@ -620,7 +620,7 @@ constexpr int kNW = 16, kDenseCtasPerSm = 1;
 constexpr int kMinRun = 2;        // steps per warp at least
 constexpr int kDenseStages = 2;
 
-constexpr int kUnitCost = 1;
+constexpr int kUnitCost = 2;
 
 // The part of a run that lies in the unit at place f of the line: steps [s0, s1)
 // of its ns (none, if the run has only the unit's first place), and the place
