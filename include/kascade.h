@@ -334,8 +334,12 @@ kascade_status kascade_run_stack_profiled(const kascade_desc* desc, int32_t mode
  * appended rows (bf16, or fp32 computed to fp32 accuracy). A length out of
  * range, or a block id outside [0, num_blocks), sets KASCADE_ERR_BAD_INPUT on the device;
  * those keys are not read and count as masked.
- * Limits beyond the descriptor's: num_blocks*block_size < 2^31,
- * B*max_blocks < 2^31 (KASCADE_ERR_UNSUPPORTED). */
+ * A sequence's keys are split over CTAs by rules that look at the whole batch,
+ * so the last bits of its output may differ between batches; one call repeated
+ * gives the same bits.
+ * Limits beyond the descriptor's: num_blocks*block_size < 2^31, B*max_blocks
+ * < 2^31, fewer than 2^28 new tokens in a call and, for attention,
+ * num_blocks*Hkv*block_size/16 < 2^28 - 1 (KASCADE_ERR_UNSUPPORTED). */
 typedef struct {
   int32_t block_size;   /* 16, 32, 64, 128 or 256 tokens */
   int32_t num_blocks;   /* blocks of the cache */
@@ -358,7 +362,10 @@ size_t kascade_qcache_workspace_size(const kascade_desc* desc, const kascade_qca
  * to append), shrinks (tokens taken back) or, with -L or less, ends. It then
  * holds ceil(L'/block_size) blocks: those it gives back are pushed on the
  * stack free_blocks [num_blocks] (free_count of them valid) in (sequence,
- * column) order, then those it takes are popped from it in that order. Writes
+ * column) order, then those it takes are popped from it in that order. A block
+ * is in one place, one sequence's part of the table or the stack: blocks that
+ * sequences share are read correctly, but each of them would give it back.
+ * Writes
  *   block_table     the entries of taken blocks (others are left as they are);
  *   kv_lens_out [B], free_count_out [1]   (may be kv_lens and free_count);
  *   cu_new [B+1]    running number of new tokens: sequence b's rows of this

@@ -236,6 +236,9 @@ kascade_status run_qreuse(const QCall& k, const void* q, const void* cache, cons
   return status_of(launch_qdecode_reuse(a, k.s.d, k.s.dtype, st));
 }
 
+// New tokens of one call: their 16-element pieces are numbered in 32 bits.
+constexpr int kMaxNewTokens = (1 << 28) - 1;
+
 // Rows of new keys and values.
 kascade_status check_rows(const kascade_qcache* cache, int n_kv_heads, int head_dim, int dtype,
                           const void* k, const void* v, const int64_t* strides,
@@ -247,6 +250,7 @@ kascade_status check_rows(const kascade_qcache* cache, int n_kv_heads, int head_
   if (n_kv_heads < 1 || n_kv_heads > kMaxQHeads || n_tokens < 0 || strides == nullptr)
     return KASCADE_ERR_INVALID_ARG;
   if (head_dim != 64 && head_dim != 128) return KASCADE_ERR_UNSUPPORTED;
+  if (n_tokens > kMaxNewTokens) return KASCADE_ERR_UNSUPPORTED;
   if (n_tokens == 0) return KASCADE_OK;
   if (!aligned(k, 16) || !aligned(v, 16) || !aligned(slot_map, 4) || !aligned(pages, 16))
     return KASCADE_ERR_INVALID_ARG;
@@ -307,7 +311,8 @@ kascade_status check_plan(const kascade_qcache* cache, int n_seqs, const int32_t
   kascade_status r = check_qcache(cache, c);
   if (r != KASCADE_OK) return r;
   if (n_seqs < 1 || max_new < 0) return KASCADE_ERR_INVALID_ARG;
-  if (n_seqs > kMaxCounterUnits || static_cast<long long>(n_seqs) * c.max_blocks >= (1ll << 31) ||
+  if (n_seqs > kMaxCounterUnits || max_new > kMaxNewTokens ||
+      static_cast<long long>(n_seqs) * c.max_blocks >= (1ll << 31) ||
       static_cast<long long>(c.max_blocks) * c.block_size >= (1ll << 31))
     return KASCADE_ERR_UNSUPPORTED;
   const void* need[] = {kv_lens, new_lens, block_table, free_blocks, free_count,

@@ -204,6 +204,26 @@ def _state(B=3, Hq=8, Hkv=2, d=128, bs=32, nb=20, width=5, dtype=BF):
                 table=torch.zeros(B, width, dtype=I32), lens=torch.zeros(B, dtype=I32))
 
 
+def test_refused_sizes(K):
+    """Sizes whose numbering would leave 32 bits (pieces of new rows, groups of the cache)."""
+    L, ref, p = K._lib, ctypes.byref, ctypes.c_void_p(1 << 20)
+    g = ref(K.QCache(64, 40, 16, 0.0, 0.0))
+    st = (ctypes.c_int64 * 4)(0, 0, 0, 0)
+    for n in (1 << 28, (1 << 31) - 1):
+        assert L.kascade_qcache_append(g, 2, 128, K.BF16, p, p, st, p, n, p, p, 256,
+                                       None) == K.UNSUPPORTED
+        assert L.kascade_qcache_read(g, 2, 64, K.F32, p, p, n, p, p, st, p, 256,
+                                     None) == K.UNSUPPORTED
+        assert L.kascade_qcache_plan(g, 2, p, p, p, p, p, p, p, p, p, n, p, 256,
+                                     None) == K.UNSUPPORTED
+    desc = K.make_desc(1, 64, 64, 128, 1000, K.BF16)
+    most = ((1 << 28) - 2) // 64
+    size = L.kascade_qcache_workspace_size
+    assert size(ref(desc), ref(K.QCache(16, most, 63, 0.0, 0.0)), 0) > 0
+    assert size(ref(desc), ref(K.QCache(16, most + 1, 63, 0.0, 0.0)), 0) == 0
+
+
+
 def test_documented_calls_pass(K, fake):
     ws = K.Workspace("cpu")
     s = _state()
