@@ -750,18 +750,31 @@ def qcache_plan(kv_lens, new_lens, block_table, free_blocks, free_count, block_s
     free_blocks are updated in place. Returns (slot_map [max_new], cu_new
     [B+1], kv_lens_out [B], free_count_out [1]), all int32; the last two may
     be given (kv_lens and free_count themselves included)."""
-    dev = _cuda(block_table, "block_table")
-    if block_table.dim() != 2:
-        raise ValueError("block_table: expected an int32 tensor [B, max_blocks]")
-    if not isinstance(free_blocks, torch.Tensor) or free_blocks.dim() != 1:
-        raise ValueError("free_blocks: expected an int32 tensor [num_blocks]")
-    B, width = block_table.shape
     i32 = torch.int32
-    _fits(block_table, "block_table", (B, width), i32, dev)
-    _fits(kv_lens, "kv_lens", (B,), i32, dev)
-    _fits(new_lens, "new_lens", (B,), i32, dev)
-    _fits(free_blocks, "free_blocks", free_blocks.shape, i32, dev)
-    _fits(free_count, "free_count", (1,), i32, dev)
+    if not (isinstance(block_table, torch.Tensor) and isinstance(kv_lens, torch.Tensor)
+            and isinstance(new_lens, torch.Tensor) and isinstance(free_blocks, torch.Tensor)
+            and isinstance(free_count, torch.Tensor) and block_table.dim() == 2
+            and free_blocks.dim() == 1 and block_table.dtype is i32 and kv_lens.dtype is i32
+            and new_lens.dtype is i32 and free_blocks.dtype is i32 and free_count.dtype is i32
+            and kv_lens.shape == block_table.shape[:1] and new_lens.shape == kv_lens.shape
+            and free_count.shape == (1,) and block_table.is_contiguous()
+            and kv_lens.is_contiguous() and new_lens.is_contiguous()
+            and free_blocks.is_contiguous() and block_table.device.type == _DEVICE_TYPE
+            and kv_lens.device == block_table.device and new_lens.device == block_table.device
+            and free_blocks.device == block_table.device
+            and free_count.device == block_table.device):
+        dev = _cuda(block_table, "block_table")      # what is wrong, in words
+        if block_table.dim() != 2:
+            raise ValueError("block_table: expected an int32 tensor [B, max_blocks]")
+        if not isinstance(free_blocks, torch.Tensor) or free_blocks.dim() != 1:
+            raise ValueError("free_blocks: expected an int32 tensor [num_blocks]")
+        _fits(block_table, "block_table", block_table.shape, i32, dev)
+        _fits(kv_lens, "kv_lens", block_table.shape[:1], i32, dev)
+        _fits(new_lens, "new_lens", block_table.shape[:1], i32, dev)
+        _fits(free_blocks, "free_blocks", free_blocks.shape, i32, dev)
+        _fits(free_count, "free_count", (1,), i32, dev)
+    dev = block_table.device
+    B, width = block_table.shape
     if kv_lens_out is not None:
         _fits(kv_lens_out, "kv_lens_out", (B,), i32, dev)
     if free_count_out is not None:
