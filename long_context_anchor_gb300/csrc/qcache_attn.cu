@@ -220,8 +220,9 @@ __device__ __forceinline__ void slice_products(const uint8_t* grp, const LanePla
   for (int r = 0; r < 2; ++r) {
     load_words(grp + at.k + 8 * r * (D / 2), k[r]);
     const uint8_t* p = grp + at.ks + 8 * r * (D / 16);
-    const uint32_t h = cvt_e4m3x2(D == 128 ? static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p))
-                                           : static_cast<uint32_t>(*p));
+    const uint32_t h =
+        cvt_e4m3x2(D == 128 ? static_cast<uint32_t>(*reinterpret_cast<const uint16_t*>(p))
+                            : static_cast<uint32_t>(*p));
     sc[r][0] = __byte_perm(h, h, 0x1010);
     if (D == 128) sc[r][D / 64 - 1] = __byte_perm(h, h, 0x3232);
   }
@@ -251,8 +252,7 @@ __device__ __forceinline__ void slice_products(const uint8_t* grp, const LanePla
 // (gid = lane/4, c4 = lane%4) owns heads 2 c4, 2 c4 + 1 and output dims
 // gid * D/8 .. + D/8 of both: o[i] = (dim 2i, head 2c4), (2i, 2c4+1),
 // (2i + 1, 2c4), (2i + 1, 2c4 + 1). m: running maxima (log2 units, within kSlack);
-// nmu = 14 - m;
-// l: this lane's sums of 2^14 p. nmu and l hold both heads, packed.
+// nmu = 14 - m; l: this lane's sums of 2^14 p. nmu and l hold both heads, packed.
 template <int D>
 struct QState {
   float m[2];
@@ -604,10 +604,10 @@ __device__ __forceinline__ int len_of(const QDecodeArgs& a, int b, bool report) 
 // batches balance. A unit starts with kUnitCost places without a step: what
 // its query, its first loads and its output cost a warp, so that runs of many
 // short units do not come last (48 sequences of 0 to 16001 keys: 82 us without,
-// 72 with one place, 66 with two, 67 with four). A run may span units: the warp's pieces of units it does
-// not hold alone go to shared memory, the CTA joins those of its warps after
-// one barrier, and a unit that several CTAs share is joined by the last of
-// them to arrive.
+// 72 with one place, 66 with two, 67 with four). A run may span units: the
+// warp's pieces of units it does not hold alone go to shared memory, the CTA
+// joins those of its warps after one barrier, and a unit that several CTAs
+// share is joined by the last of them to arrive.
 //
 // Every warp feeds itself: a ring of kDenseStages stages of one step, each
 // filled by one bulk copy per block that the step touches (groups of a block
@@ -615,7 +615,13 @@ __device__ __forceinline__ int len_of(const QDecodeArgs& a, int b, bool report) 
 // the stage; no warp waits for another one before the end.
 // One CTA of 16 warps per SM: on a GB300 the 8B shape takes 65.5 us so, 67.3 as
 // two CTAs of 8 and 69.2 as four of 4 (the joins get longer); five of 4, with
-// 102 registers per thread, 95.
+// 102 registers per thread, 95; three stages per ring change nothing.
+// What bounds it: 8 sequences of 32768 keys, 8 KV heads of 4 query heads, d 128,
+// are 302 MB in 63.5 us = 4.8 TB/s (0.70 of the copy rate). A copy of the kernel
+// that moved the bytes and computed nothing took 57.7 us, about 5 of them
+// before the first step and 8 while the last CTAs finish; the arithmetic issues
+// 333 instructions per 16 keys (16 HMMA of 8 cycles, 64 conversions of code pairs
+// on the half-rate ALU) and keeps the issue slots 61% busy meanwhile.
 constexpr int kNW = 16, kDenseCtasPerSm = 1;
 constexpr int kMinRun = 2;        // steps per warp at least
 constexpr int kDenseStages = 2;
@@ -982,8 +988,11 @@ __global__ void __launch_bounds__(256) k_qfill_tail(float* __restrict__ rows,
 // read), so that the arithmetic is the dense kernel's. Entries are loaded two
 // steps before their copies and block ids one step before, so that no copy
 // waits for either.
-// (Four CTAs per SM, 128 registers per thread, took 52.0 us on the 8B shape, three
-// 49.3; one or two larger CTAs per SM 56.8 and 55.6.)
+// Four CTAs per SM, 128 registers per thread, took 52.0 us on the 8B shape (with
+// the plan), three 49.3; one or two larger CTAs per SM 56.8 and 55.6.
+// What bounds it: scattered rows. DRAM delivers 64 bytes for each 64-byte row of
+// codes and as many for its 8 bytes of scales: 8B shape, 4096 of 32768 keys per
+// head, 37.5 us from cold caches for 127 MB of useful bytes (3.4 TB/s).
 constexpr int kReuseNW = 4, kReuseStages = 2, kReuseCtasPerSm = 3;
 // A row in one word: the group's number in the cache and the row in it.
 constexpr uint32_t kNoRow = 0xffffffffu;

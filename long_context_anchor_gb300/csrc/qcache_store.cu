@@ -36,10 +36,10 @@ namespace {
 // steps run in one CTA and one launch; larger ones in two launches of many
 // CTAs, checks first, each CTA scanning the lengths for itself.
 constexpr int kPlanThreads = 1024;
-// One launch up to this many blocks and new tokens (one round of the CTA's
-// threads or two): 1.1 us of 8 requests' step are saved by the second launch
-// not made, while 32768 moved blocks take one CTA 150 us and two launches of
-// 152 CTAs 14 us.
+// One launch up to this many blocks and new tokens. A step of 64 sequences,
+// half of them ending and half starting, all launches back to back on a GB300
+// (one CTA / two launches): 512 new tokens 5.1 / 8.0 us, 2048 6.6 / 7.5, 4096
+// 9.4 / 8.0, 32768 44 / 8.4.
 constexpr int kPlanOneCta = 2048;
 
 struct PlanScan {
@@ -273,8 +273,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_qplan(const __grid_constant__ 
 // One thread per 16 elements: thread i of (head, K or V) takes block i % (d / 16)
 // of token i / (d / 16), so that a warp writes neighbouring rows of one group
 // of the cache. Every element is read once and its 4.5 bits written once (or
-// the other way): bound by DRAM. 16384 tokens x 8 heads x 128 (105 MB either
-// way): 20 us to write, 19.5 us to read.
+// the other way): bound by DRAM. 16384 tokens x 8 heads x 128 in bf16 (86 MB
+// either way): 18.6 us to write, 18.7 us to read, 4.6 TB/s from cold caches.
 constexpr int kRowThreads = 256;
 
 __device__ __forceinline__ uint32_t e4m3_of(float x) {
