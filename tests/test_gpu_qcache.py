@@ -866,3 +866,13 @@ def test_offsets_beyond_32_bits(K):
         assert torch.equal(fn(pages, far), fn(small, near))
     out = K.qcache_dense_decode(q, small, near, ints([n]), kv_len=n)
     check_attention(q, out, small, [[0, 1, 2, 3]], [n], Hkv, d, [h // 4 for h in range(32)])
+
+
+@pytest.mark.parametrize("kind", ["plan", "append", "read", "dense", "anchor", "reuse"])
+def test_profiling_command(kind, monkeypatch, capsys):
+    from long_context_anchor_gb300 import runcase
+    argv = ["runcase", "qcache_" + kind, "--kv-len", "333", "--topk", "40", "--reps", "1",
+            "--block-size", "32"]
+    monkeypatch.setattr("sys.argv", argv)
+    runcase.main()
+    assert capsys.readouterr().out == "ok qcache_%s\n" % kind
