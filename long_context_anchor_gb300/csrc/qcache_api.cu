@@ -236,7 +236,7 @@ kascade_status run_qreuse(const QCall& k, const void* q, const void* cache, cons
   return status_of(launch_qdecode_reuse(a, k.s.d, k.s.dtype, st));
 }
 
-// New tokens of one call: their 16-element pieces are numbered in 32 bits.
+// New tokens of one call: grids and slots are numbered in 32 bits.
 constexpr int kMaxNewTokens = (1 << 28) - 1;
 
 // Rows of new keys and values.
