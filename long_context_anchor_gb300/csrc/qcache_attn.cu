@@ -756,13 +756,16 @@ __global__ void __launch_bounds__(kNW * 32, kDenseCtasPerSm)
     uint64_t* bar = &s_full[warp][in_stage];
     if (lane == 0) mbar_arrive_expect_tx(bar, __popc(got) * copy_bytes);
     __syncwarp();
-    if (ok)
-      bulk_load(ring + in_stage * kStageBytes + lane * copy_bytes,
-                in_base + static_cast<uint64_t>(static_cast<uint32_t>(id)) * block_bytes +
-                    ((static_cast<uint32_t>(in_key) >> 4) & gmask) * kGroupBytes,
-                copy_bytes, bar);
-    else if (want)
+    if (ok) {
+      uint8_t* dst = ring + in_stage * kStageBytes + lane * copy_bytes;
+      const uint8_t* src = in_base +
+                           static_cast<uint64_t>(static_cast<uint32_t>(id)) * block_bytes +
+                           ((static_cast<uint32_t>(in_key) >> 4) & gmask) * kGroupBytes;
+      if (SCORES) bulk_load(dst, src, copy_bytes, bar);
+      else bulk_load_once(dst, src, copy_bytes, bar);
+    } else if (want) {
       report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x522);
+    }
     have = __byte_perm(have, got, in_stage == 0 ? 0x3214 : 0x3240);
     in_stage ^= 1;
     ++pending;
