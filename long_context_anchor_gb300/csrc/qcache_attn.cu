@@ -498,6 +498,15 @@ __device__ __forceinline__ void joined_output(const QDecodeArgs& a, const Joined
   if (e4 == 0) write_row_stat(a, row, x.m, x.l);
 }
 
+// Adds 1: what the CTA wrote before its last barrier is seen by whoever arrives
+// later.
+__device__ __forceinline__ unsigned int arrive_acq_rel(unsigned int* counter) {
+  unsigned int old;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;"
+               : "=r"(old) : "l"(counter) : "memory");
+  return old;
+}
+
 // A unit shared by n CTAs: its first CTA's piece, and the others' from `rest` on.
 struct SharedUnit {
   int unit, b, g, n;
@@ -521,10 +530,8 @@ __device__ void arrive_and_join(const QDecodeArgs& a, int n_units, const SharedU
     if (tid < n_units) {
       const int unit = tid == 0 ? units[0].unit : units[1].unit;
       const int n = tid == 0 ? units[0].n : units[1].n;
-      __threadfence();
-      mine = atomicAdd(&a.counters[unit], 1u) == static_cast<unsigned int>(n - 1);
+      mine = arrive_acq_rel(&a.counters[unit]) == static_cast<unsigned int>(n - 1);
       if (mine) a.counters[unit] = 0u;   // ready for the next launch
-      __threadfence();
     }
     const unsigned int last = __ballot_sync(0xffffffffu, mine);
     if (tid == 0) s_last = last;
@@ -668,7 +675,7 @@ __global__ void __launch_bounds__(kNW * 32, kDenseCtasPerSm)
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ __align__(8) uint64_t s_full[kNW][kDenseStages];
   __shared__ int s_tot[kNW];
-  __shared__ int s_unit[2 * kNW], s_list[2 * kNW], s_nlist;
+  __shared__ int s_unit[2 * kNW], s_list[2 * kNW], s_start[2 * kNW + 1], s_nunits;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gid = lane >> 2, c4 = lane & 3;
   const int pf = static_cast<int>(qpart_floats(a.G, D));
   // a ring per warp, which at the end holds the warp's last piece; places before
@@ -900,15 +907,23 @@ __global__ void __launch_bounds__(kNW * 32, kDenseCtasPerSm)
     if (at.s0 < at.s1) load_q<D, TERMS>(a, at.b, at.g, qx);
   }
   __syncthreads();
-  static_assert(2 * kNW <= 32 && kNW + 2 <= kQPieces / kQMaxCtas, "a lane per slot, pieces per CTA");
-  if (warp == 0) {   // the slots in use, in order
-    const bool used = lane < 2 * kNW && s_unit[lane] >= 0;
-    const unsigned int m = __ballot_sync(0xffffffffu, used);
-    if (used) s_list[__popc(m & ((1u << lane) - 1u))] = lane;
-    if (lane == 0) s_nlist = __popc(m);
+  static_assert(2 * kNW == 32 && kNW + 2 <= kQPieces / kQMaxCtas,
+                "a lane per slot, pieces per CTA");
+  if (warp == 0) {   // the slots in use, in order, and where each unit's begin
+    const int unit = s_unit[lane];
+    const unsigned int m = __ballot_sync(0xffffffffu, unit >= 0), below = (1u << lane) - 1u;
+    const int before = __shfl_sync(0xffffffffu, unit, (31 - __clz(m & below)) & 31);
+    const bool first = unit >= 0 && ((m & below) == 0u || before != unit);
+    const unsigned int f = __ballot_sync(0xffffffffu, first);
+    if (unit >= 0) s_list[__popc(m & below)] = lane;
+    if (first) s_start[__popc(f & below)] = __popc(m & below);
+    if (lane == 0) {
+      s_nunits = __popc(f);
+      s_start[__popc(f)] = __popc(m);
+    }
   }
   __syncthreads();
-  const int nlist = s_nlist;
+  const int nunits = s_nunits;
   const int per_cta = per * kNW, c0 = static_cast<int>(blockIdx.x) * per_cta;
   // This CTA's pieces, in order of their units: a unit is joined here if the
   // CTA holds all of it, else its piece goes to CTA c's place 2c + 1 (a unit
@@ -917,10 +932,8 @@ __global__ void __launch_bounds__(kNW * 32, kDenseCtasPerSm)
   SharedUnit shared[2] = {};   // at most the first and the last unit of the run
   int n_shared = 0;
   const int elems = a.G * (D / 4);
-  for (int i = 0, first_elem = 0; i < nlist;) {
-    const int unit = s_unit[s_list[i]];
-    int j = i;
-    while (j < nlist && s_unit[s_list[j]] == unit) ++j;
+  for (int k = 0, first_elem = 0; k < nunits; ++k, first_elem += elems) {
+    const int i = s_start[k], j = s_start[k + 1], unit = s_unit[s_list[i]];
     const int b = unit / a.Hkv, g = unit % a.Hkv, nb = pref[b + 1] - pref[b];
     const int u1 = pref[b] * a.Hkv + (g + 1) * nb, u0 = u1 - nb + kUnitCost;   // its steps' places
     float* dst = nullptr;
@@ -950,8 +963,6 @@ __global__ void __launch_bounds__(kNW * 32, kDenseCtasPerSm)
         joined_output<D, F32>(a, x, b, g, h, e4);
       }
     }
-    first_elem += elems;
-    i = j;
   }
   if (n_shared > 0)
     arrive_and_join<D, F32>(a, n_shared, shared, reinterpret_cast<Joined*>(smem));
