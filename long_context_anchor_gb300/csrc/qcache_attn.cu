@@ -611,24 +611,28 @@ __device__ __forceinline__ int len_of(const QDecodeArgs& a, int b, bool report) 
 // batches balance. A unit starts with kUnitCost places without a step: what
 // its query, its first loads and its output cost a warp, so that runs of many
 // short units do not come last (48 sequences of 0 to 16001 keys: 82 us without,
-// 72 with one place, 66 with two, 67 with four). A run may span units: the
-// warp's pieces of units it does not hold alone go to shared memory, the CTA
-// joins those of its warps after one barrier, and a unit that several CTAs
-// share is joined by the last of them to arrive.
+// 72 with one place, 66 with two, 67 with four; 63.5 after later steps). A run
+// may span units: the warp's pieces of units it does not hold alone go to shared
+// memory, the CTA joins those of its warps after one barrier, and a unit that
+// several CTAs share is joined by the last of them to arrive.
 //
 // Every warp feeds itself: a ring of kDenseStages stages of one step, each
 // filled by one bulk copy per block that the step touches (groups of a block
 // are contiguous), which the first lanes issue as soon as the warp has left
 // the stage; no warp waits for another one before the end.
-// One CTA of 16 warps per SM: on a GB300 the 8B shape takes 65.5 us so, 67.3 as
+// One CTA of 16 warps per SM: on a GB300 the 8B shape took 65.5 us so, 67.3 as
 // two CTAs of 8 and 69.2 as four of 4 (the joins get longer); five of 4, with
-// 102 registers per thread, 95; three stages per ring change nothing.
+// 102 registers per thread, 95; three stages per ring changed nothing.
 // What bounds it: 8 sequences of 32768 keys, 8 KV heads of 4 query heads, d 128,
-// are 302 MB in 63.5 us = 4.8 TB/s (0.70 of the copy rate). A copy of the kernel
-// that moved the bytes and computed nothing took 57.7 us, about 5 of them
-// before the first step and 8 while the last CTAs finish; the arithmetic issues
-// 333 instructions per 16 keys (16 HMMA of 8 cycles, 64 conversions of code pairs
-// on the half-rate ALU) and keeps the issue slots 61% busy meanwhile.
+// are 302 MB in 61.1 us = 4.9 TB/s (0.73 of the copy rate). Time stamps of that
+// launch: every warp has its places after 1.7 us and its first step after 7.7 (all
+// rings fill at once), the warps' loops end between 55.6 and 58.1 (the SMs' means
+// within 0.5 of one another, a CTA's warps 3.4 apart), the CTAs' joins take 1.1 us
+// and those between CTAs 2.2. A copy of the kernel that moved the bytes and
+// computed nothing took 57.7 us before the joins were shortened by 1.5; the
+// arithmetic issues 333 instructions per 16 keys (16 HMMA of 8 cycles, 64
+// conversions of code pairs on the half-rate ALU) and keeps the issue slots 60%
+// busy meanwhile.
 constexpr int kNW = 16, kDenseCtasPerSm = 1;
 constexpr int kMinRun = 2;        // steps per warp at least
 constexpr int kDenseStages = 2;
@@ -1006,7 +1010,9 @@ __global__ void __launch_bounds__(256) k_qfill_tail(float* __restrict__ rows,
 // the plan), three 49.3; one or two larger CTAs per SM 56.8 and 55.6.
 // What bounds it: scattered rows. DRAM delivers 64 bytes for each 64-byte row of
 // codes and as many for its 8 bytes of scales: 8B shape, 4096 of 32768 keys per
-// head, 37.5 us from cold caches for 127 MB of useful bytes (3.4 TB/s).
+// head, 37.6 us from cold caches for 127 MB of useful bytes (3.4 TB/s), of which
+// 29 between the first step and the last at 5.1 TB/s of DRAM traffic. Three or four
+// stages per ring change nothing.
 constexpr int kReuseNW = 4, kReuseStages = 2, kReuseCtasPerSm = 3;
 // A row in one word: the group's number in the cache and the row in it.
 constexpr uint32_t kNoRow = 0xffffffffu;

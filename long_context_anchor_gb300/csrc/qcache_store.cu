@@ -276,9 +276,9 @@ __global__ void __launch_bounds__(kPlanThreads) k_qplan(const __grid_constant__ 
 // the cache, two rows wait for one slot, and their loads are in flight
 // together (K and V by different CTAs: 18.6 us to write, 18.7 to read 16384
 // tokens x 8 heads x 128 in bf16, 86 MB). Reading takes pieces of 8 elements, whose
-// stores join into whole sectors (14.8 us, 18.4 with 16); writing takes whole
-// blocks of 16, which find their scale alone (16.1 us, 21.7 with two threads per
-// block). 5.3 and 5.8 TB/s, 0.79 and 0.85 of the copy rate.
+// stores join into whole sectors (14.6 us, 18.4 with 16); writing takes whole
+// blocks of 16, which find their scale alone (15.6 us, 21.7 with two threads per
+// block). 5.5 and 5.9 TB/s, 0.81 and 0.87 of the copy rate.
 constexpr int kRowThreads = 256;
 constexpr int kAppendPiece = 16, kReadPiece = 8;   // elements per thread
 
