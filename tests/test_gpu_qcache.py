@@ -876,3 +876,78 @@ def test_profiling_command(kind, monkeypatch, capsys):
     monkeypatch.setattr("sys.argv", argv)
     runcase.main()
     assert capsys.readouterr().out == "ok qcache_%s\n" % kind
+
+
+def test_sequences_that_share_blocks(K):
+    """A common prefix held once: every sequence attends over it as over its own copy."""
+    rng = np.random.default_rng(11)
+    Hkv, d, bs, n = 2, 128, 32, 150
+    own, table = filled(K, rng, [n], Hkv, d, bs, spare=20)
+    first = table[0, :5]
+    used = set(first.tolist())
+    spare = [x for x in range(own.shape[0]) if x not in used]
+    copy = own.clone()
+    shared = np.stack([first, first, np.concatenate([first[:3], spare[:2]])])
+    apart = np.stack([first, spare[5:10], np.concatenate([spare[10:13], spare[:2]])])
+    for row in apart[1:]:
+        for j, b in enumerate(row):
+            if b not in spare[:2]:
+                copy[int(b)] = own[int(first[j])]
+    lens = [n, 77, 96]
+    q = torch.from_numpy(rng.standard_normal((3, 8, d))).to(BF).cuda()
+    ws = K.Workspace()
+    for fn in (lambda p, t: (K.qcache_dense_decode(q, p, ints(t), ints(lens), ws=ws),),
+               lambda p, t: K.qcache_anchor_decode(q, p, ints(t), ints(lens), 20, ws=ws)):
+        for x, y in zip(fn(own, shared), fn(copy, apart)):
+            assert torch.equal(x, y)
+    assert ws.device_error() == K.OK
+
+
+@pytest.mark.parametrize("pooled", [False, True])
+def test_repeated_calls_give_the_same_bits(K, pooled):
+    rng = np.random.default_rng(12)
+    Hkv, d, bs = 4, 64, 16
+    lens = [9000, 0, 1, 2500, 700, 31]
+    pages, table = filled(K, rng, lens, Hkv, d, bs)
+    q = torch.from_numpy(rng.standard_normal((len(lens), 16, d))).to(BF).cuda()
+    t, l, ws = ints(table), ints(lens), K.Workspace()
+    out, idx = K.qcache_anchor_decode(q, pages, t, l, 600, ws=ws, pooled=pooled)
+    reuse = K.qcache_reuse_decode(q, pages, t, l, idx, ws=ws, pooled=pooled)
+    for _ in range(30):
+        o, i = K.qcache_anchor_decode(q, pages, t, l, 600, ws=ws, pooled=pooled)
+        assert torch.equal(o, out) and torch.equal(i, idx)
+        assert torch.equal(K.qcache_reuse_decode(q, pages, t, l, idx, ws=ws, pooled=pooled), reuse)
+    assert ws.device_error() == K.OK
+
+
+def test_step_without_new_tokens(K):
+    """max_new = 0: sequences that end or roll back only; nothing to append."""
+    pages, table = filled(K, np.random.default_rng(13), [40, 20], 1, 64, 16)
+    free = ints([-1] * pages.shape[0])
+    slots, cu, lens, count = K.qcache_plan(ints([40, 20]), ints([-40, -5]), ints(table), free,
+                                           ints([0]), 16, 0)
+    assert slots.shape == (0,) and not cu.any()
+    assert lens.tolist() == [0, 15] and int(count) == 4
+    assert free[:4].tolist() == list(table[0, :3]) + [table[1, 1]]
+    x = torch.empty(0, 1, 64, dtype=BF, device="cuda")
+    before = pages.clone()
+    K.qcache_append(x, x, slots, pages)
+    assert torch.equal(pages, before)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_read_into_strided_rows(K, dtype):
+    """Only the rows asked for are written, at their strides; one token and one head too."""
+    for T, Hkv in ((5, 3), (1, 3), (5, 1), (1, 1)):
+        pages = K.qcache_alloc(2, Hkv, 64, 16)
+        x = torch.randn(2, T, Hkv, 64, device="cuda").to(dtype)
+        slots = ints([3, 17, 31, 0, 8][:T])
+        K.qcache_append(x[0], x[1], slots, pages)
+        want = K.qcache_read(pages, slots, dtype=dtype)
+        out = torch.full((2, Hkv + 2, T + 1, 80), 7.0, dtype=dtype, device="cuda")
+        k, v = (out[i, 1:Hkv + 1, :T, 8:72].transpose(0, 1) for i in range(2))
+        K.qcache_read(pages, slots, k=k, v=v)
+        assert torch.equal(k, want[0]) and torch.equal(v, want[1])
+        k.fill_(7.0)
+        v.fill_(7.0)
+        assert (out == 7.0).all()
