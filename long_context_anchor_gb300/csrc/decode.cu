@@ -443,8 +443,8 @@ __global__ void __launch_bounds__((NW + 1) * 32)
 // ------------------------------------------------------------------------
 // Union plan, one CTA per (key-range chunk c, sequence b, KV head g): the G
 // ascending per-head sets are cut to keys [c*R, (c+1)*R) by a warp-wide
-// 32-ary lower-bound search, marked in per-slot shared bitmaps and emitted as
-// one ascending list of entries key | (head-slot mask << 24) into
+// 32-ary lower-bound search, marked in a shared byte of heads per key and emitted,
+// eight keys per thread, as one ascending list of entries key | (head-slot mask << 24) into
 // plan[unit][c][kPlanCap], with its length in plan_count[unit][c]. Reuse
 // CTA (c, unit) consumes exactly chunk c.
 // ------------------------------------------------------------------------
@@ -479,9 +479,10 @@ __global__ void __launch_bounds__(256) k_build_union_plan(const __grid_constant_
                                                           int R) {
   pdl_wait();
   pdl_trigger();
-  __shared__ uint32_t bm[8][kPlanCap / 32];
-  __shared__ int s_lo[8], s_hi[8];
-  __shared__ int s_scan[256];
+  constexpr int kWarps = 8, kPer = kPlanCap / 256;   // keys per thread when the list is emitted
+  static_assert(kPer == 8, "two words of four keys per thread");
+  __shared__ uint2 s_mask[256];      // a byte of head slots per key of the chunk
+  __shared__ int s_lo[8], s_hi[8], s_tot[kWarps];
   const int c = blockIdx.x, unit = blockIdx.y, nch = gridDim.x;
   const int b = unit / a.Hkv, g = unit % a.Hkv;
   const int G = a.G, topk = a.topk;
@@ -490,8 +491,7 @@ __global__ void __launch_bounds__(256) k_build_union_plan(const __grid_constant_
   const bool padded = a.lens != nullptr;
   const int n = padded ? min(max(a.lens[b], 0), a.N) : a.N;
   const int n0 = c * R, n1 = min(n, n0 + R);
-  const int words = (R + 31) / 32;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // sets of this unit: one per query head of the group, or the group's one
   // pooled set (whose entries then carry every head of the group)
   const int nsets = a.pooled ? 1 : G;
@@ -499,10 +499,10 @@ __global__ void __launch_bounds__(256) k_build_union_plan(const __grid_constant_
     return a.pooled ? a.idx + static_cast<size_t>(unit) * topk
                     : a.idx + (static_cast<size_t>(b) * a.Hq + a.heads[g * G + slot]) * topk;
   };
-  for (int i = threadIdx.x; i < nsets * words; i += blockDim.x) bm[i / words][i % words] = 0u;
+  s_mask[tid] = make_uint2(0u, 0u);
   // search job j: the chunk start of set j (j < nsets) or the chunk end of
-  // set j - nsets, spread over the 8 warps so the searches run concurrently
-  for (int job = warp; job < 2 * nsets; job += 8) {
+  // set j - nsets, spread over the warps so the searches run concurrently
+  for (int job = warp; job < 2 * nsets; job += kWarps) {
     const int slot = job < nsets ? job : job - nsets;
     const bool is_hi = job >= nsets;
     const int32_t* row = set_row(slot);
@@ -517,10 +517,14 @@ __global__ void __launch_bounds__(256) k_build_union_plan(const __grid_constant_
     }
   }
   __syncthreads();
-  for (int slot = 0; slot < nsets; ++slot) {
+  // a set's entries go to the warps slot, slot + nsets, .. (nsets is 1, 2, 4 or 8)
+  {
+    const int slot = warp & (nsets - 1), step = 32 * (kWarps / nsets);
     const int32_t* row = set_row(slot);
-    const int hi = s_hi[slot];
-    for (int i = s_lo[slot] + threadIdx.x; i < hi; i += blockDim.x) {
+    const int hi = s_hi[slot], i0 = lane + 32 * (warp / nsets);
+    const uint32_t bits = a.pooled ? (1u << G) - 1u : 1u << slot;
+    uint32_t* words = reinterpret_cast<uint32_t*>(s_mask);
+    for (int i = s_lo[slot] + i0; i < hi; i += step) {
       const int raw = __ldg(row + i);
       const int key = raw - n0;
       // the sets must be strictly ascending and inside [0, N)
@@ -528,45 +532,37 @@ __global__ void __launch_bounds__(256) k_build_union_plan(const __grid_constant_
         report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x202);
         if (key < 0 || key >= n1 - n0) continue;
       }
-      atomicOr(&bm[slot][key >> 5], 1u << (key & 31));
+      atomicOr(&words[key >> 2], bits << (8 * (key & 3)));
     }
     if (padded && c == nch - 1)   // nothing but padding behind a set's last key
-      for (int i = hi + threadIdx.x; i < topk; i += blockDim.x)
+      for (int i = hi + i0; i < topk; i += step)
         if (__ldg(row + i) != -1) report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x204);
   }
   __syncthreads();
-  // contiguous word runs per thread; block scan of union counts
-  const int per = (words + blockDim.x - 1) / blockDim.x;
-  const int w0 = min(words, static_cast<int>(threadIdx.x) * per), w1 = min(words, w0 + per);
-  int cnt = 0;
-  for (int w = w0; w < w1; ++w) {
-    uint32_t u = 0;
-    for (int slot = 0; slot < nsets; ++slot) u |= bm[slot][w];
-    cnt += __popc(u);
+  // eight keys per thread; their places from a scan of the counts
+  const uint2 m = s_mask[tid];
+  const int cnt = (__popc(__vcmpne4(m.x, 0u)) + __popc(__vcmpne4(m.y, 0u))) >> 3;
+  int incl = cnt;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += o;
   }
-  s_scan[threadIdx.x] = cnt;
+  if (lane == 31) s_tot[warp] = incl;
   __syncthreads();
-  for (int off = 1; off < static_cast<int>(blockDim.x); off <<= 1) {
-    const int v = static_cast<int>(threadIdx.x) >= off ? s_scan[threadIdx.x - off] : 0;
-    __syncthreads();
-    s_scan[threadIdx.x] += v;
-    __syncthreads();
+  int before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) before += s_tot[w];
+    total += s_tot[w];
   }
-  int pos = s_scan[threadIdx.x] - cnt;
-  uint32_t* out = plan + (static_cast<size_t>(unit) * nch + c) * kPlanCap;
-  for (int w = w0; w < w1; ++w) {
-    uint32_t u = 0;
-    for (int slot = 0; slot < nsets; ++slot) u |= bm[slot][w];
-    while (u) {
-      const int bit = __ffs(u) - 1;
-      u &= u - 1;
-      uint32_t mask = a.pooled ? (1u << G) - 1u : 0u;
-      if (!a.pooled)
-        for (int slot = 0; slot < G; ++slot) mask |= ((bm[slot][w] >> bit) & 1u) << slot;
-      out[pos++] = static_cast<uint32_t>(n0 + w * 32 + bit) | (mask << 24);
-    }
+  uint32_t* out = plan + (static_cast<size_t>(unit) * nch + c) * kPlanCap + before + incl - cnt;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const uint32_t mask = ((i < 4 ? m.x : m.y) >> (8 * (i & 3))) & 0xffu;
+    if (mask != 0u) *out++ = static_cast<uint32_t>(n0 + tid * kPer + i) | (mask << 24);
   }
-  if (threadIdx.x == blockDim.x - 1) plan_count[unit * nch + c] = s_scan[threadIdx.x];
+  if (tid == 0) plan_count[unit * nch + c] = total;
 }
 
 // The same plan from the heads' selection bitmaps (one word per 32 keys per
