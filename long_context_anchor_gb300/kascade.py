@@ -786,10 +786,11 @@ def qcache_plan(kv_lens, new_lens, block_table, free_blocks, free_count, block_s
         with _on(dev, stream):
             return qcache_plan(kv_lens, new_lens, block_table, free_blocks, free_count, block_size,
                                max_new, kv_lens_out, free_count_out, ws)
-    slots, cu, lens, count = torch.split_with_sizes(
-        torch.empty(max_new + 2 * B + 2, dtype=i32, device=dev), (max_new, B + 1, B, 1))
-    lens = lens if kv_lens_out is None else kv_lens_out
-    count = count if free_count_out is None else free_count_out
+    # one by one: an allocation and three views of it take 2 us longer
+    slots = torch.empty(max(max_new, 0), dtype=i32, device=dev)
+    cu = torch.empty(B + 1, dtype=i32, device=dev)
+    lens = torch.empty(B, dtype=i32, device=dev) if kv_lens_out is None else kv_lens_out
+    count = torch.empty(1, dtype=i32, device=dev) if free_count_out is None else free_count_out
     buf = _qws(ws, dev, index, 256)
     _check(_lib.kascade_qcache_plan(geo, B, kv_lens.data_ptr(), new_lens.data_ptr(),
                                     block_table.data_ptr(), free_blocks.data_ptr(),

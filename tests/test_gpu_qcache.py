@@ -929,6 +929,8 @@ def test_step_without_new_tokens(K):
     assert slots.shape == (0,) and not cu.any()
     assert lens.tolist() == [0, 15] and int(count) == 4
     assert free[:4].tolist() == list(table[0, :3]) + [table[1, 1]]
+    with pytest.raises(K.KascadeError):
+        K.qcache_plan(lens, lens, ints(table), free, count, 16, -1)
     x = torch.empty(0, 1, 64, dtype=BF, device="cuda")
     before = pages.clone()
     K.qcache_append(x, x, slots, pages)
