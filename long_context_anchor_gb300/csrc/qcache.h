@@ -38,6 +38,7 @@ struct QDecodeArgs {
   unsigned int* counters;     // [B*Hkv] split arrival counters (self-resetting)
   unsigned int* err;
   int firsts_global;          // dense: where a warp's first piece waits (see there)
+  int pages_once;             // with logits: the pages' L2 lines are the first to go
   int fill_tail;              // scores behind a sequence's last key become -inf
   int B, Hq, Hkv, G, N;
   int bs_shift, num_blocks, max_blocks;

@@ -639,6 +639,13 @@ constexpr int kDenseStages = 2;
 
 constexpr int kUnitCost = 2;
 
+// The pages are read once, so their L2 lines are the first to go (62.6 us
+// against 63.5 on the 8B shape). With logits that leaves room for them until the
+// Top-k has read them, as long as they fit: an anchor layer with 34 MB of them takes
+// 104 us against 107, with 98 MB 120 against 126; 134 MB pass the cache's 129 MB
+// and are best written out at once: 158 us against 154.
+constexpr size_t kL2Logits = size_t(100) << 20;
+
 // The part of a run that lies in the unit at place f of the line: steps [s0, s1)
 // of its ns (none, if the run has only the unit's first place), and the place
 // behind it.
@@ -772,7 +779,7 @@ __global__ void __launch_bounds__(kNW * 32, kDenseCtasPerSm)
       const uint8_t* src = in_base +
                            static_cast<uint64_t>(static_cast<uint32_t>(id)) * block_bytes +
                            ((static_cast<uint32_t>(in_key) >> 4) & gmask) * kGroupBytes;
-      if (SCORES) bulk_load(dst, src, copy_bytes, bar);
+      if (SCORES && !a.pages_once) bulk_load(dst, src, copy_bytes, bar);
       else bulk_load_once(dst, src, copy_bytes, bar);
     } else if (want) {
       report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x522);
@@ -1299,6 +1306,7 @@ cudaError_t launch_dense_t(const QDecodeArgs& a, cudaStream_t st) {
   const size_t firsts = kNW * qpart_floats(a.G, D) * sizeof(float);
   QDecodeArgs u = a;
   u.firsts_global = smem + firsts > 224 * 1024 ? 1 : 0;
+  u.pages_once = static_cast<size_t>(a.B) * a.Hq * a.N * 4 <= kL2Logits ? 1 : 0;
   if (!u.firsts_global) smem += firsts;
   constexpr auto kern = k_qdecode_dense<D, TERMS, SCORES>;
   int ctas = 0;
