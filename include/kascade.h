@@ -334,6 +334,8 @@ kascade_status kascade_run_stack_profiled(const kascade_desc* desc, int32_t mode
  * appended rows (bf16, or fp32 computed to fp32 accuracy). A length out of
  * range, or a block id outside [0, num_blocks), sets KASCADE_ERR_BAD_INPUT on the device;
  * those keys are not read and count as masked.
+ * Softmax weights are rounded to 11 bits (bf16) or 22 (fp32), and to multiples
+ * of at most 2^-38 of the row's largest one.
  * A sequence's keys are split over CTAs by rules that look at the whole batch,
  * so the last bits of its output may differ between batches; one call repeated
  * gives the same bits.
