@@ -311,8 +311,9 @@ __device__ __forceinline__ uint32_t e2m1x8(const float (&x)[8]) {
 // to its last bit, and exact where the quotient has few bits, as every tie
 // has. A bf16 x (8 bits) over an s of at most 4 bits is otherwise at least 2^-13
 // away from a tie, so that is all it needs (EXACT false). The quotient of an
-// fp32 x may round onto a tie: where the division leaves a remainder, q moves
-// one last place towards it.
+// fp32 x may lie within a last place of a tie: where the division leaves a
+// remainder, q is rounded to odd (cut towards zero, its last bit set), which keeps
+// it on the exact quotient's side of every number of fewer bits.
 template <bool EXACT>
 __device__ __forceinline__ float round_quotient(float x, float s, float inv) {
   float q = x * inv;
@@ -320,8 +321,8 @@ __device__ __forceinline__ float round_quotient(float x, float s, float inv) {
   if (EXACT) {
     const float r = fmaf(-q, s, x);
     if (r != 0.f && q != 0.f) {
-      const int step = ((r > 0.f) == (q > 0.f)) ? 1 : -1;
-      q = __int_as_float(__float_as_int(q) + step);
+      const int cut = ((r > 0.f) == (q > 0.f)) ? 0 : 1;
+      q = __int_as_float((__float_as_int(q) - cut) | 1);
     }
   }
   return q;

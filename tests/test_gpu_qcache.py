@@ -953,3 +953,36 @@ def test_read_into_strided_rows(K, dtype):
         k.fill_(7.0)
         v.fill_(7.0)
         assert (out == 7.0).all()
+
+
+def rows_beside_ties(d):
+    """fp32 rows [T, 1, d] of blocks whose codes, or whose scales, lie on a tie or one or two
+    last places beside it: every significand of the scale, every tie of both formats."""
+    def near(x):
+        x = np.float32(x)
+        return [(x.view(np.int32) + np.int32(i)).view(np.float32) for i in range(-2, 3)]
+
+    blocks = []
+    for s in [m / 8 * 2.0 ** e for e in (-6, -1, 0, 7) for m in range(8, 16)]:
+        x = [y for a, b in zip(Q.E2M1, Q.E2M1[1:]) for y in near((a + b) / 2 * s)]
+        x = [-y if i % 2 else y for i, y in enumerate(x)]
+        x += [0.0] * (-len(x) % 15)
+        blocks += [[6 * s] + x[i:i + 15] for i in range(0, len(x), 15)]   # 6 s: the scale is s
+    for a, b in zip(Q.E4M3, Q.E4M3[1:]):
+        blocks += [[y] + [y * np.float32(f) for f in np.linspace(-0.99, 0.99, 15)]
+                   for y in near((a + b) / 2 * 6)]
+    blocks += [[0.0] * 16] * (-len(blocks) % (d // 16))
+    return np.array(blocks, dtype=np.float32).reshape(-1, 1, d)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -7, 2.0 ** 20])
+def test_append_rounds_fp32_beside_ties_once(K, d, scale):
+    x = torch.from_numpy(rows_beside_ties(d) * np.float32(scale))
+    T = len(x)
+    pages = K.qcache_alloc((T + 15) // 16, 1, d, 16)
+    slots = ints(range(T))
+    K.qcache_append(x.cuda(), x.cuda(), slots, pages, scale, scale)
+    want = Q.stored(f64(x), scale)
+    for got in K.qcache_read(pages, slots, dtype=F32, k_scale=scale, v_scale=scale):
+        assert np.array_equal(f64(got), want)
