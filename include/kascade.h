@@ -374,7 +374,8 @@ size_t kascade_qcache_workspace_size(const kascade_desc* desc, const kascade_qca
  *                   step are cu_new[b] .. cu_new[b+1]-1;
  *   slot_map [max_new]   the slot of every new token, -1 behind the last.
  * A step that cannot be served (too few free blocks, more tokens than
- * max_blocks*block_size or than max_new, an id or a length out of range)
+ * max_blocks*block_size or than max_new, a length out of range, an id out of
+ * range among the blocks given back, taken or written to by new tokens)
  * changes no table, stack, length or count, leaves every slot -1 and cu_new
  * 0, and sets KASCADE_ERR_BAD_INPUT on the device. n_seqs <= 16384. */
 kascade_status kascade_qcache_plan(const kascade_qcache* cache, int32_t n_seqs,

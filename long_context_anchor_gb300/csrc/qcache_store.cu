@@ -176,13 +176,20 @@ __device__ __forceinline__ int plan_taken(const QPlanArgs& a, const PlanScan& r,
   return j < r.gives ? plan_given(a, give, r.gives - 1 - j) : a.free_blocks[r.c + r.gives - 1 - j];
 }
 
-// Ids that move: those given back, and the old part of the stack that is taken.
+// Ids that the step uses: those given back, the old part of the stack that is
+// taken, and the partly filled block that a growing sequence's first new tokens go to.
 __device__ bool plan_bad_ids(const QPlanArgs& a, const PlanScan& r, const int* give, int t0,
                              int step) {
   bool bad = false;
   auto check = [&](int id) { bad |= id < 0 || id >= a.num_blocks; };
   for (int i = t0; i < r.gives; i += step) check(plan_given(a, give, i));
   for (int j = r.gives + t0; j < r.takes; j += step) check(plan_taken(a, r, give, j));
+  for (int b = t0; b < a.B; b += step) {
+    int L, to;
+    plan_len(a, b, L, to);
+    if (to > L && (L & ((1 << a.bs_shift) - 1)) != 0)
+      check(a.table[static_cast<size_t>(b) * a.max_blocks + (L >> a.bs_shift)]);
+  }
   return bad;
 }
 
@@ -208,11 +215,10 @@ __device__ void plan_apply(const QPlanArgs& a, const PlanScan& r, int* const (&p
       int L, to;
       plan_len(a, b, L, to);
       const int p = L + i - pre[2][b], col = p >> sh, have = plan_blocks(a, L);
-      // the block that the sequence's last token is in, or one taken now
+      // the block that the sequence's last token is in, or one taken now: checked
       const int id = col < have ? a.table[static_cast<size_t>(b) * a.max_blocks + col]
                                 : plan_taken(a, r, pre[0], pre[1][b] + col - have);
-      if (id >= 0 && id < a.num_blocks) slot = (id << sh) | (p & ((1 << sh) - 1));
-      else report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x502);
+      slot = (id << sh) | (p & ((1 << sh) - 1));
     }
     a.slot_map[i] = slot;
   }

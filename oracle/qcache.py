@@ -81,7 +81,9 @@ def plan(kv_lens, new_lens, table, free, count, bs, max_new):
         return None
     stack = [int(x) for x in free[:count]] + given
     used = [stack[len(stack) - 1 - i] for i in range(len(taken))]
-    if any(not 0 <= x < nb for x in given + used):
+    # the partly filled block that a growing sequence's first new tokens go to
+    tail = [int(table[b, int(l) // bs]) for b, l in enumerate(kv_lens) if to[b] > l and l % bs]
+    if any(not 0 <= x < nb for x in given + used + tail):
         return None
     free[count:count + len(given)] = given
     for (b, j), x in zip(taken, used):

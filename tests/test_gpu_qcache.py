@@ -986,3 +986,29 @@ def test_append_rounds_fp32_beside_ties_once(K, d, scale):
     want = Q.stored(f64(x), scale)
     for got in K.qcache_read(pages, slots, dtype=F32, k_scale=scale, v_scale=scale):
         assert np.array_equal(f64(got), want)
+
+
+@pytest.mark.parametrize("nb", [12, 3012])      # one launch, two launches
+@pytest.mark.parametrize("bad", [-1, "nb", 2 ** 31 - 1, -2 ** 31])
+def test_plan_refuses_a_bad_block_that_new_tokens_go_to(K, nb, bad):
+    """Sequence 1's partly filled block is out of range: the other sequences' changes do not
+    happen either. A sequence that does not grow, or whose last block is full, may hold such
+    an entry."""
+    bs, bad = 16, nb if bad == "nb" else bad
+    table = np.array([[0, 1, -1, -1], [2, 3, bad, -1], [5, 6, 7, 8]])
+    free = np.array([9, 10, 11] + [-1] * (nb - 3))
+    ws = K.Workspace()
+    for lens, new, ok in (([20, 33, 64], [15, 5, -40], False), ([20, 47, 64], [15, 1, -40], False),
+                          ([20, 33, 64], [15, 0, -40], True), ([20, 48, 64], [15, 1, -40], True)):
+        want = Q.plan(lens, new, table, free, 3, bs, 30)
+        assert (want is not None) == ok
+        d = [ints(x) for x in (lens, new, table, free, [3])]
+        slots, cu, l2, c2 = K.qcache_plan(*d, bs, 30, ws=ws)
+        assert ws.device_error() == (K.OK if ok else K.BAD_INPUT)
+        if ok:
+            assert np.array_equal(slots.cpu().numpy(), want[0])
+            assert np.array_equal(d[2].cpu().numpy(), want[4]) and int(c2) == want[3]
+            continue
+        assert (slots == -1).all() and not cu.any()
+        assert torch.equal(l2, d[0]) and int(c2) == 3
+        assert torch.equal(d[2], ints(table)) and torch.equal(d[3], ints(free))

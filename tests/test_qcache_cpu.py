@@ -318,3 +318,13 @@ def test_captured_workspace_does_not_grow(K, fake):
     assert ws.get(1024) is ws.buf
     with pytest.raises(RuntimeError, match="captured"):
         ws.get(8192)
+
+
+def test_plan_refuses_a_bad_block_that_new_tokens_go_to():
+    """The partly filled block of a growing sequence is neither given back nor taken."""
+    free = np.array([1, 2, 3, 0])
+    for bad in (-1, 4, 2 ** 31 - 1):
+        table = np.array([[0, bad, -1]])
+        assert Q.plan([20], [5], table, free, 3, 16, 8) is None
+        assert Q.plan([20], [0], table, free, 3, 16, 8) is not None     # nothing goes there
+        assert Q.plan([32], [5], table, free, 3, 16, 8) is not None     # full: not touched
