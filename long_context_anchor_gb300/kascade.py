@@ -656,10 +656,13 @@ def _cuda(t, name):
 
 
 # torch.cuda.current_device, current_stream and is_current_stream_capturing
-# without their wrapper objects (each costs a microsecond or two)
-_current_device = torch._C._cuda_getDevice
-_current_raw_stream = torch._C._cuda_getCurrentRawStream
-_capturing = torch._C._cuda_isCurrentStreamCapturing
+# without their wrapper objects (each costs a microsecond or two); these
+# themselves where torch does not have the functions behind them
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda index: torch.cuda.current_stream(index).cuda_stream)
+_capturing = getattr(torch._C, "_cuda_isCurrentStreamCapturing",
+                     torch.cuda.is_current_stream_capturing)
 
 
 def _elsewhere(index, stream):

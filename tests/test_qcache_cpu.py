@@ -1,6 +1,8 @@
 """Paged 4-bit cache without a GPU: the oracle's pins, the library's argument
 validation (before any launch) and the binding's tensor checks."""
 import ctypes
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -328,3 +330,25 @@ def test_plan_refuses_a_bad_block_that_new_tokens_go_to():
         assert Q.plan([20], [5], table, free, 3, 16, 8) is None
         assert Q.plan([20], [0], table, free, 3, 16, 8) is not None     # nothing goes there
         assert Q.plan([32], [5], table, free, 3, 16, 8) is not None     # full: not touched
+
+
+_WITHOUT_PRIVATE_NAMES = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream", "_cuda_isCurrentStreamCapturing"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+from long_context_anchor_gb300 import kascade as K
+assert K._current_device is torch.cuda.current_device
+assert K._capturing is torch.cuda.is_current_stream_capturing
+class Stream:
+    cuda_stream = 77
+torch.cuda.current_stream = lambda index: Stream() if index == 3 else None
+assert K._current_raw_stream(3) == 77
+"""
+
+
+def test_binding_without_torchs_private_functions(K):
+    """The functions behind torch.cuda's public ones are a shortcut, not a need."""
+    r = subprocess.run([sys.executable, "-c", _WITHOUT_PRIVATE_NAMES], cwd=__graft_entry__.ROOT,
+                       capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
