@@ -359,6 +359,11 @@ size_t kascade_qcache_bytes(const kascade_qcache* cache, int32_t n_kv_heads, int
 size_t kascade_qcache_workspace_size(const kascade_desc* desc, const kascade_qcache* cache,
                                      int32_t topk);
 
+/* What kascade_qcache_reuse_decode alone needs of that: it keeps no logits,
+ * which are B*Hq*kv_len*4 bytes of an anchor layer's. */
+size_t kascade_qcache_reuse_workspace_size(const kascade_desc* desc, const kascade_qcache* cache,
+                                           int32_t topk);
+
 /* Block tables and slots of one step, on the device. Sequence b goes from
  * L = kv_lens[b] to L' = max(0, L + new_lens[b]) tokens: it grows (new tokens
  * to append), shrinks (tokens taken back) or, with -L or less, ends. It then

@@ -56,8 +56,9 @@ kascade_status check_qcache(const kascade_qcache* c, QCacheShape& s) {
 
 struct QLayout {
   size_t counters, part;                                  // every attention call
-  size_t spill, row_stat, pool, plan, plan_count;         // topk >= 1
-  size_t total;
+  size_t plan, plan_count;                                // topk >= 1, sets per query head
+  size_t spill, row_stat, pool;                           // topk >= 1, anchor layers
+  size_t reuse, total;                                    // bytes: without an anchor layer, in all
 };
 
 QLayout qlayout(const Shape& s, int topk) {
@@ -66,6 +67,14 @@ QLayout qlayout(const Shape& s, int topk) {
   size_t off = kWsStateBytes;
   L.part = off;
   off = align256(off + static_cast<size_t>(kQPieces) * qpart_floats(s.G, s.d) * 4);
+  if (topk >= 1 && !s.pooled) {
+    const size_t chunks = decode_union_chunks(s.B * s.Hkv, s.N);
+    L.plan = off;
+    off = align256(off + static_cast<size_t>(s.B) * s.Hkv * chunks * kPlanCapEntries * 4);
+    L.plan_count = off;
+    off = align256(off + static_cast<size_t>(s.B) * s.Hkv * chunks * 4);
+  }
+  L.reuse = off;
   if (topk >= 1) {
     L.spill = off;
     off = align256(off + static_cast<size_t>(s.B) * s.Hq * s.N * 4);
@@ -74,12 +83,6 @@ QLayout qlayout(const Shape& s, int topk) {
       off = align256(off + static_cast<size_t>(s.B) * s.Hq * 8);
       L.pool = off;
       off = align256(off + static_cast<size_t>(s.B) * s.Hkv * s.N * 4);
-    } else {
-      const size_t chunks = decode_union_chunks(s.B * s.Hkv, s.N);
-      L.plan = off;
-      off = align256(off + static_cast<size_t>(s.B) * s.Hkv * chunks * kPlanCapEntries * 4);
-      L.plan_count = off;
-      off = align256(off + static_cast<size_t>(s.B) * s.Hkv * chunks * 4);
     }
   }
   L.total = off;
@@ -107,9 +110,10 @@ kascade_status check_call(const kascade_desc* desc, const kascade_qcache* cache,
   return KASCADE_OK;
 }
 
-kascade_status check_qws(QCall& k, int topk, void* ws, size_t ws_bytes) {
+kascade_status check_qws(QCall& k, int topk, void* ws, size_t ws_bytes, bool reuse = false) {
   k.L = qlayout(k.s, topk);
-  if (!aligned(ws, 256) || ws_bytes < k.L.total) return KASCADE_ERR_WORKSPACE;
+  if (!aligned(ws, 256) || ws_bytes < (reuse ? k.L.reuse : k.L.total))
+    return KASCADE_ERR_WORKSPACE;
   return KASCADE_OK;
 }
 
@@ -346,6 +350,13 @@ size_t kascade_qcache_workspace_size(const kascade_desc* desc, const kascade_qca
   return qlayout(k.s, topk).total;
 }
 
+size_t kascade_qcache_reuse_workspace_size(const kascade_desc* desc, const kascade_qcache* cache,
+                                           int32_t topk) {
+  QCall k;
+  if (check_call(desc, cache, k) != KASCADE_OK || topk < 1) return 0;
+  return qlayout(k.s, topk).reuse;
+}
+
 kascade_status kascade_qcache_plan(const kascade_qcache* cache, int32_t n_seqs,
                                    const int32_t* kv_lens, const int32_t* new_lens,
                                    int32_t* block_table, int32_t* free_blocks,
@@ -443,7 +454,7 @@ kascade_status kascade_qcache_reuse_decode(const kascade_desc* desc, const kasca
   if (r != KASCADE_OK) return r;
   if ((r = check_attn_ptrs(q, pages, block_table, kv_lens, out)) != KASCADE_OK) return r;
   if (topk < 1 || topk > k.s.N || !aligned(idx, 4)) return KASCADE_ERR_INVALID_ARG;
-  if ((r = check_qws(k, topk, ws, ws_bytes)) != KASCADE_OK) return r;
+  if ((r = check_qws(k, topk, ws, ws_bytes, true)) != KASCADE_OK) return r;
   return run_qreuse(k, q, pages, block_table, kv_lens, topk, idx, out, ws, false,
                     static_cast<cudaStream_t>(stream));
 }

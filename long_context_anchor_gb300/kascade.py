@@ -87,6 +87,7 @@ _SIGS = {
                                                   _vp, _vp, _sz, _vp, ctypes.POINTER(_vp)]),
     "kascade_qcache_bytes": (_sz, [_QP, _i32, _i32]),
     "kascade_qcache_workspace_size": (_sz, [_DP, _QP, _i32]),
+    "kascade_qcache_reuse_workspace_size": (_sz, [_DP, _QP, _i32]),
     "kascade_qcache_plan": (ctypes.c_int, [_QP, _i32] + [_vp] * 9 + [_i32, _vp, _sz, _vp]),
     "kascade_qcache_append": (ctypes.c_int, [_QP, _i32, _i32, _i32, _vp, _vp, _I64P, _vp, _i32,
                                              _vp, _vp, _sz, _vp]),
@@ -729,18 +730,22 @@ def _qgeo(block_size, num_blocks, max_blocks, k_scale, v_scale):
 
 
 @functools.lru_cache(maxsize=256)
-def _qdesc(B, Hq, Hkv, d, N, code, scale, group_map, pooled, bs, nb, width, k_scale, v_scale, topk):
+def _qdesc(B, Hq, Hkv, d, N, code, scale, group_map, pooled, bs, nb, width, k_scale, v_scale, topk,
+           reuse):
     """Descriptor, geometry (ctypes references, read only) and workspace bytes of
     an attention call of these sizes."""
     desc = make_desc(B, Hq, Hkv, d, N, code, scale, group_map, pooled)
     geo = QCache(bs, nb, width, k_scale, v_scale)
-    return ctypes.byref(desc), ctypes.byref(geo), qcache_workspace_size(desc, geo, topk)
+    return ctypes.byref(desc), ctypes.byref(geo), qcache_workspace_size(desc, geo, topk, reuse)
 
 
-def qcache_workspace_size(desc, geo, topk: int) -> int:
-    n = _lib.kascade_qcache_workspace_size(ctypes.byref(desc), ctypes.byref(geo), int(topk))
+def qcache_workspace_size(desc, geo, topk: int, reuse: bool = False) -> int:
+    """Workspace bytes of a cache attention call (topk 0: dense decode); reuse: of a
+    reuse layer alone, which keeps no logits."""
+    name = "kascade_qcache_reuse_workspace_size" if reuse else "kascade_qcache_workspace_size"
+    n = getattr(_lib, name)(ctypes.byref(desc), ctypes.byref(geo), int(topk))
     if n == 0:
-        raise KascadeError(INVALID_ARG, "kascade_qcache_workspace_size")
+        raise KascadeError(INVALID_ARG, name)
     return n
 
 
@@ -901,7 +906,7 @@ def qcache_read(pages, slot_map, dtype=torch.bfloat16, k_scale=1.0, v_scale=1.0,
 
 
 def _qattn(q, pages, block_table, kv_lens, kv_len, group_map, scale, k_scale, v_scale, pooled, topk,
-           out):
+           out, reuse=False):
     """Checks one attention call's common tensors; returns (descriptor and
     geometry references, workspace bytes, (B, Hq, Hkv, N), device)."""
     nb, hkv, bs, d = _pages(pages)
@@ -933,7 +938,8 @@ def _qattn(q, pages, block_table, kv_lens, kv_len, group_map, scale, k_scale, v_
     desc, geo, nbytes = _qdesc(B, Hq, hkv, d, N, _ROW_CODES[q.dtype][0],
                                0.0 if scale is None else float(scale),
                                None if group_map is None else tuple(int(x) for x in group_map),
-                               bool(pooled), bs, nb, width, float(k_scale), float(v_scale), topk)
+                               bool(pooled), bs, nb, width, float(k_scale), float(v_scale), topk,
+                               reuse)
     return desc, geo, nbytes, (B, Hq, hkv, N), dev
 
 
@@ -1007,7 +1013,7 @@ def qcache_reuse_decode(q, pages, block_table, kv_lens, idx, kv_len=None, group_
     topk = idx.shape[2]
     desc, geo, nbytes, (B, Hq, hkv, _), dev = _qattn(q, pages, block_table, kv_lens, kv_len,
                                                      group_map, scale, k_scale, v_scale, pooled,
-                                                     max(topk, 1), out)
+                                                     max(topk, 1), out, reuse=True)
     _fits(idx, "idx", (B, hkv if pooled else Hq, topk), torch.int32, dev)
     index = pages.get_device()
     if _elsewhere(index, stream):

@@ -1012,3 +1012,29 @@ def test_plan_refuses_a_bad_block_that_new_tokens_go_to(K, nb, bad):
         assert (slots == -1).all() and not cu.any()
         assert torch.equal(l2, d[0]) and int(c2) == 3
         assert torch.equal(d[2], ints(table)) and torch.equal(d[3], ints(free))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("pooled", [False, True])
+def test_reuse_stays_within_its_workspace(K, pooled, dtype):
+    """A workspace of exactly a reuse layer's size, with guard bytes behind it."""
+    rng = np.random.default_rng(41)
+    lens, Hq, Hkv, d, bs, k = [5000, 0, 300], 16, 4, 64, 32, 700
+    pages, table = filled(K, rng, lens, Hkv, d, bs)
+    H = Hkv if pooled else Hq
+    _, idx = random_sets(rng, lens, H, k)
+    q = torch.from_numpy(rng.standard_normal((3, Hq, d))).to(dtype).cuda()
+    args = (q, pages, ints(table), ints(lens), ints(idx))
+    big = K.Workspace()
+    want = K.qcache_reuse_decode(*args, pooled=pooled, ws=big)
+    width = table.shape[1]
+    desc = K.make_desc(3, Hq, Hkv, d, width * bs, K.BF16 if dtype is BF else K.F32, pooled=pooled)
+    n = K.qcache_workspace_size(desc, K.QCache(bs, pages.shape[0], width, 0.0, 0.0), k, reuse=True)
+    assert n < K.qcache_workspace_size(desc, K.QCache(bs, pages.shape[0], width, 0.0, 0.0), k)
+    assert big.buf.numel() == n
+    buf = torch.zeros(n + (1 << 20), dtype=torch.uint8, device="cuda")
+    buf[n:] = 171
+    ws = K.Workspace()
+    ws.buf = buf[:n]
+    assert torch.equal(K.qcache_reuse_decode(*args, pooled=pooled, ws=ws), want)
+    assert ws.device_error() == K.OK and bool((buf[n:] == 171).all())

@@ -352,3 +352,28 @@ def test_binding_without_torchs_private_functions(K):
     r = subprocess.run([sys.executable, "-c", _WITHOUT_PRIVATE_NAMES], cwd=__graft_entry__.ROOT,
                        capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.mark.parametrize("pooled", [False, True])
+def test_reuse_workspace_holds_no_logits(K, pooled):
+    """A reuse layer's workspace: below an anchor layer's by the logits and what ranks them, and
+    refused one byte short of it."""
+    B, Hq, Hkv, N = 64, 32, 8, 131072
+    desc = K.make_desc(B, Hq, Hkv, 128, N, K.BF16, pooled=pooled)
+    geo = K.QCache(64, 4096, N // 64, 0.0, 0.0)
+    L, ref, p = K._lib, ctypes.byref, ctypes.c_void_p(1 << 20)
+    dense = K.qcache_workspace_size(desc, geo, 0)
+    anchor = K.qcache_workspace_size(desc, geo, 4096)
+    reuse = K.qcache_workspace_size(desc, geo, 4096, reuse=True)
+    logits = B * Hq * N * 4
+    assert dense <= reuse <= anchor - logits
+    if pooled:
+        assert reuse == dense and anchor - reuse >= logits + B * Hkv * N * 4
+    else:
+        assert reuse == anchor - logits
+    assert L.kascade_qcache_reuse_decode(ref(desc), ref(geo), p, p, p, p, 4096, p, p, p, reuse - 1,
+                                         None) == K.WORKSPACE
+    assert L.kascade_qcache_anchor_decode(ref(desc), ref(geo), p, p, p, p, 4096, p, p, None, p,
+                                          reuse, None) == K.WORKSPACE
+    size = L.kascade_qcache_reuse_workspace_size
+    assert size(ref(desc), ref(geo), 0) == 0 and size(ref(desc), None, 1) == 0
