@@ -326,10 +326,9 @@ __device__ __forceinline__ float round_quotient(float x, float s, float inv) {
   q = fmaf(fmaf(-q, s, x), inv, q);
   if (EXACT) {
     const float r = fmaf(-q, s, x);
-    if (r != 0.f && q != 0.f) {
-      const int cut = ((r > 0.f) == (q > 0.f)) ? 0 : 1;
-      q = __int_as_float((__float_as_int(q) - cut) | 1);
-    }
+    // a quotient that passed the exact one: r and q differ in sign
+    const int u = __float_as_int(q), cut = (__float_as_int(r) ^ u) >> 31;
+    if (r != 0.f) q = __int_as_float((u + cut) | 1);
   }
   return q;
 }
