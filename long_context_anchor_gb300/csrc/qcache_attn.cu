@@ -12,8 +12,12 @@
 // its largest element lies in [2^12, 2^13): a bf16 q is then exact in fp16
 // down to 2^-26 of that element, an fp32 q is the sum of two fp16 terms (22
 // bits). The softmax weights are kept as 2^14 p, so that a weight down to 2^-38
-// of the row's largest one still counts; for fp32 outputs they too are a sum of
-// two fp16 terms.
+// of the row's largest one still counts in the product with V; smaller ones count
+// in the sum of the weights alone, which is taken in fp32 before the rounding. For
+// bf16 outputs a weight is one fp16 term, whose half step of 2^-11 is an eighth of
+// the output's own 2^-8 (distance from 64-bit results on 8 x 32768 keys: 1.7e-3
+// of the output's norm, 1.6e-3 with weights in 32 bits). For fp32 outputs it too
+// is a sum of two fp16 terms.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -630,7 +634,7 @@ __device__ __forceinline__ int len_of(const QDecodeArgs& a, int b, bool report) 
 // within 0.5 of one another, a CTA's warps 3.4 apart), the CTAs' joins take 1.1 us
 // and those between CTAs 2.2. A copy of the kernel that moved the bytes and
 // computed nothing took 57.7 us before the joins were shortened by 1.5; the
-// arithmetic issues 333 instructions per 16 keys (16 HMMA of 8 cycles, 64
+// arithmetic issues 331 instructions per 16 keys (16 HMMA of 8 cycles, 64
 // conversions of code pairs on the half-rate ALU) and keeps the issue slots 60%
 // busy meanwhile.
 constexpr int kNW = 16, kDenseCtasPerSm = 1;
@@ -1331,6 +1335,7 @@ cudaError_t launch_reuse_t(const QDecodeArgs& a, cudaStream_t st) {
   int ctas = 0;
   const cudaError_t e = resident_ctas<kern>(smem, kReuseNW * 32, ctas);
   if (e != cudaSuccess) return e;
+  if (ctas > kQPieces) ctas = kQPieces;   // a place per CTA, as S * units <= ctas or S = 1
   QDecodeArgs u = a;
   const int units = a.B * a.Hkv;
   // as many CTAs per unit as fill one wave, and at least one step per warp
@@ -1340,7 +1345,6 @@ cudaError_t launch_reuse_t(const QDecodeArgs& a, cudaStream_t st) {
   int s = ctas / units;
   if (s > most) s = most;
   if (s > kMaxSplits) s = kMaxSplits;   // the last CTA joins that many pieces
-  if (s * units > kQPieces) s = 1;      // one piece needs no room
   u.S = s < 1 ? 1 : s;
   return launch_pdl(kern, dim3(u.S, units), dim3(kReuseNW * 32), smem, st, u);
 }
