@@ -330,12 +330,15 @@ kascade_status kascade_run_stack_profiled(const kascade_desc* desc, int32_t mode
  * sequence, 0 <= kv_lens[b] <= desc->kv_len, read on the device; a sequence
  * of length 0 outputs zeros. What the pages hold behind a sequence's last
  * token is never used. desc->kv_len <= max_blocks*block_size is the longest
- * length and the row stride of scores; desc->dtype is that of q, out and of
- * appended rows (bf16, or fp32 computed to fp32 accuracy). A length out of
+ * length, the row stride of scores, and what workspaces and limits go by, so it
+ * is best kept near the lengths in use where the table is wide. desc->dtype is
+ * that of q, out and of appended rows: bf16, or fp32, for which a query's
+ * elements keep 22 bits; sums are in fp32. A length out of
  * range, or a block id outside [0, num_blocks), sets KASCADE_ERR_BAD_INPUT on the device;
  * those keys are not read and count as masked.
- * Softmax weights are rounded to 11 bits (bf16) or 22 (fp32), and to multiples
- * of at most 2^-38 of the row's largest one.
+ * In the product with V softmax weights are rounded to 11 bits (bf16) or 22
+ * (fp32), and to multiples of at most 2^-38 of the row's largest one; their sum
+ * is taken unrounded.
  * A sequence's keys are split over CTAs by rules that look at the whole batch,
  * so the last bits of its output may differ between batches; one call repeated
  * gives the same bits.
@@ -403,9 +406,10 @@ kascade_status kascade_qcache_append(const kascade_qcache* cache, int32_t n_kv_h
                                      const int32_t* slot_map, int32_t n_tokens, void* pages,
                                      void* ws, size_t ws_bytes, void* stream);
 
-/* The stored values of rows, in the same layouts (to attend over a cached
- * prefix with the prefill calls, or to calibrate on it); zeros for a negative
- * slot. Slots may repeat. */
+/* The stored values of rows, in the same layouts, for the calls that take
+ * contiguous keys and values (a prompt's prefill, which needs a query row for
+ * every key, or a calibration); zeros for a negative slot. Slots may repeat.
+ * The rows that are written must not overlap. */
 kascade_status kascade_qcache_read(const kascade_qcache* cache, int32_t n_kv_heads,
                                    int32_t head_dim, int32_t dtype, const void* pages,
                                    const int32_t* slot_map, int32_t n_tokens, void* k, void* v,

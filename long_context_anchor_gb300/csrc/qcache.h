@@ -33,7 +33,8 @@ struct QDecodeArgs {
   const int32_t* lens;        // [B] cached tokens
   void* out;                  // [B,Hq,d], q's type
   float* scores;              // [B,Hq,N] scaled logits, or null
-  float2* row_stat;           // [B*Hq] (max logit, 1 / sum exp(logit - max)), or null
+  float2* row_stat;           // [B*Hq] (reference, 1 / sum exp(logit - reference)), or null;
+                              // the reference is the largest logit or up to 1.75 ln 2 below it
   float* part;                // split partials
   unsigned int* counters;     // [B*Hkv] split arrival counters (self-resetting)
   unsigned int* err;

@@ -32,14 +32,17 @@ namespace {
 // move and every slot is made on its own.
 //
 // Everything is checked before anything is written: a step that cannot be
-// served changes nothing, leaves every slot -1 and records bad input. Small
-// steps run in one CTA and one launch; larger ones in two launches of many
-// CTAs, checks first, each CTA scanning the lengths for itself.
+// served changes nothing, leaves every slot -1 and records bad input. Steps over
+// a small pool with few new tokens run in one CTA and one launch; others in two
+// launches of many CTAs, checks first, each CTA scanning the lengths for itself.
 constexpr int kPlanThreads = 1024;
-// One launch up to this many blocks and new tokens. A step of 64 sequences,
-// half of them ending and half starting, all launches back to back on a GB300
-// (one CTA / two launches): 512 new tokens 5.1 / 8.0 us, 2048 6.6 / 7.5, 4096
-// 9.4 / 8.0, 32768 44 / 8.4.
+// One launch up to this many blocks of the pool (any of which a step may move: the
+// host does not know the lengths) and new tokens. A step of 64 sequences, half of
+// them ending and half starting, blocks of 16, a pool that holds both halves, calls
+// back to back in a graph on a GB300 (one CTA / two launches): 512 new tokens 5.3 /
+// 7.9 us, 2048 7.1 / 8.6, 4096 9.5 / 8.7, 32768 47 / 10. A step that moves
+// little over a large pool pays for the second launch: eight sequences that add a
+// token each take 3.3 us over 100 blocks and 6.1 over 4200.
 constexpr int kPlanOneCta = 2048;
 
 struct PlanScan {
@@ -284,7 +287,8 @@ __global__ void __launch_bounds__(kPlanThreads) k_qplan(const __grid_constant__ 
 // tokens x 8 heads x 128 in bf16, 86 MB). Reading takes pieces of 8 elements, whose
 // stores join into whole sectors (14.6 us, 18.4 with 16); writing takes whole
 // blocks of 16, which find their scale alone (15.6 us, 21.7 with two threads per
-// block). 5.5 and 5.9 TB/s, 0.81 and 0.87 of the copy rate.
+// block). 5.5 and 5.9 TB/s, 0.81 and 0.87 of the copy rate. The same rows in fp32,
+// 153 MB: 25.8 us to write (5.9 TB/s), 35.1 to read (4.4 TB/s, 0.64).
 constexpr int kRowThreads = 256;
 constexpr int kAppendPiece = 16, kReadPiece = 8;   // elements per thread
 

@@ -949,7 +949,9 @@ def qcache_dense_decode(q, pages, block_table, kv_lens, kv_len=None, group_map=N
     """Exact decode attention q [B,Hq,d] over the cached tokens of each sequence
     -> out [B,Hq,d], or (out, scores [B,Hq,kv_len] fp32 logits, -inf behind
     the last token). kv_len: the longest length any kv_lens[b] may have
-    (default: what the block table can hold)."""
+    (default: what the block table can hold). The workspace and the limits of a
+    call go by kv_len, not by the lengths themselves: give it where the table is
+    wide."""
     desc, geo, nbytes, (B, Hq, _, N), dev = _qattn(q, pages, block_table, kv_lens, kv_len,
                                                    group_map, scale, k_scale, v_scale, False, 0,
                                                    out)

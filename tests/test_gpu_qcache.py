@@ -9,6 +9,9 @@ magnitude the row averages over and e_s the error of a logit:
         fp16, half a step 2^-11; a logit error moves numerator and sum);
   fp32  2^-24 |out| + (2^-21 + n 2^-23 + 2 e_s) A (weights as two fp16 terms, fp32
         sums over n keys).
+  Weights are held as multiples of 2^-24 of 2^14 p: half a step adds 2^-39 p_max sum_j |v_j|,
+        which these bounds leave out. It matters where every heavy key's V is zero
+        (test_dense_weights_below_the_smallest_step has it).
 Everything the cache stores or plans is compared exactly."""
 import numpy as np
 import pytest
@@ -1038,3 +1041,34 @@ def test_reuse_stays_within_its_workspace(K, pooled, dtype):
     ws.buf = buf[:n]
     assert torch.equal(K.qcache_reuse_decode(*args, pooled=pooled, ws=ws), want)
     assert ws.device_error() == K.OK and bool((buf[n:] == 171).all())
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_dense_weights_below_the_smallest_step(K, dtype):
+    """One key takes nearly all the weight and its V is zero in half of the row, where keys of
+    2^-36 to 2^-44 of its weight decide: within the head's bounds and half a step per key."""
+    rng = np.random.default_rng(51)
+    n, d, bs = 3000, 64, 32
+    nb = (n + bs - 1) // bs
+    table = rng.permutation(nb).reshape(1, nb)
+    k = np.zeros((n, 1, d))
+    k[:, 0, 0] = -6.0
+    k[:, 0, 16] = rng.choice([-6.0, -3.0, -0.5, 0.0, 1.0, 4.0, 6.0], n)
+    k[:, 0, 1:16] = k[:, 0, 17:32] = 6.0      # these blocks' scale is 1
+    k[1234, 0, [0, 16]] = 0.0
+    v = rng.standard_normal((n, 1, d))
+    v[1234, 0, :32] = 0.0
+    pages = K.qcache_alloc(nb, 1, d, bs)
+    slots = table[0, np.arange(n) // bs] * bs + np.arange(n) % bs
+    rows = [torch.from_numpy(x).float().cuda() for x in (k, v)]
+    K.qcache_append(rows[0], rows[1], ints(slots), pages)
+    q = torch.zeros(1, 1, d)
+    q[0, 0, 0], q[0, 0, 16] = 40 * np.log(2) / 6, 4 * np.log(2) / 6
+    q = q.to(dtype).cuda()
+    out = K.qcache_dense_decode(q, pages, ints(table), ints([n]), kv_len=n, scale=1.0)
+    kk, vv = Q.rows_of(pages.cpu().numpy(), table[0], n, 0, d)
+    ref, _, p = Q.attention(f64(q)[0, 0], kk, vv, 1.0)
+    tol = bounds(f64(q)[0, 0], kk, vv, p, np.arange(n), ref, 1.0, dtype is F32)
+    tol += 2.0 ** -39 * p.max() * np.abs(vv).sum(0)
+    assert (np.abs(f64(out)[0, 0] - ref) <= tol).all()
+    assert np.abs(ref[:32]).max() < 1e-7 and np.abs(ref[32:]).max() > 0.1
