@@ -1072,3 +1072,155 @@ def test_dense_weights_below_the_smallest_step(K, dtype):
     tol += 2.0 ** -39 * p.max() * np.abs(vv).sum(0)
     assert (np.abs(f64(out)[0, 0] - ref) <= tol).all()
     assert np.abs(ref[:32]).max() < 1e-7 and np.abs(ref[32:]).max() > 0.1
+
+
+def test_every_call_on_another_stream(K):
+    """stream=: each entry point on a stream that is not the current one, its results those of
+    the current one."""
+    rng = np.random.default_rng(61)
+    B, Hq, Hkv, d, bs, width, nb, k = 3, 8, 2, 128, 16, 8, 30, 20
+    side = torch.cuda.Stream()
+    new = ints([70, 1, 33])
+    rows = torch.randn(2, 104, Hkv, d, device="cuda").to(BF)
+    more = [torch.randn(3, Hkv, d, device="cuda").to(BF) for _ in range(4)]
+    qs = [torch.randn(B, Hq, d, device="cuda").to(BF) for _ in range(2)]
+    order, one = ints(rng.permutation(nb)), ints([1, 1, 1])
+    ws = [K.Workspace(), K.Workspace()]
+    got = []
+    for w, kw in ((ws[0], {}), (ws[1], dict(stream=side))):
+        table, free, count = ints(np.full((B, width), -1)), order.clone(), ints([nb])
+        lens = ints([0] * B)
+        pages = [K.qcache_alloc(nb, Hkv, d, bs) for _ in range(2)]
+        torch.cuda.synchronize()
+        kw = dict(ws=w, **kw)
+        slots, cu, lens, count = K.qcache_plan(lens, new, table, free, count, bs, 104, **kw)
+        K.qcache_append(rows[0], rows[1], slots, pages[0], **kw)
+        K.qcache_append(rows[1], rows[0], slots, pages[1], **kw)
+        res = list(K.qcache_read(pages[0], slots, **kw))
+        res += list(K.qcache_dense_decode(qs[0], pages[0], table, lens, return_scores=True, **kw))
+        for pooled in (False, True):
+            res += list(K.qcache_anchor_decode(qs[0], pages[0], table, lens, k, pooled=pooled,
+                                               return_scores=True, **kw))
+            res.append(K.qcache_reuse_decode(qs[1], pages[1], table, lens, res[-2], pooled=pooled,
+                                             **kw))
+        outs, idx = K.qcache_run_stack(qs, pages, table, lens, k, [0], new_ks=more[:2],
+                                       new_vs=more[2:], new_lens=one, free_blocks=free,
+                                       free_count=count, **kw)
+        torch.cuda.synchronize()
+        assert w.device_error() == K.OK
+        got.append(res + list(outs) + [idx, slots, cu, lens, count, table, free] + pages)
+    assert len(got[0]) == len(got[1]) and all(torch.equal(x, y) for x, y in zip(*got))
+
+
+@pytest.mark.parametrize("pooled", [False, True])
+@pytest.mark.parametrize("dtype,anchors", [(BF, [1]), (F32, [0, 2]), (BF, [])])
+def test_stack_without_a_plan(K, dtype, anchors, pooled):
+    """Rows go to the caller's slots (some of them padding) and the lengths count them already;
+    group map, scale, cache scales and kv_len reach every layer."""
+    rng = np.random.default_rng(62)
+    lens, Hq, Hkv, d, bs, k, L = [90, 0, 41], 4, 2, 64, 16, 12, 4
+    gm = [1, 0, 0, 1]
+    cs = dict(k_scale=0.5, v_scale=4.0)
+    pages, table = filled(K, rng, lens, Hkv, d, bs, width=9, **cs)
+    pages = [pages.clone() for _ in range(L)]
+    T, dl = ints(table), ints(lens)
+    slots = ints([table[0, 5] * bs + 9, -1, table[2, 2] * bs + 8])     # the last tokens of 0 and 2
+    rows = lambda x: [torch.randn(3, Hkv, d, device="cuda").to(dtype) * x for _ in range(L)]
+    nk, nv = rows(0.5), rows(4.0)
+    qs = [torch.randn(3, Hq, d, device="cuda").to(dtype) for _ in range(L)]
+    kw = dict(kv_len=100, group_map=gm, scale=0.2, ws=K.Workspace(), **cs)
+    ref, want, idx = [p.clone() for p in pages], [], None
+    for l in range(L):
+        K.qcache_append(nk[l], nv[l], slots, ref[l], ws=kw["ws"], **cs)
+        a = (qs[l], ref[l], T, dl)
+        if l in anchors:
+            o, idx = K.qcache_anchor_decode(*a, k, pooled=pooled, **kw)
+        elif idx is not None:
+            o = K.qcache_reuse_decode(*a, idx, pooled=pooled, **kw)
+        else:
+            o = K.qcache_dense_decode(*a, **kw)
+        want.append(o)
+    outs, ib = K.qcache_run_stack(qs, pages, T, dl, k, anchors, new_ks=nk, new_vs=nv,
+                                  slot_map=slots, pooled=pooled, **kw)
+    assert kw["ws"].device_error() == K.OK
+    assert all(torch.equal(x, y) for x, y in zip(outs, want))
+    assert all(torch.equal(x, y) for x, y in zip(pages, ref))
+    assert idx is None or torch.equal(ib, idx)
+    assert torch.equal(dl, ints(lens)) and torch.equal(T, ints(table))
+    if 0 not in anchors:
+        check_attention(qs[0], outs[0], pages[0], table, lens, Hkv, d, gm, scale=0.2, **cs)
+
+
+def test_largest_plan(K):
+    """16384 sequences that start, grow, roll back and end in one step."""
+    rng = np.random.default_rng(63)
+    B, bs, width = 16384, 16, 3
+    nb = B * width
+    lens = rng.integers(0, width * bs + 1, B).tolist()
+    table = table_of(rng, lens, bs, nb, width)
+    held = set(table[table >= 0].tolist())
+    rest = [x for x in rng.permutation(nb).tolist() if x not in held]
+    free = np.full(nb, -1, dtype=np.int64)
+    free[:len(rest)] = rest
+    new = random_step(rng, lens, width, bs)
+    max_new = sum(max(0, x) for x in new)
+    want = Q.plan(lens, new, table, free, len(rest), bs, max_new)
+    d = [ints(x) for x in (lens, new, table, free, [len(rest)])]
+    ws = K.Workspace()
+    got = K.qcache_plan(*d, bs, max_new, ws=ws)
+    assert ws.device_error() == K.OK
+    for x, y in zip(got[:3], want[:3]):
+        assert np.array_equal(x.cpu().numpy(), y)
+    assert int(got[3]) == want[3] and np.array_equal(d[2].cpu().numpy(), want[4])
+    assert np.array_equal(d[3].cpu().numpy()[:want[3]], want[5][:want[3]])
+
+
+@pytest.mark.parametrize("pooled", [False, True])
+def test_longest_sets_per_query_head(K, pooled):
+    """kv_len 262144, the most that sets per query head take: one full sequence beside short
+    and empty ones, the anchor's sets exact on its own scores, the reuse layer on them."""
+    rng = np.random.default_rng(64)
+    lens, Hq, Hkv, d, bs, k = [262144, 3, 0, 5000], 4, 2, 64, 256, 1500
+    pages, table = filled(K, rng, lens, Hkv, d, bs)
+    q = torch.from_numpy(rng.standard_normal((4, Hq, d))).to(BF).cuda()
+    ws = K.Workspace()
+    kw = dict(kv_len=262144, pooled=pooled, ws=ws)
+    args = (q, pages, ints(table), ints(lens))
+    out, idx, sc = K.qcache_anchor_decode(*args, k, return_scores=True, **kw)
+    again = K.qcache_reuse_decode(*args, idx, **kw)
+    assert ws.device_error() == K.OK
+    sn, got = f64(sc), idx.cpu().numpy()
+    sets = [[] for _ in lens]
+    for b, n in enumerate(lens):
+        for h in range(Hkv if pooled else Hq):
+            m = min(k, n)
+            want = topk_indices(sn[b, h, :n], m) if m else np.zeros(0, dtype=np.int64)
+            assert np.array_equal(got[b, h, :m], want) and (got[b, h, m:] == -1).all()
+            assert (sn[b, h, n:] == -np.inf).all()
+            sets[b].append(want)
+    kv = [h // (Hq // Hkv) for h in range(Hq)]
+    check_attention(q, out, pages, table, lens, Hkv, d, kv)
+    check_attention(q, again, pages, table, lens, Hkv, d, kv, sets=sets, pooled=pooled)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_nan_and_infinite_queries_stay_in_their_head(K, d, dtype):
+    """Over every key and over sets: the head's own output is NaN, the others within bounds."""
+    rng = np.random.default_rng(65)
+    lens, Hq, bs, k = [300, 70], 8, 32, 40
+    pages, table = filled(K, rng, lens, 1, d, bs)
+    q = torch.from_numpy(rng.standard_normal((2, Hq, d))).to(dtype).cuda()
+    sets, idx = random_sets(rng, lens, Hq, k)
+    args = (pages, ints(table), ints(lens))
+    bad = q.clone()
+    bad[0, 2, 5], bad[1, 7, 0], bad[1, 0, d - 1] = float("nan"), float("inf"), -float("inf")
+    hit = np.zeros((2, Hq), dtype=bool)
+    hit[0, 2] = hit[1, 7] = hit[1, 0] = True
+    for run, s in ((lambda x: K.qcache_dense_decode(x, *args), None),
+                   (lambda x: K.qcache_reuse_decode(x, *args, ints(idx)), sets)):
+        out = run(bad)
+        nan = torch.isnan(out).cpu().numpy()
+        assert (nan.all(-1) == hit).all() and (nan.any(-1) == hit).all()
+        fixed = torch.where(torch.from_numpy(hit).cuda()[..., None], run(q), out)
+        check_attention(q, fixed, pages, table, lens, 1, d, [0] * Hq, sets=s)
