@@ -621,7 +621,9 @@ def kascade_attention(qs, ks, vs, topk, anchors, group_map=None, scale=None, poo
 # The pages (one uint8 tensor per layer, qcache_alloc) hold num_blocks blocks of
 # block_size tokens, [num_blocks, Hkv, block_size/16, 18*d]; a block table
 # [B, max_blocks] lists each sequence's blocks and kv_lens [B] its cached
-# tokens. Number format, layout and error behaviour: include/kascade.h.
+# tokens. Number format, layout and error behaviour: include/kascade.h. stream=:
+# the torch.cuda.Stream to work on instead of the current one; its inputs have
+# to be ready on it, and its outputs belong to it.
 
 def qcache_alloc(num_blocks, n_kv_heads, head_dim, block_size=64, device="cuda"):
     """Zeroed pages of one layer: uint8 [num_blocks, Hkv, block_size/16, 18*d]."""
@@ -672,16 +674,21 @@ def _elsewhere(index, stream):
     return stream is not None or (index >= 0 and index != _current_device())
 
 
-def _on(dev, stream):
+def _on(dev, stream, *tensors):
     """Context in which the tensors' device and the call's stream are current,
     so that what the call allocates belongs to that stream; inside it the call
-    is made again without a stream."""
+    is made again without a stream. The stream is noted on the call's tensors
+    (None among them: not given), so that the memory of one that the caller drops
+    is not given out again while the stream still reads or writes it."""
     if dev.type != "cuda":      # only reachable with a stand-in library
         return contextlib.nullcontext()
     if stream is None:
         return torch.cuda.device(dev)
     if stream.device != dev:
         raise ValueError("stream: on %s, expected %s" % (stream.device, dev))
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
     return torch.cuda.stream(stream)
 
 
@@ -791,7 +798,8 @@ def qcache_plan(kv_lens, new_lens, block_table, free_blocks, free_count, block_s
     geo = _qgeo(int(block_size), free_blocks.shape[0], width, 0.0, 0.0)
     index = block_table.get_device()
     if _elsewhere(index, stream):
-        with _on(dev, stream):
+        with _on(dev, stream, kv_lens, new_lens, block_table, free_blocks, free_count,
+                 kv_lens_out, free_count_out):
             return qcache_plan(kv_lens, new_lens, block_table, free_blocks, free_count, block_size,
                                max_new, kv_lens_out, free_count_out, ws)
     # one by one: an allocation and three views of it take 2 us longer
@@ -854,7 +862,7 @@ def qcache_append(k, v, slot_map, pages, k_scale=1.0, v_scale=1.0, ws=None, stre
     geo = _qgeo(bs, nb, 1, float(k_scale), float(v_scale))
     index = pages.get_device()
     if _elsewhere(index, stream):
-        with _on(dev, stream):
+        with _on(dev, stream, k, v, slot_map, pages):
             return qcache_append(k, v, slot_map, pages, k_scale, v_scale, ws)
     buf = _qws(ws, dev, index, 256)
     _check(_lib.kascade_qcache_append(geo, hkv, d, code, k.data_ptr(), v.data_ptr(),
@@ -893,7 +901,7 @@ def qcache_read(pages, slot_map, dtype=torch.bfloat16, k_scale=1.0, v_scale=1.0,
     geo = _qgeo(bs, nb, 1, float(k_scale), float(v_scale))
     index = pages.get_device()
     if _elsewhere(index, stream):
-        with _on(dev, stream):
+        with _on(dev, stream, pages, slot_map, k, v):
             return qcache_read(pages, slot_map, dtype, k_scale, v_scale, k, v, ws)
     ok = torch.empty(shape, dtype=dtype, device=dev) if k is None else k
     ov = torch.empty(shape, dtype=dtype, device=dev) if v is None else v
@@ -957,7 +965,7 @@ def qcache_dense_decode(q, pages, block_table, kv_lens, kv_len=None, group_map=N
                                                    out)
     index = pages.get_device()
     if _elsewhere(index, stream):
-        with _on(dev, stream):
+        with _on(dev, stream, q, pages, block_table, kv_lens, out):
             return qcache_dense_decode(q, pages, block_table, kv_lens, kv_len, group_map, scale,
                                        k_scale, v_scale, return_scores, out, ws)
     o = torch.empty_like(q) if out is None else out
@@ -988,7 +996,7 @@ def qcache_anchor_decode(q, pages, block_table, kv_lens, topk, kv_len=None, grou
         _fits(idx, "idx", (B, H, topk), torch.int32, dev)
     index = pages.get_device()
     if _elsewhere(index, stream):
-        with _on(dev, stream):
+        with _on(dev, stream, q, pages, block_table, kv_lens, out, idx):
             return qcache_anchor_decode(q, pages, block_table, kv_lens, topk, kv_len, group_map, scale,
                                         k_scale, v_scale, return_scores, out, idx, ws,
                                         pooled=pooled)
@@ -1019,7 +1027,7 @@ def qcache_reuse_decode(q, pages, block_table, kv_lens, idx, kv_len=None, group_
     _fits(idx, "idx", (B, hkv if pooled else Hq, topk), torch.int32, dev)
     index = pages.get_device()
     if _elsewhere(index, stream):
-        with _on(dev, stream):
+        with _on(dev, stream, q, pages, block_table, kv_lens, idx, out):
             return qcache_reuse_decode(q, pages, block_table, kv_lens, idx, kv_len, group_map, scale,
                                        k_scale, v_scale, out, ws, pooled=pooled)
     o = torch.empty_like(q) if out is None else out
@@ -1083,7 +1091,9 @@ def qcache_run_stack(qs, pages, block_table, kv_lens, topk, anchors, new_ks=None
         _fits(idx_buf, "idx_buf", (B, H, max(topk, 1)), torch.int32, dev)
     index = qs[0].get_device()
     if _elsewhere(index, stream):
-        with _on(dev, stream):
+        lists = [ts for ts in (qs, pages, new_ks, new_vs, outs) if ts is not None]
+        with _on(dev, stream, block_table, kv_lens, new_lens, free_blocks, free_count, slot_map,
+                 cu_new, idx_buf, *(t for ts in lists for t in ts)):
             return qcache_run_stack(qs, pages, block_table, kv_lens, topk, anchors, new_ks, new_vs,
                                     new_lens, free_blocks, free_count, slot_map, cu_new, kv_len,
                                     group_map, scale, k_scale, v_scale, outs, idx_buf, ws,

@@ -1224,3 +1224,55 @@ def test_nan_and_infinite_queries_stay_in_their_head(K, d, dtype):
         assert (nan.all(-1) == hit).all() and (nan.any(-1) == hit).all()
         fixed = torch.where(torch.from_numpy(hit).cuda()[..., None], run(q), out)
         check_attention(q, fixed, pages, table, lens, 1, d, [0] * Hq, sets=s)
+
+
+def test_dropped_inputs_of_another_stream_are_not_given_out_again(K):
+    """Tensors that the caller drops while the stream has yet to read them keep their memory.
+    The stream waits behind a bounded delay, so the call has not run when they are dropped."""
+    rng = np.random.default_rng(66)
+    B, Hq, Hkv, d, bs, width, nb, k = 2, 8, 2, 128, 16, 8, 20, 10
+    side, ws = torch.cuda.Stream(), K.Workspace()
+    lens = [100, 37]
+    pages, table = filled(K, rng, lens, Hkv, d, bs, width=width, spare=nb)
+    _, idx = random_sets(rng, lens, Hq, k)
+    nblk = pages.shape[0]
+    fresh = dict(
+        q=lambda: torch.randn(B, Hq, d, device="cuda").to(BF), pages=lambda: pages.clone(),
+        block_table=lambda: ints(table), kv_lens=lambda: ints(lens), idx=lambda: ints(idx),
+        rows=lambda: torch.randn(2, Hkv, d, device="cuda").to(BF), slot_map=lambda: ints([-1, -1]),
+        new_lens=lambda: ints([0, 0]), free_blocks=lambda: ints([-1] * nblk),
+        free_count=lambda: ints([0]))
+    attn = ("q", "pages", "block_table", "kv_lens")
+    step = ("block_table", "kv_lens", "new_lens", "free_blocks", "free_count")
+    calls = [
+        (lambda t: K.qcache_dense_decode(*[t[x] for x in attn], ws=ws, stream=side), attn),
+        (lambda t: K.qcache_anchor_decode(*[t[x] for x in attn], k, ws=ws, stream=side), attn),
+        (lambda t: K.qcache_reuse_decode(*[t[x] for x in attn], t["idx"], ws=ws, stream=side),
+         attn + ("idx",)),
+        (lambda t: K.qcache_append(t["rows"], t["rows"], t["slot_map"], t["pages"], ws=ws,
+                                   stream=side), ("rows", "slot_map", "pages")),
+        (lambda t: K.qcache_read(t["pages"], t["slot_map"], ws=ws, stream=side),
+         ("slot_map", "pages")),
+        (lambda t: K.qcache_plan(t["kv_lens"], t["new_lens"], *[t[x] for x in (
+            "block_table", "free_blocks", "free_count")], bs, 4, ws=ws, stream=side), step),
+        (lambda t: K.qcache_run_stack([t["q"]], [t["pages"]], t["block_table"], t["kv_lens"], k, [0],
+                                      new_ks=[t["rows"]], new_vs=[t["rows"]],
+                                      new_lens=t["new_lens"], free_blocks=t["free_blocks"],
+                                      free_count=t["free_count"], ws=ws, stream=side),
+         ("q", "pages", "rows") + step)]
+    for call, names in calls:
+        first, t = ({n: fresh[n]() for n in names} for _ in range(2))
+        old = {n: (x.data_ptr(), x.shape, x.dtype) for n, x in t.items()}
+        torch.cuda.synchronize()
+        call(first)                                      # sizes the workspace
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(100_000_000)               # about 50 ms
+        kept = call(t)
+        t.clear()
+        new = [torch.empty(s, dtype=ty, device="cuda") for _, s, ty in old.values()]
+        assert not side.query()                          # it has not come to the call yet
+        assert not {x.data_ptr() for x in new} & {p for p, _, _ in old.values()}, names
+        torch.cuda.synchronize()
+        del kept, new
+    assert ws.device_error() == K.OK
