@@ -195,7 +195,8 @@ class Workspace:
         self.captured = False     # a graph holds the buffer's address
 
     def get(self, nbytes: int, stream=None) -> torch.Tensor:
-        if self.buf is None or self.buf.numel() < nbytes:
+        old = self.buf
+        if old is None or old.numel() < nbytes:
             if self.captured:
                 raise RuntimeError("this workspace was captured into a CUDA graph, which holds its "
                                    "address: it cannot grow to %d bytes (use another one, or size "
@@ -203,7 +204,18 @@ class Workspace:
             self.buf = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=self.device)
             _check(_lib.kascade_workspace_init(_ptr(self.buf), self.buf.numel(), _stream(stream)),
                    "kascade_workspace_init")
+            if old is not None and not (old.is_cuda and torch.cuda.is_current_stream_capturing()):
+                self._carry(old, stream)
         return self.buf
+
+    def _carry(self, old, stream):
+        """A device error that waits to be read in the smaller buffer goes into the new one."""
+        if not old.is_cuda:
+            self.buf[:8].copy_(old[:8])
+            return
+        s = stream if stream is not None else torch.cuda.current_stream(old.device)
+        with torch.cuda.stream(s):
+            self.buf[:8].copy_(old[:8])
 
     def check_wait_timeout(self, stream=None) -> int:
         """Run one device wait that can only time out; returns the device error status."""

@@ -1276,3 +1276,19 @@ def test_dropped_inputs_of_another_stream_are_not_given_out_again(K):
         torch.cuda.synchronize()
         del kept, new
     assert ws.device_error() == K.OK
+
+
+def test_growing_workspace_keeps_the_error(K):
+    """A refused plan in a workspace of 256 bytes is still reported after a call that grows it."""
+    rng = np.random.default_rng(67)
+    lens, d, bs = [100, 50], 64, 16
+    pages, table = filled(K, rng, lens, 1, d, bs, width=8)
+    ws = K.Workspace()
+    K.qcache_plan(ints([-1, 50]), ints([1, 1]), ints(table), ints([-1] * pages.shape[0]), ints([0]),
+                  bs, 2, ws=ws)
+    small = ws.buf.numel()
+    q = torch.randn(2, 2, d, device="cuda").to(BF)
+    out = K.qcache_dense_decode(q, pages, ints(table), ints(lens), ws=ws)
+    assert ws.buf.numel() > small
+    assert ws.device_error() == K.BAD_INPUT and ws.device_error() == K.OK
+    assert torch.equal(out, K.qcache_dense_decode(q, pages, ints(table), ints(lens)))

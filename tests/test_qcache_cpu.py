@@ -377,3 +377,10 @@ def test_reuse_workspace_holds_no_logits(K, pooled):
                                           reuse, None) == K.WORKSPACE
     size = L.kascade_qcache_reuse_workspace_size
     assert size(ref(desc), ref(geo), 0) == 0 and size(ref(desc), None, 1) == 0
+
+
+def test_growing_workspace_keeps_the_error_word(K, fake):
+    ws = K.Workspace("cpu")
+    ws.get(256)[:8] = torch.tensor([16, 0, 0, 0, 1, 5, 0, 0], dtype=torch.uint8)
+    assert ws.get(4096).numel() == 4096
+    assert ws.buf[:8].tolist() == [16, 0, 0, 0, 1, 5, 0, 0]
