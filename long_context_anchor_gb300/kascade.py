@@ -209,11 +209,14 @@ class Workspace:
         return self.buf
 
     def _carry(self, old, stream):
-        """A device error that waits to be read in the smaller buffer goes into the new one."""
+        """A device error that waits to be read in the smaller buffer goes into the new
+        one; the old one's memory is kept until the stream, which may be another than
+        its own, has done with it."""
         if not old.is_cuda:
             self.buf[:8].copy_(old[:8])
             return
         s = stream if stream is not None else torch.cuda.current_stream(old.device)
+        old.record_stream(s)
         with torch.cuda.stream(s):
             self.buf[:8].copy_(old[:8])
 

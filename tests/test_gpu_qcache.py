@@ -1292,3 +1292,31 @@ def test_growing_workspace_keeps_the_error(K):
     assert ws.buf.numel() > small
     assert ws.device_error() == K.BAD_INPUT and ws.device_error() == K.OK
     assert torch.equal(out, K.qcache_dense_decode(q, pages, ints(table), ints(lens)))
+
+
+def test_growing_workspace_keeps_the_old_memory_for_its_stream(K):
+    """The buffer that a growing workspace drops, last used on another stream than its own, is
+    not given out again before that stream has come past its calls."""
+    rng = np.random.default_rng(68)
+    lens, d, bs = [100, 50], 64, 16
+    pages, table = filled(K, rng, lens, 1, d, bs, width=8)
+    T, dl, slots = ints(table), ints(lens), ints([-1])
+    x = torch.zeros(1, 1, d, device="cuda").to(BF)
+    q = torch.randn(2, 2, d, device="cuda").to(BF)
+    side, ws = torch.cuda.Stream(), K.Workspace()
+    ws.get(3 << 20)                                      # on the current stream
+    old = ws.buf.data_ptr()
+    n = K.Workspace()
+    K.qcache_anchor_decode(q, pages, T, dl, 10, ws=n)
+    want = n.buf.numel()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)                   # about 50 ms
+    K.qcache_append(x, x, slots, pages, ws=ws, stream=side)
+    with torch.cuda.stream(side):
+        ws.get(max(want, 4 << 20))
+    new = torch.empty(3 << 20, dtype=torch.uint8, device="cuda")
+    assert not side.query() and new.data_ptr() != old and ws.buf.data_ptr() != old
+    K.qcache_anchor_decode(q, pages, T, dl, 10, ws=ws, stream=side)
+    torch.cuda.synchronize()
+    assert ws.device_error() == K.OK
