@@ -240,7 +240,8 @@ _default_ws = {}
 def default_workspace(device, stream=None) -> Workspace:
     """The workspace of calls that name none: one per device, and one more per
     stream other than the device's default one for the cache calls (qcache_*),
-    so that those on two streams do not share one. stream: torch.cuda.Stream."""
+    so that those on two streams do not share one. Threads that call on one stream
+    at a time need a workspace each. stream: torch.cuda.Stream."""
     dev = torch.device(device)
     index = dev.index if dev.index is not None else torch.cuda.current_device()
     raw = 0 if stream is None else stream.cuda_stream
