@@ -307,6 +307,44 @@ kascade_status kascade_run_stack_profiled(const kascade_desc* desc, int32_t mode
                                           void* ws, size_t ws_bytes, void* stream,
                                           void* const* layer_events);
 
+/* ------------------------------------------------------------- rotation -- */
+/* Attention takes queries and keys that are turned by their positions (the
+ * pages say nothing about that; their layers' q and k are the turned ones). */
+
+/* A rotation. Pair i of a head's row is elements (i, i + n_pairs), or
+ * (2i, 2i + 1) where interleaved; elements from 2*n_pairs on stay as they are. A
+ * token at position p turns pair i by table[p][0][i] (cosine) and
+ * table[p][1][i] (sine): (a, b) -> (a c - b s, b c + a s), every product and
+ * sum rounded to fp32. With several axes (a video's time, height and width) a token
+ * has a position on each, and axes[i] names the one that pair i follows. */
+typedef struct {
+  const float* table;    /* device [n_positions][2][n_pairs], 16-byte aligned */
+  int32_t n_positions;
+  int32_t n_pairs;       /* a multiple of 16, 2*n_pairs <= head_dim */
+  int32_t interleaved;
+  int32_t n_axes;        /* 1 .. 4 */
+  const int32_t* axes;   /* host [n_pairs], read during the call; NULL: axis 0 */
+} kascade_rope;
+
+/* Queries and keys for the attention calls, in one pass: a head's row x
+ * becomes x * rsqrt(mean(x^2) + eps) * weight (weights [head_dim] of the rows'
+ * type; NULL: left out), then is turned (rope NULL: not turned, positions
+ * unused), in fp32, rounded once. q and k: row (b, t, h) of head_dim contiguous
+ * elements at q + b*strides[0] + t*strides[1] + h*strides[2], k likewise with
+ * strides[3..5], q_out and k_out with strides[6..8] and [9..11] (host array,
+ * elements, multiples of 16 bytes). q_out and k_out may be q and k with the same
+ * strides; other overlaps are not allowed. n_q_heads or n_kv_heads may be 0.
+ * positions [n_axes][batch][n_tokens] int32; one outside the table sets
+ * KASCADE_ERR_BAD_INPUT on the device, and its pairs are not turned.
+ * batch*n_tokens < 2^28. ws: the workspace header, 256 bytes. */
+kascade_status kascade_qk_norm_rope(const kascade_rope* rope, int32_t batch, int32_t n_tokens,
+                                    int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                    int32_t dtype, const void* q, const void* k,
+                                    const void* q_weight, const void* k_weight, float eps,
+                                    const int32_t* positions, void* q_out, void* k_out,
+                                    const int64_t* strides, void* ws, size_t ws_bytes,
+                                    void* stream);
+
 /* ------------------------------------------- paged 4-bit key/value cache -- */
 /* Decode for a server's cache: sequences of different lengths, each a list of
  * fixed-size blocks, keys and values held in 4 bits (the pages describe
@@ -405,6 +443,28 @@ kascade_status kascade_qcache_append(const kascade_qcache* cache, int32_t n_kv_h
                                      const void* v, const int64_t* strides,
                                      const int32_t* slot_map, int32_t n_tokens, void* pages,
                                      void* ws, size_t ws_bytes, void* stream);
+
+/* kascade_qcache_append of rows that are normalised (k_weight not NULL) and
+ * turned on their way (kascade_qk_norm_rope; the turned key is quantised from
+ * its fp32 elements; values are stored as they are), and the same for the queries
+ * of the step (q not NULL; n_q_heads heads). Positions come in one of two ways:
+ *   positions [n_axes][n_tokens]: row t of k, v and q is token t; cu_new and
+ *     kv_lens are NULL and n_seqs 0;
+ *   cu_new [n_seqs+1] and kv_lens [n_seqs] as kascade_qcache_plan wrote them
+ *     (positions NULL): row t of k and v is its new token t, and row b of q
+ *     the query of sequence b's last token. All axes have that one position.
+ * strides: k (tokens, heads), v, q, q_out: eight. q_out may be q with the same
+ * strides. Queries are written whatever their token's slot. A position outside
+ * the table sets KASCADE_ERR_BAD_INPUT, and its row is not turned. */
+kascade_status kascade_qcache_append_rope(const kascade_qcache* cache, const kascade_rope* rope,
+                                          int32_t n_q_heads, int32_t n_kv_heads,
+                                          int32_t head_dim, int32_t dtype, const void* k,
+                                          const void* v, const void* q, const int64_t* strides,
+                                          const void* k_weight, const void* q_weight, float eps,
+                                          const int32_t* slot_map, int32_t n_tokens,
+                                          const int32_t* positions, const int32_t* cu_new,
+                                          const int32_t* kv_lens, int32_t n_seqs, void* pages,
+                                          void* q_out, void* ws, size_t ws_bytes, void* stream);
 
 /* The stored values of rows, in the same layouts, for the calls that take
  * contiguous keys and values (a prompt's prefill, which needs a query row for

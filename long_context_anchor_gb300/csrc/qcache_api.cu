@@ -11,6 +11,7 @@
 #include "common.cuh"
 #include "kascade.h"
 #include "qcache.h"
+#include "rope.h"
 
 namespace kascade {
 namespace {
@@ -391,6 +392,68 @@ kascade_status kascade_qcache_append(const kascade_qcache* cache, int32_t n_kv_h
   a.scale[0] = 1.f / c.k_scale;
   a.scale[1] = 1.f / c.v_scale;
   return status_of(launch_qappend(a, dtype, static_cast<cudaStream_t>(stream)));
+}
+
+kascade_status kascade_qcache_append_rope(
+    const kascade_qcache* cache, const kascade_rope* rope, int32_t n_q_heads, int32_t n_kv_heads,
+    int32_t head_dim, int32_t dtype, const void* k, const void* v, const void* q,
+    const int64_t* strides, const void* k_weight, const void* q_weight, float eps,
+    const int32_t* slot_map, int32_t n_tokens, const int32_t* positions, const int32_t* cu_new,
+    const int32_t* kv_lens, int32_t n_seqs, void* pages, void* q_out, void* ws, size_t ws_bytes,
+    void* stream) {
+  QCacheShape c;
+  kascade_status r = check_rows(cache, n_kv_heads, head_dim, dtype, k, v, strides, slot_map,
+                                n_tokens, pages, c);
+  if (r != KASCADE_OK) return r;
+  RopeAppendArgs a{};
+  if ((r = check_rope(rope, head_dim, eps, a.rope)) != KASCADE_OK) return r;
+  const bool planned = positions == nullptr && (cu_new != nullptr || kv_lens != nullptr);
+  if (planned ? (!aligned(cu_new, 4) || !aligned(kv_lens, 4) || n_seqs < 1)
+              : (cu_new != nullptr || kv_lens != nullptr || n_seqs != 0))
+    return KASCADE_ERR_INVALID_ARG;
+  if (n_seqs > kMaxCounterUnits) return KASCADE_ERR_UNSUPPORTED;
+  if (rope != nullptr && n_tokens > 0 && !planned && !aligned(positions, 4))
+    return KASCADE_ERR_INVALID_ARG;
+  const int64_t unit = dtype == KASCADE_F32 ? 4 : 8;
+  a.Tq = planned ? n_seqs : n_tokens;
+  if (q == nullptr || a.Tq == 0) {
+    a.Tq = 0;
+  } else {
+    if (n_q_heads < 1 || n_q_heads > kMaxQHeads || !aligned(q, 16) || !aligned(q_out, 16) ||
+        (q_weight != nullptr && !aligned(q_weight, 16)))
+      return KASCADE_ERR_INVALID_ARG;
+    for (int i = 4; i < 8; ++i)
+      if (strides[i] < 0 || strides[i] % unit != 0) return KASCADE_ERR_INVALID_ARG;
+  }
+  if (k_weight != nullptr && !aligned(k_weight, 16)) return KASCADE_ERR_INVALID_ARG;
+  if (!check_small_ws(ws, ws_bytes)) return KASCADE_ERR_WORKSPACE;
+  a.k = k;
+  a.v = v;
+  a.q = q;
+  a.q_out = q_out;
+  a.weight[0] = q_weight;
+  a.weight[1] = k_weight;
+  for (int i = 0; i < 2; ++i) {
+    a.k_stride[i] = strides[i];
+    a.v_stride[i] = strides[2 + i];
+    a.q_stride[i] = strides[4 + i];
+    a.out_stride[i] = strides[6 + i];
+  }
+  a.slot_map = slot_map;
+  a.positions = positions;
+  a.cu_new = cu_new;
+  a.kv_lens = kv_lens;
+  a.cache = static_cast<uint8_t*>(pages);
+  a.err = static_cast<unsigned int*>(ws);
+  a.T = n_tokens;
+  a.n_seqs = n_seqs;
+  a.Hq = n_q_heads;
+  a.Hkv = n_kv_heads;
+  a.bs_shift = c.bs_shift;
+  a.num_blocks = c.num_blocks;
+  a.unit[0] = 1.f / c.k_scale;
+  a.unit[1] = 1.f / c.v_scale;
+  return status_of(launch_qappend_rope(a, head_dim, dtype, static_cast<cudaStream_t>(stream)));
 }
 
 kascade_status kascade_qcache_read(const kascade_qcache* cache, int32_t n_kv_heads,

@@ -45,6 +45,13 @@ class QCache(ctypes.Structure):
                 ("v_scale", ctypes.c_float)]
 
 
+class Rope(ctypes.Structure):
+    """kascade_rope: a rotation table and how its pairs lie in a head."""
+    _fields_ = [("table", ctypes.c_void_p), ("n_positions", ctypes.c_int32),
+                ("n_pairs", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("n_axes", ctypes.c_int32), ("axes", ctypes.POINTER(ctypes.c_int32))]
+
+
 class QCacheStep(ctypes.Structure):
     """kascade_qcache_step: the device state one decode step works on."""
     _fields_ = [(n, ctypes.c_void_p) for n in ("block_table", "kv_lens", "new_lens", "free_blocks",
@@ -55,6 +62,7 @@ class QCacheStep(ctypes.Structure):
 _vp, _i32, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
 _DP = ctypes.POINTER(Desc)
 _QP, _I64P = ctypes.POINTER(QCache), ctypes.POINTER(ctypes.c_int64)
+_RP = ctypes.POINTER(Rope)
 _SIGS = {
     "kascade_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "kascade_workspace_size": (_sz, [_DP, _i32, _i32]),
@@ -85,6 +93,11 @@ _SIGS = {
                                                   ctypes.POINTER(_vp), ctypes.POINTER(_vp), _i32,
                                                   ctypes.POINTER(_i32), _i32, ctypes.POINTER(_vp),
                                                   _vp, _vp, _sz, _vp, ctypes.POINTER(_vp)]),
+    "kascade_qk_norm_rope": (ctypes.c_int, [_RP] + [_i32] * 6 + [_vp] * 4 + [ctypes.c_float] +
+                             [_vp] * 3 + [_I64P, _vp, _sz, _vp]),
+    "kascade_qcache_append_rope": (ctypes.c_int, [_QP, _RP] + [_i32] * 4 + [_vp] * 3 +
+                                   [_I64P, _vp, _vp, ctypes.c_float, _vp, _i32] + [_vp] * 3 +
+                                   [_i32, _vp, _vp, _vp, _sz, _vp]),
     "kascade_qcache_bytes": (_sz, [_QP, _i32, _i32]),
     "kascade_qcache_workspace_size": (_sz, [_DP, _QP, _i32]),
     "kascade_qcache_reuse_workspace_size": (_sz, [_DP, _QP, _i32]),
@@ -833,6 +846,7 @@ def qcache_plan(kv_lens, new_lens, block_table, free_blocks, free_count, block_s
 
 
 _I64x4 = ctypes.c_int64 * 4
+_I64x8, _I64x12 = ctypes.c_int64 * 8, ctypes.c_int64 * 12
 _ROW_CODES = {torch.bfloat16: (BF16, 8), torch.float32: (F32, 4)}   # code, elements per 16 bytes
 
 
@@ -887,6 +901,222 @@ def qcache_append(k, v, slot_map, pages, k_scale=1.0, v_scale=1.0, ws=None, stre
                                       buf.data_ptr(), buf.numel(), _raw_stream(index)),
            "kascade_qcache_append")
     return pages
+
+
+# ---------------------------------------------------------------- rotation --
+
+def rope_table(inv_freq, n_positions, scale=1.0, device="cuda"):
+    """The rotation table of inverse frequencies inv_freq (radians per position, one
+    per pair): float32 [n_positions, 2, pairs], cosines then sines, times `scale`,
+    from angles in 64 bits (a program makes it once)."""
+    freq = torch.as_tensor(inv_freq, dtype=torch.float64).to(device)
+    if freq.dim() != 1:
+        raise ValueError("inv_freq: expected one number per pair")
+    angle = torch.arange(int(n_positions), dtype=torch.float64, device=device).unsqueeze(1) * freq
+    return torch.stack((torch.cos(angle), torch.sin(angle)), 1).mul_(float(scale)).float()
+
+
+@functools.lru_cache(maxsize=64)
+def _axes_array(axes):
+    return (ctypes.c_int32 * len(axes))(*axes)
+
+
+def _rope(rope, interleaved, axes, positions, shape, dev):
+    """A kascade_rope (a ctypes structure, None: nothing is turned) of a checked
+    table; positions are int32 of `shape`, behind an axis per position axis where
+    axes names several."""
+    if rope is None:
+        if axes is not None or positions is not None:
+            raise ValueError("positions and axes need a rotation table (rope)")
+        return None
+    if not isinstance(rope, torch.Tensor) or rope.dim() != 3 or rope.shape[1] != 2:
+        raise ValueError("rope: expected a float32 tensor [positions, 2, pairs]")
+    _fits(rope, "rope", rope.shape, torch.float32, dev)
+    n_axes, ptr = 1, None
+    if axes is not None:
+        axes = tuple(axes)
+        if len(axes) != rope.shape[2]:
+            raise ValueError("axes: %d entries for %d pairs" % (len(axes), rope.shape[2]))
+        n_axes = max(axes) + 1
+        if isinstance(positions, torch.Tensor) and positions.dim() == len(shape) + 1:
+            n_axes = max(n_axes, positions.shape[0])
+        ptr = _axes_array(axes)
+        shape = (n_axes,) + tuple(shape)
+    if positions is not None:
+        _fits(positions, "positions", shape, torch.int32, dev)
+    return Rope(rope.data_ptr(), rope.shape[0], rope.shape[2], 1 if interleaved else 0, n_axes,
+                ptr)
+
+
+def _head_strides(t, name, shape, dtype, dev, unit, out=False):
+    """(sequence, token, head) strides of rows [T,H,d] or [B,H,N,d], which must be
+    contiguous and start on 16-byte boundaries; an output's must not overlap."""
+    if not (isinstance(t, torch.Tensor) and t.shape == shape and t.dtype is dtype
+            and t.device == dev):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError("%s: expected a torch.Tensor" % name)
+        if t.shape != shape:
+            raise ValueError("%s: shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
+        if t.dtype is not dtype:
+            raise TypeError("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
+        raise ValueError("%s: on %s, expected %s" % (name, t.device, dev))
+    st = [x if n > 1 else 0 for x, n in zip(t.stride(), shape)]
+    if t.numel():
+        if t.stride(-1) != 1 or any(x % unit for x in st[:-1]) or t.data_ptr() % 16:
+            raise ValueError("%s: rows must be contiguous and start on 16-byte boundaries" % name)
+        if out and any(x == 0 and n > 1 for x, n in zip(st, shape)):
+            raise ValueError("%s: output rows must not overlap" % name)
+    return (0, st[0], st[1]) if len(shape) == 3 else (st[0], st[2], st[1])
+
+
+def _same_place(src, out, name):
+    """An output may be the input itself, not the same memory in another order."""
+    if out is not None and out.data_ptr() == src.data_ptr() and out.stride() != src.stride() \
+            and src.numel():
+        raise ValueError("%s: the input's memory in another order" % name)
+
+
+def _weight(w, name, d, dtype, dev):
+    if w is None:
+        return None
+    _fits(w, name, (d,), dtype, dev)
+    return w.data_ptr()
+
+
+def qk_norm_rope(q, k=None, positions=None, rope=None, q_weight=None, k_weight=None, eps=1e-6,
+                 interleaved=False, axes=None, q_out=None, k_out=None, ws=None, stream=None):
+    """Queries and keys for the attention calls in one pass: each head's row over its
+    root mean square times a weight [d] (where one is given), then turned by its
+    position. q [T,Hq,d] and k [T,Hkv,d] with positions [T], or q [B,Hq,N,d] and k
+    [B,Hkv,N,d] with positions [B,N] (int32; bf16 or fp32 rows of any strides, so the
+    views of a projection's output are taken as they are). rope: float32 [positions,
+    2, pairs] (rope_table); None: nothing is turned. Pair i is elements (i, i +
+    pairs), interleaved: (2 i, 2 i + 1); elements behind the pairs stay. axes:
+    the axis of positions [axes, ...] that each pair follows. Returns (q_out,
+    k_out), k_out None without k: contiguous, or the tensors given (any strides;
+    q and k themselves too)."""
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
+        raise ValueError("q: expected a tensor [T,Hq,d] or [B,Hq,N,d]")
+    if q.dtype not in _ROW_CODES:
+        raise TypeError("q: expected a bfloat16 or float32 tensor")
+    dev = _cuda(q, "q")
+    code, unit = _ROW_CODES[q.dtype]
+    d = q.shape[-1]
+    if q.dim() == 3:
+        B, (N, Hq) = 1, q.shape[:2]
+        lead = (N,)
+    else:
+        B, Hq, N = q.shape[:3]
+        lead = (B, N)
+    strides = _head_strides(q, "q", q.shape, q.dtype, dev, unit)
+    Hkv, kst = 0, (0, 0, 0)
+    if k is not None:
+        if not isinstance(k, torch.Tensor) or k.dim() != q.dim():
+            raise ValueError("k: expected a tensor with q's axes")
+        Hkv = k.shape[1]
+        kst = _head_strides(k, "k", (N, Hkv, d) if q.dim() == 3 else (B, Hkv, N, d), q.dtype, dev,
+                            unit)
+    elif k_out is not None or k_weight is not None:
+        raise ValueError("k_out, k_weight: there is no k")
+    if rope is not None and positions is None:
+        raise ValueError("rope needs positions")
+    desc = _rope(rope, interleaved, axes, positions, lead, dev)
+    wq = _weight(q_weight, "q_weight", d, q.dtype, dev)
+    wk = _weight(k_weight, "k_weight", d, q.dtype, dev)
+    if q_out is not None:
+        qo_st = _head_strides(q_out, "q_out", q.shape, q.dtype, dev, unit, out=True)
+        _same_place(q, q_out, "q_out")
+    if k_out is not None:
+        ko_st = _head_strides(k_out, "k_out", k.shape, q.dtype, dev, unit, out=True)
+        _same_place(k, k_out, "k_out")
+    index = q.get_device()
+    if _elsewhere(index, stream):
+        with _on(dev, stream, q, k, positions, rope, q_weight, k_weight, q_out, k_out):
+            return qk_norm_rope(q, k, positions, rope, q_weight, k_weight, eps, interleaved, axes,
+                                q_out, k_out, ws)
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        qo_st = (0, Hq * d, d) if q.dim() == 3 else (Hq * N * d, d, N * d)
+    ko_st = (0, 0, 0) if k is None else ko_st if k_out is not None else \
+        (0, Hkv * d, d) if k.dim() == 3 else (Hkv * N * d, d, N * d)
+    if k is not None and k_out is None:
+        k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
+    buf = _qws(ws, dev, index, 256)
+    _check(_lib.kascade_qk_norm_rope(None if desc is None else ctypes.byref(desc), B, N, Hq, Hkv,
+                                     d, code, q.data_ptr(), None if k is None else k.data_ptr(),
+                                     wq, wk, float(eps),
+                                     None if positions is None else positions.data_ptr(),
+                                     q_out.data_ptr(), None if k is None else k_out.data_ptr(),
+                                     _I64x12(*strides, *kst, *qo_st, *ko_st), buf.data_ptr(),
+                                     buf.numel(), _raw_stream(index)), "kascade_qk_norm_rope")
+    return q_out, k_out
+
+
+def qcache_append_rope(k, v, slot_map, pages, rope, positions=None, q=None, cu_new=None,
+                       kv_lens=None, q_weight=None, k_weight=None, eps=1e-6, interleaved=False,
+                       axes=None, k_scale=1.0, v_scale=1.0, q_out=None, ws=None, stream=None):
+    """qcache_append of keys that are turned by their positions on the way (and
+    normalised first, where k_weight is given; as qk_norm_rope), together with the
+    step's queries. positions [T] int32 (with axes: [axes, T]): row t of k, v and q
+    [T,Hq,d] is token t. Or cu_new [B+1] and kv_lens [B] as qcache_plan gave them:
+    k and v are the plan's new tokens, and q [B,Hq,d] the query of each sequence's
+    last token. Returns q_out (None without q); pages are written in place."""
+    nb, hkv, bs, d = _pages(pages)
+    dev = _cuda(pages, "pages")
+    T = _slots(slot_map, dev)
+    if not isinstance(k, torch.Tensor) or k.dtype not in _ROW_CODES:
+        raise TypeError("k: expected a bfloat16 or float32 tensor")
+    code, unit = _ROW_CODES[k.dtype]
+    kt, kh = _row_strides(k, "k", (T, hkv, d), k.dtype, dev, unit)
+    vt, vh = _row_strides(v, "v", (T, hkv, d), k.dtype, dev, unit)
+    planned = cu_new is not None or kv_lens is not None
+    if planned == (positions is not None):
+        raise ValueError("give positions, or cu_new and kv_lens")
+    if rope is None:
+        raise ValueError("rope: expected a float32 tensor [positions, 2, pairs]")
+    B = 0
+    if planned:
+        if not isinstance(kv_lens, torch.Tensor) or kv_lens.dim() != 1 or cu_new is None:
+            raise ValueError("cu_new, kv_lens: expected int32 tensors [B+1] and [B]")
+        B = kv_lens.shape[0]
+        _fits(kv_lens, "kv_lens", (B,), torch.int32, dev)
+        _fits(cu_new, "cu_new", (B + 1,), torch.int32, dev)
+    desc = _rope(rope, interleaved, axes, positions, (T,), dev)
+    wq = _weight(q_weight, "q_weight", d, k.dtype, dev)
+    wk = _weight(k_weight, "k_weight", d, k.dtype, dev)
+    Hq, st = 0, (0, 0, 0, 0)
+    if q is not None:
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q: expected a tensor [T,Hq,d], or [B,Hq,d] with kv_lens")
+        Hq = q.shape[1]
+        shape = (B if planned else T, Hq, d)
+        st = _head_strides(q, "q", shape, k.dtype, dev, unit)[1:]
+        if q_out is not None:
+            st += _head_strides(q_out, "q_out", shape, k.dtype, dev, unit, out=True)[1:]
+            _same_place(q, q_out, "q_out")
+        else:
+            st += (Hq * d, d)
+    elif q_out is not None or q_weight is not None:
+        raise ValueError("q_out, q_weight: there is no q")
+    geo = _qgeo(bs, nb, 1, float(k_scale), float(v_scale))
+    index = pages.get_device()
+    if _elsewhere(index, stream):
+        with _on(dev, stream, k, v, slot_map, pages, rope, positions, q, cu_new, kv_lens, q_weight,
+                 k_weight, q_out):
+            return qcache_append_rope(k, v, slot_map, pages, rope, positions, q, cu_new, kv_lens,
+                                      q_weight, k_weight, eps, interleaved, axes, k_scale, v_scale,
+                                      q_out, ws)
+    if q is not None and q_out is None:
+        q_out = torch.empty(q.shape, dtype=k.dtype, device=dev)
+    buf = _qws(ws, dev, index, 256)
+    addr = lambda t: None if t is None else t.data_ptr()
+    _check(_lib.kascade_qcache_append_rope(geo, ctypes.byref(desc), Hq, hkv, d, code, k.data_ptr(),
+                                           v.data_ptr(), addr(q), _I64x8(kt, kh, vt, vh, *st), wk,
+                                           wq, float(eps), slot_map.data_ptr(), T, addr(positions),
+                                           addr(cu_new), addr(kv_lens), B, pages.data_ptr(),
+                                           addr(q_out), buf.data_ptr(), buf.numel(),
+                                           _raw_stream(index)), "kascade_qcache_append_rope")
+    return q_out
 
 
 def qcache_read(pages, slot_map, dtype=torch.bfloat16, k_scale=1.0, v_scale=1.0, k=None, v=None,
