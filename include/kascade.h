@@ -485,6 +485,26 @@ kascade_status kascade_qcache_dense_decode(const kascade_desc* desc, const kasca
                                            void* out, float* scores_out, void* ws,
                                            size_t ws_bytes, void* stream);
 
+/* kascade_qcache_dense_decode for a batch whose sequences begin alike: the first
+ * prefix_len tokens (a multiple of block_size, 0 <= prefix_len <= kv_len) of
+ * every sequence with kv_lens[b] >= prefix_len lie in the same blocks, so that
+ * these sequences' rows of block_table have the same first
+ * prefix_len/block_size entries. The prefix is read, and its products are
+ * taken, once for all of them; a shorter sequence (a padding row of length 0
+ * too) is attended to on its own, whatever its blocks. Entries that differ set
+ * KASCADE_ERR_BAD_INPUT on the device, and the lowest such sequence's count.
+ * Over kascade_qcache_plan a sequence of such a batch starts with kv_lens[b] =
+ * prefix_len and its row's first entries set, and ends with new_lens[b] =
+ * prefix_len - kv_lens[b], which gives back its own blocks alone.
+ * Workspace: kascade_qcache_prefix_workspace_size. */
+size_t kascade_qcache_prefix_workspace_size(const kascade_desc* desc, const kascade_qcache* cache,
+                                            int32_t prefix_len);
+kascade_status kascade_qcache_prefix_decode(const kascade_desc* desc, const kascade_qcache* cache,
+                                            const void* q, const void* pages,
+                                            const int32_t* block_table, const int32_t* kv_lens,
+                                            int32_t prefix_len, void* out, void* ws,
+                                            size_t ws_bytes, void* stream);
+
 /* Anchor layer (as kascade_anchor_decode, both index modes): the exact output
  * and the exact Top-k of every row, min(topk, kv_lens[b]) ascending positions
  * and -1 behind them; 1 <= topk <= desc->kv_len. scores_out as there, -inf

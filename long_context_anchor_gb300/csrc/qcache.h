@@ -26,6 +26,39 @@ struct QCacheShape {
   float k_scale, v_scale;     // powers of two
 };
 
+// A shared prefix (qcache_prefix.cu): its keys in chunks, the B * G queries of a KV
+// head in row tiles. All units' places form one line that is cut into runs of
+// `per`, one per CTA: first Hkv * pairs units of two row tiles (two places per
+// chunk), then Hkv * singles units of one (a place per chunk). What CTA c does of
+// unit u it leaves as pieces 2 (u + c) and 2 (u + c) + 1: of the two tiles, or both
+// of the one tile.
+constexpr int kPfxKeys = 64, kPfxRows = 128;
+constexpr int kPfxMinRun = 4;             // places per CTA at least
+struct QPrefixGeo {
+  int nch, pairs, singles, per, ctas;
+};
+QPrefixGeo prefix_geo(int B, int G, int Hkv, int P, int dtype, int sms);
+// A piece: o [rows][d], m [rows], l [rows].
+constexpr size_t pfx_piece_floats(int d) { return static_cast<size_t>(kPfxRows) * (d + 2); }
+inline size_t pfx_pieces(const QPrefixGeo& g, int Hkv) {
+  return 2 * (static_cast<size_t>(Hkv) * (g.pairs + g.singles) + g.ctas);
+}
+
+struct QPrefixArgs {
+  const void* q;              // [B,Hq,d] bf16 or fp32
+  const uint8_t* cache;
+  const int32_t* table;       // [B,max_blocks]
+  const int32_t* lens;        // [B]
+  float* part;                // pieces
+  unsigned int* err;
+  int B, Hq, Hkv, G, N, P;    // P: tokens of the prefix, > 0
+  int bs_shift, num_blocks, max_blocks;
+  float scale;                // sigma * k_scale
+  QPrefixGeo geo;
+  int16_t heads[kMaxQHeads];
+};
+cudaError_t launch_qprefix(const QPrefixArgs& a, int head_dim, int dtype, cudaStream_t st);
+
 struct QDecodeArgs {
   const void* q;              // [B,Hq,d] bf16 or fp32
   const uint8_t* cache;
@@ -51,6 +84,11 @@ struct QDecodeArgs {
   const int32_t* plan_count;  // [B*Hkv][chunks]
   int plan_chunks, topk;
   int S;                      // splits per (sequence, KV head) of the reuse kernel
+  // dense over a shared prefix: its pieces, which are joined into the outputs of
+  // sequences with at least P tokens, whose own part starts there (0: no prefix)
+  const float* pfx_part;
+  int P;
+  QPrefixGeo geo;
   int16_t heads[kMaxQHeads];  // heads[g*G + slot]
 };
 

@@ -60,6 +60,7 @@ struct QLayout {
   size_t plan, plan_count;                                // topk >= 1, sets per query head
   size_t spill, row_stat, pool;                           // topk >= 1, anchor layers
   size_t reuse, total;                                    // bytes: without an anchor layer, in all
+  size_t prefix;                                          // decode over a shared prefix
 };
 
 QLayout qlayout(const Shape& s, int topk) {
@@ -116,6 +117,38 @@ kascade_status check_qws(QCall& k, int topk, void* ws, size_t ws_bytes, bool reu
   if (!aligned(ws, 256) || ws_bytes < (reuse ? k.L.reuse : k.L.total))
     return KASCADE_ERR_WORKSPACE;
   return KASCADE_OK;
+}
+
+// SMs of the current device (asked once per host thread and device).
+int sm_count() {
+  thread_local int dev_of = -1, sms = 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 152;
+  if (dev != dev_of) {
+    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+      return 152;
+    dev_of = dev;
+  }
+  return sms < kQMaxCtas ? sms : kQMaxCtas;
+}
+
+// The dense call's layout and behind it the prefix's pieces: room for a GPU with
+// kQMaxCtas SMs, so that the size goes by the call alone.
+QLayout prefix_layout(const Shape& s, int P) {
+  QLayout L = qlayout(s, 0);
+  L.prefix = L.total;
+  if (P > 0) {
+    const QPrefixGeo most = prefix_geo(s.B, s.G, s.Hkv, P, s.dtype, kQMaxCtas);
+    L.total = align256(L.total + pfx_pieces(most, s.Hkv) * pfx_piece_floats(s.d) * sizeof(float));
+  }
+  return L;
+}
+
+// A shared prefix: whole blocks of the longest sequence.
+kascade_status check_prefix(const QCall& k, int prefix_len) {
+  return prefix_len < 0 || prefix_len > k.s.N || prefix_len % k.c.block_size != 0
+             ? KASCADE_ERR_INVALID_ARG
+             : KASCADE_OK;
 }
 
 bool check_small_ws(const void* ws, size_t ws_bytes) {
@@ -488,6 +521,58 @@ kascade_status kascade_qcache_dense_decode(const kascade_desc* desc, const kasca
   if ((r = check_qws(k, 0, ws, ws_bytes)) != KASCADE_OK) return r;
   return run_qdense(k, q, pages, block_table, kv_lens, out, scores_out, true, nullptr, ws,
                     static_cast<cudaStream_t>(stream));
+}
+
+size_t kascade_qcache_prefix_workspace_size(const kascade_desc* desc, const kascade_qcache* cache,
+                                            int32_t prefix_len) {
+  QCall k;
+  if (check_call(desc, cache, k) != KASCADE_OK || check_prefix(k, prefix_len) != KASCADE_OK)
+    return 0;
+  return prefix_layout(k.s, prefix_len).total;
+}
+
+kascade_status kascade_qcache_prefix_decode(const kascade_desc* desc, const kascade_qcache* cache,
+                                            const void* q, const void* pages,
+                                            const int32_t* block_table, const int32_t* kv_lens,
+                                            int32_t prefix_len, void* out, void* ws,
+                                            size_t ws_bytes, void* stream) {
+  QCall k;
+  kascade_status r = check_call(desc, cache, k);
+  if (r != KASCADE_OK) return r;
+  if ((r = check_prefix(k, prefix_len)) != KASCADE_OK) return r;
+  if ((r = check_attn_ptrs(q, pages, block_table, kv_lens, out)) != KASCADE_OK) return r;
+  k.L = prefix_layout(k.s, prefix_len);
+  if (!aligned(ws, 256) || ws_bytes < k.L.total) return KASCADE_ERR_WORKSPACE;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (prefix_len == 0)
+    return run_qdense(k, q, pages, block_table, kv_lens, out, nullptr, false, nullptr, ws, st);
+  QDecodeArgs a;
+  fill_qargs(a, k, q, pages, block_table, kv_lens, out, ws);
+  a.P = prefix_len;
+  a.pfx_part = at<float>(ws, k.L.prefix);
+  a.geo = prefix_geo(k.s.B, k.s.G, k.s.Hkv, prefix_len, k.s.dtype, sm_count());
+  QPrefixArgs x;
+  memset(&x, 0, sizeof(x));
+  x.q = q;
+  x.cache = a.cache;
+  x.table = block_table;
+  x.lens = kv_lens;
+  x.part = at<float>(ws, k.L.prefix);
+  x.err = a.err;
+  x.B = a.B;
+  x.Hq = a.Hq;
+  x.Hkv = a.Hkv;
+  x.G = a.G;
+  x.N = a.N;
+  x.P = prefix_len;
+  x.bs_shift = a.bs_shift;
+  x.num_blocks = a.num_blocks;
+  x.max_blocks = a.max_blocks;
+  x.scale = a.scale;
+  x.geo = a.geo;
+  memcpy(x.heads, a.heads, sizeof(x.heads));
+  if ((r = status_of(launch_qprefix(x, k.s.d, k.s.dtype, st))) != KASCADE_OK) return r;
+  return status_of(launch_qdecode_dense(a, k.s.d, k.s.dtype, st));
 }
 
 kascade_status kascade_qcache_anchor_decode(const kascade_desc* desc, const kascade_qcache* cache,

@@ -25,21 +25,12 @@
 
 #include "common.cuh"
 #include "qcache.h"
+#include "qmath.cuh"
+#include "qprefix.cuh"
 
 namespace kascade {
 namespace {
 
-#define kNegInf (-CUDART_INF_F)
-// Running maximum before the first key: below every score, and finite, so
-// that neither exponents nor joins need a case for it.
-constexpr float kNoKey = -3.0e38f;
-constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kPShift = 14;          // weights are held as 2^14 p
-// The running maximum is a reference, not the maximum itself: it is raised once
-// a score passes it by more than this (weights then reach 2^15.75, within fp16).
-constexpr float kSlack = 1.75f;
-constexpr int kQExp = 12;            // q's largest element is scaled to [2^12, 2^13)
 // Slices of 16 keys per step: a step is 4608 bytes at either head size.
 template <int D>
 constexpr int kStepOf = 256 / D;
@@ -62,42 +53,6 @@ __device__ __forceinline__ void mma_f16_16816_first(float (&d)[4], uint32_t a0, 
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-// the four bytes of w, each two e2m1 codes, as pairs of fp16 (low half first)
-__device__ __forceinline__ void cvt_e2m1x8(uint32_t w, uint32_t (&h)[4]) {
-  asm("{.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
-      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;}"
-      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
-      : "r"(w));
-}
-__device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t b) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(b)));
-  return h;
-}
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
-  return d;
-}
-// low nibbles of a, high nibbles of b
-__device__ __forceinline__ uint32_t nibbles(uint32_t a, uint32_t b) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, %3, 0xCA;" : "=r"(d) : "r"(0x0f0f0f0fu), "r"(a), "r"(b));
-  return d;
-}
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&v);
-}
-// 2^x, to 2^-22; results below 2^-126 are zero
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float f16_rounded(float x) { return __half2float(__float2half_rn(x)); }
-
 // -------------------------------------------------------------------- query --
 // The query fragments (B operand) of head gid of the group: lane c4 holds dims
 // c4 * D/4 .. + D/4, four of them per MMA, so that a key row's codes are the A
@@ -491,10 +446,70 @@ __device__ __forceinline__ Joined join_some(Piece piece, int s0, int s1, int G, 
   return x;
 }
 
+// A sequence's cached tokens; one outside what the call and its block table
+// hold is reported and cut to it.
+__device__ __forceinline__ int len_of(const QDecodeArgs& a, int b, bool report) {
+  const int cap = static_cast<int>(
+      min(static_cast<long long>(a.N), static_cast<long long>(a.max_blocks) << a.bs_shift));
+  const int n = a.lens[b];
+  if (n >= 0 && n <= cap) return n;
+  if (report) report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x521);
+  return n < 0 ? 0 : cap;
+}
+
+// With a shared prefix: the token that sequence b's own part starts at.
+template <bool PREFIX>
+__device__ __forceinline__ int start_of(const QDecodeArgs& a, int b) {
+  return PREFIX ? pfx_start(a.lens, b, a.P, a.N, a.max_blocks, a.bs_shift) : 0;
+}
+
+// x and the prefix's pieces of the same output (b, g, head slot h, dims 4 e4 ..).
+template <int D>
+__device__ __forceinline__ Joined join_prefix(const QDecodeArgs& a, Joined x, int b, int g, int h,
+                                              int e4) {
+  if (start_of<true>(a, b) == 0) return x;
+  const QPrefixGeo& geo = a.geo;
+  const int row = b * a.G + h, tile = row / kPfxRows, r = row % kPfxRows;
+  const bool pair = tile < 2 * geo.pairs;
+  int unit, u0, u1;
+  if (pair) {
+    unit = g * geo.pairs + tile / 2;
+    u0 = unit * 2 * geo.nch;
+    u1 = u0 + 2 * geo.nch;
+  } else {
+    unit = a.Hkv * geo.pairs + g * geo.singles + tile - 2 * geo.pairs;
+    u0 = (unit + a.Hkv * geo.pairs) * geo.nch;
+    u1 = u0 + geo.nch;
+  }
+  const int c0 = u0 / geo.per, ctas = (u1 - 1) / geo.per - c0 + 1;
+  // pair: the tile's piece of every CTA; else both pieces of each
+  const int n = pair ? ctas : 2 * ctas, step = pair ? 2 : 1;
+  const size_t stride = step * pfx_piece_floats(D);
+  const float* p = a.pfx_part + pfx_piece_floats(D) * (2 * static_cast<size_t>(unit + c0) +
+                                                       (pair ? tile & 1 : 0));
+  constexpr int kBatch = 8;
+  for (int s = 0; s < n; s += kBatch) {
+    Joined y[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      y[k] = {kNoKey, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      if (s + k < n) {
+        const float* at = p + (s + k) * stride;
+        y[k].m = __ldcg(at + kPfxRows * D + r);
+        y[k].l = __ldcg(at + kPfxRows * (D + 1) + r);
+        y[k].o = __ldcg(reinterpret_cast<const float4*>(at + r * D) + e4);
+      }
+    }
+    join_into(x, y);
+  }
+  return x;
+}
+
 // The output (b, g, head slot h, dims 4 e4 ..) of a joined whole.
-template <int D, bool F32>
-__device__ __forceinline__ void joined_output(const QDecodeArgs& a, const Joined& x, int b, int g,
-                                              int h, int e4) {
+template <int D, bool F32, bool PREFIX = false>
+__device__ __forceinline__ void joined_output(const QDecodeArgs& a, Joined x, int b, int g, int h,
+                                              int e4) {
+  if (PREFIX) x = join_prefix<D>(a, x, b, g, h, e4);
   const size_t row = static_cast<size_t>(b) * a.Hq + a.heads[g * a.G + h];
   const float inv = x.l == 0.f ? 0.f : a.v_scale / x.l;   // 0: no key at all
   out_store4<F32>(a, row * D + 4 * e4,
@@ -523,7 +538,7 @@ struct SharedUnit {
 // and where this CTA is the last to arrive join all of the unit's pieces into
 // the output: equal shares of the pieces per group of threads, added in order,
 // so the result does not depend on timing. `scratch`: blockDim.x Joined.
-template <int D, bool F32>
+template <int D, bool F32, bool PREFIX = false>
 __device__ void arrive_and_join(const QDecodeArgs& a, int n_units, const SharedUnit (&units)[2],
                                 Joined* scratch) {
   __shared__ unsigned int s_last;
@@ -554,7 +569,7 @@ __device__ void arrive_and_join(const QDecodeArgs& a, int n_units, const SharedU
     if (shares <= 1) {
       for (int e = tid; e < elems; e += threads) {
         const int h = e / (D / 4);
-        joined_output<D, F32>(a, join_some<true>(mine, 0, n, G, h, e), u.b, u.g, h,
+        joined_output<D, F32, PREFIX>(a, join_some<true>(mine, 0, n, G, h, e), u.b, u.g, h,
                               e & (D / 4 - 1));
       }
       continue;
@@ -570,14 +585,14 @@ __device__ void arrive_and_join(const QDecodeArgs& a, int n_units, const SharedU
         const Joined y[1] = {scratch[i * elems + e]};
         join_into(x, y);
       }
-      joined_output<D, F32>(a, x, u.b, u.g, h, e4);
+      joined_output<D, F32, PREFIX>(a, x, u.b, u.g, h, e4);
     }
     __syncthreads();
   }
 }
 
 // A whole unit held by one warp: straight from its registers to the output.
-template <int D, bool F32>
+template <int D, bool F32, bool PREFIX>
 __device__ __forceinline__ void warp_output(const QDecodeArgs& a, const QState<D>& st, int b,
                                             int g) {
   const int lane = threadIdx.x & 31, gid = lane >> 2, c4 = lane & 3;
@@ -586,6 +601,14 @@ __device__ __forceinline__ void warp_output(const QDecodeArgs& a, const QState<D
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     if (2 * c4 + i >= a.G) continue;
+    if (PREFIX) {
+#pragma unroll
+      for (int j = 0; j < D / 16; j += 2)
+        joined_output<D, F32, true>(
+            a, {st.m[i], l[i], make_float4(st.o[j][i], st.o[j][2 + i], st.o[j + 1][i], st.o[j + 1][2 + i])},
+            b, g, 2 * c4 + i, gid * (D / 32) + j / 2);
+      continue;
+    }
     const size_t row = static_cast<size_t>(b) * a.Hq + a.heads[g * a.G + 2 * c4 + i];
     const float inv = l[i] == 0.f ? 0.f : a.v_scale / l[i];
 #pragma unroll
@@ -595,17 +618,6 @@ __device__ __forceinline__ void warp_output(const QDecodeArgs& a, const QState<D
                                   st.o[j + 1][2 + i] * inv));
     if (gid == 0) write_row_stat(a, row, st.m[i], l[i]);
   }
-}
-
-// A sequence's cached tokens; one outside what the call and its block table
-// hold is reported and cut to it.
-__device__ __forceinline__ int len_of(const QDecodeArgs& a, int b, bool report) {
-  const int cap = static_cast<int>(
-      min(static_cast<long long>(a.N), static_cast<long long>(a.max_blocks) << a.bs_shift));
-  const int n = a.lens[b];
-  if (n >= 0 && n <= cap) return n;
-  if (report) report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x521);
-  return n < 0 ? 0 : cap;
 }
 
 // -------------------------------------------------------------------- dense --
@@ -658,6 +670,7 @@ struct Part {
   int ns, s0, s1;
   int next;
 };
+template <bool PREFIX>
 __device__ __forceinline__ Part part_at(const QDecodeArgs& a, const int* pref, int f, int end) {
   int lo = 0, hi = a.B;   // the sequence: pref[lo] * Hkv <= f < pref[lo + 1] * Hkv
   while (hi - lo > 1) {
@@ -667,7 +680,7 @@ __device__ __forceinline__ Part part_at(const QDecodeArgs& a, const int* pref, i
   }
   Part p;
   p.b = lo;
-  p.n = len_of(a, lo, false);
+  p.n = len_of(a, lo, false) - start_of<PREFIX>(a, lo);
   const int places = pref[lo + 1] - pref[lo];
   const int in = f - pref[lo] * a.Hkv;
   p.g = in / places;
@@ -679,7 +692,7 @@ __device__ __forceinline__ Part part_at(const QDecodeArgs& a, const int* pref, i
   return p;
 }
 
-template <int D, int TERMS, bool SCORES>
+template <int D, int TERMS, bool SCORES, bool PREFIX>
 __global__ void __launch_bounds__(kNW * 32, kDenseCtasPerSm)
     k_qdecode_dense(const __grid_constant__ QDecodeArgs a) {
   pdl_wait();
@@ -712,7 +725,7 @@ __global__ void __launch_bounds__(kNW * 32, kDenseCtasPerSm)
   int carry = 0;
   for (int b0 = 0; b0 < a.B; b0 += kNW * 32) {
     const int b = b0 + tid;
-    int n = b < a.B ? (len_of(a, b, blockIdx.x == 0) + kKeys - 1) / kKeys : 0;
+    int n = b < a.B ? (len_of(a, b, blockIdx.x == 0) - start_of<PREFIX>(a, b) + kKeys - 1) / kKeys : 0;
     if (n > 0) n += kUnitCost;
     int incl = n;
 #pragma unroll
@@ -764,7 +777,8 @@ __global__ void __launch_bounds__(kNW * 32, kDenseCtasPerSm)
     in_left = p.s1 - p.s0;
     in_key = lane < ncopy ? p.s0 * kKeys + (lane << copy_sh) : p.n;   // other lanes copy nothing
     in_n = p.n;
-    in_row = a.table + static_cast<size_t>(p.b) * a.max_blocks;
+    in_row = a.table + static_cast<size_t>(p.b) * a.max_blocks +
+             (start_of<PREFIX>(a, p.b) >> a.bs_shift);
     in_base = a.cache + static_cast<size_t>(p.g) * head_bytes;
   };
   auto fetch_id = [&]() {
@@ -794,7 +808,7 @@ __global__ void __launch_bounds__(kNW * 32, kDenseCtasPerSm)
     in_key += kKeys;
     if (lane >= ncopy) in_key = in_n;
     if (--in_left == 0) {
-      while (in_left == 0 && in_next < w1) enter(part_at(a, pref, in_next, w1));
+      while (in_left == 0 && in_next < w1) enter(part_at<PREFIX>(a, pref, in_next, w1));
     }
     if (in_left > 0) fetch_id();
   };
@@ -802,7 +816,7 @@ __global__ void __launch_bounds__(kNW * 32, kDenseCtasPerSm)
   Part at = {};
   QRaw<D, TERMS> qx;   // the query of the unit that comes next
   at.next = w0;
-  while (at.s0 == at.s1 && at.next < w1) at = part_at(a, pref, at.next, w1);
+  while (at.s0 == at.s1 && at.next < w1) at = part_at<PREFIX>(a, pref, at.next, w1);
   if (at.s0 < at.s1) {
     enter(at);
     fetch_id();
@@ -905,7 +919,7 @@ __global__ void __launch_bounds__(kNW * 32, kDenseCtasPerSm)
       if (in_left > 0) issue();
     }
     if (steps == at.ns) {
-      warp_output<D, F32>(a, st, at.b, at.g);
+      warp_output<D, F32, PREFIX>(a, st, at.b, at.g);
     } else {
       // in part: a run's first unit or its last (whose ring is free by then)
       const int slot = 2 * warp + (first_unit ? 0 : 1);
@@ -916,7 +930,7 @@ __global__ void __launch_bounds__(kNW * 32, kDenseCtasPerSm)
     int next = at.next;
     at.s0 = at.s1 = 0;
     while (at.s0 == at.s1 && next < w1) {
-      at = part_at(a, pref, next, w1);
+      at = part_at<PREFIX>(a, pref, next, w1);
       next = at.next;
     }
     if (at.s0 < at.s1) load_q<D, TERMS>(a, at.b, at.g, qx);
@@ -975,15 +989,21 @@ __global__ void __launch_bounds__(kNW * 32, kDenseCtasPerSm)
           dst[a.G + h] = x.l;
         }
       } else {
-        joined_output<D, F32>(a, x, b, g, h, e4);
+        joined_output<D, F32, PREFIX>(a, x, b, g, h, e4);
       }
     }
   }
   if (n_shared > 0)
-    arrive_and_join<D, F32>(a, n_shared, shared, reinterpret_cast<Joined*>(smem));
+    arrive_and_join<D, F32, PREFIX>(a, n_shared, shared, reinterpret_cast<Joined*>(smem));
   // sequences without keys: zeros; scores behind the last key
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     if (pref[b + 1] != pref[b]) continue;
+    if (PREFIX && start_of<PREFIX>(a, b) > 0) {   // the prefix alone
+      for (int e = tid; e < a.Hq * (D / 4); e += kNW * 32)
+        joined_output<D, F32, true>(a, {kNoKey, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)}, b,
+                                    e / elems, e % elems / (D / 4), e & (D / 4 - 1));
+      continue;
+    }
     const size_t base = static_cast<size_t>(b) * a.Hq * D;
     for (int e = 4 * tid; e < a.Hq * D; e += 4 * kNW * 32)
       out_store4<F32>(a, base + e, make_float4(0.f, 0.f, 0.f, 0.f));
@@ -1298,7 +1318,7 @@ cudaError_t resident_ctas(size_t smem, int threads, int& ctas) {
   return cudaSuccess;
 }
 
-template <int D, int TERMS, bool SCORES>
+template <int D, int TERMS, bool SCORES, bool PREFIX>
 cudaError_t launch_dense_t(const QDecodeArgs& a, cudaStream_t st) {
   // rings (at the end the scratch of the join between CTAs), places, first
   // pieces; the latter only up to what fits beside them at every batch size
@@ -1312,7 +1332,7 @@ cudaError_t launch_dense_t(const QDecodeArgs& a, cudaStream_t st) {
   u.firsts_global = smem + firsts > 224 * 1024 ? 1 : 0;
   u.pages_once = static_cast<size_t>(a.B) * a.Hq * a.N * 4 <= kL2Logits ? 1 : 0;
   if (!u.firsts_global) smem += firsts;
-  constexpr auto kern = k_qdecode_dense<D, TERMS, SCORES>;
+  constexpr auto kern = k_qdecode_dense<D, TERMS, SCORES, PREFIX>;
   int ctas = 0;
   const cudaError_t e = resident_ctas<kern>(smem, kNW * 32, ctas);
   if (e != cudaSuccess) return e;
@@ -1322,8 +1342,9 @@ cudaError_t launch_dense_t(const QDecodeArgs& a, cudaStream_t st) {
 
 template <int D, int TERMS>
 cudaError_t launch_dense_s(const QDecodeArgs& a, cudaStream_t st) {
-  return a.scores != nullptr ? launch_dense_t<D, TERMS, true>(a, st)
-                             : launch_dense_t<D, TERMS, false>(a, st);
+  if (a.P > 0) return launch_dense_t<D, TERMS, false, true>(a, st);
+  return a.scores != nullptr ? launch_dense_t<D, TERMS, true, false>(a, st)
+                             : launch_dense_t<D, TERMS, false, false>(a, st);
 }
 
 template <int D, int TERMS, bool POOLED>

@@ -1,0 +1,561 @@
+// qcache_prefix.cu — decode attention of a batch over a prefix that its
+// sequences share in the paged 4-bit cache (layout in qcache.h): the keys of the
+// prefix for all queries of a KV head together, as a matrix product.
+//
+// A KV head has B * G queries, G per sequence: rows of tiles of 128. The
+// prefix comes in chunks of 64 keys, each turned from 4 bits into fp16 once in
+// shared memory for up to two tiles: S = Q K^T and O += P V on tcgen05 with fp16
+// operands and fp32 sums. As in the dense kernel a stored element is exact in
+// fp16, a row of q is scaled by a power of two (an fp32 q is two fp16 terms), weights
+// are 2^14 p against a reference within kSlack of the running maximum, rounded to
+// fp16 (fp32 outputs: two terms) for the product and summed unrounded.
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <math_constants.h>
+
+#include "common.cuh"
+#include "qcache.h"
+#include "qmath.cuh"
+#include "qprefix.cuh"
+#include "tc.cuh"
+
+namespace kascade {
+namespace {
+
+// Two streams, each with its scores, its running state and its O, run through
+// the same code: a unit of two row tiles gives each stream one of them and every
+// chunk; a unit of one tile gives both streams that tile and every other chunk
+// (their states are two pieces of the same rows). While one stream's softmax
+// runs, the tensor cores work for the other.
+//
+// Roles: warps 4s .. 4s+3 are stream s's softmax, a thread per row; then
+// kDeqWarps warps that turn codes into fp16; one warp that issues the MMAs; one that
+// copies the blocks in.
+constexpr int kDeqWarps = 8;
+constexpr int kMmaWarp = 8 + kDeqWarps, kLoadWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kLoadWarp + 1);
+
+template <int D>
+struct Smem {
+  static constexpr int HALF = kPfxKeys * 128;           // 64 dims of a chunk's K or V in fp16
+  static constexpr int TILE = HALF * (D / 64);          // a chunk's K, or its V
+  static constexpr int STAGE = 2 * TILE;
+  static constexpr int NST = D == 128 ? 4 : 6;          // fp16 chunks
+  static constexpr int RAW = (kPfxKeys / kQGroup) * qgroup_bytes(D);
+  static constexpr int NR = D == 128 ? 8 : 12;          // chunks as stored
+  static constexpr int RAW0 = NST * STAGE;
+  static constexpr int BAR = RAW0 + NR * RAW;
+  static constexpr int NBAR = 2 * NR + 2 * NST + 8;
+  static constexpr int VALID = BAR + NBAR * 8;          // int [NR + NST]: bit per 16 keys
+  static constexpr int TMEM = VALID + (NR + NST) * 4;
+  static constexpr int BYTES = TMEM + 8;
+  static constexpr size_t SMEM = BYTES + 1024;          // slack for 1024-byte alignment
+  static_assert(SMEM <= 232448 - 64, "fits in shared memory");
+};
+// TMEM columns: Q (fp16 pairs; two tiles, or the two terms of one), S of each
+// stream (its P over it: both terms of 64 weights are 64 columns), O
+constexpr int kTQ = 0, kTS = 128, kTO = 256;
+
+__device__ __forceinline__ uint64_t k_desc(uint32_t tile, int kk) {   // 16 dims of 64 keys
+  return sw128_desc(tile + (kk >> 2) * (kPfxKeys * 128) + (kk & 3) * 32, 16, 1024);
+}
+__device__ __forceinline__ uint64_t v_desc(uint32_t tile, int kk) {   // 16 keys of all dims
+  return sw128_desc(tile + kk * 2048, kPfxKeys * 128, 1024);
+}
+// fp16 x fp16 -> fp32
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn_major) {
+  return (1u << 4) | (static_cast<uint32_t>(b_mn_major) << 16) |
+         (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// What a CTA does of one unit: chunks c0 .. c1 - 1 for one or two row tiles.
+struct Part {
+  int unit, g, tile0, tiles, c0, c1, next;
+  __device__ __forceinline__ int chunks(int stream) const {   // of one stream
+    return tiles == 2 ? c1 - c0 : (c1 - c0 - stream + 1) / 2;
+  }
+  // local number of a stream's t-th chunk
+  __device__ __forceinline__ int local(int stream, int t) const {
+    return tiles == 2 ? t : 2 * t + stream;
+  }
+};
+__device__ __forceinline__ Part part_at(const QPrefixGeo& geo, int Hkv, int f, int end) {
+  Part p;
+  const int base = Hkv * geo.pairs * 2 * geo.nch;
+  if (f < base) {
+    const int places = 2 * geo.nch;
+    p.unit = f / places;
+    const int u0 = p.unit * places;
+    p.next = min(end, u0 + places);
+    p.g = p.unit / geo.pairs;
+    p.tile0 = 2 * (p.unit - p.g * geo.pairs);
+    p.tiles = 2;
+    p.c0 = (f - u0) / 2;
+    p.c1 = (p.next - u0) / 2;
+  } else {
+    const int us = (f - base) / geo.nch, u0 = base + us * geo.nch;
+    p.next = min(end, u0 + geo.nch);
+    p.unit = Hkv * geo.pairs + us;
+    p.g = us / geo.singles;
+    p.tile0 = 2 * geo.pairs + us - p.g * geo.singles;
+    p.tiles = 1;
+    p.c0 = f - u0;
+    p.c1 = p.next - u0;
+  }
+  return p;
+}
+
+// 32 elements of a row: 16 bytes of codes and two scales become four 16-byte
+// pieces in the swizzled tile at `tile` (row of the chunk, pieces 4 part ..).
+template <int D>
+__device__ __forceinline__ void widen(const uint8_t* grp, int codes_at, int scales_at, uint32_t tile,
+                                      int row, int part, bool valid) {
+  const int r = row & 15;
+  uint4 w = make_uint4(0u, 0u, 0u, 0u);
+  uint32_t h = 0u;
+  if (valid) {   // what lies there otherwise may be anything
+    w = *reinterpret_cast<const uint4*>(grp + codes_at + r * (D / 2) + part * 16);
+    h = cvt_e4m3x2(*reinterpret_cast<const uint16_t*>(grp + scales_at + r * (D / 16) + part * 2));
+  }
+  const uint32_t s0 = __byte_perm(h, h, 0x1010), s1 = __byte_perm(h, h, 0x3232);
+  // the pieces of parts 2 and 3 go in another order: eight lanes with two rows of
+  // four parts each then store to all banks
+  const int flip = D == 128 ? part & 2 : 0;
+  const uint32_t word[4] = {flip ? w.z : w.x, flip ? w.w : w.y, flip ? w.x : w.z, flip ? w.y : w.w};
+  const uint32_t sa = flip ? s1 : s0, sb = flip ? s0 : s1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t x[4];
+    cvt_e2m1x8(word[i], x);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = hmul2(x[j], i < 2 ? sa : sb);
+    const uint32_t to = tile + sw128_offset(kPfxKeys, row, 4 * part + (i ^ flip));
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                 "r"(x[3])
+                 : "memory");
+  }
+}
+
+// 64 elements from element `at` of a row of q as 32-bit floats.
+template <int TERMS>
+__device__ __forceinline__ void load_q8(const void* row, int at, float (&x)[8]) {
+  if (TERMS == 2) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(row) + at);
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(row) + at));
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[2 * j] = __uint_as_float(w[j] << 16);
+      x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  }
+}
+
+template <int D, int TERMS>
+__global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__ QPrefixArgs a) {
+  using SM = Smem<D>;
+  constexpr int NST = SM::NST, NR = SM::NR;
+  pdl_wait();
+  pdl_trigger();
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ int s_src;
+  unsigned char* sm = reinterpret_cast<unsigned char*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::BAR);
+  uint64_t* raw_full = bars;            // [NR] a chunk's copies have landed
+  uint64_t* raw_free = bars + NR;       // [NR] ... and were read
+  uint64_t* kv_ready = bars + 2 * NR;   // [NST] fp16 K and V written
+  uint64_t* kv_free = kv_ready + NST;   // [NST] ... and used
+  uint64_t* q_ready = kv_free + NST;    // [2] by stream: Q in TMEM
+  uint64_t* s_full = q_ready + 2;       // [2] scores of the stream's chunk
+  uint64_t* p_full = q_ready + 4;       // [2] its weights written over them
+  uint64_t* pv_done = q_ready + 6;      // [2] their product with V
+  int* raw_valid = reinterpret_cast<int*>(sm + SM::VALID);
+  int* kv_valid = raw_valid + NR;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + SM::TMEM);
+
+  // the lowest sequence that holds the whole prefix names its blocks
+  if (tid == 0) s_src = a.B;
+  __syncthreads();
+  for (int b = tid; b < a.B; b += kThreads)
+    if (pfx_start(a.lens, b, a.P, a.N, a.max_blocks, a.bs_shift) > 0) {
+      atomicMin(&s_src, b);
+      break;
+    }
+  if (tid < 2 * NR + 2 * NST + 8) {
+    const int i = tid;
+    const int count = i < NR ? 1 : i < 2 * NR ? kDeqWarps : i < 2 * NR + NST ? kDeqWarps
+                      : i < 2 * NR + 2 * NST ? 1
+                      : i < 2 * NR + 2 * NST + 2 ? 128
+                      : i < 2 * NR + 2 * NST + 4 ? 1
+                      : i < 2 * NR + 2 * NST + 6 ? 128 : 1;
+    mbar_init(bars + i, count);
+    fence_barrier_init();
+  }
+  __syncthreads();
+  const int src = s_src;
+  if (src >= a.B) return;   // nobody has it: no piece is read either
+  if (warp == kMmaWarp) tmem_alloc(s_tmem, 512);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *s_tmem;
+  const int32_t* ids = a.table + static_cast<size_t>(src) * a.max_blocks;
+
+  const int total = a.Hkv * (2 * a.geo.pairs + a.geo.singles) * a.geo.nch;
+  const int w0 = min(total, static_cast<int>(blockIdx.x) * a.geo.per);
+  const int w1 = min(total, w0 + a.geo.per);
+
+  if (warp == kLoadWarp) {
+    // ------------------------------------------------------------- copies
+    const int copy_sh = min(a.bs_shift, 6), ncopy = kPfxKeys >> copy_sh;
+    const uint32_t copy_bytes = static_cast<uint32_t>(qgroup_bytes(D)) << (copy_sh - 4);
+    const uint32_t head_bytes = static_cast<uint32_t>(qgroup_bytes(D)) << (a.bs_shift - 4);
+    const uint64_t block_bytes = static_cast<uint64_t>(head_bytes) * a.Hkv;
+    const int gmask = (1 << (a.bs_shift - 4)) - 1;
+    const unsigned int groups = (1u << (1 << (copy_sh - 4))) - 1u;   // a copy's bits
+    uint32_t kc = 0;
+    bool ok = true;
+    for (int f = w0; ok && f < w1;) {
+      const Part p = part_at(a.geo, a.Hkv, f, w1);
+      f = p.next;
+      const uint8_t* head = a.cache + static_cast<size_t>(p.g) * head_bytes;
+      auto key_of = [&](int c) { return c * kPfxKeys + (lane << copy_sh); };
+      auto fetch = [&](int c) {
+        const int key = key_of(c);
+        return lane < ncopy && c < p.c1 && key < a.P ? __ldg(ids + (key >> a.bs_shift)) : 0;
+      };
+      int next = fetch(p.c0);
+      for (int c = p.c0; c < p.c1; ++c, ++kc) {
+        const int id = next, key = key_of(c), st = kc % NR;
+        next = fetch(c + 1);
+        const bool want = lane < ncopy && key < a.P;
+        const bool take = want && static_cast<unsigned int>(id) < static_cast<unsigned int>(a.num_blocks);
+        if (want && !take) report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x552);
+        const unsigned int got = __ballot_sync(0xffffffffu, take);
+        if (!mbar_wait_warp(raw_free + st, ((kc / NR) & 1) ^ 1, a.err, 0x561)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) {
+          unsigned int bits = 0u;
+          for (int i = 0; i < ncopy; ++i)
+            if ((got >> i) & 1u) bits |= groups << (i << (copy_sh - 4));
+          raw_valid[st] = static_cast<int>(bits);
+          mbar_arrive_expect_tx(raw_full + st, __popc(got) * copy_bytes);
+        }
+        __syncwarp();
+        if (take)
+          bulk_load(sm + SM::RAW0 + st * SM::RAW + lane * copy_bytes,
+                    head + static_cast<uint64_t>(id) * block_bytes +
+                        static_cast<uint32_t>((key >> 4) & gmask) * qgroup_bytes(D),
+                    copy_bytes, raw_full + st);
+      }
+    }
+    // leave no copy in flight
+    for (uint32_t k = kc > NR ? kc - NR : 0; k < kc; ++k)
+      mbar_wait(raw_full + k % NR, (k / NR) & 1, a.err, 0x562);
+  } else if (warp == kMmaWarp) {
+    // --------------------------------------------------------- tensor cores
+    constexpr uint32_t idq = idesc_f16_f32(128, kPfxKeys, 0), idv = idesc_f16_f32(128, D, 1);
+    uint32_t kc = 0, n_unit = 0;
+    uint32_t done[2] = {0u, 0u};   // chunks of each stream so far
+    const uint32_t kv0 = smem_u32(sm);
+    bool ok = true;
+    for (int f = w0; ok && f < w1; ++n_unit) {
+      const Part p = part_at(a.geo, a.Hkv, f, w1);
+      f = p.next;
+      // S = Q K^T of stream s's t-th chunk of the part
+      auto issue_s = [&](int s, int t) {
+        const uint32_t k = kc + p.local(s, t), st = k % NST;
+        if (!mbar_wait_warp(kv_ready + st, (k / NST) & 1, a.err, 0x571)) return false;
+        tc_fence_after();
+        const uint32_t tS = tmem + kTS + 64 * s;
+#pragma unroll
+        for (int term = 0; term < TERMS; ++term)
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            tc_mma_ts(tS, tmem + kTQ + 64 * (TERMS == 2 ? term : s) + kk * 8,
+                      k_desc(kv0 + st * SM::STAGE, kk), idq, term > 0 || kk > 0 ? 1u : 0u);
+        tc_commit(s_full + s);
+        return true;
+      };
+      auto issue_pv = [&](int s, int t) {
+        const uint32_t k = kc + p.local(s, t), st = k % NST;
+        if (!mbar_wait_warp(p_full + s, (done[s] + t) & 1, a.err, 0x572)) return false;
+        tc_fence_after();
+        const uint32_t tP = tmem + kTS + 64 * s, tO = tmem + kTO + 128 * s;
+#pragma unroll
+        for (int term = 0; term < TERMS; ++term)
+#pragma unroll
+          for (int kk = 0; kk < kPfxKeys / 16; ++kk)
+            tc_mma_ts(tO, tP + 32 * term + kk * 8, v_desc(kv0 + st * SM::STAGE + SM::TILE, kk), idv,
+                      t > 0 || term > 0 || kk > 0 ? 1u : 0u);
+        tc_commit(pv_done + s);
+        if (p.tiles == 1 || s == 1) tc_commit(kv_free + st);   // the chunk's last use
+        return true;
+      };
+      const int n[2] = {p.chunks(0), p.chunks(1)};
+      for (int s = 0; ok && s < 2; ++s) {
+        ok = mbar_wait_warp(q_ready + s, n_unit & 1, a.err, 0x573);
+        if (TERMS == 2 && ok && s == 0) ok = mbar_wait_warp(q_ready + 1, n_unit & 1, a.err, 0x573);
+        tc_fence_after();
+        if (ok && n[s] > 0) ok = issue_s(s, 0);
+      }
+      for (int t = 0; ok && t < n[0]; ++t)
+        for (int s = 0; ok && s < 2; ++s) {
+          if (t >= n[s]) continue;
+          ok = issue_pv(s, t);
+          if (ok && t + 1 < n[s]) {
+            // the next scores go where this product's weights are
+            ok = mbar_wait_warp(pv_done + s, (done[s] + t) & 1, a.err, 0x574) && issue_s(s, t + 1);
+          }
+        }
+      kc += p.c1 - p.c0;
+      done[0] += n[0];
+      done[1] += n[1];
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------- codes to fp16
+    const int t = tid - 256;
+    const int row = D == 128 ? t >> 2 : (t & 127) >> 1, part = D == 128 ? t & 3 : t & 1;
+    uint32_t kc = 0;
+    bool ok = true;
+    for (int f = w0; ok && f < w1;) {
+      const Part p = part_at(a.geo, a.Hkv, f, w1);
+      f = p.next;
+      for (int c = p.c0; c < p.c1; ++c, ++kc) {
+        const int rs = kc % NR, st = kc % NST;
+        ok = mbar_wait_warp(raw_full + rs, (kc / NR) & 1, a.err, 0x581) &&
+             mbar_wait_warp(kv_free + st, ((kc / NST) & 1) ^ 1, a.err, 0x582);
+        if (!ok) break;
+        const int bits = raw_valid[rs];
+        const uint8_t* grp = sm + SM::RAW0 + rs * SM::RAW + (row >> 4) * qgroup_bytes(D);
+        const bool valid = (bits >> (row >> 4)) & 1;
+        const uint32_t tile = smem_u32(sm) + st * SM::STAGE;
+        if (D == 128 || t < 128) widen<D>(grp, 0, 8 * D, tile, row, part, valid);
+        if (D == 128 || t >= 128) widen<D>(grp, 9 * D, 17 * D, tile + SM::TILE, row, part, valid);
+        if (t == 0) kv_valid[st] = bits;
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(kv_ready + st);
+          mbar_arrive(raw_free + rs);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------- softmax
+    const int s = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t tQ = tmem + kTQ + 64 * s + lane_base, tS = tmem + kTS + 64 * s + lane_base;
+    const uint32_t tO = tmem + kTO + 128 * s + lane_base;
+    // sequences whose tables name other blocks
+    const int front = a.P >> a.bs_shift;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + tid;
+         i < static_cast<int64_t>(a.B) * front; i += static_cast<int64_t>(gridDim.x) * 256) {
+      const int b = static_cast<int>(i / front), j = static_cast<int>(i - static_cast<int64_t>(b) * front);
+      if (pfx_start(a.lens, b, a.P, a.N, a.max_blocks, a.bs_shift) > 0 &&
+          a.table[static_cast<size_t>(b) * a.max_blocks + j] != ids[j])
+        report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x551);
+    }
+    uint32_t kc = 0, done = 0;
+    bool ok = true;
+    for (int f = w0; f < w1;) {
+      const Part p = part_at(a.geo, a.Hkv, f, w1);
+      f = p.next;
+      const int gr = (p.tile0 + (p.tiles == 2 ? s : 0)) * 128 + r;   // row of the KV head
+      const int b = gr / a.G, slot = gr - b * a.G;
+      const bool live = b < a.B && pfx_start(a.lens, b, a.P, a.N, a.max_blocks, a.bs_shift) > 0;
+      const bool idle = !__any_sync(0xffffffffu, live);
+      // ---- this row of Q
+      float amax = 0.f;
+      const size_t q_row = live ? static_cast<size_t>(b) * a.Hq + a.heads[p.g * a.G + slot] : 0;
+      const void* row = static_cast<const char*>(a.q) + q_row * D * (TERMS == 2 ? 4 : 2);
+      if (live)
+        for (int i = 0; i < D; i += 8) {
+          float x[8];
+          load_q8<TERMS>(row, i, x);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]));
+        }
+      int e = kQExp;
+      if (amax > 0.f && amax < CUDART_INF_F) e = max(ilogbf(amax), -100);
+      const float up = ldexpf(1.f, kQExp - e);
+      const float ml = fmaxf(a.scale * ldexpf(1.f, e - kQExp), 1e-37f) * kLog2e;
+      // (fp32: both streams read both terms, which must not change under the other's scores)
+      if (TERMS == 2) asm volatile("bar.sync 1, 256;" ::: "memory");
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h) {
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+          if (live) load_q8<TERMS>(row, 64 * h + 8 * i, x);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float lo = x[2 * j] * up, hi = x[2 * j + 1] * up;
+            if (TERMS == 2 && s == 1) {
+              lo -= f16_rounded(lo);
+              hi -= f16_rounded(hi);
+            }
+            w[4 * i + j] = pack_f16(lo, hi);
+          }
+        }
+        tmem_st32(tQ + 32 * h, w);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(q_ready + s);
+      // ---- its chunks
+      // the reference is kept as a raw product, and taken from the products before
+      // they are scaled: a huge score's distance from it is exact
+      float ref = kNoKey, l = 0.f;
+      const float slack = kSlack / ml;
+      const int n = p.chunks(s);
+      for (int t = 0; ok && t < n; ++t) {
+        const uint32_t k = kc + p.local(s, t), st = k % NST, ph = (done + t) & 1;
+        ok = mbar_wait_warp(s_full + s, ph, a.err, 0x591) &&
+             mbar_wait_warp(kv_ready + st, (k / NST) & 1, a.err, 0x592);   // for kv_valid
+        if (!ok) break;
+        tc_fence_after();
+        if (!idle) {
+          float x[64];
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            uint32_t v[32];
+            tmem_ld32(tS + 32 * cc, v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[32 * cc + i] = __uint_as_float(v[i]);
+          }
+          const int bits = kv_valid[st];
+          tmem_wait_ld();
+          if (bits != 0xf) {
+#pragma unroll
+            for (int i = 0; i < 64; ++i)
+              if (!((bits >> (i / 16)) & 1)) x[i] = kNegInf;
+          }
+          float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int i = 4; i + 1 < 64; i += 2) mx[(i >> 1) & 3] = fmax3(mx[(i >> 1) & 3], x[i], x[i + 1]);
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+          const bool raise = top > ref + slack;
+          if (__any_sync(0xffffffffu, raise)) {
+            const float up_to = raise ? top : ref, al = ex2((ref - up_to) * ml);
+            ref = up_to;
+            l *= al;
+            if (t > 0) {
+              // the stream's previous product is complete (its scores came after it)
+              ok = mbar_wait_warp(pv_done + s, ph ^ 1, a.err, 0x593);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll
+              for (int cc = 0; cc < D / 32; ++cc) {
+                uint32_t o[32];
+                tmem_ld32(tO + 32 * cc, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+                tmem_st32(tO + 32 * cc, o);
+              }
+            }
+          }
+          const uint64_t ml2 = f2_pack(ml, ml), minus = f2_pack(-ref, -ref);
+          const uint64_t shift = f2_pack(kPShift, kPShift);
+          uint64_t sum[2] = {0ull, 0ull};
+          uint32_t hi[32], lo[TERMS == 2 ? 32 : 1];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            float p0, p1;
+            f2_unpack(f2_fma(f2_add(f2_pack(x[2 * i], x[2 * i + 1]), minus), ml2, shift), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            sum[i & 1] = f2_add(sum[i & 1], f2_pack(p0, p1));
+            hi[i] = pack_f16(p0, p1);
+            if (TERMS == 2) lo[i] = pack_f16(p0 - f16_rounded(p0), p1 - f16_rounded(p1));
+          }
+          float s0, s1;
+          f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
+          l += s0 + s1;
+          tmem_st32(tS, hi);
+          if constexpr (TERMS == 2) tmem_st32(tS + 32, lo);
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(p_full + s);
+      }
+      // ---- the piece
+      if (ok && n > 0) ok = mbar_wait_warp(pv_done + s, (done + n - 1) & 1, a.err, 0x594);
+      kc += p.c1 - p.c0;
+      done += n;
+      tc_fence_after();
+      if (!idle) {
+        float* piece = a.part + pfx_piece_floats(D) * (2 * (static_cast<size_t>(p.unit) + blockIdx.x) + s);
+#pragma unroll
+        for (int cc = 0; cc < D / 32; ++cc) {
+          uint32_t o[32];
+          tmem_ld32(tO + 32 * cc, o);
+          tmem_wait_ld();
+          float4* dst = reinterpret_cast<float4*>(piece + r * D + 32 * cc);
+          if (live)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[i] = n > 0 ? make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                           __uint_as_float(o[4 * i + 2]),
+                                           __uint_as_float(o[4 * i + 3]))
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        if (live) {
+          piece[kPfxRows * D + r] = ref == kNoKey ? kNoKey : ref * ml;
+          piece[kPfxRows * (D + 1) + r] = l;
+        }
+      }
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, int TERMS>
+cudaError_t launch_prefix_t(const QPrefixArgs& a, cudaStream_t st) {
+  constexpr size_t smem = Smem<D>::SMEM;
+  constexpr auto kern = k_qprefix<D, TERMS>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(a.geo.ctas), dim3(kThreads), smem, st, a);
+}
+
+}  // namespace
+
+// Places of all units in equal, even runs: a pair unit's place is half a chunk.
+QPrefixGeo prefix_geo(int B, int G, int Hkv, int P, int dtype, int sms) {
+  QPrefixGeo g{};
+  const int tiles = (B * G + kPfxRows - 1) / kPfxRows;
+  g.nch = (P + kPfxKeys - 1) / kPfxKeys;
+  g.pairs = dtype == KASCADE_F32 ? 0 : tiles / 2;
+  g.singles = tiles - 2 * g.pairs;
+  const int total = Hkv * tiles * g.nch;
+  g.per = 2 * ((total + 2 * sms - 1) / (2 * sms));
+  if (g.per < kPfxMinRun) g.per = kPfxMinRun;
+  g.ctas = (total + g.per - 1) / g.per;
+  return g;
+}
+
+cudaError_t launch_qprefix(const QPrefixArgs& a, int d, int dtype, cudaStream_t st) {
+  if (dtype == KASCADE_F32)
+    return d == 128 ? launch_prefix_t<128, 2>(a, st) : launch_prefix_t<64, 2>(a, st);
+  return d == 128 ? launch_prefix_t<128, 1>(a, st) : launch_prefix_t<64, 1>(a, st);
+}
+
+}  // namespace kascade

@@ -107,6 +107,9 @@ _SIGS = {
     "kascade_qcache_read": (ctypes.c_int, [_QP, _i32, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _I64P,
                                            _vp, _sz, _vp]),
     "kascade_qcache_dense_decode": (ctypes.c_int, [_DP, _QP] + [_vp] * 7 + [_sz, _vp]),
+    "kascade_qcache_prefix_workspace_size": (_sz, [_DP, _QP, _i32]),
+    "kascade_qcache_prefix_decode": (ctypes.c_int, [_DP, _QP] + [_vp] * 4 + [_i32] + [_vp] * 2 +
+                                     [_sz, _vp]),
     "kascade_qcache_anchor_decode": (ctypes.c_int, [_DP, _QP] + [_vp] * 4 + [_i32] + [_vp] * 4 +
                                      [_sz, _vp]),
     "kascade_qcache_reuse_decode": (ctypes.c_int, [_DP, _QP] + [_vp] * 4 + [_i32] + [_vp] * 3 +
@@ -767,12 +770,16 @@ def _qgeo(block_size, num_blocks, max_blocks, k_scale, v_scale):
 
 @functools.lru_cache(maxsize=256)
 def _qdesc(B, Hq, Hkv, d, N, code, scale, group_map, pooled, bs, nb, width, k_scale, v_scale, topk,
-           reuse):
+           reuse, prefix=None):
     """Descriptor, geometry (ctypes references, read only) and workspace bytes of
     an attention call of these sizes."""
     desc = make_desc(B, Hq, Hkv, d, N, code, scale, group_map, pooled)
     geo = QCache(bs, nb, width, k_scale, v_scale)
-    return ctypes.byref(desc), ctypes.byref(geo), qcache_workspace_size(desc, geo, topk, reuse)
+    if prefix is None:
+        nbytes = qcache_workspace_size(desc, geo, topk, reuse)
+    else:
+        nbytes = qcache_prefix_workspace_size(desc, geo, prefix)
+    return ctypes.byref(desc), ctypes.byref(geo), nbytes
 
 
 def qcache_workspace_size(desc, geo, topk: int, reuse: bool = False) -> int:
@@ -782,6 +789,15 @@ def qcache_workspace_size(desc, geo, topk: int, reuse: bool = False) -> int:
     n = getattr(_lib, name)(ctypes.byref(desc), ctypes.byref(geo), int(topk))
     if n == 0:
         raise KascadeError(INVALID_ARG, name)
+    return n
+
+
+def qcache_prefix_workspace_size(desc, geo, prefix_len: int) -> int:
+    """Workspace bytes of a decode call over a shared prefix."""
+    n = _lib.kascade_qcache_prefix_workspace_size(ctypes.byref(desc), ctypes.byref(geo),
+                                                  int(prefix_len))
+    if n == 0:
+        raise KascadeError(INVALID_ARG, "kascade_qcache_prefix_workspace_size")
     return n
 
 
@@ -1160,7 +1176,7 @@ def qcache_read(pages, slot_map, dtype=torch.bfloat16, k_scale=1.0, v_scale=1.0,
 
 
 def _qattn(q, pages, block_table, kv_lens, kv_len, group_map, scale, k_scale, v_scale, pooled, topk,
-           out, reuse=False):
+           out, reuse=False, prefix=None):
     """Checks one attention call's common tensors; returns (descriptor and
     geometry references, workspace bytes, (B, Hq, Hkv, N), device)."""
     nb, hkv, bs, d = _pages(pages)
@@ -1193,7 +1209,7 @@ def _qattn(q, pages, block_table, kv_lens, kv_len, group_map, scale, k_scale, v_
                                0.0 if scale is None else float(scale),
                                None if group_map is None else tuple(int(x) for x in group_map),
                                bool(pooled), bs, nb, width, float(k_scale), float(v_scale), topk,
-                               reuse)
+                               reuse, prefix)
     return desc, geo, nbytes, (B, Hq, hkv, N), dev
 
 
@@ -1225,6 +1241,30 @@ def qcache_dense_decode(q, pages, block_table, kv_lens, kv_len=None, group_map=N
                                             buf.data_ptr(), buf.numel(), _raw_stream(index)),
            "kascade_qcache_dense_decode")
     return (o, scores) if return_scores else o
+
+
+def qcache_prefix_decode(q, pages, block_table, kv_lens, prefix_len, kv_len=None, group_map=None,
+                         scale=None, k_scale=1.0, v_scale=1.0, out=None, ws=None, stream=None):
+    """qcache_dense_decode for a batch whose sequences begin with the same blocks:
+    the first prefix_len tokens (a multiple of the block size) of every sequence
+    with kv_lens[b] >= prefix_len are read, and attended to, once for all of them;
+    these sequences' rows of block_table have the same first entries. Shorter
+    sequences are attended to on their own."""
+    prefix_len = int(prefix_len)
+    desc, geo, nbytes, _, dev = _qattn(q, pages, block_table, kv_lens, kv_len, group_map, scale,
+                                       k_scale, v_scale, False, 0, out, prefix=prefix_len)
+    index = pages.get_device()
+    if _elsewhere(index, stream):
+        with _on(dev, stream, q, pages, block_table, kv_lens, out):
+            return qcache_prefix_decode(q, pages, block_table, kv_lens, prefix_len, kv_len,
+                                        group_map, scale, k_scale, v_scale, out, ws)
+    o = torch.empty_like(q) if out is None else out
+    buf = _qws(ws, dev, index, nbytes)
+    _check(_lib.kascade_qcache_prefix_decode(desc, geo, q.data_ptr(), pages.data_ptr(),
+                                             block_table.data_ptr(), kv_lens.data_ptr(),
+                                             prefix_len, o.data_ptr(), buf.data_ptr(), buf.numel(),
+                                             _raw_stream(index)), "kascade_qcache_prefix_decode")
+    return o
 
 
 def qcache_anchor_decode(q, pages, block_table, kv_lens, topk, kv_len=None, group_map=None,
