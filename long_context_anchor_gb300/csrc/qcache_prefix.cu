@@ -34,7 +34,20 @@ namespace {
 // copies the blocks in.
 constexpr int kDeqWarps = 8;
 constexpr int kMmaWarp = 8 + kDeqWarps, kLoadWarp = kMmaWarp + 1;
-constexpr int kThreads = 32 * (kLoadWarp + 1);
+constexpr int kThreads = 32 * (kLoadWarp + 3);   // a whole number of warpgroups
+// Registers: 640 threads are launched with 96 each; the warpgroups give back what
+// they do not need before the softmax takes more.
+constexpr int kLaunchRegs = 96, kSoftmaxRegs = 136, kDeqRegs = 64, kIssueRegs = 80;
+static_assert(kThreads == 640 && 256 * kSoftmaxRegs + 256 * kDeqRegs + 128 * kIssueRegs <=
+                                     kThreads * kLaunchRegs, "shares of what was launched");
+template <int N>
+__device__ __forceinline__ void more_regs() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_regs() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 template <int D>
 struct Smem {
@@ -211,6 +224,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
   const int w0 = min(total, static_cast<int>(blockIdx.x) * a.geo.per);
   const int w1 = min(total, w0 + a.geo.per);
 
+  if (warp >= kMmaWarp) {
+  fewer_regs<kIssueRegs>();
   if (warp == kLoadWarp) {
     // ------------------------------------------------------------- copies
     const int copy_sh = min(a.bs_shift, 6), ncopy = kPfxKeys >> copy_sh;
@@ -320,7 +335,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
       done[0] += n[0];
       done[1] += n[1];
     }
+  }
   } else if (warp >= 8) {
+    fewer_regs<kDeqRegs>();
     // ------------------------------------------------------- codes to fp16
     const int t = tid - 256;
     const int row = D == 128 ? t >> 2 : (t & 127) >> 1, part = D == 128 ? t & 3 : t & 1;
@@ -350,6 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
       }
     }
   } else {
+    more_regs<kSoftmaxRegs>();
     // ------------------------------------------------------------- softmax
     const int s = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
@@ -390,7 +408,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
       const float ml = fmaxf(a.scale * ldexpf(1.f, e - kQExp), 1e-37f) * kLog2e;
       // (fp32: both streams read both terms, which must not change under the other's scores)
       if (TERMS == 2) asm volatile("bar.sync 1, 256;" ::: "memory");
-#pragma unroll
+#pragma unroll 1
       for (int h = 0; h < D / 64; ++h) {
         uint32_t w[32];
 #pragma unroll
@@ -454,36 +472,41 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
               ok = mbar_wait_warp(pv_done + s, ph ^ 1, a.err, 0x593);
               if (!ok) break;
               tc_fence_after();
-#pragma unroll
-              for (int cc = 0; cc < D / 32; ++cc) {
-                uint32_t o[32];
-                tmem_ld32(tO + 32 * cc, o);
+#pragma unroll 1
+              for (int cc = 0; cc < D; cc += 16) {   // few at a time: the scores are held
+                uint32_t o[16];
+                tmem_ld16(tO + cc, o);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-                tmem_st32(tO + 32 * cc, o);
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+                tmem_st16(tO + cc, o);
               }
             }
           }
           const uint64_t ml2 = f2_pack(ml, ml), minus = f2_pack(-ref, -ref);
           const uint64_t shift = f2_pack(kPShift, kPShift);
           uint64_t sum[2] = {0ull, 0ull};
-          uint32_t hi[32], lo[TERMS == 2 ? 32 : 1];
+          // (in two halves: with all 32 words at once registers spill)
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            float p0, p1;
-            f2_unpack(f2_fma(f2_add(f2_pack(x[2 * i], x[2 * i + 1]), minus), ml2, shift), p0, p1);
-            p0 = ex2(p0);
-            p1 = ex2(p1);
-            sum[i & 1] = f2_add(sum[i & 1], f2_pack(p0, p1));
-            hi[i] = pack_f16(p0, p1);
-            if (TERMS == 2) lo[i] = pack_f16(p0 - f16_rounded(p0), p1 - f16_rounded(p1));
+          for (int half = 0; half < 2; ++half) {
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int at = 32 * half + 2 * i;
+              float p0, p1;
+              f2_unpack(f2_fma(f2_add(f2_pack(x[at], x[at + 1]), minus), ml2, shift), p0, p1);
+              p0 = ex2(p0);
+              p1 = ex2(p1);
+              sum[i & 1] = f2_add(sum[i & 1], f2_pack(p0, p1));
+              hi[i] = pack_f16(p0, p1);
+              if (TERMS == 2) lo[i] = pack_f16(p0 - f16_rounded(p0), p1 - f16_rounded(p1));
+            }
+            tmem_st16(tS + 16 * half, hi);
+            if (TERMS == 2) tmem_st16(tS + 32 + 16 * half, lo);
           }
           float s0, s1;
           f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
           l += s0 + s1;
-          tmem_st32(tS, hi);
-          if constexpr (TERMS == 2) tmem_st32(tS + 32, lo);
           tmem_wait_st();
         }
         tc_fence_before();
@@ -496,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
       tc_fence_after();
       if (!idle) {
         float* piece = a.part + pfx_piece_floats(D) * (2 * (static_cast<size_t>(p.unit) + blockIdx.x) + s);
-#pragma unroll
+#pragma unroll 1
         for (int cc = 0; cc < D / 32; ++cc) {
           uint32_t o[32];
           tmem_ld32(tO + 32 * cc, o);
