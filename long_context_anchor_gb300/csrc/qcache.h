@@ -50,6 +50,8 @@ struct QPrefixArgs {
   const int32_t* table;       // [B,max_blocks]
   const int32_t* lens;        // [B]
   float* part;                // pieces
+  float4* o;                  // [B * Hq][d / 4], [B * Hq]: the pieces joined, rows
+  float2* ml;                 // (sequence * Hkv + KV head) * G + slot
   unsigned int* err;
   int B, Hq, Hkv, G, N, P;    // P: tokens of the prefix, > 0
   int bs_shift, num_blocks, max_blocks;
@@ -84,11 +86,11 @@ struct QDecodeArgs {
   const int32_t* plan_count;  // [B*Hkv][chunks]
   int plan_chunks, topk;
   int S;                      // splits per (sequence, KV head) of the reuse kernel
-  // dense over a shared prefix: its pieces, which are joined into the outputs of
-  // sequences with at least P tokens, whose own part starts there (0: no prefix)
-  const float* pfx_part;
+  // dense over a shared prefix: its state (QPrefixArgs), which is joined into the outputs
+  // of sequences with at least P tokens, whose own part starts there (0: no prefix)
+  const float4* pfx_o;
+  const float2* pfx_ml;
   int P;
-  QPrefixGeo geo;
   int16_t heads[kMaxQHeads];  // heads[g*G + slot]
 };
 

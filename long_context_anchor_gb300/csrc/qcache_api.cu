@@ -60,7 +60,7 @@ struct QLayout {
   size_t plan, plan_count;                                // topk >= 1, sets per query head
   size_t spill, row_stat, pool;                           // topk >= 1, anchor layers
   size_t reuse, total;                                    // bytes: without an anchor layer, in all
-  size_t prefix;                                          // decode over a shared prefix
+  size_t prefix, prefix_o, prefix_ml;                     // decode over a shared prefix
 };
 
 QLayout qlayout(const Shape& s, int topk) {
@@ -139,7 +139,9 @@ QLayout prefix_layout(const Shape& s, int P) {
   L.prefix = L.total;
   if (P > 0) {
     const QPrefixGeo most = prefix_geo(s.B, s.G, s.Hkv, P, s.dtype, kQMaxCtas);
-    L.total = align256(L.total + pfx_pieces(most, s.Hkv) * pfx_piece_floats(s.d) * sizeof(float));
+    L.prefix_o = align256(L.prefix + pfx_pieces(most, s.Hkv) * pfx_piece_floats(s.d) * sizeof(float));
+    L.prefix_ml = align256(L.prefix_o + static_cast<size_t>(s.B) * s.Hq * s.d * sizeof(float));
+    L.total = align256(L.prefix_ml + static_cast<size_t>(s.B) * s.Hq * sizeof(float2));
   }
   return L;
 }
@@ -549,8 +551,8 @@ kascade_status kascade_qcache_prefix_decode(const kascade_desc* desc, const kasc
   QDecodeArgs a;
   fill_qargs(a, k, q, pages, block_table, kv_lens, out, ws);
   a.P = prefix_len;
-  a.pfx_part = at<float>(ws, k.L.prefix);
-  a.geo = prefix_geo(k.s.B, k.s.G, k.s.Hkv, prefix_len, k.s.dtype, sm_count());
+  a.pfx_o = at<float4>(ws, k.L.prefix_o);
+  a.pfx_ml = at<float2>(ws, k.L.prefix_ml);
   QPrefixArgs x;
   memset(&x, 0, sizeof(x));
   x.q = q;
@@ -558,6 +560,8 @@ kascade_status kascade_qcache_prefix_decode(const kascade_desc* desc, const kasc
   x.table = block_table;
   x.lens = kv_lens;
   x.part = at<float>(ws, k.L.prefix);
+  x.o = at<float4>(ws, k.L.prefix_o);
+  x.ml = at<float2>(ws, k.L.prefix_ml);
   x.err = a.err;
   x.B = a.B;
   x.Hq = a.Hq;
@@ -569,7 +573,7 @@ kascade_status kascade_qcache_prefix_decode(const kascade_desc* desc, const kasc
   x.num_blocks = a.num_blocks;
   x.max_blocks = a.max_blocks;
   x.scale = a.scale;
-  x.geo = a.geo;
+  x.geo = prefix_geo(k.s.B, k.s.G, k.s.Hkv, prefix_len, k.s.dtype, sm_count());
   memcpy(x.heads, a.heads, sizeof(x.heads));
   if ((r = status_of(launch_qprefix(x, k.s.d, k.s.dtype, st))) != KASCADE_OK) return r;
   return status_of(launch_qdecode_dense(a, k.s.d, k.s.dtype, st));

@@ -394,36 +394,7 @@ __device__ __forceinline__ void write_row_stat(const QDecodeArgs& a, size_t row,
 }
 
 // Four dims e (float4 index within [G][D / 4]) of head h over pieces s0 .. s1-1,
-// the i-th at piece(i): running maximum, sum and output, with the loads of
-// several pieces in flight together.
-struct Joined {
-  float m, l;
-  float4 o;
-};
-// x += the N parts y (their weights do not wait for one another)
-template <int N>
-__device__ __forceinline__ void join_into(Joined& x, const Joined (&y)[N]) {
-  float M = x.m;
-#pragma unroll
-  for (int k = 0; k < N; ++k) M = fmaxf(M, y[k].m);
-  // a part without keys has m = kNoKey and l = o = 0 (or l NaN, which stays)
-  const float wx = ex2(x.m - M);
-  x.m = M;
-  x.l *= wx;
-  x.o.x *= wx;
-  x.o.y *= wx;
-  x.o.z *= wx;
-  x.o.w *= wx;
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const float w = ex2(y[k].m - M);
-    x.l = fmaf(w, y[k].l, x.l);
-    x.o.x = fmaf(w, y[k].o.x, x.o.x);
-    x.o.y = fmaf(w, y[k].o.y, x.o.y);
-    x.o.z = fmaf(w, y[k].o.z, x.o.z);
-    x.o.w = fmaf(w, y[k].o.w, x.o.w);
-  }
-}
+// the i-th at piece(i), with the loads of several pieces in flight together.
 template <bool GLOBAL, typename Piece>
 __device__ __forceinline__ Joined join_some(Piece piece, int s0, int s1, int G, int h, int e) {
   constexpr int kBatch = GLOBAL ? 8 : 4;   // loads of L2 lines take longer
@@ -463,45 +434,15 @@ __device__ __forceinline__ int start_of(const QDecodeArgs& a, int b) {
   return PREFIX ? pfx_start(a.lens, b, a.P, a.N, a.max_blocks, a.bs_shift) : 0;
 }
 
-// x and the prefix's pieces of the same output (b, g, head slot h, dims 4 e4 ..).
+// x and the prefix's state of the same output (b, g, head slot h, dims 4 e4 ..).
 template <int D>
 __device__ __forceinline__ Joined join_prefix(const QDecodeArgs& a, Joined x, int b, int g, int h,
                                               int e4) {
   if (start_of<true>(a, b) == 0) return x;
-  const QPrefixGeo& geo = a.geo;
-  const int row = b * a.G + h, tile = row / kPfxRows, r = row % kPfxRows;
-  const bool pair = tile < 2 * geo.pairs;
-  int unit, u0, u1;
-  if (pair) {
-    unit = g * geo.pairs + tile / 2;
-    u0 = unit * 2 * geo.nch;
-    u1 = u0 + 2 * geo.nch;
-  } else {
-    unit = a.Hkv * geo.pairs + g * geo.singles + tile - 2 * geo.pairs;
-    u0 = (unit + a.Hkv * geo.pairs) * geo.nch;
-    u1 = u0 + geo.nch;
-  }
-  const int c0 = u0 / geo.per, ctas = (u1 - 1) / geo.per - c0 + 1;
-  // pair: the tile's piece of every CTA; else both pieces of each
-  const int n = pair ? ctas : 2 * ctas, step = pair ? 2 : 1;
-  const size_t stride = step * pfx_piece_floats(D);
-  const float* p = a.pfx_part + pfx_piece_floats(D) * (2 * static_cast<size_t>(unit + c0) +
-                                                       (pair ? tile & 1 : 0));
-  constexpr int kBatch = 8;
-  for (int s = 0; s < n; s += kBatch) {
-    Joined y[kBatch];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      y[k] = {kNoKey, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-      if (s + k < n) {
-        const float* at = p + (s + k) * stride;
-        y[k].m = __ldcg(at + kPfxRows * D + r);
-        y[k].l = __ldcg(at + kPfxRows * (D + 1) + r);
-        y[k].o = __ldcg(reinterpret_cast<const float4*>(at + r * D) + e4);
-      }
-    }
-    join_into(x, y);
-  }
+  const size_t row = (static_cast<size_t>(b) * a.Hkv + g) * a.G + h;
+  const float2 ml = __ldcg(a.pfx_ml + row);
+  const Joined y[1] = {{ml.x, ml.y, __ldcg(a.pfx_o + row * (D / 4) + e4)}};
+  join_into(x, y);
   return x;
 }
 

@@ -7,8 +7,11 @@
 // shared memory for up to two tiles: S = Q K^T and O += P V on tcgen05 with fp16
 // operands and fp32 sums. As in the dense kernel a stored element is exact in
 // fp16, a row of q is scaled by a power of two (an fp32 q is two fp16 terms), weights
-// are 2^14 p against a reference within kSlack of the running maximum, rounded to
-// fp16 (fp32 outputs: two terms) for the product and summed unrounded.
+// are 2^10 p against a reference within kSlackHere of the running maximum, rounded
+// to fp16 (fp32 outputs: two terms) for the product and summed unrounded. The
+// wider slack (the dense kernel has 2^14 and 1.75) is for O: raising the reference
+// of any row of a warp rescales 32 of them in TMEM, 800 cycles of a chunk's 1600,
+// and scores of a usual spread rise by less than this after the first chunk.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -23,6 +26,9 @@
 namespace kascade {
 namespace {
 
+constexpr int kShiftHere = 10;
+constexpr float kSlackHere = 5.75f;   // weights reach 2^15.75, within fp16
+
 // Two streams, each with its scores, its running state and its O, run through
 // the same code: a unit of two row tiles gives each stream one of them and every
 // chunk; a unit of one tile gives both streams that tile and every other chunk
@@ -30,11 +36,11 @@ namespace {
 // runs, the tensor cores work for the other.
 //
 // Roles: warps 4s .. 4s+3 are stream s's softmax, a thread per row; then
-// kDeqWarps warps that turn codes into fp16; one warp that issues the MMAs; one that
-// copies the blocks in.
+// kDeqWarps warps that turn codes into fp16; a warp per stream that issues its
+// MMAs; one that copies the blocks in.
 constexpr int kDeqWarps = 8;
-constexpr int kMmaWarp = 8 + kDeqWarps, kLoadWarp = kMmaWarp + 1;
-constexpr int kThreads = 32 * (kLoadWarp + 3);   // a whole number of warpgroups
+constexpr int kMmaWarp = 8 + kDeqWarps, kLoadWarp = kMmaWarp + 2;
+constexpr int kThreads = 32 * (kLoadWarp + 2);   // a whole number of warpgroups
 // Registers: 640 threads are launched with 96 each; the warpgroups give back what
 // they do not need before the softmax takes more.
 constexpr int kLaunchRegs = 96, kSoftmaxRegs = 136, kDeqRegs = 64, kIssueRegs = 80;
@@ -49,26 +55,38 @@ __device__ __forceinline__ void fewer_regs() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <int D>
-struct Smem {
+template <int D, int TERMS>
+struct Shapes {
+  // TMEM columns, 512 in all: Q (the first 64 dims of each tile, fp16 pairs; the
+  // other 64 are in shared memory; fp32: both terms of the one tile whole), S of
+  // each stream, its weights P, its O. fp32 with d = 128 has no room for P beside S:
+  // it lies over it, and the next scores wait for the product.
+  static constexpr bool OVER = D == 128 && TERMS == 2;
+  static constexpr bool QSMEM = D == 128 && TERMS == 1;
+  static constexpr int Q_COLS = TERMS == 2 ? D / 2 : 32;      // of a tile, or of a term
+  static constexpr int P_COLS = 32 * TERMS;
+  static constexpr int S0 = 2 * Q_COLS, P0 = OVER ? S0 : S0 + 128;
+  static constexpr int O_COLS = D, O0 = OVER ? S0 + 128 : P0 + 2 * P_COLS;
+  static constexpr int P_STEP = OVER ? 64 : P_COLS;
+  static_assert(O0 + 2 * O_COLS <= 512, "TMEM columns");
+
   static constexpr int HALF = kPfxKeys * 128;           // 64 dims of a chunk's K or V in fp16
   static constexpr int TILE = HALF * (D / 64);          // a chunk's K, or its V
   static constexpr int STAGE = 2 * TILE;
   static constexpr int NST = D == 128 ? 4 : 6;          // fp16 chunks
   static constexpr int RAW = (kPfxKeys / kQGroup) * qgroup_bytes(D);
-  static constexpr int NR = D == 128 ? 8 : 12;          // chunks as stored
-  static constexpr int RAW0 = NST * STAGE;
+  static constexpr int NR = D == 128 ? 7 : 12;          // chunks as stored
+  static constexpr int Q_TILE = QSMEM ? kPfxRows * 128 : 0;   // a stream's dims 64 .. 127
+  static constexpr int QS = NST * STAGE;
+  static constexpr int RAW0 = QS + 2 * Q_TILE;
   static constexpr int BAR = RAW0 + NR * RAW;
-  static constexpr int NBAR = 2 * NR + 2 * NST + 8;
+  static constexpr int NBAR = 2 * NR + 2 * NST + 10;
   static constexpr int VALID = BAR + NBAR * 8;          // int [NR + NST]: bit per 16 keys
   static constexpr int TMEM = VALID + (NR + NST) * 4;
   static constexpr int BYTES = TMEM + 8;
   static constexpr size_t SMEM = BYTES + 1024;          // slack for 1024-byte alignment
   static_assert(SMEM <= 232448 - 64, "fits in shared memory");
 };
-// TMEM columns: Q (fp16 pairs; two tiles, or the two terms of one), S of each
-// stream (its P over it: both terms of 64 weights are 64 columns), O
-constexpr int kTQ = 0, kTS = 128, kTO = 256;
 
 __device__ __forceinline__ uint64_t k_desc(uint32_t tile, int kk) {   // 16 dims of 64 keys
   return sw128_desc(tile + (kk >> 2) * (kPfxKeys * 128) + (kk & 3) * 32, 16, 1024);
@@ -170,7 +188,7 @@ __device__ __forceinline__ void load_q8(const void* row, int at, float (&x)[8]) 
 
 template <int D, int TERMS>
 __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__ QPrefixArgs a) {
-  using SM = Smem<D>;
+  using SM = Shapes<D, TERMS>;
   constexpr int NST = SM::NST, NR = SM::NR;
   pdl_wait();
   pdl_trigger();
@@ -184,10 +202,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
   uint64_t* raw_free = bars + NR;       // [NR] ... and were read
   uint64_t* kv_ready = bars + 2 * NR;   // [NST] fp16 K and V written
   uint64_t* kv_free = kv_ready + NST;   // [NST] ... and used
-  uint64_t* q_ready = kv_free + NST;    // [2] by stream: Q in TMEM
+  uint64_t* q_ready = kv_free + NST;    // [2] by stream: Q written
   uint64_t* s_full = q_ready + 2;       // [2] scores of the stream's chunk
-  uint64_t* p_full = q_ready + 4;       // [2] its weights written over them
-  uint64_t* pv_done = q_ready + 6;      // [2] their product with V
+  uint64_t* s_free = q_ready + 4;       // [2] ... read
+  uint64_t* p_full = q_ready + 6;       // [2] its weights written
+  uint64_t* pv_done = q_ready + 8;      // [2] their product with V
   int* raw_valid = reinterpret_cast<int*>(sm + SM::VALID);
   int* kv_valid = raw_valid + NR;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + SM::TMEM);
@@ -200,20 +219,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
       atomicMin(&s_src, b);
       break;
     }
-  if (tid < 2 * NR + 2 * NST + 8) {
-    const int i = tid;
-    const int count = i < NR ? 1 : i < 2 * NR ? kDeqWarps : i < 2 * NR + NST ? kDeqWarps
-                      : i < 2 * NR + 2 * NST ? 1
-                      : i < 2 * NR + 2 * NST + 2 ? 128
-                      : i < 2 * NR + 2 * NST + 4 ? 1
-                      : i < 2 * NR + 2 * NST + 6 ? 128 : 1;
+  if (tid < SM::NBAR) {
+    const int i = tid, j = i - 2 * NR, k = j - 2 * NST;   // k: pairs from q_ready on
+    const int count = i < NR ? 1 : i < 2 * NR ? kDeqWarps
+                      : j < NST ? kDeqWarps : j < 2 * NST ? 2   // both streams, or one twice
+                      : k < 2 ? 128 : k < 4 ? 1 : k < 8 ? 128 : 1;
     mbar_init(bars + i, count);
     fence_barrier_init();
   }
   __syncthreads();
   const int src = s_src;
   if (src >= a.B) return;   // nobody has it: no piece is read either
-  if (warp == kMmaWarp) tmem_alloc(s_tmem, 512);
+  if (warp == kMmaWarp) tmem_alloc(s_tmem, 512);   // one CTA per SM
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -225,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
   const int w1 = min(total, w0 + a.geo.per);
 
   if (warp >= kMmaWarp) {
-  fewer_regs<kIssueRegs>();
+    fewer_regs<kIssueRegs>();
   if (warp == kLoadWarp) {
     // ------------------------------------------------------------- copies
     const int copy_sh = min(a.bs_shift, 6), ncopy = kPfxKeys >> copy_sh;
@@ -275,65 +292,71 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
     // leave no copy in flight
     for (uint32_t k = kc > NR ? kc - NR : 0; k < kc; ++k)
       mbar_wait(raw_full + k % NR, (k / NR) & 1, a.err, 0x562);
-  } else if (warp == kMmaWarp) {
+  } else if (warp < kLoadWarp) {
     // --------------------------------------------------------- tensor cores
     constexpr uint32_t idq = idesc_f16_f32(128, kPfxKeys, 0), idv = idesc_f16_f32(128, D, 1);
-    uint32_t kc = 0, n_unit = 0;
-    uint32_t done[2] = {0u, 0u};   // chunks of each stream so far
-    const uint32_t kv0 = smem_u32(sm);
+    const int s = warp - kMmaWarp;
+    const uint32_t kv0 = smem_u32(sm), sQ = smem_u32(sm + SM::QS) + s * SM::Q_TILE;
+    const uint32_t tS = tmem + SM::S0 + 64 * s, tP = tmem + SM::P0 + SM::P_STEP * s;
+    const uint32_t tO = tmem + SM::O0 + SM::O_COLS * s;
+    uint32_t kc = 0, done = 0, n_part = 0;   // chunks of the CTA, of the stream; parts
     bool ok = true;
-    for (int f = w0; ok && f < w1; ++n_unit) {
+    for (int f = w0; ok && f < w1; ++n_part) {
       const Part p = part_at(a.geo, a.Hkv, f, w1);
       f = p.next;
-      // S = Q K^T of stream s's t-th chunk of the part
-      auto issue_s = [&](int s, int t) {
+      const int n = p.chunks(s);
+      // S = Q K^T of the t-th chunk
+      auto issue_s = [&](int t) {
         const uint32_t k = kc + p.local(s, t), st = k % NST;
         if (!mbar_wait_warp(kv_ready + st, (k / NST) & 1, a.err, 0x571)) return false;
         tc_fence_after();
-        const uint32_t tS = tmem + kTS + 64 * s;
+        const uint32_t kt = kv0 + st * SM::STAGE;
 #pragma unroll
-        for (int term = 0; term < TERMS; ++term)
+        for (int term = 0; term < TERMS; ++term) {
+          const uint32_t tQ = tmem + SM::Q_COLS * (TERMS == 2 ? term : s);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            tc_mma_ts(tS, tmem + kTQ + 64 * (TERMS == 2 ? term : s) + kk * 8,
-                      k_desc(kv0 + st * SM::STAGE, kk), idq, term > 0 || kk > 0 ? 1u : 0u);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t acc = term > 0 || kk > 0 ? 1u : 0u;
+            if (SM::QSMEM && kk >= 4)
+              tc_mma(tS, sw128_desc(sQ + (kk & 3) * 32, 16, 1024), k_desc(kt, kk), idq, acc);
+            else
+              tc_mma_ts(tS, tQ + kk * 8, k_desc(kt, kk), idq, acc);
+          }
+        }
         tc_commit(s_full + s);
         return true;
       };
-      auto issue_pv = [&](int s, int t) {
+      // O += P V; the part's first product overwrites O
+      auto issue_pv = [&](int t) {
         const uint32_t k = kc + p.local(s, t), st = k % NST;
-        if (!mbar_wait_warp(p_full + s, (done[s] + t) & 1, a.err, 0x572)) return false;
+        if (!mbar_wait_warp(p_full + s, (done + t) & 1, a.err, 0x572)) return false;
         tc_fence_after();
-        const uint32_t tP = tmem + kTS + 64 * s, tO = tmem + kTO + 128 * s;
+        const uint32_t vt = kv0 + st * SM::STAGE + SM::TILE;
 #pragma unroll
         for (int term = 0; term < TERMS; ++term)
 #pragma unroll
           for (int kk = 0; kk < kPfxKeys / 16; ++kk)
-            tc_mma_ts(tO, tP + 32 * term + kk * 8, v_desc(kv0 + st * SM::STAGE + SM::TILE, kk), idv,
+            tc_mma_ts(tO, tP + 32 * term + kk * 8, v_desc(vt, kk), idv,
                       t > 0 || term > 0 || kk > 0 ? 1u : 0u);
         tc_commit(pv_done + s);
-        if (p.tiles == 1 || s == 1) tc_commit(kv_free + st);   // the chunk's last use
+        tc_commit(kv_free + st);
+        if (p.tiles == 1) tc_commit(kv_free + st);   // for the stream that does not use it
         return true;
       };
-      const int n[2] = {p.chunks(0), p.chunks(1)};
-      for (int s = 0; ok && s < 2; ++s) {
-        ok = mbar_wait_warp(q_ready + s, n_unit & 1, a.err, 0x573);
-        if (TERMS == 2 && ok && s == 0) ok = mbar_wait_warp(q_ready + 1, n_unit & 1, a.err, 0x573);
-        tc_fence_after();
-        if (ok && n[s] > 0) ok = issue_s(s, 0);
+      ok = mbar_wait_warp(q_ready + s, n_part & 1, a.err, 0x573);
+      if (TERMS == 2 && ok) ok = mbar_wait_warp(q_ready + 1 - s, n_part & 1, a.err, 0x573);
+      tc_fence_after();
+      if (ok && n > 0) ok = issue_s(0);
+      for (int t = 0; ok && t < n; ++t) {
+        // the next scores once these are read (or, over the weights, once those are used)
+        if (!SM::OVER && t + 1 < n)
+          ok = mbar_wait_warp(s_free + s, (done + t) & 1, a.err, 0x574) && issue_s(t + 1);
+        if (ok) ok = issue_pv(t);
+        if (SM::OVER && ok && t + 1 < n)
+          ok = mbar_wait_warp(pv_done + s, (done + t) & 1, a.err, 0x575) && issue_s(t + 1);
       }
-      for (int t = 0; ok && t < n[0]; ++t)
-        for (int s = 0; ok && s < 2; ++s) {
-          if (t >= n[s]) continue;
-          ok = issue_pv(s, t);
-          if (ok && t + 1 < n[s]) {
-            // the next scores go where this product's weights are
-            ok = mbar_wait_warp(pv_done + s, (done[s] + t) & 1, a.err, 0x574) && issue_s(s, t + 1);
-          }
-        }
       kc += p.c1 - p.c0;
-      done[0] += n[0];
-      done[1] += n[1];
+      done += n;
     }
   }
   } else if (warp >= 8) {
@@ -371,8 +394,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
     // ------------------------------------------------------------- softmax
     const int s = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tQ = tmem + kTQ + 64 * s + lane_base, tS = tmem + kTS + 64 * s + lane_base;
-    const uint32_t tO = tmem + kTO + 128 * s + lane_base;
+    const uint32_t tQ = tmem + SM::Q_COLS * s + lane_base, tS = tmem + SM::S0 + 64 * s + lane_base;
+    const uint32_t tP = tmem + SM::P0 + SM::P_STEP * s + lane_base;
+    const uint32_t tO = tmem + SM::O0 + SM::O_COLS * s + lane_base;
+    const uint32_t sQ = smem_u32(sm + SM::QS) + s * SM::Q_TILE;
     // sequences whose tables name other blocks
     const int front = a.P >> a.bs_shift;
     for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + tid;
@@ -425,8 +450,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
             w[4 * i + j] = pack_f16(lo, hi);
           }
         }
-        tmem_st32(tQ + 32 * h, w);
+        if (SM::QSMEM && h == 1) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
+                             sQ + sw128_offset(kPfxRows, r, i)),
+                         "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
+                         : "memory");
+        } else {
+          tmem_st32(tQ + 32 * h, w);
+        }
       }
+      if (SM::QSMEM) fence_proxy_async_smem();
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(q_ready + s);
@@ -434,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
       // the reference is kept as a raw product, and taken from the products before
       // they are scaled: a huge score's distance from it is exact
       float ref = kNoKey, l = 0.f;
-      const float slack = kSlack / ml;
+      const float slack = kSlackHere / ml;
       const int n = p.chunks(s);
       for (int t = 0; ok && t < n; ++t) {
         const uint32_t k = kc + p.local(s, t), st = k % NST, ph = (done + t) & 1;
@@ -453,6 +488,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
           }
           const int bits = kv_valid[st];
           tmem_wait_ld();
+          if (!SM::OVER) {
+            tc_fence_before();
+            mbar_arrive(s_free + s);
+          }
           if (bits != 0xf) {
 #pragma unroll
             for (int i = 0; i < 64; ++i)
@@ -468,8 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
             ref = up_to;
             l *= al;
             if (t > 0) {
-              // the stream's previous product is complete (its scores came after it)
-              ok = mbar_wait_warp(pv_done + s, ph ^ 1, a.err, 0x593);
+              ok = mbar_wait_warp(pv_done + s, ph ^ 1, a.err, 0x593);   // O is still
               if (!ok) break;
               tc_fence_after();
 #pragma unroll 1
@@ -484,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
             }
           }
           const uint64_t ml2 = f2_pack(ml, ml), minus = f2_pack(-ref, -ref);
-          const uint64_t shift = f2_pack(kPShift, kPShift);
+          const uint64_t shift = f2_pack(kShiftHere, kShiftHere);
           uint64_t sum[2] = {0ull, 0ull};
           // (in two halves: with all 32 words at once registers spill)
 #pragma unroll
@@ -501,13 +539,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
               hi[i] = pack_f16(p0, p1);
               if (TERMS == 2) lo[i] = pack_f16(p0 - f16_rounded(p0), p1 - f16_rounded(p1));
             }
-            tmem_st16(tS + 16 * half, hi);
-            if (TERMS == 2) tmem_st16(tS + 32 + 16 * half, lo);
+            if (half == 0 && !SM::OVER && t > 0) {   // the previous weights are used
+              ok = mbar_wait_warp(pv_done + s, ph ^ 1, a.err, 0x595);
+              tc_fence_after();
+            }
+            tmem_st16(tP + 16 * half, hi);
+            if (TERMS == 2) tmem_st16(tP + 32 + 16 * half, lo);
           }
+          if (!ok) break;
           float s0, s1;
           f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
           l += s0 + s1;
           tmem_wait_st();
+        } else if (!SM::OVER) {
+          mbar_arrive(s_free + s);
+          // no arrival for these weights before the last ones' phase is over
+          if (t > 0 && !mbar_wait_warp(pv_done + s, ph ^ 1, a.err, 0x596)) {
+            ok = false;
+            break;
+          }
         }
         tc_fence_before();
         mbar_arrive(p_full + s);
@@ -534,7 +584,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
                              : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         if (live) {
-          piece[kPfxRows * D + r] = ref == kNoKey ? kNoKey : ref * ml;
+          // (as the reference of weights held as 2^14 p)
+          piece[kPfxRows * D + r] = ref == kNoKey ? kNoKey : ref * ml + (kPShift - kShiftHere);
           piece[kPfxRows * (D + 1) + r] = l;
         }
       }
@@ -549,9 +600,91 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
   }
 }
 
+// The pieces of every row joined: D / 4 threads per row and worker, `workers` of them per
+// row, which take its pieces in turn and are joined in order.
+constexpr int kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) k_qprefix_join(const __grid_constant__ QPrefixArgs a,
+                                                               int workers) {
+  pdl_wait();
+  pdl_trigger();
+  constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, kBatch = 8;
+  __shared__ Joined scratch[kJoinThreads];
+  const int group = threadIdx.x / kLanes, e4 = threadIdx.x % kLanes;
+  const int worker = group % workers;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kGroups / workers) + group / workers;
+  const int64_t total = static_cast<int64_t>(a.B) * a.Hq;
+  const int64_t unit_row = row / a.G;   // sequence * Hkv + KV head
+  const int b = static_cast<int>(unit_row / a.Hkv), g = static_cast<int>(unit_row - static_cast<int64_t>(b) * a.Hkv);
+  const bool live = row < total && pfx_start(a.lens, b, a.P, a.N, a.max_blocks, a.bs_shift) > 0;
+  Joined x = {kNoKey, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  if (live) {
+    const QPrefixGeo& geo = a.geo;
+    const int kv_row = b * a.G + static_cast<int>(row - unit_row * a.G);
+    const int tile = kv_row / kPfxRows, r = kv_row % kPfxRows;
+    const bool pair = tile < 2 * geo.pairs;
+    int unit, u0, u1;
+    if (pair) {
+      unit = g * geo.pairs + tile / 2;
+      u0 = unit * 2 * geo.nch;
+      u1 = u0 + 2 * geo.nch;
+    } else {
+      unit = a.Hkv * geo.pairs + g * geo.singles + tile - 2 * geo.pairs;
+      u0 = (unit + a.Hkv * geo.pairs) * geo.nch;
+      u1 = u0 + geo.nch;
+    }
+    const int c0 = u0 / geo.per, ctas = (u1 - 1) / geo.per - c0 + 1;
+    // pair: the tile's piece of every CTA; else both pieces of each
+    const int n = pair ? ctas : 2 * ctas;
+    const size_t stride = (pair ? 2 : 1) * pfx_piece_floats(D);
+    const float* p = a.part + pfx_piece_floats(D) * (2 * static_cast<size_t>(unit + c0) +
+                                                     (pair ? tile & 1 : 0));
+    for (int s = worker; s < n; s += kBatch * workers) {
+      Joined y[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        y[k] = {kNoKey, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        if (s + k * workers < n) {
+          const float* at = p + (s + k * workers) * stride;
+          y[k].m = __ldcg(at + kPfxRows * D + r);
+          y[k].l = __ldcg(at + kPfxRows * (D + 1) + r);
+          y[k].o = __ldcg(reinterpret_cast<const float4*>(at + r * D) + e4);
+        }
+      }
+      join_into(x, y);
+    }
+  }
+  if (workers > 1) {
+    scratch[threadIdx.x] = x;
+    __syncthreads();
+    if (worker == 0 && live)
+      for (int w = 1; w < workers; ++w) {
+        const Joined y[1] = {scratch[threadIdx.x + w * kLanes]};
+        join_into(x, y);
+      }
+  }
+  if (worker == 0 && live) {
+    a.o[row * kLanes + e4] = x.o;
+    if (e4 == 0) a.ml[row] = make_float2(x.m, x.l);
+  }
+}
+
+template <int D>
+cudaError_t launch_join_t(const QPrefixArgs& a, cudaStream_t st) {
+  // pieces of a row at most, eight of them per worker
+  const int places = (a.geo.pairs > 0 ? 2 : 1) * a.geo.nch;
+  const int ctas = (places + a.geo.per - 1) / a.geo.per + 1;
+  const int pieces = a.geo.singles > 0 ? 2 * ctas : ctas;
+  const int workers = pieces > 16 ? 4 : pieces > 8 ? 2 : 1;
+  const int64_t per_cta = kJoinThreads / (D / 4) / workers;
+  const int64_t grid = (static_cast<int64_t>(a.B) * a.Hq + per_cta - 1) / per_cta;
+  return launch_pdl(k_qprefix_join<D>, dim3(static_cast<unsigned int>(grid)), dim3(kJoinThreads), 0,
+                    st, a, workers);
+}
+
 template <int D, int TERMS>
 cudaError_t launch_prefix_t(const QPrefixArgs& a, cudaStream_t st) {
-  constexpr size_t smem = Smem<D>::SMEM;
+  constexpr size_t smem = Shapes<D, TERMS>::SMEM;
   constexpr auto kern = k_qprefix<D, TERMS>;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
@@ -576,9 +709,13 @@ QPrefixGeo prefix_geo(int B, int G, int Hkv, int P, int dtype, int sms) {
 }
 
 cudaError_t launch_qprefix(const QPrefixArgs& a, int d, int dtype, cudaStream_t st) {
+  cudaError_t e;
   if (dtype == KASCADE_F32)
-    return d == 128 ? launch_prefix_t<128, 2>(a, st) : launch_prefix_t<64, 2>(a, st);
-  return d == 128 ? launch_prefix_t<128, 1>(a, st) : launch_prefix_t<64, 1>(a, st);
+    e = d == 128 ? launch_prefix_t<128, 2>(a, st) : launch_prefix_t<64, 2>(a, st);
+  else
+    e = d == 128 ? launch_prefix_t<128, 1>(a, st) : launch_prefix_t<64, 1>(a, st);
+  if (e != cudaSuccess) return e;
+  return d == 128 ? launch_join_t<128>(a, st) : launch_join_t<64>(a, st);
 }
 
 }  // namespace kascade

@@ -55,4 +55,35 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ float f16_rounded(float x) { return __half2float(__float2half_rn(x)); }
 
+// Four output dims of some keys: running maximum (log2 units), sum of the weights
+// and of weight * value.
+struct Joined {
+  float m, l;
+  float4 o;
+};
+// x += the N parts y (their weights do not wait for one another)
+template <int N>
+__device__ __forceinline__ void join_into(Joined& x, const Joined (&y)[N]) {
+  float M = x.m;
+#pragma unroll
+  for (int k = 0; k < N; ++k) M = fmaxf(M, y[k].m);
+  // a part without keys has m = kNoKey and l = o = 0 (or l NaN, which stays)
+  const float wx = ex2(x.m - M);
+  x.m = M;
+  x.l *= wx;
+  x.o.x *= wx;
+  x.o.y *= wx;
+  x.o.z *= wx;
+  x.o.w *= wx;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const float w = ex2(y[k].m - M);
+    x.l = fmaf(w, y[k].l, x.l);
+    x.o.x = fmaf(w, y[k].o.x, x.o.x);
+    x.o.y = fmaf(w, y[k].o.y, x.o.y);
+    x.o.z = fmaf(w, y[k].o.z, x.o.z);
+    x.o.w = fmaf(w, y[k].o.w, x.o.w);
+  }
+}
+
 }  // namespace kascade
