@@ -7,11 +7,12 @@
 // shared memory for up to two tiles: S = Q K^T and O += P V on tcgen05 with fp16
 // operands and fp32 sums. As in the dense kernel a stored element is exact in
 // fp16, a row of q is scaled by a power of two (an fp32 q is two fp16 terms), weights
-// are 2^10 p against a reference within kSlackHere of the running maximum, rounded
-// to fp16 (fp32 outputs: two terms) for the product and summed unrounded. The
-// wider slack (the dense kernel has 2^14 and 1.75) is for O: raising the reference
-// of any row of a warp rescales 32 of them in TMEM, 800 cycles of a chunk's 1600,
-// and scores of a usual spread rise by less than this after the first chunk.
+// are 2^8 p against a reference that is raised to the running maximum when a
+// chunk's weights add up to more than fp16 holds, rounded to fp16 (fp32 outputs: two
+// terms) for the product and summed unrounded. So the reference moves in a
+// part's first chunk and then rarely: raising it for any row of a warp rescales
+// 32 rows of O in TMEM, and looking for the maximum costs a fifth of a chunk's
+// arithmetic.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -26,8 +27,7 @@
 namespace kascade {
 namespace {
 
-constexpr int kShiftHere = 10;
-constexpr float kSlackHere = 5.75f;   // weights reach 2^15.75, within fp16
+constexpr float kShiftHere = 8.f;
 
 // Two streams, each with its scores, its running state and its O, run through
 // the same code: a unit of two row tiles gives each stream one of them and every
@@ -38,7 +38,12 @@ constexpr float kSlackHere = 5.75f;   // weights reach 2^15.75, within fp16
 // Roles: warps 4s .. 4s+3 are stream s's softmax, a thread per row; then
 // kDeqWarps warps that turn codes into fp16; a warp per stream that issues its
 // MMAs; one that copies the blocks in.
+// The widening warps work in teams, each on chunks of its own: a chunk costs a
+// warp two waits and two arrivals whatever its share of it (all eight warps on every
+// chunk: 1130 cycles a chunk at d = 64, half of them work).
 constexpr int kDeqWarps = 8;
+template <int D>
+constexpr int kTeamWarps = D == 128 ? 4 : 2;
 constexpr int kMmaWarp = 8 + kDeqWarps, kLoadWarp = kMmaWarp + 2;
 constexpr int kThreads = 32 * (kLoadWarp + 2);   // a whole number of warpgroups
 // Registers: 640 threads are launched with 96 each; the warpgroups give back what
@@ -73,7 +78,7 @@ struct Shapes {
   static constexpr int HALF = kPfxKeys * 128;           // 64 dims of a chunk's K or V in fp16
   static constexpr int TILE = HALF * (D / 64);          // a chunk's K, or its V
   static constexpr int STAGE = 2 * TILE;
-  static constexpr int NST = D == 128 ? 4 : 6;          // fp16 chunks
+  static constexpr int NST = D == 128 ? 4 : 8;          // fp16 chunks
   static constexpr int RAW = (kPfxKeys / kQGroup) * qgroup_bytes(D);
   static constexpr int NR = D == 128 ? 7 : 12;          // chunks as stored
   static constexpr int Q_TILE = QSMEM ? kPfxRows * 128 : 0;   // a stream's dims 64 .. 127
@@ -88,11 +93,17 @@ struct Shapes {
   static_assert(SMEM <= 232448 - 64, "fits in shared memory");
 };
 
-__device__ __forceinline__ uint64_t k_desc(uint32_t tile, int kk) {   // 16 dims of 64 keys
-  return sw128_desc(tile + (kk >> 2) * (kPfxKeys * 128) + (kk & 3) * 32, 16, 1024);
+// Matrix descriptors: of a chunk's K (16 dims of 64 keys a step), V (16 keys of
+// all dims a step) and the upper half of a Q tile; a step adds to the address.
+__device__ __forceinline__ uint64_t kq_desc(uint32_t tile) { return sw128_desc(tile, 16, 1024); }
+__device__ __forceinline__ uint64_t v_desc(uint32_t tile) {
+  return sw128_desc(tile, kPfxKeys * 128, 1024);
 }
-__device__ __forceinline__ uint64_t v_desc(uint32_t tile, int kk) {   // 16 keys of all dims
-  return sw128_desc(tile + kk * 2048, kPfxKeys * 128, 1024);
+__device__ __forceinline__ constexpr uint64_t k_step(int kk) {
+  return static_cast<uint64_t>(((kk >> 2) * (kPfxKeys * 128) + (kk & 3) * 32) >> 4);
+}
+__device__ __forceinline__ constexpr uint64_t v_step(int kk) {
+  return static_cast<uint64_t>((kk * 2048) >> 4);
 }
 // fp16 x fp16 -> fp32
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn_major) {
@@ -168,22 +179,15 @@ __device__ __forceinline__ void widen(const uint8_t* grp, int codes_at, int scal
   }
 }
 
-// 64 elements from element `at` of a row of q as 32-bit floats.
-template <int TERMS>
-__device__ __forceinline__ void load_q8(const void* row, int at, float (&x)[8]) {
-  if (TERMS == 2) {
-    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(row) + at);
-    const float4 a = __ldg(p), b = __ldg(p + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-  } else {
-    const uint4 u = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(row) + at));
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[2 * j] = __uint_as_float(w[j] << 16);
-      x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+// The lowest sequence that holds the whole prefix, whose table names its blocks, into
+// src (a.B before; shared memory; all threads).
+__device__ __forceinline__ void first_holder(const QPrefixArgs& a, int& src) {
+  for (int b = threadIdx.x; b < a.B; b += blockDim.x)
+    if (pfx_start(a.lens, b, a.P, a.N, a.max_blocks, a.bs_shift) > 0) {
+      atomicMin(&src, b);
+      break;
     }
-  }
+  __syncthreads();
 }
 
 template <int D, int TERMS>
@@ -211,23 +215,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
   int* kv_valid = raw_valid + NR;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + SM::TMEM);
 
-  // the lowest sequence that holds the whole prefix names its blocks
   if (tid == 0) s_src = a.B;
-  __syncthreads();
-  for (int b = tid; b < a.B; b += kThreads)
-    if (pfx_start(a.lens, b, a.P, a.N, a.max_blocks, a.bs_shift) > 0) {
-      atomicMin(&s_src, b);
-      break;
-    }
   if (tid < SM::NBAR) {
     const int i = tid, j = i - 2 * NR, k = j - 2 * NST;   // k: pairs from q_ready on
-    const int count = i < NR ? 1 : i < 2 * NR ? kDeqWarps
-                      : j < NST ? kDeqWarps : j < 2 * NST ? 2   // both streams, or one twice
+    const int count = i < NR ? 1 : i < 2 * NR ? kTeamWarps<D>
+                      : j < NST ? kTeamWarps<D> : j < 2 * NST ? 2   // both streams, or one twice
                       : k < 2 ? 128 : k < 4 ? 1 : k < 8 ? 128 : 1;
     mbar_init(bars + i, count);
     fence_barrier_init();
   }
   __syncthreads();
+  first_holder(a, s_src);
   const int src = s_src;
   if (src >= a.B) return;   // nobody has it: no piece is read either
   if (warp == kMmaWarp) tmem_alloc(s_tmem, 512);   // one CTA per SM
@@ -257,15 +255,22 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
       const Part p = part_at(a.geo, a.Hkv, f, w1);
       f = p.next;
       const uint8_t* head = a.cache + static_cast<size_t>(p.g) * head_bytes;
-      auto key_of = [&](int c) { return c * kPfxKeys + (lane << copy_sh); };
-      auto fetch = [&](int c) {
-        const int key = key_of(c);
-        return lane < ncopy && c < p.c1 && key < a.P ? __ldg(ids + (key >> a.bs_shift)) : 0;
+      // block ids come 32 at a time, a batch ahead: a load per chunk would take its
+      // latency in every one of them
+      auto fetch = [&](int c) {   // of the copies of chunks c .. c + 32 / ncopy - 1
+        const int key = c * kPfxKeys + (lane << copy_sh);
+        return key < a.P && c + lane / ncopy < p.c1 ? __ldg(ids + (key >> a.bs_shift)) : 0;
       };
-      int next = fetch(p.c0);
+      const int batch = 32 / ncopy;
+      int now = 0, next = fetch(p.c0);
       for (int c = p.c0; c < p.c1; ++c, ++kc) {
-        const int id = next, key = key_of(c), st = kc % NR;
-        next = fetch(c + 1);
+        const int in = (c - p.c0) % batch;
+        if (in == 0) {
+          now = next;
+          next = fetch(c + batch);
+        }
+        const int id = __shfl_sync(0xffffffffu, now, (in * ncopy + lane) & 31);
+        const int key = c * kPfxKeys + (lane << copy_sh), st = kc % NR;
         const bool want = lane < ncopy && key < a.P;
         const bool take = want && static_cast<unsigned int>(id) < static_cast<unsigned int>(a.num_blocks);
         if (want && !take) report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x552);
@@ -296,7 +301,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
     // --------------------------------------------------------- tensor cores
     constexpr uint32_t idq = idesc_f16_f32(128, kPfxKeys, 0), idv = idesc_f16_f32(128, D, 1);
     const int s = warp - kMmaWarp;
-    const uint32_t kv0 = smem_u32(sm), sQ = smem_u32(sm + SM::QS) + s * SM::Q_TILE;
+    const uint32_t kv0 = smem_u32(sm);
+    const uint64_t qd = kq_desc(smem_u32(sm + SM::QS) + s * SM::Q_TILE);
     const uint32_t tS = tmem + SM::S0 + 64 * s, tP = tmem + SM::P0 + SM::P_STEP * s;
     const uint32_t tO = tmem + SM::O0 + SM::O_COLS * s;
     uint32_t kc = 0, done = 0, n_part = 0;   // chunks of the CTA, of the stream; parts
@@ -310,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
         const uint32_t k = kc + p.local(s, t), st = k % NST;
         if (!mbar_wait_warp(kv_ready + st, (k / NST) & 1, a.err, 0x571)) return false;
         tc_fence_after();
-        const uint32_t kt = kv0 + st * SM::STAGE;
+        const uint64_t kd = kq_desc(kv0 + st * SM::STAGE);
 #pragma unroll
         for (int term = 0; term < TERMS; ++term) {
           const uint32_t tQ = tmem + SM::Q_COLS * (TERMS == 2 ? term : s);
@@ -318,9 +324,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t acc = term > 0 || kk > 0 ? 1u : 0u;
             if (SM::QSMEM && kk >= 4)
-              tc_mma(tS, sw128_desc(sQ + (kk & 3) * 32, 16, 1024), k_desc(kt, kk), idq, acc);
+              tc_mma(tS, qd + k_step(kk & 3), kd + k_step(kk), idq, acc);
             else
-              tc_mma_ts(tS, tQ + kk * 8, k_desc(kt, kk), idq, acc);
+              tc_mma_ts(tS, tQ + kk * 8, kd + k_step(kk), idq, acc);
           }
         }
         tc_commit(s_full + s);
@@ -331,12 +337,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
         const uint32_t k = kc + p.local(s, t), st = k % NST;
         if (!mbar_wait_warp(p_full + s, (done + t) & 1, a.err, 0x572)) return false;
         tc_fence_after();
-        const uint32_t vt = kv0 + st * SM::STAGE + SM::TILE;
+        const uint64_t vd = v_desc(kv0 + st * SM::STAGE + SM::TILE);
 #pragma unroll
         for (int term = 0; term < TERMS; ++term)
 #pragma unroll
           for (int kk = 0; kk < kPfxKeys / 16; ++kk)
-            tc_mma_ts(tO, tP + 32 * term + kk * 8, v_desc(vt, kk), idv,
+            tc_mma_ts(tO, tP + 32 * term + kk * 8, vd + v_step(kk), idv,
                       t > 0 || term > 0 || kk > 0 ? 1u : 0u);
         tc_commit(pv_done + s);
         tc_commit(kv_free + st);
@@ -362,24 +368,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
   } else if (warp >= 8) {
     fewer_regs<kDeqRegs>();
     // ------------------------------------------------------- codes to fp16
-    const int t = tid - 256;
-    const int row = D == 128 ? t >> 2 : (t & 127) >> 1, part = D == 128 ? t & 3 : t & 1;
+    constexpr int kTeam = kTeamWarps<D>, kTeams = kDeqWarps / kTeam, kParts = D / 32;
+    constexpr int kRows = 32 * kTeam / kParts;   // rows of K (and V) at a time
+    const int team = (warp - 8) / kTeam, t = tid - 256 - team * 32 * kTeam;
+    const int row0 = t / kParts, part = t % kParts;
     uint32_t kc = 0;
     bool ok = true;
     for (int f = w0; ok && f < w1;) {
       const Part p = part_at(a.geo, a.Hkv, f, w1);
       f = p.next;
-      for (int c = p.c0; c < p.c1; ++c, ++kc) {
-        const int rs = kc % NR, st = kc % NST;
-        ok = mbar_wait_warp(raw_full + rs, (kc / NR) & 1, a.err, 0x581) &&
-             mbar_wait_warp(kv_free + st, ((kc / NST) & 1) ^ 1, a.err, 0x582);
+      const uint32_t end = kc + p.c1 - p.c0;
+      // the team's first chunk from here on
+      for (uint32_t k = kc + (team + kTeams - kc % kTeams) % kTeams; k < end; k += kTeams) {
+        const int rs = k % NR, st = k % NST;
+        ok = mbar_wait_warp(raw_full + rs, (k / NR) & 1, a.err, 0x581) &&
+             mbar_wait_warp(kv_free + st, ((k / NST) & 1) ^ 1, a.err, 0x582);
         if (!ok) break;
         const int bits = raw_valid[rs];
-        const uint8_t* grp = sm + SM::RAW0 + rs * SM::RAW + (row >> 4) * qgroup_bytes(D);
-        const bool valid = (bits >> (row >> 4)) & 1;
+        const uint8_t* raw = sm + SM::RAW0 + rs * SM::RAW;
         const uint32_t tile = smem_u32(sm) + st * SM::STAGE;
-        if (D == 128 || t < 128) widen<D>(grp, 0, 8 * D, tile, row, part, valid);
-        if (D == 128 || t >= 128) widen<D>(grp, 9 * D, 17 * D, tile + SM::TILE, row, part, valid);
+#pragma unroll
+        for (int row = row0; row < kPfxKeys; row += kRows) {
+          const uint8_t* grp = raw + (row >> 4) * qgroup_bytes(D);
+          const bool valid = (bits >> (row >> 4)) & 1;
+          widen<D>(grp, 0, 8 * D, tile, row, part, valid);
+          widen<D>(grp, 9 * D, 17 * D, tile + SM::TILE, row, part, valid);
+        }
         if (t == 0) kv_valid[st] = bits;
         fence_proxy_async_smem();
         __syncwarp();
@@ -388,6 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
           mbar_arrive(raw_free + rs);
         }
       }
+      kc = end;
     }
   } else {
     more_regs<kSoftmaxRegs>();
@@ -398,15 +413,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
     const uint32_t tP = tmem + SM::P0 + SM::P_STEP * s + lane_base;
     const uint32_t tO = tmem + SM::O0 + SM::O_COLS * s + lane_base;
     const uint32_t sQ = smem_u32(sm + SM::QS) + s * SM::Q_TILE;
-    // sequences whose tables name other blocks
-    const int front = a.P >> a.bs_shift;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + tid;
-         i < static_cast<int64_t>(a.B) * front; i += static_cast<int64_t>(gridDim.x) * 256) {
-      const int b = static_cast<int>(i / front), j = static_cast<int>(i - static_cast<int64_t>(b) * front);
-      if (pfx_start(a.lens, b, a.P, a.N, a.max_blocks, a.bs_shift) > 0 &&
-          a.table[static_cast<size_t>(b) * a.max_blocks + j] != ids[j])
-        report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x551);
-    }
     uint32_t kc = 0, done = 0;
     bool ok = true;
     for (int f = w0; f < w1;) {
@@ -416,16 +422,33 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
       const int b = gr / a.G, slot = gr - b * a.G;
       const bool live = b < a.B && pfx_start(a.lens, b, a.P, a.N, a.max_blocks, a.bs_shift) > 0;
       const bool idle = !__any_sync(0xffffffffu, live);
-      // ---- this row of Q
-      float amax = 0.f;
+      // ---- this row of Q, 64 elements at a time; all of a pass's loads are in flight
+      // together, and a bf16 row is loaded once
+      constexpr int kVecs = TERMS == 2 ? 16 : 8;   // 16-byte pieces of 64 elements
       const size_t q_row = live ? static_cast<size_t>(b) * a.Hq + a.heads[p.g * a.G + slot] : 0;
-      const void* row = static_cast<const char*>(a.q) + q_row * D * (TERMS == 2 ? 4 : 2);
-      if (live)
-        for (int i = 0; i < D; i += 8) {
-          float x[8];
-          load_q8<TERMS>(row, i, x);
+      const uint4* row = reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) +
+                                                        q_row * D * (TERMS == 2 ? 4 : 2));
+      uint4 raw[D / 64][kVecs];
+      float amax = 0.f;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(x[j]));
+      for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+          raw[h][i] = live ? __ldg(row + h * kVecs + i) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+      for (int h = 0; h < D / 64; ++h)
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) {
+          const uint32_t w[4] = {raw[h][i].x, raw[h][i].y, raw[h][i].z, raw[h][i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (TERMS == 2) {
+              amax = fmaxf(amax, fabsf(__uint_as_float(w[j])));
+            } else {
+              amax = fmaxf(amax, fabsf(__uint_as_float(w[j] << 16)));
+              amax = fmaxf(amax, fabsf(__uint_as_float(w[j] & 0xffff0000u)));
+            }
+          }
         }
       int e = kQExp;
       if (amax > 0.f && amax < CUDART_INF_F) e = max(ilogbf(amax), -100);
@@ -433,21 +456,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
       const float ml = fmaxf(a.scale * ldexpf(1.f, e - kQExp), 1e-37f) * kLog2e;
       // (fp32: both streams read both terms, which must not change under the other's scores)
       if (TERMS == 2) asm volatile("bar.sync 1, 256;" ::: "memory");
-#pragma unroll 1
+#pragma unroll
       for (int h = 0; h < D / 64; ++h) {
         uint32_t w[32];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-          if (live) load_q8<TERMS>(row, 64 * h + 8 * i, x);
+        for (int i = 0; i < kVecs; ++i) {
+          const uint32_t v[4] = {raw[h][i].x, raw[h][i].y, raw[h][i].z, raw[h][i].w};
+          if (TERMS == 2) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            float lo = x[2 * j] * up, hi = x[2 * j + 1] * up;
-            if (TERMS == 2 && s == 1) {
-              lo -= f16_rounded(lo);
-              hi -= f16_rounded(hi);
+            for (int j = 0; j < 2; ++j) {
+              float lo = __uint_as_float(v[2 * j]) * up, hi = __uint_as_float(v[2 * j + 1]) * up;
+              if (s == 1) {
+                lo -= f16_rounded(lo);
+                hi -= f16_rounded(hi);
+              }
+              w[2 * i + j] = pack_f16(lo, hi);
             }
-            w[4 * i + j] = pack_f16(lo, hi);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              w[(4 * i + j) & 31] = pack_f16(__uint_as_float(v[j] << 16) * up,
+                                             __uint_as_float(v[j] & 0xffff0000u) * up);
           }
         }
         if (SM::QSMEM && h == 1) {
@@ -466,15 +495,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
       tc_fence_before();
       mbar_arrive(q_ready + s);
       // ---- its chunks
-      // the reference is kept as a raw product, and taken from the products before
-      // they are scaled: a huge score's distance from it is exact
-      float ref = kNoKey, l = 0.f;
-      const float slack = kSlackHere / ml;
+      float ref = kNoKey, l = 0.f;   // the reference, as a raw product
+      float c = 0.f;                 // weights are 2^(product * ml + c)
+      bool careful = true;           // see raise()
       const int n = p.chunks(s);
       for (int t = 0; ok && t < n; ++t) {
         const uint32_t k = kc + p.local(s, t), st = k % NST, ph = (done + t) & 1;
-        ok = mbar_wait_warp(s_full + s, ph, a.err, 0x591) &&
-             mbar_wait_warp(kv_ready + st, (k / NST) & 1, a.err, 0x592);   // for kv_valid
+        // (kv_valid was written before kv_ready, which the scores' MMAs waited for)
+        ok = mbar_wait_warp(s_full + s, ph, a.err, 0x591);
         if (!ok) break;
         tc_fence_after();
         if (!idle) {
@@ -497,18 +525,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
             for (int i = 0; i < 64; ++i)
               if (!((bits >> (i / 16)) & 1)) x[i] = kNegInf;
           }
-          float mx[4] = {x[0], x[1], x[2], x[3]};
+          // The reference goes up to this chunk's largest product (all lanes).
+          auto raise = [&]() {
+            float mx[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-          for (int i = 4; i + 1 < 64; i += 2) mx[(i >> 1) & 3] = fmax3(mx[(i >> 1) & 3], x[i], x[i + 1]);
-          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-          const bool raise = top > ref + slack;
-          if (__any_sync(0xffffffffu, raise)) {
-            const float up_to = raise ? top : ref, al = ex2((ref - up_to) * ml);
+            for (int i = 4; i + 1 < 64; i += 2) mx[(i >> 1) & 3] = fmax3(mx[(i >> 1) & 3], x[i], x[i + 1]);
+            const float up_to = fmax3(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]), ref);
+            const float al = ex2((ref - up_to) * ml);
+            const bool moved = __any_sync(0xffffffffu, up_to > ref);
             ref = up_to;
             l *= al;
-            if (t > 0) {
-              ok = mbar_wait_warp(pv_done + s, ph ^ 1, a.err, 0x593);   // O is still
-              if (!ok) break;
+            if (moved && t > 0) {
+              ok = ok && mbar_wait_warp(pv_done + s, ph ^ 1, a.err, 0x593);   // O is still
+              if (!ok) return;
               tc_fence_after();
 #pragma unroll 1
               for (int cc = 0; cc < D; cc += 16) {   // few at a time: the scores are held
@@ -520,37 +549,58 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
                 tmem_st16(tO + cc, o);
               }
             }
-          }
-          const uint64_t ml2 = f2_pack(ml, ml), minus = f2_pack(-ref, -ref);
-          const uint64_t shift = f2_pack(kShiftHere, kShiftHere);
-          uint64_t sum[2] = {0ull, 0ull};
-          // (in two halves: with all 32 words at once registers spill)
+            // c's rounding is common to the row's weights; where it would be felt (or would
+            // overflow them) products are taken relative to the reference first
+            c = fmaf(-ref, ml, kShiftHere);
+            careful = __any_sync(0xffffffffu, !(fabsf(c) < 1024.f));
+          };
+          // A chunk's weights are taken with the reference as it is; only where their
+          // sum shows that one may have passed fp16 the products are searched for their
+          // maximum, and the weights taken again.
+          bool again = false;
+          if (t == 0 || careful) raise();
+          else again = true;
+          float sum;
+          while (true) {
+            float base = c;
+            if (careful) {
+              base = kShiftHere;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t hi[16], lo[16];
+              for (int i = 0; i < 64; ++i) x[i] -= ref;
+            }
+            const uint64_t ml2 = f2_pack(ml, ml), c2 = f2_pack(base, base);
+            uint64_t part_sum[2] = {0ull, 0ull};
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int at = 32 * half + 2 * i;
-              float p0, p1;
-              f2_unpack(f2_fma(f2_add(f2_pack(x[at], x[at + 1]), minus), ml2, shift), p0, p1);
-              p0 = ex2(p0);
-              p1 = ex2(p1);
-              sum[i & 1] = f2_add(sum[i & 1], f2_pack(p0, p1));
-              hi[i] = pack_f16(p0, p1);
-              if (TERMS == 2) lo[i] = pack_f16(p0 - f16_rounded(p0), p1 - f16_rounded(p1));
+            for (int half = 0; half < 2; ++half) {
+              uint32_t hi[16], lo[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const int at = 32 * half + 2 * i;
+                float p0, p1;
+                f2_unpack(f2_fma(f2_pack(x[at], x[at + 1]), ml2, c2), p0, p1);
+                p0 = ex2(p0);
+                p1 = ex2(p1);
+                part_sum[i & 1] = f2_add(part_sum[i & 1], f2_pack(p0, p1));
+                hi[i] = pack_f16(p0, p1);
+                if (TERMS == 2) lo[i] = pack_f16(p0 - f16_rounded(p0), p1 - f16_rounded(p1));
+              }
+              if (half == 0 && !SM::OVER && t > 0) {   // the previous weights are used
+                ok = ok && mbar_wait_warp(pv_done + s, ph ^ 1, a.err, 0x595);
+                tc_fence_after();
+              }
+              tmem_st16(tP + 16 * half, hi);
+              if (TERMS == 2) tmem_st16(tP + 32 + 16 * half, lo);
             }
-            if (half == 0 && !SM::OVER && t > 0) {   // the previous weights are used
-              ok = mbar_wait_warp(pv_done + s, ph ^ 1, a.err, 0x595);
-              tc_fence_after();
-            }
-            tmem_st16(tP + 16 * half, hi);
-            if (TERMS == 2) tmem_st16(tP + 32 + 16 * half, lo);
+            float s0, s1;
+            f2_unpack(f2_add(part_sum[0], part_sum[1]), s0, s1);
+            sum = s0 + s1;
+            tmem_wait_st();
+            if (!again || !__any_sync(0xffffffffu, !(sum < 65000.f))) break;
+            again = false;
+            raise();
           }
           if (!ok) break;
-          float s0, s1;
-          f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
-          l += s0 + s1;
-          tmem_wait_st();
+          l += sum;
         } else if (!SM::OVER) {
           mbar_arrive(s_free + s);
           // no arrival for these weights before the last ones' phase is over
@@ -585,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
         }
         if (live) {
           // (as the reference of weights held as 2^14 p)
-          piece[kPfxRows * D + r] = ref == kNoKey ? kNoKey : ref * ml + (kPShift - kShiftHere);
+          piece[kPfxRows * D + r] = ref == kNoKey ? kNoKey : (careful ? ref * ml + (kPShift - kShiftHere) : kPShift - c);
           piece[kPfxRows * (D + 1) + r] = l;
         }
       }
@@ -610,6 +660,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_qprefix_join(const __grid_cons
   pdl_trigger();
   constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, kBatch = 8;
   __shared__ Joined scratch[kJoinThreads];
+  __shared__ int s_src;
   const int group = threadIdx.x / kLanes, e4 = threadIdx.x % kLanes;
   const int worker = group % workers;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kGroups / workers) + group / workers;
@@ -654,14 +705,26 @@ __global__ void __launch_bounds__(kJoinThreads) k_qprefix_join(const __grid_cons
       join_into(x, y);
     }
   }
+  if (threadIdx.x == 0) s_src = a.B;
+  scratch[threadIdx.x] = x;
+  __syncthreads();
+  first_holder(a, s_src);
   if (workers > 1) {
-    scratch[threadIdx.x] = x;
-    __syncthreads();
     if (worker == 0 && live)
       for (int w = 1; w < workers; ++w) {
         const Joined y[1] = {scratch[threadIdx.x + w * kLanes]};
         join_into(x, y);
       }
+  }
+  // sequences whose tables name other blocks than the lowest one's
+  const int front = a.P >> a.bs_shift;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x;
+       i < static_cast<int64_t>(a.B) * front; i += static_cast<int64_t>(gridDim.x) * kJoinThreads) {
+    const int bb = static_cast<int>(i / front), j = static_cast<int>(i - static_cast<int64_t>(bb) * front);
+    if (bb <= s_src || pfx_start(a.lens, bb, a.P, a.N, a.max_blocks, a.bs_shift) == 0) continue;
+    if (a.table[static_cast<size_t>(bb) * a.max_blocks + j] !=
+        a.table[static_cast<size_t>(s_src) * a.max_blocks + j])
+      report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x551);
   }
   if (worker == 0 && live) {
     a.o[row * kLanes + e4] = x.o;
