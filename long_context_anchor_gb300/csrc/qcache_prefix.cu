@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *s_tmem;
+  const uint32_t tmem = warp_uniform(*s_tmem);
   const int32_t* ids = a.table + static_cast<size_t>(src) * a.max_blocks;
 
   const int total = a.Hkv * (2 * a.geo.pairs + a.geo.singles) * a.geo.nch;
@@ -243,55 +243,56 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
     fewer_regs<kIssueRegs>();
   if (warp == kLoadWarp) {
     // ------------------------------------------------------------- copies
-    const int copy_sh = min(a.bs_shift, 6), ncopy = kPfxKeys >> copy_sh;
+    // kAhead chunks at a time, four lanes each: one chunk at a time took 1050 cycles
+    constexpr int kAhead = D == 128 ? 2 : 4;
+    const int copy_sh = min(a.bs_shift, 6), ncopy = kPfxKeys >> copy_sh;   // copies of a chunk
     const uint32_t copy_bytes = static_cast<uint32_t>(qgroup_bytes(D)) << (copy_sh - 4);
     const uint32_t head_bytes = static_cast<uint32_t>(qgroup_bytes(D)) << (a.bs_shift - 4);
     const uint64_t block_bytes = static_cast<uint64_t>(head_bytes) * a.Hkv;
     const int gmask = (1 << (a.bs_shift - 4)) - 1;
     const unsigned int groups = (1u << (1 << (copy_sh - 4))) - 1u;   // a copy's bits
+    const int sub = lane >> 2, cp = lane & 3;
     uint32_t kc = 0;
     bool ok = true;
     for (int f = w0; ok && f < w1;) {
       const Part p = part_at(a.geo, a.Hkv, f, w1);
       f = p.next;
       const uint8_t* head = a.cache + static_cast<size_t>(p.g) * head_bytes;
-      // block ids come 32 at a time, a batch ahead: a load per chunk would take its
-      // latency in every one of them
-      auto fetch = [&](int c) {   // of the copies of chunks c .. c + 32 / ncopy - 1
-        const int key = c * kPfxKeys + (lane << copy_sh);
-        return key < a.P && c + lane / ncopy < p.c1 ? __ldg(ids + (key >> a.bs_shift)) : 0;
+      // this lane's copy of chunks c + sub; ids are loaded a turn ahead
+      auto key_of = [&](int c) { return (c + sub) * kPfxKeys + (cp << copy_sh); };
+      auto wanted = [&](int c) {
+        return sub < kAhead && cp < ncopy && c + sub < p.c1 && key_of(c) < a.P;
       };
-      const int batch = 32 / ncopy;
-      int now = 0, next = fetch(p.c0);
-      for (int c = p.c0; c < p.c1; ++c, ++kc) {
-        const int in = (c - p.c0) % batch;
-        if (in == 0) {
-          now = next;
-          next = fetch(c + batch);
-        }
-        const int id = __shfl_sync(0xffffffffu, now, (in * ncopy + lane) & 31);
-        const int key = c * kPfxKeys + (lane << copy_sh), st = kc % NR;
-        const bool want = lane < ncopy && key < a.P;
+      auto fetch = [&](int c) { return wanted(c) ? __ldg(ids + (key_of(c) >> a.bs_shift)) : 0; };
+      int next = fetch(p.c0);
+      for (int c = p.c0; c < p.c1; c += kAhead) {
+        const int id = next, key = key_of(c);
+        next = fetch(c + kAhead);
+        const bool here = sub < kAhead && c + sub < p.c1, want = wanted(c);
         const bool take = want && static_cast<unsigned int>(id) < static_cast<unsigned int>(a.num_blocks);
         if (want && !take) report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x552);
-        const unsigned int got = __ballot_sync(0xffffffffu, take);
-        if (!mbar_wait_warp(raw_free + st, ((kc / NR) & 1) ^ 1, a.err, 0x561)) {
+        const unsigned int got = (__ballot_sync(0xffffffffu, take) >> (lane & 28)) & 0xfu;
+        const uint32_t k = kc + sub, st = k % NR;
+        if (!__all_sync(0xffffffffu,
+                        !here || mbar_wait(raw_free + st, ((k / NR) & 1) ^ 1, a.err, 0x561))) {
           ok = false;
           break;
         }
-        if (lane == 0) {
+        if (here && cp == 0) {
           unsigned int bits = 0u;
-          for (int i = 0; i < ncopy; ++i)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
             if ((got >> i) & 1u) bits |= groups << (i << (copy_sh - 4));
           raw_valid[st] = static_cast<int>(bits);
           mbar_arrive_expect_tx(raw_full + st, __popc(got) * copy_bytes);
         }
         __syncwarp();
         if (take)
-          bulk_load(sm + SM::RAW0 + st * SM::RAW + lane * copy_bytes,
+          bulk_load(sm + SM::RAW0 + st * SM::RAW + cp * copy_bytes,
                     head + static_cast<uint64_t>(id) * block_bytes +
                         static_cast<uint32_t>((key >> 4) & gmask) * qgroup_bytes(D),
                     copy_bytes, raw_full + st);
+        kc += min(kAhead, p.c1 - c);
       }
     }
     // leave no copy in flight
@@ -300,9 +301,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
   } else if (warp < kLoadWarp) {
     // --------------------------------------------------------- tensor cores
     constexpr uint32_t idq = idesc_f16_f32(128, kPfxKeys, 0), idv = idesc_f16_f32(128, D, 1);
-    const int s = warp - kMmaWarp;
+    const int s = static_cast<int>(warp_uniform(static_cast<uint32_t>(warp - kMmaWarp)));
     const uint32_t kv0 = smem_u32(sm);
-    const uint64_t qd = kq_desc(smem_u32(sm + SM::QS) + s * SM::Q_TILE);
+    const uint64_t qd = warp_uniform(kq_desc(smem_u32(sm + SM::QS) + s * SM::Q_TILE));
     const uint32_t tS = tmem + SM::S0 + 64 * s, tP = tmem + SM::P0 + SM::P_STEP * s;
     const uint32_t tO = tmem + SM::O0 + SM::O_COLS * s;
     uint32_t kc = 0, done = 0, n_part = 0;   // chunks of the CTA, of the stream; parts
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
         const uint32_t k = kc + p.local(s, t), st = k % NST;
         if (!mbar_wait_warp(kv_ready + st, (k / NST) & 1, a.err, 0x571)) return false;
         tc_fence_after();
-        const uint64_t kd = kq_desc(kv0 + st * SM::STAGE);
+        const uint64_t kd = warp_uniform(kq_desc(kv0 + st * SM::STAGE));
 #pragma unroll
         for (int term = 0; term < TERMS; ++term) {
           const uint32_t tQ = tmem + SM::Q_COLS * (TERMS == 2 ? term : s);
@@ -337,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
         const uint32_t k = kc + p.local(s, t), st = k % NST;
         if (!mbar_wait_warp(p_full + s, (done + t) & 1, a.err, 0x572)) return false;
         tc_fence_after();
-        const uint64_t vd = v_desc(kv0 + st * SM::STAGE + SM::TILE);
+        const uint64_t vd = warp_uniform(v_desc(kv0 + st * SM::STAGE + SM::TILE));
 #pragma unroll
         for (int term = 0; term < TERMS; ++term)
 #pragma unroll
