@@ -50,8 +50,10 @@ struct QPrefixArgs {
   const int32_t* table;       // [B,max_blocks]
   const int32_t* lens;        // [B]
   float* part;                // pieces
-  float4* o;                  // [B * Hq][d / 4], [B * Hq]: the pieces joined, rows
-  float2* ml;                 // (sequence * Hkv + KV head) * G + slot
+  const float4* own_o;        // the sequences' own parts (QDecodeArgs::state_o, state_ml)
+  const float2* own_ml;
+  void* out;                  // [B,Hq,d], q's type
+  float v_scale;
   unsigned int* err;
   int B, Hq, Hkv, G, N, P;    // P: tokens of the prefix, > 0
   int bs_shift, num_blocks, max_blocks;
@@ -86,10 +88,11 @@ struct QDecodeArgs {
   const int32_t* plan_count;  // [B*Hkv][chunks]
   int plan_chunks, topk;
   int S;                      // splits per (sequence, KV head) of the reuse kernel
-  // dense over a shared prefix: its state (QPrefixArgs), which is joined into the outputs
-  // of sequences with at least P tokens, whose own part starts there (0: no prefix)
-  const float4* pfx_o;
-  const float2* pfx_ml;
+  // dense behind a shared prefix of P tokens (0: none): a sequence with at least as many
+  // starts there, and instead of an output every row, numbered (sequence * Hkv + KV head)
+  // * G + slot, leaves its state: sums of weight * value [d / 4], and (reference, sum)
+  float4* state_o;
+  float2* state_ml;
   int P;
   int16_t heads[kMaxQHeads];  // heads[g*G + slot]
 };

@@ -551,8 +551,8 @@ kascade_status kascade_qcache_prefix_decode(const kascade_desc* desc, const kasc
   QDecodeArgs a;
   fill_qargs(a, k, q, pages, block_table, kv_lens, out, ws);
   a.P = prefix_len;
-  a.pfx_o = at<float4>(ws, k.L.prefix_o);
-  a.pfx_ml = at<float2>(ws, k.L.prefix_ml);
+  a.state_o = at<float4>(ws, k.L.prefix_o);
+  a.state_ml = at<float2>(ws, k.L.prefix_ml);
   QPrefixArgs x;
   memset(&x, 0, sizeof(x));
   x.q = q;
@@ -560,8 +560,10 @@ kascade_status kascade_qcache_prefix_decode(const kascade_desc* desc, const kasc
   x.table = block_table;
   x.lens = kv_lens;
   x.part = at<float>(ws, k.L.prefix);
-  x.o = at<float4>(ws, k.L.prefix_o);
-  x.ml = at<float2>(ws, k.L.prefix_ml);
+  x.own_o = a.state_o;
+  x.own_ml = a.state_ml;
+  x.out = out;
+  x.v_scale = a.v_scale;
   x.err = a.err;
   x.B = a.B;
   x.Hq = a.Hq;
@@ -575,8 +577,9 @@ kascade_status kascade_qcache_prefix_decode(const kascade_desc* desc, const kasc
   x.scale = a.scale;
   x.geo = prefix_geo(k.s.B, k.s.G, k.s.Hkv, prefix_len, k.s.dtype, sm_count());
   memcpy(x.heads, a.heads, sizeof(x.heads));
-  if ((r = status_of(launch_qprefix(x, k.s.d, k.s.dtype, st))) != KASCADE_OK) return r;
-  return status_of(launch_qdecode_dense(a, k.s.d, k.s.dtype, st));
+  // the own parts' states, then the prefix's pieces, then both joined
+  if ((r = status_of(launch_qdecode_dense(a, k.s.d, k.s.dtype, st))) != KASCADE_OK) return r;
+  return status_of(launch_qprefix(x, k.s.d, k.s.dtype, st));
 }
 
 kascade_status kascade_qcache_anchor_decode(const kascade_desc* desc, const kascade_qcache* cache,

@@ -434,23 +434,17 @@ __device__ __forceinline__ int start_of(const QDecodeArgs& a, int b) {
   return PREFIX ? pfx_start(a.lens, b, a.P, a.N, a.max_blocks, a.bs_shift) : 0;
 }
 
-// x and the prefix's state of the same output (b, g, head slot h, dims 4 e4 ..).
-template <int D>
-__device__ __forceinline__ Joined join_prefix(const QDecodeArgs& a, Joined x, int b, int g, int h,
-                                              int e4) {
-  if (start_of<true>(a, b) == 0) return x;
-  const size_t row = (static_cast<size_t>(b) * a.Hkv + g) * a.G + h;
-  const float2 ml = __ldcg(a.pfx_ml + row);
-  const Joined y[1] = {{ml.x, ml.y, __ldcg(a.pfx_o + row * (D / 4) + e4)}};
-  join_into(x, y);
-  return x;
-}
-
-// The output (b, g, head slot h, dims 4 e4 ..) of a joined whole.
+// The output (b, g, head slot h, dims 4 e4 ..) of a joined whole; behind a shared
+// prefix its state.
 template <int D, bool F32, bool PREFIX = false>
-__device__ __forceinline__ void joined_output(const QDecodeArgs& a, Joined x, int b, int g, int h,
-                                              int e4) {
-  if (PREFIX) x = join_prefix<D>(a, x, b, g, h, e4);
+__device__ __forceinline__ void joined_output(const QDecodeArgs& a, const Joined& x, int b, int g,
+                                              int h, int e4) {
+  if (PREFIX) {
+    const size_t at = (static_cast<size_t>(b) * a.Hkv + g) * a.G + h;
+    a.state_o[at * (D / 4) + e4] = x.o;
+    if (e4 == 0) a.state_ml[at] = make_float2(x.m, x.l);
+    return;
+  }
   const size_t row = static_cast<size_t>(b) * a.Hq + a.heads[g * a.G + h];
   const float inv = x.l == 0.f ? 0.f : a.v_scale / x.l;   // 0: no key at all
   out_store4<F32>(a, row * D + 4 * e4,
@@ -939,7 +933,7 @@ __global__ void __launch_bounds__(kNW * 32, kDenseCtasPerSm)
   // sequences without keys: zeros; scores behind the last key
   for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
     if (pref[b + 1] != pref[b]) continue;
-    if (PREFIX && start_of<PREFIX>(a, b) > 0) {   // the prefix alone
+    if (PREFIX) {
       for (int e = tid; e < a.Hq * (D / 4); e += kNW * 32)
         joined_output<D, F32, true>(a, {kNoKey, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)}, b,
                                     e / elems, e % elems / (D / 4), e & (D / 4 - 1));

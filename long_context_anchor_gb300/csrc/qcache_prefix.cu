@@ -62,32 +62,33 @@ __device__ __forceinline__ void fewer_regs() {
 
 template <int D, int TERMS>
 struct Shapes {
-  // TMEM columns, 512 in all: Q (the first 64 dims of each tile, fp16 pairs; the
-  // other 64 are in shared memory; fp32: both terms of the one tile whole), S of
-  // each stream, its weights P, its O. fp32 with d = 128 has no room for P beside S:
-  // it lies over it, and the next scores wait for the product.
-  static constexpr bool OVER = D == 128 && TERMS == 2;
-  static constexpr bool QSMEM = D == 128 && TERMS == 1;
-  static constexpr int Q_COLS = TERMS == 2 ? D / 2 : 32;      // of a tile, or of a term
-  static constexpr int P_COLS = 32 * TERMS;
-  static constexpr int S0 = 2 * Q_COLS, P0 = OVER ? S0 : S0 + 128;
-  static constexpr int O_COLS = D, O0 = OVER ? S0 + 128 : P0 + 2 * P_COLS;
-  static constexpr int P_STEP = OVER ? 64 : P_COLS;
+  // TMEM columns, 512 in all: O of each stream, two buffers of scores for each (a
+  // chunk's weights, both terms for fp32, lie over its scores: the next chunk's scores
+  // go into the other buffer meanwhile), and at d = 64 Q (fp16 pairs; a tile per
+  // stream, or the two terms of one tile). At d = 128 Q is in shared memory.
+  static constexpr bool QSMEM = D == 128;
+  static constexpr int Q_COLS = QSMEM ? 0 : 32;
+  static constexpr int S0 = 2 * Q_COLS, O0 = S0 + 256, O_COLS = D;
   static_assert(O0 + 2 * O_COLS <= 512, "TMEM columns");
 
   static constexpr int HALF = kPfxKeys * 128;           // 64 dims of a chunk's K or V in fp16
   static constexpr int TILE = HALF * (D / 64);          // a chunk's K, or its V
-  static constexpr int STAGE = 2 * TILE;
-  static constexpr int NST = D == 128 ? 4 : 8;          // fp16 chunks
+  // Rings: K in fp16 (a stage is free once its scores are in), V in fp16, chunks as
+  // stored. A stage is always the same team's and, where each stream has its own
+  // chunks, the same stream's: who waits for a phase of its barriers has seen the
+  // phase before.
+  static constexpr int KST = D == 128 ? 2 : 8, VST = D == 128 ? 4 : 8, NR = D == 128 ? 6 : 12;
+  static constexpr int kTeams = kDeqWarps / kTeamWarps<D>;
+  static_assert(KST % kTeams == 0 && VST % kTeams == 0 && NR % kTeams == 0 && kTeams % 2 == 0,
+                "stages belong to one team and one stream");
   static constexpr int RAW = (kPfxKeys / kQGroup) * qgroup_bytes(D);
-  static constexpr int NR = D == 128 ? 7 : 12;          // chunks as stored
-  static constexpr int Q_TILE = QSMEM ? kPfxRows * 128 : 0;   // a stream's dims 64 .. 127
-  static constexpr int QS = NST * STAGE;
+  static constexpr int Q_HALF = kPfxRows * 128, Q_TILE = QSMEM ? 2 * Q_HALF : 0;
+  static constexpr int V0 = KST * TILE, QS = V0 + VST * TILE;
   static constexpr int RAW0 = QS + 2 * Q_TILE;
   static constexpr int BAR = RAW0 + NR * RAW;
-  static constexpr int NBAR = 2 * NR + 2 * NST + 10;
-  static constexpr int VALID = BAR + NBAR * 8;          // int [NR + NST]: bit per 16 keys
-  static constexpr int TMEM = VALID + (NR + NST) * 4;
+  static constexpr int NBAR = 2 * NR + KST + 2 * VST + 14;
+  static constexpr int VALID = BAR + NBAR * 8;          // int [NR + VST]: bit per 16 keys
+  static constexpr int TMEM = VALID + (NR + VST) * 4;
   static constexpr int BYTES = TMEM + 8;
   static constexpr size_t SMEM = BYTES + 1024;          // slack for 1024-byte alignment
   static_assert(SMEM <= 232448 - 64, "fits in shared memory");
@@ -102,6 +103,9 @@ __device__ __forceinline__ uint64_t v_desc(uint32_t tile) {
 __device__ __forceinline__ constexpr uint64_t k_step(int kk) {
   return static_cast<uint64_t>(((kk >> 2) * (kPfxKeys * 128) + (kk & 3) * 32) >> 4);
 }
+__device__ __forceinline__ constexpr uint64_t q_step(int kk) {
+  return static_cast<uint64_t>(((kk >> 2) * (kPfxRows * 128) + (kk & 3) * 32) >> 4);
+}
 __device__ __forceinline__ constexpr uint64_t v_step(int kk) {
   return static_cast<uint64_t>((kk * 2048) >> 4);
 }
@@ -114,12 +118,14 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn_majo
 // What a CTA does of one unit: chunks c0 .. c1 - 1 for one or two row tiles.
 struct Part {
   int unit, g, tile0, tiles, c0, c1, next;
-  __device__ __forceinline__ int chunks(int stream) const {   // of one stream
-    return tiles == 2 ? c1 - c0 : (c1 - c0 - stream + 1) / 2;
+  // kc: the CTA's chunks before this part. With one tile stream s has those whose
+  // running number in the CTA is even (s = 0) or odd.
+  __device__ __forceinline__ int chunks(int stream, uint32_t kc) const {   // of one stream
+    return tiles == 2 ? c1 - c0 : (c1 - c0 - static_cast<int>((stream ^ kc) & 1) + 1) / 2;
   }
-  // local number of a stream's t-th chunk
-  __device__ __forceinline__ int local(int stream, int t) const {
-    return tiles == 2 ? t : 2 * t + stream;
+  // running number of a stream's t-th chunk
+  __device__ __forceinline__ uint32_t chunk(int stream, int t, uint32_t kc) const {
+    return kc + (tiles == 2 ? t : 2 * t + ((stream ^ kc) & 1));
   }
 };
 __device__ __forceinline__ Part part_at(const QPrefixGeo& geo, int Hkv, int f, int end) {
@@ -193,8 +199,11 @@ __device__ __forceinline__ void first_holder(const QPrefixArgs& a, int& src) {
 template <int D, int TERMS>
 __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__ QPrefixArgs a) {
   using SM = Shapes<D, TERMS>;
-  constexpr int NST = SM::NST, NR = SM::NR;
-  pdl_wait();
+  constexpr int KST = SM::KST, VST = SM::VST, NR = SM::NR;
+  // The kernel before this one is the own parts' (launch_qdecode_dense), of which
+  // nothing is used here: a CTA starts where one of its CTAs has ended. All of those
+  // had waited for what came before them by then; the end of the kernel is waited
+  // for at this one's end, for the sake of the kernel behind it.
   pdl_trigger();
   extern __shared__ unsigned char smem_raw[];
   __shared__ int s_src;
@@ -204,30 +213,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + SM::BAR);
   uint64_t* raw_full = bars;            // [NR] a chunk's copies have landed
   uint64_t* raw_free = bars + NR;       // [NR] ... and were read
-  uint64_t* kv_ready = bars + 2 * NR;   // [NST] fp16 K and V written
-  uint64_t* kv_free = kv_ready + NST;   // [NST] ... and used
-  uint64_t* q_ready = kv_free + NST;    // [2] by stream: Q written
-  uint64_t* s_full = q_ready + 2;       // [2] scores of the stream's chunk
-  uint64_t* s_free = q_ready + 4;       // [2] ... read
-  uint64_t* p_full = q_ready + 6;       // [2] its weights written
-  uint64_t* pv_done = q_ready + 8;      // [2] their product with V
+  uint64_t* k_free = bars + 2 * NR;     // [KST] a chunk's K was used by both streams
+  uint64_t* kv_ready = k_free + KST;    // [VST] fp16 K and V written
+  uint64_t* v_free = kv_ready + VST;    // [VST] V was used by both streams
+  uint64_t* q_ready = v_free + VST;         // [2] by stream: Q written
+  // by stream and buffer (2 * stream + buffer):
+  uint64_t* s_full = q_ready + 2;       // [4] scores of a chunk
+  uint64_t* p_full = q_ready + 6;       // [4] its weights written
+  uint64_t* pv_done = q_ready + 10;     // [4] their product with V
   int* raw_valid = reinterpret_cast<int*>(sm + SM::VALID);
   int* kv_valid = raw_valid + NR;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + SM::TMEM);
 
   if (tid == 0) s_src = a.B;
   if (tid < SM::NBAR) {
-    const int i = tid, j = i - 2 * NR, k = j - 2 * NST;   // k: pairs from q_ready on
+    const int i = tid, j = i - 2 * NR, k = j - KST - 2 * VST;   // k: pairs from q_ready on
     const int count = i < NR ? 1 : i < 2 * NR ? kTeamWarps<D>
-                      : j < NST ? kTeamWarps<D> : j < 2 * NST ? 2   // both streams, or one twice
-                      : k < 2 ? 128 : k < 4 ? 1 : k < 8 ? 128 : 1;
+                      : j < KST ? 2   // both streams, or one twice
+                      : j < KST + VST ? kTeamWarps<D> : j < KST + 2 * VST ? 2
+                      : k < 2 ? 128 : k < 6 ? 1 : k < 10 ? 128 : 1;
     mbar_init(bars + i, count);
     fence_barrier_init();
   }
   __syncthreads();
   first_holder(a, s_src);
   const int src = s_src;
-  if (src >= a.B) return;   // nobody has it: no piece is read either
+  if (src >= a.B) {   // nobody has it: no piece is read either
+    if (tid == 0) pdl_wait();
+    return;
+  }
   if (warp == kMmaWarp) tmem_alloc(s_tmem, 512);   // one CTA per SM
   tc_fence_before();
   __syncthreads();
@@ -303,64 +317,66 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
     constexpr uint32_t idq = idesc_f16_f32(128, kPfxKeys, 0), idv = idesc_f16_f32(128, D, 1);
     const int s = static_cast<int>(warp_uniform(static_cast<uint32_t>(warp - kMmaWarp)));
     const uint32_t kv0 = smem_u32(sm);
-    const uint64_t qd = warp_uniform(kq_desc(smem_u32(sm + SM::QS) + s * SM::Q_TILE));
-    const uint32_t tS = tmem + SM::S0 + 64 * s, tP = tmem + SM::P0 + SM::P_STEP * s;
-    const uint32_t tO = tmem + SM::O0 + SM::O_COLS * s;
+    const uint32_t q0 = smem_u32(sm + SM::QS);
+    const uint32_t tS0 = tmem + SM::S0 + 128 * s, tO = tmem + SM::O0 + SM::O_COLS * s;
     uint32_t kc = 0, done = 0, n_part = 0;   // chunks of the CTA, of the stream; parts
     bool ok = true;
     for (int f = w0; ok && f < w1; ++n_part) {
       const Part p = part_at(a.geo, a.Hkv, f, w1);
       f = p.next;
-      const int n = p.chunks(s);
-      // S = Q K^T of the t-th chunk
+      const int n = p.chunks(s, kc);
+      // S = Q K^T of the t-th chunk, the stream's (done + t)-th
       auto issue_s = [&](int t) {
-        const uint32_t k = kc + p.local(s, t), st = k % NST;
-        if (!mbar_wait_warp(kv_ready + st, (k / NST) & 1, a.err, 0x571)) return false;
+        const uint32_t k = p.chunk(s, t, kc), st = k % VST, ks = k % KST, buf = (done + t) & 1;
+        if (!mbar_wait_warp(kv_ready + st, (k / VST) & 1, a.err, 0x571)) return false;
         tc_fence_after();
-        const uint64_t kd = warp_uniform(kq_desc(kv0 + st * SM::STAGE));
+        const uint64_t kd = warp_uniform(kq_desc(kv0 + ks * SM::TILE));
+        const uint32_t tS = tS0 + 64 * buf;
 #pragma unroll
         for (int term = 0; term < TERMS; ++term) {
-          const uint32_t tQ = tmem + SM::Q_COLS * (TERMS == 2 ? term : s);
+          const int tile = TERMS == 2 ? term : s;
+          const uint64_t qd = warp_uniform(kq_desc(q0 + tile * SM::Q_TILE));
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t acc = term > 0 || kk > 0 ? 1u : 0u;
-            if (SM::QSMEM && kk >= 4)
-              tc_mma(tS, qd + k_step(kk & 3), kd + k_step(kk), idq, acc);
+            if (SM::QSMEM)
+              tc_mma(tS, qd + q_step(kk), kd + k_step(kk), idq, acc);
             else
-              tc_mma_ts(tS, tQ + kk * 8, kd + k_step(kk), idq, acc);
+              tc_mma_ts(tS, tmem + SM::Q_COLS * tile + kk * 8, kd + k_step(kk), idq, acc);
           }
         }
-        tc_commit(s_full + s);
+        tc_commit(s_full + 2 * s + buf);
+        tc_commit(k_free + ks);
+        if (p.tiles == 1) tc_commit(k_free + ks);   // for the stream that does not use it
         return true;
       };
       // O += P V; the part's first product overwrites O
       auto issue_pv = [&](int t) {
-        const uint32_t k = kc + p.local(s, t), st = k % NST;
-        if (!mbar_wait_warp(p_full + s, (done + t) & 1, a.err, 0x572)) return false;
+        const uint32_t st = p.chunk(s, t, kc) % VST, buf = (done + t) & 1;
+        if (!mbar_wait_warp(p_full + 2 * s + buf, ((done + t) >> 1) & 1, a.err, 0x572)) return false;
         tc_fence_after();
-        const uint64_t vd = warp_uniform(v_desc(kv0 + st * SM::STAGE + SM::TILE));
+        const uint64_t vd = warp_uniform(v_desc(kv0 + SM::V0 + st * SM::TILE));
+        const uint32_t tP = tS0 + 64 * buf;
 #pragma unroll
         for (int term = 0; term < TERMS; ++term)
 #pragma unroll
           for (int kk = 0; kk < kPfxKeys / 16; ++kk)
             tc_mma_ts(tO, tP + 32 * term + kk * 8, vd + v_step(kk), idv,
                       t > 0 || term > 0 || kk > 0 ? 1u : 0u);
-        tc_commit(pv_done + s);
-        tc_commit(kv_free + st);
-        if (p.tiles == 1) tc_commit(kv_free + st);   // for the stream that does not use it
+        tc_commit(pv_done + 2 * s + buf);
+        tc_commit(v_free + st);
+        if (p.tiles == 1) tc_commit(v_free + st);
         return true;
       };
       ok = mbar_wait_warp(q_ready + s, n_part & 1, a.err, 0x573);
       if (TERMS == 2 && ok) ok = mbar_wait_warp(q_ready + 1 - s, n_part & 1, a.err, 0x573);
       tc_fence_after();
-      if (ok && n > 0) ok = issue_s(0);
+      for (int t = 0; ok && t < n && t < 2; ++t) ok = issue_s(t);
       for (int t = 0; ok && t < n; ++t) {
-        // the next scores once these are read (or, over the weights, once those are used)
-        if (!SM::OVER && t + 1 < n)
-          ok = mbar_wait_warp(s_free + s, (done + t) & 1, a.err, 0x574) && issue_s(t + 1);
-        if (ok) ok = issue_pv(t);
-        if (SM::OVER && ok && t + 1 < n)
-          ok = mbar_wait_warp(pv_done + s, (done + t) & 1, a.err, 0x575) && issue_s(t + 1);
+        ok = issue_pv(t);
+        if (ok && t + 2 < n)   // over this chunk's weights
+          ok = mbar_wait_warp(pv_done + 2 * s + ((done + t) & 1), ((done + t) >> 1) & 1, a.err,
+                              0x574) && issue_s(t + 2);
       }
       kc += p.c1 - p.c0;
       done += n;
@@ -369,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
   } else if (warp >= 8) {
     fewer_regs<kDeqRegs>();
     // ------------------------------------------------------- codes to fp16
-    constexpr int kTeam = kTeamWarps<D>, kTeams = kDeqWarps / kTeam, kParts = D / 32;
+    constexpr int kTeam = kTeamWarps<D>, kTeams = SM::kTeams, kParts = D / 32;
     constexpr int kRows = 32 * kTeam / kParts;   // rows of K (and V) at a time
     const int team = (warp - 8) / kTeam, t = tid - 256 - team * 32 * kTeam;
     const int row0 = t / kParts, part = t % kParts;
@@ -381,19 +397,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
       const uint32_t end = kc + p.c1 - p.c0;
       // the team's first chunk from here on
       for (uint32_t k = kc + (team + kTeams - kc % kTeams) % kTeams; k < end; k += kTeams) {
-        const int rs = k % NR, st = k % NST;
+        const int rs = k % NR, st = k % VST, ks = k % KST;
         ok = mbar_wait_warp(raw_full + rs, (k / NR) & 1, a.err, 0x581) &&
-             mbar_wait_warp(kv_free + st, ((k / NST) & 1) ^ 1, a.err, 0x582);
+             mbar_wait_warp(k_free + ks, ((k / KST) & 1) ^ 1, a.err, 0x582) &&
+             mbar_wait_warp(v_free + st, ((k / VST) & 1) ^ 1, a.err, 0x583);
         if (!ok) break;
         const int bits = raw_valid[rs];
         const uint8_t* raw = sm + SM::RAW0 + rs * SM::RAW;
-        const uint32_t tile = smem_u32(sm) + st * SM::STAGE;
+        const uint32_t k_tile = smem_u32(sm) + ks * SM::TILE;
+        const uint32_t v_tile = smem_u32(sm) + SM::V0 + st * SM::TILE;
 #pragma unroll
         for (int row = row0; row < kPfxKeys; row += kRows) {
           const uint8_t* grp = raw + (row >> 4) * qgroup_bytes(D);
           const bool valid = (bits >> (row >> 4)) & 1;
-          widen<D>(grp, 0, 8 * D, tile, row, part, valid);
-          widen<D>(grp, 9 * D, 17 * D, tile + SM::TILE, row, part, valid);
+          widen<D>(grp, 0, 8 * D, k_tile, row, part, valid);
+          widen<D>(grp, 9 * D, 17 * D, v_tile, row, part, valid);
         }
         if (t == 0) kv_valid[st] = bits;
         fence_proxy_async_smem();
@@ -410,8 +428,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
     // ------------------------------------------------------------- softmax
     const int s = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tQ = tmem + SM::Q_COLS * s + lane_base, tS = tmem + SM::S0 + 64 * s + lane_base;
-    const uint32_t tP = tmem + SM::P0 + SM::P_STEP * s + lane_base;
+    const uint32_t tQ = tmem + SM::Q_COLS * s + lane_base;
+    const uint32_t tS0 = tmem + SM::S0 + 128 * s + lane_base;
     const uint32_t tO = tmem + SM::O0 + SM::O_COLS * s + lane_base;
     const uint32_t sQ = smem_u32(sm + SM::QS) + s * SM::Q_TILE;
     uint32_t kc = 0, done = 0;
@@ -480,11 +498,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
                                              __uint_as_float(v[j] & 0xffff0000u) * up);
           }
         }
-        if (SM::QSMEM && h == 1) {
+        if (SM::QSMEM) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
-                             sQ + sw128_offset(kPfxRows, r, i)),
+                             sQ + sw128_offset(kPfxRows, r, 8 * h + i)),
                          "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
                          : "memory");
         } else {
@@ -492,18 +510,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
         }
       }
       if (SM::QSMEM) fence_proxy_async_smem();
-      tmem_wait_st();
+      else tmem_wait_st();
       tc_fence_before();
       mbar_arrive(q_ready + s);
       // ---- its chunks
-      float ref = kNoKey, l = 0.f;   // the reference, as a raw product
-      float c = 0.f;                 // weights are 2^(product * ml + c)
-      bool careful = true;           // see raise()
-      const int n = p.chunks(s);
+      // weights are 2^((product - ref) * ml + kShiftHere): the reference is a raw product,
+      // so a huge score's distance from it is exact
+      float ref = kNoKey, l = 0.f;
+      const int n = p.chunks(s, kc);
+      const uint64_t ml2 = f2_pack(ml, ml), shift2 = f2_pack(kShiftHere, kShiftHere);
       for (int t = 0; ok && t < n; ++t) {
-        const uint32_t k = kc + p.local(s, t), st = k % NST, ph = (done + t) & 1;
-        // (kv_valid was written before kv_ready, which the scores' MMAs waited for)
-        ok = mbar_wait_warp(s_full + s, ph, a.err, 0x591);
+        const uint32_t st = p.chunk(s, t, kc) % VST, g = done + t, buf = g & 1;
+        const uint32_t tS = tS0 + 64 * buf;
+        ok = mbar_wait_warp(s_full + 2 * s + buf, (g >> 1) & 1, a.err, 0x591);
         if (!ok) break;
         tc_fence_after();
         if (!idle) {
@@ -515,12 +534,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
 #pragma unroll
             for (int i = 0; i < 32; ++i) x[32 * cc + i] = __uint_as_float(v[i]);
           }
-          const int bits = kv_valid[st];
+          const int bits = kv_valid[st];   // (written before kv_ready, which the MMAs waited for)
           tmem_wait_ld();
-          if (!SM::OVER) {
-            tc_fence_before();
-            mbar_arrive(s_free + s);
-          }
           if (bits != 0xf) {
 #pragma unroll
             for (int i = 0; i < 64; ++i)
@@ -536,40 +551,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
             const bool moved = __any_sync(0xffffffffu, up_to > ref);
             ref = up_to;
             l *= al;
-            if (moved && t > 0) {
-              ok = ok && mbar_wait_warp(pv_done + s, ph ^ 1, a.err, 0x593);   // O is still
-              if (!ok) return;
-              tc_fence_after();
+            if (!moved || t == 0) return;
+            const uint32_t before = g - 1;   // O is still once its product is in
+            ok = mbar_wait_warp(pv_done + 2 * s + (before & 1), (before >> 1) & 1, a.err, 0x593);
+            if (!ok) return;
+            tc_fence_after();
 #pragma unroll 1
-              for (int cc = 0; cc < D; cc += 16) {   // few at a time: the scores are held
-                uint32_t o[16];
-                tmem_ld16(tO + cc, o);
-                tmem_wait_ld();
+            for (int cc = 0; cc < D; cc += 16) {   // few at a time: the scores are held
+              uint32_t o[16];
+              tmem_ld16(tO + cc, o);
+              tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-                tmem_st16(tO + cc, o);
-              }
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+              tmem_st16(tO + cc, o);
             }
-            // c's rounding is common to the row's weights; where it would be felt (or would
-            // overflow them) products are taken relative to the reference first
-            c = fmaf(-ref, ml, kShiftHere);
-            careful = __any_sync(0xffffffffu, !(fabsf(c) < 1024.f));
           };
           // A chunk's weights are taken with the reference as it is; only where their
           // sum shows that one may have passed fp16 the products are searched for their
           // maximum, and the weights taken again.
-          bool again = false;
-          if (t == 0 || careful) raise();
-          else again = true;
+          if (t == 0) raise();
           float sum;
-          while (true) {
-            float base = c;
-            if (careful) {
-              base = kShiftHere;
-#pragma unroll
-              for (int i = 0; i < 64; ++i) x[i] -= ref;
-            }
-            const uint64_t ml2 = f2_pack(ml, ml), c2 = f2_pack(base, base);
+          for (bool again = t > 0;; again = false) {
+            const uint64_t minus = f2_pack(-ref, -ref);
             uint64_t part_sum[2] = {0ull, 0ull};
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
@@ -578,43 +581,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
               for (int i = 0; i < 16; ++i) {
                 const int at = 32 * half + 2 * i;
                 float p0, p1;
-                f2_unpack(f2_fma(f2_pack(x[at], x[at + 1]), ml2, c2), p0, p1);
+                f2_unpack(f2_fma(f2_add(f2_pack(x[at], x[at + 1]), minus), ml2, shift2), p0, p1);
                 p0 = ex2(p0);
                 p1 = ex2(p1);
                 part_sum[i & 1] = f2_add(part_sum[i & 1], f2_pack(p0, p1));
                 hi[i] = pack_f16(p0, p1);
                 if (TERMS == 2) lo[i] = pack_f16(p0 - f16_rounded(p0), p1 - f16_rounded(p1));
               }
-              if (half == 0 && !SM::OVER && t > 0) {   // the previous weights are used
-                ok = ok && mbar_wait_warp(pv_done + s, ph ^ 1, a.err, 0x595);
-                tc_fence_after();
-              }
-              tmem_st16(tP + 16 * half, hi);
-              if (TERMS == 2) tmem_st16(tP + 32 + 16 * half, lo);
+              tmem_st16(tS + 16 * half, hi);
+              if (TERMS == 2) tmem_st16(tS + 32 + 16 * half, lo);
             }
             float s0, s1;
             f2_unpack(f2_add(part_sum[0], part_sum[1]), s0, s1);
             sum = s0 + s1;
             tmem_wait_st();
             if (!again || !__any_sync(0xffffffffu, !(sum < 65000.f))) break;
-            again = false;
             raise();
+            if (!ok) break;
           }
           if (!ok) break;
           l += sum;
-        } else if (!SM::OVER) {
-          mbar_arrive(s_free + s);
-          // no arrival for these weights before the last ones' phase is over
-          if (t > 0 && !mbar_wait_warp(pv_done + s, ph ^ 1, a.err, 0x596)) {
-            ok = false;
-            break;
-          }
         }
         tc_fence_before();
-        mbar_arrive(p_full + s);
+        mbar_arrive(p_full + 2 * s + buf);
       }
       // ---- the piece
-      if (ok && n > 0) ok = mbar_wait_warp(pv_done + s, (done + n - 1) & 1, a.err, 0x594);
+      if (ok && n > 0) {
+        const uint32_t g = done + n - 1;
+        ok = mbar_wait_warp(pv_done + 2 * s + (g & 1), (g >> 1) & 1, a.err, 0x594);
+      }
       kc += p.c1 - p.c0;
       done += n;
       tc_fence_after();
@@ -636,13 +631,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
         }
         if (live) {
           // (as the reference of weights held as 2^14 p)
-          piece[kPfxRows * D + r] = ref == kNoKey ? kNoKey : (careful ? ref * ml + (kPShift - kShiftHere) : kPShift - c);
+          piece[kPfxRows * D + r] = ref == kNoKey ? kNoKey : ref * ml + (kPShift - kShiftHere);
           piece[kPfxRows * (D + 1) + r] = l;
         }
       }
       tc_fence_before();
     }
   }
+  if (warp == kLoadWarp) pdl_wait();
   tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -651,28 +647,50 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
   }
 }
 
-// The pieces of every row joined: D / 4 threads per row and worker, `workers` of them per
-// row, which take its pieces in turn and are joined in order.
+// Every row's pieces and its own part's state joined into the output: D / 4 threads
+// per row and worker, `workers` of them per row, which take the row's pieces in turn
+// and are joined in order. The last `checkers` CTAs look for sequences whose tables
+// name other blocks than the lowest one's.
 constexpr int kJoinThreads = 256;
-template <int D>
+template <int D, bool F32>
 __global__ void __launch_bounds__(kJoinThreads) k_qprefix_join(const __grid_constant__ QPrefixArgs a,
-                                                               int workers) {
+                                                               int workers, int checkers) {
   pdl_wait();
   pdl_trigger();
   constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, kBatch = 8;
   __shared__ Joined scratch[kJoinThreads];
   __shared__ int s_src;
+  const int joiners = static_cast<int>(gridDim.x) - checkers;
+  if (static_cast<int>(blockIdx.x) >= joiners) {
+    if (threadIdx.x == 0) s_src = a.B;
+    __syncthreads();
+    first_holder(a, s_src);
+    const int src = s_src, front = a.P >> a.bs_shift;
+    const int32_t* ids = a.table + static_cast<size_t>(src) * a.max_blocks;
+    for (int b = src + 1 + static_cast<int>(blockIdx.x) - joiners; b < a.B; b += checkers) {
+      if (pfx_start(a.lens, b, a.P, a.N, a.max_blocks, a.bs_shift) == 0) continue;
+      bool other = false;
+      for (int j = threadIdx.x; j < front; j += kJoinThreads)
+        other |= a.table[static_cast<size_t>(b) * a.max_blocks + j] != ids[j];
+      if (other) report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x551);
+    }
+    return;
+  }
   const int group = threadIdx.x / kLanes, e4 = threadIdx.x % kLanes;
   const int worker = group % workers;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * (kGroups / workers) + group / workers;
-  const int64_t total = static_cast<int64_t>(a.B) * a.Hq;
+  const bool here = row < static_cast<int64_t>(a.B) * a.Hq;
   const int64_t unit_row = row / a.G;   // sequence * Hkv + KV head
   const int b = static_cast<int>(unit_row / a.Hkv), g = static_cast<int>(unit_row - static_cast<int64_t>(b) * a.Hkv);
-  const bool live = row < total && pfx_start(a.lens, b, a.P, a.N, a.max_blocks, a.bs_shift) > 0;
+  const int slot = static_cast<int>(row - unit_row * a.G);
   Joined x = {kNoKey, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-  if (live) {
+  if (here && worker == 0) {
+    const float2 ml = __ldcg(a.own_ml + row);
+    x = {ml.x, ml.y, __ldcg(a.own_o + row * kLanes + e4)};
+  }
+  if (here && pfx_start(a.lens, b, a.P, a.N, a.max_blocks, a.bs_shift) > 0) {
     const QPrefixGeo& geo = a.geo;
-    const int kv_row = b * a.G + static_cast<int>(row - unit_row * a.G);
+    const int kv_row = b * a.G + slot;
     const int tile = kv_row / kPfxRows, r = kv_row % kPfxRows;
     const bool pair = tile < 2 * geo.pairs;
     int unit, u0, u1;
@@ -706,44 +724,38 @@ __global__ void __launch_bounds__(kJoinThreads) k_qprefix_join(const __grid_cons
       join_into(x, y);
     }
   }
-  if (threadIdx.x == 0) s_src = a.B;
-  scratch[threadIdx.x] = x;
-  __syncthreads();
-  first_holder(a, s_src);
   if (workers > 1) {
-    if (worker == 0 && live)
-      for (int w = 1; w < workers; ++w) {
-        const Joined y[1] = {scratch[threadIdx.x + w * kLanes]};
-        join_into(x, y);
-      }
+    scratch[threadIdx.x] = x;
+    __syncthreads();
+    if (worker > 0) return;
+    for (int w = 1; w < workers; ++w) {
+      const Joined y[1] = {scratch[threadIdx.x + w * kLanes]};
+      join_into(x, y);
+    }
   }
-  // sequences whose tables name other blocks than the lowest one's
-  const int front = a.P >> a.bs_shift;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kJoinThreads + threadIdx.x;
-       i < static_cast<int64_t>(a.B) * front; i += static_cast<int64_t>(gridDim.x) * kJoinThreads) {
-    const int bb = static_cast<int>(i / front), j = static_cast<int>(i - static_cast<int64_t>(bb) * front);
-    if (bb <= s_src || pfx_start(a.lens, bb, a.P, a.N, a.max_blocks, a.bs_shift) == 0) continue;
-    if (a.table[static_cast<size_t>(bb) * a.max_blocks + j] !=
-        a.table[static_cast<size_t>(s_src) * a.max_blocks + j])
-      report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x551);
-  }
-  if (worker == 0 && live) {
-    a.o[row * kLanes + e4] = x.o;
-    if (e4 == 0) a.ml[row] = make_float2(x.m, x.l);
-  }
+  if (!here) return;
+  const float inv = x.l == 0.f ? 0.f : a.v_scale / x.l;   // 0: no key at all
+  const float4 y = make_float4(x.o.x * inv, x.o.y * inv, x.o.z * inv, x.o.w * inv);
+  const size_t at = (static_cast<size_t>(b) * a.Hq + a.heads[g * a.G + slot]) * D + 4 * e4;
+  if (F32)
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = y;
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + at) =
+        make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
 }
 
-template <int D>
+template <int D, bool F32>
 cudaError_t launch_join_t(const QPrefixArgs& a, cudaStream_t st) {
   // pieces of a row at most, eight of them per worker
   const int places = (a.geo.pairs > 0 ? 2 : 1) * a.geo.nch;
   const int ctas = (places + a.geo.per - 1) / a.geo.per + 1;
   const int pieces = a.geo.singles > 0 ? 2 * ctas : ctas;
-  const int workers = pieces > 16 ? 4 : pieces > 8 ? 2 : 1;
+  const int workers = pieces > 32 ? 8 : pieces > 16 ? 4 : pieces > 8 ? 2 : 1;
   const int64_t per_cta = kJoinThreads / (D / 4) / workers;
-  const int64_t grid = (static_cast<int64_t>(a.B) * a.Hq + per_cta - 1) / per_cta;
-  return launch_pdl(k_qprefix_join<D>, dim3(static_cast<unsigned int>(grid)), dim3(kJoinThreads), 0,
-                    st, a, workers);
+  const int64_t joiners = (static_cast<int64_t>(a.B) * a.Hq + per_cta - 1) / per_cta;
+  const int checkers = a.B < 64 ? a.B : 64;
+  return launch_pdl(k_qprefix_join<D, F32>, dim3(static_cast<unsigned int>(joiners + checkers)),
+                    dim3(kJoinThreads), 0, st, a, workers, checkers);
 }
 
 template <int D, int TERMS>
@@ -779,7 +791,9 @@ cudaError_t launch_qprefix(const QPrefixArgs& a, int d, int dtype, cudaStream_t 
   else
     e = d == 128 ? launch_prefix_t<128, 1>(a, st) : launch_prefix_t<64, 1>(a, st);
   if (e != cudaSuccess) return e;
-  return d == 128 ? launch_join_t<128>(a, st) : launch_join_t<64>(a, st);
+  if (dtype == KASCADE_F32)
+    return d == 128 ? launch_join_t<128, true>(a, st) : launch_join_t<64, true>(a, st);
+  return d == 128 ? launch_join_t<128, false>(a, st) : launch_join_t<64, false>(a, st);
 }
 
 }  // namespace kascade
