@@ -26,22 +26,23 @@ struct QCacheShape {
   float k_scale, v_scale;     // powers of two
 };
 
-// A shared prefix (qcache_prefix.cu): its keys in chunks, the B * G queries of a KV
-// head in row tiles. All units' places form one line that is cut into runs of
-// `per`, one per CTA: first Hkv * pairs units of two row tiles (two places per
-// chunk), then Hkv * singles units of one (a place per chunk). What CTA c does of
-// unit u it leaves as pieces 2 (u + c) and 2 (u + c) + 1: of the two tiles, or both
-// of the one tile.
+// A shared prefix (qcache_prefix.cu): its keys in nch chunks, the B * G queries of a KV
+// head in row tiles. A unit is two row tiles of a KV head (`pairs` per head) or one
+// (`singles`), cut into runs of pair_len or single_len chunks, one per CTA: first
+// the pairs' CTAs, then the singles'. CTA c leaves pieces 2 c and 2 c + 1: of the two
+// tiles, or both of the one tile.
 constexpr int kPfxKeys = 64, kPfxRows = 128;
-constexpr int kPfxMinRun = 4;             // places per CTA at least
+constexpr int kPfxMinRun = 4;             // chunks of a run at least
 struct QPrefixGeo {
-  int nch, pairs, singles, per, ctas;
+  int nch, pairs, singles, pair_runs, single_runs, pair_len, single_len, ctas;
 };
 QPrefixGeo prefix_geo(int B, int G, int Hkv, int P, int dtype, int sms);
 // A piece: o [rows][d], m [rows], l [rows].
 constexpr size_t pfx_piece_floats(int d) { return static_cast<size_t>(kPfxRows) * (d + 2); }
-inline size_t pfx_pieces(const QPrefixGeo& g, int Hkv) {
-  return 2 * (static_cast<size_t>(Hkv) * (g.pairs + g.singles) + g.ctas);
+// Pieces at most, on a GPU of up to `sms` SMs.
+inline size_t pfx_pieces(const QPrefixGeo& g, int Hkv, int sms) {
+  const size_t units = static_cast<size_t>(Hkv) * (g.pairs + g.singles);
+  return 2 * (units > static_cast<size_t>(sms) ? units : sms);
 }
 
 struct QPrefixArgs {

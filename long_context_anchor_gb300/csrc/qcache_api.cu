@@ -139,7 +139,7 @@ QLayout prefix_layout(const Shape& s, int P) {
   L.prefix = L.total;
   if (P > 0) {
     const QPrefixGeo most = prefix_geo(s.B, s.G, s.Hkv, P, s.dtype, kQMaxCtas);
-    L.prefix_o = align256(L.prefix + pfx_pieces(most, s.Hkv) * pfx_piece_floats(s.d) * sizeof(float));
+    L.prefix_o = align256(L.prefix + pfx_pieces(most, s.Hkv, kQMaxCtas) * pfx_piece_floats(s.d) * sizeof(float));
     L.prefix_ml = align256(L.prefix_o + static_cast<size_t>(s.B) * s.Hq * s.d * sizeof(float));
     L.total = align256(L.prefix_ml + static_cast<size_t>(s.B) * s.Hq * sizeof(float2));
   }

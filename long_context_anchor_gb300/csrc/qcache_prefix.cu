@@ -81,14 +81,18 @@ struct Shapes {
   static constexpr int kTeams = kDeqWarps / kTeamWarps<D>;
   static_assert(KST % kTeams == 0 && VST % kTeams == 0 && NR % kTeams == 0 && kTeams % 2 == 0,
                 "stages belong to one team and one stream");
+  // what the softmax reads of chunk k is written with its K: by then the scores of
+  // chunk k - KST are in, and so the softmax of the chunk 16 before is done
+  static constexpr int kValid = 16;
+  static_assert(KST + 6 <= kValid, "two scores of a stream, every other chunk, behind K's ring");
   static constexpr int RAW = (kPfxKeys / kQGroup) * qgroup_bytes(D);
   static constexpr int Q_HALF = kPfxRows * 128, Q_TILE = QSMEM ? 2 * Q_HALF : 0;
   static constexpr int V0 = KST * TILE, QS = V0 + VST * TILE;
   static constexpr int RAW0 = QS + 2 * Q_TILE;
   static constexpr int BAR = RAW0 + NR * RAW;
-  static constexpr int NBAR = 2 * NR + KST + 2 * VST + 14;
-  static constexpr int VALID = BAR + NBAR * 8;          // int [NR + VST]: bit per 16 keys
-  static constexpr int TMEM = VALID + (NR + VST) * 4;
+  static constexpr int NBAR = 2 * (NR + KST + VST) + 14;
+  static constexpr int VALID = BAR + NBAR * 8;          // int [NR + kValid]: bit per 16 keys
+  static constexpr int TMEM = VALID + (NR + kValid) * 4;
   static constexpr int BYTES = TMEM + 8;
   static constexpr size_t SMEM = BYTES + 1024;          // slack for 1024-byte alignment
   static_assert(SMEM <= 232448 - 64, "fits in shared memory");
@@ -115,42 +119,38 @@ __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, int b_mn_majo
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-// What a CTA does of one unit: chunks c0 .. c1 - 1 for one or two row tiles.
+// What a CTA does: chunks c0 .. c1 - 1 of one unit, for one or two row tiles.
 struct Part {
-  int unit, g, tile0, tiles, c0, c1, next;
-  // kc: the CTA's chunks before this part. With one tile stream s has those whose
-  // running number in the CTA is even (s = 0) or odd.
-  __device__ __forceinline__ int chunks(int stream, uint32_t kc) const {   // of one stream
-    return tiles == 2 ? c1 - c0 : (c1 - c0 - static_cast<int>((stream ^ kc) & 1) + 1) / 2;
+  int g, tile0, tiles, c0, c1;
+  // With one tile stream s has the chunks whose number in the run is even (s = 0) or odd.
+  __device__ __forceinline__ int chunks(int stream) const {   // of one stream
+    return tiles == 2 ? c1 - c0 : (c1 - c0 - stream + 1) / 2;
   }
-  // running number of a stream's t-th chunk
-  __device__ __forceinline__ uint32_t chunk(int stream, int t, uint32_t kc) const {
-    return kc + (tiles == 2 ? t : 2 * t + ((stream ^ kc) & 1));
+  __device__ __forceinline__ uint32_t chunk(int stream, int t) const {   // its t-th
+    return tiles == 2 ? t : 2 * t + stream;
   }
 };
-__device__ __forceinline__ Part part_at(const QPrefixGeo& geo, int Hkv, int f, int end) {
+__device__ __forceinline__ Part part_of(const QPrefixGeo& geo, int Hkv, int cta) {
   Part p;
-  const int base = Hkv * geo.pairs * 2 * geo.nch;
-  if (f < base) {
-    const int places = 2 * geo.nch;
-    p.unit = f / places;
-    const int u0 = p.unit * places;
-    p.next = min(end, u0 + places);
-    p.g = p.unit / geo.pairs;
-    p.tile0 = 2 * (p.unit - p.g * geo.pairs);
+  const int base = Hkv * geo.pairs * geo.pair_runs;
+  int run, len;
+  if (cta < base) {
+    const int unit = cta / geo.pair_runs;
+    run = cta - unit * geo.pair_runs;
+    len = geo.pair_len;
+    p.g = unit / geo.pairs;
+    p.tile0 = 2 * (unit - p.g * geo.pairs);
     p.tiles = 2;
-    p.c0 = (f - u0) / 2;
-    p.c1 = (p.next - u0) / 2;
   } else {
-    const int us = (f - base) / geo.nch, u0 = base + us * geo.nch;
-    p.next = min(end, u0 + geo.nch);
-    p.unit = Hkv * geo.pairs + us;
-    p.g = us / geo.singles;
-    p.tile0 = 2 * geo.pairs + us - p.g * geo.singles;
+    const int unit = (cta - base) / geo.single_runs;
+    run = cta - base - unit * geo.single_runs;
+    len = geo.single_len;
+    p.g = unit / geo.singles;
+    p.tile0 = 2 * geo.pairs + unit - p.g * geo.singles;
     p.tiles = 1;
-    p.c0 = f - u0;
-    p.c1 = p.next - u0;
   }
+  p.c0 = min(geo.nch, run * len);
+  p.c1 = min(geo.nch, p.c0 + len);
   return p;
 }
 
@@ -214,9 +214,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
   uint64_t* raw_full = bars;            // [NR] a chunk's copies have landed
   uint64_t* raw_free = bars + NR;       // [NR] ... and were read
   uint64_t* k_free = bars + 2 * NR;     // [KST] a chunk's K was used by both streams
-  uint64_t* kv_ready = k_free + KST;    // [VST] fp16 K and V written
-  uint64_t* v_free = kv_ready + VST;    // [VST] V was used by both streams
-  uint64_t* q_ready = v_free + VST;         // [2] by stream: Q written
+  uint64_t* k_ready = k_free + KST;     // [KST] K widened
+  uint64_t* v_free = k_ready + KST;     // [VST] the same for V
+  uint64_t* v_ready = v_free + VST;
+  uint64_t* q_ready = v_ready + VST;    // [2] by stream: Q written
   // by stream and buffer (2 * stream + buffer):
   uint64_t* s_full = q_ready + 2;       // [4] scores of a chunk
   uint64_t* p_full = q_ready + 6;       // [4] its weights written
@@ -227,10 +228,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
 
   if (tid == 0) s_src = a.B;
   if (tid < SM::NBAR) {
-    const int i = tid, j = i - 2 * NR, k = j - KST - 2 * VST;   // k: pairs from q_ready on
+    const int i = tid, j = i - 2 * NR, l = j - 2 * KST, k = l - 2 * VST;   // k: from q_ready on
     const int count = i < NR ? 1 : i < 2 * NR ? kTeamWarps<D>
-                      : j < KST ? 2   // both streams, or one twice
-                      : j < KST + VST ? kTeamWarps<D> : j < KST + 2 * VST ? 2
+                      : j < KST ? 2 : j < 2 * KST ? kTeamWarps<D>   // both streams, or one twice
+                      : l < VST ? 2 : l < 2 * VST ? kTeamWarps<D>
                       : k < 2 ? 128 : k < 6 ? 1 : k < 10 ? 128 : 1;
     mbar_init(bars + i, count);
     fence_barrier_init();
@@ -249,9 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
   const uint32_t tmem = warp_uniform(*s_tmem);
   const int32_t* ids = a.table + static_cast<size_t>(src) * a.max_blocks;
 
-  const int total = a.Hkv * (2 * a.geo.pairs + a.geo.singles) * a.geo.nch;
-  const int w0 = min(total, static_cast<int>(blockIdx.x) * a.geo.per);
-  const int w1 = min(total, w0 + a.geo.per);
+  const Part p = part_of(a.geo, a.Hkv, static_cast<int>(blockIdx.x));
 
   if (warp >= kMmaWarp) {
     fewer_regs<kIssueRegs>();
@@ -266,51 +265,44 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
     const int gmask = (1 << (a.bs_shift - 4)) - 1;
     const unsigned int groups = (1u << (1 << (copy_sh - 4))) - 1u;   // a copy's bits
     const int sub = lane >> 2, cp = lane & 3;
-    uint32_t kc = 0;
-    bool ok = true;
-    for (int f = w0; ok && f < w1;) {
-      const Part p = part_at(a.geo, a.Hkv, f, w1);
-      f = p.next;
-      const uint8_t* head = a.cache + static_cast<size_t>(p.g) * head_bytes;
-      // this lane's copy of chunks c + sub; ids are loaded a turn ahead
-      auto key_of = [&](int c) { return (c + sub) * kPfxKeys + (cp << copy_sh); };
-      auto wanted = [&](int c) {
-        return sub < kAhead && cp < ncopy && c + sub < p.c1 && key_of(c) < a.P;
-      };
-      auto fetch = [&](int c) { return wanted(c) ? __ldg(ids + (key_of(c) >> a.bs_shift)) : 0; };
-      int next = fetch(p.c0);
-      for (int c = p.c0; c < p.c1; c += kAhead) {
-        const int id = next, key = key_of(c);
-        next = fetch(c + kAhead);
-        const bool here = sub < kAhead && c + sub < p.c1, want = wanted(c);
-        const bool take = want && static_cast<unsigned int>(id) < static_cast<unsigned int>(a.num_blocks);
-        if (want && !take) report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x552);
-        const unsigned int got = (__ballot_sync(0xffffffffu, take) >> (lane & 28)) & 0xfu;
-        const uint32_t k = kc + sub, st = k % NR;
-        if (!__all_sync(0xffffffffu,
-                        !here || mbar_wait(raw_free + st, ((k / NR) & 1) ^ 1, a.err, 0x561))) {
-          ok = false;
-          break;
-        }
-        if (here && cp == 0) {
-          unsigned int bits = 0u;
+    const uint8_t* head = a.cache + static_cast<size_t>(p.g) * head_bytes;
+    // this lane's copy of chunks c + sub; ids are loaded a turn ahead
+    auto key_of = [&](int c) { return (c + sub) * kPfxKeys + (cp << copy_sh); };
+    auto wanted = [&](int c) {
+      return sub < kAhead && cp < ncopy && c + sub < p.c1 && key_of(c) < a.P;
+    };
+    auto fetch = [&](int c) { return wanted(c) ? __ldg(ids + (key_of(c) >> a.bs_shift)) : 0; };
+    int next = fetch(p.c0);
+    uint32_t issued = 0;
+    for (int c = p.c0; c < p.c1; c += kAhead) {
+      const int id = next, key = key_of(c);
+      next = fetch(c + kAhead);
+      const bool here = sub < kAhead && c + sub < p.c1, want = wanted(c);
+      const bool take = want && static_cast<unsigned int>(id) < static_cast<unsigned int>(a.num_blocks);
+      if (want && !take) report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x552);
+      const unsigned int got = (__ballot_sync(0xffffffffu, take) >> (lane & 28)) & 0xfu;
+      const uint32_t k = c - p.c0 + sub, st = k % NR;
+      if (!__all_sync(0xffffffffu,
+                      !here || mbar_wait(raw_free + st, ((k / NR) & 1) ^ 1, a.err, 0x561)))
+        break;
+      if (here && cp == 0) {
+        unsigned int bits = 0u;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if ((got >> i) & 1u) bits |= groups << (i << (copy_sh - 4));
-          raw_valid[st] = static_cast<int>(bits);
-          mbar_arrive_expect_tx(raw_full + st, __popc(got) * copy_bytes);
-        }
-        __syncwarp();
-        if (take)
-          bulk_load(sm + SM::RAW0 + st * SM::RAW + cp * copy_bytes,
-                    head + static_cast<uint64_t>(id) * block_bytes +
-                        static_cast<uint32_t>((key >> 4) & gmask) * qgroup_bytes(D),
-                    copy_bytes, raw_full + st);
-        kc += min(kAhead, p.c1 - c);
+        for (int i = 0; i < 4; ++i)
+          if ((got >> i) & 1u) bits |= groups << (i << (copy_sh - 4));
+        raw_valid[st] = static_cast<int>(bits);
+        mbar_arrive_expect_tx(raw_full + st, __popc(got) * copy_bytes);
       }
+      __syncwarp();
+      if (take)
+        bulk_load(sm + SM::RAW0 + st * SM::RAW + cp * copy_bytes,
+                  head + static_cast<uint64_t>(id) * block_bytes +
+                      static_cast<uint32_t>((key >> 4) & gmask) * qgroup_bytes(D),
+                  copy_bytes, raw_full + st);
+      issued += min(kAhead, p.c1 - c);
     }
     // leave no copy in flight
-    for (uint32_t k = kc > NR ? kc - NR : 0; k < kc; ++k)
+    for (uint32_t k = issued > NR ? issued - NR : 0; k < issued; ++k)
       mbar_wait(raw_full + k % NR, (k / NR) & 1, a.err, 0x562);
   } else if (warp < kLoadWarp) {
     // --------------------------------------------------------- tensor cores
@@ -319,67 +311,60 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
     const uint32_t kv0 = smem_u32(sm);
     const uint32_t q0 = smem_u32(sm + SM::QS);
     const uint32_t tS0 = tmem + SM::S0 + 128 * s, tO = tmem + SM::O0 + SM::O_COLS * s;
-    uint32_t kc = 0, done = 0, n_part = 0;   // chunks of the CTA, of the stream; parts
-    bool ok = true;
-    for (int f = w0; ok && f < w1; ++n_part) {
-      const Part p = part_at(a.geo, a.Hkv, f, w1);
-      f = p.next;
-      const int n = p.chunks(s, kc);
-      // S = Q K^T of the t-th chunk, the stream's (done + t)-th
-      auto issue_s = [&](int t) {
-        const uint32_t k = p.chunk(s, t, kc), st = k % VST, ks = k % KST, buf = (done + t) & 1;
-        if (!mbar_wait_warp(kv_ready + st, (k / VST) & 1, a.err, 0x571)) return false;
-        tc_fence_after();
-        const uint64_t kd = warp_uniform(kq_desc(kv0 + ks * SM::TILE));
-        const uint32_t tS = tS0 + 64 * buf;
-#pragma unroll
-        for (int term = 0; term < TERMS; ++term) {
-          const int tile = TERMS == 2 ? term : s;
-          const uint64_t qd = warp_uniform(kq_desc(q0 + tile * SM::Q_TILE));
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t acc = term > 0 || kk > 0 ? 1u : 0u;
-            if (SM::QSMEM)
-              tc_mma(tS, qd + q_step(kk), kd + k_step(kk), idq, acc);
-            else
-              tc_mma_ts(tS, tmem + SM::Q_COLS * tile + kk * 8, kd + k_step(kk), idq, acc);
-          }
-        }
-        tc_commit(s_full + 2 * s + buf);
-        tc_commit(k_free + ks);
-        if (p.tiles == 1) tc_commit(k_free + ks);   // for the stream that does not use it
-        return true;
-      };
-      // O += P V; the part's first product overwrites O
-      auto issue_pv = [&](int t) {
-        const uint32_t st = p.chunk(s, t, kc) % VST, buf = (done + t) & 1;
-        if (!mbar_wait_warp(p_full + 2 * s + buf, ((done + t) >> 1) & 1, a.err, 0x572)) return false;
-        tc_fence_after();
-        const uint64_t vd = warp_uniform(v_desc(kv0 + SM::V0 + st * SM::TILE));
-        const uint32_t tP = tS0 + 64 * buf;
-#pragma unroll
-        for (int term = 0; term < TERMS; ++term)
-#pragma unroll
-          for (int kk = 0; kk < kPfxKeys / 16; ++kk)
-            tc_mma_ts(tO, tP + 32 * term + kk * 8, vd + v_step(kk), idv,
-                      t > 0 || term > 0 || kk > 0 ? 1u : 0u);
-        tc_commit(pv_done + 2 * s + buf);
-        tc_commit(v_free + st);
-        if (p.tiles == 1) tc_commit(v_free + st);
-        return true;
-      };
-      ok = mbar_wait_warp(q_ready + s, n_part & 1, a.err, 0x573);
-      if (TERMS == 2 && ok) ok = mbar_wait_warp(q_ready + 1 - s, n_part & 1, a.err, 0x573);
+    const int n = p.chunks(s);
+    // S = Q K^T of the stream's t-th chunk
+    auto issue_s = [&](int t) {
+      const uint32_t k = p.chunk(s, t), ks = k % KST, buf = t & 1;
+      if (!mbar_wait_warp(k_ready + ks, (k / KST) & 1, a.err, 0x571)) return false;
       tc_fence_after();
-      for (int t = 0; ok && t < n && t < 2; ++t) ok = issue_s(t);
-      for (int t = 0; ok && t < n; ++t) {
-        ok = issue_pv(t);
-        if (ok && t + 2 < n)   // over this chunk's weights
-          ok = mbar_wait_warp(pv_done + 2 * s + ((done + t) & 1), ((done + t) >> 1) & 1, a.err,
-                              0x574) && issue_s(t + 2);
+      const uint64_t kd = warp_uniform(kq_desc(kv0 + ks * SM::TILE));
+      const uint32_t tS = tS0 + 64 * buf;
+#pragma unroll
+      for (int term = 0; term < TERMS; ++term) {
+        const int tile = TERMS == 2 ? term : s;
+        const uint64_t qd = warp_uniform(kq_desc(q0 + tile * SM::Q_TILE));
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t acc = term > 0 || kk > 0 ? 1u : 0u;
+          if (SM::QSMEM)
+            tc_mma(tS, qd + q_step(kk), kd + k_step(kk), idq, acc);
+          else
+            tc_mma_ts(tS, tmem + SM::Q_COLS * tile + kk * 8, kd + k_step(kk), idq, acc);
+        }
       }
-      kc += p.c1 - p.c0;
-      done += n;
+      tc_commit(s_full + 2 * s + buf);
+      tc_commit(k_free + ks);
+      if (p.tiles == 1) tc_commit(k_free + ks);   // for the stream that does not use it
+      return true;
+    };
+    // O += P V; the first product overwrites O
+    auto issue_pv = [&](int t) {
+      const uint32_t k = p.chunk(s, t), st = k % VST, buf = t & 1;
+      if (!mbar_wait_warp(v_ready + st, (k / VST) & 1, a.err, 0x576) ||
+          !mbar_wait_warp(p_full + 2 * s + buf, (t >> 1) & 1, a.err, 0x572))
+        return false;
+      tc_fence_after();
+      const uint64_t vd = warp_uniform(v_desc(kv0 + SM::V0 + st * SM::TILE));
+      const uint32_t tP = tS0 + 64 * buf;
+#pragma unroll
+      for (int term = 0; term < TERMS; ++term)
+#pragma unroll
+        for (int kk = 0; kk < kPfxKeys / 16; ++kk)
+          tc_mma_ts(tO, tP + 32 * term + kk * 8, vd + v_step(kk), idv,
+                    t > 0 || term > 0 || kk > 0 ? 1u : 0u);
+      tc_commit(pv_done + 2 * s + buf);
+      tc_commit(v_free + st);
+      if (p.tiles == 1) tc_commit(v_free + st);
+      return true;
+    };
+    bool ok = mbar_wait_warp(q_ready + s, 0, a.err, 0x573);
+    if (TERMS == 2 && ok) ok = mbar_wait_warp(q_ready + 1 - s, 0, a.err, 0x573);
+    tc_fence_after();
+    for (int t = 0; ok && t < n && t < 2; ++t) ok = issue_s(t);
+    for (int t = 0; ok && t < n; ++t) {
+      ok = issue_pv(t);
+      if (ok && t + 2 < n)   // over this chunk's weights
+        ok = mbar_wait_warp(pv_done + 2 * s + (t & 1), (t >> 1) & 1, a.err, 0x574) && issue_s(t + 2);
     }
   }
   } else if (warp >= 8) {
@@ -389,39 +374,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
     constexpr int kRows = 32 * kTeam / kParts;   // rows of K (and V) at a time
     const int team = (warp - 8) / kTeam, t = tid - 256 - team * 32 * kTeam;
     const int row0 = t / kParts, part = t % kParts;
-    uint32_t kc = 0;
-    bool ok = true;
-    for (int f = w0; ok && f < w1;) {
-      const Part p = part_at(a.geo, a.Hkv, f, w1);
-      f = p.next;
-      const uint32_t end = kc + p.c1 - p.c0;
-      // the team's first chunk from here on
-      for (uint32_t k = kc + (team + kTeams - kc % kTeams) % kTeams; k < end; k += kTeams) {
-        const int rs = k % NR, st = k % VST, ks = k % KST;
-        ok = mbar_wait_warp(raw_full + rs, (k / NR) & 1, a.err, 0x581) &&
-             mbar_wait_warp(k_free + ks, ((k / KST) & 1) ^ 1, a.err, 0x582) &&
-             mbar_wait_warp(v_free + st, ((k / VST) & 1) ^ 1, a.err, 0x583);
-        if (!ok) break;
-        const int bits = raw_valid[rs];
-        const uint8_t* raw = sm + SM::RAW0 + rs * SM::RAW;
-        const uint32_t k_tile = smem_u32(sm) + ks * SM::TILE;
-        const uint32_t v_tile = smem_u32(sm) + SM::V0 + st * SM::TILE;
+    for (int k = team; k < p.c1 - p.c0; k += kTeams) {
+      const int rs = k % NR, st = k % VST, ks = k % KST;
+      if (!mbar_wait_warp(raw_full + rs, (k / NR) & 1, a.err, 0x581) ||
+          !mbar_wait_warp(k_free + ks, ((k / KST) & 1) ^ 1, a.err, 0x582))
+        break;
+      const int bits = raw_valid[rs];
+      const uint8_t* raw = sm + SM::RAW0 + rs * SM::RAW;
+      auto all_rows = [&](int codes_at, int scales_at, uint32_t tile) {
 #pragma unroll
-        for (int row = row0; row < kPfxKeys; row += kRows) {
-          const uint8_t* grp = raw + (row >> 4) * qgroup_bytes(D);
-          const bool valid = (bits >> (row >> 4)) & 1;
-          widen<D>(grp, 0, 8 * D, k_tile, row, part, valid);
-          widen<D>(grp, 9 * D, 17 * D, v_tile, row, part, valid);
-        }
-        if (t == 0) kv_valid[st] = bits;
+        for (int row = row0; row < kPfxKeys; row += kRows)
+          widen<D>(raw + (row >> 4) * qgroup_bytes(D), codes_at, scales_at, tile, row, part,
+                   (bits >> (row >> 4)) & 1);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(kv_ready + st);
-          mbar_arrive(raw_free + rs);
-        }
+      };
+      all_rows(0, 8 * D, smem_u32(sm) + ks * SM::TILE);
+      if (t == 0) kv_valid[k % SM::kValid] = bits;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(k_ready + ks);
+      if (!mbar_wait_warp(v_free + st, ((k / VST) & 1) ^ 1, a.err, 0x583)) break;
+      all_rows(9 * D, 17 * D, smem_u32(sm) + SM::V0 + st * SM::TILE);
+      if (lane == 0) {
+        mbar_arrive(v_ready + st);
+        mbar_arrive(raw_free + rs);
       }
-      kc = end;
     }
   } else {
     more_regs<kSoftmaxRegs>();
@@ -432,211 +409,201 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
     const uint32_t tS0 = tmem + SM::S0 + 128 * s + lane_base;
     const uint32_t tO = tmem + SM::O0 + SM::O_COLS * s + lane_base;
     const uint32_t sQ = smem_u32(sm + SM::QS) + s * SM::Q_TILE;
-    uint32_t kc = 0, done = 0;
     bool ok = true;
-    for (int f = w0; f < w1;) {
-      const Part p = part_at(a.geo, a.Hkv, f, w1);
-      f = p.next;
-      const int gr = (p.tile0 + (p.tiles == 2 ? s : 0)) * 128 + r;   // row of the KV head
-      const int b = gr / a.G, slot = gr - b * a.G;
-      const bool live = b < a.B && pfx_start(a.lens, b, a.P, a.N, a.max_blocks, a.bs_shift) > 0;
-      const bool idle = !__any_sync(0xffffffffu, live);
-      // ---- this row of Q, 64 elements at a time; all of a pass's loads are in flight
-      // together, and a bf16 row is loaded once
-      constexpr int kVecs = TERMS == 2 ? 16 : 8;   // 16-byte pieces of 64 elements
-      const size_t q_row = live ? static_cast<size_t>(b) * a.Hq + a.heads[p.g * a.G + slot] : 0;
-      const uint4* row = reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) +
-                                                        q_row * D * (TERMS == 2 ? 4 : 2));
-      uint4 raw[D / 64][kVecs];
-      float amax = 0.f;
+    const int gr = (p.tile0 + (p.tiles == 2 ? s : 0)) * 128 + r;   // row of the KV head
+    const int b = gr / a.G, slot = gr - b * a.G;
+    const bool live = b < a.B && pfx_start(a.lens, b, a.P, a.N, a.max_blocks, a.bs_shift) > 0;
+    const bool idle = !__any_sync(0xffffffffu, live);
+    // ---- this row of Q, 64 elements at a time; all of a pass's loads are in flight
+    // together, and a bf16 row is loaded once
+    constexpr int kVecs = TERMS == 2 ? 16 : 8;   // 16-byte pieces of 64 elements
+    const size_t q_row = live ? static_cast<size_t>(b) * a.Hq + a.heads[p.g * a.G + slot] : 0;
+    const uint4* row = reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) +
+                                                      q_row * D * (TERMS == 2 ? 4 : 2));
+    uint4 raw[D / 64][kVecs];
+    float amax = 0.f;
 #pragma unroll
-      for (int h = 0; h < D / 64; ++h)
+    for (int h = 0; h < D / 64; ++h)
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i)
-          raw[h][i] = live ? __ldg(row + h * kVecs + i) : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < kVecs; ++i)
+        raw[h][i] = live ? __ldg(row + h * kVecs + i) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int h = 0; h < D / 64; ++h)
+    for (int h = 0; h < D / 64; ++h)
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-          const uint32_t w[4] = {raw[h][i].x, raw[h][i].y, raw[h][i].z, raw[h][i].w};
+      for (int i = 0; i < kVecs; ++i) {
+        const uint32_t w[4] = {raw[h][i].x, raw[h][i].y, raw[h][i].z, raw[h][i].w};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (TERMS == 2) {
-              amax = fmaxf(amax, fabsf(__uint_as_float(w[j])));
-            } else {
-              amax = fmaxf(amax, fabsf(__uint_as_float(w[j] << 16)));
-              amax = fmaxf(amax, fabsf(__uint_as_float(w[j] & 0xffff0000u)));
-            }
-          }
-        }
-      int e = kQExp;
-      if (amax > 0.f && amax < CUDART_INF_F) e = max(ilogbf(amax), -100);
-      const float up = ldexpf(1.f, kQExp - e);
-      const float ml = fmaxf(a.scale * ldexpf(1.f, e - kQExp), 1e-37f) * kLog2e;
-      // (fp32: both streams read both terms, which must not change under the other's scores)
-      if (TERMS == 2) asm volatile("bar.sync 1, 256;" ::: "memory");
-#pragma unroll
-      for (int h = 0; h < D / 64; ++h) {
-        uint32_t w[32];
-#pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-          const uint32_t v[4] = {raw[h][i].x, raw[h][i].y, raw[h][i].z, raw[h][i].w};
+        for (int j = 0; j < 4; ++j) {
           if (TERMS == 2) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float lo = __uint_as_float(v[2 * j]) * up, hi = __uint_as_float(v[2 * j + 1]) * up;
-              if (s == 1) {
-                lo -= f16_rounded(lo);
-                hi -= f16_rounded(hi);
-              }
-              w[2 * i + j] = pack_f16(lo, hi);
-            }
+            amax = fmaxf(amax, fabsf(__uint_as_float(w[j])));
           } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              w[(4 * i + j) & 31] = pack_f16(__uint_as_float(v[j] << 16) * up,
-                                             __uint_as_float(v[j] & 0xffff0000u) * up);
+            amax = fmaxf(amax, fabsf(__uint_as_float(w[j] << 16)));
+            amax = fmaxf(amax, fabsf(__uint_as_float(w[j] & 0xffff0000u)));
           }
         }
-        if (SM::QSMEM) {
+      }
+    int e = kQExp;
+    if (amax > 0.f && amax < CUDART_INF_F) e = max(ilogbf(amax), -100);
+    const float up = ldexpf(1.f, kQExp - e);
+    const float ml = fmaxf(a.scale * ldexpf(1.f, e - kQExp), 1e-37f) * kLog2e;
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
-                             sQ + sw128_offset(kPfxRows, r, 8 * h + i)),
-                         "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
-                         : "memory");
+    for (int h = 0; h < D / 64; ++h) {
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < kVecs; ++i) {
+        const uint32_t v[4] = {raw[h][i].x, raw[h][i].y, raw[h][i].z, raw[h][i].w};
+        if (TERMS == 2) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float lo = __uint_as_float(v[2 * j]) * up, hi = __uint_as_float(v[2 * j + 1]) * up;
+            if (s == 1) {
+              lo -= f16_rounded(lo);
+              hi -= f16_rounded(hi);
+            }
+            w[2 * i + j] = pack_f16(lo, hi);
+          }
         } else {
-          tmem_st32(tQ + 32 * h, w);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            w[(4 * i + j) & 31] = pack_f16(__uint_as_float(v[j] << 16) * up,
+                                           __uint_as_float(v[j] & 0xffff0000u) * up);
         }
       }
-      if (SM::QSMEM) fence_proxy_async_smem();
-      else tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(q_ready + s);
-      // ---- its chunks
-      // weights are 2^((product - ref) * ml + kShiftHere): the reference is a raw product,
-      // so a huge score's distance from it is exact
-      float ref = kNoKey, l = 0.f;
-      const int n = p.chunks(s, kc);
-      const uint64_t ml2 = f2_pack(ml, ml), shift2 = f2_pack(kShiftHere, kShiftHere);
-      for (int t = 0; ok && t < n; ++t) {
-        const uint32_t st = p.chunk(s, t, kc) % VST, g = done + t, buf = g & 1;
-        const uint32_t tS = tS0 + 64 * buf;
-        ok = mbar_wait_warp(s_full + 2 * s + buf, (g >> 1) & 1, a.err, 0x591);
-        if (!ok) break;
-        tc_fence_after();
-        if (!idle) {
-          float x[64];
+      if (SM::QSMEM) {
 #pragma unroll
-          for (int cc = 0; cc < 2; ++cc) {
-            uint32_t v[32];
-            tmem_ld32(tS + 32 * cc, v);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) x[32 * cc + i] = __uint_as_float(v[i]);
-          }
-          const int bits = kv_valid[st];   // (written before kv_ready, which the MMAs waited for)
-          tmem_wait_ld();
-          if (bits != 0xf) {
-#pragma unroll
-            for (int i = 0; i < 64; ++i)
-              if (!((bits >> (i / 16)) & 1)) x[i] = kNegInf;
-          }
-          // The reference goes up to this chunk's largest product (all lanes).
-          auto raise = [&]() {
-            float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-            for (int i = 4; i + 1 < 64; i += 2) mx[(i >> 1) & 3] = fmax3(mx[(i >> 1) & 3], x[i], x[i + 1]);
-            const float up_to = fmax3(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]), ref);
-            const float al = ex2((ref - up_to) * ml);
-            const bool moved = __any_sync(0xffffffffu, up_to > ref);
-            ref = up_to;
-            l *= al;
-            if (!moved || t == 0) return;
-            const uint32_t before = g - 1;   // O is still once its product is in
-            ok = mbar_wait_warp(pv_done + 2 * s + (before & 1), (before >> 1) & 1, a.err, 0x593);
-            if (!ok) return;
-            tc_fence_after();
-#pragma unroll 1
-            for (int cc = 0; cc < D; cc += 16) {   // few at a time: the scores are held
-              uint32_t o[16];
-              tmem_ld16(tO + cc, o);
-              tmem_wait_ld();
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-              tmem_st16(tO + cc, o);
-            }
-          };
-          // A chunk's weights are taken with the reference as it is; only where their
-          // sum shows that one may have passed fp16 the products are searched for their
-          // maximum, and the weights taken again.
-          if (t == 0) raise();
-          float sum;
-          for (bool again = t > 0;; again = false) {
-            const uint64_t minus = f2_pack(-ref, -ref);
-            uint64_t part_sum[2] = {0ull, 0ull};
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              uint32_t hi[16], lo[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const int at = 32 * half + 2 * i;
-                float p0, p1;
-                f2_unpack(f2_fma(f2_add(f2_pack(x[at], x[at + 1]), minus), ml2, shift2), p0, p1);
-                p0 = ex2(p0);
-                p1 = ex2(p1);
-                part_sum[i & 1] = f2_add(part_sum[i & 1], f2_pack(p0, p1));
-                hi[i] = pack_f16(p0, p1);
-                if (TERMS == 2) lo[i] = pack_f16(p0 - f16_rounded(p0), p1 - f16_rounded(p1));
-              }
-              tmem_st16(tS + 16 * half, hi);
-              if (TERMS == 2) tmem_st16(tS + 32 + 16 * half, lo);
-            }
-            float s0, s1;
-            f2_unpack(f2_add(part_sum[0], part_sum[1]), s0, s1);
-            sum = s0 + s1;
-            tmem_wait_st();
-            if (!again || !__any_sync(0xffffffffu, !(sum < 65000.f))) break;
-            raise();
-            if (!ok) break;
-          }
-          if (!ok) break;
-          l += sum;
-        }
-        tc_fence_before();
-        mbar_arrive(p_full + 2 * s + buf);
+        for (int i = 0; i < 8; ++i)
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
+                           sQ + sw128_offset(kPfxRows, r, 8 * h + i)),
+                       "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
+                       : "memory");
+      } else {
+        tmem_st32(tQ + 32 * h, w);
       }
-      // ---- the piece
-      if (ok && n > 0) {
-        const uint32_t g = done + n - 1;
-        ok = mbar_wait_warp(pv_done + 2 * s + (g & 1), (g >> 1) & 1, a.err, 0x594);
-      }
-      kc += p.c1 - p.c0;
-      done += n;
+    }
+    if (SM::QSMEM) fence_proxy_async_smem();
+    else tmem_wait_st();
+    tc_fence_before();
+    mbar_arrive(q_ready + s);
+    // ---- its chunks
+    // weights are 2^((product - ref) * ml + kShiftHere): the reference is a raw product,
+    // so a huge score's distance from it is exact
+    float ref = kNoKey, l = 0.f;
+    const int n = p.chunks(s);
+    const uint64_t ml2 = f2_pack(ml, ml), shift2 = f2_pack(kShiftHere, kShiftHere);
+    for (int t = 0; ok && t < n; ++t) {
+      const uint32_t k = p.chunk(s, t), buf = t & 1;
+      const uint32_t tS = tS0 + 64 * buf;
+      ok = mbar_wait_warp(s_full + 2 * s + buf, (t >> 1) & 1, a.err, 0x591);
+      if (!ok) break;
       tc_fence_after();
       if (!idle) {
-        float* piece = a.part + pfx_piece_floats(D) * (2 * (static_cast<size_t>(p.unit) + blockIdx.x) + s);
-#pragma unroll 1
-        for (int cc = 0; cc < D / 32; ++cc) {
-          uint32_t o[32];
-          tmem_ld32(tO + 32 * cc, o);
-          tmem_wait_ld();
-          float4* dst = reinterpret_cast<float4*>(piece + r * D + 32 * cc);
-          if (live)
+        float x[64];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[i] = n > 0 ? make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                           __uint_as_float(o[4 * i + 2]),
-                                           __uint_as_float(o[4 * i + 3]))
-                             : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int cc = 0; cc < 2; ++cc) {
+          uint32_t v[32];
+          tmem_ld32(tS + 32 * cc, v);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[32 * cc + i] = __uint_as_float(v[i]);
         }
-        if (live) {
-          // (as the reference of weights held as 2^14 p)
-          piece[kPfxRows * D + r] = ref == kNoKey ? kNoKey : ref * ml + (kPShift - kShiftHere);
-          piece[kPfxRows * (D + 1) + r] = l;
+        const int bits = kv_valid[k % SM::kValid];   // (written before k_ready, which the MMAs waited for)
+        tmem_wait_ld();
+        if (bits != 0xf) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (!((bits >> (i / 16)) & 1)) x[i] = kNegInf;
         }
+        // The reference goes up to this chunk's largest product (all lanes).
+        auto raise = [&]() {
+          float mx[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+          for (int i = 4; i + 1 < 64; i += 2) mx[(i >> 1) & 3] = fmax3(mx[(i >> 1) & 3], x[i], x[i + 1]);
+          const float up_to = fmax3(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]), ref);
+          const float al = ex2((ref - up_to) * ml);
+          const bool moved = __any_sync(0xffffffffu, up_to > ref);
+          ref = up_to;
+          l *= al;
+          if (!moved || t == 0) return;
+          const int before = t - 1;   // O is still once its product is in
+          ok = mbar_wait_warp(pv_done + 2 * s + (before & 1), (before >> 1) & 1, a.err, 0x593);
+          if (!ok) return;
+          tc_fence_after();
+#pragma unroll 1
+          for (int cc = 0; cc < D; cc += 16) {   // few at a time: the scores are held
+            uint32_t o[16];
+            tmem_ld16(tO + cc, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+            tmem_st16(tO + cc, o);
+          }
+        };
+        // A chunk's weights are taken with the reference as it is; only where their
+        // sum shows that one may have passed fp16 the products are searched for their
+        // maximum, and the weights taken again.
+        if (t == 0) raise();
+        float sum;
+        for (bool again = t > 0;; again = false) {
+          const uint64_t minus = f2_pack(-ref, -ref);
+          uint64_t part_sum[2] = {0ull, 0ull};
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t hi[16], lo[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int at = 32 * half + 2 * i;
+              float p0, p1;
+              f2_unpack(f2_fma(f2_add(f2_pack(x[at], x[at + 1]), minus), ml2, shift2), p0, p1);
+              p0 = ex2(p0);
+              p1 = ex2(p1);
+              part_sum[i & 1] = f2_add(part_sum[i & 1], f2_pack(p0, p1));
+              hi[i] = pack_f16(p0, p1);
+              if (TERMS == 2) lo[i] = pack_f16(p0 - f16_rounded(p0), p1 - f16_rounded(p1));
+            }
+            tmem_st16(tS + 16 * half, hi);
+            if (TERMS == 2) tmem_st16(tS + 32 + 16 * half, lo);
+          }
+          float s0, s1;
+          f2_unpack(f2_add(part_sum[0], part_sum[1]), s0, s1);
+          sum = s0 + s1;
+          tmem_wait_st();
+          if (!again || !__any_sync(0xffffffffu, !(sum < 65000.f))) break;
+          raise();
+          if (!ok) break;
+        }
+        if (!ok) break;
+        l += sum;
       }
       tc_fence_before();
+      mbar_arrive(p_full + 2 * s + buf);
     }
+    // ---- the piece
+    if (ok && n > 0) {
+      ok = mbar_wait_warp(pv_done + 2 * s + ((n - 1) & 1), ((n - 1) >> 1) & 1, a.err, 0x594);
+    }
+    tc_fence_after();
+    if (!idle) {
+      float* piece = a.part + pfx_piece_floats(D) * (2 * static_cast<size_t>(blockIdx.x) + s);
+#pragma unroll 1
+      for (int cc = 0; cc < D / 32; ++cc) {
+        uint32_t o[32];
+        tmem_ld32(tO + 32 * cc, o);
+        tmem_wait_ld();
+        float4* dst = reinterpret_cast<float4*>(piece + r * D + 32 * cc);
+        if (live)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            dst[i] = n > 0 ? make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                         __uint_as_float(o[4 * i + 2]),
+                                         __uint_as_float(o[4 * i + 3]))
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      if (live) {
+        // (as the reference of weights held as 2^14 p)
+        piece[kPfxRows * D + r] = ref == kNoKey ? kNoKey : ref * ml + (kPShift - kShiftHere);
+        piece[kPfxRows * (D + 1) + r] = l;
+      }
+    }
+    tc_fence_before();
   }
   if (warp == kLoadWarp) pdl_wait();
   tc_fence_before();
@@ -693,21 +660,13 @@ __global__ void __launch_bounds__(kJoinThreads) k_qprefix_join(const __grid_cons
     const int kv_row = b * a.G + slot;
     const int tile = kv_row / kPfxRows, r = kv_row % kPfxRows;
     const bool pair = tile < 2 * geo.pairs;
-    int unit, u0, u1;
-    if (pair) {
-      unit = g * geo.pairs + tile / 2;
-      u0 = unit * 2 * geo.nch;
-      u1 = u0 + 2 * geo.nch;
-    } else {
-      unit = a.Hkv * geo.pairs + g * geo.singles + tile - 2 * geo.pairs;
-      u0 = (unit + a.Hkv * geo.pairs) * geo.nch;
-      u1 = u0 + geo.nch;
-    }
-    const int c0 = u0 / geo.per, ctas = (u1 - 1) / geo.per - c0 + 1;
+    const int cta = pair ? (g * geo.pairs + tile / 2) * geo.pair_runs
+                         : a.Hkv * geo.pairs * geo.pair_runs +
+                               (g * geo.singles + tile - 2 * geo.pairs) * geo.single_runs;
     // pair: the tile's piece of every CTA; else both pieces of each
-    const int n = pair ? ctas : 2 * ctas;
+    const int n = pair ? geo.pair_runs : 2 * geo.single_runs;
     const size_t stride = (pair ? 2 : 1) * pfx_piece_floats(D);
-    const float* p = a.part + pfx_piece_floats(D) * (2 * static_cast<size_t>(unit + c0) +
+    const float* p = a.part + pfx_piece_floats(D) * (2 * static_cast<size_t>(cta) +
                                                      (pair ? tile & 1 : 0));
     for (int s = worker; s < n; s += kBatch * workers) {
       Joined y[kBatch];
@@ -747,9 +706,8 @@ __global__ void __launch_bounds__(kJoinThreads) k_qprefix_join(const __grid_cons
 template <int D, bool F32>
 cudaError_t launch_join_t(const QPrefixArgs& a, cudaStream_t st) {
   // pieces of a row at most, eight of them per worker
-  const int places = (a.geo.pairs > 0 ? 2 : 1) * a.geo.nch;
-  const int ctas = (places + a.geo.per - 1) / a.geo.per + 1;
-  const int pieces = a.geo.singles > 0 ? 2 * ctas : ctas;
+  const int pieces = max(a.geo.pairs > 0 ? a.geo.pair_runs : 0,
+                         a.geo.singles > 0 ? 2 * a.geo.single_runs : 0);
   const int workers = pieces > 32 ? 8 : pieces > 16 ? 4 : pieces > 8 ? 2 : 1;
   const int64_t per_cta = kJoinThreads / (D / 4) / workers;
   const int64_t joiners = (static_cast<int64_t>(a.B) * a.Hq + per_cta - 1) / per_cta;
@@ -770,17 +728,37 @@ cudaError_t launch_prefix_t(const QPrefixArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// Places of all units in equal, even runs: a pair unit's place is half a chunk.
+// Runs of equal cost, at most one CTA per SM where there are fewer units than SMs: a
+// CTA has one run of one unit (a second one in the same CTA would cost its start, its
+// queries and its pieces again, 10 us). A chunk costs a pair of tiles about 3 where it
+// costs one tile 2.
 QPrefixGeo prefix_geo(int B, int G, int Hkv, int P, int dtype, int sms) {
+  constexpr int64_t kPair = 3, kSingle = 2;
   QPrefixGeo g{};
-  const int tiles = (B * G + kPfxRows - 1) / kPfxRows;
+  const int tiles = static_cast<int>((static_cast<int64_t>(B) * G + kPfxRows - 1) / kPfxRows);
   g.nch = (P + kPfxKeys - 1) / kPfxKeys;
   g.pairs = dtype == KASCADE_F32 ? 0 : tiles / 2;
   g.singles = tiles - 2 * g.pairs;
-  const int total = Hkv * tiles * g.nch;
-  g.per = 2 * ((total + 2 * sms - 1) / (2 * sms));
-  if (g.per < kPfxMinRun) g.per = kPfxMinRun;
-  g.ctas = (total + g.per - 1) / g.per;
+  auto runs = [&](int64_t most, int64_t cost) {   // runs of a unit that cost at most that
+    int64_t len = most / cost;
+    if (len < kPfxMinRun) len = kPfxMinRun;
+    return static_cast<int>((g.nch + len - 1) / len);
+  };
+  auto ctas = [&](int64_t most) {
+    return static_cast<int64_t>(Hkv) * (static_cast<int64_t>(g.pairs) * runs(most, kPair) +
+                                        static_cast<int64_t>(g.singles) * runs(most, kSingle));
+  };
+  int64_t lo = 0, hi = kPair * g.nch;   // hi: a run per unit
+  while (hi - lo > 1) {                 // the smallest cost whose CTAs fit
+    const int64_t mid = (lo + hi) / 2;
+    if (ctas(mid) <= sms) hi = mid;
+    else lo = mid;
+  }
+  g.pair_runs = runs(hi, kPair);
+  g.single_runs = runs(hi, kSingle);
+  g.pair_len = (g.nch + g.pair_runs - 1) / g.pair_runs;
+  g.single_len = (g.nch + g.single_runs - 1) / g.single_runs;
+  g.ctas = static_cast<int>(ctas(hi));
   return g;
 }
 
