@@ -35,8 +35,9 @@ constexpr int kPfxKeys = 64, kPfxRows = 128;
 constexpr int kPfxMinRun = 4;             // chunks of a run at least
 struct QPrefixGeo {
   int nch, pairs, singles, pair_runs, single_runs, pair_len, single_len, ctas;
+  int own_sms;   // for the sequences' own parts, which run beside the prefix
 };
-QPrefixGeo prefix_geo(int B, int G, int Hkv, int P, int dtype, int sms);
+QPrefixGeo prefix_geo(int B, int G, int Hkv, int P, int own, int d, int dtype, int sms);
 // A piece: o [rows][d], m [rows], l [rows].
 constexpr size_t pfx_piece_floats(int d) { return static_cast<size_t>(kPfxRows) * (d + 2); }
 // Pieces at most, on a GPU of up to `sms` SMs.
@@ -95,6 +96,7 @@ struct QDecodeArgs {
   float4* state_o;
   float2* state_ml;
   int P;
+  int max_ctas;               // dense: CTAs at most (0: as many as fit)
   int16_t heads[kMaxQHeads];  // heads[g*G + slot]
 };
 

@@ -138,7 +138,7 @@ QLayout prefix_layout(const Shape& s, int P) {
   QLayout L = qlayout(s, 0);
   L.prefix = L.total;
   if (P > 0) {
-    const QPrefixGeo most = prefix_geo(s.B, s.G, s.Hkv, P, s.dtype, kQMaxCtas);
+    const QPrefixGeo most = prefix_geo(s.B, s.G, s.Hkv, P, s.N - P, s.d, s.dtype, kQMaxCtas);
     L.prefix_o = align256(L.prefix + pfx_pieces(most, s.Hkv, kQMaxCtas) * pfx_piece_floats(s.d) * sizeof(float));
     L.prefix_ml = align256(L.prefix_o + static_cast<size_t>(s.B) * s.Hq * s.d * sizeof(float));
     L.total = align256(L.prefix_ml + static_cast<size_t>(s.B) * s.Hq * sizeof(float2));
@@ -575,7 +575,9 @@ kascade_status kascade_qcache_prefix_decode(const kascade_desc* desc, const kasc
   x.num_blocks = a.num_blocks;
   x.max_blocks = a.max_blocks;
   x.scale = a.scale;
-  x.geo = prefix_geo(k.s.B, k.s.G, k.s.Hkv, prefix_len, k.s.dtype, sm_count());
+  x.geo = prefix_geo(k.s.B, k.s.G, k.s.Hkv, prefix_len, k.s.N - prefix_len, k.s.d, k.s.dtype,
+                     sm_count());
+  a.max_ctas = x.geo.own_sms;
   memcpy(x.heads, a.heads, sizeof(x.heads));
   // the own parts' states, then the prefix's pieces, then both joined
   if ((r = status_of(launch_qdecode_dense(a, k.s.d, k.s.dtype, st))) != KASCADE_OK) return r;

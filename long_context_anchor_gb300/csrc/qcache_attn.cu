@@ -1272,6 +1272,13 @@ cudaError_t launch_dense_t(const QDecodeArgs& a, cudaStream_t st) {
   const cudaError_t e = resident_ctas<kern>(smem, kNW * 32, ctas);
   if (e != cudaSuccess) return e;
   if (ctas > kQMaxCtas) ctas = kQMaxCtas;
+  if (a.max_ctas > 0) {
+    // beside another kernel: both SMs of a TPC or none (clusters of two), since a CTA of
+    // each kernel on one TPC slows both down (10 to 40%)
+    if (ctas > a.max_ctas) ctas = a.max_ctas;
+    if (ctas > 1)
+      return launch_pdl_clusters(2, kern, dim3(ctas & ~1), dim3(kNW * 32), smem, st, u);
+  }
   return launch_pdl(kern, dim3(ctas), dim3(kNW * 32), smem, st, u);
 }
 

@@ -7,7 +7,7 @@
 // shared memory for up to two tiles: S = Q K^T and O += P V on tcgen05 with fp16
 // operands and fp32 sums. As in the dense kernel a stored element is exact in
 // fp16, a row of q is scaled by a power of two (an fp32 q is two fp16 terms), weights
-// are 2^8 p against a reference that is raised to the running maximum when a
+// are 2^kShift p against a reference that is raised to the running maximum when a
 // chunk's weights add up to more than fp16 holds, rounded to fp16 (fp32 outputs: two
 // terms) for the product and summed unrounded. So the reference moves in a
 // part's first chunk and then rarely: raising it for any row of a warp rescales
@@ -27,7 +27,11 @@
 namespace kascade {
 namespace {
 
-constexpr float kShiftHere = 8.f;
+// Weights are 2^kShift p. Larger ones of a wide spread raise the reference less often
+// with a small shift (bf16: 12 bits of room), and small ones keep more bits with a
+// large one (fp32).
+template <int TERMS>
+constexpr float kShift = TERMS == 2 ? 8.f : 4.f;
 
 // Two streams, each with its scores, its running state and its O, run through
 // the same code: a unit of two row tiles gives each stream one of them and every
@@ -485,11 +489,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
     tc_fence_before();
     mbar_arrive(q_ready + s);
     // ---- its chunks
-    // weights are 2^((product - ref) * ml + kShiftHere): the reference is a raw product,
+    // weights are 2^((product - ref) * ml + kShift<TERMS>): the reference is a raw product,
     // so a huge score's distance from it is exact
     float ref = kNoKey, l = 0.f;
     const int n = p.chunks(s);
-    const uint64_t ml2 = f2_pack(ml, ml), shift2 = f2_pack(kShiftHere, kShiftHere);
+    const uint64_t ml2 = f2_pack(ml, ml), shift2 = f2_pack(kShift<TERMS>, kShift<TERMS>);
     for (int t = 0; ok && t < n; ++t) {
       const uint32_t k = p.chunk(s, t), buf = t & 1;
       const uint32_t tS = tS0 + 64 * buf;
@@ -599,7 +603,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
       }
       if (live) {
         // (as the reference of weights held as 2^14 p)
-        piece[kPfxRows * D + r] = ref == kNoKey ? kNoKey : ref * ml + (kPShift - kShiftHere);
+        piece[kPfxRows * D + r] = ref == kNoKey ? kNoKey : ref * ml + (kPShift - kShift<TERMS>);
         piece[kPfxRows * (D + 1) + r] = l;
       }
     }
@@ -728,37 +732,46 @@ cudaError_t launch_prefix_t(const QPrefixArgs& a, cudaStream_t st) {
 
 }  // namespace
 
-// Runs of equal cost, at most one CTA per SM where there are fewer units than SMs: a
-// CTA has one run of one unit (a second one in the same CTA would cost its start, its
-// queries and its pieces again, 10 us). A chunk costs a pair of tiles about 3 where it
-// costs one tile 2.
-QPrefixGeo prefix_geo(int B, int G, int Hkv, int P, int dtype, int sms) {
-  constexpr int64_t kPair = 3, kSingle = 2;
+// A unit's runs are as many as finish first together with the sequences' own parts, whose
+// kernel runs beside this one on the SMs that are left (own_sms): one CTA per SM, and
+// a CTA has one run of one unit (a second one would cost its start, its queries
+// and its pieces again, 10 us). Measured: a chunk takes an SM `pair` ns with two tiles
+// of queries and `single` with one, the own parts' kernel reads 24 bytes a ns on an SM, and
+// each takes about 9 us to start and end. Half of the `own` tokens that a sequence may
+// have are assumed, since the lengths are not known here.
+QPrefixGeo prefix_geo(int B, int G, int Hkv, int P, int own, int d, int dtype, int sms) {
+  const double pair = d == 128 ? 1080 : 850;
+  const double single = (d == 128 ? 625 : 440) * (dtype == KASCADE_F32 ? 2 : 1);
+  const double rest = 0.5 * B * Hkv * static_cast<double>(own) * (9 * d / 8) / 24, start = 9000;
   QPrefixGeo g{};
   const int tiles = static_cast<int>((static_cast<int64_t>(B) * G + kPfxRows - 1) / kPfxRows);
   g.nch = (P + kPfxKeys - 1) / kPfxKeys;
   g.pairs = dtype == KASCADE_F32 ? 0 : tiles / 2;
   g.singles = tiles - 2 * g.pairs;
-  auto runs = [&](int64_t most, int64_t cost) {   // runs of a unit that cost at most that
-    int64_t len = most / cost;
-    if (len < kPfxMinRun) len = kPfxMinRun;
-    return static_cast<int>((g.nch + len - 1) / len);
-  };
-  auto ctas = [&](int64_t most) {
-    return static_cast<int64_t>(Hkv) * (static_cast<int64_t>(g.pairs) * runs(most, kPair) +
-                                        static_cast<int64_t>(g.singles) * runs(most, kSingle));
-  };
-  int64_t lo = 0, hi = kPair * g.nch;   // hi: a run per unit
-  while (hi - lo > 1) {                 // the smallest cost whose CTAs fit
-    const int64_t mid = (lo + hi) / 2;
-    if (ctas(mid) <= sms) hi = mid;
-    else lo = mid;
+  const int least = sms / 16 & ~1, most_runs = (g.nch + kPfxMinRun - 1) / kPfxMinRun;
+  double best = 0;
+  // runs of the larger kind of unit; the smaller kind's take as long at most
+  for (int r = 1; r <= most_runs; ++r) {
+    const int len = (g.nch + r - 1) / r;
+    int single_len = g.pairs > 0 ? static_cast<int>(len * pair / single) : len;
+    if (single_len < kPfxMinRun) single_len = kPfxMinRun;
+    const int single_runs = (g.nch + single_len - 1) / single_len;
+    const int64_t ctas = static_cast<int64_t>(Hkv) * (static_cast<int64_t>(g.pairs) * r +
+                                                      static_cast<int64_t>(g.singles) * single_runs);
+    if (r > 1 && ctas > sms - least) break;
+    const int own_sms = ctas > sms - least ? least : (sms - static_cast<int>(ctas)) & ~1;   // whole TPCs
+    const double t_prefix = start + len * (g.pairs > 0 ? pair : single), t_own = start + rest / own_sms;
+    const double t = t_prefix > t_own ? t_prefix : t_own;
+    if (r == 1 || t < best) {
+      best = t;
+      g.pair_runs = g.pairs > 0 ? r : 1;
+      g.single_runs = single_runs;
+      g.ctas = static_cast<int>(ctas);
+      g.own_sms = own_sms;
+    }
   }
-  g.pair_runs = runs(hi, kPair);
-  g.single_runs = runs(hi, kSingle);
   g.pair_len = (g.nch + g.pair_runs - 1) / g.pair_runs;
   g.single_len = (g.nch + g.single_runs - 1) / g.single_runs;
-  g.ctas = static_cast<int>(ctas(hi));
   return g;
 }
 
