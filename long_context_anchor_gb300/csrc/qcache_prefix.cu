@@ -489,93 +489,111 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
     tc_fence_before();
     mbar_arrive(q_ready + s);
     // ---- its chunks
-    // weights are 2^((product - ref) * ml + kShift<TERMS>): the reference is a raw product,
-    // so a huge score's distance from it is exact
-    float ref = kNoKey, l = 0.f;
+    // weights are 2^(product * ml + c), c = kShift - ref * ml: the reference is a raw
+    // product. c's rounding is common to a row's weights; where it would be felt, or
+    // would overflow them, `careful` chunks have the reference taken off their products
+    // first (c = kShift then).
+    float ref = kNoKey, l = 0.f, c = 0.f;
+    bool careful = false;
     const int n = p.chunks(s);
-    const uint64_t ml2 = f2_pack(ml, ml), shift2 = f2_pack(kShift<TERMS>, kShift<TERMS>);
     for (int t = 0; ok && t < n; ++t) {
-      const uint32_t k = p.chunk(s, t), buf = t & 1;
-      const uint32_t tS = tS0 + 64 * buf;
+      const uint32_t buf = t & 1, tS = tS0 + 64 * buf;
       ok = mbar_wait_warp(s_full + 2 * s + buf, (t >> 1) & 1, a.err, 0x591);
       if (!ok) break;
       tc_fence_after();
       if (!idle) {
-        float x[64];
+        // (written before k_ready, which the MMAs waited for)
+        const int bits = kv_valid[p.chunk(s, t) % SM::kValid];
+        if (bits != 0xf) {   // rare: the products of keys that do not count
+          uint32_t none[16];
 #pragma unroll
-        for (int cc = 0; cc < 2; ++cc) {
-          uint32_t v[32];
-          tmem_ld32(tS + 32 * cc, v);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[32 * cc + i] = __uint_as_float(v[i]);
-        }
-        const int bits = kv_valid[k % SM::kValid];   // (written before k_ready, which the MMAs waited for)
-        tmem_wait_ld();
-        if (bits != 0xf) {
-#pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (!((bits >> (i / 16)) & 1)) x[i] = kNegInf;
-        }
-        // The reference goes up to this chunk's largest product (all lanes).
-        auto raise = [&]() {
-          float mx[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-          for (int i = 4; i + 1 < 64; i += 2) mx[(i >> 1) & 3] = fmax3(mx[(i >> 1) & 3], x[i], x[i + 1]);
-          const float up_to = fmax3(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]), ref);
-          const float al = ex2((ref - up_to) * ml);
-          const bool moved = __any_sync(0xffffffffu, up_to > ref);
-          ref = up_to;
-          l *= al;
-          if (!moved || t == 0) return;
-          const int before = t - 1;   // O is still once its product is in
-          ok = mbar_wait_warp(pv_done + 2 * s + (before & 1), (before >> 1) & 1, a.err, 0x593);
-          if (!ok) return;
-          tc_fence_after();
+          for (int i = 0; i < 16; ++i) none[i] = __float_as_uint(kNegInf);
 #pragma unroll 1
-          for (int cc = 0; cc < D; cc += 16) {   // few at a time: the scores are held
-            uint32_t o[16];
-            tmem_ld16(tO + cc, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
-            tmem_st16(tO + cc, o);
-          }
-        };
-        // A chunk's weights are taken with the reference as it is; only where their
-        // sum shows that one may have passed fp16 the products are searched for their
-        // maximum, and the weights taken again.
-        if (t == 0) raise();
+          for (int i = 0; i < 4; ++i)
+            if (!((bits >> i) & 1)) tmem_st16(tS + 16 * i, none);
+          tmem_wait_st();
+        }
+        // A chunk's weights are taken with the reference as it is; only where their sum
+        // shows that one may have passed fp16 the reference goes up to the chunk's
+        // largest product (all lanes), and the weights are taken again. The weights lie
+        // over the products, so they are kept until then.
+        uint32_t hi[32], lo[TERMS == 2 ? 32 : 1];
         float sum;
-        for (bool again = t > 0;; again = false) {
-          const uint64_t minus = f2_pack(-ref, -ref);
+        for (bool raise = t == 0 || careful;; raise = true) {
+          if (raise) {
+            float up_to = ref;
+#pragma unroll 1
+            for (int cc = 0; cc < 64; cc += 16) {
+              uint32_t v[16];
+              tmem_ld16(tS + cc, v);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; i += 2)
+                up_to = fmax3(up_to, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+            }
+            const float al = ex2((ref - up_to) * ml);
+            const bool moved = __any_sync(0xffffffffu, up_to > ref);
+            ref = up_to;
+            l *= al;
+            if (moved && t > 0) {
+              const int before = t - 1;   // O is still once its product is in
+              ok = mbar_wait_warp(pv_done + 2 * s + (before & 1), (before >> 1) & 1, a.err, 0x593);
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int cc = 0; cc < D; cc += 16) {
+                uint32_t o[16];
+                tmem_ld16(tO + cc, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * al);
+                tmem_st16(tO + cc, o);
+              }
+            }
+            c = fmaf(-ref, ml, kShift<TERMS>);
+            careful = __any_sync(0xffffffffu, !(fabsf(c) < 1024.f));
+            if (careful) {
+              c = kShift<TERMS>;
+#pragma unroll 1
+              for (int cc = 0; cc < 64; cc += 16) {
+                uint32_t v[16];
+                tmem_ld16(tS + cc, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) - ref);
+                tmem_st16(tS + cc, v);
+              }
+            }
+            tmem_wait_st();
+          }
+          uint32_t v[2][32];
+          tmem_ld32(tS, v[0]);
+          tmem_ld32(tS + 32, v[1]);
+          tmem_wait_ld();
+          const uint64_t ml2 = f2_pack(ml, ml), c2 = f2_pack(c, c);
           uint64_t part_sum[2] = {0ull, 0ull};
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            uint32_t hi[16], lo[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int at = 32 * half + 2 * i;
-              float p0, p1;
-              f2_unpack(f2_fma(f2_add(f2_pack(x[at], x[at + 1]), minus), ml2, shift2), p0, p1);
-              p0 = ex2(p0);
-              p1 = ex2(p1);
-              part_sum[i & 1] = f2_add(part_sum[i & 1], f2_pack(p0, p1));
-              hi[i] = pack_f16(p0, p1);
-              if (TERMS == 2) lo[i] = pack_f16(p0 - f16_rounded(p0), p1 - f16_rounded(p1));
-            }
-            tmem_st16(tS + 16 * half, hi);
-            if (TERMS == 2) tmem_st16(tS + 32 + 16 * half, lo);
+          for (int i = 0; i < 32; ++i) {
+            const uint32_t(&x)[32] = v[i >> 4];
+            const int at = 2 * (i & 15);
+            float p0, p1;
+            f2_unpack(f2_fma(f2_pack(__uint_as_float(x[at]), __uint_as_float(x[at + 1])), ml2, c2), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            part_sum[i & 1] = f2_add(part_sum[i & 1], f2_pack(p0, p1));
+            hi[i] = pack_f16(p0, p1);
+            if (TERMS == 2) lo[i] = pack_f16(p0 - f16_rounded(p0), p1 - f16_rounded(p1));
           }
           float s0, s1;
           f2_unpack(f2_add(part_sum[0], part_sum[1]), s0, s1);
           sum = s0 + s1;
-          tmem_wait_st();
-          if (!again || !__any_sync(0xffffffffu, !(sum < 65000.f))) break;
-          raise();
-          if (!ok) break;
+          if (raise || !__any_sync(0xffffffffu, !(sum < 65000.f))) break;
         }
         if (!ok) break;
+        tmem_st32(tS, hi);
+        if constexpr (TERMS == 2) tmem_st32(tS + 32, lo);
         l += sum;
+        tmem_wait_st();
       }
       tc_fence_before();
       mbar_arrive(p_full + 2 * s + buf);
@@ -603,7 +621,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
       }
       if (live) {
         // (as the reference of weights held as 2^14 p)
-        piece[kPfxRows * D + r] = ref == kNoKey ? kNoKey : ref * ml + (kPShift - kShift<TERMS>);
+        piece[kPfxRows * D + r] = ref == kNoKey ? kNoKey
+                                  : careful ? ref * ml + (kPShift - kShift<TERMS>) : kPShift - c;
         piece[kPfxRows * (D + 1) + r] = l;
       }
     }
