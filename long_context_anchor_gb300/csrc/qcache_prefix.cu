@@ -158,36 +158,52 @@ __device__ __forceinline__ Part part_of(const QPrefixGeo& geo, int Hkv, int cta)
   return p;
 }
 
-// 32 elements of a row: 16 bytes of codes and two scales become four 16-byte
-// pieces in the swizzled tile at `tile` (row of the chunk, pieces 4 part ..).
+// A widening thread's 32 elements of a row: 16 bytes of codes and two scales become
+// four 16-byte pieces of the swizzled tile. The rows a thread takes are a multiple
+// of 8 apart, so its places in a row are the same in all of them. At d = 128 the
+// pieces of parts 2 and 3 go in another order (their second half first): eight lanes
+// with two rows of four parts each then store to all banks.
 template <int D>
-__device__ __forceinline__ void widen(const uint8_t* grp, int codes_at, int scales_at, uint32_t tile,
-                                      int row, int part, bool valid) {
-  const int r = row & 15;
-  uint4 w = make_uint4(0u, 0u, 0u, 0u);
-  uint32_t h = 0u;
-  if (valid) {   // what lies there otherwise may be anything
-    w = *reinterpret_cast<const uint4*>(grp + codes_at + r * (D / 2) + part * 16);
-    h = cvt_e4m3x2(*reinterpret_cast<const uint16_t*>(grp + scales_at + r * (D / 16) + part * 2));
-  }
-  const uint32_t s0 = __byte_perm(h, h, 0x1010), s1 = __byte_perm(h, h, 0x3232);
-  // the pieces of parts 2 and 3 go in another order: eight lanes with two rows of
-  // four parts each then store to all banks
-  const int flip = D == 128 ? part & 2 : 0;
-  const uint32_t word[4] = {flip ? w.z : w.x, flip ? w.w : w.y, flip ? w.x : w.z, flip ? w.y : w.w};
-  const uint32_t sa = flip ? s1 : s0, sb = flip ? s0 : s1;
+struct Widen {
+  static constexpr int kParts = D / 32;
+  int codes[2], scales;         // of the first row: its two halves in the order they go, its scales
+  uint32_t to[4];               // places of the pieces
+  uint32_t pick[2];             // which scale the halves have
+  __device__ __forceinline__ Widen(int row, int part) {
+    const int flip = D == 128 ? part & 2 : 0, r = row & 15;
+    codes[0] = (row >> 4) * qgroup_bytes(D) + r * (D / 2) + part * 16 + (flip ? 8 : 0);
+    codes[1] = (row >> 4) * qgroup_bytes(D) + r * (D / 2) + part * 16 + (flip ? 0 : 8);
+    scales = (row >> 4) * qgroup_bytes(D) + r * (D / 16) + part * 2;
+    pick[0] = flip ? 0x3232u : 0x1010u;
+    pick[1] = flip ? 0x1010u : 0x3232u;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    uint32_t x[4];
-    cvt_e2m1x8(word[i], x);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) x[j] = hmul2(x[j], i < 2 ? sa : sb);
-    const uint32_t to = tile + sw128_offset(kPfxKeys, row, 4 * part + (i ^ flip));
-    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(to), "r"(x[0]), "r"(x[1]), "r"(x[2]),
-                 "r"(x[3])
-                 : "memory");
+    for (int i = 0; i < 4; ++i) to[i] = sw128_offset(kPfxKeys, row, 4 * part + (i ^ flip));
   }
-}
+  // The row `rows` (a constant) behind the first; raw: K's codes of the chunk, or V's.
+  template <int ROWS>
+  __device__ __forceinline__ void row(const uint8_t* raw, uint32_t tile, bool valid) const {
+    static_assert(ROWS % 16 == 0, "whole groups");
+    const uint8_t* p = raw + (ROWS / 16) * qgroup_bytes(D);
+    uint2 half[2] = {};
+    uint32_t h = 0u;
+    if (valid) {   // what lies there otherwise may be anything
+      half[0] = *reinterpret_cast<const uint2*>(p + codes[0]);
+      half[1] = *reinterpret_cast<const uint2*>(p + codes[1]);
+      h = cvt_e4m3x2(*reinterpret_cast<const uint16_t*>(p + 8 * D + scales));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t s = __byte_perm(h, h, pick[i >> 1]);
+      uint32_t x[4];
+      cvt_e2m1x8((i & 1) ? half[i >> 1].y : half[i >> 1].x, x);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j] = hmul2(x[j], s);
+      asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(tile + to[i] + ROWS * 128),
+                   "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
+                   : "memory");
+    }
+  }
+};
 
 // The lowest sequence that holds the whole prefix, whose table names its blocks, into
 // src (a.B before; shared memory; all threads).
@@ -374,10 +390,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
   } else if (warp >= 8) {
     fewer_regs<kDeqRegs>();
     // ------------------------------------------------------- codes to fp16
-    constexpr int kTeam = kTeamWarps<D>, kTeams = SM::kTeams, kParts = D / 32;
+    constexpr int kTeam = kTeamWarps<D>, kTeams = SM::kTeams, kParts = Widen<D>::kParts;
     constexpr int kRows = 32 * kTeam / kParts;   // rows of K (and V) at a time
+    static_assert(kRows == 32 && kPfxKeys == 64, "two rows per thread, whole groups apart");
     const int team = (warp - 8) / kTeam, t = tid - 256 - team * 32 * kTeam;
-    const int row0 = t / kParts, part = t % kParts;
+    const Widen<D> w(t / kParts, t % kParts);
+    const int group0 = t / kParts / 16;
     for (int k = team; k < p.c1 - p.c0; k += kTeams) {
       const int rs = k % NR, st = k % VST, ks = k % KST;
       if (!mbar_wait_warp(raw_full + rs, (k / NR) & 1, a.err, 0x581) ||
@@ -385,20 +403,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
         break;
       const int bits = raw_valid[rs];
       const uint8_t* raw = sm + SM::RAW0 + rs * SM::RAW;
-      auto all_rows = [&](int codes_at, int scales_at, uint32_t tile) {
-#pragma unroll
-        for (int row = row0; row < kPfxKeys; row += kRows)
-          widen<D>(raw + (row >> 4) * qgroup_bytes(D), codes_at, scales_at, tile, row, part,
-                   (bits >> (row >> 4)) & 1);
+      auto both_rows = [&](int at, uint32_t tile) {
+        if (bits == 0xf) {
+          w.template row<0>(raw + at, tile, true);
+          w.template row<32>(raw + at, tile, true);
+        } else {
+          w.template row<0>(raw + at, tile, (bits >> group0) & 1);
+          w.template row<32>(raw + at, tile, (bits >> (group0 + 2)) & 1);
+        }
         fence_proxy_async_smem();
         __syncwarp();
       };
-      all_rows(0, 8 * D, smem_u32(sm) + ks * SM::TILE);
+      both_rows(0, smem_u32(sm) + ks * SM::TILE);
       if (t == 0) kv_valid[k % SM::kValid] = bits;
       __syncwarp();
       if (lane == 0) mbar_arrive(k_ready + ks);
       if (!mbar_wait_warp(v_free + st, ((k / VST) & 1) ^ 1, a.err, 0x583)) break;
-      all_rows(9 * D, 17 * D, smem_u32(sm) + SM::V0 + st * SM::TILE);
+      both_rows(9 * D, smem_u32(sm) + SM::V0 + st * SM::TILE);
       if (lane == 0) {
         mbar_arrive(v_ready + st);
         mbar_arrive(raw_free + rs);
