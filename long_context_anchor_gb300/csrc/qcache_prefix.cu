@@ -64,6 +64,12 @@ __device__ __forceinline__ void fewer_regs() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// mbar_wait_warp with the test that usually succeeds in front.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, unsigned int* err,
+                                          unsigned int where) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || mbar_wait_warp(bar, parity, err, where);
+}
+
 template <int D, int TERMS>
 struct Shapes {
   // TMEM columns, 512 in all: O of each stream, two buffers of scores for each (a
@@ -335,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
     // S = Q K^T of the stream's t-th chunk
     auto issue_s = [&](int t) {
       const uint32_t k = p.chunk(s, t), ks = k % KST, buf = t & 1;
-      if (!mbar_wait_warp(k_ready + ks, (k / KST) & 1, a.err, 0x571)) return false;
+      if (!wait_warp(k_ready + ks, (k / KST) & 1, a.err, 0x571)) return false;
       tc_fence_after();
       const uint64_t kd = warp_uniform(kq_desc(kv0 + ks * SM::TILE));
       const uint32_t tS = tS0 + 64 * buf;
@@ -360,8 +366,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
     // O += P V; the first product overwrites O
     auto issue_pv = [&](int t) {
       const uint32_t k = p.chunk(s, t), st = k % VST, buf = t & 1;
-      if (!mbar_wait_warp(v_ready + st, (k / VST) & 1, a.err, 0x576) ||
-          !mbar_wait_warp(p_full + 2 * s + buf, (t >> 1) & 1, a.err, 0x572))
+      if (!wait_warp(v_ready + st, (k / VST) & 1, a.err, 0x576) ||
+          !wait_warp(p_full + 2 * s + buf, (t >> 1) & 1, a.err, 0x572))
         return false;
       tc_fence_after();
       const uint64_t vd = warp_uniform(v_desc(kv0 + SM::V0 + st * SM::TILE));
@@ -377,14 +383,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
       if (p.tiles == 1) tc_commit(v_free + st);
       return true;
     };
-    bool ok = mbar_wait_warp(q_ready + s, 0, a.err, 0x573);
-    if (TERMS == 2 && ok) ok = mbar_wait_warp(q_ready + 1 - s, 0, a.err, 0x573);
+    bool ok = wait_warp(q_ready + s, 0, a.err, 0x573);
+    if (TERMS == 2 && ok) ok = wait_warp(q_ready + 1 - s, 0, a.err, 0x573);
     tc_fence_after();
     for (int t = 0; ok && t < n && t < 2; ++t) ok = issue_s(t);
     for (int t = 0; ok && t < n; ++t) {
       ok = issue_pv(t);
       if (ok && t + 2 < n)   // over this chunk's weights
-        ok = mbar_wait_warp(pv_done + 2 * s + (t & 1), (t >> 1) & 1, a.err, 0x574) && issue_s(t + 2);
+        ok = wait_warp(pv_done + 2 * s + (t & 1), (t >> 1) & 1, a.err, 0x574) && issue_s(t + 2);
     }
   }
   } else if (warp >= 8) {
@@ -398,8 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
     const int group0 = t / kParts / 16;
     for (int k = team; k < p.c1 - p.c0; k += kTeams) {
       const int rs = k % NR, st = k % VST, ks = k % KST;
-      if (!mbar_wait_warp(raw_full + rs, (k / NR) & 1, a.err, 0x581) ||
-          !mbar_wait_warp(k_free + ks, ((k / KST) & 1) ^ 1, a.err, 0x582))
+      if (!wait_warp(raw_full + rs, (k / NR) & 1, a.err, 0x581) ||
+          !wait_warp(k_free + ks, ((k / KST) & 1) ^ 1, a.err, 0x582))
         break;
       const int bits = raw_valid[rs];
       const uint8_t* raw = sm + SM::RAW0 + rs * SM::RAW;
@@ -418,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
       if (t == 0) kv_valid[k % SM::kValid] = bits;
       __syncwarp();
       if (lane == 0) mbar_arrive(k_ready + ks);
-      if (!mbar_wait_warp(v_free + st, ((k / VST) & 1) ^ 1, a.err, 0x583)) break;
+      if (!wait_warp(v_free + st, ((k / VST) & 1) ^ 1, a.err, 0x583)) break;
       both_rows(9 * D, smem_u32(sm) + SM::V0 + st * SM::TILE);
       if (lane == 0) {
         mbar_arrive(v_ready + st);
@@ -519,7 +525,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
     const int n = p.chunks(s);
     for (int t = 0; ok && t < n; ++t) {
       const uint32_t buf = t & 1, tS = tS0 + 64 * buf;
-      ok = mbar_wait_warp(s_full + 2 * s + buf, (t >> 1) & 1, a.err, 0x591);
+      ok = wait_warp(s_full + 2 * s + buf, (t >> 1) & 1, a.err, 0x591);
       if (!ok) break;
       tc_fence_after();
       if (!idle) {
@@ -558,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
             l *= al;
             if (moved && t > 0) {
               const int before = t - 1;   // O is still once its product is in
-              ok = mbar_wait_warp(pv_done + 2 * s + (before & 1), (before >> 1) & 1, a.err, 0x593);
+              ok = wait_warp(pv_done + 2 * s + (before & 1), (before >> 1) & 1, a.err, 0x593);
               if (!ok) break;
               tc_fence_after();
 #pragma unroll 1
@@ -621,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
     }
     // ---- the piece
     if (ok && n > 0) {
-      ok = mbar_wait_warp(pv_done + 2 * s + ((n - 1) & 1), ((n - 1) >> 1) & 1, a.err, 0x594);
+      ok = wait_warp(pv_done + 2 * s + ((n - 1) & 1), ((n - 1) >> 1) & 1, a.err, 0x594);
     }
     tc_fence_after();
     if (!idle) {
