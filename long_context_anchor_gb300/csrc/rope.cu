@@ -27,159 +27,178 @@ namespace kascade {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kCtasPerSm = 4, kAppendCtasPerSm = 3;   // 64 and 80 registers a thread
 
-// A thread has 32 elements of a row, two blocks of 16 that hold whole pairs:
-// blocks (t, t + n_pairs / 16) where pair i is (i, i + n_pairs), neighbouring
-// ones where it is (2 i, 2 i + 1) or where nothing is turned. D / 32 threads
-// share a row, and the pairs of thread t are 16 t .. 16 t + 15.
-template <int D>
+// ------------------------------------------------------------- q and k rows --
+// A thread has two 16-byte pieces of a row that hold whole pairs: pieces (t, t +
+// n_pairs / kVec) where pair i is (i, i + n_pairs), neighbouring ones where it is
+// (2 i, 2 i + 1) or where nothing is turned; the pairs of thread t are kVec t .. . So
+// the loads and the stores of neighbouring threads fill whole sectors, and a token's
+// cosines and sines stay in 4 kVec registers while a warp goes through its heads.
+template <typename T, int D>
 struct Lane {
-  static constexpr int kPerRow = D / 32, kSlots = 32 / kPerRow;   // threads, rows of a warp
-  int t, slot, at[2];   // thread of the row, row of the warp, first element of the blocks
+  static constexpr int kVec = 16 / sizeof(T), kPerRow = D / (2 * kVec), kSlots = 32 / kPerRow;
+  int t, slot, at[2];   // thread of the row, row of the warp, first element of the pieces
   bool turns;
   __device__ __forceinline__ Lane(const RopeSpec& r) {
-    const int lane = threadIdx.x & 31, groups = r.n_pairs >> 4;
+    const int lane = threadIdx.x & 31, groups = r.n_pairs / kVec;
     t = lane % kPerRow;
     slot = lane / kPerRow;
     turns = t < groups;
     const bool far = turns && !r.interleaved;
-    at[0] = far ? 16 * t : 32 * t;
-    at[1] = far ? 16 * (t + groups) : 32 * t + 16;
+    at[0] = far ? kVec * t : 2 * kVec * t;
+    at[1] = far ? kVec * (t + groups) : 2 * kVec * t + kVec;
   }
 };
 
-// 32 elements as they are in memory.
-template <typename T>
-struct Raw {
-  static constexpr int kVec = sizeof(T);   // 16-byte pieces of a block
-  uint4 v[2][kVec];
-  __device__ __forceinline__ void load(const T* row, const int (&at)[2], bool ok) {
+__device__ __forceinline__ void unpack(const uint4& v, float (&x)[4]) {
+  x[0] = __uint_as_float(v.x), x[1] = __uint_as_float(v.y);
+  x[2] = __uint_as_float(v.z), x[3] = __uint_as_float(v.w);
+}
+__device__ __forceinline__ void unpack(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int i = 0; i < kVec; ++i)
-        v[b][i] = ok ? *(reinterpret_cast<const uint4*>(row + at[b]) + i) : make_uint4(0u, 0u, 0u, 0u);
+  for (int j = 0; j < 4; ++j) {
+    x[2 * j] = __uint_as_float(w[j] << 16);
+    x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
   }
-  __device__ __forceinline__ void get(float (&x)[32]) const {
+}
+__device__ __forceinline__ uint4 packed(const float (&x)[4]) {
+  return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                    __float_as_uint(x[3]));
+}
+__device__ __forceinline__ uint4 packed(const float (&x)[8]) {
+  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]),
+                    pack_bf16(x[6], x[7]));
+}
+// Rows may be turned in place, so they are no read-only data.
+template <typename T>
+__device__ __forceinline__ uint4 load16(const T* p) { return *reinterpret_cast<const uint4*>(p); }
+
+// Row `pos` of the table (null: outside it, reported).
+__device__ __forceinline__ const float* table_row(const RopeSpec& r, int pos, unsigned int* err) {
+  if (pos < 0 || pos >= r.n_pos) {
+    report_error(err, KASCADE_ERR_BAD_INPUT, 0x541);
+    return nullptr;
+  }
+  return r.table + pos * (2 * static_cast<size_t>(r.n_pairs));
+}
+
+// Four pairs' cosines and sines from pair `first` on (a multiple of 4) at rows[axis].
+template <bool MIXED>
+__device__ __forceinline__ void load_turn4(const RopeSpec& r, const float* const (&rows)[4], int first,
+                                           float* c, float* s) {
+  auto row_of = [&](int axis) {
+    return axis == 0 ? rows[0] : axis == 1 ? rows[1] : axis == 2 ? rows[2] : rows[3];
+  };
+  if (MIXED && !r.quads) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int i = 0; i < 4; ++i) {
+      const float* p = row_of(r.axis[first + i]);
+      c[i] = p != nullptr ? __ldg(p + first + i) : 1.f;
+      s[i] = p != nullptr ? __ldg(p + r.n_pairs + first + i) : 0.f;
+    }
+    return;
+  }
+  const float* p = MIXED ? row_of(r.axis[first]) : rows[0];
+  float4 a = make_float4(1.f, 1.f, 1.f, 1.f), b = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p != nullptr) {
+    a = __ldg(reinterpret_cast<const float4*>(p + first));
+    b = __ldg(reinterpret_cast<const float4*>(p + r.n_pairs + first));
+  }
+  c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
+  s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
+}
+// The rows of the axes a token has positions on; pos(axis) gives them.
+template <bool MIXED, typename Pos>
+__device__ __forceinline__ void table_rows(const RopeSpec& r, Pos pos, unsigned int* err,
+                                           const float* (&rows)[4]) {
+  if (MIXED) {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        const uint32_t w[4] = {v[b][i].x, v[b][i].y, v[b][i].z, v[b][i].w};
+    for (int i = 0; i < 4; ++i) rows[i] = i < r.n_axes ? table_row(r, pos(i), err) : nullptr;
+  } else {
+    rows[0] = table_row(r, pos(r.axis[0]), err);
+    rows[1] = rows[2] = rows[3] = nullptr;
+  }
+}
+
+__device__ __forceinline__ void turn_pair(float& xa, float& xb, float c, float s) {
+  const float a = xa, b = xb;
+  xa = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  xb = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+}
+
+// What a warp does of one token's rows: heads h0 .. h1 - 1 of a list, kSlots at a time,
+// the next ones loaded while these are computed. src(h), dst(h): rows, weight(h): the
+// norm's weights or null (any: whether some head has them).
+template <typename T, int D, bool INTER, bool MIXED, typename Src, typename Dst, typename Weight,
+          typename Pos>
+__device__ __forceinline__ void turn_rows(const RopeSpec& r, int h0, int h1, Src src, Dst dst,
+                                          Weight weight, bool any, Pos pos, unsigned int* err) {
+  using L = Lane<T, D>;
+  constexpr int V = L::kVec;
+  const L l(r);
+  uint4 raw[2];
+  int h = h0 + l.slot;
+  auto load = [&](int at) {
+    raw[0] = raw[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (at < h1) {
+      const T* row = src(at);
+      raw[0] = load16(row + l.at[0]);
+      raw[1] = load16(row + l.at[1]);
+    }
+  };
+  load(h);
+  float c[V], s[V];
+  if (l.turns) {
+    const float* rows[4];
+    table_rows<MIXED>(r, pos, err, rows);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (sizeof(T) == 4) {
-            x[16 * b + 4 * i + j] = __uint_as_float(w[j]);
-          } else {
-            x[16 * b + 8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-            x[16 * b + 8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-          }
+    for (int i = 0; i < V; i += 4) load_turn4<MIXED>(r, rows, V * l.t + i, c + i, s + i);
+  }
+  for (int first = h0; first < h1; first += L::kSlots, h += L::kSlots) {
+    float x[2][V];
+    unpack(raw[0], x[0]);
+    unpack(raw[1], x[1]);
+    if (first + L::kSlots < h1) load(h + L::kSlots);
+    if (any) {
+      const T* w = weight(min(h, h1 - 1));
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) ss = fmaf(x[0][i], x[0][i], ss);
+#pragma unroll
+      for (int i = 0; i < V; ++i) ss = fmaf(x[1][i], x[1][i], ss);
+#pragma unroll
+      for (int off = 1; off < L::kPerRow; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+      if (w != nullptr) {
+        const float n = rsqrtf(ss * (1.f / D) + r.eps);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          float g[V];
+          unpack(__ldg(reinterpret_cast<const uint4*>(w + l.at[b])), g);
+#pragma unroll
+          for (int i = 0; i < V; ++i) x[b][i] = x[b][i] * n * g[i];
         }
       }
-  }
-};
-
-__device__ __forceinline__ void store_row(float* row, const int (&at)[2], const float (&x)[32]) {
-#pragma unroll
-  for (int b = 0; b < 2; ++b)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float* p = x + 16 * b + 4 * i;
-      *(reinterpret_cast<float4*>(row + at[b]) + i) = make_float4(p[0], p[1], p[2], p[3]);
     }
-}
-__device__ __forceinline__ void store_row(__nv_bfloat16* row, const int (&at)[2],
-                                          const float (&x)[32]) {
+    if (l.turns) {
 #pragma unroll
-  for (int b = 0; b < 2; ++b)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float* p = x + 16 * b + 8 * i;
-      *(reinterpret_cast<uint4*>(row + at[b]) + i) =
-          make_uint4(pack_bf16(p[0], p[1]), pack_bf16(p[2], p[3]), pack_bf16(p[4], p[5]),
-                     pack_bf16(p[6], p[7]));
+      for (int i = 0; i < V; ++i) {
+        if (INTER) turn_pair(x[2 * i / V][2 * i % V], x[2 * i / V][2 * i % V + 1], c[i], s[i]);
+        else turn_pair(x[0][i], x[1][i], c[i], s[i]);
+      }
     }
-}
-
-// Cosines and sines of this thread's pairs. pos(axis) gives the token's position.
-struct Turn {
-  float c[16], s[16];
-};
-template <bool MIXED, int D, typename Pos>
-__device__ __forceinline__ void load_turn(const RopeSpec& r, const Lane<D>& l, Pos pos,
-                                          unsigned int* err, Turn& u) {
-  if (!l.turns) return;
-  const size_t width = 2 * static_cast<size_t>(r.n_pairs);
-  auto row = [&](int axis) -> const float* {   // null: a position outside the table
-    const int p = pos(axis);
-    if (p < 0 || p >= r.n_pos) {
-      report_error(err, KASCADE_ERR_BAD_INPUT, 0x541);
-      return nullptr;
-    }
-    return r.table + p * width + 16 * l.t;
-  };
-  if (MIXED) {
-    const float* rows[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) rows[i] = i < r.n_axes ? row(i) : nullptr;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int axis = r.axis[16 * l.t + i];
-      const float* p = axis == 0 ? rows[0] : axis == 1 ? rows[1] : axis == 2 ? rows[2] : rows[3];
-      u.c[i] = p != nullptr ? __ldg(p + i) : 1.f;
-      u.s[i] = p != nullptr ? __ldg(p + r.n_pairs + i) : 0.f;
-    }
-  } else {
-    const float* p = row(r.axis[0]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 c = p != nullptr ? __ldg(reinterpret_cast<const float4*>(p) + i)
-                                    : make_float4(1.f, 1.f, 1.f, 1.f);
-      const float4 s = p != nullptr ? __ldg(reinterpret_cast<const float4*>(p + r.n_pairs) + i)
-                                    : make_float4(0.f, 0.f, 0.f, 0.f);
-      u.c[4 * i] = c.x, u.c[4 * i + 1] = c.y, u.c[4 * i + 2] = c.z, u.c[4 * i + 3] = c.w;
-      u.s[4 * i] = s.x, u.s[4 * i + 1] = s.y, u.s[4 * i + 2] = s.z, u.s[4 * i + 3] = s.w;
+    if (h < h1) {
+      T* row = dst(h);
+      *reinterpret_cast<uint4*>(row + l.at[0]) = packed(x[0]);
+      *reinterpret_cast<uint4*>(row + l.at[1]) = packed(x[1]);
     }
   }
 }
 
-// x / rms(row) * w; all lanes of the warp.
-template <typename T, int D>
-__device__ __forceinline__ void normalise(float (&x)[32], const T* w, const Lane<D>& l, float eps) {
-  float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int i = 0; i < 32; ++i) part[i & 3] = fmaf(x[i], x[i], part[i & 3]);
-  float ss = (part[0] + part[1]) + (part[2] + part[3]);
-#pragma unroll
-  for (int off = 1; off < Lane<D>::kPerRow; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
-  const float r = rsqrtf(ss * (1.f / D) + eps);
-  Raw<T> raw;
-  raw.load(w, l.at, true);
-  float g[32];
-  raw.get(g);
-#pragma unroll
-  for (int i = 0; i < 32; ++i) x[i] = x[i] * r * g[i];
-}
-
-template <bool INTER, int D>
-__device__ __forceinline__ void turn(float (&x)[32], const Turn& u, const Lane<D>& l) {
-  if (!l.turns) return;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    constexpr int kA = INTER ? 2 : 1, kB = INTER ? 1 : 16;
-    float& xa = x[kA * i];
-    float& xb = x[kA * i + kB];
-    const float a = xa, b = xb;
-    xa = __fsub_rn(__fmul_rn(a, u.c[i]), __fmul_rn(b, u.s[i]));
-    xb = __fadd_rn(__fmul_rn(b, u.c[i]), __fmul_rn(a, u.s[i]));
-  }
-}
-
-// ------------------------------------------------------------- q and k rows --
-// A warp has one token and `per` heads of its list of q and k heads, kSlots of
-// them at a time.
 template <typename T, int D, bool INTER, bool MIXED>
-__global__ void __launch_bounds__(kThreads) k_qk_rope(const __grid_constant__ RopeRowArgs a) {
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+    k_qk_rope(const __grid_constant__ RopeRowArgs a) {
   pdl_wait();
   pdl_trigger();
   const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
@@ -187,46 +206,22 @@ __global__ void __launch_bounds__(kThreads) k_qk_rope(const __grid_constant__ Ro
   if (token >= static_cast<int64_t>(a.B) * a.N) return;
   const int part = static_cast<int>(unit - token * a.splits);
   const int b = static_cast<int>(token / a.N), n = static_cast<int>(token - static_cast<int64_t>(b) * a.N);
-  const Lane<D> l(a.rope);
-  const int total = a.H[0] + a.H[1], h1 = min(total, (part + 1) * a.per);
   const int64_t plane = static_cast<int64_t>(a.B) * a.N;
-  Turn u;
-  Raw<T> raw;
-  auto load = [&](int h) {
-    const int which = h >= a.H[0] ? 1 : 0;
-    const int64_t* st = a.src_stride[which];
-    const T* row = static_cast<const T*>(a.src[which]) + b * st[0] + n * st[1] +
-                   (h - (which ? a.H[0] : 0)) * st[2];
-    raw.load(row, l.at, h < h1);
-  };
-  int h = part * a.per + l.slot;
-  load(h);
-  load_turn<MIXED>(a.rope, l, [&](int axis) { return __ldg(a.positions + axis * plane + token); },
-                   a.err, u);
-  for (int h0 = part * a.per; h0 < h1; h0 += Lane<D>::kSlots, h += Lane<D>::kSlots) {
-    float x[32];
-    raw.get(x);
-    if (h0 + Lane<D>::kSlots < h1) load(h + Lane<D>::kSlots);
-    const int which = h >= a.H[0] ? 1 : 0;
-    const T* w = static_cast<const T*>(a.weight[which]);
-    if (a.weight[0] != nullptr || a.weight[1] != nullptr) {
-      float y[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) y[i] = x[i];
-      normalise<T, D>(y, w != nullptr ? w : static_cast<const T*>(a.weight[1 - which]), l,
-                      a.rope.eps);
-      if (w != nullptr)
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = y[i];
-    }
-    turn<INTER, D>(x, u, l);
-    if (h < h1) {
-      const int64_t* st = a.dst_stride[which];
-      store_row(static_cast<T*>(a.dst[which]) + b * st[0] + n * st[1] +
-                    (h - (which ? a.H[0] : 0)) * st[2],
-                l.at, x);
-    }
-  }
+  // q's head 0, and what would be k's if its heads were counted from q's first one
+  const T* q = static_cast<const T*>(a.src[0]) + b * a.src_stride[0][0] + n * a.src_stride[0][1];
+  const T* k = static_cast<const T*>(a.src[1]) + b * a.src_stride[1][0] + n * a.src_stride[1][1] -
+               a.H[0] * a.src_stride[1][2];
+  T* q_to = static_cast<T*>(a.dst[0]) + b * a.dst_stride[0][0] + n * a.dst_stride[0][1];
+  T* k_to = static_cast<T*>(a.dst[1]) + b * a.dst_stride[1][0] + n * a.dst_stride[1][1] -
+            a.H[0] * a.dst_stride[1][2];
+  const int h0 = part * a.per;
+  turn_rows<T, D, INTER, MIXED>(
+      a.rope, h0, min(a.H[0] + a.H[1], h0 + a.per),
+      [&](int h) { return h < a.H[0] ? q + h * a.src_stride[0][2] : k + h * a.src_stride[1][2]; },
+      [&](int h) { return h < a.H[0] ? q_to + h * a.dst_stride[0][2] : k_to + h * a.dst_stride[1][2]; },
+      [&](int h) { return static_cast<const T*>(h < a.H[0] ? a.weight[0] : a.weight[1]); },
+      a.weight[0] != nullptr || a.weight[1] != nullptr,
+      [&](int axis) { return __ldg(a.positions + axis * plane + token); }, a.err);
 }
 
 // ------------------------------------------------------------ cache appends --
@@ -247,46 +242,25 @@ __device__ __forceinline__ int owner_of_row(const int32_t* cu, int n_seqs, int t
   return lo;
 }
 
-template <typename T, int D, bool INTER, bool MIXED>
-__global__ void __launch_bounds__(kThreads)
-    k_qappend_rope(const __grid_constant__ RopeAppendArgs a) {
-  pdl_wait();
-  pdl_trigger();
-  constexpr int kSlots = Lane<D>::kSlots;
-  int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const int64_t q_units = static_cast<int64_t>(a.Tq) * a.q_splits;
-  const Lane<D> l(a.rope);
-  Turn u;
-  if (unit < q_units) {   // queries
-    const int row = static_cast<int>(unit / a.q_splits), part = static_cast<int>(unit % a.q_splits);
-    const int h1 = min(a.Hq, (part + 1) * a.q_per);
-    const T* src = static_cast<const T*>(a.q) + row * a.q_stride[0];
-    T* dst = static_cast<T*>(a.q_out) + row * a.out_stride[0];
-    int h = part * a.q_per + l.slot;
-    Raw<T> raw;
-    raw.load(src + h * a.q_stride[1], l.at, h < h1);
-    load_turn<MIXED>(
-        a.rope, l,
-        [&](int axis) {
-          return a.positions != nullptr ? __ldg(a.positions + static_cast<int64_t>(axis) * a.T + row)
-                                        : max(0, __ldg(a.kv_lens + row) - 1);
-        },
-        a.err, u);
-    for (int h0 = part * a.q_per; h0 < h1; h0 += kSlots, h += kSlots) {
-      float x[32];
-      raw.get(x);
-      if (h0 + kSlots < h1) raw.load(src + (h + kSlots) * a.q_stride[1], l.at, h + kSlots < h1);
-      if (a.weight[0] != nullptr)
-        normalise<T, D>(x, static_cast<const T*>(a.weight[0]), l, a.rope.eps);
-      turn<INTER, D>(x, u, l);
-      if (h < h1) store_row(dst + h * a.out_stride[1], l.at, x);
-    }
-    return;
+// New keys and values: a thread has 32 elements of a row, two blocks of 16 that find
+// their scales alone (blocks as the pieces above: (t, t + n_pairs / 16) or neighbouring
+// ones). Few heads share a token's cosines and sines, which are loaded where they are
+// used instead of held.
+template <typename T>
+__device__ __forceinline__ void load_block(const T* p, float (&x)[16]) {
+  constexpr int V = 16 / sizeof(T);
+#pragma unroll
+  for (int i = 0; i < 16; i += V) {
+    float y[V];
+    unpack(load16(p + i), y);
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[i + j] = y[j];
   }
-  unit -= q_units;
-  const int64_t token = unit / a.kv_splits;
-  if (token >= a.T) return;
-  const int t = static_cast<int>(token), part = static_cast<int>(unit - token * a.kv_splits);
+}
+
+template <typename T, int D, bool INTER, bool MIXED>
+__device__ __forceinline__ void append_rows(const RopeAppendArgs& a, int t, int h0, int h1) {
+  constexpr int kPerRow = D / 32, kSlots = 32 / kPerRow;
   const int slot = a.slot_map[t];
   if (slot < 0) return;
   const int sh = a.bs_shift;
@@ -294,67 +268,115 @@ __global__ void __launch_bounds__(kThreads)
     report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x511);
     return;
   }
-  const int h1 = min(2 * a.Hkv, (part + 1) * a.kv_per);   // K heads, then V heads
-  const T* src[2] = {static_cast<const T*>(a.k) + t * a.k_stride[0],
-                     static_cast<const T*>(a.v) + t * a.v_stride[0]};
-  Raw<T> raw;
-  auto load = [&](int h) {
-    const int which = h >= a.Hkv ? 1 : 0;
-    raw.load(src[which] + (which ? (h - a.Hkv) * a.v_stride[1] : h * a.k_stride[1]), l.at, h < h1);
-  };
-  int h = part * a.kv_per + l.slot;
-  load(h);
-  if (part * a.kv_per < a.Hkv) {
+  const int lane = threadIdx.x & 31, part = lane % kPerRow, groups = a.rope.n_pairs / 16;
+  const bool turns = part < groups, far = turns && !INTER;
+  const int at[2] = {far ? 16 * part : 32 * part, far ? 16 * (part + groups) : 32 * part + 16};
+  const float* rows[4] = {};
+  if (h0 < a.Hkv) {
     int from_plan = 0;
     if (a.positions == nullptr) {
       const int b = owner_of_row(a.cu_new, a.n_seqs, t);
       from_plan = __ldg(a.kv_lens + b) - __ldg(a.cu_new + b + 1) + t;
     }
-    load_turn<MIXED>(
-        a.rope, l,
-        [&](int axis) {
-          return a.positions != nullptr ? __ldg(a.positions + static_cast<int64_t>(axis) * a.T + t)
-                                        : from_plan;
-        },
-        a.err, u);
+    if (turns)
+      table_rows<MIXED>(
+          a.rope,
+          [&](int axis) {
+            return a.positions != nullptr ? __ldg(a.positions + static_cast<int64_t>(axis) * a.T + t)
+                                          : from_plan;
+          },
+          a.err, rows);
   }
   const int r = slot & 15;
   const size_t first = (static_cast<size_t>(slot >> sh) * a.Hkv << (sh - 4)) +
                        ((slot & ((1 << sh) - 1)) >> 4);
-  for (int h0 = part * a.kv_per; h0 < h1; h0 += kSlots, h += kSlots) {
-    float x[32];
-    raw.get(x);
+  for (int g0 = h0; g0 < h1; g0 += kSlots) {
+    const int h = g0 + lane / kPerRow;   // K heads, then V heads
     const bool key = h < a.Hkv;
-    if (h0 + kSlots < h1) load(h + kSlots);
-    if (a.weight[1] != nullptr && h0 < a.Hkv) {
-      float y[32];
-#pragma unroll
-      for (int i = 0; i < 32; ++i) y[i] = x[i];
-      normalise<T, D>(y, static_cast<const T*>(a.weight[1]), l, a.rope.eps);
-      if (key)
-#pragma unroll
-        for (int i = 0; i < 32; ++i) x[i] = y[i];
-    }
-    if (key) turn<INTER, D>(x, u, l);
-    if (h >= h1) continue;
     const int head = key ? h : h - a.Hkv;
+    Row16<float> x[2] = {};
+    if (h < h1) {
+      const T* row = key ? static_cast<const T*>(a.k) + t * a.k_stride[0] + head * a.k_stride[1]
+                         : static_cast<const T*>(a.v) + t * a.v_stride[0] + head * a.v_stride[1];
+      load_block(row + at[0], x[0].x);
+      load_block(row + at[1], x[1].x);
+    }
+    if (a.weight[1] != nullptr && g0 < a.Hkv) {
+      float ss = 0.f;
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ss = fmaf(x[b].x[i], x[b].x[i], ss);
+#pragma unroll
+      for (int off = 1; off < kPerRow; off <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
+      if (key) {
+        const float n = rsqrtf(ss * (1.f / D) + a.rope.eps);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          float g[16];
+          load_block(static_cast<const T*>(a.weight[1]) + at[b], g);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) x[b].x[i] = x[b].x[i] * n * g[i];
+        }
+      }
+    }
+    if (key && turns) {
+#pragma unroll
+      for (int i = 0; i < 16; i += 4) {
+        float c[4], s[4];
+        load_turn4<MIXED>(a.rope, rows, 16 * part + i, c, s);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int k = i + j;
+          if (INTER) turn_pair(x[k / 8].x[2 * k % 16], x[k / 8].x[2 * k % 16 + 1], c[j], s[j]);
+          else turn_pair(x[0].x[k], x[1].x[k], c[j], s[j]);
+        }
+      }
+    }
+    if (h >= h1) continue;
     uint8_t* grp = a.cache + (first + (static_cast<size_t>(head) << (sh - 4))) * (18 * D) +
                    (key ? 0 : 9 * D);
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      Row16<float> y;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) y.x[i] = x[16 * b + i];
-      put16(y, a.unit[key ? 0 : 1], grp + r * (D / 2) + l.at[b] / 2,
-            grp + 8 * D + r * (D / 16) + l.at[b] / 16);
-    }
+    for (int b = 0; b < 2; ++b)
+      put16(x[b], a.unit[key ? 0 : 1], grp + r * (D / 2) + at[b] / 2,
+            grp + 8 * D + r * (D / 16) + at[b] / 16);
   }
+}
+
+template <typename T, int D, bool INTER, bool MIXED>
+__global__ void __launch_bounds__(kThreads, kAppendCtasPerSm)
+    k_qappend_rope(const __grid_constant__ RopeAppendArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const int64_t q_units = static_cast<int64_t>(a.Tq) * a.q_splits;
+  if (unit < q_units) {   // queries
+    const int row = static_cast<int>(unit / a.q_splits), part = static_cast<int>(unit % a.q_splits);
+    const T* src = static_cast<const T*>(a.q) + row * a.q_stride[0];
+    T* dst = static_cast<T*>(a.q_out) + row * a.out_stride[0];
+    const int h0 = part * a.q_per;
+    turn_rows<T, D, INTER, MIXED>(
+        a.rope, h0, min(a.Hq, h0 + a.q_per), [&](int h) { return src + h * a.q_stride[1]; },
+        [&](int h) { return dst + h * a.out_stride[1]; },
+        [&](int) { return static_cast<const T*>(a.weight[0]); }, a.weight[0] != nullptr,
+        [&](int axis) {
+          return a.positions != nullptr ? __ldg(a.positions + static_cast<int64_t>(axis) * a.T + row)
+                                        : max(0, __ldg(a.kv_lens + row) - 1);
+        },
+        a.err);
+    return;
+  }
+  unit -= q_units;
+  const int64_t token = unit / a.kv_splits;
+  if (token >= a.T) return;
+  const int h0 = static_cast<int>(unit - token * a.kv_splits) * a.kv_per;
+  append_rows<T, D, INTER, MIXED>(a, static_cast<int>(token), h0, min(2 * a.Hkv, h0 + a.kv_per));
 }
 
 // Heads of a warp: all of a token's, where there are enough tokens to fill the
 // GPU with `want` warps, else fewer.
 void split_heads(int64_t tokens, int heads, int slots, int& splits, int& per) {
-  constexpr int64_t want = 152 * 16;
+  constexpr int64_t want = 152 * 32;
   const int chunks = (heads + slots - 1) / slots;
   int64_t n = tokens > 0 ? (want + tokens - 1) / tokens : 1;
   if (n > chunks) n = chunks;
@@ -367,7 +389,7 @@ template <typename T, int D>
 cudaError_t launch_qk(const RopeRowArgs& a, cudaStream_t st) {
   RopeRowArgs u = a;
   const int64_t tokens = static_cast<int64_t>(a.B) * a.N;
-  split_heads(tokens, a.H[0] + a.H[1], Lane<D>::kSlots, u.splits, u.per);
+  split_heads(tokens, a.H[0] + a.H[1], Lane<T, D>::kSlots, u.splits, u.per);
   const int64_t ctas = (tokens * u.splits + kWarps - 1) / kWarps;
   if (ctas >= (int64_t(1) << 31)) return cudaErrorNotSupported;
   const dim3 grid(static_cast<unsigned int>(ctas));
@@ -380,8 +402,8 @@ cudaError_t launch_qk(const RopeRowArgs& a, cudaStream_t st) {
 template <typename T, int D>
 cudaError_t launch_append(const RopeAppendArgs& a, cudaStream_t st) {
   RopeAppendArgs u = a;
-  split_heads(a.Tq, a.Hq, Lane<D>::kSlots, u.q_splits, u.q_per);
-  split_heads(a.T, 2 * a.Hkv, Lane<D>::kSlots, u.kv_splits, u.kv_per);
+  split_heads(a.Tq, a.Hq, Lane<T, D>::kSlots, u.q_splits, u.q_per);
+  split_heads(a.T, 2 * a.Hkv, 32 / (D / 32), u.kv_splits, u.kv_per);
   const int64_t warps = static_cast<int64_t>(a.Tq) * u.q_splits + static_cast<int64_t>(a.T) * u.kv_splits;
   const int64_t ctas = (warps + kWarps - 1) / kWarps;
   if (ctas >= (int64_t(1) << 31)) return cudaErrorNotSupported;
@@ -435,6 +457,9 @@ kascade_status check_rope(const kascade_rope* rope, int head_dim, float eps, Rop
     s.axis[i] = static_cast<uint8_t>(rope->axes[i]);
     if (s.axis[i] != s.axis[0]) s.mixed = 1;
   }
+  s.quads = 1;
+  for (int i = 0; i < rope->n_pairs; ++i)
+    if (s.axis[i] != s.axis[i & ~3]) s.quads = 0;
   return KASCADE_OK;
 }
 

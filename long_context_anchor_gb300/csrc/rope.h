@@ -12,6 +12,7 @@ struct RopeSpec {
   const float* table;     // [n_pos][2][n_pairs], or null: nothing is turned
   int n_pos, n_pairs, n_axes, interleaved;
   int mixed;              // pairs of one head follow different axes
+  int quads;              // ... but four neighbouring ones the same
   float eps;
   uint8_t axis[64];
 };
