@@ -794,7 +794,7 @@ QPrefixGeo prefix_geo(int B, int G, int Hkv, int P, int own, int d, int dtype, i
   g.nch = (P + kPfxKeys - 1) / kPfxKeys;
   g.pairs = dtype == KASCADE_F32 ? 0 : tiles / 2;
   g.singles = tiles - 2 * g.pairs;
-  const int least = sms / 16 & ~1, most_runs = (g.nch + kPfxMinRun - 1) / kPfxMinRun;
+  const int least = sms < 32 ? 2 : sms / 16 & ~1, most_runs = (g.nch + kPfxMinRun - 1) / kPfxMinRun;
   double best = 0;
   // runs of the larger kind of unit; the smaller kind's take as long at most
   for (int r = 1; r <= most_runs; ++r) {
@@ -805,7 +805,7 @@ QPrefixGeo prefix_geo(int B, int G, int Hkv, int P, int own, int d, int dtype, i
     const int64_t ctas = static_cast<int64_t>(Hkv) * (static_cast<int64_t>(g.pairs) * r +
                                                       static_cast<int64_t>(g.singles) * single_runs);
     if (r > 1 && ctas > sms - least) break;
-    const int own_sms = ctas > sms - least ? least : (sms - static_cast<int>(ctas)) & ~1;   // whole TPCs
+    const int own_sms = ctas > sms - least ? least : (sms - static_cast<int>(ctas)) & ~1;   // whole TPCs, one at least
     const double t_prefix = start + len * (g.pairs > 0 ? pair : single), t_own = start + rest / own_sms;
     const double t = t_prefix > t_own ? t_prefix : t_own;
     if (r == 1 || t < best) {

@@ -27,7 +27,7 @@ namespace kascade {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 4, kAppendCtasPerSm = 3;   // 64 and 80 registers a thread
+constexpr int kCtasPerSm = 4;   // 64 registers a thread
 
 // ------------------------------------------------------------- q and k rows --
 // A thread has two 16-byte pieces of a row that hold whole pairs: pieces (t, t +
@@ -343,8 +343,8 @@ __device__ __forceinline__ void append_rows(const RopeAppendArgs& a, int t, int 
   }
 }
 
-template <typename T, int D, bool INTER, bool MIXED>
-__global__ void __launch_bounds__(kThreads, kAppendCtasPerSm)
+template <typename T, int D, bool INTER, bool MIXED, int CTAS_PER_SM>
+__global__ void __launch_bounds__(kThreads, CTAS_PER_SM)
     k_qappend_rope(const __grid_constant__ RopeAppendArgs a) {
   pdl_wait();
   pdl_trigger();
@@ -399,6 +399,13 @@ cudaError_t launch_qk(const RopeRowArgs& a, cudaStream_t st) {
   return a.rope.mixed ? go(k_qk_rope<T, D, false, true>) : go(k_qk_rope<T, D, false, false>);
 }
 
+// From this many tokens (those with keys plus those with queries) on, four CTAs of 64
+// registers a thread share an SM, below it three of 80, whose cache rows have more loads
+// in flight. 32 and 8 heads of 128, as many queries as keys: 16384 tokens of each take
+// 70.1 us with four CTAs and 76.3 with three, 4096 take 19.9 and 21.6, 2048 take 10.7 and
+// 11.1, 1024 take 7.1 and 6.5, 512 take 6.3 and 5.1.
+constexpr int64_t kAppendMany = 4096;
+
 template <typename T, int D>
 cudaError_t launch_append(const RopeAppendArgs& a, cudaStream_t st) {
   RopeAppendArgs u = a;
@@ -409,11 +416,15 @@ cudaError_t launch_append(const RopeAppendArgs& a, cudaStream_t st) {
   if (ctas >= (int64_t(1) << 31)) return cudaErrorNotSupported;
   const dim3 grid(static_cast<unsigned int>(ctas));
   auto go = [&](auto kern) { return launch_pdl(kern, grid, dim3(kThreads), 0, st, u); };
-  if (a.rope.interleaved)
-    return a.rope.mixed ? go(k_qappend_rope<T, D, true, true>)
-                        : go(k_qappend_rope<T, D, true, false>);
-  return a.rope.mixed ? go(k_qappend_rope<T, D, false, true>)
-                      : go(k_qappend_rope<T, D, false, false>);
+  const bool many = static_cast<int64_t>(a.T) + a.Tq >= kAppendMany;
+  if (a.rope.interleaved) {
+    if (a.rope.mixed)
+      return many ? go(k_qappend_rope<T, D, true, true, 4>) : go(k_qappend_rope<T, D, true, true, 3>);
+    return many ? go(k_qappend_rope<T, D, true, false, 4>) : go(k_qappend_rope<T, D, true, false, 3>);
+  }
+  if (a.rope.mixed)
+    return many ? go(k_qappend_rope<T, D, false, true, 4>) : go(k_qappend_rope<T, D, false, true, 3>);
+  return many ? go(k_qappend_rope<T, D, false, false, 4>) : go(k_qappend_rope<T, D, false, false, 3>);
 }
 
 inline bool aligned(const void* p, uintptr_t n) {
