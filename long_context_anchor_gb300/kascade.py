@@ -862,7 +862,6 @@ def qcache_plan(kv_lens, new_lens, block_table, free_blocks, free_count, block_s
 
 
 _I64x4 = ctypes.c_int64 * 4
-_I64x8, _I64x12 = ctypes.c_int64 * 8, ctypes.c_int64 * 12
 _ROW_CODES = {torch.bfloat16: (BF16, 8), torch.float32: (F32, 4)}   # code, elements per 16 bytes
 
 
@@ -976,13 +975,28 @@ def _head_strides(t, name, shape, dtype, dev, unit, out=False):
         if t.dtype is not dtype:
             raise TypeError("%s: dtype %s, expected %s" % (name, t.dtype, dtype))
         raise ValueError("%s: on %s, expected %s" % (name, t.device, dev))
-    st = [x if n > 1 else 0 for x, n in zip(t.stride(), shape)]
-    if t.numel():
-        if t.stride(-1) != 1 or any(x % unit for x in st[:-1]) or t.data_ptr() % 16:
-            raise ValueError("%s: rows must be contiguous and start on 16-byte boundaries" % name)
-        if out and any(x == 0 and n > 1 for x, n in zip(st, shape)):
-            raise ValueError("%s: output rows must not overlap" % name)
-    return (0, st[0], st[1]) if len(shape) == 3 else (st[0], st[2], st[1])
+    rows, apart, st = _layout(t.shape, t.stride(), unit)
+    if not rows or t.data_ptr() % 16 and t.numel():
+        raise ValueError("%s: rows must be contiguous and start on 16-byte boundaries" % name)
+    if out and not apart:
+        raise ValueError("%s: output rows must not overlap" % name)
+    return st
+
+
+@functools.lru_cache(maxsize=256)
+def _layout(shape, strides, unit):
+    """Whether rows of these strides are contiguous and whole units apart, whether
+    none is another's, and the strides of _head_strides."""
+    st = [x if n > 1 else 0 for x, n in zip(strides, shape)]
+    empty = 0 in shape
+    rows = empty or strides[-1] == 1 and not any(x % unit for x in st[:-1])
+    apart = empty or not any(x == 0 and n > 1 for x, n in zip(st, shape))
+    return rows, apart, (0, st[0], st[1]) if len(shape) == 3 else (st[0], st[2], st[1])
+
+
+@functools.lru_cache(maxsize=256)
+def _strides_array(*strides):
+    return (ctypes.c_int64 * len(strides))(*strides)
 
 
 def _same_place(src, out, name):
@@ -1051,19 +1065,19 @@ def qk_norm_rope(q, k=None, positions=None, rope=None, q_weight=None, k_weight=N
             return qk_norm_rope(q, k, positions, rope, q_weight, k_weight, eps, interleaved, axes,
                                 q_out, k_out, ws)
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        q_out = q.new_empty(q.shape)
         qo_st = (0, Hq * d, d) if q.dim() == 3 else (Hq * N * d, d, N * d)
     ko_st = (0, 0, 0) if k is None else ko_st if k_out is not None else \
         (0, Hkv * d, d) if k.dim() == 3 else (Hkv * N * d, d, N * d)
     if k is not None and k_out is None:
-        k_out = torch.empty(k.shape, dtype=q.dtype, device=dev)
+        k_out = k.new_empty(k.shape)
     buf = _qws(ws, dev, index, 256)
     _check(_lib.kascade_qk_norm_rope(None if desc is None else ctypes.byref(desc), B, N, Hq, Hkv,
                                      d, code, q.data_ptr(), None if k is None else k.data_ptr(),
                                      wq, wk, float(eps),
                                      None if positions is None else positions.data_ptr(),
                                      q_out.data_ptr(), None if k is None else k_out.data_ptr(),
-                                     _I64x12(*strides, *kst, *qo_st, *ko_st), buf.data_ptr(),
+                                     _strides_array(*strides, *kst, *qo_st, *ko_st), buf.data_ptr(),
                                      buf.numel(), _raw_stream(index)), "kascade_qk_norm_rope")
     return q_out, k_out
 
@@ -1123,11 +1137,11 @@ def qcache_append_rope(k, v, slot_map, pages, rope, positions=None, q=None, cu_n
                                       q_weight, k_weight, eps, interleaved, axes, k_scale, v_scale,
                                       q_out, ws)
     if q is not None and q_out is None:
-        q_out = torch.empty(q.shape, dtype=k.dtype, device=dev)
+        q_out = q.new_empty(q.shape)
     buf = _qws(ws, dev, index, 256)
     addr = lambda t: None if t is None else t.data_ptr()
     _check(_lib.kascade_qcache_append_rope(geo, ctypes.byref(desc), Hq, hkv, d, code, k.data_ptr(),
-                                           v.data_ptr(), addr(q), _I64x8(kt, kh, vt, vh, *st), wk,
+                                           v.data_ptr(), addr(q), _strides_array(kt, kh, vt, vh, *st), wk,
                                            wq, float(eps), slot_map.data_ptr(), T, addr(positions),
                                            addr(cu_new), addr(kv_lens), B, pages.data_ptr(),
                                            addr(q_out), buf.data_ptr(), buf.numel(),
