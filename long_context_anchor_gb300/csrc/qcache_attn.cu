@@ -309,7 +309,7 @@ __device__ __forceinline__ void attend(QState<D>& st, const uint64_t (&t)[kStepO
     const float al0 = ex2(st.m[0] - x0), al1 = ex2(st.m[1] - x1);
     st.m[0] = x0;
     st.m[1] = x1;
-    st.nmu = f2_pack(kPShift - x0, kPShift - x1);
+    st.nmu = f2_pack(below_shift(x0), below_shift(x1));
     st.l = f2_mul(st.l, f2_pack(al0, al1));
 #pragma unroll
     for (int i = 0; i < D / 16; ++i) {

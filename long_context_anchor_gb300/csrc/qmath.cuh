@@ -18,6 +18,13 @@ constexpr int kPShift = 14;          // weights are held as 2^14 p
 // The running maximum is a reference, not the maximum itself: it is raised once
 // a score passes it by more than this (weights then reach 2^15.75, within fp16).
 constexpr float kSlack = 1.75f;
+// kPShift - m for the weights' exponents. From |m| = 2^25 on 14 is less than a few steps
+// of m's type, and the difference to the nearest could make the weight at m 2^16, which
+// fp16 does not hold; there it is rounded down (weights at m are then 2^0 to 2^14).
+__device__ __forceinline__ float below_shift(float m) {
+  const float x = kPShift - m;
+  return x + m > kPShift + kSlack ? __fsub_rd(static_cast<float>(kPShift), m) : x;
+}
 constexpr int kQExp = 12;            // q's largest element is scaled to [2^12, 2^13)
 // the four bytes of w, each two e2m1 codes, as pairs of fp16 (low half first)
 __device__ __forceinline__ void cvt_e2m1x8(uint32_t w, uint32_t (&h)[4]) {
