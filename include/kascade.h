@@ -496,6 +496,10 @@ kascade_status kascade_qcache_dense_decode(const kascade_desc* desc, const kasca
  * Over kascade_qcache_plan a sequence of such a batch starts with kv_lens[b] =
  * prefix_len and its row's first entries set, and ends with new_lens[b] =
  * prefix_len - kv_lens[b], which gives back its own blocks alone.
+ * Weights of the prefix are multiples of 2^-28 (bf16) or 2^-32 (fp32) of the
+ * row's largest one at most. How the SMs are shared out goes by prefix_len and
+ * desc->kv_len - prefix_len, not by the lengths (they are not known to the
+ * host), so kv_len is best given as the longest length in use.
  * Workspace: kascade_qcache_prefix_workspace_size. */
 size_t kascade_qcache_prefix_workspace_size(const kascade_desc* desc, const kascade_qcache* cache,
                                             int32_t prefix_len);

@@ -12,7 +12,26 @@
 // terms) for the product and summed unrounded. So the reference moves in a
 // part's first chunk and then rarely: raising it for any row of a warp rescales
 // 32 rows of O in TMEM, and looking for the maximum costs a fifth of a chunk's
-// arithmetic.
+// arithmetic. The weights' fp16 steps are 2^-24, so 2^-28 (bf16) or 2^-32 (fp32) of a
+// reference's weight.
+//
+//   k_qdecode_dense  (qcache_attn.cu) leaves each sequence's state over its own keys
+//   k_qprefix        beside it on other SMs: the prefix, a run of chunks per CTA
+//   k_qprefix_join   both, and the tables' check
+//
+// Measured (bf16, one launch sequence in a graph): 16 sequences x 64 heads over 131072
+// keys at d = 64 57.8 us (595 TFLOP/s of the products, 1.3 TB/s of pages), 128 x 32 heads
+// over 32768 at d = 128 86.8 us (791 TFLOP/s), 32 x 32 heads over 8192 with 1024 own keys
+// each 29.3 us; one by one, as the dense call does it, 218, 810 and 66.5 us. A chunk takes
+// an SM 740 cycles at d = 64, two tiles of one 1770 at d = 128. What bounds it is a chunk's
+// way round with two score buffers: 1500 cycles of softmax (830 of arithmetic beside the
+// other warps', 400 of a TMEM load) and as many from the weights to the next scores in
+// their place (product, its wait, scores, five waits of 100 cycles); the issue slots are
+// 50 to 60% full, tensor cores busy 30% (d = 64) and 50% (d = 128, where the scores read Q
+// from shared memory, as TMEM is full). About 9 us of a launch are its start and end.
+// Slower: two warps per 32 rows with half of the keys each (61.5, 91 us), the next
+// chunk's load begun before this one's end (63, 91), scores and products issued by
+// warps of their own (65, 103), one arrival per warp for the weights (58.7, 87.9).
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>

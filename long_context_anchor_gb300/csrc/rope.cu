@@ -13,6 +13,14 @@
 // compiler or a plain program makes of it: the 4-bit codes behind it depend on
 // every bit. The pages describe no rotation; a Kascade layer's q and k are
 // the rotated ones.
+//
+// Both are bound by memory where they are large. Rows of 16384 tokens, 32 + 8 heads of
+// 128, bf16 with norm: 60.2 us, 5.7 TB/s (issue slots 70% full); 131072 tokens, 64 + 8
+// heads of 64, half turned: 399 us, 6.1 TB/s; 2 x 5003 tokens, 16 + 4 heads of 64 in fp32
+// on three axes: 23.8 us, 4.4 TB/s, start and end among it. Into the cache with queries,
+// 16384 tokens, 32 + 8 heads: 70 us, 5.0 TB/s (issue 54%, loads waited for 7 issues each: a
+// warp has few rows in flight in 64 registers). A step's few rows take 2.3 and 3.4 us, a
+// launch's latency.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
