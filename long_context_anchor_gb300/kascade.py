@@ -999,6 +999,14 @@ def _strides_array(*strides):
     return (ctypes.c_int64 * len(strides))(*strides)
 
 
+_NO_ROWS = (0, 0, 0)
+
+
+def _packed(t, shape):
+    """A new contiguous tensor like t (empty_like costs half of new_empty)."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(shape)
+
+
 def _same_place(src, out, name):
     """An output may be the input itself, not the same memory in another order."""
     if out is not None and out.data_ptr() == src.data_ptr() and out.stride() != src.stride() \
@@ -1027,37 +1035,37 @@ def qk_norm_rope(q, k=None, positions=None, rope=None, q_weight=None, k_weight=N
     q and k themselves too)."""
     if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
         raise ValueError("q: expected a tensor [T,Hq,d] or [B,Hq,N,d]")
-    if q.dtype not in _ROW_CODES:
+    shape, dtype = q.shape, q.dtype
+    if dtype not in _ROW_CODES:
         raise TypeError("q: expected a bfloat16 or float32 tensor")
     dev = _cuda(q, "q")
-    code, unit = _ROW_CODES[q.dtype]
-    d = q.shape[-1]
-    if q.dim() == 3:
-        B, (N, Hq) = 1, q.shape[:2]
+    code, unit = _ROW_CODES[dtype]
+    if len(shape) == 3:
+        B, (N, Hq, d) = 1, shape
         lead = (N,)
     else:
-        B, Hq, N = q.shape[:3]
+        B, Hq, N, d = shape
         lead = (B, N)
-    strides = _head_strides(q, "q", q.shape, q.dtype, dev, unit)
-    Hkv, kst = 0, (0, 0, 0)
+    strides = _head_strides(q, "q", shape, dtype, dev, unit)
+    Hkv, kst, ko_st = 0, _NO_ROWS, _NO_ROWS
     if k is not None:
-        if not isinstance(k, torch.Tensor) or k.dim() != q.dim():
+        if not isinstance(k, torch.Tensor) or k.dim() != len(shape):
             raise ValueError("k: expected a tensor with q's axes")
         Hkv = k.shape[1]
-        kst = _head_strides(k, "k", (N, Hkv, d) if q.dim() == 3 else (B, Hkv, N, d), q.dtype, dev,
-                            unit)
+        k_shape = (N, Hkv, d) if len(shape) == 3 else (B, Hkv, N, d)
+        kst = _head_strides(k, "k", k_shape, dtype, dev, unit)
     elif k_out is not None or k_weight is not None:
         raise ValueError("k_out, k_weight: there is no k")
     if rope is not None and positions is None:
         raise ValueError("rope needs positions")
     desc = _rope(rope, interleaved, axes, positions, lead, dev)
-    wq = _weight(q_weight, "q_weight", d, q.dtype, dev)
-    wk = _weight(k_weight, "k_weight", d, q.dtype, dev)
+    wq = _weight(q_weight, "q_weight", d, dtype, dev)
+    wk = _weight(k_weight, "k_weight", d, dtype, dev)
     if q_out is not None:
-        qo_st = _head_strides(q_out, "q_out", q.shape, q.dtype, dev, unit, out=True)
+        qo_st = _head_strides(q_out, "q_out", shape, dtype, dev, unit, out=True)
         _same_place(q, q_out, "q_out")
     if k_out is not None:
-        ko_st = _head_strides(k_out, "k_out", k.shape, q.dtype, dev, unit, out=True)
+        ko_st = _head_strides(k_out, "k_out", k_shape, dtype, dev, unit, out=True)
         _same_place(k, k_out, "k_out")
     index = q.get_device()
     if _elsewhere(index, stream):
@@ -1065,20 +1073,20 @@ def qk_norm_rope(q, k=None, positions=None, rope=None, q_weight=None, k_weight=N
             return qk_norm_rope(q, k, positions, rope, q_weight, k_weight, eps, interleaved, axes,
                                 q_out, k_out, ws)
     if q_out is None:
-        q_out = q.new_empty(q.shape)
-        qo_st = (0, Hq * d, d) if q.dim() == 3 else (Hq * N * d, d, N * d)
-    ko_st = (0, 0, 0) if k is None else ko_st if k_out is not None else \
-        (0, Hkv * d, d) if k.dim() == 3 else (Hkv * N * d, d, N * d)
+        q_out = _packed(q, shape)
+        qo_st = (0, Hq * d, d) if len(shape) == 3 else (Hq * N * d, d, N * d)
     if k is not None and k_out is None:
-        k_out = k.new_empty(k.shape)
+        k_out = _packed(k, k_shape)
+        ko_st = (0, Hkv * d, d) if len(shape) == 3 else (Hkv * N * d, d, N * d)
     buf = _qws(ws, dev, index, 256)
     _check(_lib.kascade_qk_norm_rope(None if desc is None else ctypes.byref(desc), B, N, Hq, Hkv,
                                      d, code, q.data_ptr(), None if k is None else k.data_ptr(),
                                      wq, wk, float(eps),
                                      None if positions is None else positions.data_ptr(),
                                      q_out.data_ptr(), None if k is None else k_out.data_ptr(),
-                                     _strides_array(*strides, *kst, *qo_st, *ko_st), buf.data_ptr(),
-                                     buf.numel(), _raw_stream(index)), "kascade_qk_norm_rope")
+                                     _strides_array(*strides, *kst, *qo_st, *ko_st),
+                                     buf.data_ptr(), buf.numel(), _raw_stream(index)),
+           "kascade_qk_norm_rope")
     return q_out, k_out
 
 
@@ -1094,11 +1102,12 @@ def qcache_append_rope(k, v, slot_map, pages, rope, positions=None, q=None, cu_n
     nb, hkv, bs, d = _pages(pages)
     dev = _cuda(pages, "pages")
     T = _slots(slot_map, dev)
-    if not isinstance(k, torch.Tensor) or k.dtype not in _ROW_CODES:
+    dtype = k.dtype if isinstance(k, torch.Tensor) else None
+    if dtype not in _ROW_CODES:
         raise TypeError("k: expected a bfloat16 or float32 tensor")
-    code, unit = _ROW_CODES[k.dtype]
-    kt, kh = _row_strides(k, "k", (T, hkv, d), k.dtype, dev, unit)
-    vt, vh = _row_strides(v, "v", (T, hkv, d), k.dtype, dev, unit)
+    code, unit = _ROW_CODES[dtype]
+    kt, kh = _row_strides(k, "k", (T, hkv, d), dtype, dev, unit)
+    vt, vh = _row_strides(v, "v", (T, hkv, d), dtype, dev, unit)
     planned = cu_new is not None or kv_lens is not None
     if planned == (positions is not None):
         raise ValueError("give positions, or cu_new and kv_lens")
@@ -1112,17 +1121,17 @@ def qcache_append_rope(k, v, slot_map, pages, rope, positions=None, q=None, cu_n
         _fits(kv_lens, "kv_lens", (B,), torch.int32, dev)
         _fits(cu_new, "cu_new", (B + 1,), torch.int32, dev)
     desc = _rope(rope, interleaved, axes, positions, (T,), dev)
-    wq = _weight(q_weight, "q_weight", d, k.dtype, dev)
-    wk = _weight(k_weight, "k_weight", d, k.dtype, dev)
+    wq = _weight(q_weight, "q_weight", d, dtype, dev)
+    wk = _weight(k_weight, "k_weight", d, dtype, dev)
     Hq, st = 0, (0, 0, 0, 0)
     if q is not None:
         if not isinstance(q, torch.Tensor) or q.dim() != 3:
             raise ValueError("q: expected a tensor [T,Hq,d], or [B,Hq,d] with kv_lens")
         Hq = q.shape[1]
         shape = (B if planned else T, Hq, d)
-        st = _head_strides(q, "q", shape, k.dtype, dev, unit)[1:]
+        st = _head_strides(q, "q", shape, dtype, dev, unit)[1:]
         if q_out is not None:
-            st += _head_strides(q_out, "q_out", shape, k.dtype, dev, unit, out=True)[1:]
+            st += _head_strides(q_out, "q_out", shape, dtype, dev, unit, out=True)[1:]
             _same_place(q, q_out, "q_out")
         else:
             st += (Hq * d, d)
@@ -1137,7 +1146,7 @@ def qcache_append_rope(k, v, slot_map, pages, rope, positions=None, q=None, cu_n
                                       q_weight, k_weight, eps, interleaved, axes, k_scale, v_scale,
                                       q_out, ws)
     if q is not None and q_out is None:
-        q_out = q.new_empty(q.shape)
+        q_out = _packed(q, q.shape)
     buf = _qws(ws, dev, index, 256)
     addr = lambda t: None if t is None else t.data_ptr()
     _check(_lib.kascade_qcache_append_rope(geo, ctypes.byref(desc), Hq, hkv, d, code, k.data_ptr(),
