@@ -492,22 +492,26 @@ kascade_status kascade_qcache_dense_decode(const kascade_desc* desc, const kasca
  * prefix_len/block_size entries. The prefix is read, and its products are
  * taken, once for all of them; a shorter sequence (a padding row of length 0
  * too) is attended to on its own, whatever its blocks. Entries that differ set
- * KASCADE_ERR_BAD_INPUT on the device, and the lowest such sequence's count.
+ * KASCADE_ERR_BAD_INPUT on the device; the sequence's own ones are used then, or
+ * those of the lowest sequence that holds the prefix.
  * Over kascade_qcache_plan a sequence of such a batch starts with kv_lens[b] =
  * prefix_len and its row's first entries set, and ends with new_lens[b] =
  * prefix_len - kv_lens[b], which gives back its own blocks alone.
  * Weights of the prefix are multiples of 2^-28 (bf16) or 2^-32 (fp32) of the
  * row's largest one at most. How the SMs are shared out goes by prefix_len and
  * desc->kv_len - prefix_len, not by the lengths (they are not known to the
- * host), so kv_len is best given as the longest length in use.
+ * host), so kv_len is best given as the longest length in use. So does whether
+ * it is done at all: with `always` 0 a batch that sharing is not reckoned to
+ * help (few sequences, a short prefix) is attended to one by one, with the same
+ * check of the tables; with 1 the prefix is shared whatever it costs.
  * Workspace: kascade_qcache_prefix_workspace_size. */
 size_t kascade_qcache_prefix_workspace_size(const kascade_desc* desc, const kascade_qcache* cache,
                                             int32_t prefix_len);
 kascade_status kascade_qcache_prefix_decode(const kascade_desc* desc, const kascade_qcache* cache,
                                             const void* q, const void* pages,
                                             const int32_t* block_table, const int32_t* kv_lens,
-                                            int32_t prefix_len, void* out, void* ws,
-                                            size_t ws_bytes, void* stream);
+                                            int32_t prefix_len, int32_t always, void* out,
+                                            void* ws, size_t ws_bytes, void* stream);
 
 /* Anchor layer (as kascade_anchor_decode, both index modes): the exact output
  * and the exact Top-k of every row, min(topk, kv_lens[b]) ascending positions

@@ -36,6 +36,7 @@ constexpr int kPfxMinRun = 4;             // chunks of a run at least
 struct QPrefixGeo {
   int nch, pairs, singles, pair_runs, single_runs, pair_len, single_len, ctas;
   int own_sms;   // for the sequences' own parts, which run beside the prefix
+  bool alone;    // not worth it: every sequence on its own
 };
 QPrefixGeo prefix_geo(int B, int G, int Hkv, int P, int own, int d, int dtype, int sms);
 // A piece: o [rows][d], m [rows], l [rows].
@@ -64,6 +65,7 @@ struct QPrefixArgs {
   int16_t heads[kMaxQHeads];
 };
 cudaError_t launch_qprefix(const QPrefixArgs& a, int head_dim, int dtype, cudaStream_t st);
+cudaError_t launch_qprefix_check(const QPrefixArgs& a, cudaStream_t st);   // of the tables alone
 
 struct QDecodeArgs {
   const void* q;              // [B,Hq,d] bf16 or fp32

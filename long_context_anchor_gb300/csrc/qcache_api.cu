@@ -536,12 +536,13 @@ size_t kascade_qcache_prefix_workspace_size(const kascade_desc* desc, const kasc
 kascade_status kascade_qcache_prefix_decode(const kascade_desc* desc, const kascade_qcache* cache,
                                             const void* q, const void* pages,
                                             const int32_t* block_table, const int32_t* kv_lens,
-                                            int32_t prefix_len, void* out, void* ws,
-                                            size_t ws_bytes, void* stream) {
+                                            int32_t prefix_len, int32_t always, void* out,
+                                            void* ws, size_t ws_bytes, void* stream) {
   QCall k;
   kascade_status r = check_call(desc, cache, k);
   if (r != KASCADE_OK) return r;
   if ((r = check_prefix(k, prefix_len)) != KASCADE_OK) return r;
+  if (always != 0 && always != 1) return KASCADE_ERR_INVALID_ARG;
   if ((r = check_attn_ptrs(q, pages, block_table, kv_lens, out)) != KASCADE_OK) return r;
   k.L = prefix_layout(k.s, prefix_len);
   if (!aligned(ws, 256) || ws_bytes < k.L.total) return KASCADE_ERR_WORKSPACE;
@@ -577,6 +578,12 @@ kascade_status kascade_qcache_prefix_decode(const kascade_desc* desc, const kasc
   x.scale = a.scale;
   x.geo = prefix_geo(k.s.B, k.s.G, k.s.Hkv, prefix_len, k.s.N - prefix_len, k.s.d, k.s.dtype,
                      sm_count());
+  if (x.geo.alone && always == 0) {
+    if ((r = run_qdense(k, q, pages, block_table, kv_lens, out, nullptr, false, nullptr, ws, st)) !=
+        KASCADE_OK)
+      return r;
+    return status_of(launch_qprefix_check(x, st));
+  }
   a.max_ctas = x.geo.own_sms;
   memcpy(x.heads, a.heads, sizeof(x.heads));
   // the own parts' states, then the prefix's pieces, then both joined

@@ -19,6 +19,9 @@
 //   k_qprefix        beside it on other SMs: the prefix, a run of chunks per CTA
 //   k_qprefix_join   both, and the tables' check
 //
+// or, where that is not reckoned to help (prefix_geo), the dense call's kernel and
+//   k_qprefix_check  the tables' check alone
+//
 // Measured (bf16, one launch sequence in a graph): 16 sequences x 64 heads over 131072
 // keys at d = 64 57.8 us (595 TFLOP/s of the products, 1.3 TB/s of pages), 128 x 32 heads
 // over 32768 at d = 128 86.8 us (791 TFLOP/s), 32 x 32 heads over 8192 with 1024 own keys
@@ -685,9 +688,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
 
 // Every row's pieces and its own part's state joined into the output: D / 4 threads
 // per row and worker, `workers` of them per row, which take the row's pieces in turn
-// and are joined in order. The last `checkers` CTAs look for sequences whose tables
-// name other blocks than the lowest one's.
+// and are joined in order. The last `checkers` CTAs check the tables.
 constexpr int kJoinThreads = 256;
+
+// Sequences whose tables name other blocks than the lowest one's; this CTA's share of
+// `ctas`: a warp has kCheck entries of one sequence at a time (all threads).
+constexpr int kCheck = 256;
+__device__ __forceinline__ void check_tables(const QPrefixArgs& a, int& s_src, int cta, int ctas) {
+  if (threadIdx.x == 0) s_src = a.B;
+  __syncthreads();
+  first_holder(a, s_src);
+  const int src = s_src, front = a.P >> a.bs_shift, pieces = (front + kCheck - 1) / kCheck;
+  const int32_t* ids = a.table + static_cast<size_t>(src) * a.max_blocks;
+  const int64_t units = static_cast<int64_t>(a.B - src - 1) * pieces;   // none: -1
+  for (int64_t u = static_cast<int64_t>(cta) * (kJoinThreads / 32) + (threadIdx.x >> 5); u < units;
+       u += static_cast<int64_t>(ctas) * (kJoinThreads / 32)) {
+    const int b = src + 1 + static_cast<int>(u / pieces), j0 = static_cast<int>(u % pieces) * kCheck;
+    if (pfx_start(a.lens, b, a.P, a.N, a.max_blocks, a.bs_shift) == 0) continue;
+    bool other = false;
+#pragma unroll
+    for (int i = 0; i < kCheck; i += 32) {
+      const int j = j0 + i + static_cast<int>(threadIdx.x & 31);
+      if (j < front) other |= a.table[static_cast<size_t>(b) * a.max_blocks + j] != ids[j];
+    }
+    if (other) report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x551);
+  }
+}
+
+// The check alone, beside the dense call's kernel (what it reads that kernel has waited
+// for; its end is waited for here for the sake of what comes behind).
+__global__ void __launch_bounds__(kJoinThreads) k_qprefix_check(const __grid_constant__ QPrefixArgs a) {
+  __shared__ int s_src;
+  pdl_trigger();
+  check_tables(a, s_src, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
+  pdl_wait();
+}
+
 template <int D, bool F32>
 __global__ void __launch_bounds__(kJoinThreads) k_qprefix_join(const __grid_constant__ QPrefixArgs a,
                                                                int workers, int checkers) {
@@ -698,18 +734,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_qprefix_join(const __grid_cons
   __shared__ int s_src;
   const int joiners = static_cast<int>(gridDim.x) - checkers;
   if (static_cast<int>(blockIdx.x) >= joiners) {
-    if (threadIdx.x == 0) s_src = a.B;
-    __syncthreads();
-    first_holder(a, s_src);
-    const int src = s_src, front = a.P >> a.bs_shift;
-    const int32_t* ids = a.table + static_cast<size_t>(src) * a.max_blocks;
-    for (int b = src + 1 + static_cast<int>(blockIdx.x) - joiners; b < a.B; b += checkers) {
-      if (pfx_start(a.lens, b, a.P, a.N, a.max_blocks, a.bs_shift) == 0) continue;
-      bool other = false;
-      for (int j = threadIdx.x; j < front; j += kJoinThreads)
-        other |= a.table[static_cast<size_t>(b) * a.max_blocks + j] != ids[j];
-      if (other) report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x551);
-    }
+    check_tables(a, s_src, static_cast<int>(blockIdx.x) - joiners, checkers);
     return;
   }
   const int group = threadIdx.x / kLanes, e4 = threadIdx.x % kLanes;
@@ -772,6 +797,13 @@ __global__ void __launch_bounds__(kJoinThreads) k_qprefix_join(const __grid_cons
         make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
 }
 
+// CTAs that check the tables.
+int checkers_of(const QPrefixArgs& a) {
+  const int front = a.P >> a.bs_shift, pieces = (front + kCheck - 1) / kCheck;
+  const int64_t ctas = (static_cast<int64_t>(a.B) * pieces + kJoinThreads / 32 - 1) / (kJoinThreads / 32);
+  return ctas < 256 ? static_cast<int>(ctas) : 256;
+}
+
 template <int D, bool F32>
 cudaError_t launch_join_t(const QPrefixArgs& a, cudaStream_t st) {
   // pieces of a row at most, eight of them per worker
@@ -780,7 +812,7 @@ cudaError_t launch_join_t(const QPrefixArgs& a, cudaStream_t st) {
   const int workers = pieces > 32 ? 8 : pieces > 16 ? 4 : pieces > 8 ? 2 : 1;
   const int64_t per_cta = kJoinThreads / (D / 4) / workers;
   const int64_t joiners = (static_cast<int64_t>(a.B) * a.Hq + per_cta - 1) / per_cta;
-  const int checkers = a.B < 64 ? a.B : 64;
+  const int checkers = checkers_of(a);
   return launch_pdl(k_qprefix_join<D, F32>, dim3(static_cast<unsigned int>(joiners + checkers)),
                     dim3(kJoinThreads), 0, st, a, workers, checkers);
 }
@@ -800,14 +832,23 @@ cudaError_t launch_prefix_t(const QPrefixArgs& a, cudaStream_t st) {
 // A unit's runs are as many as finish first together with the sequences' own parts, whose
 // kernel runs beside this one on the SMs that are left (own_sms): one CTA per SM, and
 // a CTA has one run of one unit (a second one would cost its start, its queries
-// and its pieces again, 10 us). Measured: a chunk takes an SM `pair` ns with two tiles
+// and its pieces again, 10 us); units that are more than the SMs have one run and come CTA
+// after CTA. Measured: a chunk takes an SM `pair` ns with two tiles
 // of queries and `single` with one, the own parts' kernel reads 24 bytes a ns on an SM, and
 // each takes about 9 us to start and end. Half of the `own` tokens that a sequence may
 // have are assumed, since the lengths are not known here.
+//
+// `alone`: every sequence on its own (the dense call's kernel), unless sharing is reckoned
+// to be a tenth quicker (a third, where CTAs come after CTAs): 13 us for that kernel's start and end and 36 bytes a ns and SM; 8 us
+// for the join, own parts at 33; 350 ns of an SM for a sequence and KV head either
+// way. Measured, 32 heads on 8, d = 128, bf16 (shared, alone): 32 sequences of 512 + up to
+// 500 tokens 21.1 us, 16.5; of 2048 + 500 23.1, 26.6; 8 of 1024 + 8000 25.7, 18.9; 128 of
+// 1024 + 4000 78.4, 90.6; 2048 of 1024 + 512 299, 552; one of 131072 (64 heads, d = 64) 80, 25.
 QPrefixGeo prefix_geo(int B, int G, int Hkv, int P, int own, int d, int dtype, int sms) {
   const double pair = d == 128 ? 1080 : 850;
   const double single = (d == 128 ? 625 : 440) * (dtype == KASCADE_F32 ? 2 : 1);
-  const double rest = 0.5 * B * Hkv * static_cast<double>(own) * (9 * d / 8) / 24, start = 9000;
+  const double token = static_cast<double>(B) * Hkv * (9 * d / 8), start = 9000;
+  const double rest = 0.5 * token * own / 24, units = 350.0 * B * Hkv;
   QPrefixGeo g{};
   const int tiles = static_cast<int>((static_cast<int64_t>(B) * G + kPfxRows - 1) / kPfxRows);
   g.nch = (P + kPfxKeys - 1) / kPfxKeys;
@@ -815,6 +856,7 @@ QPrefixGeo prefix_geo(int B, int G, int Hkv, int P, int own, int d, int dtype, i
   g.singles = tiles - 2 * g.pairs;
   const int least = sms < 32 ? 2 : sms / 16 & ~1, most_runs = (g.nch + kPfxMinRun - 1) / kPfxMinRun;
   double best = 0;
+  bool best_fits = false;
   // runs of the larger kind of unit; the smaller kind's take as long at most
   for (int r = 1; r <= most_runs; ++r) {
     const int len = (g.nch + r - 1) / r;
@@ -824,20 +866,36 @@ QPrefixGeo prefix_geo(int B, int G, int Hkv, int P, int own, int d, int dtype, i
     const int64_t ctas = static_cast<int64_t>(Hkv) * (static_cast<int64_t>(g.pairs) * r +
                                                       static_cast<int64_t>(g.singles) * single_runs);
     if (r > 1 && ctas > sms - least) break;
-    const int own_sms = ctas > sms - least ? least : (sms - static_cast<int>(ctas)) & ~1;   // whole TPCs, one at least
-    const double t_prefix = start + len * (g.pairs > 0 ? pair : single), t_own = start + rest / own_sms;
-    const double t = t_prefix > t_own ? t_prefix : t_own;
-    if (r == 1 || t < best) {
-      best = t;
-      g.pair_runs = g.pairs > 0 ? r : 1;
-      g.single_runs = single_runs;
-      g.ctas = static_cast<int>(ctas);
-      g.own_sms = own_sms;
+    const double run = start + len * (g.pairs > 0 ? pair : single);
+    // SMs for the own parts: whole TPCs, what the runs leave or, with one run, more
+    const int first = ctas <= sms - least ? (sms - static_cast<int>(ctas)) & ~1 : least;
+    for (int o = first; o < sms && (o == first || r == 1); o += 2) {
+      const double t_prefix = run * static_cast<double>((ctas + sms - o - 1) / (sms - o));
+      const double t_own = start + (rest + units) / o, t = t_prefix > t_own ? t_prefix : t_own;
+      // (CTA after CTA only where it gains much: 16 units and 4000 own tokens take 79 us with
+      // an SM for each unit, 107 with half as many)
+      if (g.own_sms == 0 || t < (ctas > sms - o && best_fits ? 0.75 : 1) * best) {
+        best = t;
+        best_fits = ctas <= sms - o;
+        const double own_parts = start + (rest * 24 / 33 + units) / o;
+        g.alone = 13000 + (token * (P + 0.5 * own) / 36 + units) / sms <
+                  (best_fits ? 1.1 : 1.35) * (8000 + (t_prefix > own_parts ? t_prefix : own_parts));
+        g.pair_runs = g.pairs > 0 ? r : 1;
+        g.single_runs = single_runs;
+        g.ctas = static_cast<int>(ctas);
+        g.own_sms = o;
+      }
     }
   }
   g.pair_len = (g.nch + g.pair_runs - 1) / g.pair_runs;
   g.single_len = (g.nch + g.single_runs - 1) / g.single_runs;
   return g;
+}
+
+cudaError_t launch_qprefix_check(const QPrefixArgs& a, cudaStream_t st) {
+  if (a.B < 2) return cudaSuccess;
+  return launch_pdl(k_qprefix_check, dim3(static_cast<unsigned int>(checkers_of(a))),
+                    dim3(kJoinThreads), 0, st, a);
 }
 
 cudaError_t launch_qprefix(const QPrefixArgs& a, int d, int dtype, cudaStream_t st) {

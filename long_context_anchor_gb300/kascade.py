@@ -108,7 +108,7 @@ _SIGS = {
                                            _vp, _sz, _vp]),
     "kascade_qcache_dense_decode": (ctypes.c_int, [_DP, _QP] + [_vp] * 7 + [_sz, _vp]),
     "kascade_qcache_prefix_workspace_size": (_sz, [_DP, _QP, _i32]),
-    "kascade_qcache_prefix_decode": (ctypes.c_int, [_DP, _QP] + [_vp] * 4 + [_i32] + [_vp] * 2 +
+    "kascade_qcache_prefix_decode": (ctypes.c_int, [_DP, _QP] + [_vp] * 4 + [_i32] * 2 + [_vp] * 2 +
                                      [_sz, _vp]),
     "kascade_qcache_anchor_decode": (ctypes.c_int, [_DP, _QP] + [_vp] * 4 + [_i32] + [_vp] * 4 +
                                      [_sz, _vp]),
@@ -1267,12 +1267,15 @@ def qcache_dense_decode(q, pages, block_table, kv_lens, kv_len=None, group_map=N
 
 
 def qcache_prefix_decode(q, pages, block_table, kv_lens, prefix_len, kv_len=None, group_map=None,
-                         scale=None, k_scale=1.0, v_scale=1.0, out=None, ws=None, stream=None):
+                         scale=None, k_scale=1.0, v_scale=1.0, out=None, ws=None, stream=None,
+                         always=False):
     """qcache_dense_decode for a batch whose sequences begin with the same blocks:
     the first prefix_len tokens (a multiple of the block size) of every sequence
     with kv_lens[b] >= prefix_len are read, and attended to, once for all of them;
     these sequences' rows of block_table have the same first entries. Shorter
-    sequences are attended to on their own."""
+    sequences are attended to on their own, and so are all where sharing is
+    reckoned not to help (from the sizes, kv_len among them), unless always is
+    set."""
     prefix_len = int(prefix_len)
     desc, geo, nbytes, _, dev = _qattn(q, pages, block_table, kv_lens, kv_len, group_map, scale,
                                        k_scale, v_scale, False, 0, out, prefix=prefix_len)
@@ -1280,13 +1283,15 @@ def qcache_prefix_decode(q, pages, block_table, kv_lens, prefix_len, kv_len=None
     if _elsewhere(index, stream):
         with _on(dev, stream, q, pages, block_table, kv_lens, out):
             return qcache_prefix_decode(q, pages, block_table, kv_lens, prefix_len, kv_len,
-                                        group_map, scale, k_scale, v_scale, out, ws)
+                                        group_map, scale, k_scale, v_scale, out, ws,
+                                        always=always)
     o = torch.empty_like(q) if out is None else out
     buf = _qws(ws, dev, index, nbytes)
     _check(_lib.kascade_qcache_prefix_decode(desc, geo, q.data_ptr(), pages.data_ptr(),
                                              block_table.data_ptr(), kv_lens.data_ptr(),
-                                             prefix_len, o.data_ptr(), buf.data_ptr(), buf.numel(),
-                                             _raw_stream(index)), "kascade_qcache_prefix_decode")
+                                             prefix_len, 1 if always else 0, o.data_ptr(),
+                                             buf.data_ptr(), buf.numel(), _raw_stream(index)),
+           "kascade_qcache_prefix_decode")
     return o
 
 

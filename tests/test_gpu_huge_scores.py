@@ -40,7 +40,8 @@ def test_one_key_has_the_weight(K, dtype, d, exponent, prefix):
     best = rng.choice(n, B, replace=False)
     q = dev(kept[best][:, None] * 2.0 ** exponent)
     args = (q, pages, ints(table), ints([n] * B))
-    got = K.qcache_dense_decode(*args) if prefix is None else K.qcache_prefix_decode(*args, prefix)
+    got = (K.qcache_dense_decode(*args) if prefix is None
+           else K.qcache_prefix_decode(*args, prefix, always=True))
     want = vals[best]
     assert not torch.isnan(got).any()
     # the weight and the sum are the same number: the division and the output round

@@ -23,6 +23,11 @@ def K():
     return kascade
 
 
+def shared_decode(K, *args, **kw):
+    """With the prefix shared, however small the batch is."""
+    return K.qcache_prefix_decode(*args, always=True, **kw)
+
+
 def shared_batch(K, rng, lens, P, Hkv, d, bs, dtype, scales=(1.0, 1.0), garbage=255, extra=0):
     """Pages (unused bytes all 0xff: NaN scales) and tables: sequences of at least P tokens
     share their first blocks, shorter ones have blocks of their own."""
@@ -78,10 +83,10 @@ def test_ragged_batches(K, B, G, Hkv, d, bs, P, dtype):
     q = queries(rng, B, G * Hkv, d, dtype)
     ws = K.Workspace("cuda")
     args = (q, pages, ints(table), ints(lens))
-    got = K.qcache_prefix_decode(*args, P, ws=ws)
+    got = shared_decode(K, *args, P, ws=ws)
     assert ws.device_error() == K.OK
     check_attention(q, got, pages, table, lens, Hkv, d, straight(G * Hkv, Hkv))
-    assert torch.equal(got, K.qcache_prefix_decode(*args, P, ws=ws))
+    assert torch.equal(got, shared_decode(K, *args, P, ws=ws))
 
 
 @pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
@@ -93,8 +98,8 @@ def test_head_map_scales_and_wide_tables(K, dtype, d):
     lens = [P + 7 * b for b in range(B)]
     pages, table = shared_batch(K, rng, lens, P, Hkv, d, bs, dtype, scales, extra=3)
     q = queries(rng, B, 8, d, dtype) * 8
-    got = K.qcache_prefix_decode(q, pages, ints(table), ints(lens), P, kv_len=max(lens),
-                                 group_map=heads, scale=0.07, k_scale=scales[0], v_scale=scales[1])
+    got = shared_decode(K, q, pages, ints(table), ints(lens), P, kv_len=max(lens),
+                        group_map=heads, scale=0.07, k_scale=scales[0], v_scale=scales[1])
     check_attention(q, got, pages, table, lens, Hkv, d, heads, k_scale=scales[0],
                     v_scale=scales[1], scale=0.07)
 
@@ -106,7 +111,7 @@ def test_no_sequence_has_the_prefix_and_no_prefix(K):
     q = queries(rng, 4, 8, 64, BF)
     for p in (P, 0):
         ws = K.Workspace("cuda")
-        got = K.qcache_prefix_decode(q, pages, ints(table), ints(lens), p, kv_len=48, ws=ws)
+        got = shared_decode(K, q, pages, ints(table), ints(lens), p, kv_len=48, ws=ws)
         assert ws.device_error() == K.OK
         check_attention(q, got, pages, table, lens, 2, 64, straight(8, 2))
 
@@ -119,7 +124,7 @@ def test_many_row_tiles_and_a_long_prefix(K, dtype):
     lens[17], lens[149] = 0, P
     pages, table = shared_batch(K, rng, lens, P, 2, 64, bs, dtype)
     q = queries(rng, 150, 8, 64, dtype)
-    got = K.qcache_prefix_decode(q, pages, ints(table), ints(lens), P)
+    got = shared_decode(K, q, pages, ints(table), ints(lens), P)
     check_attention(q, got, pages, table, lens, 2, 64, straight(8, 2))
 
 
@@ -141,7 +146,7 @@ def test_rising_scores(K, dtype):
                     ints(slots), pages)
     q = torch.zeros(9, 4, d, dtype=dtype, device="cuda")
     q[..., :16] = torch.from_numpy(rng.choice([-1.0, 1.0, 2.0], (9, 4, 1))).to(dtype).cuda()
-    got = K.qcache_prefix_decode(q, pages, ints(table), ints(lens), P)
+    got = shared_decode(K, q, pages, ints(table), ints(lens), P)
     check_attention(q, got, pages, table, lens, 1, d, straight(4, 1))
 
 
@@ -153,11 +158,11 @@ def test_nan_values_reach_only_their_readers(K):
     lens = [P + 3, P, 40, 0, P + 30]
     pages, table = shared_batch(K, rng, lens, P, 2, d, bs, BF)
     q = queries(rng, 5, 4, d, BF)
-    clean = K.qcache_prefix_decode(q, pages, ints(table), ints(lens), P)
+    clean = shared_decode(K, q, pages, ints(table), ints(lens), P)
     assert torch.isfinite(clean).all()
     block = int(table[0, 2])
     pages[block, 1, 0, 17 * d + 5 * (d // 16) + 1] = 0x7f       # key 37's V, dims 16 .. 31
-    got = K.qcache_prefix_decode(q, pages, ints(table), ints(lens), P)
+    got = shared_decode(K, q, pages, ints(table), ints(lens), P)
     bad = torch.isnan(got)
     for b, n in enumerate(lens):
         for h in range(4):
@@ -180,7 +185,7 @@ def test_huge_and_infinite_queries(K, dtype):
     q[3] = 0.0
     q[4, 0, 3] = float("inf")
     q[5, 1, 7] = float("nan")
-    got = K.qcache_prefix_decode(q, pages, ints(table), ints(lens), P)
+    got = shared_decode(K, q, pages, ints(table), ints(lens), P)
     fine = [b for b in range(6) if b != 1]
     for b in fine:
         for h in range(2):
@@ -204,7 +209,7 @@ def test_device_errors(K):
     pages, table = shared_batch(K, rng, lens, P, 1, d, bs, BF)
     q = queries(rng, 4, 4, d, BF)
     ws = K.Workspace("cuda")
-    run = lambda t, n: K.qcache_prefix_decode(q, pages, ints(t), ints(n), P, ws=ws)
+    run = lambda t, n: shared_decode(K, q, pages, ints(t), ints(n), P, ws=ws)
     run(table, lens)
     assert ws.device_error() == K.OK
     other = table.copy()
@@ -236,21 +241,21 @@ def test_graph_stream_and_one_workspace_for_many_shapes(K):
         lens = [P + 5 * (b % 9) for b in range(B)]
         pages, table = shared_batch(K, rng, lens, P, Hkv, d, bs, dtype)
         q, t, n = queries(rng, B, G * Hkv, d, dtype), ints(table), ints(lens)
-        want = K.qcache_prefix_decode(q, pages, t, n, P, ws=ws)
+        want = shared_decode(K, q, pages, t, n, P, ws=ws)
         s = torch.cuda.Stream()
         s.wait_stream(torch.cuda.current_stream())
-        got = K.qcache_prefix_decode(q, pages, t, n, P, stream=s)
+        got = shared_decode(K, q, pages, t, n, P, stream=s)
         torch.cuda.current_stream().wait_stream(s)
         assert torch.equal(got, want)
         own, out = K.Workspace("cuda"), torch.empty_like(q)
-        K.qcache_prefix_decode(q, pages, t, n, P, ws=own, out=out)
+        shared_decode(K, q, pages, t, n, P, ws=own, out=out)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            K.qcache_prefix_decode(q, pages, t, n, P, ws=own, out=out)
+            shared_decode(K, q, pages, t, n, P, ws=own, out=out)
         q.mul_(-0.5)
         n.sub_(3)                     # those of exactly P tokens no longer take part
         g.replay()
-        assert torch.equal(out, K.qcache_prefix_decode(q, pages, t, n, P, ws=ws))
+        assert torch.equal(out, shared_decode(K, q, pages, t, n, P, ws=ws))
         assert own.device_error() == K.OK and ws.device_error() == K.OK
         dense = K.qcache_dense_decode(q, pages, t, n)
         step = 2.0 ** -7 if dtype == BF else 2.0 ** -18
@@ -272,12 +277,60 @@ def test_pages_beyond_32_bits(K):
             for _ in range(2))
     K.qcache_append(k, v, ints(slots), pages)
     q = queries(rng, 3, 16, d, BF)
-    got = K.qcache_prefix_decode(q, pages, ints(table), ints(lens), P)
+    got = shared_decode(K, q, pages, ints(table), ints(lens), P)
     used = sorted({int(x) for x in table.reshape(-1) if x >= 0})
     small = pages[torch.tensor(used, device="cuda")]
     at = {x: i for i, x in enumerate(used)}
     back = np.array([[at.get(int(x), -1) for x in row] for row in table])
     check_attention(q, got, small, back, lens, Hkv, d, straight(16, Hkv))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("B", [1, 2, 70])
+def test_batches_that_sharing_does_not_help(K, B, dtype):
+    """Unless told otherwise a small batch gets the dense call's results, bit for bit, and the
+    check of its tables."""
+    rng = np.random.default_rng(13)
+    P, bs = 64, 16
+    lens = [P + 3 * (b % 7) for b in range(B)]
+    pages, table = shared_batch(K, rng, lens, P, 2, 64, bs, dtype)
+    q, t, n = queries(rng, B, 8, 64, dtype), ints(table), ints(lens)
+    ws, out = K.Workspace("cuda"), torch.empty_like(q)
+    assert torch.equal(K.qcache_prefix_decode(q, pages, t, n, P, ws=ws, out=out),
+                       K.qcache_dense_decode(q, pages, t, n))
+    assert ws.device_error() == K.OK
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        K.qcache_prefix_decode(q, pages, t, n, P, ws=ws, out=out)
+    t[B - 1, 2] = (t[B - 1, 2] + 1) % pages.shape[0]
+    q.mul_(-1)
+    g.replay()
+    assert ws.device_error() == (K.BAD_INPUT if B > 1 else K.OK)
+    if B > 1:
+        n[B - 1] = P - 1              # then its blocks are its own
+        g.replay()
+        assert ws.device_error() == K.OK
+        assert torch.equal(out, K.qcache_dense_decode(q, pages, t, n))
+
+
+@pytest.mark.parametrize("B,G,Hkv,d,P,own", [(520, 4, 8, 128, 1024, 40), (2048, 8, 4, 64, 512, 20)])
+def test_more_rows_than_sms(K, B, G, Hkv, d, P, own):
+    """Several CTAs after one another on an SM, beside the own parts: against the dense call."""
+    rng = np.random.default_rng(14)
+    bs = 16
+    lens = [P + int(x) for x in rng.integers(0, own, B)]
+    lens[5] = 7
+    pages, table = shared_batch(K, rng, lens, P, Hkv, d, bs, BF)
+    q, t, n = queries(rng, B, G * Hkv, d, BF), ints(table), ints(lens)
+    ws = K.Workspace("cuda")
+    got = shared_decode(K, q, pages, t, n, P, kv_len=P + own, ws=ws)
+    assert ws.device_error() == K.OK
+    dense = K.qcache_dense_decode(q, pages, t, n)
+    # either is off by its weights' 2^-11 and an output's 2^-8 of the values it averages
+    assert (got.float() - dense.float()).abs().max() <= 2.0 ** -7 * dense.abs().max()
+    some = rng.choice(B, 6, replace=False)
+    check_attention(q[some], got[some], pages, table[some], [lens[b] for b in some], Hkv, d,
+                    straight(G * Hkv, Hkv))
 
 
 def test_a_server_over_one_prefix(K):

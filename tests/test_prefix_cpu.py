@@ -19,10 +19,10 @@ def K():
     return kascade
 
 
-def call(K, desc, geo, prefix, nws, q=P, pages=P, table=P, lens=P, out=P, ws=P):
+def call(K, desc, geo, prefix, nws, q=P, pages=P, table=P, lens=P, out=P, ws=P, always=0):
     return K._lib.kascade_qcache_prefix_decode(
         None if desc is None else ctypes.byref(desc), None if geo is None else ctypes.byref(geo), q,
-        pages, table, lens, prefix, out, ws, nws, None)
+        pages, table, lens, prefix, always, out, ws, nws, None)
 
 
 def test_validation_before_launch(K):
@@ -42,6 +42,9 @@ def test_validation_before_launch(K):
     assert call(K, desc, geo, 512, n - 1) == K.WORKSPACE
     assert call(K, desc, geo, 512, n, ws=ODD) == K.WORKSPACE
     assert call(K, desc, geo, 512, n, ws=None) == K.WORKSPACE
+    for always in (-1, 2):
+        assert call(K, desc, geo, 512, n, always=always) == K.INVALID_ARG
+    assert call(K, desc, geo, 512, n - 1, always=1) == K.WORKSPACE
     assert call(K, None, geo, 512, n) == K.INVALID_ARG
     assert call(K, desc, None, 512, n) == K.INVALID_ARG
     assert call(K, desc, K.QCache(64, 40, 15, 0.0, 0.0), 512, n) == K.INVALID_ARG  # 960 < kv_len
@@ -105,10 +108,11 @@ def test_binding_takes_the_documented_call(K, fake):
     assert K.qcache_prefix_decode(**t, prefix_len=0, out=into, scale=0.5, k_scale=2.0, ws=ws,
                                   group_map=[0, 1] * 4) is into
     name, args = fake.calls[-1]
-    assert name == "kascade_qcache_prefix_decode" and args[6] == 0 and args[7] == into.data_ptr()
-    assert [a[6] for n, a in fake.calls if n == name] == [64, 0]
+    assert name == "kascade_qcache_prefix_decode" and args[6:8] == (0, 0) and args[8] == into.data_ptr()
+    K.qcache_prefix_decode(**t, prefix_len=32, always=True, ws=ws)
+    assert [a[6:8] for n, a in fake.calls if n == name] == [(64, 0), (0, 0), (32, 1)]
     sizes = [a for n, a in fake.calls if n == "kascade_qcache_prefix_workspace_size"]
-    assert [a[2] for a in sizes] == [64, 0]
+    assert [a[2] for a in sizes] == [64, 0, 32]
 
 
 @pytest.mark.parametrize("change", [
