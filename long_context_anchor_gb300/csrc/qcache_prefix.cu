@@ -842,8 +842,8 @@ cudaError_t launch_prefix_t(const QPrefixArgs& a, cudaStream_t st) {
 // to be a tenth quicker (a third, where CTAs come after CTAs): 13 us for that kernel's start and end and 36 bytes a ns and SM; 8 us
 // for the join, own parts at 33; 350 ns of an SM for a sequence and KV head either
 // way. Measured, 32 heads on 8, d = 128, bf16 (shared, alone): 32 sequences of 512 + up to
-// 500 tokens 21.1 us, 16.5; of 2048 + 500 23.1, 26.6; 8 of 1024 + 8000 25.7, 18.9; 128 of
-// 1024 + 4000 78.4, 90.6; 2048 of 1024 + 512 299, 552; one of 131072 (64 heads, d = 64) 80, 25.
+// 500 tokens 19.7 us, 16.2; of 2048 + 500 21.6, 25.8; 8 of 1024 + 8000 21.7, 16.7; 128 of
+// 1024 + 4000 75.2, 87.4; 2048 of 1024 + 512 270, 544; one of 131072 (64 heads, d = 64) 53, 25.
 QPrefixGeo prefix_geo(int B, int G, int Hkv, int P, int own, int d, int dtype, int sms) {
   const double pair = d == 128 ? 1080 : 850;
   const double single = (d == 128 ? 625 : 440) * (dtype == KASCADE_F32 ? 2 : 1);
