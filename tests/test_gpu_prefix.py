@@ -333,6 +333,27 @@ def test_more_rows_than_sms(K, B, G, Hkv, d, P, own):
                     straight(G * Hkv, Hkv))
 
 
+def test_two_streams_at_once(K):
+    """Calls of two streams that share the GPU, each with its workspace: the results of calls
+    one after the other."""
+    rng = np.random.default_rng(15)
+    sets = []
+    for B, G, Hkv, d, P, dtype in ((40, 4, 2, 128, 2048, BF), (24, 8, 4, 64, 4096, F32)):
+        lens = [P + 11 * (b % 13) for b in range(B)]
+        pages, table = shared_batch(K, rng, lens, P, Hkv, d, 32, dtype)
+        args = (queries(rng, B, G * Hkv, d, dtype), pages, ints(table), ints(lens), P)
+        sets.append((args, shared_decode(K, *args), torch.cuda.Stream(), K.Workspace("cuda")))
+    torch.cuda.synchronize()
+    outs = [[] for _ in sets]
+    for _ in range(25):
+        for (args, _, s, ws), got in zip(sets, outs):
+            got.append(shared_decode(K, *args, ws=ws, stream=s))
+    torch.cuda.synchronize()
+    for (_, want, _, ws), got in zip(sets, outs):
+        assert ws.device_error() == K.OK
+        assert all(torch.equal(x, want) for x in got)
+
+
 def test_a_server_over_one_prefix(K):
     """Plan, turned appends and decode together: a prompt that is cached once, requests
     that start behind it, grow, end and start again; the oracle follows every token."""

@@ -306,3 +306,23 @@ def test_append_bad_positions_and_slots(K):
     ck, cv = K.qcache_read(pages, ints([0, 1, 5]), dtype=F32)
     assert np.array_equal(f64(ck), Q.stored(f32_turned(k, tab, pos, None, False))[:3])
     assert np.array_equal(f64(cv), Q.stored(f64(v))[:3])
+
+
+@pytest.mark.parametrize("axis", [0, 1, 2])
+def test_rows_that_lie_beyond_32_bits(K, axis):
+    """Strides of 2^31 elements and more between sequences, heads or tokens, in and out."""
+    rng = np.random.default_rng(20 + axis)
+    shape = (2, 2, 2, 64)
+    strides = [256, 128, 64, 1]
+    strides[axis] = (1 << 31) + 64
+    base = torch.empty((1 << 31) + 1024, dtype=BF, device="cuda")
+    q = base.as_strided(shape, strides)
+    rows = torch.from_numpy(rng.standard_normal(shape)).to(BF).cuda()
+    q.copy_(rows)
+    pos = torch.tensor([[3, 0], [7, 5]], dtype=I32, device="cuda")
+    tab = K.rope_table(100.0 ** (-np.arange(32) / 32), 8)
+    want, _ = K.qk_norm_rope(rows, None, pos, tab)
+    got, _ = K.qk_norm_rope(q, None, pos, tab)
+    assert torch.equal(got, want)
+    K.qk_norm_rope(rows, None, pos, tab, q_out=q)
+    assert torch.equal(q, want)
