@@ -39,7 +39,7 @@ struct QPrefixGeo {
   bool alone;    // not worth it: every sequence on its own
 };
 QPrefixGeo prefix_geo(int B, int G, int Hkv, int P, int own, int d, int dtype, int sms);
-// A piece: o [rows][d], m [rows], l [rows].
+// A piece: o [rows/8][d/4][8] of float4, m [rows], l [rows].
 constexpr size_t pfx_piece_floats(int d) { return static_cast<size_t>(kPfxRows) * (d + 2); }
 // Pieces at most, on a GPU of up to `sms` SMs.
 inline size_t pfx_pieces(const QPrefixGeo& g, int Hkv, int sms) {

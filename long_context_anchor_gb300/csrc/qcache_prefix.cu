@@ -118,7 +118,7 @@ struct Shapes {
   static constexpr int kValid = 16;
   static_assert(KST + 6 <= kValid, "two scores of a stream, every other chunk, behind K's ring");
   static constexpr int RAW = (kPfxKeys / kQGroup) * qgroup_bytes(D);
-  static constexpr int Q_HALF = kPfxRows * 128, Q_TILE = QSMEM ? 2 * Q_HALF : 0;
+  static constexpr int Q_TILE = kPfxRows * 2 * D;   // d = 64: on its way to TMEM
   static constexpr int V0 = KST * TILE, QS = V0 + VST * TILE;
   static constexpr int RAW0 = QS + 2 * Q_TILE;
   static constexpr int BAR = RAW0 + NR * RAW;
@@ -233,6 +233,14 @@ struct Widen {
   }
 };
 
+// A query row's largest element is scaled to [2^kQExp, 2^(kQExp + 1)), one below 2^-100 as if it
+// were that. Zero and infinity are left.
+__device__ __forceinline__ int q_exponent(float amax) {
+  const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;   // denormals: -127
+  return amax > 0.f && e < 128 ? max(e, -100) : kQExp;
+}
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
 // The lowest sequence that holds the whole prefix, whose table names its blocks, into
 // src (a.B before; shared memory; all threads).
 __device__ __forceinline__ void first_holder(const QPrefixArgs& a, int& src) {
@@ -243,6 +251,12 @@ __device__ __forceinline__ void first_holder(const QPrefixArgs& a, int& src) {
     }
   __syncthreads();
 }
+
+// The float4 e4 of row r in a piece: eight rows side by side, so that both the rows'
+// threads and the join's fill whole lines (a row after the other, the stores of a
+// piece took 5 us).
+template <int D>
+__device__ __forceinline__ int pfx_piece_at(int r, int e4) { return ((r >> 3) * (D / 4) + e4) * 8 + (r & 7); }
 
 template <int D, int TERMS>
 __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__ QPrefixArgs a) {
@@ -274,6 +288,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
   int* kv_valid = raw_valid + NR;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(sm + SM::TMEM);
 
+  const Part p = part_of(a.geo, a.Hkv, static_cast<int>(blockIdx.x));
+  // a softmax thread's row of the KV head's queries, and whether it takes part
+  const int gr = (p.tile0 + (p.tiles == 2 ? (tid >> 7) & 1 : 0)) * 128 + (tid & 127);
+  const bool live = tid < 256 && gr < a.B * a.G &&
+                    pfx_start(a.lens, gr / a.G, a.P, a.N, a.max_blocks, a.bs_shift) > 0;
   if (tid == 0) s_src = a.B;
   if (tid < SM::NBAR) {
     const int i = tid, j = i - 2 * NR, l = j - 2 * KST, k = l - 2 * VST;   // k: from q_ready on
@@ -284,21 +303,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
     mbar_init(bars + i, count);
     fence_barrier_init();
   }
-  __syncthreads();
-  first_holder(a, s_src);
-  const int src = s_src;
-  if (src >= a.B) {   // nobody has it: no piece is read either
-    if (tid == 0) pdl_wait();
-    return;
-  }
   if (warp == kMmaWarp) tmem_alloc(s_tmem, 512);   // one CTA per SM
   tc_fence_before();
   __syncthreads();
+  first_holder(a, s_src);
   tc_fence_after();
   const uint32_t tmem = warp_uniform(*s_tmem);
+  const int src = s_src;
+  if (src >= a.B) {   // nobody has it: no piece is read either
+    if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+    if (tid == 0) pdl_wait();
+    return;
+  }
   const int32_t* ids = a.table + static_cast<size_t>(src) * a.max_blocks;
-
-  const Part p = part_of(a.geo, a.Hkv, static_cast<int>(blockIdx.x));
 
   if (warp >= kMmaWarp) {
     fewer_regs<kIssueRegs>();
@@ -458,83 +475,101 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
     // ------------------------------------------------------------- softmax
     const int s = warp >> 2, r = (warp & 3) * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t tQ = tmem + SM::Q_COLS * s + lane_base;
     const uint32_t tS0 = tmem + SM::S0 + 128 * s + lane_base;
     const uint32_t tO = tmem + SM::O0 + SM::O_COLS * s + lane_base;
     const uint32_t sQ = smem_u32(sm + SM::QS) + s * SM::Q_TILE;
     bool ok = true;
-    const int gr = (p.tile0 + (p.tiles == 2 ? s : 0)) * 128 + r;   // row of the KV head
-    const int b = gr / a.G, slot = gr - b * a.G;
-    const bool live = b < a.B && pfx_start(a.lens, b, a.P, a.N, a.max_blocks, a.bs_shift) > 0;
-    const bool idle = !__any_sync(0xffffffffu, live);
-    // ---- this row of Q, 64 elements at a time; all of a pass's loads are in flight
-    // together, and a bf16 row is loaded once
-    constexpr int kVecs = TERMS == 2 ? 16 : 8;   // 16-byte pieces of 64 elements
-    const size_t q_row = live ? static_cast<size_t>(b) * a.Hq + a.heads[p.g * a.G + slot] : 0;
-    const uint4* row = reinterpret_cast<const uint4*>(static_cast<const char*>(a.q) +
-                                                      q_row * D * (TERMS == 2 ? 4 : 2));
-    uint4 raw[D / 64][kVecs];
-    float amax = 0.f;
+    const uint32_t alive = __ballot_sync(0xffffffffu, live);
+    const bool idle = alive == 0u;
+    // ---- these 32 rows of Q: neighbouring lanes load neighbouring pieces (a row per
+    // thread, as the softmax has them, took 3 us of loads of 32 lines each), scale them
+    // and put them into the tile
+    constexpr int kPerRow = D * (TERMS == 2 ? 4 : 2) / 16, kRowsAt = 32 / kPerRow;   // lanes per row
+    constexpr int kLoads = 32 / kRowsAt, kBatch = kLoads < 16 ? kLoads : 16;
+    const int piece = lane % kPerRow;
+    const int q_row = live ? (gr / a.G) * a.Hq + a.heads[p.g * a.G + gr % a.G] : 0;   // of row r
+    float amax = 0.f;                                                                // of row r
 #pragma unroll
-    for (int h = 0; h < D / 64; ++h)
+    for (int i0 = 0; i0 < kLoads; i0 += kBatch) {
+      uint4 raw[kBatch];
+      float m[kBatch];
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i)
-        raw[h][i] = live ? __ldg(row + h * kVecs + i) : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < kBatch; ++i) {
+        const int j = (i0 + i) * kRowsAt + lane / kPerRow;
+        const int from = __shfl_sync(0xffffffffu, q_row, j);
+        raw[i] = make_uint4(0u, 0u, 0u, 0u);
+        if ((alive >> j) & 1u)
+          raw[i] = __ldg(reinterpret_cast<const uint4*>(a.q) + static_cast<size_t>(from) * kPerRow + piece);
+      }
 #pragma unroll
-    for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        const uint32_t w[4] = {raw[h][i].x, raw[h][i].y, raw[h][i].z, raw[h][i].w};
+      for (int i = 0; i < kBatch; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        m[i] = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (TERMS == 2) {
-            amax = fmaxf(amax, fabsf(__uint_as_float(w[j])));
+            m[i] = fmaxf(m[i], fabsf(__uint_as_float(w[j])));
           } else {
-            amax = fmaxf(amax, fabsf(__uint_as_float(w[j] << 16)));
-            amax = fmaxf(amax, fabsf(__uint_as_float(w[j] & 0xffff0000u)));
+            m[i] = fmaxf(m[i], fabsf(__uint_as_float(w[j] << 16)));
+            m[i] = fmaxf(m[i], fabsf(__uint_as_float(w[j] & 0xffff0000u)));
           }
         }
       }
-    int e = kQExp;
-    if (amax > 0.f && amax < CUDART_INF_F) e = max(ilogbf(amax), -100);
-    const float up = ldexpf(1.f, kQExp - e);
-    const float ml = fmaxf(a.scale * ldexpf(1.f, e - kQExp), 1e-37f) * kLog2e;
 #pragma unroll
-    for (int h = 0; h < D / 64; ++h) {
-      uint32_t w[32];
+      for (int off = 1; off < kPerRow; off <<= 1)   // all rows' steps in flight together
 #pragma unroll
-      for (int i = 0; i < kVecs; ++i) {
-        const uint32_t v[4] = {raw[h][i].x, raw[h][i].y, raw[h][i].z, raw[h][i].w};
+        for (int i = 0; i < kBatch; ++i) m[i] = fmaxf(m[i], __shfl_xor_sync(0xffffffffu, m[i], off));
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float own = __shfl_sync(0xffffffffu, m[i], (lane % kRowsAt) * kPerRow);
+        if (lane / kRowsAt == i0 + i) amax = own;
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        const float up = pow2(kQExp - q_exponent(m[i]));
+        const int to = (warp & 3) * 32 + (i0 + i) * kRowsAt + lane / kPerRow;
         if (TERMS == 2) {
+          uint32_t x[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float lo = __uint_as_float(v[2 * j]) * up, hi = __uint_as_float(v[2 * j + 1]) * up;
+            float lo = __uint_as_float(w[2 * j]) * up, hi = __uint_as_float(w[2 * j + 1]) * up;
             if (s == 1) {
               lo -= f16_rounded(lo);
               hi -= f16_rounded(hi);
             }
-            w[2 * i + j] = pack_f16(lo, hi);
+            x[j] = pack_f16(lo, hi);
           }
+          asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(
+                           sQ + sw128_offset(kPfxRows, to, piece >> 1) + 8 * (piece & 1)),
+                       "r"(x[0]), "r"(x[1])
+                       : "memory");
         } else {
+          uint32_t x[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            w[(4 * i + j) & 31] = pack_f16(__uint_as_float(v[j] << 16) * up,
-                                           __uint_as_float(v[j] & 0xffff0000u) * up);
+            x[j] = pack_f16(__uint_as_float(w[j] << 16) * up, __uint_as_float(w[j] & 0xffff0000u) * up);
+          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(sQ + sw128_offset(kPfxRows, to, piece)),
+                       "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3])
+                       : "memory");
         }
       }
-      if (SM::QSMEM) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
-                           sQ + sw128_offset(kPfxRows, r, 8 * h + i)),
-                       "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
-                       : "memory");
-      } else {
-        tmem_st32(tQ + 32 * h, w);
-      }
     }
-    if (SM::QSMEM) fence_proxy_async_smem();
-    else tmem_wait_st();
+    const float ml = fmaxf(a.scale * pow2(q_exponent(amax) - kQExp), 1e-37f) * kLog2e;
+    if constexpr (SM::QSMEM) {
+      fence_proxy_async_smem();
+    } else {   // a row per thread from here on
+      __syncwarp();
+      uint32_t w[32];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                     : "r"(sQ + sw128_offset(kPfxRows, r, i))
+                     : "memory");
+      tmem_st32(tmem + SM::Q_COLS * s + lane_base, w);
+      tmem_wait_st();
+    }
     tc_fence_before();
     mbar_arrive(q_ready + s);
     // ---- its chunks
@@ -572,12 +607,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
           if (raise) {
             float up_to = ref;
 #pragma unroll 1
-            for (int cc = 0; cc < 64; cc += 16) {
-              uint32_t v[16];
-              tmem_ld16(tS + cc, v);
+            for (int cc = 0; cc < 64; cc += 32) {
+              uint32_t v[32];
+              tmem_ld32(tS + cc, v);
               tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; i += 2)
+              for (int i = 0; i < 32; i += 2)
                 up_to = fmax3(up_to, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
             }
             const float al = ex2((ref - up_to) * ml);
@@ -659,11 +694,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
         uint32_t o[32];
         tmem_ld32(tO + 32 * cc, o);
         tmem_wait_ld();
-        float4* dst = reinterpret_cast<float4*>(piece + r * D + 32 * cc);
+        float4* dst = reinterpret_cast<float4*>(piece) + pfx_piece_at<D>(r, 8 * cc);
         if (live)
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            dst[i] = n > 0 ? make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+            dst[8 * i] = n > 0 ? make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
                                          __uint_as_float(o[4 * i + 2]),
                                          __uint_as_float(o[4 * i + 3]))
                            : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -686,9 +721,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
   }
 }
 
-// Every row's pieces and its own part's state joined into the output: D / 4 threads
-// per row and worker, `workers` of them per row, which take the row's pieces in turn
-// and are joined in order. The last `checkers` CTAs check the tables.
+// Every row's pieces and its own part's state joined into the output: a thread has four
+// dims of a row, or every WORKERS-th of its pieces, which are then joined in order. A CTA has
+// kRows rows of a KV head and kLanes of their float4s (kParts CTAs have a row); those behind the
+// last head check the tables.
 constexpr int kJoinThreads = 256;
 
 // Sequences whose tables name other blocks than the lowest one's; this CTA's share of
@@ -724,34 +760,39 @@ __global__ void __launch_bounds__(kJoinThreads) k_qprefix_check(const __grid_con
   pdl_wait();
 }
 
-template <int D, bool F32>
-__global__ void __launch_bounds__(kJoinThreads) k_qprefix_join(const __grid_constant__ QPrefixArgs a,
-                                                               int workers, int checkers) {
+template <int D, int WORKERS>
+struct JoinShape {
+  static constexpr int kLanes = WORKERS * (D / 4) > 32 ? 32 / WORKERS : D / 4;
+  static constexpr int kRows = kJoinThreads / (kLanes * WORKERS), kParts = D / 4 / kLanes;
+};
+
+template <int D, bool F32, int WORKERS>
+__global__ void __launch_bounds__(kJoinThreads) k_qprefix_join(const __grid_constant__ QPrefixArgs a) {
   pdl_wait();
   pdl_trigger();
-  constexpr int kLanes = D / 4, kGroups = kJoinThreads / kLanes, kBatch = 8;
+  using J = JoinShape<D, WORKERS>;
+  constexpr int kBatch = 8;
   __shared__ Joined scratch[kJoinThreads];
   __shared__ int s_src;
-  const int joiners = static_cast<int>(gridDim.x) - checkers;
-  if (static_cast<int>(blockIdx.x) >= joiners) {
-    check_tables(a, s_src, static_cast<int>(blockIdx.x) - joiners, checkers);
+  const int g = static_cast<int>(blockIdx.y);
+  if (g == a.Hkv) {
+    check_tables(a, s_src, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
     return;
   }
-  const int group = threadIdx.x / kLanes, e4 = threadIdx.x % kLanes;
-  const int worker = group % workers;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (kGroups / workers) + group / workers;
-  const bool here = row < static_cast<int64_t>(a.B) * a.Hq;
-  const int64_t unit_row = row / a.G;   // sequence * Hkv + KV head
-  const int b = static_cast<int>(unit_row / a.Hkv), g = static_cast<int>(unit_row - static_cast<int64_t>(b) * a.Hkv);
-  const int slot = static_cast<int>(row - unit_row * a.G);
+  // neighbouring lanes have neighbouring rows, which lie side by side in a piece
+  const int e4 = static_cast<int>(blockIdx.x) % J::kParts * J::kLanes + threadIdx.x / J::kRows % J::kLanes;
+  const int worker = threadIdx.x / (J::kRows * J::kLanes);
+  const int kv_row = static_cast<int>(blockIdx.x) / J::kParts * J::kRows + threadIdx.x % J::kRows;
+  const int b = kv_row >> (31 - __clz(a.G)), slot = kv_row & (a.G - 1);   // G: a power of two
+  const bool here = b < a.B;
   Joined x = {kNoKey, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
   if (here && worker == 0) {
-    const float2 ml = __ldcg(a.own_ml + row);
-    x = {ml.x, ml.y, __ldcg(a.own_o + row * kLanes + e4)};
+    const int64_t at = (static_cast<int64_t>(b) * a.Hkv + g) * a.G + slot;
+    const float2 ml = __ldcg(a.own_ml + at);
+    x = {ml.x, ml.y, __ldcg(a.own_o + at * (D / 4) + e4)};
   }
   if (here && pfx_start(a.lens, b, a.P, a.N, a.max_blocks, a.bs_shift) > 0) {
     const QPrefixGeo& geo = a.geo;
-    const int kv_row = b * a.G + slot;
     const int tile = kv_row / kPfxRows, r = kv_row % kPfxRows;
     const bool pair = tile < 2 * geo.pairs;
     const int cta = pair ? (g * geo.pairs + tile / 2) * geo.pair_runs
@@ -762,27 +803,27 @@ __global__ void __launch_bounds__(kJoinThreads) k_qprefix_join(const __grid_cons
     const size_t stride = (pair ? 2 : 1) * pfx_piece_floats(D);
     const float* p = a.part + pfx_piece_floats(D) * (2 * static_cast<size_t>(cta) +
                                                      (pair ? tile & 1 : 0));
-    for (int s = worker; s < n; s += kBatch * workers) {
+    for (int s = worker; s < n; s += kBatch * WORKERS) {
       Joined y[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         y[k] = {kNoKey, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-        if (s + k * workers < n) {
-          const float* at = p + (s + k * workers) * stride;
+        if (s + k * WORKERS < n) {
+          const float* at = p + (s + k * WORKERS) * stride;
           y[k].m = __ldcg(at + kPfxRows * D + r);
           y[k].l = __ldcg(at + kPfxRows * (D + 1) + r);
-          y[k].o = __ldcg(reinterpret_cast<const float4*>(at + r * D) + e4);
+          y[k].o = __ldcg(reinterpret_cast<const float4*>(at) + pfx_piece_at<D>(r, e4));
         }
       }
       join_into(x, y);
     }
   }
-  if (workers > 1) {
+  if (WORKERS > 1) {
     scratch[threadIdx.x] = x;
     __syncthreads();
     if (worker > 0) return;
-    for (int w = 1; w < workers; ++w) {
-      const Joined y[1] = {scratch[threadIdx.x + w * kLanes]};
+    for (int w = 1; w < WORKERS; ++w) {
+      const Joined y[1] = {scratch[threadIdx.x + w * J::kRows * J::kLanes]};
       join_into(x, y);
     }
   }
@@ -804,17 +845,24 @@ int checkers_of(const QPrefixArgs& a) {
   return ctas < 256 ? static_cast<int>(ctas) : 256;
 }
 
+template <int D, bool F32, int WORKERS>
+cudaError_t launch_join_w(const QPrefixArgs& a, cudaStream_t st) {
+  using J = JoinShape<D, WORKERS>;
+  const int blocks = (a.B * a.G + J::kRows - 1) / J::kRows * J::kParts;
+  return launch_pdl(k_qprefix_join<D, F32, WORKERS>,
+                    dim3(static_cast<unsigned int>(blocks), static_cast<unsigned int>(a.Hkv) + 1),
+                    dim3(kJoinThreads), 0, st, a);
+}
+
 template <int D, bool F32>
 cudaError_t launch_join_t(const QPrefixArgs& a, cudaStream_t st) {
   // pieces of a row at most, eight of them per worker
   const int pieces = max(a.geo.pairs > 0 ? a.geo.pair_runs : 0,
                          a.geo.singles > 0 ? 2 * a.geo.single_runs : 0);
-  const int workers = pieces > 32 ? 8 : pieces > 16 ? 4 : pieces > 8 ? 2 : 1;
-  const int64_t per_cta = kJoinThreads / (D / 4) / workers;
-  const int64_t joiners = (static_cast<int64_t>(a.B) * a.Hq + per_cta - 1) / per_cta;
-  const int checkers = checkers_of(a);
-  return launch_pdl(k_qprefix_join<D, F32>, dim3(static_cast<unsigned int>(joiners + checkers)),
-                    dim3(kJoinThreads), 0, st, a, workers, checkers);
+  return pieces > 32   ? launch_join_w<D, F32, 8>(a, st)
+         : pieces > 16 ? launch_join_w<D, F32, 4>(a, st)
+         : pieces > 8  ? launch_join_w<D, F32, 2>(a, st)
+                       : launch_join_w<D, F32, 1>(a, st);
 }
 
 template <int D, int TERMS>
