@@ -23,18 +23,20 @@
 //   k_qprefix_check  the tables' check alone
 //
 // Measured (bf16, one launch sequence in a graph): 16 sequences x 64 heads over 131072
-// keys at d = 64 57.8 us (595 TFLOP/s of the products, 1.3 TB/s of pages), 128 x 32 heads
-// over 32768 at d = 128 86.8 us (791 TFLOP/s), 32 x 32 heads over 8192 with 1024 own keys
-// each 29.3 us; one by one, as the dense call does it, 218, 810 and 66.5 us. A chunk takes
-// an SM 740 cycles at d = 64, two tiles of one 1770 at d = 128. What bounds it is a chunk's
+// keys at d = 64 56.8 us (605 TFLOP/s of the products, 1.4 TB/s of pages), 128 x 32 heads
+// over 32768 at d = 128 77.9 us (881 TFLOP/s), 32 x 32 heads over 8192 with 1024 own keys
+// each 25.5 us; one by one, as the dense call does it, 218, 810 and 66.5 us. A chunk takes
+// an SM 740 cycles at d = 64, two tiles of one 1700 at d = 128. What bounds it is a chunk's
 // way round with two score buffers: 1500 cycles of softmax (830 of arithmetic beside the
 // other warps', 400 of a TMEM load) and as many from the weights to the next scores in
 // their place (product, its wait, scores, five waits of 100 cycles); the issue slots are
 // 50 to 60% full, tensor cores busy 30% (d = 64) and 50% (d = 128, where the scores read Q
-// from shared memory, as TMEM is full). About 9 us of a launch are its start and end.
-// Slower: two warps per 32 rows with half of the keys each (61.5, 91 us), the next
-// chunk's load begun before this one's end (63, 91), scores and products issued by
-// warps of their own (65, 103), one arrival per warp for the weights (58.7, 87.9).
+// from shared memory, as TMEM is full). About 6 us of a launch are its start (4: lengths,
+// queries, first chunk) and end. Slower (against 57.8 and 86.8 us, when those were 9): two warps per 32 rows with
+// half of the keys each (61.5, 91), the next chunk's load begun before this one's end (63,
+// 91), scores and products issued by warps of their own (65, 103), one arrival per warp
+// for the weights (58.7, 87.9); against 56.8 and 77.9: queries loaded before the barriers are
+// set up (59.6, 81).
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -881,22 +883,22 @@ cudaError_t launch_prefix_t(const QPrefixArgs& a, cudaStream_t st) {
 // kernel runs beside this one on the SMs that are left (own_sms): one CTA per SM, and
 // a CTA has one run of one unit (a second one would cost its start, its queries
 // and its pieces again, 10 us); units that are more than the SMs have one run and come CTA
-// after CTA. Measured: a chunk takes an SM `pair` ns with two tiles
-// of queries and `single` with one, the own parts' kernel reads 24 bytes a ns on an SM, and
-// each takes about 9 us to start and end. Half of the `own` tokens that a sequence may
-// have are assumed, since the lengths are not known here.
+// after CTA. Measured: a chunk takes an SM `pair` ns with two tiles of queries and `single`
+// with one, the own parts' kernel reads 33 bytes a ns on an SM and spends 350 ns on a
+// sequence and KV head; 6.5 and 9 us to start and end. Half of the `own` tokens that a
+// sequence may have are assumed, since the lengths are not known here.
 //
 // `alone`: every sequence on its own (the dense call's kernel), unless sharing is reckoned
-// to be a tenth quicker (a third, where CTAs come after CTAs): 13 us for that kernel's start and end and 36 bytes a ns and SM; 8 us
-// for the join, own parts at 33; 350 ns of an SM for a sequence and KV head either
-// way. Measured, 32 heads on 8, d = 128, bf16 (shared, alone): 32 sequences of 512 + up to
-// 500 tokens 19.7 us, 16.2; of 2048 + 500 21.6, 25.8; 8 of 1024 + 8000 21.7, 16.7; 128 of
-// 1024 + 4000 75.2, 87.4; 2048 of 1024 + 512 270, 544; one of 131072 (64 heads, d = 64) 53, 25.
+// to be a tenth quicker (a third, where CTAs come after CTAs): 13 us for that kernel's start
+// and end and 36 bytes a ns and SM; 8 us for the join. Measured, 32 heads on 8, d = 128, bf16
+// (shared, alone): 32 sequences of 512 + up to 500 tokens 18.5 us, 16.2; of 2048 + 500 19.0,
+// 26.0; 8 of 1024 + 8000 21.3, 17.0; 128 of 1024 + 4000 74.5, 86.9; 2048 of 1024 + 512 251,
+// 544; one of 131072 (64 heads, d = 64) 53, 25.
 QPrefixGeo prefix_geo(int B, int G, int Hkv, int P, int own, int d, int dtype, int sms) {
-  const double pair = d == 128 ? 1080 : 850;
-  const double single = (d == 128 ? 625 : 440) * (dtype == KASCADE_F32 ? 2 : 1);
+  const double pair = d == 128 ? 900 : 780;
+  const double single = (d == 128 ? 640 : 400) * (dtype == KASCADE_F32 ? 2 : 1);
   const double token = static_cast<double>(B) * Hkv * (9 * d / 8), start = 9000;
-  const double rest = 0.5 * token * own / 24, units = 350.0 * B * Hkv;
+  const double rest = 0.5 * token * own / 33, units = 350.0 * B * Hkv;
   QPrefixGeo g{};
   const int tiles = static_cast<int>((static_cast<int64_t>(B) * G + kPfxRows - 1) / kPfxRows);
   g.nch = (P + kPfxKeys - 1) / kPfxKeys;
@@ -914,7 +916,7 @@ QPrefixGeo prefix_geo(int B, int G, int Hkv, int P, int own, int d, int dtype, i
     const int64_t ctas = static_cast<int64_t>(Hkv) * (static_cast<int64_t>(g.pairs) * r +
                                                       static_cast<int64_t>(g.singles) * single_runs);
     if (r > 1 && ctas > sms - least) break;
-    const double run = start + len * (g.pairs > 0 ? pair : single);
+    const double run = 6500 + len * (g.pairs > 0 ? pair : single);
     // SMs for the own parts: whole TPCs, what the runs leave or, with one run, more
     const int first = ctas <= sms - least ? (sms - static_cast<int>(ctas)) & ~1 : least;
     for (int o = first; o < sms && (o == first || r == 1); o += 2) {
@@ -925,9 +927,8 @@ QPrefixGeo prefix_geo(int B, int G, int Hkv, int P, int own, int d, int dtype, i
       if (g.own_sms == 0 || t < (ctas > sms - o && best_fits ? 0.75 : 1) * best) {
         best = t;
         best_fits = ctas <= sms - o;
-        const double own_parts = start + (rest * 24 / 33 + units) / o;
         g.alone = 13000 + (token * (P + 0.5 * own) / 36 + units) / sms <
-                  (best_fits ? 1.1 : 1.35) * (8000 + (t_prefix > own_parts ? t_prefix : own_parts));
+                  (best_fits ? 1.1 : 1.35) * (8000 + t);
         g.pair_runs = g.pairs > 0 ? r : 1;
         g.single_runs = single_runs;
         g.ctas = static_cast<int>(ctas);
