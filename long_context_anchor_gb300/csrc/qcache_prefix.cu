@@ -850,7 +850,8 @@ int checkers_of(const QPrefixArgs& a) {
 template <int D, bool F32, int WORKERS>
 cudaError_t launch_join_w(const QPrefixArgs& a, cudaStream_t st) {
   using J = JoinShape<D, WORKERS>;
-  const int blocks = (a.B * a.G + J::kRows - 1) / J::kRows * J::kParts;
+  // (a few rows' CTAs would be too few for a long table)
+  const int blocks = max((a.B * a.G + J::kRows - 1) / J::kRows * J::kParts, checkers_of(a));
   return launch_pdl(k_qprefix_join<D, F32, WORKERS>,
                     dim3(static_cast<unsigned int>(blocks), static_cast<unsigned int>(a.Hkv) + 1),
                     dim3(kJoinThreads), 0, st, a);
