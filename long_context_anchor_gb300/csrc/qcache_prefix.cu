@@ -723,10 +723,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
   }
 }
 
-// Every row's pieces and its own part's state joined into the output: a thread has four
-// dims of a row, or every WORKERS-th of its pieces, which are then joined in order. A CTA has
-// kRows rows of a KV head and kLanes of their float4s (kParts CTAs have a row); those behind the
-// last head check the tables.
 constexpr int kJoinThreads = 256;
 
 // Sequences whose tables name other blocks than the lowest one's; this CTA's share of
@@ -762,6 +758,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_qprefix_check(const __grid_con
   pdl_wait();
 }
 
+// Every row's pieces and its own part's state joined into the output: a thread has four
+// dims of a row, or every WORKERS-th of its pieces, which are then joined in order. A CTA has
+// kRows rows of a KV head and kLanes of their float4s (kParts CTAs have a row); those behind the
+// last head check the tables.
 template <int D, int WORKERS>
 struct JoinShape {
   static constexpr int kLanes = WORKERS * (D / 4) > 32 ? 32 / WORKERS : D / 4;
