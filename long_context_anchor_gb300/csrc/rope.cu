@@ -382,11 +382,13 @@ __global__ void __launch_bounds__(kThreads, CTAS_PER_SM)
 }
 
 // Heads of a warp: all of a token's, where there are enough tokens to fill the
-// GPU with `want` warps, else fewer.
+// GPU with `want` warps, else fewer. No tokens or heads (an append without queries): none.
 void split_heads(int64_t tokens, int heads, int slots, int& splits, int& per) {
   constexpr int64_t want = 152 * 32;
+  splits = per = 0;
+  if (tokens < 1 || heads < 1) return;
   const int chunks = (heads + slots - 1) / slots;
-  int64_t n = tokens > 0 ? (want + tokens - 1) / tokens : 1;
+  int64_t n = (want + tokens - 1) / tokens;
   if (n > chunks) n = chunks;
   const int each = (chunks + static_cast<int>(n) - 1) / static_cast<int>(n);
   per = each * slots;

@@ -1,6 +1,9 @@
 """Rotation without a GPU: the oracle's pins, the library's argument validation (before any
 launch) and the binding's tensor checks."""
 import ctypes
+import subprocess
+import sys
+from pathlib import Path
 
 import numpy as np
 import pytest
@@ -131,6 +134,20 @@ def test_appends_are_validated_before_the_launch(K):
         st[i] += 4
         assert append_call(K, strides=st) == bad
     assert append_call(K, nws=0) == K.WORKSPACE and append_call(K, ws=None) == K.WORKSPACE
+
+
+@pytest.mark.parametrize("call", ["Hq=0, q=None, qo=None", "Hq=0, q=None, qo=None, T=5000",
+                                  "Hq=0, q=None, qo=None, pos=None, cu=FAKE, lens=FAKE, n=2",
+                                  "pos=None, cu=FAKE, lens=FAKE, n=2, T=0"])
+def test_appends_of_keys_or_queries_alone_reach_the_launch(K, call):
+    """What the library reckons in front of a launch, in a process that sees no GPU: the
+    launch fails with a status, and the process lives to report it."""
+    code = ("import os, sys; os.environ['CUDA_VISIBLE_DEVICES'] = ''; sys.path[:0] = %r\n"
+            "from test_rope_cpu import FAKE, append_call\n"
+            "from long_context_anchor_gb300 import kascade as K\n"
+            "sys.exit(0 if append_call(K, %s) == K.CUDA else 3)\n"
+            % ([str(Path(__file__).parent), str(Path(__file__).parent.parent)], call))
+    assert subprocess.run([sys.executable, "-c", code], timeout=300).returncode == 0
 
 
 class _Recorder:
