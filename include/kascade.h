@@ -453,6 +453,7 @@ kascade_status kascade_qcache_append(const kascade_qcache* cache, int32_t n_kv_h
  *   cu_new [n_seqs+1] and kv_lens [n_seqs] as kascade_qcache_plan wrote them
  *     (positions NULL): row t of k and v is its new token t, and row b of q
  *     the query of sequence b's last token. All axes have that one position.
+ * With rope NULL (a norm alone) the first way needs no positions either.
  * strides: k (tokens, heads), v, q, q_out: eight. q_out may be q with the same
  * strides. Queries are written whatever their token's slot. A position outside
  * the table sets KASCADE_ERR_BAD_INPUT, and its row is not turned. */

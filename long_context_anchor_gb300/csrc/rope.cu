@@ -280,7 +280,7 @@ __device__ __forceinline__ void append_rows(const RopeAppendArgs& a, int t, int 
   const bool turns = part < groups, far = turns && !INTER;
   const int at[2] = {far ? 16 * part : 32 * part, far ? 16 * (part + groups) : 32 * part + 16};
   const float* rows[4] = {};
-  if (h0 < a.Hkv) {
+  if (h0 < a.Hkv && a.rope.table != nullptr) {   // without a table there may be no positions
     int from_plan = 0;
     if (a.positions == nullptr) {
       const int b = owner_of_row(a.cu_new, a.n_seqs, t);

@@ -7,6 +7,8 @@ normalised a, b: two products and a sum in fp32, each off by at most 2^-24 of it
 positive), its mean and eps by 2 2^-24, rsqrt by 2^-22 (two units), the factors r and w by
 2 2^-24: half of the first two, 2^-22 and the last, at most (d / 2 + 8) 2^-24 of a and b.
 Then half a step of the output's type."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -248,6 +250,36 @@ def test_append_with_norm(K, dtype, d, inter):
     _, k32 = K.qk_norm_rope(q.float(), k.float(), ints(pos), tab, q_weight=w[0].float(),
                             k_weight=w[1].float(), eps=EPS, interleaved=inter)
     ck, cv = K.qcache_read(pages, ints(slots), dtype=F32)
+    assert np.array_equal(f64(ck), Q.stored(f64(k32)))
+    assert np.array_equal(f64(cv), Q.stored(f64(v)))
+
+
+@pytest.mark.parametrize("planned", [False, True])
+@pytest.mark.parametrize("dtype,d,norm", [(BF, 128, True), (F32, 64, True), (BF, 64, False)])
+def test_append_without_a_rotation(K, dtype, d, norm, planned):
+    """The C call without a rotation, and so without positions (the binding wants one): a norm
+    alone, or what qcache_append does."""
+    rng = np.random.default_rng(d + planned)
+    T, Hq, Hkv, bs, B = 50, 12, 3, 16, 4
+    q = torch.from_numpy(rng.standard_normal((B if planned else T, Hq, d))).to(dtype).cuda()
+    k, v = (torch.from_numpy(rng.standard_normal((T, Hkv, d))).to(dtype).cuda() for _ in range(2))
+    w = torch.from_numpy(1 + 0.3 * rng.standard_normal((2, d))).to(dtype).cuda()
+    slots = ints(rng.permutation(64)[:T])
+    cu, lens = ints([0, 20, 20, 21, T]), ints([20, 7, 9, T])
+    pages, out, ws = K.qcache_alloc(4, Hkv, d, bs), torch.empty_like(q), K.Workspace("cuda")
+    geo, buf = K.QCache(bs, 4, 1, 0.0, 0.0), ws.get(256)
+    strides = [Hkv * d, d] * 2 + [Hq * d, d] * 2
+    at = lambda t, used=True: t.data_ptr() if used else None
+    status = K._lib.kascade_qcache_append_rope(
+        ctypes.byref(geo), None, Hq, Hkv, d, K.F32 if dtype is F32 else K.BF16, at(k), at(v), at(q),
+        (ctypes.c_int64 * 8)(*strides), at(w[1], norm), at(w[0], norm), EPS, at(slots), T, None,
+        at(cu, planned), at(lens, planned), B if planned else 0, at(pages), at(out), at(buf),
+        buf.numel(), torch.cuda.current_stream().cuda_stream)
+    assert status == K.OK and ws.device_error() == K.OK
+    wq, wk = (w[0], w[1].float()) if norm else (None, None)
+    assert torch.equal(out, K.qk_norm_rope(q, None, q_weight=wq, eps=EPS)[0])
+    k32 = K.qk_norm_rope(k.float(), None, q_weight=wk, eps=EPS)[0]
+    ck, cv = K.qcache_read(pages, slots, dtype=F32)
     assert np.array_equal(f64(ck), Q.stored(f64(k32)))
     assert np.array_equal(f64(cv), Q.stored(f64(v)))
 
