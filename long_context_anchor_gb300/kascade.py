@@ -986,11 +986,16 @@ def _head_strides(t, name, shape, dtype, dev, unit, out=False):
 @functools.lru_cache(maxsize=256)
 def _layout(shape, strides, unit):
     """Whether rows of these strides are contiguous and whole units apart, whether
-    none is another's, and the strides of _head_strides."""
+    each axis steps over all that the axes of smaller strides cover (so that no two
+    rows meet), and the strides of _head_strides."""
     st = [x if n > 1 else 0 for x, n in zip(strides, shape)]
     empty = 0 in shape
     rows = empty or strides[-1] == 1 and not any(x % unit for x in st[:-1])
-    apart = empty or not any(x == 0 and n > 1 for x, n in zip(st, shape))
+    covered, apart = shape[-1], True
+    for x, n in sorted((x, n) for x, n in zip(st[:-1], shape) if n > 1):
+        apart = apart and x >= covered
+        covered += (n - 1) * x
+    apart = empty or apart
     return rows, apart, (0, st[0], st[1]) if len(shape) == 3 else (st[0], st[2], st[1])
 
 
@@ -1031,8 +1036,8 @@ def qk_norm_rope(q, k=None, positions=None, rope=None, q_weight=None, k_weight=N
     2, pairs] (rope_table); None: nothing is turned. Pair i is elements (i, i +
     pairs), interleaved: (2 i, 2 i + 1); elements behind the pairs stay. axes:
     the axis of positions [axes, ...] that each pair follows. Returns (q_out,
-    k_out), k_out None without k: contiguous, or the tensors given (any strides;
-    q and k themselves too)."""
+    k_out), k_out None without k: contiguous, or the tensors given (any strides
+    that keep rows apart, as a slice's do; q and k themselves too)."""
     if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4):
         raise ValueError("q: expected a tensor [T,Hq,d] or [B,Hq,N,d]")
     shape, dtype = q.shape, q.dtype

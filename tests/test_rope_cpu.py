@@ -242,3 +242,35 @@ def test_binding_refuses(K, fake):
         with pytest.raises((ValueError, TypeError)):
             call(**kw)
     assert len([c for c in fake.calls[n:] if "rope" in c[0]]) == 1
+
+
+def test_binding_refuses_outputs_whose_rows_meet(K, fake):
+    ws, base = K.Workspace("cpu"), torch.zeros(1 << 14, dtype=BF)
+    tab, pos = torch.zeros(20, 2, 32), torch.zeros(9, dtype=I32)
+    q = torch.zeros(9, 4, 64, dtype=BF)
+    slots, pages = torch.zeros(9, dtype=I32), torch.zeros(4, 4, 1, 1152, dtype=torch.uint8)
+
+    def both(strides, shape=q.shape):
+        out = base.as_strided(shape, strides)
+        K.qk_norm_rope(q[:shape[0], :shape[1]], None, pos[:shape[0]], tab, q_out=out, ws=ws)
+        n = shape[0]
+        K.qcache_append_rope(q[:n], q[:n], slots[:n], pages, tab, positions=pos[:n],
+                             q=q[:n, :shape[1]], q_out=out, ws=ws)
+
+    for strides in [(256, 64, 1), (64, 576, 1), (320, 72, 1), (1024, 64, 1)]:
+        both(strides)
+    both((8, 64, 1), (1, 4, 64))                    # one token: its stride is not used
+    both((64, 8, 1), (9, 1, 64))
+    n = len(fake.calls)
+    for strides in [(64, 64, 1), (256, 32, 1), (248, 64, 1), (64, 568, 1), (56, 576, 1), (0, 64, 1),
+                    (256, 0, 1)]:
+        with pytest.raises(ValueError):
+            both(strides)
+    # sequences that reach into each other
+    four, pos2 = torch.zeros(2, 4, 3, 64, dtype=BF), torch.zeros(2, 3, dtype=I32)
+    for first in (64 * 11, 0, 8):
+        with pytest.raises(ValueError):
+            K.qk_norm_rope(four, None, pos2, tab, ws=ws,
+                           q_out=base.as_strided(four.shape, (first, 64, 256, 1)))
+    assert len(fake.calls) == n
+    K.qk_norm_rope(four, None, pos2, tab, ws=ws, q_out=base.as_strided(four.shape, (64 * 12, 64, 256, 1)))
