@@ -1012,10 +1012,10 @@ def _packed(t, shape):
     return torch.empty_like(t) if t.is_contiguous() else t.new_empty(shape)
 
 
-def _same_place(src, out, name):
-    """An output may be the input itself, not the same memory in another order."""
-    if out is not None and out.data_ptr() == src.data_ptr() and out.stride() != src.stride() \
-            and src.numel():
+def _same_place(src, out, strides, out_strides, name):
+    """An output may be the input itself, not the same memory in another order
+    (strides as _head_strides gives them: axes of one row do not count)."""
+    if out_strides != strides and out.data_ptr() == src.data_ptr() and src.numel():
         raise ValueError("%s: the input's memory in another order" % name)
 
 
@@ -1068,10 +1068,10 @@ def qk_norm_rope(q, k=None, positions=None, rope=None, q_weight=None, k_weight=N
     wk = _weight(k_weight, "k_weight", d, dtype, dev)
     if q_out is not None:
         qo_st = _head_strides(q_out, "q_out", shape, dtype, dev, unit, out=True)
-        _same_place(q, q_out, "q_out")
+        _same_place(q, q_out, strides, qo_st, "q_out")
     if k_out is not None:
         ko_st = _head_strides(k_out, "k_out", k_shape, dtype, dev, unit, out=True)
-        _same_place(k, k_out, "k_out")
+        _same_place(k, k_out, kst, ko_st, "k_out")
     index = q.get_device()
     if _elsewhere(index, stream):
         with _on(dev, stream, q, k, positions, rope, q_weight, k_weight, q_out, k_out):
@@ -1136,8 +1136,9 @@ def qcache_append_rope(k, v, slot_map, pages, rope, positions=None, q=None, cu_n
         shape = (B if planned else T, Hq, d)
         st = _head_strides(q, "q", shape, dtype, dev, unit)[1:]
         if q_out is not None:
-            st += _head_strides(q_out, "q_out", shape, dtype, dev, unit, out=True)[1:]
-            _same_place(q, q_out, "q_out")
+            out_st = _head_strides(q_out, "q_out", shape, dtype, dev, unit, out=True)[1:]
+            _same_place(q, q_out, st, out_st, "q_out")
+            st += out_st
         else:
             st += (Hq * d, d)
     elif q_out is not None or q_weight is not None:

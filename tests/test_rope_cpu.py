@@ -274,3 +274,28 @@ def test_binding_refuses_outputs_whose_rows_meet(K, fake):
                            q_out=base.as_strided(four.shape, (first, 64, 256, 1)))
     assert len(fake.calls) == n
     K.qk_norm_rope(four, None, pos2, tab, ws=ws, q_out=base.as_strided(four.shape, (64 * 12, 64, 256, 1)))
+
+
+def test_binding_takes_one_row_in_place_whatever_its_strides(K, fake):
+    """Strides of axes of length 1 say nothing about the order."""
+    ws, proj = K.Workspace("cpu"), torch.zeros(1, 8, 64, dtype=BF)
+    tab, pos = torch.zeros(20, 2, 32), torch.zeros(1, dtype=I32)
+    q, k, v = proj[:, :4], proj[:, 4:6], proj[:, 6:]
+    flat = proj.view(-1)[:256].view(1, 4, 64), proj.view(-1)[256:384].view(1, 2, 64)
+    assert flat[0].data_ptr() == q.data_ptr() and flat[0].stride() != q.stride()
+    out = K.qk_norm_rope(q, k, pos, tab, q_out=flat[0], k_out=flat[1], ws=ws)
+    assert out[0] is flat[0] and out[1] is flat[1]
+    slots, pages = torch.zeros(1, dtype=I32), torch.zeros(4, 2, 1, 1152, dtype=torch.uint8)
+    assert K.qcache_append_rope(k, v, slots, pages, tab, positions=pos, q=q, q_out=flat[0],
+                                ws=ws) is flat[0]
+    one = torch.zeros(4, 1, 64, dtype=BF)           # one head
+    K.qk_norm_rope(one, None, pos.expand(4).contiguous(), tab,
+                   q_out=one.as_strided((4, 1, 64), (64, 256, 1)), ws=ws)
+    square = torch.zeros(4, 4, 64, dtype=BF)
+    for call in (lambda t: K.qk_norm_rope(square, None, pos.expand(4).contiguous(), tab, q_out=t, ws=ws),
+                 lambda t: K.qcache_append_rope(square[:, :2], square[:, :2], slots.expand(4).contiguous(),
+                                                pages, tab, positions=pos.expand(4).contiguous(),
+                                                q=square, q_out=t, ws=ws)):
+        call(square)
+        with pytest.raises(ValueError):
+            call(square.transpose(0, 1))
