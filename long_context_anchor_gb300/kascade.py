@@ -794,8 +794,9 @@ def qcache_workspace_size(desc, geo, topk: int, reuse: bool = False) -> int:
 
 def qcache_prefix_workspace_size(desc, geo, prefix_len: int) -> int:
     """Workspace bytes of a decode call over a shared prefix."""
-    n = _lib.kascade_qcache_prefix_workspace_size(ctypes.byref(desc), ctypes.byref(geo),
-                                                  int(prefix_len))
+    prefix_len = int(prefix_len)
+    n = 0 if prefix_len != ctypes.c_int32(prefix_len).value else \
+        _lib.kascade_qcache_prefix_workspace_size(ctypes.byref(desc), ctypes.byref(geo), prefix_len)
     if n == 0:
         raise KascadeError(INVALID_ARG, "kascade_qcache_prefix_workspace_size")
     return n
@@ -952,6 +953,8 @@ def _rope(rope, interleaved, axes, positions, shape, dev):
         axes = tuple(axes)
         if len(axes) != rope.shape[2]:
             raise ValueError("axes: %d entries for %d pairs" % (len(axes), rope.shape[2]))
+        if not all(0 <= x < 4 for x in axes):
+            raise ValueError("axes: expected numbers from 0 to 3")
         n_axes = max(axes) + 1
         if isinstance(positions, torch.Tensor) and positions.dim() == len(shape) + 1:
             n_axes = max(n_axes, positions.shape[0])

@@ -137,3 +137,11 @@ def test_binding_raises_what_the_library_refuses(K):
     for prefix in (-64, 100, 1024):
         with pytest.raises(K.KascadeError):
             K.qcache_prefix_workspace_size(desc, geo, prefix)
+
+
+@pytest.mark.parametrize("prefix", [1 << 32, (1 << 32) + 64, -(1 << 32) + 64, 1 << 31])
+def test_binding_refuses_a_prefix_beyond_32_bits(K, fake, prefix):
+    """It is not cut to a length that the library takes."""
+    with pytest.raises(K.KascadeError):
+        K.qcache_prefix_decode(**tensors(), prefix_len=prefix, ws=K.Workspace("cpu"))
+    assert not any(n.endswith("decode") for n, _ in fake.calls)

@@ -299,3 +299,20 @@ def test_binding_takes_one_row_in_place_whatever_its_strides(K, fake):
         call(square)
         with pytest.raises(ValueError):
             call(square.transpose(0, 1))
+
+
+@pytest.mark.parametrize("bad", [4, -1, 1 << 32, -(1 << 32), (1 << 32) + 1])
+def test_binding_refuses_axes_that_are_none(K, fake, bad):
+    """Nothing is cut to 32 bits on its way into the library."""
+    ws, q, cu = K.Workspace("cpu"), torch.zeros(3, 4, 64, dtype=BF), torch.zeros(4, dtype=I32)
+    tab, slots = torch.zeros(20, 2, 32), torch.zeros(3, dtype=I32)
+    pages = torch.zeros(4, 4, 1, 1152, dtype=torch.uint8)
+    call = lambda axes: K.qcache_append_rope(q, q, slots, pages, tab, cu_new=cu, kv_lens=slots, q=q,
+                                             axes=axes, ws=ws)
+    call([0] * 31 + [3])
+    n = len(fake.calls)
+    with pytest.raises(ValueError):
+        call([0] * 31 + [bad])
+    with pytest.raises(ValueError):
+        call([bad] * 32)
+    assert len(fake.calls) == n
