@@ -335,7 +335,8 @@ typedef struct {
  * elements, multiples of 16 bytes). q_out and k_out may be q and k with the same
  * strides; other overlaps are not allowed. n_q_heads or n_kv_heads may be 0.
  * positions [n_axes][batch][n_tokens] int32; one outside the table sets
- * KASCADE_ERR_BAD_INPUT on the device, and its pairs are not turned.
+ * KASCADE_ERR_BAD_INPUT on the device, and its axis' pairs are turned by no angle
+ * (cosine 1, sine 0). Positions on an axis that no pair follows are not looked at.
  * batch*n_tokens < 2^28. ws: the workspace header, 256 bytes. */
 kascade_status kascade_qk_norm_rope(const kascade_rope* rope, int32_t batch, int32_t n_tokens,
                                     int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
@@ -456,7 +457,8 @@ kascade_status kascade_qcache_append(const kascade_qcache* cache, int32_t n_kv_h
  * With rope NULL (a norm alone) the first way needs no positions either.
  * strides: k (tokens, heads), v, q, q_out: eight. q_out may be q with the same
  * strides. Queries are written whatever their token's slot. A position outside
- * the table sets KASCADE_ERR_BAD_INPUT, and its row is not turned. */
+ * the table does what it does in kascade_qk_norm_rope; those of keys without a
+ * slot are not looked at. */
 kascade_status kascade_qcache_append_rope(const kascade_qcache* cache, const kascade_rope* rope,
                                           int32_t n_q_heads, int32_t n_kv_heads,
                                           int32_t head_dim, int32_t dtype, const void* k,

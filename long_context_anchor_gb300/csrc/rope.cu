@@ -117,13 +117,13 @@ __device__ __forceinline__ void load_turn4(const RopeSpec& r, const float* const
   c[0] = a.x, c[1] = a.y, c[2] = a.z, c[3] = a.w;
   s[0] = b.x, s[1] = b.y, s[2] = b.z, s[3] = b.w;
 }
-// The rows of the axes a token has positions on; pos(axis) gives them.
+// The rows of the axes that pairs follow; pos(axis) gives a token's positions.
 template <bool MIXED, typename Pos>
 __device__ __forceinline__ void table_rows(const RopeSpec& r, Pos pos, unsigned int* err,
                                            const float* (&rows)[4]) {
   if (MIXED) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) rows[i] = i < r.n_axes ? table_row(r, pos(i), err) : nullptr;
+    for (int i = 0; i < 4; ++i) rows[i] = (r.used >> i) & 1 ? table_row(r, pos(i), err) : nullptr;
   } else {
     rows[0] = table_row(r, pos(r.axis[0]), err);
     rows[1] = rows[2] = rows[3] = nullptr;
@@ -461,7 +461,6 @@ kascade_status check_rope(const kascade_rope* rope, int head_dim, float eps, Rop
   memset(&s, 0, sizeof(s));
   if (!(eps >= 0.f) || eps > 1e30f) return KASCADE_ERR_INVALID_ARG;
   s.eps = eps;
-  s.n_axes = 1;
   if (head_dim != 64 && head_dim != 128) return KASCADE_ERR_UNSUPPORTED;
   if (rope == nullptr) return KASCADE_OK;
   if (!aligned(rope->table, 16) || rope->n_positions < 1 || rope->n_pairs < 1 ||
@@ -471,7 +470,6 @@ kascade_status check_rope(const kascade_rope* rope, int head_dim, float eps, Rop
   s.table = rope->table;
   s.n_pos = rope->n_positions;
   s.n_pairs = rope->n_pairs;
-  s.n_axes = rope->n_axes;
   s.interleaved = rope->interleaved != 0;
   for (int i = 0; rope->axes != nullptr && i < rope->n_pairs; ++i) {
     if (rope->axes[i] < 0 || rope->axes[i] >= rope->n_axes) return KASCADE_ERR_INVALID_ARG;
@@ -479,8 +477,10 @@ kascade_status check_rope(const kascade_rope* rope, int head_dim, float eps, Rop
     if (s.axis[i] != s.axis[0]) s.mixed = 1;
   }
   s.quads = 1;
-  for (int i = 0; i < rope->n_pairs; ++i)
+  for (int i = 0; i < rope->n_pairs; ++i) {
     if (s.axis[i] != s.axis[i & ~3]) s.quads = 0;
+    s.used |= 1 << s.axis[i];
+  }
   return KASCADE_OK;
 }
 

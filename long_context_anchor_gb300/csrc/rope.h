@@ -10,7 +10,8 @@ namespace kascade {
 // A checked kascade_rope, and the norm in front of it.
 struct RopeSpec {
   const float* table;     // [n_pos][2][n_pairs], or null: nothing is turned
-  int n_pos, n_pairs, n_axes, interleaved;
+  int n_pos, n_pairs, interleaved;
+  int used;               // bit per axis that some pair follows
   int mixed;              // pairs of one head follow different axes
   int quads;              // ... but four neighbouring ones the same
   float eps;

@@ -145,6 +145,50 @@ def test_positions_outside_the_table(K):
     assert torch.equal(got[2:5], q[2:5])
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("kind", ["cyclic", "sections"])
+def test_one_axis_outside_the_table(K, kind, inter):
+    """Its pairs alone keep their values, in rows and in cached keys."""
+    rng = np.random.default_rng(15)
+    q, v = (torch.from_numpy(rng.standard_normal((6, 4, 64))).to(F32).cuda() for _ in range(2))
+    tab, ax = make_table(K, 32, 10), axes_of(kind, 32)
+    pos = rng.integers(1, 10, (3, 6))
+    pos[0, 1], pos[1, 2], pos[2, 3], pos[:, 4] = 10, -1, 2 ** 31 - 1, 99
+    ws = K.Workspace("cuda")
+    got, _ = K.qk_norm_rope(q, None, ints(pos), tab, axes=ax, interleaved=inter, ws=ws)
+    assert ws.device_error() == K.BAD_INPUT
+    check(got, expected(q, tab, pos, ax, None, inter, F32))
+    for t, axis in ((1, 0), (2, 1), (3, 2)):
+        pairs = np.array([i for i in range(32) if ax[i] == axis])
+        kept = np.r_[2 * pairs, 2 * pairs + 1] if inter else np.r_[pairs, pairs + 32]
+        assert np.array_equal(f64(got[t])[:, kept], f64(q[t])[:, kept])
+    assert torch.equal(got[4], q[4])
+    pages, slots = K.qcache_alloc(1, 4, 64, 16), ints(np.arange(6))
+    K.qcache_append_rope(q, v, slots, pages, tab, positions=ints(pos), axes=ax, interleaved=inter, ws=ws)
+    assert ws.device_error() == K.BAD_INPUT
+    ck, _ = K.qcache_read(pages, slots, dtype=F32)
+    assert np.array_equal(f64(ck), Q.stored(f32_turned(q, tab, pos, ax, inter)))
+
+
+@pytest.mark.parametrize("ax", [[0, 2] * 16, [2] * 32, [0] * 16 + [2] * 16])
+def test_axes_that_no_pair_follows(K, ax):
+    """Positions there may be anything."""
+    rng = np.random.default_rng(16)
+    q, k = (torch.from_numpy(rng.standard_normal((6, h, 64))).to(BF).cuda() for h in (4, 2))
+    tab, pos = make_table(K, 32, 10), rng.integers(0, 10, (4, 6))
+    pos[1], pos[3] = -5, 2 ** 31 - 1
+    ws = K.Workspace("cuda")
+    got = K.qk_norm_rope(q, k, ints(pos), tab, axes=ax, ws=ws)
+    assert ws.device_error() == K.OK
+    check(got[0], expected(q, tab, pos, ax, None, False, BF))
+    check(got[1], expected(k, tab, pos, ax, None, False, BF))
+    pages, slots = K.qcache_alloc(1, 2, 64, 16), ints(np.arange(6))
+    to = K.qcache_append_rope(k, k, slots, pages, tab, positions=ints(pos), q=q, axes=ax, ws=ws)
+    assert ws.device_error() == K.OK and torch.equal(to, got[0])
+    ck, _ = K.qcache_read(pages, slots, dtype=F32)
+    assert np.array_equal(f64(ck), Q.stored(f32_turned(k, tab, pos, ax, False)))
+
+
 def test_special_values_stay_in_their_pair(K):
     q = torch.ones(2, 1, 64, dtype=F32, device="cuda")
     q[0, 0, 3], q[1, 0, 60] = float("nan"), float("inf")
