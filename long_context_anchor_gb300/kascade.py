@@ -934,7 +934,10 @@ def rope_table(inv_freq, n_positions, scale=1.0, device="cuda"):
 
 @functools.lru_cache(maxsize=64)
 def _axes_array(axes):
-    return (ctypes.c_int32 * len(axes))(*axes)
+    """Checked axes of the pairs as the library takes them, and the highest + 1."""
+    if not all(0 <= x < 4 for x in axes):
+        raise ValueError("axes: expected numbers from 0 to 3")
+    return (ctypes.c_int32 * len(axes))(*axes), max(axes) + 1
 
 
 def _rope(rope, interleaved, axes, positions, shape, dev):
@@ -953,12 +956,9 @@ def _rope(rope, interleaved, axes, positions, shape, dev):
         axes = tuple(axes)
         if len(axes) != rope.shape[2]:
             raise ValueError("axes: %d entries for %d pairs" % (len(axes), rope.shape[2]))
-        if not all(0 <= x < 4 for x in axes):
-            raise ValueError("axes: expected numbers from 0 to 3")
-        n_axes = max(axes) + 1
+        ptr, n_axes = _axes_array(axes)
         if isinstance(positions, torch.Tensor) and positions.dim() == len(shape) + 1:
             n_axes = max(n_axes, positions.shape[0])
-        ptr = _axes_array(axes)
         shape = (n_axes,) + tuple(shape)
     if positions is not None:
         _fits(positions, "positions", shape, torch.int32, dev)
