@@ -505,7 +505,7 @@ __device__ void arrive_and_join(const QDecodeArgs& a, int n_units, const SharedU
       for (int e = tid; e < elems; e += threads) {
         const int h = e / (D / 4);
         joined_output<D, F32, PREFIX>(a, join_some<true>(mine, 0, n, G, h, e), u.b, u.g, h,
-                              e & (D / 4 - 1));
+                                      e & (D / 4 - 1));
       }
       continue;
     }

@@ -32,11 +32,14 @@
 // their place (product, its wait, scores, five waits of 100 cycles); the issue slots are
 // 50 to 60% full, tensor cores busy 30% (d = 64) and 50% (d = 128, where the scores read Q
 // from shared memory, as TMEM is full). About 6 us of a launch are its start (4: lengths,
-// queries, first chunk) and end. Slower (against 57.8 and 86.8 us, when those were 9): two warps per 32 rows with
-// half of the keys each (61.5, 91), the next chunk's load begun before this one's end (63,
-// 91), scores and products issued by warps of their own (65, 103), one arrival per warp
-// for the weights (58.7, 87.9); against 56.8 and 77.9: queries loaded before the barriers are
-// set up (59.6, 81).
+// queries, first chunk) and end. Slower, 16 x 131072 keys and 128 x 32768: against 57.8 and
+// 86.8 us, when those were the times, two warps per 32 rows with half of the keys each (61.5,
+// 91), the next chunk's load begun before this one's end (63, 91), scores and products issued
+// by warps of their own (65, 103), one arrival per warp for the weights (58.7, 87.9); against
+// 56.8 and 77.9, queries loaded before the barriers are set up (59.6, 81).
+// fp32 queries have two terms, and so have their weights: twice the products, a tile per CTA.
+// 128 x 8192 keys, 32 heads, d = 128 64.8 us (bf16 41), 16 x 131072, 64 heads, d = 64 77.6
+// (57), 32 x 8192 with 1024 own keys each 34.6 (25.5); one by one 278, 285 and 84.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -321,119 +324,119 @@ __global__ void __launch_bounds__(kThreads, 1) k_qprefix(const __grid_constant__
 
   if (warp >= kMmaWarp) {
     fewer_regs<kIssueRegs>();
-  if (warp == kLoadWarp) {
-    // ------------------------------------------------------------- copies
-    // kAhead chunks at a time, four lanes each: one chunk at a time took 1050 cycles
-    constexpr int kAhead = D == 128 ? 2 : 4;
-    const int copy_sh = min(a.bs_shift, 6), ncopy = kPfxKeys >> copy_sh;   // copies of a chunk
-    const uint32_t copy_bytes = static_cast<uint32_t>(qgroup_bytes(D)) << (copy_sh - 4);
-    const uint32_t head_bytes = static_cast<uint32_t>(qgroup_bytes(D)) << (a.bs_shift - 4);
-    const uint64_t block_bytes = static_cast<uint64_t>(head_bytes) * a.Hkv;
-    const int gmask = (1 << (a.bs_shift - 4)) - 1;
-    const unsigned int groups = (1u << (1 << (copy_sh - 4))) - 1u;   // a copy's bits
-    const int sub = lane >> 2, cp = lane & 3;
-    const uint8_t* head = a.cache + static_cast<size_t>(p.g) * head_bytes;
-    // this lane's copy of chunks c + sub; ids are loaded a turn ahead
-    auto key_of = [&](int c) { return (c + sub) * kPfxKeys + (cp << copy_sh); };
-    auto wanted = [&](int c) {
-      return sub < kAhead && cp < ncopy && c + sub < p.c1 && key_of(c) < a.P;
-    };
-    auto fetch = [&](int c) { return wanted(c) ? __ldg(ids + (key_of(c) >> a.bs_shift)) : 0; };
-    int next = fetch(p.c0);
-    uint32_t issued = 0;
-    for (int c = p.c0; c < p.c1; c += kAhead) {
-      const int id = next, key = key_of(c);
-      next = fetch(c + kAhead);
-      const bool here = sub < kAhead && c + sub < p.c1, want = wanted(c);
-      const bool take = want && static_cast<unsigned int>(id) < static_cast<unsigned int>(a.num_blocks);
-      if (want && !take) report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x552);
-      const unsigned int got = (__ballot_sync(0xffffffffu, take) >> (lane & 28)) & 0xfu;
-      const uint32_t k = c - p.c0 + sub, st = k % NR;
-      if (!__all_sync(0xffffffffu,
-                      !here || mbar_wait(raw_free + st, ((k / NR) & 1) ^ 1, a.err, 0x561)))
-        break;
-      if (here && cp == 0) {
-        unsigned int bits = 0u;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if ((got >> i) & 1u) bits |= groups << (i << (copy_sh - 4));
-        raw_valid[st] = static_cast<int>(bits);
-        mbar_arrive_expect_tx(raw_full + st, __popc(got) * copy_bytes);
-      }
-      __syncwarp();
-      if (take)
-        bulk_load(sm + SM::RAW0 + st * SM::RAW + cp * copy_bytes,
-                  head + static_cast<uint64_t>(id) * block_bytes +
-                      static_cast<uint32_t>((key >> 4) & gmask) * qgroup_bytes(D),
-                  copy_bytes, raw_full + st);
-      issued += min(kAhead, p.c1 - c);
-    }
-    // leave no copy in flight
-    for (uint32_t k = issued > NR ? issued - NR : 0; k < issued; ++k)
-      mbar_wait(raw_full + k % NR, (k / NR) & 1, a.err, 0x562);
-  } else if (warp < kLoadWarp) {
-    // --------------------------------------------------------- tensor cores
-    constexpr uint32_t idq = idesc_f16_f32(128, kPfxKeys, 0), idv = idesc_f16_f32(128, D, 1);
-    const int s = static_cast<int>(warp_uniform(static_cast<uint32_t>(warp - kMmaWarp)));
-    const uint32_t kv0 = smem_u32(sm);
-    const uint32_t q0 = smem_u32(sm + SM::QS);
-    const uint32_t tS0 = tmem + SM::S0 + 128 * s, tO = tmem + SM::O0 + SM::O_COLS * s;
-    const int n = p.chunks(s);
-    // S = Q K^T of the stream's t-th chunk
-    auto issue_s = [&](int t) {
-      const uint32_t k = p.chunk(s, t), ks = k % KST, buf = t & 1;
-      if (!wait_warp(k_ready + ks, (k / KST) & 1, a.err, 0x571)) return false;
-      tc_fence_after();
-      const uint64_t kd = warp_uniform(kq_desc(kv0 + ks * SM::TILE));
-      const uint32_t tS = tS0 + 64 * buf;
-#pragma unroll
-      for (int term = 0; term < TERMS; ++term) {
-        const int tile = TERMS == 2 ? term : s;
-        const uint64_t qd = warp_uniform(kq_desc(q0 + tile * SM::Q_TILE));
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t acc = term > 0 || kk > 0 ? 1u : 0u;
-          if (SM::QSMEM)
-            tc_mma(tS, qd + q_step(kk), kd + k_step(kk), idq, acc);
-          else
-            tc_mma_ts(tS, tmem + SM::Q_COLS * tile + kk * 8, kd + k_step(kk), idq, acc);
+    if (warp == kLoadWarp) {
+      // ------------------------------------------------------------- copies
+      // kAhead chunks at a time, four lanes each: one chunk at a time took 1050 cycles
+      constexpr int kAhead = D == 128 ? 2 : 4;
+      const int copy_sh = min(a.bs_shift, 6), ncopy = kPfxKeys >> copy_sh;   // copies of a chunk
+      const uint32_t copy_bytes = static_cast<uint32_t>(qgroup_bytes(D)) << (copy_sh - 4);
+      const uint32_t head_bytes = static_cast<uint32_t>(qgroup_bytes(D)) << (a.bs_shift - 4);
+      const uint64_t block_bytes = static_cast<uint64_t>(head_bytes) * a.Hkv;
+      const int gmask = (1 << (a.bs_shift - 4)) - 1;
+      const unsigned int groups = (1u << (1 << (copy_sh - 4))) - 1u;   // a copy's bits
+      const int sub = lane >> 2, cp = lane & 3;
+      const uint8_t* head = a.cache + static_cast<size_t>(p.g) * head_bytes;
+      // this lane's copy of chunks c + sub; ids are loaded a turn ahead
+      auto key_of = [&](int c) { return (c + sub) * kPfxKeys + (cp << copy_sh); };
+      auto wanted = [&](int c) {
+        return sub < kAhead && cp < ncopy && c + sub < p.c1 && key_of(c) < a.P;
+      };
+      auto fetch = [&](int c) { return wanted(c) ? __ldg(ids + (key_of(c) >> a.bs_shift)) : 0; };
+      int next = fetch(p.c0);
+      uint32_t issued = 0;
+      for (int c = p.c0; c < p.c1; c += kAhead) {
+        const int id = next, key = key_of(c);
+        next = fetch(c + kAhead);
+        const bool here = sub < kAhead && c + sub < p.c1, want = wanted(c);
+        const bool take = want && static_cast<unsigned int>(id) < static_cast<unsigned int>(a.num_blocks);
+        if (want && !take) report_error(a.err, KASCADE_ERR_BAD_INPUT, 0x552);
+        const unsigned int got = (__ballot_sync(0xffffffffu, take) >> (lane & 28)) & 0xfu;
+        const uint32_t k = c - p.c0 + sub, st = k % NR;
+        if (!__all_sync(0xffffffffu,
+                        !here || mbar_wait(raw_free + st, ((k / NR) & 1) ^ 1, a.err, 0x561)))
+          break;
+        if (here && cp == 0) {
+          unsigned int bits = 0u;
+  #pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if ((got >> i) & 1u) bits |= groups << (i << (copy_sh - 4));
+          raw_valid[st] = static_cast<int>(bits);
+          mbar_arrive_expect_tx(raw_full + st, __popc(got) * copy_bytes);
         }
+        __syncwarp();
+        if (take)
+          bulk_load(sm + SM::RAW0 + st * SM::RAW + cp * copy_bytes,
+                    head + static_cast<uint64_t>(id) * block_bytes +
+                        static_cast<uint32_t>((key >> 4) & gmask) * qgroup_bytes(D),
+                    copy_bytes, raw_full + st);
+        issued += min(kAhead, p.c1 - c);
       }
-      tc_commit(s_full + 2 * s + buf);
-      tc_commit(k_free + ks);
-      if (p.tiles == 1) tc_commit(k_free + ks);   // for the stream that does not use it
-      return true;
-    };
-    // O += P V; the first product overwrites O
-    auto issue_pv = [&](int t) {
-      const uint32_t k = p.chunk(s, t), st = k % VST, buf = t & 1;
-      if (!wait_warp(v_ready + st, (k / VST) & 1, a.err, 0x576) ||
-          !wait_warp(p_full + 2 * s + buf, (t >> 1) & 1, a.err, 0x572))
-        return false;
+      // leave no copy in flight
+      for (uint32_t k = issued > NR ? issued - NR : 0; k < issued; ++k)
+        mbar_wait(raw_full + k % NR, (k / NR) & 1, a.err, 0x562);
+    } else if (warp < kLoadWarp) {
+      // --------------------------------------------------------- tensor cores
+      constexpr uint32_t idq = idesc_f16_f32(128, kPfxKeys, 0), idv = idesc_f16_f32(128, D, 1);
+      const int s = static_cast<int>(warp_uniform(static_cast<uint32_t>(warp - kMmaWarp)));
+      const uint32_t kv0 = smem_u32(sm);
+      const uint32_t q0 = smem_u32(sm + SM::QS);
+      const uint32_t tS0 = tmem + SM::S0 + 128 * s, tO = tmem + SM::O0 + SM::O_COLS * s;
+      const int n = p.chunks(s);
+      // S = Q K^T of the stream's t-th chunk
+      auto issue_s = [&](int t) {
+        const uint32_t k = p.chunk(s, t), ks = k % KST, buf = t & 1;
+        if (!wait_warp(k_ready + ks, (k / KST) & 1, a.err, 0x571)) return false;
+        tc_fence_after();
+        const uint64_t kd = warp_uniform(kq_desc(kv0 + ks * SM::TILE));
+        const uint32_t tS = tS0 + 64 * buf;
+  #pragma unroll
+        for (int term = 0; term < TERMS; ++term) {
+          const int tile = TERMS == 2 ? term : s;
+          const uint64_t qd = warp_uniform(kq_desc(q0 + tile * SM::Q_TILE));
+  #pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t acc = term > 0 || kk > 0 ? 1u : 0u;
+            if (SM::QSMEM)
+              tc_mma(tS, qd + q_step(kk), kd + k_step(kk), idq, acc);
+            else
+              tc_mma_ts(tS, tmem + SM::Q_COLS * tile + kk * 8, kd + k_step(kk), idq, acc);
+          }
+        }
+        tc_commit(s_full + 2 * s + buf);
+        tc_commit(k_free + ks);
+        if (p.tiles == 1) tc_commit(k_free + ks);   // for the stream that does not use it
+        return true;
+      };
+      // O += P V; the first product overwrites O
+      auto issue_pv = [&](int t) {
+        const uint32_t k = p.chunk(s, t), st = k % VST, buf = t & 1;
+        if (!wait_warp(v_ready + st, (k / VST) & 1, a.err, 0x576) ||
+            !wait_warp(p_full + 2 * s + buf, (t >> 1) & 1, a.err, 0x572))
+          return false;
+        tc_fence_after();
+        const uint64_t vd = warp_uniform(v_desc(kv0 + SM::V0 + st * SM::TILE));
+        const uint32_t tP = tS0 + 64 * buf;
+  #pragma unroll
+        for (int term = 0; term < TERMS; ++term)
+  #pragma unroll
+          for (int kk = 0; kk < kPfxKeys / 16; ++kk)
+            tc_mma_ts(tO, tP + 32 * term + kk * 8, vd + v_step(kk), idv,
+                      t > 0 || term > 0 || kk > 0 ? 1u : 0u);
+        tc_commit(pv_done + 2 * s + buf);
+        tc_commit(v_free + st);
+        if (p.tiles == 1) tc_commit(v_free + st);
+        return true;
+      };
+      bool ok = wait_warp(q_ready + s, 0, a.err, 0x573);
+      if (TERMS == 2 && ok) ok = wait_warp(q_ready + 1 - s, 0, a.err, 0x573);
       tc_fence_after();
-      const uint64_t vd = warp_uniform(v_desc(kv0 + SM::V0 + st * SM::TILE));
-      const uint32_t tP = tS0 + 64 * buf;
-#pragma unroll
-      for (int term = 0; term < TERMS; ++term)
-#pragma unroll
-        for (int kk = 0; kk < kPfxKeys / 16; ++kk)
-          tc_mma_ts(tO, tP + 32 * term + kk * 8, vd + v_step(kk), idv,
-                    t > 0 || term > 0 || kk > 0 ? 1u : 0u);
-      tc_commit(pv_done + 2 * s + buf);
-      tc_commit(v_free + st);
-      if (p.tiles == 1) tc_commit(v_free + st);
-      return true;
-    };
-    bool ok = wait_warp(q_ready + s, 0, a.err, 0x573);
-    if (TERMS == 2 && ok) ok = wait_warp(q_ready + 1 - s, 0, a.err, 0x573);
-    tc_fence_after();
-    for (int t = 0; ok && t < n && t < 2; ++t) ok = issue_s(t);
-    for (int t = 0; ok && t < n; ++t) {
-      ok = issue_pv(t);
-      if (ok && t + 2 < n)   // over this chunk's weights
-        ok = wait_warp(pv_done + 2 * s + (t & 1), (t >> 1) & 1, a.err, 0x574) && issue_s(t + 2);
+      for (int t = 0; ok && t < n && t < 2; ++t) ok = issue_s(t);
+      for (int t = 0; ok && t < n; ++t) {
+        ok = issue_pv(t);
+        if (ok && t + 2 < n)   // over this chunk's weights
+          ok = wait_warp(pv_done + 2 * s + (t & 1), (t >> 1) & 1, a.err, 0x574) && issue_s(t + 2);
+      }
     }
-  }
   } else if (warp >= 8) {
     fewer_regs<kDeqRegs>();
     // ------------------------------------------------------- codes to fp16

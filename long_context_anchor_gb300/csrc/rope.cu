@@ -17,10 +17,12 @@
 // Both are bound by memory where they are large. Rows of 16384 tokens, 32 + 8 heads of
 // 128, bf16 with norm: 60.2 us, 5.7 TB/s (issue slots 70% full); 131072 tokens, 64 + 8
 // heads of 64, half turned: 399 us, 6.1 TB/s; 2 x 5003 tokens, 16 + 4 heads of 64 in fp32
-// on three axes: 23.8 us, 4.4 TB/s, start and end among it. Into the cache with queries,
-// 16384 tokens, 32 + 8 heads: 70 us, 5.0 TB/s (issue 54%, loads waited for 7 issues each: a
-// warp has few rows in flight in 64 registers). A step's few rows take 2.3 and 3.4 us, a
-// launch's latency.
+// on three axes: 23.8 us, 4.4 TB/s: its 1251 CTAs are 2.06 rounds of the 608 that run at once
+// (9728 tokens, 2.00 rounds, take 20.4). Into the cache with queries, 16384 tokens, 32 + 8
+// heads: 71 us, 5.0 TB/s (issue 54%, loads waited for 7 issues each: a warp has few rows in
+// flight in 64 registers), 74 with norms. A step's few rows take 2.3 and 3.4 us (3.8 with
+// norms), a launch's latency; a row's way into the cache is a chain of slot, owner, lengths
+// and the table's row, in front of its first elements.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
